@@ -19,13 +19,15 @@ __all__ = [
     "Cfg", "PagedCache", "GroupState", "load", "compress", "index_workspace_bytes", "index_topk", "attend",
     "gather_dequant", "layer", "status_string", "CsaError", "CACHE_FP4", "CACHE_BF16", "MODE_FULL",
     "MODE_REINDEX", "MODE_REUSE", "PAGE", "library_path", "capture", "swa_encode", "CACHE_FP4_S32",
-    "FMT_IDX_68B", "FMT_SWA_FP8", "FMT_IDX_QFP4", "SWA_FP8_ROW",
+    "FMT_IDX_68B", "FMT_SWA_FP8", "FMT_IDX_QFP4", "SWA_FP8_ROW", "KVCfg", "KVCache", "kv_append", "kv_attend",
+    "kv_cross_attend", "kv_workspace_bytes", "rope_table", "ROPE_INTERLEAVED", "ROPE_HALF",
 ]
 
 CACHE_FP4, CACHE_BF16, CACHE_FP4_S32 = 0, 1, 2
 FMT_IDX_68B, FMT_SWA_FP8, FMT_IDX_QFP4 = 1, 2, 4
 SWA_FP8_ROW = 528  # bytes of one MXFP8 window row
 MODE_FULL, MODE_REINDEX, MODE_REUSE = 0, 1, 2
+ROPE_INTERLEAVED, ROPE_HALF = 0, 1
 PAGE = 64
 
 
@@ -74,6 +76,23 @@ class _LayerIO(C.Structure):
                 ("lse", C.c_void_p)]
 
 
+class KVCfg(C.Structure):
+    """csa2_kv_cfg: an ordinary grouped-query layer -- `n_heads` query heads over `kv_heads` key / value heads of
+    `head_dim` (64 or 128) channels, an FP4 or BF16 cache, a sliding `window` (0: none) and RoPE over the first
+    `rope_dims` channels (ROPE_INTERLEAVED pairs, or ROPE_HALF)."""
+    _fields_ = [("n_heads", C.c_int32), ("kv_heads", C.c_int32), ("head_dim", C.c_int32), ("cache_dtype", C.c_int32),
+                ("window", C.c_int32), ("rope_dims", C.c_int32), ("rope_style", C.c_int32), ("reserved", C.c_int32)]
+
+    def __init__(self, n_heads=64, kv_heads=8, head_dim=128, cache_dtype=CACHE_FP4, window=0, rope_dims=64,
+                 rope_style=ROPE_INTERLEAVED):
+        super().__init__(n_heads, kv_heads, head_dim, cache_dtype, window, rope_dims, rope_style, 0)
+
+
+class _KVCacheDesc(C.Structure):
+    _fields_ = [("k_data", C.c_void_p), ("k_scales", C.c_void_p), ("v_data", C.c_void_p), ("v_scales", C.c_void_p),
+                ("block_table", C.c_void_p), ("max_pages", C.c_int32), ("num_pages", C.c_int32)]
+
+
 _lib = None
 _lock = threading.Lock()
 
@@ -113,6 +132,18 @@ def load():
         L.csa2_layer.argtypes = [vp, i32, vp, vp, vp]
         L.csa2_swa_encode.restype = i32
         L.csa2_swa_encode.argtypes = [i32, i32, vp, vp, vp, i32, vp, vp]
+        i64, kvc = C.c_int64, C.POINTER(KVCfg)
+        kvd = C.POINTER(_KVCacheDesc)
+        L.csa2_kv_page_bytes.restype = sz
+        L.csa2_kv_page_bytes.argtypes = [kvc, i32]
+        L.csa2_kv_workspace_bytes.restype = sz
+        L.csa2_kv_workspace_bytes.argtypes = [kvc, i32, i32, i32, i32]
+        L.csa2_kv_append.restype = i32
+        L.csa2_kv_append.argtypes = [kvc, i32, i32, vp, i64, vp, i64, vp, i64, vp, vp, vp, i64, kvd, vp, i64, vp, vp,
+                                     vp, vp]
+        for f in (L.csa2_kv_attend, L.csa2_kv_cross_attend):
+            f.restype = i32
+            f.argtypes = [kvc, i32, i32, vp, i64, vp, kvd, vp, i32, i32, C.c_float, vp, i64, vp, vp, sz, vp, vp]
         _lib = L
         return L
 
@@ -302,6 +333,187 @@ def layer(cfg: Cfg, mode: int, state: GroupState, q_pos, q, swa, swa_len, swa_po
                   _ptr(swa_pos0, torch.int64, "swa_pos0"), 1.0 / math.sqrt(512) if scale is None else float(scale),
                   _ptr(out, torch.float32, "out"), _ptr(lse, torch.float32, "lse"))
     _check("csa2_layer", load().csa2_layer(C.byref(cfg), int(mode), C.byref(state._c), C.byref(io), _stream(stream)))
+
+
+class KVCache:
+    """Paged keys and values of `batch` sequences with `capacity` tokens each (layout in include/csa2.h).  Pages are
+    handed out in `page_order` (a permutation of range(num_pages); identity by default)."""
+
+    def __init__(self, cfg: KVCfg, batch: int, capacity: int, device="cuda", page_order=None, spare_pages: int = 0):
+        max_pages = max(1, math.ceil(capacity / PAGE))
+        n = batch * max_pages + spare_pages
+        order = torch.arange(batch * max_pages) if page_order is None else torch.as_tensor(page_order)
+        table = order[: batch * max_pages].reshape(batch, max_pages).to(device=device, dtype=torch.int32).contiguous()
+        h, d = cfg.kv_heads, cfg.head_dim
+        if cfg.cache_dtype == CACHE_FP4:
+            data = [torch.zeros((n, h, PAGE, d // 2), dtype=torch.uint8, device=device) for _ in "kv"]
+            scales = [torch.zeros((n, h, PAGE, d // 16), dtype=torch.uint8, device=device) for _ in "kv"]
+        else:
+            data = [torch.zeros((n, h, d // 8, PAGE, 8), dtype=torch.bfloat16, device=device) for _ in "kv"]
+            scales = [None, None]
+        self._set(cfg, data[0], data[1], table, scales[0], scales[1])
+
+    @classmethod
+    def over(cls, cfg: KVCfg, k_data, v_data, block_table, k_scales=None, v_scales=None) -> "KVCache":
+        """A cache over pages that the caller holds: data [pages][kv_heads][64][head_dim / 2] uint8 with scales
+        [pages][kv_heads][64][head_dim / 16] uint8 (FP4), or [pages][kv_heads][head_dim / 8][64][8] bf16; block_table
+        [batch][max_pages] int32.  `block_table` may be rewritten in place between calls."""
+        self = cls.__new__(cls)
+        self._set(cfg, k_data, v_data, block_table, k_scales, v_scales)
+        return self
+
+    def _set(self, cfg, k_data, v_data, block_table, k_scales, v_scales):
+        n, h, d = k_data.shape[0], cfg.kv_heads, cfg.head_dim
+        fp4 = cfg.cache_dtype == CACHE_FP4
+        if load().csa2_kv_page_bytes(C.byref(cfg), 0) == 0:
+            raise ValueError("unsupported KV configuration")
+        want = (n, h, PAGE, d // 2) if fp4 else (n, h, d // 8, PAGE, 8)
+        parts = [("k_data", k_data, want, torch.uint8 if fp4 else torch.bfloat16),
+                 ("v_data", v_data, want, torch.uint8 if fp4 else torch.bfloat16)]
+        if fp4:
+            parts += [(m, t, (n, h, PAGE, d // 16), torch.uint8) for m, t in (("k_scales", k_scales), ("v_scales", v_scales))]
+        elif k_scales is not None or v_scales is not None:
+            raise ValueError("a BF16 cache has no scales")
+        for name, t, shape, dtype in parts:
+            if t is None or tuple(t.shape) != shape:
+                raise ValueError("%s must be %s" % (name, list(shape)))
+            _ptr(t, dtype, name)
+        if block_table.dim() != 2:
+            raise ValueError("block_table must be [batch][max_pages]")
+        _ptr(block_table, torch.int32, "block_table")
+        if len({t.device for t in (k_data, v_data, block_table, *(s for s in (k_scales, v_scales) if s is not None))}) > 1:
+            raise ValueError("the pages and the block table must be on one device")
+        self.k_data, self.v_data, self.k_scales, self.v_scales = k_data, v_data, k_scales, v_scales
+        self.block_table, self.device = block_table, k_data.device
+        self.batch, self.max_pages, self.num_pages = block_table.shape[0], block_table.shape[1], n
+        self.capacity = self.max_pages * PAGE
+        self.layout = (h, d, cfg.cache_dtype)
+        self._c = _KVCacheDesc(k_data.data_ptr(), k_scales.data_ptr() if fp4 else None, v_data.data_ptr(),
+                               v_scales.data_ptr() if fp4 else None, block_table.data_ptr(), self.max_pages, n)
+
+
+def rope_table(n: int, rope_dims: int, theta: float = 1e4, device="cuda"):
+    """(cos, sin) of positions 0 .. n - 1 for kv_append: [n][rope_dims / 2][2] fp32, angles position *
+    theta^(-2i / rope_dims) formed in fp64."""
+    half = rope_dims // 2
+    freq = float(theta) ** (-torch.arange(half, dtype=torch.float64, device=device) / half)
+    angle = torch.arange(n, dtype=torch.float64, device=device)[:, None] * freq
+    return torch.stack((angle.cos(), angle.sin()), -1).float().contiguous()
+
+
+def _kv_rows(t, heads, dim, name, device):
+    """Address and row distance of [T][heads][dim] bf16 rows; a row is contiguous, the rows may stand apart."""
+    if t.dtype != torch.bfloat16:
+        raise TypeError("%s must be torch.bfloat16, got %s" % (name, t.dtype))
+    shape, stride = t.shape, t.stride()
+    if len(shape) != 3 or shape[1] != heads or shape[2] != dim:
+        raise ValueError("%s must be [T][%d][%d], got %s" % (name, heads, dim, list(shape)))
+    if stride[2] != 1 or (heads > 1 and stride[1] != dim):
+        raise ValueError("%s: the channels of a row must be contiguous" % name)
+    if t.device != device:
+        raise ValueError("%s must be on the cache's device" % name)
+    return t.data_ptr(), (stride[0] if shape[0] > 1 else heads * dim)
+
+
+def _kv_ptr(t, dtype, shape, name, device):
+    """Address of a contiguous tensor of a given shape (None entries: any length) on the cache's device."""
+    if t is None:
+        return None
+    if t.dtype != dtype:
+        raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
+    if t.dim() != len(shape) or any(w is not None and w != n for w, n in zip(shape, t.shape)):
+        raise ValueError("%s must be %s, got %s" % (name, list(shape), list(t.shape)))
+    if t.device != device:
+        raise ValueError("%s must be on the cache's device" % name)
+    if not t.is_contiguous():
+        raise ValueError("%s must be contiguous" % name)
+    return t.data_ptr()
+
+
+def _kv_call(fn, cache, stream, *args):
+    """Call fn on `stream`, or on the current stream of the cache's device, with that device current."""
+    dev = cache.device
+    if dev.index == torch.cuda.current_device():
+        s = stream.cuda_stream if stream is not None else torch.cuda.current_stream(dev).cuda_stream
+        return fn(*args, s)
+    with torch.cuda.device(dev):
+        s = stream.cuda_stream if stream is not None else torch.cuda.current_stream(dev).cuda_stream
+        return fn(*args, s)
+
+
+def _kv_same(cfg, cache):
+    if cache.layout != (cfg.kv_heads, cfg.head_dim, cfg.cache_dtype):
+        raise ValueError("the cache was made for another configuration")
+
+
+def kv_append(cfg: KVCfg, k, v, cu, pos0, cache: KVCache, rope=None, q=None, q_out=None, k_out=None, v_out=None,
+              status=None, stream=None):
+    """New tokens of a ragged batch into the cache: k, v [T][kv_heads][head_dim] bf16 (row i of sequence b at
+    cu[b] + i, position pos0[b] + i), keys and queries q [T][n_heads][head_dim] rotated by `rope` [rows][rope_dims / 2]
+    [2] fp32.  q_out (which may be q) takes the rotated queries, k_out / v_out the values as stored."""
+    _kv_same(cfg, cache)
+    dev, h, d = cache.device, cfg.kv_heads, cfg.head_dim
+    T, B = k.shape[0], cache.batch
+    kp, ks = _kv_rows(k, h, d, "k", dev)
+    vp, vs = _kv_rows(v, h, d, "v", dev)
+    if v.shape[0] != T:
+        raise ValueError("k and v must have the same rows")
+    qp = qs = op = os_ = None
+    if (q is None) != (q_out is None):
+        raise ValueError("q and q_out are given together")
+    if q is not None:
+        qp, qs = _kv_rows(q, cfg.n_heads, d, "q", dev)
+        op, os_ = _kv_rows(q_out, cfg.n_heads, d, "q_out", dev)
+        if q.shape[0] != T or q_out.shape[0] != T:
+            raise ValueError("q, q_out and k must have the same rows")
+    _check("csa2_kv_append", _kv_call(
+        load().csa2_kv_append, cache, stream, C.byref(cfg), B, T, qp, qs or 0, kp, ks, vp, vs,
+        _kv_ptr(cu, torch.int32, (B + 1,), "cu", dev), _kv_ptr(pos0, torch.int64, (B,), "pos0", dev),
+        _kv_ptr(rope, torch.float32, (None, cfg.rope_dims // 2, 2), "rope", dev), 0 if rope is None else rope.shape[0],
+        C.byref(cache._c), op, os_ or 0, _kv_ptr(k_out, torch.bfloat16, (T, h, d), "k_out", dev),
+        _kv_ptr(v_out, torch.bfloat16, (T, h, d), "v_out", dev), _kv_ptr(status, torch.int32, (1,), "status", dev)))
+
+
+def kv_workspace_bytes(cfg: KVCfg, B: int, T: int, max_q: int, max_kv: int) -> int:
+    """Workspace with which kv_attend and kv_cross_attend divide keys of these sizes as they would best."""
+    return int(load().csa2_kv_workspace_bytes(C.byref(cfg), B, T, max_q, max_kv))
+
+
+def _kv_attend(name, cfg, q, cu, cache, kv_len, max_q, max_kv, out, lse, scale, workspace, status, stream):
+    _kv_same(cfg, cache)
+    dev, h, d = cache.device, cfg.n_heads, cfg.head_dim
+    T, B = q.shape[0], cache.batch
+    qp, qs = _kv_rows(q, h, d, "q", dev)
+    op, os_ = _kv_rows(out, h, d, "out", dev)
+    if out.shape[0] != T:
+        raise ValueError("q and out must have the same rows")
+    wp, wn = None, 0
+    if workspace is not None:
+        if workspace.device != dev or not workspace.is_contiguous():
+            raise ValueError("workspace must be contiguous on the cache's device")
+        wp, wn = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    scale = 1.0 / math.sqrt(d) if scale is None else float(scale)
+    lib = load()
+    _check("csa2_" + name, _kv_call(
+        lib.csa2_kv_attend if name == "kv_attend" else lib.csa2_kv_cross_attend, cache, stream, C.byref(cfg), B, T, qp,
+        qs, _kv_ptr(cu, torch.int32, (B + 1,), "cu", dev), C.byref(cache._c),
+        _kv_ptr(kv_len, torch.int32, (B,), "kv_len", dev), int(max_q), int(max_kv), scale, op, os_,
+        _kv_ptr(lse, torch.float32, (T, h), "lse", dev), wp if wn else None, wn,
+        _kv_ptr(status, torch.int32, (1,), "status", dev)))
+
+
+def kv_attend(cfg: KVCfg, q, cu, cache: KVCache, kv_len, max_q: int, max_kv: int, out, lse=None, scale=None,
+              workspace=None, status=None, stream=None):
+    """Causal attention (over cfg.window keys if set) of each sequence's last rows, q [T][n_heads][head_dim] bf16 in a
+    ragged batch (row i of sequence b at cu[b] + i), over kv_len [B] int32 cached tokens -> out like q, lse
+    [T][n_heads] fp32.  `workspace` (kv_workspace_bytes) lets the keys be divided among more CTAs."""
+    _kv_attend("kv_attend", cfg, q, cu, cache, kv_len, max_q, max_kv, out, lse, scale, workspace, status, stream)
+
+
+def kv_cross_attend(cfg: KVCfg, q, cu, cache: KVCache, kv_len, max_q: int, max_kv: int, out, lse=None, scale=None,
+                    workspace=None, status=None, stream=None):
+    """kv_attend without a causal mask: every row of sequence b sees all kv_len[b] states of the cache (an encoder's)."""
+    _kv_attend("kv_cross_attend", cfg, q, cu, cache, kv_len, max_q, max_kv, out, lse, scale, workspace, status, stream)
 
 
 class Captured:

@@ -1,0 +1,89 @@
+// Shared by the paged key / value operators (kv_append, kv_attend,
+// kv_cross_attend): the cache view, a ragged batch's sequence bounds and the
+// range of keys that a tile of query rows sees.
+#pragma once
+
+#include "internal.h"
+
+namespace csa2 {
+
+struct KvView {
+  uint8_t* k;
+  uint8_t* ks;
+  uint8_t* v;
+  uint8_t* vs;
+  const int32_t* table;
+  int32_t max_pages;
+  int32_t num_pages;
+};
+
+// Bytes of one (page, kv head) block of keys or of values.
+__host__ __device__ constexpr int kv_block_bytes(int dim, bool fp4) { return fp4 ? kPage * dim / 2 : kPage * dim * 2; }
+__host__ __device__ constexpr int kv_scale_bytes(int dim) { return kPage * dim / 16; }
+
+// Arguments of an attention call.
+struct KvAtt {
+  int T, n_heads, kv_heads, group, window, causal, max_q;
+  int max_kv;
+  const uint16_t* q;
+  int64_t q_stride;
+  const int32_t* cu;
+  KvView c;
+  const int32_t* kv_len;
+  float scale;  // softmax scale
+  uint16_t* out;
+  int64_t out_stride;
+  float* lse;
+  // division of the keys: parts of `part_pages` pages; with n_parts > 1 the
+  // partial outputs go to part_o [n_parts][T * n_heads][dim] and their
+  // log2-sum-exp2 to part_l [n_parts][T * n_heads]
+  int n_parts, part_pages;
+  float* part_o;
+  float* part_l;
+  int32_t* status;
+};
+
+// Rows and keys of sequence b; false (status set) when they are out of bounds.
+__device__ __forceinline__ bool kv_sequence(const KvAtt& a, int b, int& row0, int& rows, int& keys) {
+  const int lo = __ldg(a.cu + b), hi = __ldg(a.cu + b + 1), n = __ldg(a.kv_len + b);
+  if (lo < 0 || hi < lo || hi > a.T || hi - lo > a.max_q || n < 0 || n > a.max_kv) {
+    report(a.status, CSA2_ERR_BAD_INDEX);
+    return false;
+  }
+  row0 = lo;
+  rows = hi - lo;
+  keys = n;
+  return true;
+}
+
+// Position up to which (exclusive) row `i` of `rows` sees keys, and from which.
+__device__ __forceinline__ int kv_hi(const KvAtt& a, int i, int rows, int keys) {
+  if (!a.causal) return keys;
+  const int h = keys - rows + i + 1;
+  return h < 0 ? 0 : h;
+}
+__device__ __forceinline__ int kv_lo(const KvAtt& a, int i, int rows, int keys) {
+  if (!a.causal || a.window == 0) return 0;
+  const int l = keys - rows + i + 1 - a.window;
+  return l < 0 ? 0 : l;
+}
+
+// Pages [p0, p1) that rows i0 .. i1 (inclusive) see.
+__device__ __forceinline__ void kv_pages(const KvAtt& a, int i0, int i1, int rows, int keys, int& p0, int& p1) {
+  const int lo = kv_lo(a, i0, rows, keys), hi = kv_hi(a, i1, rows, keys);
+  p0 = lo / kPage;
+  p1 = hi > lo ? (hi + kPage - 1) / kPage : p0;
+}
+
+cudaError_t launch_kv_append(const csa2_kv_cfg& cfg, int B, int T, const uint16_t* q, int64_t q_stride,
+                             const uint16_t* k, int64_t k_stride, const uint16_t* v, int64_t v_stride,
+                             const int32_t* cu, const int64_t* pos0, const float* rope, int64_t rope_rows,
+                             const KvView& c, uint16_t* q_out, int64_t q_out_stride, uint16_t* k_out, uint16_t* v_out,
+                             int32_t* status, cudaStream_t stream);
+
+// n_parts and part_pages of a call, from sizes alone (the most parts it uses).
+void kv_plan(const csa2_kv_cfg& cfg, int B, int max_q, int max_kv, bool cross, int most_parts, int* n_parts,
+             int* part_pages);
+cudaError_t launch_kv_attend(const csa2_kv_cfg& cfg, int B, KvAtt& a, cudaStream_t stream);
+
+}  // namespace csa2

@@ -348,6 +348,118 @@ typedef struct csa2_layer_io {
 CSA2_API int32_t csa2_layer(const csa2_cfg* cfg, int32_t mode, csa2_group_state* state,
                    const csa2_layer_io* io, void* stream);
 
+/* ---- layers that keep whole keys and values ----
+ * The model's first two layers and its draft layers carry no compressor
+ * (compress ratio 0, config list of hn.213312.xyz sec. 1.2), a decoder attends
+ * to its encoder's states (CED, sec. 2.2), and the layers of other models that
+ * are served beside it are ordinary grouped-query layers: each kv head keeps
+ * one key and one value per token.  Three calls serve them over one paged
+ * cache, in the codec and page size of the latent caches:
+ *   csa2_kv_append        rotates new queries and keys, encodes keys and
+ *                         values and writes them to their pages;
+ *   csa2_kv_attend        causal attention (optionally over a sliding window)
+ *                         of each sequence's newest tokens, one or many;
+ *   csa2_kv_cross_attend  attention of a decoder's rows over all the states of
+ *                         another sequence (an encoder's), whatever its length.
+ *
+ * Ragged batches: the rows of all sequences stand one after another, row i of
+ * sequence b at cu[b] + i, cu[0] .. cu[B] ascending device int32 with
+ * cu[B] <= T; rows from cu[B] on are neither read nor written.  Rows of q, k, v
+ * and out may be slices of wider rows: a row is heads * head_dim contiguous
+ * bf16, `*_stride` is the distance between rows in elements (a multiple of 8).
+ *
+ * Paged KV cache: token j of sequence b lives in page
+ * block_table[b * max_pages + j / 64], slot j % 64; keys and values have pages
+ * of the same number in arrays of their own, num_pages pages of
+ *  FP4:  codes  [kv_heads][64][head_dim / 2] bytes (channel 2i in the low
+ *        nibble of byte i), scales [kv_heads][64][head_dim / 16] E4M3 bytes;
+ *  BF16: values [kv_heads][head_dim / 8][64][8] (16-byte chunk c of slot s at
+ *        (c * 64 + s) * 16), no scales.
+ * Pages may be shared by sequences as long as no call appends to a shared one.
+ * 16-byte alignment is required of q, k, v, their outputs, out and the pages,
+ * 256 of the workspace.
+ *
+ * Conditions found on the device (written to *status, the sequence's or page's
+ * work skipped): cu not ascending inside [0, T], more rows than max_q, a
+ * kv_len outside [0, max_kv], positions outside the cache or the rope table
+ * (CSA2_ERR_BAD_INDEX); a page id outside the pool (CSA2_ERR_BAD_PAGE). */
+enum { CSA2_ROPE_INTERLEAVED = 0, CSA2_ROPE_HALF = 1 };
+
+typedef struct csa2_kv_cfg {
+  int32_t n_heads;     /* query heads, a multiple of kv_heads, at most 1024 */
+  int32_t kv_heads;    /* key / value heads */
+  int32_t head_dim;    /* 64 or 128 */
+  int32_t cache_dtype; /* CSA2_CACHE_FP4 or CSA2_CACHE_BF16 */
+  int32_t window;      /* csa2_kv_attend: keys a query sees, itself included; 0 = all */
+  int32_t rope_dims;   /* leading channels rotated: a multiple of 16 up to head_dim; 0 = none */
+  int32_t rope_style;  /* pairs (2i, 2i + 1), or (i, i + rope_dims / 2) with CSA2_ROPE_HALF */
+  int32_t reserved;    /* must be 0 */
+} csa2_kv_cfg;
+
+typedef struct csa2_kv_cache {
+  void* k_data;
+  void* k_scales;             /* NULL for BF16 */
+  void* v_data;
+  void* v_scales;             /* NULL for BF16 */
+  const int32_t* block_table; /* [B][max_pages] page ids */
+  int32_t max_pages;          /* block_table row stride; capacity = 64 * max_pages */
+  int32_t num_pages;
+} csa2_kv_cache;
+
+/* Bytes of one page of keys (and of values): which = 0 data, 1 scales; 0 for
+ * an unsupported configuration (and for the scales of a BF16 cache). */
+CSA2_API size_t csa2_kv_page_bytes(const csa2_kv_cfg* cfg, int32_t which);
+
+/* New tokens into the cache (hn.213312.xyz sec. 2.4.4: quantised after RoPE).
+ * Row i of sequence b stands at position p = pos0[b] + i, which is its slot in
+ * the cache.  Over the first rope_dims channels of queries and keys each pair
+ * (a, b) becomes (a cos - b sin, a sin + b cos), the products and the sum each
+ * rounded to fp32, with (cos, sin) = rope[p][pair]; rope is [rope_rows]
+ * [rope_dims / 2][2] fp32, so a table with scaled frequencies serves scaled
+ * RoPE.  Keys and values are encoded as csa2_compress encodes entries (FP4:
+ * scale = RNE_E4M3(amax / 6), code = RNE_E2M1(x / scale), ties to even,
+ * saturating, a value that rounds to zero is +0; BF16: round to nearest even);
+ * queries are rounded to bf16 in q_out, which may be q itself.  k_out and
+ * v_out [T][kv_heads][head_dim], either or both NULL, receive the values as
+ * stored (FP4 values are exact in bf16).  A value that is not finite after the
+ * rotation sets CSA2_ERR_RANGE and is stored as the largest of its sign, NaN
+ * as 0, so that a cache never holds one.
+ * q and q_out may both be NULL (then n_heads is not used); rope is NULL
+ * if and only if rope_dims is 0. */
+CSA2_API int32_t csa2_kv_append(const csa2_kv_cfg* cfg, int32_t B, int32_t T, const uint16_t* q, int64_t q_stride,
+                                const uint16_t* k, int64_t k_stride, const uint16_t* v, int64_t v_stride,
+                                const int32_t* cu, const int64_t* pos0, const float* rope, int64_t rope_rows,
+                                const csa2_kv_cache* cache, uint16_t* q_out, int64_t q_out_stride, uint16_t* k_out,
+                                uint16_t* v_out, int32_t* status, void* stream);
+
+/* Workspace bytes with which csa2_kv_attend and csa2_kv_cross_attend divide
+ * the keys of these sizes as they would best; they take any workspace (NULL
+ * included) and divide less where it is smaller.  Two calls that may overlap
+ * (other streams, graphs replayed at once) need workspaces of their own. */
+CSA2_API size_t csa2_kv_workspace_bytes(const csa2_kv_cfg* cfg, int32_t B, int32_t T, int32_t max_q, int32_t max_kv);
+
+/* Attention over the cache: head h reads kv head h / (n_heads / kv_heads),
+ * out = softmax(scale * q . K) V over the keys the row sees, in fp32, rounded
+ * to bf16; lse (natural log, [T][n_heads] fp32) may be NULL.
+ *  csa2_kv_attend: the rows of sequence b are its last positions, row i of n
+ *    at position kv_len[b] - n + i, and see positions 0 .. their own, or the
+ *    last `window` of these.
+ *  csa2_kv_cross_attend: every row sees all kv_len[b] keys (window must be 0).
+ * A row that sees nothing (kv_len 0, or more rows than keys) is 0 with lse
+ * -inf.  max_q and max_kv bound the rows and keys of a sequence (they size the
+ * grid).  A page whose id is outside the pool counts as not seen.  Cache slots
+ * from kv_len on may hold anything.  A query row that is not finite yields NaN
+ * or unspecified values in its own outputs alone. */
+CSA2_API int32_t csa2_kv_attend(const csa2_kv_cfg* cfg, int32_t B, int32_t T, const uint16_t* q, int64_t q_stride,
+                                const int32_t* cu, const csa2_kv_cache* cache, const int32_t* kv_len, int32_t max_q,
+                                int32_t max_kv, float scale, uint16_t* out, int64_t out_stride, float* lse,
+                                void* workspace, size_t workspace_bytes, int32_t* status, void* stream);
+CSA2_API int32_t csa2_kv_cross_attend(const csa2_kv_cfg* cfg, int32_t B, int32_t T, const uint16_t* q,
+                                      int64_t q_stride, const int32_t* cu, const csa2_kv_cache* cache,
+                                      const int32_t* kv_len, int32_t max_q, int32_t max_kv, float scale,
+                                      uint16_t* out, int64_t out_stride, float* lse, void* workspace,
+                                      size_t workspace_bytes, int32_t* status, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -1,0 +1,440 @@
+"""Paged key / value operators on the GPU against their plain restatement in fp64."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import compressed_sparse_attention_07_gb300 as csa
+from tests import _kv
+
+pytestmark = pytest.mark.gpu
+
+FP4, BF16 = csa.CACHE_FP4, csa.CACHE_BF16
+HALF, INTER = csa.ROPE_HALF, csa.ROPE_INTERLEAVED
+
+
+def _dev(x, dtype=torch.bfloat16):
+    return torch.from_numpy(np.ascontiguousarray(x)).to("cuda").to(dtype)
+
+
+def _cu(lengths):
+    return torch.tensor([0] + list(np.cumsum(lengths)), dtype=torch.int32, device="cuda")
+
+
+def _status():
+    return torch.zeros(1, dtype=torch.int32, device="cuda")
+
+
+def _cache(cfg, batch, capacity, seed=0):
+    pages = batch * max(1, -(-capacity // 64))
+    order = np.random.default_rng(seed).permutation(pages + 3)[:pages]
+    return csa.KVCache(cfg, batch, capacity, page_order=order, spare_pages=3)
+
+
+def _noise(cache):
+    """Every bit pattern into the pages: E4M3 NaNs among the scales, NaN and infinities among bf16 values."""
+    for t in (cache.k_data, cache.v_data, cache.k_scales, cache.v_scales):
+        if t is not None:
+            t.view(torch.uint8).random_(0, 256)
+    for t in (cache.k_scales, cache.v_scales):
+        if t is not None:
+            t.view(-1)[::3] = 0x7F
+    if cache.k_scales is None:
+        for t in (cache.k_data, cache.v_data):
+            t.view(-1)[::5] = float("nan")
+            t.view(-1)[1::5] = float("inf")
+
+
+# ----------------------------------------------------------------- append --
+
+@pytest.mark.parametrize("dtype", [FP4, BF16])
+@pytest.mark.parametrize("dim,hq,hkv,rope,style", [
+    (64, 1, 1, 64, INTER), (64, 6, 3, 32, HALF), (128, 28, 4, 128, HALF), (128, 8, 8, 64, INTER), (128, 16, 1, 96, HALF),
+    (64, 4, 2, 16, HALF), (128, 5, 5, 0, INTER)])
+def test_append_matches(dtype, dim, hq, hkv, rope, style):
+    rng = np.random.default_rng(dim + hq + rope)
+    lengths, starts = [3, 0, 1, 70, 64], [0, 5, 63, 60, 128]
+    cfg = csa.KVCfg(hq, hkv, dim, dtype, rope_dims=rope, rope_style=style)
+    cache = _cache(cfg, 5, 200)
+    _noise(cache)
+    before = [t.clone() for t in (cache.k_data, cache.v_data)]
+    T = sum(lengths)
+    rows = _kv.normal(rng, T + 4, hq + 2 * hkv + 1, dim)  # a projection's rows, wider than what is taken of them
+    rows[0, -2, :16] = 0.0                                # a group of zeros (scale code 0) among the values
+    wide = _dev(rows)
+    q, k, v = wide[:, :hq], wide[:, hq:hq + hkv], wide[:, hq + hkv:hq + 2 * hkv]
+    q_out = torch.full((T + 4, hq, dim), 7.0, dtype=torch.bfloat16, device="cuda")
+    k_out, v_out = (torch.full((T + 4, hkv, dim), 7.0, dtype=torch.bfloat16, device="cuda") for _ in "kv")
+    st = _status()
+    table = csa.rope_table(300, rope) if rope else None
+    csa.kv_append(cfg, k, v, _cu(lengths), torch.tensor(starts, device="cuda"), cache, rope=table, q=q, q_out=q_out,
+                  k_out=k_out, v_out=v_out, status=st)
+    assert int(st.item()) == 0
+    pos = np.concatenate([np.arange(n) + s for n, s in zip(lengths, starts)])
+    host = table.cpu().numpy() if rope else None
+    x = rows[:T].astype(np.float64)
+    want_q = _kv.rotate(x[:, :hq], host, pos, rope, style == HALF)
+    want_k = _kv.rotate(x[:, hq:hq + hkv], host, pos, rope, style == HALF)
+    want_v = x[:, hq + hkv:hq + 2 * hkv]
+    assert torch.equal(q_out[:T].cpu(), torch.from_numpy(want_q).to(torch.bfloat16))
+    assert (q_out[T:] == 7).all() and (k_out[T:] == 7).all() and (v_out[T:] == 7).all()
+    t0 = 0
+    for b, (n, s) in enumerate(zip(lengths, starts)):
+        for kind, want, plain in (("k", want_k, k_out), ("v", want_v, v_out)):
+            w = want[t0:t0 + n]
+            val, codes, sc = _kv.fp4_round(w) if dtype == FP4 else (_kv.bf16(w), None, None)
+            got, gcodes, gsc = _kv.read(cache, cfg, b, kind, s + n)
+            assert np.array_equal(got[s:], val)
+            assert np.array_equal(plain[t0:t0 + n].double().cpu().numpy(), val)
+            if dtype == FP4:
+                assert np.array_equal(gcodes[s:], codes) and np.array_equal(gsc[s:], sc)
+        t0 += n
+    # nothing else changed: the written slots put back, the pages are as they were
+    tab = cache.block_table.cpu().numpy()
+    for t, old in zip((cache.k_data, cache.v_data), before):
+        for b, (n, s) in enumerate(zip(lengths, starts)):
+            for j in range(s, s + n):
+                at = (tab[b, j // 64], slice(None), j % 64) if dtype == FP4 else (tab[b, j // 64], slice(None), slice(None), j % 64)
+                t[at] = old[at]
+        assert torch.equal(t.view(torch.uint8), old.view(torch.uint8))
+
+
+def test_append_in_place_and_without_queries():
+    rng = np.random.default_rng(3)
+    cfg = csa.KVCfg(8, 2, 128, FP4, rope_dims=128, rope_style=HALF)
+    table = csa.rope_table(64, 128)
+    q, k, v = (_dev(_kv.normal(rng, 9, h, 128)) for h in (8, 2, 2))
+    a, b = _cache(cfg, 1, 64), _cache(cfg, 1, 64)
+    pos0 = torch.tensor([11], device="cuda")
+    q_out = torch.empty_like(q)
+    csa.kv_append(cfg, k, v, _cu([9]), pos0, a, rope=table, q=q, q_out=q_out)
+    csa.kv_append(cfg, k, v, _cu([9]), pos0, b, rope=table)
+    same = q.clone()
+    csa.kv_append(cfg, k, v, _cu([9]), pos0, b, rope=table, q=same, q_out=same)
+    assert torch.equal(same, q_out)
+    assert torch.equal(a.k_data, b.k_data) and torch.equal(a.v_scales, b.v_scales)
+
+
+@pytest.mark.parametrize("dtype", [FP4, BF16])
+def test_append_of_what_is_not_finite(dtype):
+    cfg = csa.KVCfg(2, 1, 64, dtype, rope_dims=0)
+    cache = _cache(cfg, 1, 64)
+    k = torch.full((2, 1, 64), 6.0, dtype=torch.bfloat16, device="cuda")  # scale 1, code 6
+    v = k.clone()
+    v[0, 0, 3], v[0, 0, 20], v[1, 0, 40] = float("inf"), float("nan"), float("-inf")
+    st = _status()
+    out = torch.empty_like(v)
+    csa.kv_append(cfg, k, v, _cu([2]), torch.zeros(1, dtype=torch.int64, device="cuda"), cache, v_out=out, status=st)
+    assert csa.status_string(int(st.item())) == csa.status_string(19)
+    assert torch.isfinite(out.float()).all() and out[0, 0, 3] > 1000 and out[1, 0, 40] < -1000
+    assert out[0, 0, 20] == 0 and out[0, 0, 21] == 6 and out[0, 0, 50] == 6
+    assert np.isfinite(_kv.read(cache, cfg, 0, "v", 2)[0]).all()
+
+
+def test_append_reports_places_out_of_bounds():
+    cfg = csa.KVCfg(2, 1, 64, FP4, rope_dims=64)
+    x = torch.ones(4, 1, 64, dtype=torch.bfloat16, device="cuda")
+    for code, starts, lens, rows, page in ((17, [62, 0], [3, 1], 300, None), (17, [-1, 0], [3, 1], 300, None),
+                                           (17, [9, 0], [3, 1], 10, None), (16, [0, 0], [3, 1], 300, 77),
+                                           (16, [0, 0], [3, 1], 300, -1), (17, [0, 0], [3, 2], 300, None)):
+        cache = csa.KVCache(cfg, 2, 64)
+        if page is not None:
+            cache.block_table[0, 0] = page
+        st = _status()
+        csa.kv_append(cfg, x, x, _cu(lens), torch.tensor(starts, device="cuda"), cache, rope=csa.rope_table(rows, 64),
+                      status=st)
+        assert int(st.item()) == code
+        # the other sequence is written (unless its own rows reach past T)
+        assert bool(cache.k_data[1].any()) == (lens[1] == 1)
+        if page is not None or starts[0] == 0:
+            assert bool(cache.k_data[0].any()) == (page is None)
+
+
+# -------------------------------------------------------------- attention --
+
+def _attend_case(cfg, nq, kv, cross=False, seed=0, workspace=True, std=1.0, scale=None, pad=0, wide=0, slack=0,
+                 noise=True, capture=False):
+    rng = np.random.default_rng(seed)
+    B, D, T = len(nq), cfg.head_dim, sum(nq)
+    cache = _cache(cfg, B, max(max(kv), 1) + 70, seed)
+    if noise:
+        _noise(cache)
+    ks, vs = [], []
+    for b, n in enumerate(kv):
+        for kind, into in (("k", ks), ("v", vs)):
+            x = _kv.normal(rng, n, cfg.kv_heads, D)
+            if n:
+                _kv.fill(cache, cfg, b, kind, x)
+            into.append(_kv.fp4_round(x)[0] if cfg.cache_dtype == FP4 else x)
+    rows = _kv.normal(rng, T + pad, cfg.n_heads + wide, D, std=std)
+    q = _dev(rows)[:, : cfg.n_heads]
+    out = torch.full((T + pad, cfg.n_heads + wide, D), 7.0, dtype=torch.bfloat16, device="cuda")[:, : cfg.n_heads]
+    lse = torch.full((T + pad, cfg.n_heads), 7.0, device="cuda")
+    st = _status()
+    mq, mk = max(nq) + slack, max(kv) + (70 if slack else 0)
+    need = csa.kv_workspace_bytes(cfg, B, T + pad, mq, mk)
+    ws = torch.full((need,), 255, dtype=torch.uint8, device="cuda") if workspace and need else None
+    scale = 1 / math.sqrt(D) if scale is None else scale
+    call = csa.kv_cross_attend if cross else csa.kv_attend
+    cu, lens = _cu(nq), torch.tensor(kv, dtype=torch.int32, device="cuda")
+
+    def go():
+        call(cfg, q, cu, cache, lens, mq, mk, out, lse=lse, scale=scale, workspace=ws, status=st)
+
+    if capture:
+        run = csa.capture(go)
+        out.fill_(7.0)
+        lse.fill_(7.0)
+        run()
+        run()
+    else:
+        go()
+    assert int(st.item()) == 0
+    assert (out[T:] == 7).all() and (lse[T:] == 7).all()
+    t0 = 0
+    o, l = out.double().cpu().numpy(), lse.double().cpu().numpy()
+    for b, n in enumerate(nq):
+        want = _kv.attend(rows[t0:t0 + n, : cfg.n_heads], ks[b], vs[b], scale, not cross, cfg.window)
+        tol, ltol = _kv.tolerances(cfg, kv[b], *want)
+        got, gl = o[t0:t0 + n], l[t0:t0 + n]
+        empty = ~np.isfinite(want[1])
+        assert (gl[empty] == -np.inf).all() and (got[empty] == 0).all()
+        far = np.abs(got - want[0]) / tol
+        assert far.max(initial=0) <= 1, "sequence %d: %.3g of the tolerance" % (b, far.max())
+        lfar = np.abs(np.where(empty, 0, gl) - np.where(empty, 0, want[1])) / ltol
+        assert lfar.max(initial=0) <= 1, "sequence %d: lse %.3g of the tolerance" % (b, lfar.max())
+        t0 += n
+    return out
+
+
+HEADS = [(64, 1, 1), (128, 8, 1), (64, 7, 1), (128, 28, 4), (64, 16, 16), (128, 64, 2), (64, 24, 2)]
+
+
+@pytest.mark.parametrize("dtype", [FP4, BF16])
+@pytest.mark.parametrize("dim,hq,hkv", HEADS)
+def test_single_tokens(dtype, dim, hq, hkv):
+    _attend_case(csa.KVCfg(hq, hkv, dim, dtype), [1] * 9, [1, 2, 63, 64, 65, 0, 130, 257, 500], seed=dim + hq)
+
+
+@pytest.mark.parametrize("dtype", [FP4, BF16])
+@pytest.mark.parametrize("dim,hq,hkv", HEADS)
+@pytest.mark.parametrize("cross", [False, True])
+def test_ragged_rows(dtype, dim, hq, hkv, cross):
+    # more rows than keys (rows that see nothing), none, one, tiles that end inside a page
+    _attend_case(csa.KVCfg(hq, hkv, dim, dtype), [5, 0, 1, 33, 20, 65, 2], [5, 40, 90, 33, 7, 200, 0], cross=cross,
+                 seed=dim + hq, pad=3, slack=9)
+
+
+@pytest.mark.parametrize("dtype", [FP4, BF16])
+@pytest.mark.parametrize("dim,hq,hkv", [(128, 8, 8), (64, 8, 2), (128, 12, 1)])
+@pytest.mark.parametrize("window", [1, 17, 64, 100])
+def test_windows(dtype, dim, hq, hkv, window):
+    cfg = csa.KVCfg(hq, hkv, dim, dtype, window=window)
+    _attend_case(cfg, [1, 3, 70, 150], [300, 65, 70, 400], seed=window)
+
+
+@pytest.mark.parametrize("dtype", [FP4, BF16])
+@pytest.mark.parametrize("dim,hq,hkv", [(128, 8, 2), (64, 14, 2)])
+@pytest.mark.parametrize("nq", [1, 5, 40])
+@pytest.mark.parametrize("workspace", [False, True])
+def test_long_keys_divided_or_not(dtype, dim, hq, hkv, nq, workspace):
+    _attend_case(csa.KVCfg(hq, hkv, dim, dtype), [nq, nq], [6007, 1500], seed=nq, workspace=workspace)
+
+
+@pytest.mark.parametrize("dtype", [FP4, BF16])
+@pytest.mark.parametrize("cross", [False, True])
+def test_prompts(dtype, cross):
+    _attend_case(csa.KVCfg(8, 2, 128, dtype), [300, 129, 64], [700, 129, 100], cross=cross, seed=5)
+    _attend_case(csa.KVCfg(6, 3, 64, dtype), [260, 17], [261, 300], cross=cross, seed=6)
+
+
+@pytest.mark.parametrize("dtype", [FP4, BF16])
+@pytest.mark.parametrize("nq", [1, 3, 90])
+def test_rows_apart_and_extreme_scales(dtype, nq):
+    cfg = csa.KVCfg(8, 2, 64, dtype)
+    _attend_case(cfg, [nq, nq], [300, 100], seed=1, wide=3)
+    _attend_case(cfg, [nq, nq], [300, 100], seed=2, std=30.0)              # peaked: one key takes all
+    _attend_case(cfg, [nq, nq], [300, 100], seed=3, scale=-0.3)
+    _attend_case(cfg, [nq, nq], [300, 100], seed=4, scale=0.0)             # all keys alike
+    _attend_case(cfg, [nq, nq], [300, 100], seed=5, std=2.0 ** 60, scale=2.0 ** -63)   # beyond f16's range
+    _attend_case(cfg, [nq, nq], [300, 100], seed=6, std=2.0 ** -40, scale=2.0 ** 37)
+
+
+@pytest.mark.parametrize("dtype", [FP4, BF16])
+@pytest.mark.parametrize("nq,kv", [(1, 3000), (5, 900), (80, 500)])
+def test_same_results_each_time_and_in_a_graph(dtype, nq, kv):
+    cfg = csa.KVCfg(16, 2, 128, dtype)
+    first = _attend_case(cfg, [nq] * 3, [kv, kv // 2, kv - 7], seed=9)
+    again = _attend_case(cfg, [nq] * 3, [kv, kv // 2, kv - 7], seed=9)
+    graph = _attend_case(cfg, [nq] * 3, [kv, kv // 2, kv - 7], seed=9, capture=True)
+    assert torch.equal(first, again) and torch.equal(first, graph)
+
+
+@pytest.mark.parametrize("dtype", [FP4, BF16])
+@pytest.mark.parametrize("nq", [1, 60])
+def test_a_bad_query_stays_alone(dtype, nq):
+    cfg = csa.KVCfg(8, 2, 64, dtype)
+    cache = _cache(cfg, 1, 256)
+    rng = np.random.default_rng(8)
+    for kind in "kv":
+        _kv.fill(cache, cfg, 0, kind, _kv.normal(rng, 200, 2, 64))
+    q = _dev(_kv.normal(rng, nq, 8, 64))
+    lens = torch.tensor([200], dtype=torch.int32, device="cuda")
+    good, got = torch.empty_like(q), torch.empty_like(q)
+    csa.kv_attend(cfg, q, _cu([nq]), cache, lens, nq, 200, good)
+    q[nq - 1, 3, 5] = float("nan")
+    q[0, 6, 0] = float("inf")
+    csa.kv_attend(cfg, q, _cu([nq]), cache, lens, nq, 200, got)
+    keep = torch.ones(nq, 8, dtype=torch.bool, device="cuda")
+    keep[nq - 1, 3] = keep[0, 6] = False
+    assert torch.equal(good[keep], got[keep])
+
+
+@pytest.mark.parametrize("nq", [1, 70])
+def test_reports_lengths_and_pages_out_of_bounds(nq):
+    cfg = csa.KVCfg(4, 2, 64, FP4)
+    rng = np.random.default_rng(4)
+    T = 2 * nq
+
+    def run(kv, cu, table=None, max_q=nq, max_kv=256):
+        cache = csa.KVCache(cfg, 2, 256)
+        for b in (0, 1):
+            for kind in "kv":
+                _kv.fill(cache, cfg, b, kind, _kv.normal(rng, 200, 2, 64))
+        if table is not None:
+            cache.block_table[0, 1] = table
+        q = torch.ones(T, 4, 64, dtype=torch.bfloat16, device="cuda")
+        out, st = torch.full_like(q, 7.0), _status()
+        csa.kv_attend(cfg, q, torch.tensor(cu, dtype=torch.int32, device="cuda"), cache,
+                      torch.tensor(kv, dtype=torch.int32, device="cuda"), max_q, max_kv, out, status=st)
+        return int(st.item()), out
+
+    for kv, cu in (([257, 200], [0, nq, T]), ([-1, 200], [0, nq, T]), ([200, 200], [-1, nq, T])):
+        code, out = run(kv, cu)
+        assert code == 17 and (out[:nq] == 7).all() and not (out[nq:] == 7).any()
+    code, out = run([200, 200], [0, nq, T + 1])
+    assert code == 17 and (out[nq:] == 7).all()
+    code, out = run([200, 200], [0, nq + 1, nq])
+    assert code == 17 and (out == 7).all()
+    for page in (-1, 9, 1 << 30):
+        code, out = run([200, 200], [0, nq, T], table=page)
+        assert code == 16 and torch.isfinite(out.float()).all() and not (out == 7).any()
+
+
+@pytest.mark.parametrize("dtype", [FP4, BF16])
+def test_a_pool_past_32_bits(dtype):
+    """Pages whose byte offsets pass 2^32 are read and written where they are."""
+    cfg = csa.KVCfg(16, 8, 128, dtype, rope_dims=0)
+    page = 8 * 64 * (64 if dtype == FP4 else 256)
+    n = (1 << 32) // page + 40
+    shape = (n, 8, 64, 64) if dtype == FP4 else (n, 8, 16, 64, 8)
+    kind = torch.uint8 if dtype == FP4 else torch.bfloat16
+    k_data, v_data = (torch.empty(shape, dtype=kind, device="cuda") for _ in "kv")
+    sc = [torch.empty((n, 8, 64, 8), dtype=torch.uint8, device="cuda") for _ in "kv"] if dtype == FP4 else [None, None]
+    table = torch.tensor([[n - 1, 0, n - 7, n - 3]], dtype=torch.int32, device="cuda")
+    cache = csa.KVCache.over(cfg, k_data, v_data, table, *sc)
+    rng = np.random.default_rng(2)
+    x = _kv.normal(rng, 200, 32, 128)
+    zero = torch.zeros(1, dtype=torch.int64, device="cuda")
+    csa.kv_append(cfg, _dev(x[:, :8]), _dev(x[:, 8:16]), _cu([200]), zero, cache)
+    stored = [_kv.fp4_round(x[:, 8 * i:8 * i + 8])[0] if dtype == FP4 else x[:, 8 * i:8 * i + 8] for i in (0, 1)]
+    for nq in (1, 40):
+        q = x[:nq, 16:]
+        out = torch.empty(nq, 16, 128, dtype=torch.bfloat16, device="cuda")
+        lens = torch.tensor([200], dtype=torch.int32, device="cuda")
+        csa.kv_attend(cfg, _dev(q), _cu([nq]), cache, lens, nq, 200, out)
+        want = _kv.attend(q, *stored, 1 / math.sqrt(128), True)
+        assert (np.abs(out.double().cpu().numpy() - want[0]) <= _kv.tolerances(cfg, 200, *want)[0]).all()
+
+
+# --------------------------------------------------- used one after another --
+
+@pytest.mark.parametrize("dtype", [FP4, BF16])
+@pytest.mark.parametrize("window", [0, 50])
+def test_prompt_then_steps(dtype, window):
+    """A prompt appended and attended, then a token at a time: each step's rows equal those of the whole sequence
+    computed at once from what the cache holds."""
+    rng = np.random.default_rng(11)
+    cfg = csa.KVCfg(8, 2, 64, dtype, window=window, rope_dims=64)
+    prompt, steps, B = [37, 100], 4, 2
+    total = [n + steps for n in prompt]
+    cache = _cache(cfg, B, 128)
+    table = csa.rope_table(128, 64)
+    q, k, v = ([_kv.normal(rng, n, h, 64) for n in total] for h in (8, 2, 2))
+    lens = torch.zeros(B, dtype=torch.int32, device="cuda")
+    got = [[] for _ in range(B)]
+    at = [0] * B
+    for step in range(steps + 1):
+        n = prompt if step == 0 else [1] * B
+        cut = [slice(a, a + m) for a, m in zip(at, n)]
+        qd, kd, vd = (_dev(np.concatenate([x[b][cut[b]] for b in range(B)])) for x in (q, k, v))
+        pos0 = torch.tensor(at, dtype=torch.int64, device="cuda")
+        csa.kv_append(cfg, kd, vd, _cu(n), pos0, cache, rope=table, q=qd, q_out=qd)
+        at = [a + m for a, m in zip(at, n)]
+        lens.copy_(torch.tensor(at, dtype=torch.int32))
+        out = torch.empty_like(qd)
+        csa.kv_attend(cfg, qd, _cu(n), cache, lens, max(n), 128, out)
+        o = out.double().cpu().numpy()
+        got[0].append(o[: n[0]])
+        got[1].append(o[n[0]:])
+    host = table.cpu().numpy()
+    for b in range(B):
+        qr = _kv.bf16(_kv.rotate(q[b], host, np.arange(total[b]), 64, False))
+        ks, vs = (_kv.read(cache, cfg, b, kind, total[b])[0] for kind in "kv")
+        want = _kv.attend(qr, ks, vs, 1 / 8, True, window)
+        tol = _kv.tolerances(cfg, total[b], *want)[0]
+        assert (np.abs(np.concatenate(got[b]) - want[0]) <= tol).all()
+
+
+def test_decoder_over_its_encoder_in_graphs_on_two_streams():
+    """An encoder's states appended once (no rotation), then decoder steps over them captured in two graphs with
+    workspaces of their own and replayed on two streams at once."""
+    rng = np.random.default_rng(12)
+    cfg = csa.KVCfg(12, 4, 64, FP4, rope_dims=0)
+    enc, B = [1500, 700, 0], 3
+    cache = _cache(cfg, B, 1500)
+    x = [_kv.normal(rng, n, 8, 64) for n in enc]
+    rows = _dev(np.concatenate(x))
+    csa.kv_append(cfg, rows[:, :4], rows[:, 4:], _cu(enc), torch.zeros(B, dtype=torch.int64, device="cuda"), cache)
+    lens = torch.tensor(enc, dtype=torch.int32, device="cuda")
+    cu = _cu([1] * B)
+    runs = []
+    for i in range(2):
+        q = _kv.normal(rng, B, 12, 64)
+        qd = _dev(q)
+        out = torch.empty_like(qd)
+        ws = torch.empty(csa.kv_workspace_bytes(cfg, B, B, 1, 1500), dtype=torch.uint8, device="cuda")
+        g = csa.capture(lambda: csa.kv_cross_attend(cfg, qd, cu, cache, lens, 1, 1500, out, workspace=ws))
+        runs.append((q, out, g, torch.cuda.Stream(), qd, ws))
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for _, _, g, s, _, _ in runs:
+            with torch.cuda.stream(s):
+                g()
+    torch.cuda.synchronize()
+    for q, out, *_ in runs:
+        for b in range(B):
+            ks, vs = (_kv.read(cache, cfg, b, kind, enc[b])[0] for kind in "kv")
+            want = _kv.attend(q[b:b + 1], ks, vs, 1 / 8, False)
+            tol = _kv.tolerances(cfg, enc[b], *want)[0]
+            assert (np.abs(out[b:b + 1].double().cpu().numpy() - want[0]) <= tol).all()
+
+
+def test_sequences_that_share_pages():
+    """Samples of one prompt: their block tables name the same pages."""
+    rng = np.random.default_rng(13)
+    cfg = csa.KVCfg(8, 8, 64, FP4, rope_dims=0)
+    cache = _cache(cfg, 3, 200)
+    x = _kv.normal(rng, 130, 16, 64)
+    for kind, part in (("k", x[:, :8]), ("v", x[:, 8:])):
+        _kv.fill(cache, cfg, 0, kind, part)
+    cache.block_table[1].copy_(cache.block_table[0])
+    cache.block_table[2].copy_(cache.block_table[0])
+    q = _kv.normal(rng, 3, 8, 64)
+    out = torch.empty(3, 8, 64, dtype=torch.bfloat16, device="cuda")
+    lens = torch.tensor([130, 64, 1], dtype=torch.int32, device="cuda")
+    csa.kv_attend(cfg, _dev(q), _cu([1, 1, 1]), cache, lens, 1, 130, out)
+    for b, n in enumerate((130, 64, 1)):
+        want = _kv.attend(q[b:b + 1], _kv.fp4_round(x[:n, :8])[0], _kv.fp4_round(x[:n, 8:])[0], 1 / 8, True)
+        assert (np.abs(out[b:b + 1].double().cpu().numpy() - want[0]) <= _kv.tolerances(cfg, n, *want)[0]).all()

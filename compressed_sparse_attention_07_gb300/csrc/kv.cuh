@@ -17,6 +17,48 @@ struct KvView {
   int32_t num_pages;
 };
 
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ uint32_t f16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ uint32_t mul2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+  uint32_t r;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+  return r;
+}
+// Two E4M3 bytes -> f16 pair (exact).
+__device__ __forceinline__ uint32_t scales2(uint32_t pair) {
+  uint32_t r;
+  const uint16_t p = (uint16_t)pair;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(p));
+  return r;
+}
+// Eight E2M1 codes -> four f16 pairs.
+__device__ __forceinline__ void codes8(uint32_t w, uint32_t (&r)[4]) {
+  asm("{\n .reg .b8 b0, b1, b2, b3;\n mov.b32 {b0, b1, b2, b3}, %4;\n"
+      " cvt.rn.f16x2.e2m1x2 %0, b0;\n cvt.rn.f16x2.e2m1x2 %1, b1;\n"
+      " cvt.rn.f16x2.e2m1x2 %2, b2;\n cvt.rn.f16x2.e2m1x2 %3, b3;\n}\n"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+      : "r"(w));
+}
 // Bytes of one (page, kv head) block of keys or of values.
 __host__ __device__ constexpr int kv_block_bytes(int dim, bool fp4) { return fp4 ? kPage * dim / 2 : kPage * dim * 2; }
 __host__ __device__ constexpr int kv_scale_bytes(int dim) { return kPage * dim / 16; }
@@ -84,6 +126,14 @@ cudaError_t launch_kv_append(const csa2_kv_cfg& cfg, int B, int T, const uint16_
 // n_parts and part_pages of a call, from sizes alone (the most parts it uses).
 void kv_plan(const csa2_kv_cfg& cfg, int B, int max_q, int max_kv, bool cross, int most_parts, int* n_parts,
              int* part_pages);
+// The same of the tile kernel, which takes more rows of a kv head than
+// kMostRows; its launch, and the rows of its CTA.
+constexpr int kMostRows = 32;
+void kv_tiles_plan(const csa2_kv_cfg& cfg, int B, int max_q, int64_t max_kv, bool cross, int most_parts, int* n_parts,
+                   int* part_pages);
+cudaError_t launch_kv_tiles(const csa2_kv_cfg& cfg, int B, const KvAtt& a, cudaStream_t stream);
+int kv_tiles_rows();
+
 cudaError_t launch_kv_attend(const csa2_kv_cfg& cfg, int B, KvAtt& a, cudaStream_t stream);
 
 }  // namespace csa2

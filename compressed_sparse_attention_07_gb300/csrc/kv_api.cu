@@ -57,11 +57,12 @@ int32_t attend(const csa2_kv_cfg* cfg, bool cross, int32_t B, int32_t T, const u
       !aligned(kv_len, 4) || !aligned(lse, 4) || !aligned(status, 4) || !cache_ok(*cfg, cache))
     return CSA2_ERR_INVALID_ARG;
   if (workspace ? !aligned(workspace, 256) : workspace_bytes != 0) return CSA2_ERR_INVALID_ARG;
-  if (B > 65535) return CSA2_ERR_UNSUPPORTED;
+  const int64_t most = max_q < T ? max_q : T;  // rows of a sequence; row numbers are 32-bit in the kernels
+  if (B > 65535 || most * cfg->n_heads > (1 << 30)) return CSA2_ERR_UNSUPPORTED;
   if (max_kv > (int64_t)cache->max_pages * kPage) return CSA2_ERR_CAPACITY;
   KvAtt a = {};
   a.T = T, a.n_heads = cfg->n_heads, a.kv_heads = cfg->kv_heads, a.group = cfg->n_heads / cfg->kv_heads;
-  a.window = cfg->window, a.causal = cross ? 0 : 1, a.max_q = max_q < T ? max_q : T, a.max_kv = max_kv;
+  a.window = cfg->window, a.causal = cross ? 0 : 1, a.max_q = (int)most, a.max_kv = max_kv;
   a.q = q, a.q_stride = q_stride, a.cu = cu, a.c = view_of(*cache), a.kv_len = kv_len, a.scale = scale;
   a.out = out, a.out_stride = out_stride, a.lse = lse, a.status = status;
   const int64_t rows = (int64_t)T * cfg->n_heads;

@@ -30,7 +30,6 @@
 namespace csa2 {
 namespace {
 
-constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr int kWarps = 4;
 
 template <int D, bool kFp4, int NT>
@@ -49,46 +48,6 @@ struct Rows {
   static constexpr int kCtas = kSmem > 112 * 1024 ? 1 : (kSmem > 72 * 1024 || NT > 1) ? 2 : 3;
 };
 
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-__device__ __forceinline__ uint32_t f16x2(float lo, float hi) {
-  uint32_t r;
-  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
-}
-__device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
-  uint32_t r;
-  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
-}
-__device__ __forceinline__ uint32_t mul2(uint32_t a, uint32_t b) {
-  uint32_t r;
-  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-  return r;
-}
-__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
-  uint32_t r;
-  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
-  return r;
-}
-// Two E4M3 bytes -> f16 pair (exact).
-__device__ __forceinline__ uint32_t scales2(uint32_t pair) {
-  uint32_t r;
-  const uint16_t p = (uint16_t)pair;
-  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(p));
-  return r;
-}
-// Eight E2M1 codes -> four f16 pairs.
-__device__ __forceinline__ void codes8(uint32_t w, uint32_t (&r)[4]) {
-  asm("{\n .reg .b8 b0, b1, b2, b3;\n mov.b32 {b0, b1, b2, b3}, %4;\n"
-      " cvt.rn.f16x2.e2m1x2 %0, b0;\n cvt.rn.f16x2.e2m1x2 %1, b1;\n"
-      " cvt.rn.f16x2.e2m1x2 %2, b2;\n cvt.rn.f16x2.e2m1x2 %3, b3;\n}\n"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-      : "r"(w));
-}
 template <bool kF16>
 __device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                     uint32_t b1) {
@@ -273,7 +232,7 @@ __global__ void __launch_bounds__(kWarps * 32, Rows<D, kFp4, NT>::kCtas) kv_rows
   for (int it = 0; tile < te; tile += kWarps, ++it) {
     const int stage = it & 1;
     if ((filled >> stage) & 1u) {
-      if (!tc::mbar_wait(&bars[warp][stage], (phase >> stage) & 1u)) {
+      if (!__all_sync(0xffffffffu, tc::mbar_wait(&bars[warp][stage], (phase >> stage) & 1u))) {
         late = true;
         // nothing may land in shared memory after the CTA has left
         if ((filled >> (stage ^ 1)) & 1u) tc::mbar_wait(&bars[warp][stage ^ 1], (phase >> (stage ^ 1)) & 1u);
@@ -602,6 +561,8 @@ int row_blocks(int64_t n) { return n <= 8 ? 1 : n <= 16 ? 2 : 4; }
 void kv_plan(const csa2_kv_cfg& cfg, int B, int max_q, int max_kv, bool cross, int most_parts, int* n_parts,
              int* part_pages) {
   const int group = cfg.n_heads / cfg.kv_heads;
+  if ((int64_t)max_q * group > kMostRows)
+    return kv_tiles_plan(cfg, B, max_q, max_kv, cross, most_parts, n_parts, part_pages);
   const int nt = row_blocks((int64_t)max_q * group);
   const int64_t tiles = ((int64_t)max_q * group + 8 * nt - 1) / (8 * nt);
   int64_t pages = ((int64_t)max_kv + kPage - 1) / kPage;
@@ -633,13 +594,16 @@ cudaError_t launch_kv_attend(const csa2_kv_cfg& cfg, int B, KvAtt& a, cudaStream
   cudaError_t e;
 #define CSA2_ROWS(D, F) \
   (nt == 1 ? launch<D, F, 1>(B, a, stream) : nt == 2 ? launch<D, F, 2>(B, a, stream) : launch<D, F, 4>(B, a, stream))
-  if (cfg.head_dim == 128) e = fp4 ? CSA2_ROWS(128, true) : CSA2_ROWS(128, false);
+  const bool many = (int64_t)a.max_q * a.group > kMostRows;
+  const int tile_rows = many ? kv_tiles_rows() : 8 * nt;
+  if (many) e = launch_kv_tiles(cfg, B, a, stream);
+  else if (cfg.head_dim == 128) e = fp4 ? CSA2_ROWS(128, true) : CSA2_ROWS(128, false);
   else e = fp4 ? CSA2_ROWS(64, true) : CSA2_ROWS(64, false);
 #undef CSA2_ROWS
   if (e != cudaSuccess || a.n_parts <= 1) return e;
   const dim3 grid((unsigned)(((int64_t)a.max_q * a.n_heads + 7) / 8), B);
-  return cfg.head_dim == 128 ? launch_k(kv_join_kernel<128>, grid, dim3(256), 0, stream, 0, a, 8 * nt)
-                             : launch_k(kv_join_kernel<64>, grid, dim3(256), 0, stream, 0, a, 8 * nt);
+  return cfg.head_dim == 128 ? launch_k(kv_join_kernel<128>, grid, dim3(256), 0, stream, 0, a, tile_rows)
+                             : launch_k(kv_join_kernel<64>, grid, dim3(256), 0, stream, 0, a, tile_rows);
 }
 
 }  // namespace csa2

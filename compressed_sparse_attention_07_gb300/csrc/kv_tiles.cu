@@ -1,0 +1,436 @@
+// Attention of many query rows over the paged key / value cache (prompts,
+// chunks, a decoder's rows over its encoder) on the tensor cores.
+//
+// One CTA takes one kv head, 256 rows (two tiles of 128; a row is one query
+// head at one token) and a part of the keys, 128 at a time:
+//   S_j = Q_j K^T  (M = 128 rows, N = 128 keys)   TMEM columns 128 j
+//   P_j = exp2(S_j - m) as f16 (bf16 caches: bf16) over S_j, read by
+//   O_j += P_j V   (A from TMEM, N = head_dim)    TMEM columns 256 + D j
+// with the softmax of tile 0 beside the products of tile 1 and the other way
+// round.  Warps 0-3 and 4-7 hold the rows of the two tiles (thread = row =
+// TMEM lane), warps 8-11 bring keys and values into shared memory as
+// [channel chunk][128 keys][16 B] (which is K-major for the first product and
+// MN-major for the second), decoding FP4 to f16 on the way, one key a thread;
+// warp 12 issues the products.
+//
+// The output in TMEM is rescaled only when a row's maximum grew by more than
+// 2^8 since its last rescaling (weights up to 2^8 are as exact as those up to
+// 1), which after the first keys is rare.  Query rows over FP4 caches are
+// scaled by a power of two as in kv_rows.cu.
+#include <algorithm>
+
+#include "kv.cuh"
+#include "tc.cuh"
+
+namespace csa2 {
+namespace {
+
+constexpr int kTileRows = 128, kCtaRows = 256, kTileKeys = 128, kStages = 2;
+constexpr int kSoftWarps = 8, kLoadWarps = 4, kThreads = 32 * (kSoftWarps + kLoadWarps + 1);
+
+template <int D>
+struct Tiles {
+  static constexpr int kOperand = 128 * D * 2;  // one operand tile
+  static constexpr int kQ = 0, kK = 2 * kOperand, kV = kK + kStages * kOperand;
+  // one CTA per SM: it takes all of TMEM
+  static constexpr int kSmem = std::max(kV + kStages * kOperand, 120 * 1024);
+};
+
+// Chunk-major operand tile: element (row, channel) at ((c / 8) * 128 + row) * 16 + (c % 8) * 2.
+constexpr uint32_t kChunk = 128 * 16;
+
+template <int D, bool kFp4>
+__global__ void __launch_bounds__(kThreads, 1) kv_tiles_kernel(KvAtt a) {
+  using L = Tiles<D>;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  __shared__ __align__(8) uint64_t k_full[kStages], v_full[kStages], k_free[kStages], v_free[kStages], s_ready[2],
+      p_ready[2], o_full[2];
+  __shared__ uint32_t tmem_base;
+  __shared__ int late_flag;
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int n_tiles = gridDim.x / a.n_parts;
+  const int part = blockIdx.x % a.n_parts, kh = blockIdx.y, b = blockIdx.z;
+  const int tile0 = (n_tiles - 1 - (int)(blockIdx.x / a.n_parts)) * kCtaRows;  // the longest first
+  griddep_wait();
+  griddep_launch();
+  int row0, rows, keys;
+  if (!kv_sequence(a, b, row0, rows, keys)) return;
+  const int n_rows = rows * a.group;
+  if (tile0 >= n_rows) return;
+  const int last = min(tile0 + kCtaRows, n_rows) - 1;
+  int p0, p1;
+  kv_pages(a, tile0 / a.group, last / a.group, rows, keys, p0, p1);
+  const int n_act = (p1 - p0 + a.part_pages - 1) / a.part_pages;
+  if (part > 0 && part >= n_act) return;
+  const int pb = p0 + part * a.part_pages, pe = min(pb + a.part_pages, p1);
+  const int key0 = pb * kPage;
+  const int n_it = (pe - pb + 1) / 2;
+  const int both = tile0 + kTileRows < n_rows ? 2 : 1;
+  const int32_t* table = a.c.table + (int64_t)b * a.c.max_pages;
+
+  if (tid == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      tc::mbar_init(&k_full[s], 32 * kLoadWarps);
+      tc::mbar_init(&v_full[s], 32 * kLoadWarps);
+      tc::mbar_init(&k_free[s], 1);
+      tc::mbar_init(&v_free[s], 1);
+    }
+    for (int j = 0; j < 2; ++j) {
+      tc::mbar_init(&s_ready[j], 1);
+      tc::mbar_init(&p_ready[j], 128);
+      tc::mbar_init(&o_full[j], 1);
+    }
+    late_flag = 0;
+    tc::fence_mbar_init();
+  }
+  if (warp == kSoftWarps + kLoadWarps) {
+    tc::tmem_alloc(&tmem_base, 512);
+    tc::tmem_relinquish();
+  }
+
+  // ---- the query rows, f16 (bf16 caches: bf16)
+  float scale = 0.0f;
+  int hi = 0, lo = 0;
+  const int r = tile0 + tid;  // warps 0-7
+  if (warp < kSoftWarps) {
+    const bool live = r < n_rows;
+    const int i = live ? r / a.group : 0, h = kh * a.group + (live ? r % a.group : 0);
+    if (live) hi = kv_hi(a, i, rows, keys), lo = kv_lo(a, i, rows, keys);
+    const uint16_t* q = a.q + (int64_t)(row0 + i) * a.q_stride + h * D;
+    uint8_t* dst = smem + L::kQ + (tid / kTileRows) * L::kOperand + (tid % kTileRows) * 16;
+    const uint32_t sign = a.scale < 0.0f ? 0x80008000u : 0u;  // into the query: the scale is positive below
+    scale = fabsf(a.scale) * kLog2e;
+    uint4 w[D / 8];
+#pragma unroll
+    for (int c = 0; c < D / 8; ++c) {
+      w[c] = make_uint4(0, 0, 0, 0);
+      if (live) w[c] = __ldg(reinterpret_cast<const uint4*>(q) + c);
+    }
+    float down = 1.0f;
+    if constexpr (kFp4) {
+      uint32_t most = 0;
+#pragma unroll
+      for (int c = 0; c < D / 8; ++c) {
+        const uint32_t u[4] = {w[c].x, w[c].y, w[c].z, w[c].w};
+#pragma unroll
+        for (int y = 0; y < 4; ++y) most = max(most, max(u[y] & 0x7F80u, (u[y] >> 16) & 0x7F80u));
+      }
+      // the largest channel's exponent, biased, where its power of two and the
+      // inverse are both normal numbers
+      const uint32_t e = min(max(most >> 7, 1u), 253u);
+      down = __uint_as_float((254u - e) << 23);
+      scale *= __uint_as_float(e << 23);
+    }
+#pragma unroll
+    for (int c = 0; c < D / 8; ++c) {
+      uint32_t u[4] = {w[c].x, w[c].y, w[c].z, w[c].w};
+#pragma unroll
+      for (int y = 0; y < 4; ++y) {
+        if constexpr (kFp4)
+          u[y] = f16x2(__uint_as_float(u[y] << 16) * down, __uint_as_float(u[y] & 0xFFFF0000u) * down);
+        u[y] ^= sign;
+      }
+      *reinterpret_cast<uint4*>(dst + c * kChunk) = make_uint4(u[0], u[1], u[2], u[3]);
+    }
+  }
+  tc::fence_async_smem();
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  const uint32_t tb = tmem_base;
+  const uint32_t sbase = tc::smem_u32(smem);
+  bool ok = true;
+
+  if (warp < kSoftWarps) {
+    // ---------------------------------------------------------- softmax --
+    const int j = warp / 4;
+    const uint32_t lane_base = 32 * (warp & 3);
+    const uint32_t s_addr = tc::taddr(tb, lane_base, 128 * j), o_addr = tc::taddr(tb, lane_base, 256 + D * j);
+    float m = -INFINITY, l = 0.0f;
+    if (j < both) {
+      for (int it = 0; it < n_it; ++it) {
+        const int k0 = key0 + it * kTileKeys;
+        int v_lo = lo - k0, v_hi = hi - k0;  // the row's keys in this tile
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          const int pg = pb + 2 * it + x;
+          if (pg >= pe) {
+            v_hi = min(v_hi, 64 * x);
+          } else {
+            const int32_t id = __ldg(table + pg);
+            if (id < 0 || id >= a.c.num_pages) {
+              if (x == 0) v_lo = max(v_lo, 64);
+              else v_hi = min(v_hi, 64);
+            }
+          }
+        }
+        const bool masked = __any_sync(0xffffffffu, v_lo > 0 || v_hi < kTileKeys);
+        if (!__all_sync(0xffffffffu, tc::mbar_wait(&s_ready[j], it & 1))) {
+          ok = false;
+          break;
+        }
+        tc::fence_after_sync();
+        float top = -INFINITY;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          uint32_t s[32];
+          tc::tmem_ld32(s_addr + 32 * c, s);
+          tc::tmem_wait_ld();
+          if (masked) {
+#pragma unroll
+            for (int x = 0; x < 32; ++x)
+              if (32 * c + x >= v_lo && 32 * c + x < v_hi) top = fmaxf(top, __uint_as_float(s[x]));
+          } else {
+#pragma unroll
+            for (int x = 0; x < 32; ++x) top = fmaxf(top, __uint_as_float(s[x]));
+          }
+        }
+        if (top > -INFINITY) top *= scale;
+        const bool grew = top > m + 8.0f || (m == -INFINITY && top > -INFINITY);
+        if (__any_sync(0xffffffffu, grew)) {
+          const float f = (grew && m > -INFINITY) ? ex2(m - top) : 1.0f;
+          if (grew) m = top;
+          l *= f;
+          if (it > 0) {
+#pragma unroll
+            for (int c = 0; c < D / 16; ++c) {
+              uint32_t o[16];
+              tc::tmem_ld16(o_addr + 16 * c, o);
+              tc::tmem_wait_ld();
+#pragma unroll
+              for (int x = 0; x < 16; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * f);
+              tc::tmem_st16(o_addr + 16 * c, o);
+            }
+          }
+        }
+        const float z = m == -INFINITY ? 0.0f : m;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          uint32_t s[32];
+          tc::tmem_ld32(s_addr + 32 * c, s);
+          tc::tmem_wait_ld();
+          uint32_t p[16];
+#pragma unroll
+          for (int x = 0; x < 16; ++x) {
+            float u = ex2(fmaf(__uint_as_float(s[2 * x]), scale, -z));
+            float v = ex2(fmaf(__uint_as_float(s[2 * x + 1]), scale, -z));
+            if (masked) {
+              const int k = 32 * c + 2 * x;
+              if (k < v_lo || k >= v_hi) u = 0.0f;
+              if (k + 1 < v_lo || k + 1 >= v_hi) v = 0.0f;
+            }
+            l += u;
+            l += v;
+            p[x] = kFp4 ? f16x2(u, v) : bf16x2(u, v);
+          }
+          tc::tmem_st16(s_addr + 16 * c, p);
+        }
+        tc::tmem_wait_st();
+        tc::fence_before_sync();
+        tc::mbar_arrive(&p_ready[j]);
+      }
+    }
+    if (j < both && ok) {
+      const bool got = __all_sync(0xffffffffu, n_it == 0 || tc::mbar_wait(&o_full[j], 0));
+      ok = got;
+      if (got) {
+        tc::fence_after_sync();
+        const bool live = r < n_rows;
+        const int i = row0 + (live ? r / a.group : 0), h = kh * a.group + (live ? r % a.group : 0);
+        const int64_t at = (int64_t)i * a.n_heads + h;
+        const bool whole = n_act <= 1;
+        const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+        const float lse2 = l == 0.0f ? -INFINITY : m + log2f(l);
+        const int64_t pa = (int64_t)part * a.T * a.n_heads + at;
+        if (live) {
+          if (whole) {
+            if (a.lse) a.lse[at] = lse2 * kLn2;
+          } else {
+            a.part_l[pa] = lse2;
+          }
+        }
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c) {
+          uint32_t o[32];
+          if (n_it) {
+            tc::tmem_ld32(o_addr + 32 * c, o);
+            tc::tmem_wait_ld();
+          }
+#pragma unroll
+          for (int x = 0; x < 32; ++x) o[x] = l == 0.0f ? 0u : __float_as_uint(__uint_as_float(o[x]) * inv);
+          if (!live) continue;
+          if (whole) {
+            uint4* dst = reinterpret_cast<uint4*>(a.out + (int64_t)i * a.out_stride + h * D + 32 * c);
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+              uint32_t u[4];
+#pragma unroll
+              for (int y = 0; y < 4; ++y)
+                u[y] = bf16x2(__uint_as_float(o[8 * x + 2 * y]), __uint_as_float(o[8 * x + 2 * y + 1]));
+              dst[x] = make_uint4(u[0], u[1], u[2], u[3]);
+            }
+          } else {
+            uint4* dst = reinterpret_cast<uint4*>(a.part_o + pa * D + 32 * c);
+#pragma unroll
+            for (int x = 0; x < 8; ++x) dst[x] = make_uint4(o[4 * x], o[4 * x + 1], o[4 * x + 2], o[4 * x + 3]);
+          }
+        }
+      }
+    }
+  } else if (warp < kSoftWarps + kLoadWarps) {
+    // ------------------------------------------------- keys and values --
+    const int key = tid - 32 * kSoftWarps;  // of each tile
+    for (int it = 0; it < n_it && ok; ++it) {
+      const int s = it % kStages, at = key0 + it * kTileKeys + key, pg = pb + 2 * it + key / 64;
+      const bool seen = pg < pe && at < keys;
+      int32_t page = seen ? __ldg(table + pg) : -1;
+      if (seen && (page < 0 || page >= a.c.num_pages)) {
+        report(a.status, CSA2_ERR_BAD_PAGE);
+        page = -1;
+      }
+      const int64_t block = (int64_t)page * a.kv_heads + kh;
+      const int slot = at % kPage;
+#pragma unroll 1
+      for (int v = 0; v < 2; ++v) {
+        uint8_t* dst = smem + (v ? L::kV : L::kK) + s * L::kOperand + key * 16;
+        uint64_t* free_bar = v ? &v_free[s] : &k_free[s];
+        constexpr int W = kFp4 ? D / 32 : D / 8;  // 16-byte pieces of a row
+        uint4 w[W];
+        uint32_t f[D / 64];
+#pragma unroll
+        for (int x = 0; x < W; ++x) w[x] = make_uint4(0, 0, 0, 0);
+#pragma unroll
+        for (int x = 0; x < D / 64; ++x) f[x] = 0;
+        if (page >= 0) {
+          const uint8_t* src = (v ? a.c.v : a.c.k) + block * kv_block_bytes(D, kFp4);
+#pragma unroll
+          for (int x = 0; x < W; ++x)
+            w[x] = __ldg(reinterpret_cast<const uint4*>(src + (kFp4 ? slot * (D / 2) + 16 * x : (x * kPage + slot) * 16)));
+          if constexpr (kFp4) {
+            const uint8_t* sc = (v ? a.c.vs : a.c.ks) + block * kv_scale_bytes(D) + slot * (D / 16);
+#pragma unroll
+            for (int x = 0; x < D / 64; ++x) f[x] = __ldg(reinterpret_cast<const uint32_t*>(sc) + x);
+          }
+        }
+        if (it >= kStages && !tc::mbar_wait(free_bar, ((it / kStages) & 1) ^ 1)) {
+          ok = false;
+          break;
+        }
+        if constexpr (kFp4) {
+#pragma unroll
+          for (int x = 0; x < W; ++x) {  // 32 channels: two scales, four chunks
+            const uint32_t u[4] = {w[x].x, w[x].y, w[x].z, w[x].w};
+            const uint32_t sc = scales2(f[x / 2] >> (16 * (x & 1)));
+#pragma unroll
+            for (int y = 0; y < 4; ++y) {
+              uint32_t h[4];
+              codes8(u[y], h);
+              const uint32_t one = __byte_perm(sc, 0, y < 2 ? 0x1010u : 0x3232u);
+              *reinterpret_cast<uint4*>(dst + (4 * x + y) * kChunk) =
+                  make_uint4(mul2(h[0], one), mul2(h[1], one), mul2(h[2], one), mul2(h[3], one));
+            }
+          }
+        } else {
+#pragma unroll
+          for (int x = 0; x < W; ++x) *reinterpret_cast<uint4*>(dst + x * kChunk) = w[x];
+        }
+        tc::fence_async_smem();
+        tc::mbar_arrive(v ? &v_full[s] : &k_full[s]);
+      }
+    }
+  } else if (lane == 0 && n_it > 0) {
+    // --------------------------------------------------------- products --
+    constexpr uint32_t kIdS = tc::idesc_f16(128, kTileKeys, !kFp4, !kFp4, false, false);
+    constexpr uint32_t kIdO = tc::idesc_f16(128, D, !kFp4, !kFp4, false, true);
+    auto second = [&](int j, int it) -> bool {  // O_j += P_j V
+      if (!tc::mbar_wait(&p_ready[j], it & 1)) return false;
+      if (j == 0 && !tc::mbar_wait(&v_full[it % kStages], (it / kStages) & 1)) return false;
+      tc::fence_after_sync();
+      const uint32_t vb = sbase + L::kV + (it % kStages) * L::kOperand;
+#pragma unroll
+      for (int ks = 0; ks < kTileKeys / 16; ++ks)
+        tc::mma_ts(tb + 256 + D * j, tb + 128 * j + 8 * ks, tc::sdesc(vb + ks * 256, 128, kChunk), kIdO,
+                   (it > 0 || ks > 0) ? 1u : 0u);
+      return true;
+    };
+    for (int it = 0; it < n_it && ok; ++it) {
+      ok = tc::mbar_wait(&k_full[it % kStages], (it / kStages) & 1);
+      const uint32_t kb = sbase + L::kK + (it % kStages) * L::kOperand;
+      for (int j = 0; j < both && ok; ++j) {
+        if (it > 0) ok = second(j, it - 1);
+        if (!ok) break;
+        tc::fence_after_sync();
+        const uint32_t qb = sbase + L::kQ + j * L::kOperand;
+#pragma unroll
+        for (int ks = 0; ks < D / 16; ++ks)
+          tc::mma_ss(tb + 128 * j, tc::sdesc(qb + ks * 2 * kChunk, kChunk, 128), tc::sdesc(kb + ks * 2 * kChunk, kChunk, 128),
+                     kIdS, ks > 0);
+        tc::mma_commit(&s_ready[j]);
+      }
+      if (ok) {
+        tc::mma_commit(&k_free[it % kStages]);
+        if (it > 0) tc::mma_commit(&v_free[(it - 1) % kStages]);
+      }
+    }
+    for (int j = 0; j < both && ok; ++j) {
+      ok = second(j, n_it - 1);
+      if (ok) tc::mma_commit(&o_full[j]);
+    }
+    if (!ok) {  // nothing may run on after TMEM is given back
+      tc::mma_commit(&o_full[1]);
+      tc::mbar_wait(&o_full[1], 0);
+    }
+  }
+  __syncwarp();
+  if (!ok) late_flag = 1;
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  if (tid == 0 && late_flag) report(a.status, CSA2_ERR_TIMEOUT);
+  if (warp == kSoftWarps + kLoadWarps) tc::tmem_dealloc(tb, 512);
+}
+
+template <int D, bool kFp4>
+cudaError_t launch(int B, const KvAtt& a, cudaStream_t stream) {
+  auto kern = kv_tiles_kernel<D, kFp4>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Tiles<D>::kSmem);
+  if (e != cudaSuccess) return e;
+  const int64_t tiles = ((int64_t)a.max_q * a.group + kCtaRows - 1) / kCtaRows;
+  return launch_k(kern, dim3((unsigned)(tiles * a.n_parts), a.kv_heads, B), dim3(kThreads), Tiles<D>::kSmem, stream, 0, a);
+}
+
+}  // namespace
+
+void kv_tiles_plan(const csa2_kv_cfg& cfg, int B, int max_q, int64_t max_kv, bool cross, int most_parts, int* n_parts,
+                   int* part_pages) {
+  const int group = cfg.n_heads / cfg.kv_heads;
+  const int64_t tiles = ((int64_t)max_q * group + kCtaRows - 1) / kCtaRows;
+  int64_t pages = (max_kv + kPage - 1) / kPage;
+  if (cfg.window && !cross)
+    pages = std::min<int64_t>(pages, ((int64_t)cfg.window + std::min<int64_t>(max_q, kCtaRows / group + 2) + kPage - 2) / kPage + 1);
+  const int64_t steps = std::max<int64_t>(1, (pages + 1) / 2), base = B * cfg.kv_heads * tiles, slots = num_sms();
+  // the number of parts whose waves of CTAs end soonest; a CTA's start and end
+  // cost about three key tiles, joining about two
+  int64_t best = 1;
+  double cost = 1e30;
+  for (int64_t s = 1; s <= most_parts && s <= 64; ++s) {
+    const int64_t n = (steps + s - 1) / s;
+    if (s > 1 && n < 2) break;
+    const double c = (double)((base * s + slots - 1) / slots) * (n + 3) + (s > 1 ? 2 : 0);
+    if (c < cost * 0.999) cost = c, best = s;
+  }
+  const int64_t per = (steps + best - 1) / best;
+  *part_pages = (int)(2 * per);
+  *n_parts = (int)((steps + per - 1) / per);
+}
+
+cudaError_t launch_kv_tiles(const csa2_kv_cfg& cfg, int B, const KvAtt& a, cudaStream_t stream) {
+  const bool fp4 = cfg.cache_dtype == CSA2_CACHE_FP4;
+  if (cfg.head_dim == 128) return fp4 ? launch<128, true>(B, a, stream) : launch<128, false>(B, a, stream);
+  return fp4 ? launch<64, true>(B, a, stream) : launch<64, false>(B, a, stream);
+}
+
+int kv_tiles_rows() { return kCtaRows; }
+
+}  // namespace csa2

@@ -572,16 +572,19 @@ void kv_plan(const csa2_kv_cfg& cfg, int B, int max_q, int max_kv, bool cross, i
   const bool fp4 = cfg.cache_dtype == CSA2_CACHE_FP4;
   const int per_sm = cfg.head_dim == 128 ? (fp4 ? ctas<128, true>(nt) : ctas<128, false>(nt))
                                          : (fp4 ? ctas<64, true>(nt) : ctas<64, false>(nt));
-  const int64_t slots = (int64_t)per_sm * num_sms(), base = (int64_t)B * cfg.kv_heads * tiles;
-  // the number of parts whose waves of CTAs end soonest, a CTA costing its
-  // pages (four at a time) and about four pages' time besides; joining costs
-  // about two
+  const int64_t sms = num_sms(), base = (int64_t)B * cfg.kv_heads * tiles;
+  // The number of parts that ends soonest, in units of a page's share of an
+  // SM's throughput: an SM's CTAs (n at most, each its pages and about three
+  // pages' work besides) share it, but one warp alone needs about ten units for
+  // a page and a CTA eight to start and end; joining costs ten.
   int best = 1;
   double cost = 1e30;
   for (int s = 1; s <= most_parts && s <= 128; ++s) {
-    const int64_t pp = (pages + s - 1) / s;
+    const int64_t pp = (pages + s - 1) / s, n = (base * s + sms - 1) / sms;
     if (s > 1 && pp < kWarps) break;
-    const double c = (double)((base * s + slots - 1) / slots) * ((pp + kWarps - 1) / kWarps + 4) + (s > 1 ? 2 : 0);
+    const double c = std::max((double)n * (pp + 3),
+                              (double)((n + per_sm - 1) / per_sm) * ((pp + kWarps - 1) / kWarps * 10 + 8)) +
+                     (s > 1 ? 10 : 0);
     if (c < cost * 0.999) cost = c, best = s;
   }
   *part_pages = (int)((pages + best - 1) / best);

@@ -8,7 +8,7 @@
 //   O_j += P_j V   (A from TMEM, N = head_dim)    TMEM columns 256 + D j
 // with the softmax of tile 0 beside the products of tile 1 and the other way
 // round.  Warps 0-3 and 4-7 hold the rows of the two tiles (thread = row =
-// TMEM lane), warps 8-11 bring keys and values into shared memory as
+// TMEM lane, with 192 registers to hold its 128 scores), warps 8-11 bring keys and values into shared memory as
 // [channel chunk][128 keys][16 B] (which is K-major for the first product and
 // MN-major for the second), decoding FP4 to f16 on the way, one key a thread;
 // warp 12 issues the products.
@@ -26,7 +26,7 @@ namespace csa2 {
 namespace {
 
 constexpr int kTileRows = 128, kCtaRows = 256, kTileKeys = 128, kStages = 2;
-constexpr int kSoftWarps = 8, kLoadWarps = 4, kThreads = 32 * (kSoftWarps + kLoadWarps + 1);
+constexpr int kSoftWarps = 8, kLoadWarps = 4, kThreads = 512;
 
 template <int D>
 struct Tiles {
@@ -35,6 +35,35 @@ struct Tiles {
   // one CTA per SM: it takes all of TMEM
   static constexpr int kSmem = std::max(kV + kStages * kOperand, 120 * 1024);
 };
+
+template <int N>
+__device__ __forceinline__ void regs_inc() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void regs_dec() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+// Pairs of fp32 for the packed arithmetic.
+__device__ __forceinline__ uint64_t pack2(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void unpack2(uint64_t x, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(x));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
 
 // Chunk-major operand tile: element (row, channel) at ((c / 8) * 128 + row) * 16 + (c % 8) * 2.
 constexpr uint32_t kChunk = 128 * 16;
@@ -133,6 +162,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tiles_kernel(KvAtt a) {
       }
       *reinterpret_cast<uint4*>(dst + c * kChunk) = make_uint4(u[0], u[1], u[2], u[3]);
     }
+    scale = fmaxf(scale, 1e-37f);  // above 0: a hidden key's -inf stays -inf
   }
   tc::fence_async_smem();
   tc::fence_before_sync();
@@ -144,6 +174,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tiles_kernel(KvAtt a) {
 
   if (warp < kSoftWarps) {
     // ---------------------------------------------------------- softmax --
+    regs_inc<192>();
     const int j = warp / 4;
     const uint32_t lane_base = 32 * (warp & 3);
     const uint32_t s_addr = tc::taddr(tb, lane_base, 128 * j), o_addr = tc::taddr(tb, lane_base, 256 + D * j);
@@ -171,21 +202,25 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tiles_kernel(KvAtt a) {
           break;
         }
         tc::fence_after_sync();
-        float top = -INFINITY;
+        uint32_t s[4][32];
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          uint32_t s[32];
-          tc::tmem_ld32(s_addr + 32 * c, s);
-          tc::tmem_wait_ld();
-          if (masked) {
+        for (int c = 0; c < 4; ++c) tc::tmem_ld32(s_addr + 32 * c, s[c]);
+        tc::tmem_wait_ld();
+        if (masked) {
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
 #pragma unroll
             for (int x = 0; x < 32; ++x)
-              if (32 * c + x >= v_lo && 32 * c + x < v_hi) top = fmaxf(top, __uint_as_float(s[x]));
-          } else {
-#pragma unroll
-            for (int x = 0; x < 32; ++x) top = fmaxf(top, __uint_as_float(s[x]));
-          }
+              if (32 * c + x < v_lo || 32 * c + x >= v_hi) s[c][x] = 0xFF800000u;  // -inf
         }
+        float t4[4];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          t4[c] = __uint_as_float(s[c][0]);
+#pragma unroll
+          for (int x = 1; x < 32; ++x) t4[c] = fmaxf(t4[c], __uint_as_float(s[c][x]));
+        }
+        float top = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3]));
         if (top > -INFINITY) top *= scale;
         const bool grew = top > m + 8.0f || (m == -INFINITY && top > -INFINITY);
         if (__any_sync(0xffffffffu, grew)) {
@@ -193,7 +228,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tiles_kernel(KvAtt a) {
           if (grew) m = top;
           l *= f;
           if (it > 0) {
-#pragma unroll
+#pragma unroll 1
             for (int c = 0; c < D / 16; ++c) {
               uint32_t o[16];
               tc::tmem_ld16(o_addr + 16 * c, o);
@@ -204,27 +239,27 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tiles_kernel(KvAtt a) {
             }
           }
         }
-        const float z = m == -INFINITY ? 0.0f : m;
+        const uint64_t scale2 = pack2(scale, scale);
+        const float z = m == -INFINITY ? 0.0f : -m;
+        const uint64_t z2 = pack2(z, z);
+        uint64_t sum[2] = {pack2(l, 0.0f), 0ull};
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
-          uint32_t s[32];
-          tc::tmem_ld32(s_addr + 32 * c, s);
-          tc::tmem_wait_ld();
           uint32_t p[16];
 #pragma unroll
           for (int x = 0; x < 16; ++x) {
-            float u = ex2(fmaf(__uint_as_float(s[2 * x]), scale, -z));
-            float v = ex2(fmaf(__uint_as_float(s[2 * x + 1]), scale, -z));
-            if (masked) {
-              const int k = 32 * c + 2 * x;
-              if (k < v_lo || k >= v_hi) u = 0.0f;
-              if (k + 1 < v_lo || k + 1 >= v_hi) v = 0.0f;
-            }
-            l += u;
-            l += v;
+            float u, v;
+            unpack2(fma2(pack2(__uint_as_float(s[c][2 * x]), __uint_as_float(s[c][2 * x + 1])), scale2, z2), u, v);
+            u = ex2(u), v = ex2(v);
+            sum[x & 1] = add2(sum[x & 1], pack2(u, v));
             p[x] = kFp4 ? f16x2(u, v) : bf16x2(u, v);
           }
           tc::tmem_st16(s_addr + 16 * c, p);
+        }
+        {
+          float u, v;
+          unpack2(add2(sum[0], sum[1]), u, v);
+          l = u + v;
         }
         tc::tmem_wait_st();
         tc::fence_before_sync();
@@ -280,6 +315,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tiles_kernel(KvAtt a) {
     }
   } else if (warp < kSoftWarps + kLoadWarps) {
     // ------------------------------------------------- keys and values --
+    regs_dec<64>();
     const int key = tid - 32 * kSoftWarps;  // of each tile
     for (int it = 0; it < n_it && ok; ++it) {
       const int s = it % kStages, at = key0 + it * kTileKeys + key, pg = pb + 2 * it + key / 64;
@@ -339,7 +375,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tiles_kernel(KvAtt a) {
         tc::mbar_arrive(v ? &v_full[s] : &k_full[s]);
       }
     }
-  } else if (lane == 0 && n_it > 0) {
+  } else {
+    regs_dec<64>();
+    if (warp == kSoftWarps + kLoadWarps && lane == 0 && n_it > 0) {
     // --------------------------------------------------------- products --
     constexpr uint32_t kIdS = tc::idesc_f16(128, kTileKeys, !kFp4, !kFp4, false, false);
     constexpr uint32_t kIdO = tc::idesc_f16(128, D, !kFp4, !kFp4, false, true);
@@ -380,6 +418,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tiles_kernel(KvAtt a) {
     if (!ok) {  // nothing may run on after TMEM is given back
       tc::mma_commit(&o_full[1]);
       tc::mbar_wait(&o_full[1], 0);
+    }
     }
   }
   __syncwarp();

@@ -403,42 +403,46 @@ def rope_table(n: int, rope_dims: int, theta: float = 1e4, device="cuda"):
 
 def _kv_rows(t, heads, dim, name, device):
     """Address and row distance of [T][heads][dim] bf16 rows; a row is contiguous, the rows may stand apart."""
+    shape, stride = t.shape, t.stride()
+    if t.dtype is torch.bfloat16 and t.device == device and len(shape) == 3 and shape[1] == heads and \
+            shape[2] == dim and stride[2] == 1 and (stride[1] == dim or heads == 1):
+        return t.data_ptr(), (stride[0] if shape[0] > 1 else heads * dim)
     if t.dtype != torch.bfloat16:
         raise TypeError("%s must be torch.bfloat16, got %s" % (name, t.dtype))
-    shape, stride = t.shape, t.stride()
     if len(shape) != 3 or shape[1] != heads or shape[2] != dim:
         raise ValueError("%s must be [T][%d][%d], got %s" % (name, heads, dim, list(shape)))
-    if stride[2] != 1 or (heads > 1 and stride[1] != dim):
-        raise ValueError("%s: the channels of a row must be contiguous" % name)
     if t.device != device:
         raise ValueError("%s must be on the cache's device" % name)
-    return t.data_ptr(), (stride[0] if shape[0] > 1 else heads * dim)
+    raise ValueError("%s: the channels of a row must be contiguous" % name)
 
 
 def _kv_ptr(t, dtype, shape, name, device):
-    """Address of a contiguous tensor of a given shape (None entries: any length) on the cache's device."""
+    """Address of a contiguous tensor of a given shape on the cache's device."""
     if t is None:
         return None
+    if t.dtype is dtype and t.shape == shape and t.device == device and t.is_contiguous():
+        return t.data_ptr()
     if t.dtype != dtype:
         raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
-    if t.dim() != len(shape) or any(w is not None and w != n for w, n in zip(shape, t.shape)):
+    if t.shape != shape:
         raise ValueError("%s must be %s, got %s" % (name, list(shape), list(t.shape)))
     if t.device != device:
         raise ValueError("%s must be on the cache's device" % name)
-    if not t.is_contiguous():
-        raise ValueError("%s must be contiguous" % name)
-    return t.data_ptr()
+    raise ValueError("%s must be contiguous" % name)
+
+
+# the address of a device's current stream, without a Stream object around it
+_raw_stream = torch._C._cuda_getCurrentRawStream if hasattr(torch._C, "_cuda_getCurrentRawStream") else (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
 def _kv_call(fn, cache, stream, *args):
     """Call fn on `stream`, or on the current stream of the cache's device, with that device current."""
-    dev = cache.device
-    if dev.index == torch.cuda.current_device():
-        s = stream.cuda_stream if stream is not None else torch.cuda.current_stream(dev).cuda_stream
-        return fn(*args, s)
-    with torch.cuda.device(dev):
-        s = stream.cuda_stream if stream is not None else torch.cuda.current_stream(dev).cuda_stream
-        return fn(*args, s)
+    index = cache.device.index
+    if index == torch.cuda.current_device():
+        return fn(*args, _raw_stream(index) if stream is None else stream.cuda_stream)
+    with torch.cuda.device(index):
+        return fn(*args, _raw_stream(index) if stream is None else stream.cuda_stream)
 
 
 def _kv_same(cfg, cache):
@@ -458,6 +462,7 @@ def kv_append(cfg: KVCfg, k, v, cu, pos0, cache: KVCache, rope=None, q=None, q_o
     vp, vs = _kv_rows(v, h, d, "v", dev)
     if v.shape[0] != T:
         raise ValueError("k and v must have the same rows")
+    rows = 0 if rope is None else rope.shape[0]
     qp = qs = op = os_ = None
     if (q is None) != (q_out is None):
         raise ValueError("q and q_out are given together")
@@ -467,9 +472,9 @@ def kv_append(cfg: KVCfg, k, v, cu, pos0, cache: KVCache, rope=None, q=None, q_o
         if q.shape[0] != T or q_out.shape[0] != T:
             raise ValueError("q, q_out and k must have the same rows")
     _check("csa2_kv_append", _kv_call(
-        load().csa2_kv_append, cache, stream, C.byref(cfg), B, T, qp, qs or 0, kp, ks, vp, vs,
+        (_lib or load()).csa2_kv_append, cache, stream, C.byref(cfg), B, T, qp, qs or 0, kp, ks, vp, vs,
         _kv_ptr(cu, torch.int32, (B + 1,), "cu", dev), _kv_ptr(pos0, torch.int64, (B,), "pos0", dev),
-        _kv_ptr(rope, torch.float32, (None, cfg.rope_dims // 2, 2), "rope", dev), 0 if rope is None else rope.shape[0],
+        _kv_ptr(rope, torch.float32, (rows, cfg.rope_dims // 2, 2), "rope", dev), rows,
         C.byref(cache._c), op, os_ or 0, _kv_ptr(k_out, torch.bfloat16, (T, h, d), "k_out", dev),
         _kv_ptr(v_out, torch.bfloat16, (T, h, d), "v_out", dev), _kv_ptr(status, torch.int32, (1,), "status", dev)))
 
@@ -493,7 +498,7 @@ def _kv_attend(name, cfg, q, cu, cache, kv_len, max_q, max_kv, out, lse, scale, 
             raise ValueError("workspace must be contiguous on the cache's device")
         wp, wn = workspace.data_ptr(), workspace.numel() * workspace.element_size()
     scale = 1.0 / math.sqrt(d) if scale is None else float(scale)
-    lib = load()
+    lib = _lib or load()
     _check("csa2_" + name, _kv_call(
         lib.csa2_kv_attend if name == "kv_attend" else lib.csa2_kv_cross_attend, cache, stream, C.byref(cfg), B, T, qp,
         qs, _kv_ptr(cu, torch.int32, (B + 1,), "cu", dev), C.byref(cache._c),

@@ -126,6 +126,17 @@ cudaError_t launch_kv_append(const csa2_kv_cfg& cfg, int B, int T, const uint16_
 // n_parts and part_pages of a call, from sizes alone (the most parts it uses).
 void kv_plan(const csa2_kv_cfg& cfg, int B, int max_q, int max_kv, bool cross, int most_parts, int* n_parts,
              int* part_pages);
+// Let `kern` use `bytes` of dynamic shared memory: set once on each device.
+template <typename K>
+cudaError_t allow_smem(K kern, int bytes, bool (&done)[64]) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess || (dev < 64 && done[dev])) return e;
+  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess && dev < 64) done[dev] = true;
+  return e;
+}
+
 // The same of the tile kernel, which takes more rows of a kv head than
 // kMostRows; its launch, and the rows of its CTA.
 constexpr int kMostRows = 32;

@@ -16,7 +16,7 @@
 namespace csa2 {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 256, kMostPasses = 4;
 
 struct AppendArgs {
   int B, T, n_q, n_kv, rope_dims, half;
@@ -74,13 +74,29 @@ __device__ __forceinline__ uint32_t e2m1x8(const float (&x)[8], float s) {
   return m | (w & (nz << 3));
 }
 
-template <int kDim_, bool kFp4>
+template <int kDim_, bool kFp4, int kPasses>
 __global__ void __launch_bounds__(kThreads) kv_append_kernel(AppendArgs a) {
   constexpr int kLanes = kDim_ / 8;              // threads of a row
   constexpr int kRows = kThreads / kLanes;       // rows of a pass
   griddep_wait();  // every input may be the previous kernel's output
   griddep_launch();
   const int n = blockIdx.x, tid = threadIdx.x;
+  const int col = tid % kLanes, c0 = 8 * col;  // this thread's channels in every row
+  const int n_rows = a.n_q + 2 * a.n_kv;
+  const int first = (blockIdx.y * kPasses) * kRows + tid / kLanes;
+  // the rows first: their way from HBM covers the look-ups below
+  uint4 raw[kPasses];
+#pragma unroll
+  for (int p = 0; p < kPasses; ++p) {
+    const int r = first + p * kRows;
+    raw[p] = make_uint4(0, 0, 0, 0);
+    if (r < n_rows) {
+      const uint16_t* src = r < a.n_q            ? a.q + (int64_t)n * a.q_stride + r * kDim_
+                            : r < a.n_q + a.n_kv ? a.k + (int64_t)n * a.k_stride + (r - a.n_q) * kDim_
+                                                 : a.v + (int64_t)n * a.v_stride + (r - a.n_q - a.n_kv) * kDim_;
+      raw[p] = *reinterpret_cast<const uint4*>(src + c0);
+    }
+  }
   // the token's sequence: how many sequences end at or before it
   int b = 0;
   for (int i0 = 0; i0 < a.B; i0 += kThreads) {
@@ -101,7 +117,6 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(AppendArgs a) {
   const bool page_ok = page >= 0 && page < a.c.num_pages;
   if (!page_ok && tid == 0) report(a.status, CSA2_ERR_BAD_PAGE);
 
-  const int col = tid % kLanes, c0 = 8 * col;  // this thread's channels in every row
   const int pairs = a.rope_dims / 2;
   const bool turned = c0 < a.rope_dims;
   const bool second = a.half && c0 >= pairs;  // holds the b's of its pairs
@@ -127,21 +142,14 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(AppendArgs a) {
   }
   const int mate = second ? (tid & 31) - pairs / 8 : (tid & 31) + pairs / 8;
 
-  const int n_rows = a.n_q + 2 * a.n_kv;
-  for (int r0 = blockIdx.y * kRows; r0 < n_rows; r0 += gridDim.y * kRows) {
-    const int r = r0 + tid / kLanes;
+#pragma unroll
+  for (int p = 0; p < kPasses; ++p) {
+    const int r = first + p * kRows;
     const bool live = r < n_rows;
     const bool is_q = r < a.n_q, is_v = r >= a.n_q + a.n_kv;
     const int h = is_q ? r : is_v ? r - a.n_q - a.n_kv : r - a.n_q;
     float x[8];
-    if (live) {
-      const uint16_t* src = is_q ? a.q + (int64_t)n * a.q_stride : is_v ? a.v + (int64_t)n * a.v_stride
-                                                                         : a.k + (int64_t)n * a.k_stride;
-      unpack8(*reinterpret_cast<const uint4*>(src + h * kDim_ + c0), x);
-    } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) x[i] = 0.0f;
-    }
+    unpack8(raw[p], x);
     if (a.half) {  // uniform: the pair's other member is in another thread of the row
       float y[8];
 #pragma unroll
@@ -219,16 +227,17 @@ cudaError_t launch_kv_append(const csa2_kv_cfg& cfg, int B, int T, const uint16_
                status};
   const int rows = kThreads / (cfg.head_dim / 8);
   const int passes = (a.n_q + 2 * a.n_kv + rows - 1) / rows;
-  // CTAs of a token: all its passes at once while the tokens alone do not
-  // fill the GPU, then one CTA for a token
-  const int ny = (int64_t)T * passes <= 8 * num_sms() ? passes : 1;
-  const dim3 grid(T, ny), block(kThreads);
+  // a CTA for each of a token's passes while these do not fill the GPU, then a
+  // CTA for four
+  const bool few = (int64_t)T * passes <= 8 * num_sms();
+  const dim3 grid(T, few ? passes : (passes + kMostPasses - 1) / kMostPasses), block(kThreads);
   const bool fp4 = cfg.cache_dtype == CSA2_CACHE_FP4;
-  if (cfg.head_dim == 128)
-    return fp4 ? launch_k(kv_append_kernel<128, true>, grid, block, 0, stream, 0, a)
-               : launch_k(kv_append_kernel<128, false>, grid, block, 0, stream, 0, a);
-  return fp4 ? launch_k(kv_append_kernel<64, true>, grid, block, 0, stream, 0, a)
-             : launch_k(kv_append_kernel<64, false>, grid, block, 0, stream, 0, a);
+#define CSA2_APPEND(D, F)                                                                      \
+  (few ? launch_k(kv_append_kernel<D, F, 1>, grid, block, 0, stream, 0, a)                     \
+       : launch_k(kv_append_kernel<D, F, kMostPasses>, grid, block, 0, stream, 0, a))
+  if (cfg.head_dim == 128) return fp4 ? CSA2_APPEND(128, true) : CSA2_APPEND(128, false);
+  return fp4 ? CSA2_APPEND(64, true) : CSA2_APPEND(64, false);
+#undef CSA2_APPEND
 }
 
 }  // namespace csa2

@@ -543,7 +543,8 @@ template <int D, bool kFp4, int NT>
 cudaError_t launch(int B, const KvAtt& a, cudaStream_t stream) {
   using R = Rows<D, kFp4, NT>;
   auto kern = kv_rows_kernel<D, kFp4, NT>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, R::kSmem);
+  static bool done[64];
+  const cudaError_t e = allow_smem(kern, R::kSmem, done);
   if (e != cudaSuccess) return e;
   const int tiles = (int)(((int64_t)a.max_q * a.group + 8 * NT - 1) / (8 * NT));
   return launch_k(kern, dim3(a.n_parts, tiles * a.kv_heads, B), dim3(kWarps * 32), R::kSmem, stream, 0, a);

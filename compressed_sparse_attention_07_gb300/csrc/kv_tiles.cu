@@ -7,11 +7,16 @@
 //   P_j = exp2(S_j - m) as f16 (bf16 caches: bf16) over S_j, read by
 //   O_j += P_j V   (A from TMEM, N = head_dim)    TMEM columns 256 + D j
 // with the softmax of tile 0 beside the products of tile 1 and the other way
-// round.  Warps 0-3 and 4-7 hold the rows of the two tiles (thread = row =
-// TMEM lane, with 192 registers to hold its 128 scores), warps 8-11 bring keys and values into shared memory as
-// [channel chunk][128 keys][16 B] (which is K-major for the first product and
-// MN-major for the second), decoding FP4 to f16 on the way, one key a thread;
-// warp 12 issues the products.
+// round.  A CTA with no more than 128 rows (drafts, short texts) gives both
+// places to the same rows and key tiles in turn, and joins the two at the end.
+//
+// Warps 0-3 and 4-7 hold the rows (thread = row = TMEM lane, with 192 registers
+// to hold its 128 scores); warps 8-11 bring keys and values into shared memory
+// as [channel chunk][128 keys][16 B], which is K-major for the first product
+// and MN-major for the second: FP4 decoded to f16 on the way, one key a thread,
+// from a ring of pages that warp 13 fills with bulk copies (warps 14 and 15 help
+// decoding); bf16 pages, stored in that order, by bulk copies (warp 8 keys, warp
+// 9 values).  Warp 12 issues the products.
 //
 // The output in TMEM is rescaled only when a row's maximum grew by more than
 // 2^8 since its last rescaling (weights up to 2^8 are as exact as those up to
@@ -26,14 +31,24 @@ namespace csa2 {
 namespace {
 
 constexpr int kTileRows = 128, kCtaRows = 256, kTileKeys = 128, kStages = 2;
-constexpr int kSoftWarps = 8, kLoadWarps = 4, kThreads = 512;
+constexpr int kSoftWarps = 8, kThreads = 512;
+constexpr int kProductWarp = 12, kFetchWarp = 13, kDecodeWarps = 6;  // decoding: warps 8-11, 14 and 15
+constexpr int kRing = 3, kLongRing = 6;                              // undecoded tiles on their way
 
 template <int D>
 struct Tiles {
   static constexpr int kOperand = 128 * D * 2;  // one operand tile
   static constexpr int kQ = 0, kK = 2 * kOperand, kV = kK + kStages * kOperand;
+  // undecoded FP4 tiles: the ring's first kRing behind the operands, the others
+  // (turns) in the place of the second tile of queries
+  static constexpr int kRaw = kV + kStages * kOperand, kRawData = kTileKeys * D / 2, kRawScales = kTileKeys * D / 16;
+  static constexpr int kRawTile = kRawData + kRawScales;
+  static_assert((kLongRing - kRing) * kRawTile <= kOperand, "the long ring fits");
   // one CTA per SM: it takes all of TMEM
-  static constexpr int kSmem = std::max(kV + kStages * kOperand, 120 * 1024);
+  static constexpr int kSmem = std::max(kRaw + kRing * kRawTile, 120 * 1024);
+  __device__ static __forceinline__ int raw(int slot) {
+    return slot < kRing ? kRaw + slot * kRawTile : kQ + kOperand + (slot - kRing) * kRawTile;
+  }
 };
 
 template <int N>
@@ -76,6 +91,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tiles_kernel(KvAtt a) {
       p_ready[2], o_full[2];
   __shared__ uint32_t tmem_base;
   __shared__ int late_flag;
+  __shared__ __align__(8) uint64_t raw_full[kLongRing], raw_free[kLongRing], tail_full;
+  __shared__ int raw_pages[kLongRing];  // which of a tile's two pages are there
+  __shared__ float half_m[2][kTileRows], half_l[2][kTileRows];
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int n_tiles = gridDim.x / a.n_parts;
@@ -94,26 +112,35 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tiles_kernel(KvAtt a) {
   if (part > 0 && part >= n_act) return;
   const int pb = p0 + part * a.part_pages, pe = min(pb + a.part_pages, p1);
   const int key0 = pb * kPage;
-  const int n_it = (pe - pb + 1) / 2;
-  const int both = tile0 + kTileRows < n_rows ? 2 : 1;
+  const int n_it = (pe - pb + 1) / 2;  // key tiles
+  // turns: no second tile of rows, so that place 0 takes the even key tiles of
+  // the one there is and place 1 the odd ones
+  const bool turns = tile0 + kTileRows >= n_rows;
   const int32_t* table = a.c.table + (int64_t)b * a.c.max_pages;
 
   if (tid == 0) {
+    const uint32_t filling = kFp4 ? kTileKeys : 32;
+    for (int s = 0; s < kLongRing; ++s) {
+      tc::mbar_init(&raw_full[s], 1);
+      tc::mbar_init(&raw_free[s], kTileKeys);
+    }
     for (int s = 0; s < kStages; ++s) {
-      tc::mbar_init(&k_full[s], 32 * kLoadWarps);
-      tc::mbar_init(&v_full[s], 32 * kLoadWarps);
+      tc::mbar_init(&k_full[s], filling);
+      tc::mbar_init(&v_full[s], filling);
       tc::mbar_init(&k_free[s], 1);
       tc::mbar_init(&v_free[s], 1);
     }
     for (int j = 0; j < 2; ++j) {
+      const int live = n_rows - tile0 - (turns ? 0 : kTileRows * j);  // rows of place j
       tc::mbar_init(&s_ready[j], 1);
-      tc::mbar_init(&p_ready[j], 128);
+      tc::mbar_init(&p_ready[j], 32 * max(1, min(4, (live + 31) / 32)));
       tc::mbar_init(&o_full[j], 1);
     }
+    tc::mbar_init(&tail_full, 1);
     late_flag = 0;
     tc::fence_mbar_init();
   }
-  if (warp == kSoftWarps + kLoadWarps) {
+  if (warp == kProductWarp) {
     tc::tmem_alloc(&tmem_base, 512);
     tc::tmem_relinquish();
   }
@@ -121,7 +148,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tiles_kernel(KvAtt a) {
   // ---- the query rows, f16 (bf16 caches: bf16)
   float scale = 0.0f;
   int hi = 0, lo = 0;
-  const int r = tile0 + tid;  // warps 0-7
+  const int r = tile0 + (turns ? tid % kTileRows : tid);  // warps 0-7
   if (warp < kSoftWarps) {
     const bool live = r < n_rows;
     const int i = live ? r / a.group : 0, h = kh * a.group + (live ? r % a.group : 0);
@@ -151,16 +178,18 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tiles_kernel(KvAtt a) {
       down = __uint_as_float((254u - e) << 23);
       scale *= __uint_as_float(e << 23);
     }
+    if (!turns || tid < kTileRows) {
 #pragma unroll
-    for (int c = 0; c < D / 8; ++c) {
-      uint32_t u[4] = {w[c].x, w[c].y, w[c].z, w[c].w};
+      for (int c = 0; c < D / 8; ++c) {
+        uint32_t u[4] = {w[c].x, w[c].y, w[c].z, w[c].w};
 #pragma unroll
-      for (int y = 0; y < 4; ++y) {
-        if constexpr (kFp4)
-          u[y] = f16x2(__uint_as_float(u[y] << 16) * down, __uint_as_float(u[y] & 0xFFFF0000u) * down);
-        u[y] ^= sign;
+        for (int y = 0; y < 4; ++y) {
+          if constexpr (kFp4)
+            u[y] = f16x2(__uint_as_float(u[y] << 16) * down, __uint_as_float(u[y] & 0xFFFF0000u) * down);
+          u[y] ^= sign;
+        }
+        *reinterpret_cast<uint4*>(dst + c * kChunk) = make_uint4(u[0], u[1], u[2], u[3]);
       }
-      *reinterpret_cast<uint4*>(dst + c * kChunk) = make_uint4(u[0], u[1], u[2], u[3]);
     }
     scale = fmaxf(scale, 1e-37f);  // above 0: a hidden key's -inf stays -inf
   }
@@ -178,9 +207,11 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tiles_kernel(KvAtt a) {
     const int j = warp / 4;
     const uint32_t lane_base = 32 * (warp & 3);
     const uint32_t s_addr = tc::taddr(tb, lane_base, 128 * j), o_addr = tc::taddr(tb, lane_base, 256 + D * j);
+    const bool warp_live = r - lane < n_rows;
     float m = -INFINITY, l = 0.0f;
-    if (j < both) {
-      for (int it = 0; it < n_it; ++it) {
+    if (warp_live) {
+      int u = 0;  // key tiles of this place so far
+      for (int it = turns ? j : 0; it < n_it; it += turns ? 2 : 1, ++u) {
         const int k0 = key0 + it * kTileKeys;
         int v_lo = lo - k0, v_hi = hi - k0;  // the row's keys in this tile
 #pragma unroll
@@ -197,7 +228,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tiles_kernel(KvAtt a) {
           }
         }
         const bool masked = __any_sync(0xffffffffu, v_lo > 0 || v_hi < kTileKeys);
-        if (!__all_sync(0xffffffffu, tc::mbar_wait(&s_ready[j], it & 1))) {
+        if (!__all_sync(0xffffffffu, tc::mbar_wait(&s_ready[j], u & 1))) {
           ok = false;
           break;
         }
@@ -227,7 +258,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tiles_kernel(KvAtt a) {
           const float f = (grew && m > -INFINITY) ? ex2(m - top) : 1.0f;
           if (grew) m = top;
           l *= f;
-          if (it > 0) {
+          if (u > 0) {
 #pragma unroll 1
             for (int c = 0; c < D / 16; ++c) {
               uint32_t o[16];
@@ -248,52 +279,79 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tiles_kernel(KvAtt a) {
           uint32_t p[16];
 #pragma unroll
           for (int x = 0; x < 16; ++x) {
-            float u, v;
-            unpack2(fma2(pack2(__uint_as_float(s[c][2 * x]), __uint_as_float(s[c][2 * x + 1])), scale2, z2), u, v);
-            u = ex2(u), v = ex2(v);
-            sum[x & 1] = add2(sum[x & 1], pack2(u, v));
-            p[x] = kFp4 ? f16x2(u, v) : bf16x2(u, v);
+            float y0, y1;
+            unpack2(fma2(pack2(__uint_as_float(s[c][2 * x]), __uint_as_float(s[c][2 * x + 1])), scale2, z2), y0, y1);
+            y0 = ex2(y0), y1 = ex2(y1);
+            sum[x & 1] = add2(sum[x & 1], pack2(y0, y1));
+            p[x] = kFp4 ? f16x2(y0, y1) : bf16x2(y0, y1);
           }
           tc::tmem_st16(s_addr + 16 * c, p);
         }
         {
-          float u, v;
-          unpack2(add2(sum[0], sum[1]), u, v);
-          l = u + v;
+          float y0, y1;
+          unpack2(add2(sum[0], sum[1]), y0, y1);
+          l = y0 + y1;
         }
         tc::tmem_wait_st();
         tc::fence_before_sync();
         tc::mbar_arrive(&p_ready[j]);
       }
     }
-    if (j < both && ok) {
-      const bool got = __all_sync(0xffffffffu, n_it == 0 || tc::mbar_wait(&o_full[j], 0));
-      ok = got;
-      if (got) {
+    // ---- the rows' outputs: place 0's, place 1's, or (turns) both for one row
+    float f[2] = {0.0f, 0.0f};  // factors of the places' outputs
+    f[j] = 1.0f;
+    if (turns) {
+      half_m[j][tid % kTileRows] = m, half_l[j][tid % kTileRows] = l;
+      asm volatile("bar.sync 1, 256;" ::: "memory");
+      const float m0 = half_m[0][tid % kTileRows], m1 = half_m[1][tid % kTileRows];
+      m = fmaxf(m0, m1);
+      f[0] = m0 == -INFINITY ? 0.0f : ex2(m0 - m);
+      f[1] = m1 == -INFINITY ? 0.0f : ex2(m1 - m);
+      l = f[0] * half_l[0][tid % kTileRows] + f[1] * half_l[1][tid % kTileRows];
+    }
+    if (warp_live && ok) {
+      if (n_it > 0) {
+        if (!turns) ok = tc::mbar_wait(&o_full[j], 0);
+        else ok = tc::mbar_wait(&o_full[0], 0) && (n_it < 2 || tc::mbar_wait(&o_full[1], 0));
+      }
+      ok = __all_sync(0xffffffffu, ok);
+      if (ok) {
         tc::fence_after_sync();
         const bool live = r < n_rows;
         const int i = row0 + (live ? r / a.group : 0), h = kh * a.group + (live ? r % a.group : 0);
-        const int64_t at = (int64_t)i * a.n_heads + h;
+        const int64_t at = (int64_t)i * a.n_heads + h, pa = (int64_t)part * a.T * a.n_heads + at;
         const bool whole = n_act <= 1;
         const float inv = l == 0.0f ? 0.0f : 1.0f / l;
         const float lse2 = l == 0.0f ? -INFINITY : m + log2f(l);
-        const int64_t pa = (int64_t)part * a.T * a.n_heads + at;
-        if (live) {
-          if (whole) {
-            if (a.lse) a.lse[at] = lse2 * kLn2;
-          } else {
-            a.part_l[pa] = lse2;
-          }
+        if (live && (!turns || j == 0)) {
+          if (!whole) a.part_l[pa] = lse2;
+          else if (a.lse) a.lse[at] = lse2 * kLn2;
         }
+        const uint32_t o0 = tc::taddr(tb, lane_base, 256), o1 = tc::taddr(tb, lane_base, 256 + D);
+        // (turns) each place writes one half of the channels
 #pragma unroll
         for (int c = 0; c < D / 32; ++c) {
+          if (turns && c / (D / 64) != j) continue;
           uint32_t o[32];
-          if (n_it) {
-            tc::tmem_ld32(o_addr + 32 * c, o);
+          if (n_it > 0) {
+            tc::tmem_ld32((j == 1 && !turns ? o1 : o0) + 32 * c, o);
             tc::tmem_wait_ld();
-          }
+            const float g = inv * (turns ? f[0] : 1.0f);
 #pragma unroll
-          for (int x = 0; x < 32; ++x) o[x] = l == 0.0f ? 0u : __float_as_uint(__uint_as_float(o[x]) * inv);
+            for (int x = 0; x < 32; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * g);
+          }
+          if (turns && n_it > 1) {
+            uint32_t o2[32];
+            tc::tmem_ld32(o1 + 32 * c, o2);
+            tc::tmem_wait_ld();
+            const float g = inv * f[1];
+#pragma unroll
+            for (int x = 0; x < 32; ++x) o[x] = __float_as_uint(fmaf(__uint_as_float(o2[x]), g, __uint_as_float(o[x])));
+          }
+          if (l == 0.0f) {
+#pragma unroll
+            for (int x = 0; x < 32; ++x) o[x] = 0u;
+          }
           if (!live) continue;
           if (whole) {
             uint4* dst = reinterpret_cast<uint4*>(a.out + (int64_t)i * a.out_stride + h * D + 32 * c);
@@ -313,112 +371,234 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tiles_kernel(KvAtt a) {
         }
       }
     }
-  } else if (warp < kSoftWarps + kLoadWarps) {
-    // ------------------------------------------------- keys and values --
+  } else {
     regs_dec<64>();
-    const int key = tid - 32 * kSoftWarps;  // of each tile
-    for (int it = 0; it < n_it && ok; ++it) {
-      const int s = it % kStages, at = key0 + it * kTileKeys + key, pg = pb + 2 * it + key / 64;
-      const bool seen = pg < pe && at < keys;
-      int32_t page = seen ? __ldg(table + pg) : -1;
-      if (seen && (page < 0 || page >= a.c.num_pages)) {
-        report(a.status, CSA2_ERR_BAD_PAGE);
-        page = -1;
-      }
-      const int64_t block = (int64_t)page * a.kv_heads + kh;
-      const int slot = at % kPage;
-#pragma unroll 1
-      for (int v = 0; v < 2; ++v) {
-        uint8_t* dst = smem + (v ? L::kV : L::kK) + s * L::kOperand + key * 16;
-        uint64_t* free_bar = v ? &v_free[s] : &k_free[s];
-        constexpr int W = kFp4 ? D / 32 : D / 8;  // 16-byte pieces of a row
-        uint4 w[W];
-        uint32_t f[D / 64];
+    const int ring = turns ? kLongRing : kRing;
+    if (n_it == 0) {
+      // no key: nothing to bring or to multiply
+    } else if (warp == kProductWarp) {
+      // ------------------------------------------------------- products --
+      constexpr uint32_t kIdS = tc::idesc_f16(128, kTileKeys, !kFp4, !kFp4, false, false);
+      constexpr uint32_t kIdO = tc::idesc_f16(128, D, !kFp4, !kFp4, false, true);
+      // S_j = Q K^T with key tile `it`
+      auto first = [&](int j, int it) {
+        tc::fence_after_sync();
+        const uint32_t qb = sbase + L::kQ + (turns ? 0 : j) * L::kOperand;
+        const uint32_t kb = sbase + L::kK + (it % kStages) * L::kOperand;
+        if (tc::elect_one()) {
 #pragma unroll
-        for (int x = 0; x < W; ++x) w[x] = make_uint4(0, 0, 0, 0);
+          for (int ks = 0; ks < D / 16; ++ks)
+            tc::mma_ss(tb + 128 * j, tc::sdesc(qb + ks * 2 * kChunk, kChunk, 128),
+                       tc::sdesc(kb + ks * 2 * kChunk, kChunk, 128), kIdS, ks > 0);
+          tc::mma_commit(&s_ready[j]);
+        }
+        __syncwarp();
+      };
+      auto commit = [&](uint64_t* bar) {
+        if (tc::elect_one()) tc::mma_commit(bar);
+        __syncwarp();
+      };
+      auto wait = [&](uint64_t* bar, int parity) { return __all_sync(0xffffffffu, tc::mbar_wait(bar, parity)); };
+      // O_j += P_j V with key tile `it`, the u-th of place j
+      auto second = [&](int j, int it, int u) -> bool {
+        if (!wait(&p_ready[j], u & 1)) return false;
+        if ((turns || j == 0) && !wait(&v_full[it % kStages], (it / kStages) & 1)) return false;
+        tc::fence_after_sync();
+        const uint32_t vb = sbase + L::kV + (it % kStages) * L::kOperand;
+        if (tc::elect_one()) {
 #pragma unroll
-        for (int x = 0; x < D / 64; ++x) f[x] = 0;
-        if (page >= 0) {
-          const uint8_t* src = (v ? a.c.v : a.c.k) + block * kv_block_bytes(D, kFp4);
-#pragma unroll
-          for (int x = 0; x < W; ++x)
-            w[x] = __ldg(reinterpret_cast<const uint4*>(src + (kFp4 ? slot * (D / 2) + 16 * x : (x * kPage + slot) * 16)));
-          if constexpr (kFp4) {
-            const uint8_t* sc = (v ? a.c.vs : a.c.ks) + block * kv_scale_bytes(D) + slot * (D / 16);
-#pragma unroll
-            for (int x = 0; x < D / 64; ++x) f[x] = __ldg(reinterpret_cast<const uint32_t*>(sc) + x);
+          for (int ks = 0; ks < kTileKeys / 16; ++ks)
+            tc::mma_ts(tb + 256 + D * j, tb + 128 * j + 8 * ks, tc::sdesc(vb + ks * 256, 128, kChunk), kIdO,
+                       (u > 0 || ks > 0) ? 1u : 0u);
+        }
+        __syncwarp();
+        return true;
+      };
+      if (turns) {
+        for (int it = 0; it < n_it && ok; ++it) {
+          if (it >= 2) {
+            ok = second(it & 1, it - 2, it / 2 - 1);
+            if (ok) commit(&v_free[it % kStages]);
+          }
+          ok = ok && wait(&k_full[it % kStages], (it / kStages) & 1);
+          if (!ok) break;
+          first(it & 1, it);
+          commit(&k_free[it % kStages]);
+        }
+        for (int it = max(0, n_it - 2); it < n_it && ok; ++it) {
+          ok = second(it & 1, it, it / 2);
+          if (ok) commit(&o_full[it & 1]);
+        }
+      } else {
+        for (int it = 0; it < n_it && ok; ++it) {
+          for (int j = 0; j < 2 && ok; ++j) {
+            if (it > 0) ok = second(j, it - 1, it - 1);
+            if (ok && j == 0) ok = wait(&k_full[it % kStages], (it / kStages) & 1);
+            if (ok) first(j, it);
+          }
+          if (ok) {
+            commit(&k_free[it % kStages]);
+            if (it > 0) commit(&v_free[(it - 1) % kStages]);
           }
         }
-        if (it >= kStages && !tc::mbar_wait(free_bar, ((it / kStages) & 1) ^ 1)) {
+        for (int j = 0; j < 2 && ok; ++j) {
+          ok = second(j, n_it - 1, n_it - 1);
+          if (ok) commit(&o_full[j]);
+        }
+      }
+      if (!ok) {  // nothing may run on after TMEM is given back
+        commit(&o_full[1]);
+        tc::mbar_wait(&o_full[1], 0);
+      }
+    } else if (kFp4 && warp == kFetchWarp) {
+      // ------------------------------------ pages into the ring, K, V, K ..
+      int32_t id[2], next[2] = {-1, -1};
+      auto find = [&](int it) {
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          const int pg = pb + 2 * it + x;
+          next[x] = it < n_it && pg < pe ? __ldg(table + pg) : -1;
+        }
+      };
+      find(0);
+      for (int op = 0; op < 2 * n_it; ++op) {
+        const int slot = op % ring;
+        if ((op & 1) == 0) {
+          id[0] = next[0], id[1] = next[1];
+          find(op / 2 + 1);
+          const bool bad = id[0] < 0 || id[0] >= a.c.num_pages ||
+                           (pb + op + 1 < pe && (id[1] < 0 || id[1] >= a.c.num_pages));
+          if (bad && lane == 0) report(a.status, CSA2_ERR_BAD_PAGE);
+        }
+        if (op >= ring && !__all_sync(0xffffffffu, tc::mbar_wait(&raw_free[slot], ((op / ring) & 1) ^ 1))) {
           ok = false;
           break;
         }
-        if constexpr (kFp4) {
+        const int there = (id[0] >= 0 && id[0] < a.c.num_pages ? 1 : 0) | (id[1] >= 0 && id[1] < a.c.num_pages ? 2 : 0);
+        if (lane == 0) {
+          raw_pages[slot] = there;
+          tc::mbar_arrive_expect_tx(&raw_full[slot], __popc(there) * (L::kRawTile / 2));
+        }
+        __syncwarp();
+        const int x = lane & 1;  // page; lanes 0 and 1 its codes, 2 and 3 its scales
+        if (lane < 4 && ((there >> x) & 1)) {
+          uint8_t* dst = smem + L::raw(slot);
+          const int64_t block = (int64_t)(x ? id[1] : id[0]) * a.kv_heads + kh;
+          if (lane < 2)
+            tc::bulk_g2s(dst + x * (L::kRawData / 2), ((op & 1) ? a.c.v : a.c.k) + block * (L::kRawData / 2),
+                         L::kRawData / 2, &raw_full[slot]);
+          else
+            tc::bulk_g2s(dst + L::kRawData + x * (L::kRawScales / 2),
+                         ((op & 1) ? a.c.vs : a.c.ks) + block * (L::kRawScales / 2), L::kRawScales / 2, &raw_full[slot]);
+        }
+      }
+      // nothing may land in shared memory after the CTA has left
+      for (int op = max(0, 2 * n_it - ring); !ok && op < 2 * n_it; ++op) tc::mbar_wait(&raw_full[op % ring], (op / ring) & 1);
+    } else if (kFp4) {
+      // -------------------------------------------------------- decoding --
+      // 32 keys of an operand tile are a task; warps 8, 9 and 14 take the keys',
+      // warps 10, 11 and 15 the values' in turn (neither waits for the other's place)
+      const int v = warp == 10 || warp == 11 || warp == 15;
+      constexpr int W = D / 32, kStep = kDecodeWarps / 2;  // 16-byte pieces of a row
+      const int tasks = 4 * n_it;
+      // The pieces are taken from another one on by each few keys, so that the
+      // eight keys of a quarter warp's read lie in different banks.
+      auto first_piece = [&](int task) { return ((task & 3) * 32 + lane) / (256 / D); };
+      uint4 w[W];
+      uint32_t f[W];
+      auto read = [&](int task) -> bool {  // a row's codes and scales into registers
+        const int it = task / 4, op = 2 * it + v, slot = op % ring, key = (task & 3) * 32 + lane;
+        if (!__all_sync(0xffffffffu, tc::mbar_wait(&raw_full[slot], (op / ring) & 1))) return false;
+        const uint8_t* raw = smem + L::raw(slot);
+        const bool seen = key0 + it * kTileKeys + key < keys && pb + 2 * it + key / 64 < pe && ((raw_pages[slot] >> (key / 64)) & 1);
+        const int turn = first_piece(task);
 #pragma unroll
-          for (int x = 0; x < W; ++x) {  // 32 channels: two scales, four chunks
-            const uint32_t u[4] = {w[x].x, w[x].y, w[x].z, w[x].w};
-            const uint32_t sc = scales2(f[x / 2] >> (16 * (x & 1)));
+        for (int x = 0; x < W; ++x) {
+          const int piece = (x + turn) % W;
+          w[x] = *reinterpret_cast<const uint4*>(raw + key * (D / 2) + piece * 16);
+          f[x] = *reinterpret_cast<const uint16_t*>(raw + L::kRawData + key * (D / 16) + 2 * piece);
+          if (!seen) w[x] = make_uint4(0, 0, 0, 0), f[x] = 0;  // not there: anything
+        }
+        tc::mbar_arrive(&raw_free[slot]);
+        return true;
+      };
+      int task = warp < 12 ? warp & 1 : 2;
+      if (task < tasks) ok = read(task);
+      for (; task < tasks && ok; task += kStep) {
+        const int it = task / 4, s = it % kStages, turn = first_piece(task);
+        uint4 u[W];
+        uint32_t sc[W];
 #pragma unroll
-            for (int y = 0; y < 4; ++y) {
-              uint32_t h[4];
-              codes8(u[y], h);
-              const uint32_t one = __byte_perm(sc, 0, y < 2 ? 0x1010u : 0x3232u);
-              *reinterpret_cast<uint4*>(dst + (4 * x + y) * kChunk) =
-                  make_uint4(mul2(h[0], one), mul2(h[1], one), mul2(h[2], one), mul2(h[3], one));
-            }
+        for (int x = 0; x < W; ++x) u[x] = w[x], sc[x] = scales2(f[x]);
+        if (task + kStep < tasks) ok = read(task + kStep);
+        if (ok && it >= kStages)
+          ok = __all_sync(0xffffffffu, tc::mbar_wait(v ? &v_free[s] : &k_free[s], ((it / kStages) & 1) ^ 1));
+        if (!ok) break;
+        uint8_t* dst = smem + (v ? L::kV : L::kK) + s * L::kOperand + ((task & 3) * 32 + lane) * 16;
+#pragma unroll
+        for (int x = 0; x < W; ++x) {  // 32 channels: two scales, four chunks
+          uint8_t* at = dst + ((x + turn) % W) * (4 * kChunk);
+          const uint32_t c[4] = {u[x].x, u[x].y, u[x].z, u[x].w};
+#pragma unroll
+          for (int y = 0; y < 4; ++y) {
+            uint32_t h[4];
+            codes8(c[y], h);
+            const uint32_t one = __byte_perm(sc[x], 0, y < 2 ? 0x1010u : 0x3232u);
+            *reinterpret_cast<uint4*>(at + y * kChunk) =
+                make_uint4(mul2(h[0], one), mul2(h[1], one), mul2(h[2], one), mul2(h[3], one));
           }
-        } else {
-#pragma unroll
-          for (int x = 0; x < W; ++x) *reinterpret_cast<uint4*>(dst + x * kChunk) = w[x];
         }
         tc::fence_async_smem();
         tc::mbar_arrive(v ? &v_full[s] : &k_full[s]);
       }
-    }
-  } else {
-    regs_dec<64>();
-    if (warp == kSoftWarps + kLoadWarps && lane == 0 && n_it > 0) {
-    // --------------------------------------------------------- products --
-    constexpr uint32_t kIdS = tc::idesc_f16(128, kTileKeys, !kFp4, !kFp4, false, false);
-    constexpr uint32_t kIdO = tc::idesc_f16(128, D, !kFp4, !kFp4, false, true);
-    auto second = [&](int j, int it) -> bool {  // O_j += P_j V
-      if (!tc::mbar_wait(&p_ready[j], it & 1)) return false;
-      if (j == 0 && !tc::mbar_wait(&v_full[it % kStages], (it / kStages) & 1)) return false;
-      tc::fence_after_sync();
-      const uint32_t vb = sbase + L::kV + (it % kStages) * L::kOperand;
+    } else if (warp < kSoftWarps + 2) {
+      const bool v = warp > kSoftWarps;
+      const uint8_t* src = v ? a.c.v : a.c.k;
+      uint64_t* full = v ? v_full : k_full;
+      uint64_t* free_ = v ? v_free : k_free;
+      for (int it = 0; it < n_it; ++it) {
+        const int s = it % kStages;
+        uint8_t* dst = smem + (v ? L::kV : L::kK) + s * L::kOperand;
+        if (it >= kStages && !__all_sync(0xffffffffu, tc::mbar_wait(&free_[s], ((it / kStages) & 1) ^ 1))) {
+          ok = false;
+          break;
+        }
+        int64_t at[2];  // the tile's pages; -1: not there
 #pragma unroll
-      for (int ks = 0; ks < kTileKeys / 16; ++ks)
-        tc::mma_ts(tb + 256 + D * j, tb + 128 * j + 8 * ks, tc::sdesc(vb + ks * 256, 128, kChunk), kIdO,
-                   (it > 0 || ks > 0) ? 1u : 0u);
-      return true;
-    };
-    for (int it = 0; it < n_it && ok; ++it) {
-      ok = tc::mbar_wait(&k_full[it % kStages], (it / kStages) & 1);
-      const uint32_t kb = sbase + L::kK + (it % kStages) * L::kOperand;
-      for (int j = 0; j < both && ok; ++j) {
-        if (it > 0) ok = second(j, it - 1);
-        if (!ok) break;
-        tc::fence_after_sync();
-        const uint32_t qb = sbase + L::kQ + j * L::kOperand;
-#pragma unroll
-        for (int ks = 0; ks < D / 16; ++ks)
-          tc::mma_ss(tb + 128 * j, tc::sdesc(qb + ks * 2 * kChunk, kChunk, 128), tc::sdesc(kb + ks * 2 * kChunk, kChunk, 128),
-                     kIdS, ks > 0);
-        tc::mma_commit(&s_ready[j]);
+        for (int x = 0; x < 2; ++x) {
+          const int pg = pb + 2 * it + x;
+          const int32_t page = pg < pe ? __ldg(table + pg) : -1;
+          const bool there = page >= 0 && page < a.c.num_pages;
+          if (pg < pe && !there && lane == 0) report(a.status, CSA2_ERR_BAD_PAGE);
+          at[x] = there ? ((int64_t)page * a.kv_heads + kh) * kv_block_bytes(D, false) : -1;
+        }
+        // Scores of keys that are not seen are never used, but values are
+        // multiplied by weight 0: what lies in slots from kv_len on (anything) and
+        // in the place of pages that are not there has to be 0.
+        const int live = keys - key0 - it * kTileKeys;
+        const bool tail = v && live < kTileKeys && (live < kPage ? at[0] : at[1]) >= 0;
+        const uint32_t bytes = ((at[0] >= 0) + (at[1] >= 0)) * (L::kOperand / 2);
+        uint64_t* bar = tail ? &tail_full : &full[s];
+        if (lane == 0) tc::mbar_arrive_expect_tx(bar, bytes);
+        __syncwarp();
+        for (int x = lane; x < 2 * (D / 8); x += 32)
+          if ((x & 1 ? at[1] : at[0]) >= 0)
+            tc::bulk_g2s(dst + (x / 2) * kChunk + (x & 1) * (kPage * 16),
+                         src + (x & 1 ? at[1] : at[0]) + (x / 2) * (kPage * 16), kPage * 16, bar);
+        if (tail) {  // the last tile
+          ok = __all_sync(0xffffffffu, tc::mbar_wait(&tail_full, 0));
+          if (!ok) break;
+        }
+        if (v && (tail || bytes != L::kOperand)) {
+          for (int x = lane; x < kTileKeys * (D / 8); x += 32) {
+            const int key = x % kTileKeys;
+            if (key >= live || (key < kPage ? at[0] : at[1]) < 0)
+              *reinterpret_cast<uint4*>(dst + (x / kTileKeys) * kChunk + key * 16) = make_uint4(0, 0, 0, 0);
+          }
+          tc::fence_async_smem();
+        }
+        if (lane != 0 || tail) tc::mbar_arrive(&full[s]);
       }
-      if (ok) {
-        tc::mma_commit(&k_free[it % kStages]);
-        if (it > 0) tc::mma_commit(&v_free[(it - 1) % kStages]);
-      }
-    }
-    for (int j = 0; j < both && ok; ++j) {
-      ok = second(j, n_it - 1);
-      if (ok) tc::mma_commit(&o_full[j]);
-    }
-    if (!ok) {  // nothing may run on after TMEM is given back
-      tc::mma_commit(&o_full[1]);
-      tc::mbar_wait(&o_full[1], 0);
-    }
     }
   }
   __syncwarp();
@@ -427,13 +607,14 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tiles_kernel(KvAtt a) {
   __syncthreads();
   tc::fence_after_sync();
   if (tid == 0 && late_flag) report(a.status, CSA2_ERR_TIMEOUT);
-  if (warp == kSoftWarps + kLoadWarps) tc::tmem_dealloc(tb, 512);
+  if (warp == kProductWarp) tc::tmem_dealloc(tb, 512);
 }
 
 template <int D, bool kFp4>
 cudaError_t launch(int B, const KvAtt& a, cudaStream_t stream) {
   auto kern = kv_tiles_kernel<D, kFp4>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Tiles<D>::kSmem);
+  static bool done[64];
+  const cudaError_t e = allow_smem(kern, Tiles<D>::kSmem, done);
   if (e != cudaSuccess) return e;
   const int64_t tiles = ((int64_t)a.max_q * a.group + kCtaRows - 1) / kCtaRows;
   return launch_k(kern, dim3((unsigned)(tiles * a.n_parts), a.kv_heads, B), dim3(kThreads), Tiles<D>::kSmem, stream, 0, a);

@@ -364,7 +364,8 @@ CSA2_API int32_t csa2_layer(const csa2_cfg* cfg, int32_t mode, csa2_group_state*
  *
  * Ragged batches: the rows of all sequences stand one after another, row i of
  * sequence b at cu[b] + i, cu[0] .. cu[B] ascending device int32 with
- * cu[B] <= T; rows from cu[B] on are neither read nor written.  Rows of q, k, v
+ * cu[B] <= T; rows before cu[0] and from cu[B] on are not written, and what stands
+ * there has no effect.  Rows of q, k, v
  * and out may be slices of wider rows: a row is heads * head_dim contiguous
  * bf16, `*_stride` is the distance between rows in elements (a multiple of 8).
  *

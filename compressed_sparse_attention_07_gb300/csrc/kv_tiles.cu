@@ -10,13 +10,12 @@
 // round.  A CTA with no more than 128 rows (drafts, short texts) gives both
 // places to the same rows and key tiles in turn, and joins the two at the end.
 //
-// Warps 0-3 and 4-7 hold the rows (thread = row = TMEM lane, with 192 registers
-// to hold its 128 scores); warps 8-11 bring keys and values into shared memory
-// as [channel chunk][128 keys][16 B], which is K-major for the first product
-// and MN-major for the second: FP4 decoded to f16 on the way, one key a thread,
-// from a ring of pages that warp 13 fills with bulk copies (warps 14 and 15 help
-// decoding); bf16 pages, stored in that order, by bulk copies (warp 8 keys, warp
-// 9 values).  Warp 12 issues the products.
+// Warps 0-3 and 4-7 hold the rows (thread = row = TMEM lane, with registers for
+// its 128 scores); warps 8-11 bring keys, 12-15 values into shared memory as
+// [channel chunk][128 keys][16 B], which is K-major for the first product and
+// MN-major for the second: FP4 decoded to f16 on the way, one row a thread, from
+// a ring of pages that warp 17 fills with bulk copies; bf16 pages, stored in
+// that order, by bulk copies (warps 8 and 12).  Warp 16 issues the products.
 //
 // The output in TMEM is rescaled only when a row's maximum grew by more than
 // 2^8 since its last rescaling (weights up to 2^8 are as exact as those up to
@@ -31,8 +30,10 @@ namespace csa2 {
 namespace {
 
 constexpr int kTileRows = 128, kCtaRows = 256, kTileKeys = 128, kStages = 2;
-constexpr int kSoftWarps = 8, kThreads = 512;
-constexpr int kProductWarp = 12, kFetchWarp = 13, kDecodeWarps = 6;  // decoding: warps 8-11, 14 and 15
+constexpr int kSoftWarps = 8, kThreads = 640;
+constexpr int kKeyWarp = 8, kValueWarp = 12, kProductWarp = 16, kFetchWarp = 17;  // keys 8-11, values 12-15
+// registers of a thread: 96 at the launch, moved to the softmax's (640 x 96 = 256 x 168 + 384 x 48)
+constexpr int kSoftRegs = 168, kOtherRegs = 48;
 constexpr int kRing = 3, kLongRing = 6;                              // undecoded tiles on their way
 
 template <int D>
@@ -91,7 +92,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tiles_kernel(KvAtt a) {
       p_ready[2], o_full[2];
   __shared__ uint32_t tmem_base;
   __shared__ int late_flag;
-  __shared__ __align__(8) uint64_t raw_full[kLongRing], raw_free[kLongRing], tail_full;
+  __shared__ __align__(8) uint64_t raw_full[kLongRing], raw_free[kLongRing], tail_full, q_full;
   __shared__ int raw_pages[kLongRing];  // which of a tile's two pages are there
   __shared__ float half_m[2][kTileRows], half_l[2][kTileRows];
 
@@ -137,6 +138,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tiles_kernel(KvAtt a) {
       tc::mbar_init(&o_full[j], 1);
     }
     tc::mbar_init(&tail_full, 1);
+    tc::mbar_init(&q_full, 32 * kSoftWarps);
     late_flag = 0;
     tc::fence_mbar_init();
   }
@@ -145,55 +147,6 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tiles_kernel(KvAtt a) {
     tc::tmem_relinquish();
   }
 
-  // ---- the query rows, f16 (bf16 caches: bf16)
-  float scale = 0.0f;
-  int hi = 0, lo = 0;
-  const int r = tile0 + (turns ? tid % kTileRows : tid);  // warps 0-7
-  if (warp < kSoftWarps) {
-    const bool live = r < n_rows;
-    const int i = live ? r / a.group : 0, h = kh * a.group + (live ? r % a.group : 0);
-    if (live) hi = kv_hi(a, i, rows, keys), lo = kv_lo(a, i, rows, keys);
-    const uint16_t* q = a.q + (int64_t)(row0 + i) * a.q_stride + h * D;
-    uint8_t* dst = smem + L::kQ + (tid / kTileRows) * L::kOperand + (tid % kTileRows) * 16;
-    const uint32_t sign = a.scale < 0.0f ? 0x80008000u : 0u;  // into the query: the scale is positive below
-    scale = fabsf(a.scale) * kLog2e;
-    uint4 w[D / 8];
-#pragma unroll
-    for (int c = 0; c < D / 8; ++c) {
-      w[c] = make_uint4(0, 0, 0, 0);
-      if (live) w[c] = __ldg(reinterpret_cast<const uint4*>(q) + c);
-    }
-    float down = 1.0f;
-    if constexpr (kFp4) {
-      uint32_t most = 0;
-#pragma unroll
-      for (int c = 0; c < D / 8; ++c) {
-        const uint32_t u[4] = {w[c].x, w[c].y, w[c].z, w[c].w};
-#pragma unroll
-        for (int y = 0; y < 4; ++y) most = max(most, max(u[y] & 0x7F80u, (u[y] >> 16) & 0x7F80u));
-      }
-      // the largest channel's exponent, biased, where its power of two and the
-      // inverse are both normal numbers
-      const uint32_t e = min(max(most >> 7, 1u), 253u);
-      down = __uint_as_float((254u - e) << 23);
-      scale *= __uint_as_float(e << 23);
-    }
-    if (!turns || tid < kTileRows) {
-#pragma unroll
-      for (int c = 0; c < D / 8; ++c) {
-        uint32_t u[4] = {w[c].x, w[c].y, w[c].z, w[c].w};
-#pragma unroll
-        for (int y = 0; y < 4; ++y) {
-          if constexpr (kFp4)
-            u[y] = f16x2(__uint_as_float(u[y] << 16) * down, __uint_as_float(u[y] & 0xFFFF0000u) * down);
-          u[y] ^= sign;
-        }
-        *reinterpret_cast<uint4*>(dst + c * kChunk) = make_uint4(u[0], u[1], u[2], u[3]);
-      }
-    }
-    scale = fmaxf(scale, 1e-37f);  // above 0: a hidden key's -inf stays -inf
-  }
-  tc::fence_async_smem();
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
@@ -203,7 +156,57 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tiles_kernel(KvAtt a) {
 
   if (warp < kSoftWarps) {
     // ---------------------------------------------------------- softmax --
-    regs_inc<192>();
+    regs_inc<kSoftRegs>();
+    // the query rows, f16 (bf16 caches: bf16)
+    float scale;
+    int hi = 0, lo = 0;
+    const int r = tile0 + (turns ? tid % kTileRows : tid);
+    {
+      const bool live = r < n_rows;
+      const int i = live ? r / a.group : 0, h = kh * a.group + (live ? r % a.group : 0);
+      if (live) hi = kv_hi(a, i, rows, keys), lo = kv_lo(a, i, rows, keys);
+      const uint16_t* q = a.q + (int64_t)(row0 + i) * a.q_stride + h * D;
+      uint8_t* dst = smem + L::kQ + (tid / kTileRows) * L::kOperand + (tid % kTileRows) * 16;
+      const uint32_t sign = a.scale < 0.0f ? 0x80008000u : 0u;  // into the query: the scale is positive below
+      scale = fabsf(a.scale) * kLog2e;
+      uint4 w[D / 8];
+#pragma unroll
+      for (int c = 0; c < D / 8; ++c) {
+        w[c] = make_uint4(0, 0, 0, 0);
+        if (live) w[c] = __ldg(reinterpret_cast<const uint4*>(q) + c);
+      }
+      float down = 1.0f;
+      if constexpr (kFp4) {
+        uint32_t most = 0;
+#pragma unroll
+        for (int c = 0; c < D / 8; ++c) {
+          const uint32_t u[4] = {w[c].x, w[c].y, w[c].z, w[c].w};
+#pragma unroll
+          for (int y = 0; y < 4; ++y) most = max(most, max(u[y] & 0x7F80u, (u[y] >> 16) & 0x7F80u));
+        }
+        // the largest channel's exponent, biased, where its power of two and the
+        // inverse are both normal numbers
+        const uint32_t e = min(max(most >> 7, 1u), 253u);
+        down = __uint_as_float((254u - e) << 23);
+        scale *= __uint_as_float(e << 23);
+      }
+      if (!turns || tid < kTileRows) {
+#pragma unroll
+        for (int c = 0; c < D / 8; ++c) {
+          uint32_t u[4] = {w[c].x, w[c].y, w[c].z, w[c].w};
+#pragma unroll
+          for (int y = 0; y < 4; ++y) {
+            if constexpr (kFp4)
+              u[y] = f16x2(__uint_as_float(u[y] << 16) * down, __uint_as_float(u[y] & 0xFFFF0000u) * down);
+            u[y] ^= sign;
+          }
+          *reinterpret_cast<uint4*>(dst + c * kChunk) = make_uint4(u[0], u[1], u[2], u[3]);
+        }
+      }
+      scale = fmaxf(scale, 1e-37f);  // above 0: a hidden key's -inf stays -inf
+    }
+    tc::fence_async_smem();
+    tc::mbar_arrive(&q_full);
     const int j = warp / 4;
     const uint32_t lane_base = 32 * (warp & 3);
     const uint32_t s_addr = tc::taddr(tb, lane_base, 128 * j), o_addr = tc::taddr(tb, lane_base, 256 + D * j);
@@ -239,10 +242,13 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tiles_kernel(KvAtt a) {
         tc::tmem_wait_ld();
         if (masked) {
 #pragma unroll
-          for (int c = 0; c < 4; ++c)
+          for (int c = 0; c < 4; ++c) {
+            const int from = min(max(v_lo - 32 * c, 0), 32), to = min(max(v_hi - 32 * c, 0), 32);
+            const uint32_t bits = (uint32_t)((1ull << to) - 1) & (uint32_t)(0xFFFFFFFFull << from);
 #pragma unroll
             for (int x = 0; x < 32; ++x)
-              if (32 * c + x < v_lo || 32 * c + x >= v_hi) s[c][x] = 0xFF800000u;  // -inf
+              if (!(bits & (1u << x))) s[c][x] = 0xFF800000u;  // -inf
+          }
         }
         float t4[4];
 #pragma unroll
@@ -372,7 +378,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tiles_kernel(KvAtt a) {
       }
     }
   } else {
-    regs_dec<64>();
+    regs_dec<kOtherRegs>();
     const int ring = turns ? kLongRing : kRing;
     if (n_it == 0) {
       // no key: nothing to bring or to multiply
@@ -414,6 +420,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tiles_kernel(KvAtt a) {
         __syncwarp();
         return true;
       };
+      ok = wait(&q_full, 0);
       if (turns) {
         for (int it = 0; it < n_it && ok; ++it) {
           if (it >= 2) {
@@ -494,24 +501,23 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tiles_kernel(KvAtt a) {
       }
       // nothing may land in shared memory after the CTA has left
       for (int op = max(0, 2 * n_it - ring); !ok && op < 2 * n_it; ++op) tc::mbar_wait(&raw_full[op % ring], (op / ring) & 1);
-    } else if (kFp4) {
+    } else if (kFp4 && warp < kProductWarp) {
       // -------------------------------------------------------- decoding --
-      // 32 keys of an operand tile are a task; warps 8, 9 and 14 take the keys',
-      // warps 10, 11 and 15 the values' in turn (neither waits for the other's place)
-      const int v = warp == 10 || warp == 11 || warp == 15;
-      constexpr int W = D / 32, kStep = kDecodeWarps / 2;  // 16-byte pieces of a row
-      const int tasks = 4 * n_it;
+      // a row of each tile for each thread: warps 8-11 keys, 12-15 values
+      constexpr int W = D / 32;  // 16-byte pieces of a row
+      const bool v = warp >= kValueWarp;
+      const int key = tid % kTileKeys;
       // The pieces are taken from another one on by each few keys, so that the
       // eight keys of a quarter warp's read lie in different banks.
-      auto first_piece = [&](int task) { return ((task & 3) * 32 + lane) / (256 / D); };
-      uint4 w[W];
-      uint32_t f[W];
-      auto read = [&](int task) -> bool {  // a row's codes and scales into registers
-        const int it = task / 4, op = 2 * it + v, slot = op % ring, key = (task & 3) * 32 + lane;
-        if (!__all_sync(0xffffffffu, tc::mbar_wait(&raw_full[slot], (op / ring) & 1))) return false;
+      const int turn = key / (256 / D);
+      for (int it = 0; it < n_it; ++it) {
+        const int op = 2 * it + v, slot = op % ring, s = it % kStages;
+        ok = __all_sync(0xffffffffu, tc::mbar_wait(&raw_full[slot], (op / ring) & 1));
+        if (!ok) break;
         const uint8_t* raw = smem + L::raw(slot);
         const bool seen = key0 + it * kTileKeys + key < keys && pb + 2 * it + key / 64 < pe && ((raw_pages[slot] >> (key / 64)) & 1);
-        const int turn = first_piece(task);
+        uint4 w[W];
+        uint32_t f[W];
 #pragma unroll
         for (int x = 0; x < W; ++x) {
           const int piece = (x + turn) % W;
@@ -520,30 +526,21 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tiles_kernel(KvAtt a) {
           if (!seen) w[x] = make_uint4(0, 0, 0, 0), f[x] = 0;  // not there: anything
         }
         tc::mbar_arrive(&raw_free[slot]);
-        return true;
-      };
-      int task = warp < 12 ? warp & 1 : 2;
-      if (task < tasks) ok = read(task);
-      for (; task < tasks && ok; task += kStep) {
-        const int it = task / 4, s = it % kStages, turn = first_piece(task);
-        uint4 u[W];
-        uint32_t sc[W];
-#pragma unroll
-        for (int x = 0; x < W; ++x) u[x] = w[x], sc[x] = scales2(f[x]);
-        if (task + kStep < tasks) ok = read(task + kStep);
-        if (ok && it >= kStages)
+        if (it >= kStages) {
           ok = __all_sync(0xffffffffu, tc::mbar_wait(v ? &v_free[s] : &k_free[s], ((it / kStages) & 1) ^ 1));
-        if (!ok) break;
-        uint8_t* dst = smem + (v ? L::kV : L::kK) + s * L::kOperand + ((task & 3) * 32 + lane) * 16;
+          if (!ok) break;
+        }
+        uint8_t* dst = smem + (v ? L::kV : L::kK) + s * L::kOperand + key * 16;
 #pragma unroll
         for (int x = 0; x < W; ++x) {  // 32 channels: two scales, four chunks
           uint8_t* at = dst + ((x + turn) % W) * (4 * kChunk);
-          const uint32_t c[4] = {u[x].x, u[x].y, u[x].z, u[x].w};
+          const uint32_t c[4] = {w[x].x, w[x].y, w[x].z, w[x].w};
+          const uint32_t sc = scales2(f[x]);
 #pragma unroll
           for (int y = 0; y < 4; ++y) {
             uint32_t h[4];
             codes8(c[y], h);
-            const uint32_t one = __byte_perm(sc[x], 0, y < 2 ? 0x1010u : 0x3232u);
+            const uint32_t one = __byte_perm(sc, 0, y < 2 ? 0x1010u : 0x3232u);
             *reinterpret_cast<uint4*>(at + y * kChunk) =
                 make_uint4(mul2(h[0], one), mul2(h[1], one), mul2(h[2], one), mul2(h[3], one));
           }
@@ -551,8 +548,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tiles_kernel(KvAtt a) {
         tc::fence_async_smem();
         tc::mbar_arrive(v ? &v_full[s] : &k_full[s]);
       }
-    } else if (warp < kSoftWarps + 2) {
-      const bool v = warp > kSoftWarps;
+    } else if (!kFp4 && (warp == kKeyWarp || warp == kValueWarp)) {
+      const bool v = warp == kValueWarp;
       const uint8_t* src = v ? a.c.v : a.c.k;
       uint64_t* full = v ? v_full : k_full;
       uint64_t* free_ = v ? v_free : k_free;

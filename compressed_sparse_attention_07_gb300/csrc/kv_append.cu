@@ -10,13 +10,25 @@
 // E2M1 nearest to x / scale) and stored in the token's page.
 // The call moves 2 B a channel in and 2 B (queries) or 0.5625 B (FP4) out and
 // computes a few operations on each: bound by HBM for long prompts, by latency
-// for a decode step, which is why a token's rows are spread over CTAs there.
+// for a decode step.  So there are two kernels:
+//  - kv_append_few_kernel: a CTA for 32 or 16 rows of a token (16 a pass), which
+//    reads its rows while it looks up the token's sequence, page and angles;
+//  - kv_append_stream_kernel, from kFewItems pieces on: two CTAs an SM take
+//    pieces of up to 24 KB of a token in turn; one warp looks up 32 pieces at a
+//    time and keeps four pieces on their way by bulk copies, eight warps rotate,
+//    encode and store.  (A CTA for each piece spends its time waiting for the
+//    look-ups: 8 prompts of 37 .. 2021 tokens, 64 + 2 x 8 heads of 128, took
+//    107 us so.)
+#include <algorithm>
+
 #include "kv.cuh"
+#include "tc.cuh"
 
 namespace csa2 {
 namespace {
 
-constexpr int kThreads = 256, kMostPasses = 4;
+constexpr int kThreads = 256;
+constexpr int kFewItems = 8;  // pieces an SM from which the stream kernel is the faster
 
 struct AppendArgs {
   int B, T, n_q, n_kv, rope_dims, half;
@@ -33,35 +45,33 @@ struct AppendArgs {
   int32_t* status;
 };
 
-__device__ __forceinline__ void unpack8(uint4 w, float (&x)[8]) {
-  const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+__device__ __forceinline__ void widen(const uint32_t (&u)[4], float (&x)[8]) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     x[2 * i] = __uint_as_float(u[i] << 16);
     x[2 * i + 1] = __uint_as_float(u[i] & 0xFFFF0000u);
   }
 }
-__device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
-  uint32_t r;
-  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
-}
-__device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
-  return make_uint4(bf16x2(x[0], x[1]), bf16x2(x[2], x[3]), bf16x2(x[4], x[5]), bf16x2(x[6], x[7]));
-}
-
 // E4M3 code nearest to y >= 0, saturating.
 __device__ __forceinline__ uint32_t e4m3_code(float y) {
   uint16_t r;
   asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(0.0f), "f"(y));
   return r & 0xFFu;
 }
-// Codes of x / s, ties to the even code, saturating: eight nibbles, channel 0
-// lowest.  The sign of a value that rounds to zero is dropped.
+// Codes of x / s (0 < s; |x| below about 6.4 s, or s the largest scale), ties to
+// the even code, saturating: eight nibbles, channel 0 lowest.  The quotient is
+// rounded correctly from the reciprocal by one step with the remainder
+// (Markstein), so that a value half way between two codes is seen as such; where
+// the remainder underflows, the code is 0 either way.  The sign of a value that
+// rounds to zero is dropped.
 __device__ __forceinline__ uint32_t e2m1x8(const float (&x)[8], float s) {
+  const float inv = __frcp_rn(s);
   float y[8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) y[i] = __fdiv_rn(x[i], s);
+  for (int i = 0; i < 8; ++i) {
+    const float q = __fmul_rn(x[i], inv);
+    y[i] = __fmaf_rn(__fmaf_rn(-q, s, x[i]), inv, q);
+  }
   uint32_t w;
   asm("{\n .reg .b8 b0, b1, b2, b3;\n"
       " cvt.rn.satfinite.e2m1x2.f32 b0, %2, %1;\n cvt.rn.satfinite.e2m1x2.f32 b1, %4, %3;\n"
@@ -74,8 +84,120 @@ __device__ __forceinline__ uint32_t e2m1x8(const float (&x)[8], float s) {
   return m | (w & (nz << 3));
 }
 
+// What a thread keeps for its eight channels of every row of a token: the
+// cosines, and the sines with the sign they have in that channel.
+struct Turn {
+  float c[8], s[8];
+  // table: the token's row of angles (global or shared memory)
+  __device__ __forceinline__ void load(const float4* table, int c0, int pairs, bool half) {
+    if (half) {  // eight pairs, of which this thread holds the a's or the b's
+      const bool second = c0 >= pairs;
+      const float4* t = table + (second ? c0 - pairs : c0) / 2;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float4 f = t[i];
+        c[2 * i] = f.x, c[2 * i + 1] = f.z;
+        s[2 * i] = second ? f.y : -f.y, s[2 * i + 1] = second ? f.w : -f.w;
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const float4 f = table[c0 / 4 + i];
+        c[4 * i] = c[4 * i + 1] = f.x, c[4 * i + 2] = c[4 * i + 3] = f.z;
+        s[4 * i] = -f.y, s[4 * i + 1] = f.y, s[4 * i + 2] = -f.w, s[4 * i + 3] = f.w;
+      }
+    }
+  }
+};
+
+struct Place {
+  int n;         // token
+  int32_t page;  // -1: not there
+  int slot;
+};
+
+// Eight channels w (column col) of row r of a token's queries, keys and values
+// -> rotated, encoded and stored.  The whole warp calls it; `mate`: the lane
+// with the other members of this thread's pairs (half style), `turned`: whether
+// its channels are rotated at all.
+template <int kDim_, bool kFp4>
+__device__ __forceinline__ void put_row(const AppendArgs& a, const Place& at, int r, bool live, int col, const Turn& turn,
+                                        bool turned, int mate, uint4 w) {
+  const int c0 = 8 * col;
+  const bool is_q = r < a.n_q, is_v = r >= a.n_q + a.n_kv;
+  const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+  float v[8];
+  widen(u, v);
+  if (a.rope_dims) {
+    // v c + y s, y the other member: each product and the sum rounded by itself
+    // (the packed fp32 operations do not keep the products apart)
+    uint32_t o[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) o[i] = a.half ? __shfl_sync(0xffffffffu, u[i], mate) : __byte_perm(u[i], 0, 0x1032);
+    if (turned && !is_v) {
+      float y[8];
+      widen(o, y);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = __fadd_rn(__fmul_rn(v[i], turn.c[i]), __fmul_rn(y[i], turn.s[i]));
+    }
+  }
+  if (is_q && live)
+    *reinterpret_cast<uint4*>(a.q_out + (int64_t)at.n * a.q_out_stride + r * kDim_ + c0) =
+        make_uint4(bf16x2(v[0], v[1]), bf16x2(v[2], v[3]), bf16x2(v[4], v[5]), bf16x2(v[6], v[7]));
+  const bool mine = live && !is_q;
+  if (!__any_sync(0xffffffffu, mine)) return;
+  float amax = 0.0f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fabsf(v[i]));
+  constexpr float kMost = 3.3895313892515355e38f;  // largest bf16
+  float sum = 0.0f;  // NaN if any is
+#pragma unroll
+  for (int i = 0; i < 8; ++i) sum = fmaf(v[i], 0.0f, sum);
+  if (mine && (!(amax <= kMost) || sum != 0.0f)) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (!(fabsf(v[i]) <= kMost)) v[i] = v[i] != v[i] ? 0.0f : copysignf(kMost, v[i]);
+    amax = fminf(amax, kMost);
+    report(a.status, CSA2_ERR_RANGE);
+  }
+  uint16_t* plain = is_v ? a.v_out : a.k_out;
+  const int h = is_v ? r - a.n_q - a.n_kv : r - a.n_q;
+  const int64_t block = (int64_t)at.page * a.n_kv + h;
+  uint4 stored;
+  if constexpr (kFp4) {
+    amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+    if (!mine) return;
+    const uint32_t sc = e4m3_code(__fdiv_rn(amax, 6.0f));
+    const float s = e4m3_to_float(sc);
+    const uint32_t codes = sc ? e2m1x8(v, s) : 0u;
+    if (at.page >= 0) {
+      uint8_t* data = (is_v ? a.c.v : a.c.k) + block * kv_block_bytes(kDim_, true);
+      *reinterpret_cast<uint32_t*>(data + at.slot * (kDim_ / 2) + c0 / 2) = codes;
+      if ((col & 1) == 0)
+        ((is_v ? a.c.vs : a.c.ks) + block * kv_scale_bytes(kDim_))[at.slot * (kDim_ / 16) + col / 2] = (uint8_t)sc;
+    }
+    if (!plain) return;
+    uint32_t d[4];
+    codes8(codes, d);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {  // E2M1 x E4M3: exact in fp32 and in bf16
+      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&d[i]));
+      d[i] = bf16x2(f.x * s, f.y * s);
+    }
+    stored = make_uint4(d[0], d[1], d[2], d[3]);
+  } else {
+    if (!mine) return;
+    stored = make_uint4(bf16x2(v[0], v[1]), bf16x2(v[2], v[3]), bf16x2(v[4], v[5]), bf16x2(v[6], v[7]));
+    if (at.page >= 0)
+      *reinterpret_cast<uint4*>((is_v ? a.c.v : a.c.k) + block * kv_block_bytes(kDim_, false) +
+                                (col * kPage + at.slot) * 16) = stored;
+    if (!plain) return;
+  }
+  *reinterpret_cast<uint4*>(plain + ((int64_t)at.n * a.n_kv + h) * kDim_ + c0) = stored;
+}
+
 template <int kDim_, bool kFp4, int kPasses>
-__global__ void __launch_bounds__(kThreads) kv_append_kernel(AppendArgs a) {
+__global__ void __launch_bounds__(kThreads) kv_append_few_kernel(AppendArgs a) {
   constexpr int kLanes = kDim_ / 8;              // threads of a row
   constexpr int kRows = kThreads / kLanes;       // rows of a pass
   griddep_wait();  // every input may be the previous kernel's output
@@ -113,106 +235,170 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(AppendArgs a) {
     return;
   }
   const int32_t page = __ldg(a.c.table + (int64_t)b * a.c.max_pages + pos / kPage);
-  const int slot = (int)(pos % kPage);
   const bool page_ok = page >= 0 && page < a.c.num_pages;
   if (!page_ok && tid == 0) report(a.status, CSA2_ERR_BAD_PAGE);
+  const Place at{n, page_ok ? page : -1, (int)(pos % kPage)};
 
   const int pairs = a.rope_dims / 2;
   const bool turned = c0 < a.rope_dims;
-  const bool second = a.half && c0 >= pairs;  // holds the b's of its pairs
-  float cs[8], sn[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) cs[i] = 1.0f, sn[i] = 0.0f;
-  if (turned) {
-    const float4* t = reinterpret_cast<const float4*>(a.rope + pos * a.rope_dims);
-    if (a.half) {
-      const int p = second ? c0 - pairs : c0;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float4 f = __ldg(t + p / 2 + i);
-        cs[2 * i] = f.x, sn[2 * i] = f.y, cs[2 * i + 1] = f.z, sn[2 * i + 1] = f.w;
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const float4 f = __ldg(t + c0 / 4 + i);
-        cs[2 * i] = f.x, sn[2 * i] = f.y, cs[2 * i + 1] = f.z, sn[2 * i + 1] = f.w;
-      }
-    }
-  }
-  const int mate = second ? (tid & 31) - pairs / 8 : (tid & 31) + pairs / 8;
-
+  Turn turn = {};
+  if (turned) turn.load(reinterpret_cast<const float4*>(a.rope + pos * a.rope_dims), c0, pairs, a.half);
+  const int mate = ((tid & 31) + (c0 >= pairs ? -pairs : pairs) / 8) & 31;
 #pragma unroll
   for (int p = 0; p < kPasses; ++p) {
     const int r = first + p * kRows;
-    const bool live = r < n_rows;
-    const bool is_q = r < a.n_q, is_v = r >= a.n_q + a.n_kv;
-    const int h = is_q ? r : is_v ? r - a.n_q - a.n_kv : r - a.n_q;
-    float x[8];
-    unpack8(raw[p], x);
-    if (a.half) {  // uniform: the pair's other member is in another thread of the row
-      float y[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) y[i] = __shfl_sync(0xffffffffu, x[i], mate & 31);
-      if (turned && !is_v) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-          x[i] = second ? __fadd_rn(__fmul_rn(y[i], sn[i]), __fmul_rn(x[i], cs[i]))
-                        : __fsub_rn(__fmul_rn(x[i], cs[i]), __fmul_rn(y[i], sn[i]));
-      }
-    } else if (turned && !is_v) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float u = x[2 * i], w = x[2 * i + 1];
-        x[2 * i] = __fsub_rn(__fmul_rn(u, cs[i]), __fmul_rn(w, sn[i]));
-        x[2 * i + 1] = __fadd_rn(__fmul_rn(u, sn[i]), __fmul_rn(w, cs[i]));
-      }
-    }
-    if (!is_q) {
-      constexpr float kMost = 3.3895313892515355e38f;  // largest bf16
-      bool bad = false;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        if (!(fabsf(x[i]) <= kMost)) {
-          bad = true;
-          x[i] = x[i] != x[i] ? 0.0f : copysignf(kMost, x[i]);
-        }
-      }
-      if (bad && live) report(a.status, CSA2_ERR_RANGE);
-    }
-    float amax = 0.0f;
-    if (kFp4) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fabsf(x[i]));
-      amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-    }
-    if (!live) continue;
-    if (is_q) {
-      *reinterpret_cast<uint4*>(a.q_out + (int64_t)n * a.q_out_stride + h * kDim_ + c0) = pack8(x);
-      continue;
-    }
-    uint16_t* plain = is_v ? a.v_out : a.k_out;
-    const int64_t block = (int64_t)page * a.n_kv + h;
-    if (kFp4) {
-      const uint32_t sc = e4m3_code(__fdiv_rn(amax, 6.0f));
-      const float s = e4m3_to_float(sc);
-      const uint32_t w = sc ? e2m1x8(x, s) : 0u;
-      if (page_ok) {
-        uint8_t* data = (is_v ? a.c.v : a.c.k) + block * kv_block_bytes(kDim_, true);
-        *reinterpret_cast<uint32_t*>(data + slot * (kDim_ / 2) + c0 / 2) = w;
-        if ((col & 1) == 0)
-          ((is_v ? a.c.vs : a.c.ks) + block * kv_scale_bytes(kDim_))[slot * (kDim_ / 16) + col / 2] = (uint8_t)sc;
-      }
-      if (plain) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] = e2m1_to_float((w >> (4 * i)) & 15u) * s;
-      }
-    } else if (page_ok) {
-      uint8_t* data = (is_v ? a.c.v : a.c.k) + block * kv_block_bytes(kDim_, false);
-      *reinterpret_cast<uint4*>(data + (col * kPage + slot) * 16) = pack8(x);
-    }
-    if (plain) *reinterpret_cast<uint4*>(plain + ((int64_t)n * a.n_kv + h) * kDim_ + c0) = pack8(x);
+    put_row<kDim_, kFp4>(a, at, r, r < n_rows, col, turn, turned, mate, raw[p]);
   }
+}
+
+// ---- many tokens
+constexpr int kSlots = 4, kWorkWarps = 8, kStreamThreads = 32 * (kWorkWarps + 1);
+template <int kDim_>
+constexpr int kPieceRows = 24576 / (2 * kDim_);  // at most, of one token
+
+struct StreamPiece {  // what the workers need to know of a piece
+  Place at;
+  int row0, rows;
+};
+
+// Sequence of token n by bisection over cu (the first that ends behind n), and
+// its place; false when it has none.
+__device__ __forceinline__ bool find_place(const AppendArgs& a, int n, Place& at, int64_t& pos) {
+  int lo_b = 0, hi_b = a.B;
+  while (lo_b < hi_b) {
+    const int mid = (lo_b + hi_b) / 2;
+    if (__ldg(a.cu + mid + 1) <= n) lo_b = mid + 1;
+    else hi_b = mid;
+  }
+  if (lo_b >= a.B) return false;  // behind the last sequence
+  const int lo = __ldg(a.cu + lo_b), hi = __ldg(a.cu + lo_b + 1);
+  if (n < lo && lo_b == 0 && lo <= a.T) return false;  // ahead of the first
+  pos = __ldg(a.pos0 + lo_b) + (n - lo);
+  if (lo < 0 || n < lo || n >= hi || hi > a.T || pos < 0 || pos >= (int64_t)a.c.max_pages * kPage ||
+      (a.rope_dims && pos >= a.rope_rows)) {
+    report(a.status, CSA2_ERR_BAD_INDEX);
+    return false;
+  }
+  const int32_t page = __ldg(a.c.table + (int64_t)lo_b * a.c.max_pages + pos / kPage);
+  const bool there = page >= 0 && page < a.c.num_pages;
+  if (!there) report(a.status, CSA2_ERR_BAD_PAGE);
+  at = Place{n, there ? page : -1, (int)(pos % kPage)};
+  return true;
+}
+
+template <int kDim_>
+constexpr int slot_bytes() { return kPieceRows<kDim_> * kDim_ * 2 + kDim_ * 4; }  // rows, then the angles
+
+template <int kDim_, bool kFp4>
+__global__ void __launch_bounds__(kStreamThreads, 2) kv_append_stream_kernel(AppendArgs a) {
+  constexpr int kLanes = kDim_ / 8, kRows = 32 * kWorkWarps / kLanes;
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ __align__(8) uint64_t full[kSlots], empty[kSlots];
+  __shared__ StreamPiece piece[kSlots];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (tid == 0) {
+    for (int s = 0; s < kSlots; ++s) {
+      tc::mbar_init(&full[s], 1);
+      tc::mbar_init(&empty[s], 32 * kWorkWarps);
+    }
+    tc::fence_mbar_init();
+  }
+  __syncthreads();
+  griddep_wait();  // every input may be the previous kernel's output
+  griddep_launch();
+  const int n_rows = a.n_q + 2 * a.n_kv, per = (n_rows + kPieceRows<kDim_> - 1) / kPieceRows<kDim_>;
+  const int most = ((n_rows + per - 1) / per + kRows - 1) / kRows * kRows;  // rows of a piece
+  const int64_t items = (int64_t)a.T * per;
+  bool ok = true;
+  if (warp == kWorkWarps) {
+    int count = 0;  // pieces sent so far
+    for (int64_t base = blockIdx.x; base < items && ok; base += 32 * (int64_t)gridDim.x) {
+      const int64_t item = base + lane * (int64_t)gridDim.x;
+      Place at{0, -1, 0};
+      int64_t pos = 0;
+      // (pieces are whole passes: the last of a token may be empty)
+      const bool there = item < items && (item % per) * most < n_rows && find_place(a, (int)(item / per), at, pos);
+      const int row0 = there ? (int)(item % per) * most : 0;
+      uint32_t todo = __ballot_sync(0xffffffffu, there);
+      while (todo && ok) {
+        const int src = __ffs(todo) - 1;
+        todo &= todo - 1;
+        const int s = count % kSlots;
+        if (count >= kSlots) ok = __all_sync(0xffffffffu, tc::mbar_wait(&empty[s], ((count / kSlots) & 1) ^ 1));
+        if (!ok) break;
+        ++count;
+        if (lane == src) {
+          const int rows = min(most, n_rows - row0);
+          piece[s] = StreamPiece{at, row0, rows};
+          uint8_t* dst = smem + s * slot_bytes<kDim_>();
+          tc::mbar_arrive_expect_tx(&full[s], rows * kDim_ * 2 + a.rope_dims * 4);
+          // the piece's queries, keys and values: up to three runs
+          const int q1 = min(row0 + rows, a.n_q), k1 = min(row0 + rows, a.n_q + a.n_kv);
+          if (row0 < q1)
+            tc::bulk_g2s(dst, a.q + (int64_t)at.n * a.q_stride + row0 * kDim_, (q1 - row0) * kDim_ * 2, &full[s]);
+          const int k0 = max(row0, a.n_q);
+          if (k0 < k1)
+            tc::bulk_g2s(dst + (k0 - row0) * kDim_ * 2, a.k + (int64_t)at.n * a.k_stride + (k0 - a.n_q) * kDim_,
+                         (k1 - k0) * kDim_ * 2, &full[s]);
+          const int v0 = max(row0, a.n_q + a.n_kv), v1 = row0 + rows;
+          if (v0 < v1)
+            tc::bulk_g2s(dst + (v0 - row0) * kDim_ * 2, a.v + (int64_t)at.n * a.v_stride + (v0 - a.n_q - a.n_kv) * kDim_,
+                         (v1 - v0) * kDim_ * 2, &full[s]);
+          if (a.rope_dims)
+            tc::bulk_g2s(dst + kPieceRows<kDim_> * kDim_ * 2, a.rope + pos * a.rope_dims, a.rope_dims * 4, &full[s]);
+        }
+        __syncwarp();
+      }
+    }
+    // the end: a piece without rows
+    const int s = count % kSlots;
+    if (ok && count >= kSlots) ok = __all_sync(0xffffffffu, tc::mbar_wait(&empty[s], ((count / kSlots) & 1) ^ 1));
+    if (lane == 0) {
+      if (ok) {
+        piece[s].rows = 0;
+        tc::mbar_arrive(&full[s]);
+      } else {
+        report(a.status, CSA2_ERR_TIMEOUT);
+      }
+    }
+    // nothing may land in shared memory after the CTA has left
+    for (int i = max(0, count - kSlots + 1); i < count; ++i) tc::mbar_wait(&full[i % kSlots], (i / kSlots) & 1);
+  } else {
+    const int col = tid % kLanes, c0 = 8 * col, pairs = a.rope_dims / 2;
+    const bool turned = c0 < a.rope_dims;
+    const int mate = (lane + (c0 >= pairs ? -pairs : pairs) / 8) & 31;
+    for (int count = 0;; ++count) {
+      const int s = count % kSlots;
+      if (!__all_sync(0xffffffffu, tc::mbar_wait(&full[s], (count / kSlots) & 1))) {
+        if (lane == 0) report(a.status, CSA2_ERR_TIMEOUT);
+        break;
+      }
+      const StreamPiece p = piece[s];
+      if (p.rows == 0) break;
+      const uint8_t* src = smem + s * slot_bytes<kDim_>();
+      Turn turn = {};
+      if (turned) turn.load(reinterpret_cast<const float4*>(src + kPieceRows<kDim_> * kDim_ * 2), c0, pairs, a.half);
+#pragma unroll 2
+      for (int r0 = 0; r0 < p.rows; r0 += kRows) {
+        const int r = r0 + tid / kLanes;
+        const bool live = r < p.rows;
+        put_row<kDim_, kFp4>(a, p.at, p.row0 + r, live, col, turn, turned, mate,
+                             live ? *reinterpret_cast<const uint4*>(src + (r * kDim_ + c0) * 2) : make_uint4(0, 0, 0, 0));
+      }
+      tc::mbar_arrive(&empty[s]);
+    }
+  }
+}
+
+template <int kDim_, bool kFp4>
+cudaError_t stream_of(const AppendArgs& a, int64_t pieces, cudaStream_t stream) {
+  auto kern = kv_append_stream_kernel<kDim_, kFp4>;
+  constexpr int kSmem = kSlots * slot_bytes<kDim_>();
+  static bool done[64];
+  const cudaError_t e = allow_smem(kern, kSmem, done);
+  if (e != cudaSuccess) return e;
+  const int64_t ctas = std::min<int64_t>(pieces, 2 * num_sms());
+  return launch_k(kern, dim3((unsigned)ctas), dim3(kStreamThreads), kSmem, stream, 0, a);
 }
 
 }  // namespace
@@ -225,16 +411,21 @@ cudaError_t launch_kv_append(const csa2_kv_cfg& cfg, int B, int T, const uint16_
   AppendArgs a{B, T, q ? cfg.n_heads : 0, cfg.kv_heads, cfg.rope_dims, cfg.rope_style == CSA2_ROPE_HALF ? 1 : 0,
                q, k, v, q_stride, k_stride, v_stride, cu, pos0, rope, rope_rows, c, q_out, q_out_stride, k_out, v_out,
                status};
-  const int rows = kThreads / (cfg.head_dim / 8);
-  const int passes = (a.n_q + 2 * a.n_kv + rows - 1) / rows;
-  // a CTA for each of a token's passes while these do not fill the GPU, then a
-  // CTA for four
-  const bool few = (int64_t)T * passes <= 8 * num_sms();
-  const dim3 grid(T, few ? passes : (passes + kMostPasses - 1) / kMostPasses), block(kThreads);
+  const int rows = a.n_q + 2 * a.n_kv;
   const bool fp4 = cfg.cache_dtype == CSA2_CACHE_FP4;
-#define CSA2_APPEND(D, F)                                                                      \
-  (few ? launch_k(kv_append_kernel<D, F, 1>, grid, block, 0, stream, 0, a)                     \
-       : launch_k(kv_append_kernel<D, F, kMostPasses>, grid, block, 0, stream, 0, a))
+  const int piece_rows = 24576 / (2 * cfg.head_dim);
+  const int64_t pieces = (int64_t)T * ((rows + piece_rows - 1) / piece_rows);
+  if (pieces >= kFewItems * num_sms()) {
+    if (cfg.head_dim == 128) return fp4 ? stream_of<128, true>(a, pieces, stream) : stream_of<128, false>(a, pieces, stream);
+    return fp4 ? stream_of<64, true>(a, pieces, stream) : stream_of<64, false>(a, pieces, stream);
+  }
+  const int per_pass = kThreads / (cfg.head_dim / 8), passes = (rows + per_pass - 1) / per_pass;
+  // one pass a CTA while the passes do not fill the GPU, two beyond
+  const bool few = (int64_t)T * passes <= 4 * num_sms();
+  const dim3 grid(T, few ? passes : (passes + 1) / 2), block(kThreads);
+#define CSA2_APPEND(D, F)                                                          \
+  (few ? launch_k(kv_append_few_kernel<D, F, 1>, grid, block, 0, stream, 0, a)     \
+       : launch_k(kv_append_few_kernel<D, F, 2>, grid, block, 0, stream, 0, a))
   if (cfg.head_dim == 128) return fp4 ? CSA2_APPEND(128, true) : CSA2_APPEND(128, false);
   return fp4 ? CSA2_APPEND(64, true) : CSA2_APPEND(64, false);
 #undef CSA2_APPEND

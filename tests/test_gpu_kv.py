@@ -53,10 +53,21 @@ def _noise(cache):
     (64, 1, 1, 64, INTER), (64, 6, 3, 32, HALF), (128, 28, 4, 128, HALF), (128, 8, 8, 64, INTER), (128, 16, 1, 96, HALF),
     (64, 4, 2, 16, HALF), (128, 5, 5, 0, INTER)])
 def test_append_matches(dtype, dim, hq, hkv, rope, style):
+    _append_case(dtype, dim, hq, hkv, rope, style, [3, 0, 1, 70, 64], [0, 5, 63, 60, 128])
+
+
+@pytest.mark.parametrize("dtype", [FP4, BF16])
+@pytest.mark.parametrize("dim,hq,hkv,rope,style", [
+    (64, 3, 1, 64, INTER), (64, 200, 2, 32, HALF), (128, 112, 1, 128, HALF), (128, 7, 1, 64, INTER), (128, 0, 2, 0, INTER)])
+def test_append_of_many_tokens(dtype, dim, hq, hkv, rope, style):
+    # more rows than one piece of a token holds, and tokens without queries
+    _append_case(dtype, dim, hq, hkv, rope, style, [901, 0, 1, 400, 64], [0, 5, 63, 60, 128])
+
+
+def _append_case(dtype, dim, hq, hkv, rope, style, lengths, starts):
     rng = np.random.default_rng(dim + hq + rope)
-    lengths, starts = [3, 0, 1, 70, 64], [0, 5, 63, 60, 128]
-    cfg = csa.KVCfg(hq, hkv, dim, dtype, rope_dims=rope, rope_style=style)
-    cache = _cache(cfg, 5, 200)
+    cfg = csa.KVCfg(hq or hkv, hkv, dim, dtype, rope_dims=rope, rope_style=style)
+    cache = _cache(cfg, 5, max(a + b for a, b in zip(lengths, starts)))
     _noise(cache)
     before = [t.clone() for t in (cache.k_data, cache.v_data)]
     T = sum(lengths)
@@ -67,9 +78,9 @@ def test_append_matches(dtype, dim, hq, hkv, rope, style):
     q_out = torch.full((T + 4, hq, dim), 7.0, dtype=torch.bfloat16, device="cuda")
     k_out, v_out = (torch.full((T + 4, hkv, dim), 7.0, dtype=torch.bfloat16, device="cuda") for _ in "kv")
     st = _status()
-    table = csa.rope_table(300, rope) if rope else None
-    csa.kv_append(cfg, k, v, _cu(lengths), torch.tensor(starts, device="cuda"), cache, rope=table, q=q, q_out=q_out,
-                  k_out=k_out, v_out=v_out, status=st)
+    table = csa.rope_table(1000, rope) if rope else None
+    csa.kv_append(cfg, k, v, _cu(lengths), torch.tensor(starts, device="cuda"), cache, rope=table, q=q if hq else None,
+                  q_out=q_out if hq else None, k_out=k_out, v_out=v_out, status=st)
     assert int(st.item()) == 0
     pos = np.concatenate([np.arange(n) + s for n, s in zip(lengths, starts)])
     host = table.cpu().numpy() if rope else None
@@ -77,7 +88,8 @@ def test_append_matches(dtype, dim, hq, hkv, rope, style):
     want_q = _kv.rotate(x[:, :hq], host, pos, rope, style == HALF)
     want_k = _kv.rotate(x[:, hq:hq + hkv], host, pos, rope, style == HALF)
     want_v = x[:, hq + hkv:hq + 2 * hkv]
-    assert torch.equal(q_out[:T].cpu(), torch.from_numpy(want_q).to(torch.bfloat16))
+    if hq:
+        assert torch.equal(q_out[:T].cpu(), torch.from_numpy(want_q).to(torch.bfloat16))
     assert (q_out[T:] == 7).all() and (k_out[T:] == 7).all() and (v_out[T:] == 7).all()
     t0 = 0
     for b, (n, s) in enumerate(zip(lengths, starts)):

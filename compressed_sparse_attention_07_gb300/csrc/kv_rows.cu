@@ -117,12 +117,13 @@ __global__ void __launch_bounds__(kWarps * 32, Rows<D, kFp4, NT>::kCtas) kv_rows
     if (lane == 0) tc::mbar_arrive_expect_tx(bar, R::kStage);
     __syncwarp();
     if constexpr (kFp4) {
-      if (lane < 4) {
-        const bool v = lane & 1;
-        const uint8_t* src = lane < 2 ? (v ? a.c.v : a.c.k) + block * R::kData : (v ? a.c.vs : a.c.ks) + block * R::kScales;
-        tc::bulk_g2s(dst + (lane < 2 ? lane * R::kData : 2 * R::kData + v * R::kScales), src,
-                     lane < 2 ? R::kData : R::kScales, bar);
+      if (tc::elect_one()) {
+        tc::bulk_g2s(dst, a.c.k + block * R::kData, R::kData, bar);
+        tc::bulk_g2s(dst + R::kData, a.c.v + block * R::kData, R::kData, bar);
+        tc::bulk_g2s(dst + 2 * R::kData, a.c.ks + block * R::kScales, R::kScales, bar);
+        tc::bulk_g2s(dst + 2 * R::kData + R::kScales, a.c.vs + block * R::kScales, R::kScales, bar);
       }
+      __syncwarp();
     } else {
       constexpr int kRun = R::kTile * 16;  // bytes of one channel chunk of the tile
       const int half = tile % R::kPerPage;

@@ -14,7 +14,7 @@
 // its 128 scores); warps 8-11 bring keys, 12-15 values into shared memory as
 // [channel chunk][128 keys][16 B], which is K-major for the first product and
 // MN-major for the second: FP4 decoded to f16 on the way, one row a thread, from
-// a ring of pages that warp 17 fills with bulk copies; bf16 pages, stored in
+// a ring of pages that warps 17 and 18 fill with bulk copies; bf16 pages, stored in
 // that order, by bulk copies (warps 8 and 12).  Warp 16 issues the products.
 //
 // The output in TMEM is rescaled only when a row's maximum grew by more than
@@ -34,21 +34,24 @@ constexpr int kSoftWarps = 8, kThreads = 640;
 constexpr int kKeyWarp = 8, kValueWarp = 12, kProductWarp = 16, kFetchWarp = 17;  // keys 8-11, values 12-15
 // registers of a thread: 96 at the launch, moved to the softmax's (640 x 96 = 256 x 168 + 384 x 48)
 constexpr int kSoftRegs = 168, kOtherRegs = 48;
-constexpr int kRing = 3, kLongRing = 6;                              // undecoded tiles on their way
+// Undecoded tiles on their way (turns: the long ring).  Both even: keys and values
+// alternate, so that a place in the ring belongs to one of the two, whose reading
+// threads see every one of its phases.
+constexpr int kRing = 2, kLongRing = 6, kTailSlots = 3;
 
 template <int D>
 struct Tiles {
   static constexpr int kOperand = 128 * D * 2;  // one operand tile
   static constexpr int kQ = 0, kK = 2 * kOperand, kV = kK + kStages * kOperand;
-  // undecoded FP4 tiles: the ring's first kRing behind the operands, the others
+  // undecoded FP4 tiles: the first kTailSlots behind the operands, the others
   // (turns) in the place of the second tile of queries
   static constexpr int kRaw = kV + kStages * kOperand, kRawData = kTileKeys * D / 2, kRawScales = kTileKeys * D / 16;
   static constexpr int kRawTile = kRawData + kRawScales;
-  static_assert((kLongRing - kRing) * kRawTile <= kOperand, "the long ring fits");
+  static_assert(kRing % 2 == 0 && kLongRing % 2 == 0 && (kLongRing - kTailSlots) * kRawTile <= kOperand, "the long ring fits");
   // one CTA per SM: it takes all of TMEM
-  static constexpr int kSmem = std::max(kRaw + kRing * kRawTile, 120 * 1024);
+  static constexpr int kSmem = std::max(kRaw + kTailSlots * kRawTile, 120 * 1024);
   __device__ static __forceinline__ int raw(int slot) {
-    return slot < kRing ? kRaw + slot * kRawTile : kQ + kOperand + (slot - kRing) * kRawTile;
+    return slot < kTailSlots ? kRaw + slot * kRawTile : kQ + kOperand + (slot - kTailSlots) * kRawTile;
   }
 };
 
@@ -437,8 +440,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tiles_kernel(KvAtt a) {
         commit(&o_full[1]);
         tc::mbar_wait(&o_full[1], 0);
       }
-    } else if (kFp4 && warp == kFetchWarp) {
-      // ------------------------------------ pages into the ring, K, V, K ..
+    } else if (kFp4 && (warp == kFetchWarp || warp == kFetchWarp + 1)) {
+      // ---------------- pages into the ring (K, V, K ..), a warp for each --
+      const bool v = warp != kFetchWarp;
       int32_t id[2], next[2] = {-1, -1};
       auto find = [&](int it) {
 #pragma unroll
@@ -448,15 +452,13 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tiles_kernel(KvAtt a) {
         }
       };
       find(0);
-      for (int op = 0; op < 2 * n_it; ++op) {
-        const int slot = op % ring;
-        if ((op & 1) == 0) {
-          id[0] = next[0], id[1] = next[1];
-          find(op / 2 + 1);
-          const bool bad = id[0] < 0 || id[0] >= a.c.num_pages ||
-                           (pb + op + 1 < pe && (id[1] < 0 || id[1] >= a.c.num_pages));
-          if (bad && lane == 0) report(a.status, CSA2_ERR_BAD_PAGE);
-        }
+      for (int it = 0; it < n_it; ++it) {
+        const int op = 2 * it + v, slot = op % ring;
+        id[0] = next[0], id[1] = next[1];
+        find(it + 1);
+        const bool bad = id[0] < 0 || id[0] >= a.c.num_pages ||
+                         (pb + 2 * it + 1 < pe && (id[1] < 0 || id[1] >= a.c.num_pages));
+        if (bad && lane == 0) report(a.status, CSA2_ERR_BAD_PAGE);
         if (op >= ring && !__all_sync(0xffffffffu, tc::mbar_wait(&raw_free[slot], ((op / ring) & 1) ^ 1))) {
           ok = false;
           break;
@@ -467,20 +469,23 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tiles_kernel(KvAtt a) {
           tc::mbar_arrive_expect_tx(&raw_full[slot], __popc(there) * (L::kRawTile / 2));
         }
         __syncwarp();
-        const int x = lane & 1;  // page; lanes 0 and 1 its codes, 2 and 3 its scales
-        if (lane < 4 && ((there >> x) & 1)) {
+        if (tc::elect_one()) {
           uint8_t* dst = smem + L::raw(slot);
-          const int64_t block = (int64_t)(x ? id[1] : id[0]) * a.kv_heads + kh;
-          if (lane < 2)
-            tc::bulk_g2s(dst + x * (L::kRawData / 2), ((op & 1) ? a.c.v : a.c.k) + block * (L::kRawData / 2),
-                         L::kRawData / 2, &raw_full[slot]);
-          else
-            tc::bulk_g2s(dst + L::kRawData + x * (L::kRawScales / 2),
-                         ((op & 1) ? a.c.vs : a.c.ks) + block * (L::kRawScales / 2), L::kRawScales / 2, &raw_full[slot]);
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            if (!((there >> x) & 1)) continue;
+            const int64_t block = (int64_t)id[x] * a.kv_heads + kh;
+            tc::bulk_g2s(dst + x * (L::kRawData / 2), (v ? a.c.v : a.c.k) + block * (L::kRawData / 2), L::kRawData / 2,
+                         &raw_full[slot]);
+            tc::bulk_g2s(dst + L::kRawData + x * (L::kRawScales / 2), (v ? a.c.vs : a.c.ks) + block * (L::kRawScales / 2),
+                         L::kRawScales / 2, &raw_full[slot]);
+          }
         }
+        __syncwarp();
       }
       // nothing may land in shared memory after the CTA has left
-      for (int op = max(0, 2 * n_it - ring); !ok && op < 2 * n_it; ++op) tc::mbar_wait(&raw_full[op % ring], (op / ring) & 1);
+      for (int op = max(0, 2 * n_it - ring); !ok && op < 2 * n_it; ++op)
+        tc::mbar_wait(&raw_full[op % ring], (op / ring) & 1);
     } else if (kFp4 && warp < kProductWarp) {
       // -------------------------------------------------------- decoding --
       // a row of each tile for each thread: warps 8-11 keys, 12-15 values

@@ -14,8 +14,10 @@
 // its 128 scores); warps 8-11 bring keys, 12-15 values into shared memory as
 // [channel chunk][128 keys][16 B], which is K-major for the first product and
 // MN-major for the second: FP4 decoded to f16 on the way, one row a thread, from
-// a ring of pages that warps 17 and 18 fill with bulk copies; bf16 pages, stored in
-// that order, by bulk copies (warps 8 and 12).  Warp 16 issues the products.
+// a ring of pages that warps 18 and 19 fill with bulk copies; bf16 pages, stored in
+// that order, by bulk copies (warps 8 and 12).  Warp 16 issues the products (a
+// warp for each place made their batches longer, not the pauses between them
+// shorter).
 //
 // The output in TMEM is rescaled only when a row's maximum grew by more than
 // 2^8 since its last rescaling (weights up to 2^8 are as exact as those up to
@@ -31,9 +33,9 @@ namespace {
 
 constexpr int kTileRows = 128, kCtaRows = 256, kTileKeys = 128, kStages = 2;
 constexpr int kSoftWarps = 8, kThreads = 640;
-constexpr int kKeyWarp = 8, kValueWarp = 12, kProductWarp = 16, kFetchWarp = 17;  // keys 8-11, values 12-15
-// registers of a thread: 96 at the launch, moved to the softmax's (640 x 96 = 256 x 168 + 384 x 48)
-constexpr int kSoftRegs = 168, kOtherRegs = 48;
+constexpr int kKeyWarp = 8, kValueWarp = 12, kProductWarp = 16, kFetchWarp = 18;  // keys 8-11, values 12-15
+// registers of a thread: 96 at the launch, then by role (640 x 96 = 256 x 160 + 256 x 48 + 128 x 64)
+constexpr int kSoftRegs = 160, kDecodeRegs = 48, kIssueRegs = 64;
 // Undecoded tiles on their way (turns: the long ring).  Both even: keys and values
 // alternate, so that a place in the ring belongs to one of the two, whose reading
 // threads see every one of its phases.
@@ -64,6 +66,12 @@ __device__ __forceinline__ void regs_dec() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 
+// A number that a generic lambda sees at compile time.
+template <int N>
+struct Num {
+  __device__ constexpr int operator()() const { return N; }
+};
+
 // Chunk-major operand tile: element (row, channel) at ((c / 8) * 128 + row) * 16 + (c % 8) * 2.
 constexpr uint32_t kChunk = 128 * 16;
 
@@ -75,7 +83,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tiles_kernel(KvAtt a) {
       p_ready[2], o_full[2];
   __shared__ uint32_t tmem_base;
   __shared__ int late_flag;
-  __shared__ __align__(8) uint64_t raw_full[kLongRing], raw_free[kLongRing], tail_full, q_full;
+  __shared__ __align__(8) uint64_t raw_full[kLongRing], raw_free[kLongRing], tail_full, q_full, drained;
   __shared__ int raw_pages[kLongRing];  // which of a tile's two pages are there
   __shared__ float half_m[2][kTileRows], half_l[2][kTileRows];
 
@@ -103,10 +111,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tiles_kernel(KvAtt a) {
   const int32_t* table = a.c.table + (int64_t)b * a.c.max_pages;
 
   if (tid == 0) {
-    const uint32_t filling = kFp4 ? kTileKeys : 32;
+    const uint32_t filling = kFp4 ? 4 : 32;  // warps; or lanes of the one that copies
     for (int s = 0; s < kLongRing; ++s) {
       tc::mbar_init(&raw_full[s], 1);
-      tc::mbar_init(&raw_free[s], kTileKeys);
+      tc::mbar_init(&raw_free[s], 4);
     }
     for (int s = 0; s < kStages; ++s) {
       tc::mbar_init(&k_full[s], filling);
@@ -117,11 +125,12 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tiles_kernel(KvAtt a) {
     for (int j = 0; j < 2; ++j) {
       const int live = n_rows - tile0 - (turns ? 0 : kTileRows * j);  // rows of place j
       tc::mbar_init(&s_ready[j], 1);
-      tc::mbar_init(&p_ready[j], 32 * max(1, min(4, (live + 31) / 32)));
+      tc::mbar_init(&p_ready[j], max(1, min(4, (live + 31) / 32)));  // warps with rows
       tc::mbar_init(&o_full[j], 1);
     }
     tc::mbar_init(&tail_full, 1);
-    tc::mbar_init(&q_full, 32 * kSoftWarps);
+    tc::mbar_init(&drained, 1);
+    tc::mbar_init(&q_full, kSoftWarps);
     late_flag = 0;
     tc::fence_mbar_init();
   }
@@ -136,6 +145,11 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tiles_kernel(KvAtt a) {
   const uint32_t tb = tmem_base;
   const uint32_t sbase = tc::smem_u32(smem);
   bool ok = true;
+  // one arrival for a warp, once all its lanes are here
+  auto warp_arrive = [&](uint64_t* bar) {
+    __syncwarp();
+    if (lane == 0) tc::mbar_arrive(bar);
+  };
 
   if (warp < kSoftWarps) {
     // ---------------------------------------------------------- softmax --
@@ -189,7 +203,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tiles_kernel(KvAtt a) {
       scale = fmaxf(scale, 1e-37f);  // above 0: a hidden key's -inf stays -inf
     }
     tc::fence_async_smem();
-    tc::mbar_arrive(&q_full);
+    warp_arrive(&q_full);
     const int j = warp / 4;
     const uint32_t lane_base = 32 * (warp & 3);
     const uint32_t s_addr = tc::taddr(tb, lane_base, 128 * j), o_addr = tc::taddr(tb, lane_base, 256 + D * j);
@@ -283,7 +297,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tiles_kernel(KvAtt a) {
         }
         tc::tmem_wait_st();
         tc::fence_before_sync();
-        tc::mbar_arrive(&p_ready[j]);
+        warp_arrive(&p_ready[j]);
       }
     }
     // ---- the rows' outputs: place 0's, place 1's, or (turns) both for one row
@@ -361,7 +375,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tiles_kernel(KvAtt a) {
       }
     }
   } else {
-    regs_dec<kOtherRegs>();
+    if (warp < kProductWarp) regs_dec<kDecodeRegs>();
+    else regs_dec<kIssueRegs>();
     const int ring = turns ? kLongRing : kRing;
     if (n_it == 0) {
       // no key: nothing to bring or to multiply
@@ -369,76 +384,97 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tiles_kernel(KvAtt a) {
       // ------------------------------------------------------- products --
       constexpr uint32_t kIdS = tc::idesc_f16(128, kTileKeys, !kFp4, !kFp4, false, false);
       constexpr uint32_t kIdO = tc::idesc_f16(128, D, !kFp4, !kFp4, false, true);
-      // S_j = Q K^T with key tile `it`
-      auto first = [&](int j, int it) {
+      constexpr uint32_t kHiK = tc::sdesc_hi(128), kHiV = tc::sdesc_hi(kChunk);
+      constexpr uint32_t kTile16 = L::kOperand / 16;
+      static_assert(kStages == 2, "the loops below go over two key tiles");
+      // Place and stage are compile-time numbers, the descriptors' low words formed
+      // once: see tc.cuh.
+      const uint32_t q_lo = tc::sdesc_lo(sbase + L::kQ, kChunk), k_lo = tc::sdesc_lo(sbase + L::kK, kChunk);
+      const uint32_t v_lo = tc::sdesc_lo(sbase + L::kV, 128);
+      auto wait = [&](uint64_t* bar, int parity) { return __all_sync(0xffffffffu, tc::mbar_wait(bar, parity)); };
+      // S_j = Q_q K^T with the keys of stage s, the last to read them if `over`
+      auto scores = [&](auto q, auto j, auto s, bool over) {
         tc::fence_after_sync();
-        const uint32_t qb = sbase + L::kQ + (turns ? 0 : j) * L::kOperand;
-        const uint32_t kb = sbase + L::kK + (it % kStages) * L::kOperand;
         if (tc::elect_one()) {
 #pragma unroll
           for (int ks = 0; ks < D / 16; ++ks)
-            tc::mma_ss(tb + 128 * j, tc::sdesc(qb + ks * 2 * kChunk, kChunk, 128),
-                       tc::sdesc(kb + ks * 2 * kChunk, kChunk, 128), kIdS, ks > 0);
-          tc::mma_commit(&s_ready[j]);
+            tc::mma_ss_lo(tb + 128 * j(), q_lo + q() * kTile16 + ks * (2 * kChunk / 16),
+                          k_lo + s() * kTile16 + ks * (2 * kChunk / 16), kHiK, kHiK, kIdS, ks > 0);
+          tc::mma_commit(&s_ready[j()]);
+          if (over) tc::mma_commit(&k_free[s()]);
         }
         __syncwarp();
       };
-      auto commit = [&](uint64_t* bar) {
-        if (tc::elect_one()) tc::mma_commit(bar);
-        __syncwarp();
-      };
-      auto wait = [&](uint64_t* bar, int parity) { return __all_sync(0xffffffffu, tc::mbar_wait(bar, parity)); };
-      // O_j += P_j V with key tile `it`, the u-th of place j
-      auto second = [&](int j, int it, int u) -> bool {
-        if (!wait(&p_ready[j], u & 1)) return false;
-        if ((turns || j == 0) && !wait(&v_full[it % kStages], (it / kStages) & 1)) return false;
+      // O_j += P_j V with the values of stage s, the u-th tile of place j
+      auto outputs = [&](auto j, auto s, int u, uint64_t* done) {
         tc::fence_after_sync();
-        const uint32_t vb = sbase + L::kV + (it % kStages) * L::kOperand;
         if (tc::elect_one()) {
+          tc::mma_ts_lo(tb + 256 + D * j(), tb + 128 * j(), v_lo + s() * kTile16, kHiV, kIdO, u > 0);
 #pragma unroll
-          for (int ks = 0; ks < kTileKeys / 16; ++ks)
-            tc::mma_ts(tb + 256 + D * j, tb + 128 * j + 8 * ks, tc::sdesc(vb + ks * 256, 128, kChunk), kIdO,
-                       (u > 0 || ks > 0) ? 1u : 0u);
+          for (int ks = 1; ks < kTileKeys / 16; ++ks)
+            tc::mma_ts_lo(tb + 256 + D * j(), tb + 128 * j() + 8 * ks, v_lo + s() * kTile16 + ks * (256 / 16), kHiV, kIdO,
+                          1u);
+          if (done) tc::mma_commit(done);
         }
         __syncwarp();
-        return true;
       };
       ok = wait(&q_full, 0);
       if (turns) {
-        for (int it = 0; it < n_it && ok; ++it) {
+        // tile `it`, of stage and place s, and the outputs of the place's last one
+        auto step = [&](auto s, int it) {
+          ok = wait(&k_full[s()], (it / kStages) & 1);
           if (it >= 2) {
-            ok = second(it & 1, it - 2, it / 2 - 1);
-            if (ok) commit(&v_free[it % kStages]);
+            ok = ok && wait(&v_full[s()], (it / kStages - 1) & 1) && wait(&p_ready[s()], (it / 2 - 1) & 1);
+            if (ok) outputs(s, s, it / 2 - 1, &v_free[s()]);
           }
-          ok = ok && wait(&k_full[it % kStages], (it / kStages) & 1);
-          if (!ok) break;
-          first(it & 1, it);
-          commit(&k_free[it % kStages]);
+          if (ok) scores(Num<0>{}, s, s, true);
+        };
+        auto end = [&](auto s, int it) {
+          ok = wait(&v_full[s()], (it / kStages) & 1) && wait(&p_ready[s()], (it / 2) & 1);
+          if (ok) outputs(s, s, it / 2, &o_full[s()]);
+        };
+        for (int it = 0; it < n_it && ok; it += 2) {
+          step(Num<0>{}, it);
+          if (ok && it + 1 < n_it) step(Num<1>{}, it + 1);
         }
         for (int it = max(0, n_it - 2); it < n_it && ok; ++it) {
-          ok = second(it & 1, it, it / 2);
-          if (ok) commit(&o_full[it & 1]);
+          if (it & 1) end(Num<1>{}, it);
+          else end(Num<0>{}, it);
         }
       } else {
-        for (int it = 0; it < n_it && ok; ++it) {
-          for (int j = 0; j < 2 && ok; ++j) {
-            if (it > 0) ok = second(j, it - 1, it - 1);
-            if (ok && j == 0) ok = wait(&k_full[it % kStages], (it / kStages) & 1);
-            if (ok) first(j, it);
+        // tile `it` (stage s), and the outputs of the one before it (stage p)
+        auto step = [&](auto s, auto p, int it) {
+          ok = wait(&k_full[s()], (it / kStages) & 1);
+          if (it > 0) {
+            ok = ok && wait(&v_full[p()], ((it - 1) / kStages) & 1) && wait(&p_ready[0], (it - 1) & 1);
+            if (ok) outputs(Num<0>{}, p, it - 1, nullptr);
           }
-          if (ok) {
-            commit(&k_free[it % kStages]);
-            if (it > 0) commit(&v_free[(it - 1) % kStages]);
+          if (ok) scores(Num<0>{}, Num<0>{}, s, false);
+          if (it > 0) {
+            ok = ok && wait(&p_ready[1], (it - 1) & 1);
+            if (ok) outputs(Num<1>{}, p, it - 1, &v_free[p()]);
           }
+          if (ok) scores(Num<1>{}, Num<1>{}, s, true);
+        };
+        auto end = [&](auto s) {
+          ok = wait(&v_full[s()], ((n_it - 1) / kStages) & 1) && wait(&p_ready[0], (n_it - 1) & 1);
+          if (ok) outputs(Num<0>{}, s, n_it - 1, &o_full[0]);
+          ok = ok && wait(&p_ready[1], (n_it - 1) & 1);
+          if (ok) outputs(Num<1>{}, s, n_it - 1, &o_full[1]);
+        };
+        for (int it = 0; it < n_it && ok; it += 2) {
+          step(Num<0>{}, Num<1>{}, it);
+          if (ok && it + 1 < n_it) step(Num<1>{}, Num<0>{}, it + 1);
         }
-        for (int j = 0; j < 2 && ok; ++j) {
-          ok = second(j, n_it - 1, n_it - 1);
-          if (ok) commit(&o_full[j]);
+        if (ok) {
+          if (n_it & 1) end(Num<0>{});
+          else end(Num<1>{});
         }
       }
       if (!ok) {  // nothing may run on after TMEM is given back
-        commit(&o_full[1]);
-        tc::mbar_wait(&o_full[1], 0);
+        if (tc::elect_one()) tc::mma_commit(&drained);
+        __syncwarp();
+        tc::mbar_wait(&drained, 0);
       }
     } else if (kFp4 && (warp == kFetchWarp || warp == kFetchWarp + 1)) {
       // ---------------- pages into the ring (K, V, K ..), a warp for each --
@@ -510,7 +546,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tiles_kernel(KvAtt a) {
           f[x] = *reinterpret_cast<const uint16_t*>(raw + L::kRawData + key * (D / 16) + 2 * piece);
           if (!seen) w[x] = make_uint4(0, 0, 0, 0), f[x] = 0;  // not there: anything
         }
-        tc::mbar_arrive(&raw_free[slot]);
+        warp_arrive(&raw_free[slot]);
         if (it >= kStages) {
           ok = __all_sync(0xffffffffu, tc::mbar_wait(v ? &v_free[s] : &k_free[s], ((it / kStages) & 1) ^ 1));
           if (!ok) break;
@@ -531,7 +567,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tiles_kernel(KvAtt a) {
           }
         }
         tc::fence_async_smem();
-        tc::mbar_arrive(v ? &v_full[s] : &k_full[s]);
+        warp_arrive(v ? &v_full[s] : &k_full[s]);
       }
     } else if (!kFp4 && (warp == kKeyWarp || warp == kValueWarp)) {
       const bool v = warp == kValueWarp;

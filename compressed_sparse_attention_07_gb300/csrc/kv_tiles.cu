@@ -34,8 +34,8 @@ namespace {
 constexpr int kTileRows = 128, kCtaRows = 256, kTileKeys = 128, kStages = 2;
 constexpr int kSoftWarps = 8, kThreads = 640;
 constexpr int kKeyWarp = 8, kValueWarp = 12, kProductWarp = 16, kFetchWarp = 18;  // keys 8-11, values 12-15
-// registers of a thread: 96 at the launch, then by role (640 x 96 = 256 x 160 + 256 x 48 + 128 x 64)
-constexpr int kSoftRegs = 160, kDecodeRegs = 48, kIssueRegs = 64;
+// registers of a thread: 96 at the launch, then by role (640 x 96 = 256 x 152 + 256 x 48 + 128 x 80)
+constexpr int kSoftRegs = 152, kDecodeRegs = 48, kIssueRegs = 80;
 // Undecoded tiles on their way (turns: the long ring).  Both even: keys and values
 // alternate, so that a place in the ring belongs to one of the two, whose reading
 // threads see every one of its phases.
@@ -374,13 +374,109 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tiles_kernel(KvAtt a) {
         }
       }
     }
-  } else {
-    if (warp < kProductWarp) regs_dec<kDecodeRegs>();
-    else regs_dec<kIssueRegs>();
+  } else if (warp < kProductWarp) {
+    regs_dec<kDecodeRegs>();
     const int ring = turns ? kLongRing : kRing;
-    if (n_it == 0) {
-      // no key: nothing to bring or to multiply
-    } else if (warp == kProductWarp) {
+    if (kFp4) {
+      // -------------------------------------------------------- decoding --
+      // a row of each tile for each thread: warps 8-11 keys, 12-15 values
+      constexpr int W = D / 32;  // 16-byte pieces of a row
+      const bool v = warp >= kValueWarp;
+      const int key = tid % kTileKeys;
+      // The pieces are taken from another one on by each few keys, so that the
+      // eight keys of a quarter warp's read lie in different banks.
+      const int turn = key / (256 / D);
+      for (int it = 0; it < n_it; ++it) {
+        const int op = 2 * it + v, slot = op % ring, s = it % kStages;
+        ok = __all_sync(0xffffffffu, tc::mbar_wait(&raw_full[slot], (op / ring) & 1));
+        if (!ok) break;
+        const uint8_t* raw = smem + L::raw(slot);
+        const bool seen = key0 + it * kTileKeys + key < keys && pb + 2 * it + key / 64 < pe && ((raw_pages[slot] >> (key / 64)) & 1);
+        uint4 w[W];
+        uint32_t f[W];
+#pragma unroll
+        for (int x = 0; x < W; ++x) {
+          const int piece = (x + turn) % W;
+          w[x] = *reinterpret_cast<const uint4*>(raw + key * (D / 2) + piece * 16);
+          f[x] = *reinterpret_cast<const uint16_t*>(raw + L::kRawData + key * (D / 16) + 2 * piece);
+          if (!seen) w[x] = make_uint4(0, 0, 0, 0), f[x] = 0;  // not there: anything
+        }
+        warp_arrive(&raw_free[slot]);
+        if (it >= kStages) {
+          ok = __all_sync(0xffffffffu, tc::mbar_wait(v ? &v_free[s] : &k_free[s], ((it / kStages) & 1) ^ 1));
+          if (!ok) break;
+        }
+        uint8_t* dst = smem + (v ? L::kV : L::kK) + s * L::kOperand + key * 16;
+#pragma unroll
+        for (int x = 0; x < W; ++x) {  // 32 channels: two scales, four chunks
+          uint8_t* at = dst + ((x + turn) % W) * (4 * kChunk);
+          const uint32_t c[4] = {w[x].x, w[x].y, w[x].z, w[x].w};
+          const uint32_t sc = scales2(f[x]);
+#pragma unroll
+          for (int y = 0; y < 4; ++y) {
+            uint32_t h[4];
+            codes8(c[y], h);
+            const uint32_t one = __byte_perm(sc, 0, y < 2 ? 0x1010u : 0x3232u);
+            *reinterpret_cast<uint4*>(at + y * kChunk) =
+                make_uint4(mul2(h[0], one), mul2(h[1], one), mul2(h[2], one), mul2(h[3], one));
+          }
+        }
+        tc::fence_async_smem();
+        warp_arrive(v ? &v_full[s] : &k_full[s]);
+      }
+    } else if (warp == kKeyWarp || warp == kValueWarp) {
+      const bool v = warp == kValueWarp;
+      const uint8_t* src = v ? a.c.v : a.c.k;
+      uint64_t* full = v ? v_full : k_full;
+      uint64_t* free_ = v ? v_free : k_free;
+      for (int it = 0; it < n_it; ++it) {
+        const int s = it % kStages;
+        uint8_t* dst = smem + (v ? L::kV : L::kK) + s * L::kOperand;
+        if (it >= kStages && !__all_sync(0xffffffffu, tc::mbar_wait(&free_[s], ((it / kStages) & 1) ^ 1))) {
+          ok = false;
+          break;
+        }
+        int64_t at[2];  // the tile's pages; -1: not there
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          const int pg = pb + 2 * it + x;
+          const int32_t page = pg < pe ? __ldg(table + pg) : -1;
+          const bool there = page >= 0 && page < a.c.num_pages;
+          if (pg < pe && !there && lane == 0) report(a.status, CSA2_ERR_BAD_PAGE);
+          at[x] = there ? ((int64_t)page * a.kv_heads + kh) * kv_block_bytes(D, false) : -1;
+        }
+        // Scores of keys that are not seen are never used, but values are
+        // multiplied by weight 0: what lies in slots from kv_len on (anything) and
+        // in the place of pages that are not there has to be 0.
+        const int live = keys - key0 - it * kTileKeys;
+        const bool tail = v && live < kTileKeys && (live < kPage ? at[0] : at[1]) >= 0;
+        const uint32_t bytes = ((at[0] >= 0) + (at[1] >= 0)) * (L::kOperand / 2);
+        uint64_t* bar = tail ? &tail_full : &full[s];
+        if (lane == 0) tc::mbar_arrive_expect_tx(bar, bytes);
+        __syncwarp();
+        for (int x = lane; x < 2 * (D / 8); x += 32)
+          if ((x & 1 ? at[1] : at[0]) >= 0)
+            tc::bulk_g2s(dst + (x / 2) * kChunk + (x & 1) * (kPage * 16),
+                         src + (x & 1 ? at[1] : at[0]) + (x / 2) * (kPage * 16), kPage * 16, bar);
+        if (tail) {  // the last tile
+          ok = __all_sync(0xffffffffu, tc::mbar_wait(&tail_full, 0));
+          if (!ok) break;
+        }
+        if (v && (tail || bytes != L::kOperand)) {
+          for (int x = lane; x < kTileKeys * (D / 8); x += 32) {
+            const int key = x % kTileKeys;
+            if (key >= live || (key < kPage ? at[0] : at[1]) < 0)
+              *reinterpret_cast<uint4*>(dst + (x / kTileKeys) * kChunk + key * 16) = make_uint4(0, 0, 0, 0);
+          }
+          tc::fence_async_smem();
+        }
+        if (lane != 0 || tail) tc::mbar_arrive(&full[s]);
+      }
+    }
+  } else {
+    regs_dec<kIssueRegs>();
+    const int ring = turns ? kLongRing : kRing;
+    if (warp == kProductWarp && n_it > 0) {
       // ------------------------------------------------------- products --
       constexpr uint32_t kIdS = tc::idesc_f16(128, kTileKeys, !kFp4, !kFp4, false, false);
       constexpr uint32_t kIdO = tc::idesc_f16(128, D, !kFp4, !kFp4, false, true);
@@ -522,101 +618,6 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tiles_kernel(KvAtt a) {
       // nothing may land in shared memory after the CTA has left
       for (int op = max(0, 2 * n_it - ring); !ok && op < 2 * n_it; ++op)
         tc::mbar_wait(&raw_full[op % ring], (op / ring) & 1);
-    } else if (kFp4 && warp < kProductWarp) {
-      // -------------------------------------------------------- decoding --
-      // a row of each tile for each thread: warps 8-11 keys, 12-15 values
-      constexpr int W = D / 32;  // 16-byte pieces of a row
-      const bool v = warp >= kValueWarp;
-      const int key = tid % kTileKeys;
-      // The pieces are taken from another one on by each few keys, so that the
-      // eight keys of a quarter warp's read lie in different banks.
-      const int turn = key / (256 / D);
-      for (int it = 0; it < n_it; ++it) {
-        const int op = 2 * it + v, slot = op % ring, s = it % kStages;
-        ok = __all_sync(0xffffffffu, tc::mbar_wait(&raw_full[slot], (op / ring) & 1));
-        if (!ok) break;
-        const uint8_t* raw = smem + L::raw(slot);
-        const bool seen = key0 + it * kTileKeys + key < keys && pb + 2 * it + key / 64 < pe && ((raw_pages[slot] >> (key / 64)) & 1);
-        uint4 w[W];
-        uint32_t f[W];
-#pragma unroll
-        for (int x = 0; x < W; ++x) {
-          const int piece = (x + turn) % W;
-          w[x] = *reinterpret_cast<const uint4*>(raw + key * (D / 2) + piece * 16);
-          f[x] = *reinterpret_cast<const uint16_t*>(raw + L::kRawData + key * (D / 16) + 2 * piece);
-          if (!seen) w[x] = make_uint4(0, 0, 0, 0), f[x] = 0;  // not there: anything
-        }
-        warp_arrive(&raw_free[slot]);
-        if (it >= kStages) {
-          ok = __all_sync(0xffffffffu, tc::mbar_wait(v ? &v_free[s] : &k_free[s], ((it / kStages) & 1) ^ 1));
-          if (!ok) break;
-        }
-        uint8_t* dst = smem + (v ? L::kV : L::kK) + s * L::kOperand + key * 16;
-#pragma unroll
-        for (int x = 0; x < W; ++x) {  // 32 channels: two scales, four chunks
-          uint8_t* at = dst + ((x + turn) % W) * (4 * kChunk);
-          const uint32_t c[4] = {w[x].x, w[x].y, w[x].z, w[x].w};
-          const uint32_t sc = scales2(f[x]);
-#pragma unroll
-          for (int y = 0; y < 4; ++y) {
-            uint32_t h[4];
-            codes8(c[y], h);
-            const uint32_t one = __byte_perm(sc, 0, y < 2 ? 0x1010u : 0x3232u);
-            *reinterpret_cast<uint4*>(at + y * kChunk) =
-                make_uint4(mul2(h[0], one), mul2(h[1], one), mul2(h[2], one), mul2(h[3], one));
-          }
-        }
-        tc::fence_async_smem();
-        warp_arrive(v ? &v_full[s] : &k_full[s]);
-      }
-    } else if (!kFp4 && (warp == kKeyWarp || warp == kValueWarp)) {
-      const bool v = warp == kValueWarp;
-      const uint8_t* src = v ? a.c.v : a.c.k;
-      uint64_t* full = v ? v_full : k_full;
-      uint64_t* free_ = v ? v_free : k_free;
-      for (int it = 0; it < n_it; ++it) {
-        const int s = it % kStages;
-        uint8_t* dst = smem + (v ? L::kV : L::kK) + s * L::kOperand;
-        if (it >= kStages && !__all_sync(0xffffffffu, tc::mbar_wait(&free_[s], ((it / kStages) & 1) ^ 1))) {
-          ok = false;
-          break;
-        }
-        int64_t at[2];  // the tile's pages; -1: not there
-#pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          const int pg = pb + 2 * it + x;
-          const int32_t page = pg < pe ? __ldg(table + pg) : -1;
-          const bool there = page >= 0 && page < a.c.num_pages;
-          if (pg < pe && !there && lane == 0) report(a.status, CSA2_ERR_BAD_PAGE);
-          at[x] = there ? ((int64_t)page * a.kv_heads + kh) * kv_block_bytes(D, false) : -1;
-        }
-        // Scores of keys that are not seen are never used, but values are
-        // multiplied by weight 0: what lies in slots from kv_len on (anything) and
-        // in the place of pages that are not there has to be 0.
-        const int live = keys - key0 - it * kTileKeys;
-        const bool tail = v && live < kTileKeys && (live < kPage ? at[0] : at[1]) >= 0;
-        const uint32_t bytes = ((at[0] >= 0) + (at[1] >= 0)) * (L::kOperand / 2);
-        uint64_t* bar = tail ? &tail_full : &full[s];
-        if (lane == 0) tc::mbar_arrive_expect_tx(bar, bytes);
-        __syncwarp();
-        for (int x = lane; x < 2 * (D / 8); x += 32)
-          if ((x & 1 ? at[1] : at[0]) >= 0)
-            tc::bulk_g2s(dst + (x / 2) * kChunk + (x & 1) * (kPage * 16),
-                         src + (x & 1 ? at[1] : at[0]) + (x / 2) * (kPage * 16), kPage * 16, bar);
-        if (tail) {  // the last tile
-          ok = __all_sync(0xffffffffu, tc::mbar_wait(&tail_full, 0));
-          if (!ok) break;
-        }
-        if (v && (tail || bytes != L::kOperand)) {
-          for (int x = lane; x < kTileKeys * (D / 8); x += 32) {
-            const int key = x % kTileKeys;
-            if (key >= live || (key < kPage ? at[0] : at[1]) < 0)
-              *reinterpret_cast<uint4*>(dst + (x / kTileKeys) * kChunk + key * 16) = make_uint4(0, 0, 0, 0);
-          }
-          tc::fence_async_smem();
-        }
-        if (lane != 0 || tail) tc::mbar_arrive(&full[s]);
-      }
     }
   }
   __syncwarp();

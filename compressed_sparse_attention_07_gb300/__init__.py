@@ -384,7 +384,7 @@ class KVCache:
         if len({t.device for t in (k_data, v_data, block_table, *(s for s in (k_scales, v_scales) if s is not None))}) > 1:
             raise ValueError("the pages and the block table must be on one device")
         self.k_data, self.v_data, self.k_scales, self.v_scales = k_data, v_data, k_scales, v_scales
-        self.block_table, self.device = block_table, k_data.device
+        self.block_table, self.device, self.device_index = block_table, k_data.device, k_data.get_device()
         self.batch, self.max_pages, self.num_pages = block_table.shape[0], block_table.shape[1], n
         self.capacity = self.max_pages * PAGE
         self.layout = (h, d, cfg.cache_dtype)
@@ -404,14 +404,14 @@ def rope_table(n: int, rope_dims: int, theta: float = 1e4, device="cuda"):
 def _kv_rows(t, heads, dim, name, device):
     """Address and row distance of [T][heads][dim] bf16 rows; a row is contiguous, the rows may stand apart."""
     shape, stride = t.shape, t.stride()
-    if t.dtype is torch.bfloat16 and t.device == device and len(shape) == 3 and shape[1] == heads and \
+    if t.dtype is torch.bfloat16 and t.get_device() == device and len(shape) == 3 and shape[1] == heads and \
             shape[2] == dim and stride[2] == 1 and (stride[1] == dim or heads == 1):
         return t.data_ptr(), (stride[0] if shape[0] > 1 else heads * dim)
     if t.dtype != torch.bfloat16:
         raise TypeError("%s must be torch.bfloat16, got %s" % (name, t.dtype))
     if len(shape) != 3 or shape[1] != heads or shape[2] != dim:
         raise ValueError("%s must be [T][%d][%d], got %s" % (name, heads, dim, list(shape)))
-    if t.device != device:
+    if t.get_device() != device:
         raise ValueError("%s must be on the cache's device" % name)
     raise ValueError("%s: the channels of a row must be contiguous" % name)
 
@@ -420,13 +420,13 @@ def _kv_ptr(t, dtype, shape, name, device):
     """Address of a contiguous tensor of a given shape on the cache's device."""
     if t is None:
         return None
-    if t.dtype is dtype and t.shape == shape and t.device == device and t.is_contiguous():
+    if t.dtype is dtype and t.shape == shape and t.get_device() == device and t.is_contiguous():
         return t.data_ptr()
     if t.dtype != dtype:
         raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
     if t.shape != shape:
         raise ValueError("%s must be %s, got %s" % (name, list(shape), list(t.shape)))
-    if t.device != device:
+    if t.get_device() != device:
         raise ValueError("%s must be on the cache's device" % name)
     raise ValueError("%s must be contiguous" % name)
 
@@ -438,7 +438,7 @@ _raw_stream = torch._C._cuda_getCurrentRawStream if hasattr(torch._C, "_cuda_get
 
 def _kv_call(fn, cache, stream, *args):
     """Call fn on `stream`, or on the current stream of the cache's device, with that device current."""
-    index = cache.device.index
+    index = cache.device_index
     if index == torch.cuda.current_device():
         return fn(*args, _raw_stream(index) if stream is None else stream.cuda_stream)
     with torch.cuda.device(index):
@@ -456,7 +456,7 @@ def kv_append(cfg: KVCfg, k, v, cu, pos0, cache: KVCache, rope=None, q=None, q_o
     cu[b] + i, position pos0[b] + i), keys and queries q [T][n_heads][head_dim] rotated by `rope` [rows][rope_dims / 2]
     [2] fp32.  q_out (which may be q) takes the rotated queries, k_out / v_out the values as stored."""
     _kv_same(cfg, cache)
-    dev, h, d = cache.device, cfg.kv_heads, cfg.head_dim
+    dev, h, d = cache.device_index, cfg.kv_heads, cfg.head_dim
     T, B = k.shape[0], cache.batch
     kp, ks = _kv_rows(k, h, d, "k", dev)
     vp, vs = _kv_rows(v, h, d, "v", dev)
@@ -486,7 +486,7 @@ def kv_workspace_bytes(cfg: KVCfg, B: int, T: int, max_q: int, max_kv: int) -> i
 
 def _kv_attend(name, cfg, q, cu, cache, kv_len, max_q, max_kv, out, lse, scale, workspace, status, stream):
     _kv_same(cfg, cache)
-    dev, h, d = cache.device, cfg.n_heads, cfg.head_dim
+    dev, h, d = cache.device_index, cfg.n_heads, cfg.head_dim
     T, B = q.shape[0], cache.batch
     qp, qs = _kv_rows(q, h, d, "q", dev)
     op, os_ = _kv_rows(out, h, d, "out", dev)
@@ -494,7 +494,7 @@ def _kv_attend(name, cfg, q, cu, cache, kv_len, max_q, max_kv, out, lse, scale, 
         raise ValueError("q and out must have the same rows")
     wp, wn = None, 0
     if workspace is not None:
-        if workspace.device != dev or not workspace.is_contiguous():
+        if workspace.get_device() != dev or not workspace.is_contiguous():
             raise ValueError("workspace must be contiguous on the cache's device")
         wp, wn = workspace.data_ptr(), workspace.numel() * workspace.element_size()
     scale = 1.0 / math.sqrt(d) if scale is None else float(scale)

@@ -99,6 +99,7 @@ struct KvAtt {
   // partial outputs go to part_o [n_parts][T * n_heads][dim] and their
   // log2-sum-exp2 to part_l [n_parts][T * n_heads]
   int n_parts, part_pages;
+  int cluster;  // the parts of a head join in a cluster instead
   float* part_o;
   float* part_l;
   int32_t* status;
@@ -142,9 +143,14 @@ cudaError_t launch_kv_append(const csa2_kv_cfg& cfg, int B, int T, const uint16_
                              const KvView& c, uint16_t* q_out, int64_t q_out_stride, uint16_t* k_out, uint16_t* v_out,
                              int32_t* status, cudaStream_t stream);
 
-// n_parts and part_pages of a call, from sizes alone (the most parts it uses).
-void kv_plan(const csa2_kv_cfg& cfg, int B, int max_q, int max_kv, bool cross, int most_parts, int* n_parts,
-             int* part_pages);
+// How a call divides the keys, from sizes alone; most_parts: what the workspace
+// holds.
+struct KvPlan {
+  int n_parts, part_pages;
+  bool cluster;  // the parts join in a cluster, without workspace
+};
+KvPlan kv_plan(const csa2_kv_cfg& cfg, int B, int max_q, int max_kv, bool cross, int most_parts);
+
 // Let `kern` use `bytes` of dynamic shared memory: set once on each device.
 template <typename K>
 cudaError_t allow_smem(K kern, int bytes, bool (&done)[64]) {
@@ -156,8 +162,8 @@ cudaError_t allow_smem(K kern, int bytes, bool (&done)[64]) {
   return e;
 }
 
-// The same of the tile kernel, which takes more rows of a kv head than
-// kMostRows; its launch, and the rows of its CTA.
+// The plan of the tile kernel, which takes more rows of a kv head than kMostRows;
+// its launch, and the rows of its CTA.
 constexpr int kMostRows = 32;
 void kv_tiles_plan(const csa2_kv_cfg& cfg, int B, int max_q, int64_t max_kv, bool cross, int most_parts, int* n_parts,
                    int* part_pages);

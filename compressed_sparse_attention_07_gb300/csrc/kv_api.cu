@@ -68,8 +68,9 @@ int32_t attend(const csa2_kv_cfg* cfg, bool cross, int32_t B, int32_t T, const u
   const int64_t rows = (int64_t)T * cfg->n_heads;
   const size_t one = (size_t)rows * (cfg->head_dim + 1) * 4;
   const size_t fit = workspace_bytes / one;
-  kv_plan(*cfg, B, a.max_q, max_kv, cross, fit > 1024 ? 1024 : (int)fit, &a.n_parts, &a.part_pages);
-  if (a.n_parts > 1) {
+  const KvPlan plan = kv_plan(*cfg, B, a.max_q, max_kv, cross, fit > 1024 ? 1024 : (int)fit);
+  a.n_parts = plan.n_parts, a.part_pages = plan.part_pages, a.cluster = plan.cluster ? 1 : 0;
+  if (a.n_parts > 1 && !a.cluster) {
     a.part_o = static_cast<float*>(workspace);
     a.part_l = a.part_o + a.n_parts * rows * cfg->head_dim;
   }
@@ -110,11 +111,13 @@ int32_t csa2_kv_append(const csa2_kv_cfg* cfg, int32_t B, int32_t T, const uint1
 
 size_t csa2_kv_workspace_bytes(const csa2_kv_cfg* cfg, int32_t B, int32_t T, int32_t max_q, int32_t max_kv) {
   if (check_cfg(cfg) || B < 0 || T < 0 || max_q < 0 || max_kv < 0 || B == 0 || T == 0 || max_q == 0) return 0;
-  int self = 1, cross = 1, pages;
   if (max_q > T) max_q = T;
-  kv_plan(*cfg, B, max_q, max_kv, false, 1024, &self, &pages);
-  if (!cfg->window) kv_plan(*cfg, B, max_q, max_kv, true, 1024, &cross, &pages);
-  const int n = self > cross ? self : cross;
+  int n = 1;
+  for (const bool cross : {false, true}) {
+    if (cross && cfg->window) break;
+    const KvPlan plan = kv_plan(*cfg, B, max_q, max_kv, cross, 1024);
+    if (!plan.cluster && plan.n_parts > n) n = plan.n_parts;
+  }
   return n > 1 ? (size_t)n * T * cfg->n_heads * (cfg->head_dim + 1) * 4 : 0;
 }
 

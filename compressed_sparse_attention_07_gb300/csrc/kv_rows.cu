@@ -2,11 +2,14 @@
 // decode, drafted blocks): every key and value is read once from HBM for up to
 // 32 rows (query heads of a kv head x new tokens), so the cache's bytes decide.
 //
-// One CTA takes one kv head, up to 8 NT rows and a part of the keys; its four
-// warps take tiles of 64 keys (FP4, one page) or 32 (bf16) in turn, each with
+// One CTA takes one kv head, up to 8 NT rows and a part of the keys; its warps
+// (four) take tiles of 64 keys (FP4, one page) or 32 (bf16) in turn, each with
 // its own two-stage ring of bulk copies, its own running maximum, sum and
 // output in registers, joined through shared memory at the end.  With several
-// parts a second kernel joins them (in part order, so results do not vary).
+// parts a second kernel joins them (in part order, so results do not vary);
+// where up to eight parts of every head run at once, one CTA an SM, the parts of
+// a head are a cluster of CTAs of eight warps, which join through distributed
+// shared memory: one launch, and no workspace.
 //
 // The products are formed transposed, S^T = K Q^T (m16n8k16: 16 keys, 8 rows)
 // and O^T = V^T P^T (16 channels, 8 rows), so 8 rows fill an instruction where
@@ -30,10 +33,11 @@
 namespace csa2 {
 namespace {
 
-constexpr int kWarps = 4;
+constexpr int kMostCluster = 8;  // CTAs that join through distributed shared memory
 
-template <int D, bool kFp4, int NT>
+template <int D, bool kFp4, int NT, bool kCluster>
 struct Rows {
+  static constexpr int kWarps = kCluster && (kFp4 || D == 64) ? 8 : 4;
   static constexpr int kTile = kFp4 ? 64 : 32;                   // keys of a tile
   static constexpr int kPerPage = kPage / kTile;
   static constexpr int kSub = (kFp4 && NT < 4) ? 64 : 32;        // keys of a softmax step
@@ -43,9 +47,10 @@ struct Rows {
   static constexpr int kWarpBytes = 2 * kStage;
   static constexpr int kOPitch = D + 8;                          // floats of a row in the joining area
   static constexpr int kQFrag = NT * (D / 16) * 32 * 8;  // query fragments
-  static constexpr int kSmem = kWarps * kWarpBytes + kQFrag;
+  static constexpr int kJoined = kCluster ? 8 * NT * D * 4 : 0;  // this CTA's part, for the cluster to read
+  static constexpr int kSmem = kWarps * kWarpBytes + kQFrag + kJoined;
   static_assert(8 * NT * kOPitch * 4 <= kWarpBytes, "the joining area fits a warp's ring");
-  static constexpr int kCtas = kSmem > 112 * 1024 ? 1 : (kSmem > 72 * 1024 || NT > 1) ? 2 : 3;
+  static constexpr int kCtas = kCluster || kSmem > 112 * 1024 ? 1 : (kSmem > 72 * 1024 || NT > 1) ? 2 : 3;
 };
 
 template <bool kF16>
@@ -74,15 +79,17 @@ __device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
                  : "memory");
 }
 
-template <int D, bool kFp4, int NT>
-__global__ void __launch_bounds__(kWarps * 32, Rows<D, kFp4, NT>::kCtas) kv_rows_kernel(KvAtt a) {
-  using R = Rows<D, kFp4, NT>;
-  constexpr int kRows = 8 * NT, KS = D / 16, MT = D / 16;
+template <int D, bool kFp4, int NT, bool kCluster>
+__global__ void __launch_bounds__(Rows<D, kFp4, NT, kCluster>::kWarps * 32, Rows<D, kFp4, NT, kCluster>::kCtas)
+    kv_rows_kernel(KvAtt a) {
+  using R = Rows<D, kFp4, NT, kCluster>;
+  constexpr int kWarps = R::kWarps, kRows = 8 * NT, KS = D / 16, MT = D / 16;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ __align__(8) uint64_t bars[kWarps][2];
   __shared__ int row_hi[kRows], row_lo[kRows];
   __shared__ float row_scale[kRows];
   __shared__ float join_m[kWarps][kRows], join_l[kWarps][kRows];
+  __shared__ float part_l[kRows];  // (cluster) this CTA's log2-sum-exp2 of each row
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
   const int part = blockIdx.x, kh = blockIdx.y % a.kv_heads, tile0 = (blockIdx.y / a.kv_heads) * kRows, b = blockIdx.z;
@@ -98,8 +105,8 @@ __global__ void __launch_bounds__(kWarps * 32, Rows<D, kFp4, NT>::kCtas) kv_rows
   int p0, p1;
   kv_pages(a, tile0 / a.group, last / a.group, rows, keys, p0, p1);
   const int n_act = (p1 - p0 + a.part_pages - 1) / a.part_pages;
-  if (part > 0 && part >= n_act) return;
-  const int pb = p0 + part * a.part_pages, pe = min(pb + a.part_pages, p1);
+  if (!kCluster && part > 0 && part >= n_act) return;
+  const int pb = min(p0 + part * a.part_pages, p1), pe = min(pb + a.part_pages, p1);
   const int key_end = kv_hi(a, last / a.group, rows, keys);  // no row sees keys from here on
   const int tb = pb * R::kPerPage, te = min(pe * R::kPerPage, (key_end + R::kTile - 1) / R::kTile);
 
@@ -436,7 +443,8 @@ __global__ void __launch_bounds__(kWarps * 32, Rows<D, kFp4, NT>::kCtas) kv_rows
     if (tile + 2 * kWarps < te && load(tile + 2 * kWarps, stage)) filled |= 1u << stage;
   }
   if (late && lane == 0) report(a.status, CSA2_ERR_TIMEOUT);
-  if (__syncthreads_or(late)) return;
+  late = __syncthreads_or(late);
+  if (!kCluster && late) return;
 
   // ---- join the warps
 #pragma unroll
@@ -459,6 +467,7 @@ __global__ void __launch_bounds__(kWarps * 32, Rows<D, kFp4, NT>::kCtas) kv_rows
             make_float2(o[x][n][e], o[x][n][2 + e]);
   __syncthreads();
   const bool whole = n_act <= 1;
+  float* joined = reinterpret_cast<float*>(smem + kWarps * R::kWarpBytes + R::kQFrag);  // [kRows][D] (cluster)
   for (int x = tid; x < kRows * (D / 2); x += kWarps * 32) {
     const int r = x / (D / 2), c = 2 * (x % (D / 2));
     if (tile0 + r >= n_rows) break;
@@ -484,13 +493,58 @@ __global__ void __launch_bounds__(kWarps * 32, Rows<D, kFp4, NT>::kCtas) kv_rows
     const int64_t at = (int64_t)i * a.n_heads + h;
     const float lse2 = sum == 0.0f ? -INFINITY : top + log2f(sum);
     if (whole) {
+      if (kCluster && part > 0) break;
       *reinterpret_cast<uint32_t*>(a.out + (int64_t)i * a.out_stride + h * D + c) = bf16x2(v0 * inv, v1 * inv);
       if (a.lse && c == 0) a.lse[at] = lse2 * kLn2;
+    } else if (kCluster) {
+      *reinterpret_cast<float2*>(joined + r * D + c) = make_float2(v0 * inv, v1 * inv);
+      if (c == 0) part_l[r] = lse2;
     } else {
       const int64_t pa = (int64_t)part * a.T * a.n_heads + at;
       *reinterpret_cast<float2*>(a.part_o + pa * D + c) = make_float2(v0 * inv, v1 * inv);
       if (c == 0) a.part_l[pa] = lse2;
     }
+  }
+  if constexpr (kCluster) {
+    // ---- join the parts through distributed shared memory, each CTA a share of
+    // the channels, in part order
+    __syncthreads();
+    tc::cluster_sync();
+    if (!whole) {
+      const uint32_t mine_o = tc::smem_u32(joined), mine_l = tc::smem_u32(part_l);
+      for (int x = part * (kWarps * 32) + tid; x < kRows * (D / 4); x += gridDim.x * (kWarps * 32)) {
+        const int r = x / (D / 4), c = 4 * (x % (D / 4));
+        if (tile0 + r >= n_rows) break;
+        float lp[kMostCluster];
+        float4 v[kMostCluster];
+        float top = -INFINITY;
+#pragma unroll
+        for (int p = 0; p < kMostCluster; ++p) {
+          lp[p] = -INFINITY;
+          if (p < n_act) {
+            lp[p] = tc::ld_dsmem(tc::map_rank(mine_l + 4 * r, p));
+            v[p] = tc::ld_dsmem_v4(tc::map_rank(mine_o + 4 * (r * D + c), p));
+            top = fmaxf(top, lp[p]);
+          }
+        }
+        float sum = 0.0f, o0 = 0.0f, o1 = 0.0f, o2 = 0.0f, o3 = 0.0f;
+#pragma unroll
+        for (int p = 0; p < kMostCluster; ++p) {
+          if (p < n_act) {
+            const float f = lp[p] == -INFINITY ? 0.0f : ex2(lp[p] - top);
+            sum += f;
+            o0 += f * v[p].x, o1 += f * v[p].y, o2 += f * v[p].z, o3 += f * v[p].w;
+          }
+        }
+        const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+        const int i = row0 + (tile0 + r) / a.group, h = kh * a.group + (tile0 + r) % a.group;
+        *reinterpret_cast<uint2*>(a.out + (int64_t)i * a.out_stride + h * D + c) =
+            make_uint2(bf16x2(o0 * inv, o1 * inv), bf16x2(o2 * inv, o3 * inv));
+        if (a.lse && c == 0) a.lse[(int64_t)i * a.n_heads + h] = sum == 0.0f ? -INFINITY : (top + log2f(sum)) * kLn2;
+      }
+    }
+    __syncthreads();
+    tc::cluster_sync();  // nobody leaves while his part may be read
   }
 }
 
@@ -540,31 +594,47 @@ __global__ void __launch_bounds__(256) kv_join_kernel(KvAtt a, int tile_rows) {
   if (a.lse && lane == 0) a.lse[at] = sum == 0.0f ? -INFINITY : (top + log2f(sum)) * kLn2;
 }
 
-template <int D, bool kFp4, int NT>
+template <int D, bool kFp4, int NT, bool kCluster>
 cudaError_t launch(int B, const KvAtt& a, cudaStream_t stream) {
-  using R = Rows<D, kFp4, NT>;
-  auto kern = kv_rows_kernel<D, kFp4, NT>;
+  using R = Rows<D, kFp4, NT, kCluster>;
+  auto kern = kv_rows_kernel<D, kFp4, NT, kCluster>;
   static bool done[64];
   const cudaError_t e = allow_smem(kern, R::kSmem, done);
   if (e != cudaSuccess) return e;
   const int tiles = (int)(((int64_t)a.max_q * a.group + 8 * NT - 1) / (8 * NT));
-  return launch_k(kern, dim3(a.n_parts, tiles * a.kv_heads, B), dim3(kWarps * 32), R::kSmem, stream, 0, a);
+  return launch_k(kern, dim3(a.n_parts, tiles * a.kv_heads, B), dim3(R::kWarps * 32), R::kSmem, stream,
+                  kCluster ? a.n_parts : 0, a);
 }
 
 template <int D, bool kFp4>
-int ctas(int nt) {
-  return nt == 1 ? Rows<D, kFp4, 1>::kCtas : nt == 2 ? Rows<D, kFp4, 2>::kCtas : Rows<D, kFp4, 4>::kCtas;
+cudaError_t launch_rows(int nt, int B, const KvAtt& a, cudaStream_t stream) {
+  if (a.cluster)
+    return nt == 1   ? launch<D, kFp4, 1, true>(B, a, stream)
+           : nt == 2 ? launch<D, kFp4, 2, true>(B, a, stream)
+                     : launch<D, kFp4, 4, true>(B, a, stream);
+  return nt == 1   ? launch<D, kFp4, 1, false>(B, a, stream)
+         : nt == 2 ? launch<D, kFp4, 2, false>(B, a, stream)
+                   : launch<D, kFp4, 4, false>(B, a, stream);
+}
+
+// CTAs of an SM without clusters, and warps of a CTA with.
+template <int D, bool kFp4>
+void shape(int nt, int* ctas, int* warps) {
+  *ctas = nt == 1 ? Rows<D, kFp4, 1, false>::kCtas : nt == 2 ? Rows<D, kFp4, 2, false>::kCtas : Rows<D, kFp4, 4, false>::kCtas;
+  *warps = Rows<D, kFp4, 1, true>::kWarps;
 }
 
 int row_blocks(int64_t n) { return n <= 8 ? 1 : n <= 16 ? 2 : 4; }
 
 }  // namespace
 
-void kv_plan(const csa2_kv_cfg& cfg, int B, int max_q, int max_kv, bool cross, int most_parts, int* n_parts,
-             int* part_pages) {
+KvPlan kv_plan(const csa2_kv_cfg& cfg, int B, int max_q, int max_kv, bool cross, int most_parts) {
   const int group = cfg.n_heads / cfg.kv_heads;
-  if ((int64_t)max_q * group > kMostRows)
-    return kv_tiles_plan(cfg, B, max_q, max_kv, cross, most_parts, n_parts, part_pages);
+  KvPlan plan = {1, 1, false};
+  if ((int64_t)max_q * group > kMostRows) {
+    kv_tiles_plan(cfg, B, max_q, max_kv, cross, most_parts, &plan.n_parts, &plan.part_pages);
+    return plan;
+  }
   const int nt = row_blocks((int64_t)max_q * group);
   const int64_t tiles = ((int64_t)max_q * group + 8 * nt - 1) / (8 * nt);
   int64_t pages = ((int64_t)max_kv + kPage - 1) / kPage;
@@ -572,40 +642,46 @@ void kv_plan(const csa2_kv_cfg& cfg, int B, int max_q, int max_kv, bool cross, i
     pages = std::min<int64_t>(pages, ((int64_t)cfg.window + std::min<int64_t>(max_q, 8 * nt) + kPage - 2) / kPage + 1);
   if (pages < 1) pages = 1;
   const bool fp4 = cfg.cache_dtype == CSA2_CACHE_FP4;
-  const int per_sm = cfg.head_dim == 128 ? (fp4 ? ctas<128, true>(nt) : ctas<128, false>(nt))
-                                         : (fp4 ? ctas<64, true>(nt) : ctas<64, false>(nt));
+  int per_sm, wide;
+  if (cfg.head_dim == 128) fp4 ? shape<128, true>(nt, &per_sm, &wide) : shape<128, false>(nt, &per_sm, &wide);
+  else fp4 ? shape<64, true>(nt, &per_sm, &wide) : shape<64, false>(nt, &per_sm, &wide);
   const int64_t sms = num_sms(), base = (int64_t)B * cfg.kv_heads * tiles;
   // The number of parts that ends soonest, in units of a page's share of an
   // SM's throughput: an SM's CTAs (n at most, each its pages and about three
   // pages' work besides) share it, but one warp alone needs about ten units for
-  // a page and a CTA eight to start and end; joining costs ten.
+  // a page and a CTA eight to start and end; joining in a second kernel costs
+  // ten, in a cluster four.  Clusters, of `wide` warps a CTA, where they all run
+  // at once, one CTA an SM.
   int best = 1;
   double cost = 1e30;
-  for (int s = 1; s <= most_parts && s <= 128; ++s) {
+  for (int s = 1; s <= 128; ++s) {
     const int64_t pp = (pages + s - 1) / s, n = (base * s + sms - 1) / sms;
-    if (s > 1 && pp < kWarps) break;
-    const double c = std::max((double)n * (pp + 3),
-                              (double)((n + per_sm - 1) / per_sm) * ((pp + kWarps - 1) / kWarps * 10 + 8)) +
-                     (s > 1 ? 10 : 0);
-    if (c < cost * 0.999) cost = c, best = s;
+    if (s > 1 && pp < 4) break;
+    if (s <= most_parts || s == 1) {
+      const double c = std::max((double)n * (pp + 3), (double)((n + per_sm - 1) / per_sm) * ((pp + 3) / 4 * 10 + 8)) +
+                       (s > 1 ? 10 : 0);
+      if (c < cost * 0.999) cost = c, best = s, plan.cluster = false;
+    }
+    if (s > 1 && s <= kMostCluster && n == 1) {
+      const double c = std::max((double)(pp + 3), (double)((pp + wide - 1) / wide * 10 + 8)) + 4;
+      if (c < cost * 0.999) cost = c, best = s, plan.cluster = true;
+    }
   }
-  *part_pages = (int)((pages + best - 1) / best);
-  *n_parts = (int)((pages + *part_pages - 1) / *part_pages);
+  plan.part_pages = (int)((pages + best - 1) / best);
+  plan.n_parts = (int)((pages + plan.part_pages - 1) / plan.part_pages);
+  if (plan.n_parts == 1) plan.cluster = false;
+  return plan;
 }
 
 cudaError_t launch_kv_attend(const csa2_kv_cfg& cfg, int B, KvAtt& a, cudaStream_t stream) {
   const int nt = row_blocks((int64_t)a.max_q * a.group);
-  const bool fp4 = cfg.cache_dtype == CSA2_CACHE_FP4;
-  cudaError_t e;
-#define CSA2_ROWS(D, F) \
-  (nt == 1 ? launch<D, F, 1>(B, a, stream) : nt == 2 ? launch<D, F, 2>(B, a, stream) : launch<D, F, 4>(B, a, stream))
-  const bool many = (int64_t)a.max_q * a.group > kMostRows;
+  const bool fp4 = cfg.cache_dtype == CSA2_CACHE_FP4, many = (int64_t)a.max_q * a.group > kMostRows;
   const int tile_rows = many ? kv_tiles_rows() : 8 * nt;
+  cudaError_t e;
   if (many) e = launch_kv_tiles(cfg, B, a, stream);
-  else if (cfg.head_dim == 128) e = fp4 ? CSA2_ROWS(128, true) : CSA2_ROWS(128, false);
-  else e = fp4 ? CSA2_ROWS(64, true) : CSA2_ROWS(64, false);
-#undef CSA2_ROWS
-  if (e != cudaSuccess || a.n_parts <= 1) return e;
+  else if (cfg.head_dim == 128) e = fp4 ? launch_rows<128, true>(nt, B, a, stream) : launch_rows<128, false>(nt, B, a, stream);
+  else e = fp4 ? launch_rows<64, true>(nt, B, a, stream) : launch_rows<64, false>(nt, B, a, stream);
+  if (e != cudaSuccess || a.n_parts <= 1 || a.cluster) return e;
   const dim3 grid((unsigned)(((int64_t)a.max_q * a.n_heads + 7) / 8), B);
   return cfg.head_dim == 128 ? launch_k(kv_join_kernel<128>, grid, dim3(256), 0, stream, 0, a, tile_rows)
                              : launch_k(kv_join_kernel<64>, grid, dim3(256), 0, stream, 0, a, tile_rows);

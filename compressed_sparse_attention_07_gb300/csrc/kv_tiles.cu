@@ -158,46 +158,60 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tiles_kernel(KvAtt a) {
     float scale;
     int hi = 0, lo = 0;
     const int r = tile0 + (turns ? tid % kTileRows : tid);
+    if (r < n_rows) hi = kv_hi(a, r / a.group, rows, keys), lo = kv_lo(a, r / a.group, rows, keys);
     {
-      const bool live = r < n_rows;
-      const int i = live ? r / a.group : 0, h = kh * a.group + (live ? r % a.group : 0);
-      if (live) hi = kv_hi(a, i, rows, keys), lo = kv_lo(a, i, rows, keys);
-      const uint16_t* q = a.q + (int64_t)(row0 + i) * a.q_stride + h * D;
-      uint8_t* dst = smem + L::kQ + (tid / kTileRows) * L::kOperand + (tid % kTileRows) * 16;
+      // A lane loads parts of four rows, 8 x + its number & 7 of the warp's: 64
+      // neighbouring bytes of eight rows at a time (a lane with a row to itself, 16
+      // bytes of 32 rows at a time, took 8 000 cycles for 64 channels), and eight
+      // lanes store the same chunk of neighbouring rows.
+      const int sub = lane & 7, c0 = lane >> 3;
       const uint32_t sign = a.scale < 0.0f ? 0x80008000u : 0u;  // into the query: the scale is positive below
       scale = fabsf(a.scale) * kLog2e;
-      uint4 w[D / 8];
+      uint4 w[4][D / 32];
 #pragma unroll
-      for (int c = 0; c < D / 8; ++c) {
-        w[c] = make_uint4(0, 0, 0, 0);
-        if (live) w[c] = __ldg(reinterpret_cast<const uint4*>(q) + c);
-      }
-      float down = 1.0f;
-      if constexpr (kFp4) {
-        uint32_t most = 0;
+      for (int x = 0; x < 4; ++x) {
+        const int rr = r - lane + 8 * x + sub;
+        const bool live = rr < n_rows;
+        const uint16_t* q = a.q;
+        if (live) q += (int64_t)(row0 + rr / a.group) * a.q_stride + (kh * a.group + rr % a.group) * D;
 #pragma unroll
-        for (int c = 0; c < D / 8; ++c) {
-          const uint32_t u[4] = {w[c].x, w[c].y, w[c].z, w[c].w};
-#pragma unroll
-          for (int y = 0; y < 4; ++y) most = max(most, max(u[y] & 0x7F80u, (u[y] >> 16) & 0x7F80u));
+        for (int c = 0; c < D / 32; ++c) {
+          w[x][c] = make_uint4(0, 0, 0, 0);
+          if (live) w[x][c] = __ldg(reinterpret_cast<const uint4*>(q) + 4 * c + c0);
         }
-        // the largest channel's exponent, biased, where its power of two and the
-        // inverse are both normal numbers
-        const uint32_t e = min(max(most >> 7, 1u), 253u);
-        down = __uint_as_float((254u - e) << 23);
-        scale *= __uint_as_float(e << 23);
       }
-      if (!turns || tid < kTileRows) {
 #pragma unroll
-        for (int c = 0; c < D / 8; ++c) {
-          uint32_t u[4] = {w[c].x, w[c].y, w[c].z, w[c].w};
+      for (int x = 0; x < 4; ++x) {
+        float down = 1.0f;
+        if constexpr (kFp4) {
+          uint32_t most = 0;
 #pragma unroll
-          for (int y = 0; y < 4; ++y) {
-            if constexpr (kFp4)
-              u[y] = f16x2(__uint_as_float(u[y] << 16) * down, __uint_as_float(u[y] & 0xFFFF0000u) * down);
-            u[y] ^= sign;
+          for (int c = 0; c < D / 32; ++c) {
+            const uint32_t u[4] = {w[x][c].x, w[x][c].y, w[x][c].z, w[x][c].w};
+#pragma unroll
+            for (int y = 0; y < 4; ++y) most = max(most, max(u[y] & 0x7F80u, (u[y] >> 16) & 0x7F80u));
           }
-          *reinterpret_cast<uint4*>(dst + c * kChunk) = make_uint4(u[0], u[1], u[2], u[3]);
+          most = max(most, __shfl_xor_sync(0xffffffffu, most, 8));
+          most = max(most, __shfl_xor_sync(0xffffffffu, most, 16));
+          // the largest channel's exponent, biased, where its power of two and the
+          // inverse are both normal numbers
+          const uint32_t e = min(max(most >> 7, 1u), 253u);
+          down = __uint_as_float((254u - e) << 23);
+          if (c0 == x) scale *= __uint_as_float(e << 23);  // this lane's own row
+        }
+        if (!turns || tid < kTileRows) {
+          uint8_t* dst = smem + L::kQ + (tid / kTileRows) * L::kOperand + (32 * (warp & 3) + 8 * x + sub) * 16;
+#pragma unroll
+          for (int c = 0; c < D / 32; ++c) {
+            uint32_t u[4] = {w[x][c].x, w[x][c].y, w[x][c].z, w[x][c].w};
+#pragma unroll
+            for (int y = 0; y < 4; ++y) {
+              if constexpr (kFp4)
+                u[y] = f16x2(__uint_as_float(u[y] << 16) * down, __uint_as_float(u[y] & 0xFFFF0000u) * down);
+              u[y] ^= sign;
+            }
+            *reinterpret_cast<uint4*>(dst + (4 * c + c0) * kChunk) = make_uint4(u[0], u[1], u[2], u[3]);
+          }
         }
       }
       scale = fmaxf(scale, 1e-37f);  // above 0: a hidden key's -inf stays -inf

@@ -344,46 +344,72 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tiles_kernel(KvAtt a) {
           if (!whole) a.part_l[pa] = lse2;
           else if (a.lse) a.lse[at] = lse2 * kLn2;
         }
+        // where this lane's row goes, or 0
+        const uint64_t home = !live ? 0 : whole ? reinterpret_cast<uint64_t>(a.out + (int64_t)i * a.out_stride + h * D)
+                                                : reinterpret_cast<uint64_t>(a.part_o + pa * D);
         const uint32_t o0 = tc::taddr(tb, lane_base, 256), o1 = tc::taddr(tb, lane_base, 256 + D);
-        // (turns) each place writes one half of the channels
+        // The rows pass through shared memory (the place's queries are done with),
+        // so that neighbouring lanes write neighbouring 16 bytes of a row: its unit x
+        // of 64 bytes stands at x ^ (row / 2 & 3).
+        uint8_t* pad = smem + L::kQ + j * L::kOperand + (warp & 3) * 2048;
+        const float g0 = inv * (turns ? f[0] : 1.0f), g1 = inv * f[1];
+        uint64_t to[4];  // four lanes a row, eight rows at a time
+#pragma unroll
+        for (int x = 0; x < 4; ++x) to[x] = __shfl_sync(0xffffffffu, home, 8 * x + lane / 4);
 #pragma unroll
         for (int c = 0; c < D / 32; ++c) {
-          if (turns && c / (D / 64) != j) continue;
+          if (turns && c / (D / 64) != j) continue;  // (turns) each place writes one half of the channels
           uint32_t o[32];
           if (n_it > 0) {
             tc::tmem_ld32((j == 1 && !turns ? o1 : o0) + 32 * c, o);
             tc::tmem_wait_ld();
-            const float g = inv * (turns ? f[0] : 1.0f);
 #pragma unroll
-            for (int x = 0; x < 32; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * g);
+            for (int x = 0; x < 32; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * g0);
           }
           if (turns && n_it > 1) {
             uint32_t o2[32];
             tc::tmem_ld32(o1 + 32 * c, o2);
             tc::tmem_wait_ld();
-            const float g = inv * f[1];
 #pragma unroll
-            for (int x = 0; x < 32; ++x) o[x] = __float_as_uint(fmaf(__uint_as_float(o2[x]), g, __uint_as_float(o[x])));
+            for (int x = 0; x < 32; ++x) o[x] = __float_as_uint(fmaf(__uint_as_float(o2[x]), g1, __uint_as_float(o[x])));
           }
           if (l == 0.0f) {
 #pragma unroll
             for (int x = 0; x < 32; ++x) o[x] = 0u;
           }
-          if (!live) continue;
-          if (whole) {
-            uint4* dst = reinterpret_cast<uint4*>(a.out + (int64_t)i * a.out_stride + h * D + 32 * c);
+          __syncwarp();
+          if (whole) {  // 64 bytes of a row
 #pragma unroll
             for (int x = 0; x < 4; ++x) {
               uint32_t u[4];
 #pragma unroll
               for (int y = 0; y < 4; ++y)
                 u[y] = bf16x2(__uint_as_float(o[8 * x + 2 * y]), __uint_as_float(o[8 * x + 2 * y + 1]));
-              dst[x] = make_uint4(u[0], u[1], u[2], u[3]);
+              *reinterpret_cast<uint4*>(pad + lane * 64 + ((x ^ ((lane >> 1) & 3)) * 16)) = make_uint4(u[0], u[1], u[2], u[3]);
             }
-          } else {
-            uint4* dst = reinterpret_cast<uint4*>(a.part_o + pa * D + 32 * c);
+            __syncwarp();
 #pragma unroll
-            for (int x = 0; x < 8; ++x) dst[x] = make_uint4(o[4 * x], o[4 * x + 1], o[4 * x + 2], o[4 * x + 3]);
+            for (int x = 0; x < 4; ++x) {
+              const int row = 8 * x + lane / 4, unit = lane & 3;
+              const uint4 v = *reinterpret_cast<const uint4*>(pad + row * 64 + ((unit ^ ((row >> 1) & 3)) * 16));
+              if (to[x]) *reinterpret_cast<uint4*>(to[x] + 64 * c + 16 * unit) = v;
+            }
+          } else {  // 128 bytes, in halves
+#pragma unroll
+            for (int hf = 0; hf < 2; ++hf) {
+              if (hf) __syncwarp();
+#pragma unroll
+              for (int x = 0; x < 4; ++x)
+                *reinterpret_cast<uint4*>(pad + lane * 64 + ((x ^ ((lane >> 1) & 3)) * 16)) =
+                    make_uint4(o[16 * hf + 4 * x], o[16 * hf + 4 * x + 1], o[16 * hf + 4 * x + 2], o[16 * hf + 4 * x + 3]);
+              __syncwarp();
+#pragma unroll
+              for (int x = 0; x < 4; ++x) {
+                const int row = 8 * x + lane / 4, unit = lane & 3;
+                const uint4 v = *reinterpret_cast<const uint4*>(pad + row * 64 + ((unit ^ ((row >> 1) & 3)) * 16));
+                if (to[x]) *reinterpret_cast<uint4*>(to[x] + 128 * c + 64 * hf + 16 * unit) = v;
+              }
+            }
           }
         }
       }

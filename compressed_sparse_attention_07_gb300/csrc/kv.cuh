@@ -85,6 +85,7 @@ __host__ __device__ constexpr int kv_scale_bytes(int dim) { return kPage * dim /
 // Arguments of an attention call.
 struct KvAtt {
   int T, n_heads, kv_heads, group, window, causal, max_q;
+  uint32_t group_mul, group_shift;  // n / group = n * group_mul >> group_shift for 0 <= n < 2^31
   int max_kv;
   const uint16_t* q;
   int64_t q_stride;
@@ -104,6 +105,12 @@ struct KvAtt {
   float* part_l;
   int32_t* status;
 };
+
+// n / group for 0 <= n < 2^31: with s = ceil(log2 group) and m = floor(2^(31 + s) /
+// group) + 1 the error of n m / 2^(31 + s) is below n / 2^(31 + s) < 1 / group.
+__device__ __forceinline__ int group_of(const KvAtt& a, int n) {
+  return (int)(((uint64_t)(uint32_t)n * a.group_mul) >> a.group_shift);
+}
 
 // Rows and keys of sequence b; false (status set) when they are out of bounds.
 __device__ __forceinline__ bool kv_sequence(const KvAtt& a, int b, int& row0, int& rows, int& keys) {

@@ -103,11 +103,11 @@ __global__ void __launch_bounds__(Rows<D, kFp4, NT, kCluster>::kWarps * 32, Rows
   if (tile0 >= n_rows) return;
   const int last = min(tile0 + kRows, n_rows) - 1;
   int p0, p1;
-  kv_pages(a, tile0 / a.group, last / a.group, rows, keys, p0, p1);
+  kv_pages(a, group_of(a, tile0), group_of(a, last), rows, keys, p0, p1);
   const int n_act = (p1 - p0 + a.part_pages - 1) / a.part_pages;
   if (!kCluster && part > 0 && part >= n_act) return;
   const int pb = min(p0 + part * a.part_pages, p1), pe = min(pb + a.part_pages, p1);
-  const int key_end = kv_hi(a, last / a.group, rows, keys);  // no row sees keys from here on
+  const int key_end = kv_hi(a, group_of(a, last), rows, keys);  // no row sees keys from here on
   const int tb = pb * R::kPerPage, te = min(pe * R::kPerPage, (key_end + R::kTile - 1) / R::kTile);
 
   uint8_t* ring = smem + warp * R::kWarpBytes;
@@ -154,7 +154,7 @@ __global__ void __launch_bounds__(Rows<D, kFp4, NT, kCluster>::kWarps * 32, Rows
   for (int n = warp; n < NT; n += kWarps) {
     const int r = tile0 + 8 * n + g;
     const bool live = r < n_rows;
-    const int i = live ? r / a.group : 0, h = live ? kh * a.group + r % a.group : 0;
+    const int i = live ? group_of(a, r) : 0, h = live ? kh * a.group + r - group_of(a, r) * a.group : 0;
     const uint16_t* q = a.q + (int64_t)(row0 + i) * a.q_stride + h * D;
     if constexpr (kFp4) {
       uint4 w[D / 32];  // channels D/4 * t .. of row g
@@ -207,7 +207,7 @@ __global__ void __launch_bounds__(Rows<D, kFp4, NT, kCluster>::kWarps * 32, Rows
   }
   __syncthreads();
   // keys that every row sees: no masks inside
-  const int all_lo = kv_lo(a, last / a.group, rows, keys), all_hi = kv_hi(a, tile0 / a.group, rows, keys);
+  const int all_lo = kv_lo(a, group_of(a, last), rows, keys), all_hi = kv_hi(a, group_of(a, tile0), rows, keys);
 
   float sc[NT][2], m[NT][2], l[NT][2], o[MT][NT][4];
 #pragma unroll
@@ -489,7 +489,7 @@ __global__ void __launch_bounds__(Rows<D, kFp4, NT, kCluster>::kWarps * 32, Rows
       }
     }
     const float inv = sum > 0.0f ? 1.0f / sum : (sum == 0.0f ? 0.0f : NAN);
-    const int i = row0 + (tile0 + r) / a.group, h = kh * a.group + (tile0 + r) % a.group;
+    const int i = row0 + group_of(a, tile0 + r), h = kh * a.group + (tile0 + r - group_of(a, tile0 + r) * a.group);
     const int64_t at = (int64_t)i * a.n_heads + h;
     const float lse2 = sum == 0.0f ? -INFINITY : top + log2f(sum);
     if (whole) {
@@ -537,7 +537,7 @@ __global__ void __launch_bounds__(Rows<D, kFp4, NT, kCluster>::kWarps * 32, Rows
           }
         }
         const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-        const int i = row0 + (tile0 + r) / a.group, h = kh * a.group + (tile0 + r) % a.group;
+        const int i = row0 + group_of(a, tile0 + r), h = kh * a.group + (tile0 + r - group_of(a, tile0 + r) * a.group);
         *reinterpret_cast<uint2*>(a.out + (int64_t)i * a.out_stride + h * D + c) =
             make_uint2(bf16x2(o0 * inv, o1 * inv), bf16x2(o2 * inv, o3 * inv));
         if (a.lse && c == 0) a.lse[(int64_t)i * a.n_heads + h] = sum == 0.0f ? -INFINITY : (top + log2f(sum)) * kLn2;
@@ -562,7 +562,7 @@ __global__ void __launch_bounds__(256) kv_join_kernel(KvAtt a, int tile_rows) {
   const int tile0 = (i * a.group + h % a.group) / tile_rows * tile_rows;
   const int last = min(tile0 + tile_rows, rows * a.group) - 1;
   int p0, p1;
-  kv_pages(a, tile0 / a.group, last / a.group, rows, keys, p0, p1);
+  kv_pages(a, group_of(a, tile0), group_of(a, last), rows, keys, p0, p1);
   const int n = (p1 - p0 + a.part_pages - 1) / a.part_pages;
   if (n <= 1) return;
   const int64_t at = (int64_t)(row0 + i) * a.n_heads + h, step = (int64_t)a.T * a.n_heads;

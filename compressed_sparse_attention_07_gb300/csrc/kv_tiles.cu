@@ -99,7 +99,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tiles_kernel(KvAtt a) {
   if (tile0 >= n_rows) return;
   const int last = min(tile0 + kCtaRows, n_rows) - 1;
   int p0, p1;
-  kv_pages(a, tile0 / a.group, last / a.group, rows, keys, p0, p1);
+  kv_pages(a, group_of(a, tile0), group_of(a, last), rows, keys, p0, p1);
   const int n_act = (p1 - p0 + a.part_pages - 1) / a.part_pages;
   if (part > 0 && part >= n_act) return;
   const int pb = p0 + part * a.part_pages, pe = min(pb + a.part_pages, p1);
@@ -158,7 +158,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tiles_kernel(KvAtt a) {
     float scale;
     int hi = 0, lo = 0;
     const int r = tile0 + (turns ? tid % kTileRows : tid);
-    if (r < n_rows) hi = kv_hi(a, r / a.group, rows, keys), lo = kv_lo(a, r / a.group, rows, keys);
+    if (r < n_rows) hi = kv_hi(a, group_of(a, r), rows, keys), lo = kv_lo(a, group_of(a, r), rows, keys);
     {
       // A lane loads parts of four rows, 8 x + its number & 7 of the warp's: 64
       // neighbouring bytes of eight rows at a time (a lane with a row to itself, 16
@@ -173,7 +173,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tiles_kernel(KvAtt a) {
         const int rr = r - lane + 8 * x + sub;
         const bool live = rr < n_rows;
         const uint16_t* q = a.q;
-        if (live) q += (int64_t)(row0 + rr / a.group) * a.q_stride + (kh * a.group + rr % a.group) * D;
+        if (live) q += (int64_t)(row0 + group_of(a, rr)) * a.q_stride + (kh * a.group + rr - group_of(a, rr) * a.group) * D;
 #pragma unroll
         for (int c = 0; c < D / 32; ++c) {
           w[x][c] = make_uint4(0, 0, 0, 0);
@@ -335,7 +335,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tiles_kernel(KvAtt a) {
       if (ok) {
         tc::fence_after_sync();
         const bool live = r < n_rows;
-        const int i = row0 + (live ? r / a.group : 0), h = kh * a.group + (live ? r % a.group : 0);
+        const int i = row0 + (live ? group_of(a, r) : 0), h = kh * a.group + (live ? r - group_of(a, r) * a.group : 0);
         const int64_t at = (int64_t)i * a.n_heads + h, pa = (int64_t)part * a.T * a.n_heads + at;
         const bool whole = n_act <= 1;
         const float inv = l == 0.0f ? 0.0f : 1.0f / l;

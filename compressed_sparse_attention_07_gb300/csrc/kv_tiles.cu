@@ -487,28 +487,36 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tiles_kernel(KvAtt a) {
         }
         // Scores of keys that are not seen are never used, but values are
         // multiplied by weight 0: what lies in slots from kv_len on (anything) and
-        // in the place of pages that are not there has to be 0.
+        // in the place of a page outside the pool has to be 0.
         const int live = keys - key0 - it * kTileKeys;
         const bool tail = v && live < kTileKeys && (live < kPage ? at[0] : at[1]) >= 0;
-        const uint32_t bytes = ((at[0] >= 0) + (at[1] >= 0)) * (L::kOperand / 2);
         uint64_t* bar = tail ? &tail_full : &full[s];
-        if (lane == 0) tc::mbar_arrive_expect_tx(bar, bytes);
+        if (lane == 0) tc::mbar_arrive_expect_tx(bar, ((at[0] >= 0) + (at[1] >= 0)) * (L::kOperand / 2));
         __syncwarp();
-        for (int x = lane; x < 2 * (D / 8); x += 32)
-          if ((x & 1 ? at[1] : at[0]) >= 0)
-            tc::bulk_g2s(dst + (x / 2) * kChunk + (x & 1) * (kPage * 16),
-                         src + (x & 1 ? at[1] : at[0]) + (x / 2) * (kPage * 16), kPage * 16, bar);
-        if (tail) {  // the last tile
-          ok = __all_sync(0xffffffffu, tc::mbar_wait(&tail_full, 0));
-          if (!ok) break;
-        }
-        if (v && (tail || bytes != L::kOperand)) {
-          for (int x = lane; x < kTileKeys * (D / 8); x += 32) {
-            const int key = x % kTileKeys;
-            if (key >= live || (key < kPage ? at[0] : at[1]) < 0)
-              *reinterpret_cast<uint4*>(dst + (x / kTileKeys) * kChunk + key * 16) = make_uint4(0, 0, 0, 0);
+        if (tc::elect_one()) {
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            if (at[x] < 0) continue;
+#pragma unroll
+            for (int c = 0; c < D / 8; ++c)
+              tc::bulk_g2s(dst + c * kChunk + x * (kPage * 16), src + at[x] + c * (kPage * 16), kPage * 16, bar);
           }
-          tc::fence_async_smem();
+        }
+        __syncwarp();
+        if (v) {
+          auto clear = [&](int from, int to) {  // values of these keys
+            for (int key = from + lane; key < to; key += 32)
+#pragma unroll
+              for (int c = 0; c < D / 8; ++c) *reinterpret_cast<uint4*>(dst + c * kChunk + key * 16) = make_uint4(0, 0, 0, 0);
+            tc::fence_async_smem();
+          };
+          if (tail) {  // the last tile
+            ok = __all_sync(0xffffffffu, tc::mbar_wait(&tail_full, 0));
+            if (!ok) break;
+            clear(live, live < kPage ? kPage : kTileKeys);
+          }
+          if (at[0] < 0) clear(0, kPage);
+          if (at[1] < 0 && pb + 2 * it + 1 < pe) clear(kPage, kTileKeys);
         }
         if (lane != 0 || tail) tc::mbar_arrive(&full[s]);
       }
@@ -542,18 +550,22 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tiles_kernel(KvAtt a) {
         __syncwarp();
       };
       // O_j += P_j V with the values of stage s, the u-th tile of place j
-      auto outputs = [&](auto j, auto s, int u, uint64_t* done) {
+      // (half: the tile has one page)
+      auto outputs = [&](auto j, auto s, int u, uint64_t* done, bool half) {
         tc::fence_after_sync();
         if (tc::elect_one()) {
           tc::mma_ts_lo(tb + 256 + D * j(), tb + 128 * j(), v_lo + s() * kTile16, kHiV, kIdO, u > 0);
 #pragma unroll
-          for (int ks = 1; ks < kTileKeys / 16; ++ks)
+          for (int ks = 1; ks < kTileKeys / 16; ++ks) {
+            if (ks >= kPage / 16 && half) break;
             tc::mma_ts_lo(tb + 256 + D * j(), tb + 128 * j() + 8 * ks, v_lo + s() * kTile16 + ks * (256 / 16), kHiV, kIdO,
                           1u);
+          }
           if (done) tc::mma_commit(done);
         }
         __syncwarp();
       };
+      const bool odd = (pe - pb) & 1;  // the last tile has one page
       ok = wait(&q_full, 0);
       if (turns) {
         // tile `it`, of stage and place s, and the outputs of the place's last one
@@ -561,13 +573,13 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tiles_kernel(KvAtt a) {
           ok = wait(&k_full[s()], (it / kStages) & 1);
           if (it >= 2) {
             ok = ok && wait(&v_full[s()], (it / kStages - 1) & 1) && wait(&p_ready[s()], (it / 2 - 1) & 1);
-            if (ok) outputs(s, s, it / 2 - 1, &v_free[s()]);
+            if (ok) outputs(s, s, it / 2 - 1, &v_free[s()], false);
           }
           if (ok) scores(Num<0>{}, s, s, true);
         };
         auto end = [&](auto s, int it) {
           ok = wait(&v_full[s()], (it / kStages) & 1) && wait(&p_ready[s()], (it / 2) & 1);
-          if (ok) outputs(s, s, it / 2, &o_full[s()]);
+          if (ok) outputs(s, s, it / 2, &o_full[s()], odd && it == n_it - 1);
         };
         for (int it = 0; it < n_it && ok; it += 2) {
           step(Num<0>{}, it);
@@ -583,20 +595,20 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tiles_kernel(KvAtt a) {
           ok = wait(&k_full[s()], (it / kStages) & 1);
           if (it > 0) {
             ok = ok && wait(&v_full[p()], ((it - 1) / kStages) & 1) && wait(&p_ready[0], (it - 1) & 1);
-            if (ok) outputs(Num<0>{}, p, it - 1, nullptr);
+            if (ok) outputs(Num<0>{}, p, it - 1, nullptr, false);
           }
           if (ok) scores(Num<0>{}, Num<0>{}, s, false);
           if (it > 0) {
             ok = ok && wait(&p_ready[1], (it - 1) & 1);
-            if (ok) outputs(Num<1>{}, p, it - 1, &v_free[p()]);
+            if (ok) outputs(Num<1>{}, p, it - 1, &v_free[p()], false);
           }
           if (ok) scores(Num<1>{}, Num<1>{}, s, true);
         };
         auto end = [&](auto s) {
           ok = wait(&v_full[s()], ((n_it - 1) / kStages) & 1) && wait(&p_ready[0], (n_it - 1) & 1);
-          if (ok) outputs(Num<0>{}, s, n_it - 1, &o_full[0]);
+          if (ok) outputs(Num<0>{}, s, n_it - 1, &o_full[0], odd);
           ok = ok && wait(&p_ready[1], (n_it - 1) & 1);
-          if (ok) outputs(Num<1>{}, s, n_it - 1, &o_full[1]);
+          if (ok) outputs(Num<1>{}, s, n_it - 1, &o_full[1], odd);
         };
         for (int it = 0; it < n_it && ok; it += 2) {
           step(Num<0>{}, Num<1>{}, it);

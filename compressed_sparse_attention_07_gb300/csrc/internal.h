@@ -17,7 +17,9 @@ namespace csa2 {
 // memory and before any global load whose value a kernel of the library may
 // write -- before the wait a kernel issues L2 prefetch hints and reads only
 // the attention's query and window rows, which only csa2_swa_encode writes,
-// and that kernel lets its successor start only at its completion.
+// and that kernel lets its successor start only at its completion (a caller
+// that hands on kv_append's or kv_attend's outputs as such keeps the header's
+// rule: another call between the two).
 // cluster_x > 0 adds a cluster shape.
 template <typename... KArgs, typename... Args>
 cudaError_t launch_k(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t stream, int cluster_x,

@@ -65,7 +65,8 @@ int32_t attend(const csa2_kv_cfg* cfg, bool cross, int32_t B, int32_t T, const u
   int s = 0;
   while ((1 << s) < a.group) ++s;
   a.group_mul = (uint32_t)((1ull << (31 + s)) / a.group + 1), a.group_shift = 31 + s;
-  a.window = cfg->window, a.causal = cross ? 0 : 1, a.max_q = (int)most, a.max_kv = max_kv;
+  a.window = cfg->window >= max_kv ? 0 : cfg->window;  // as wide as the keys: none
+  a.causal = cross ? 0 : 1, a.max_q = (int)most, a.max_kv = max_kv;
   a.q = q, a.q_stride = q_stride, a.cu = cu, a.c = view_of(*cache), a.kv_len = kv_len, a.scale = scale;
   a.out = out, a.out_stride = out_stride, a.lse = lse, a.status = status;
   const int64_t rows = (int64_t)T * cfg->n_heads;

@@ -238,8 +238,10 @@ CSA2_API int32_t csa2_index_select(const csa2_cfg* cfg, int32_t B, int32_t Tq, c
  * Read before the wait on the previous kernel (so that the loads overlap a
  * preceding selection): q, swa, swa_len, swa_pos0 and q_pos.  They must not
  * be written by the kernel enqueued immediately before this call on the
- * stream; of this library's calls only csa2_swa_encode writes any of them,
- * so enqueue another call (the indexer of a decode step) between the two.
+ * stream; of this library's calls only csa2_swa_encode writes any of them
+ * (and csa2_kv_append or the csa2_kv_* attention, where a caller hands on
+ * their outputs as such), so enqueue another call (the indexer of a decode
+ * step) between the two.
  * topk, n_entries and the main cache are read after that kernel has
  * completed. */
 CSA2_API int32_t csa2_attend(const csa2_cfg* cfg, int32_t B, int32_t Tq, const uint16_t* q,
@@ -434,9 +436,11 @@ CSA2_API int32_t csa2_kv_append(const csa2_kv_cfg* cfg, int32_t B, int32_t T, co
                                 uint16_t* v_out, int32_t* status, void* stream);
 
 /* Workspace bytes with which csa2_kv_attend and csa2_kv_cross_attend divide
- * the keys of these sizes as they would best; they take any workspace (NULL
- * included) and divide less where it is smaller.  Two calls that may overlap
- * (other streams, graphs replayed at once) need workspaces of their own. */
+ * the keys of these sizes among CTAs as they would best (0 where that needs
+ * none); they take any workspace (NULL included) and divide less where it is
+ * smaller.  Its contents need not be kept between calls.  Two calls that may
+ * overlap (other streams, graphs replayed at once) need workspaces of their
+ * own. */
 CSA2_API size_t csa2_kv_workspace_bytes(const csa2_kv_cfg* cfg, int32_t B, int32_t T, int32_t max_q, int32_t max_kv);
 
 /* Attention over the cache: head h reads kv head h / (n_heads / kv_heads),
@@ -448,7 +452,10 @@ CSA2_API size_t csa2_kv_workspace_bytes(const csa2_kv_cfg* cfg, int32_t B, int32
  *  csa2_kv_cross_attend: every row sees all kv_len[b] keys (window must be 0).
  * A row that sees nothing (kv_len 0, or more rows than keys) is 0 with lse
  * -inf.  max_q and max_kv bound the rows and keys of a sequence (they size the
- * grid).  A page whose id is outside the pool counts as not seen.  Cache slots
+ * grid).  q and out must not overlap.  Queries, logits' factors and weights: over
+ * FP4 caches the products multiply f16 (queries relative to a power of two of
+ * their row, exact but for channels below 2^-14 of its largest; weights
+ * rounded to f16), over bf16 caches bf16; all sums are fp32.  A page whose id is outside the pool counts as not seen.  Cache slots
  * from kv_len on may hold anything.  A query row that is not finite yields NaN
  * or unspecified values in its own outputs alone. */
 CSA2_API int32_t csa2_kv_attend(const csa2_kv_cfg* cfg, int32_t B, int32_t T, const uint16_t* q, int64_t q_stride,

@@ -240,10 +240,11 @@ def test_ragged_rows(dtype, dim, hq, hkv, cross):
 
 @pytest.mark.parametrize("dtype", [FP4, BF16])
 @pytest.mark.parametrize("dim,hq,hkv", [(128, 8, 8), (64, 8, 2), (128, 12, 1)])
-@pytest.mark.parametrize("window", [1, 17, 64, 100])
+@pytest.mark.parametrize("window", [1, 17, 64, 100, 2 ** 31 - 1])
 def test_windows(dtype, dim, hq, hkv, window):
     cfg = csa.KVCfg(hq, hkv, dim, dtype, window=window)
-    _attend_case(cfg, [1, 3, 70, 150], [300, 65, 70, 400], seed=window)
+    _attend_case(cfg, [1, 3, 70, 150], [300, 65, 70, 400], seed=window % 1000)
+    _attend_case(cfg, [1, 2], [300, 65], seed=window % 1000 + 1)
 
 
 @pytest.mark.parametrize("dtype", [FP4, BF16])
@@ -252,6 +253,22 @@ def test_windows(dtype, dim, hq, hkv, window):
 @pytest.mark.parametrize("workspace", [False, True])
 def test_long_keys_divided_or_not(dtype, dim, hq, hkv, nq, workspace):
     _attend_case(csa.KVCfg(hq, hkv, dim, dtype), [nq, nq], [6007, 1500], seed=nq, workspace=workspace)
+
+
+@pytest.mark.parametrize("dtype", [FP4, BF16])
+def test_pages_of_all_last_lengths(dtype):
+    # the last page of a tile alone, full, and ending at every kind of place, for one row, few and many
+    kv = [1, 63, 64, 65, 127, 128, 129, 191, 192, 193, 256]
+    for nq in (1, 9, 150):
+        _attend_case(csa.KVCfg(2, 1, 64, dtype), [nq] * len(kv), kv, cross=True, seed=nq)
+        _attend_case(csa.KVCfg(2, 1, 128, dtype), [nq] * len(kv), kv, seed=nq)
+
+
+@pytest.mark.parametrize("dtype", [FP4, BF16])
+def test_many_small_sequences_and_one_long(dtype):
+    kv = [3] * 40 + [9000] + [700] * 5
+    _attend_case(csa.KVCfg(8, 4, 64, dtype), [1] * 46, kv, seed=3)
+    _attend_case(csa.KVCfg(4, 4, 128, dtype), [2] * 46, kv, cross=True, seed=4)
 
 
 @pytest.mark.parametrize("dtype", [FP4, BF16])

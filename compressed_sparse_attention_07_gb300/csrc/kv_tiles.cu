@@ -8,7 +8,9 @@
 //   O_j += P_j V   (A from TMEM, N = head_dim)    TMEM columns 256 + D j
 // with the softmax of tile 0 beside the products of tile 1 and the other way
 // round.  A CTA with no more than 128 rows (drafts, short texts) gives both
-// places to the same rows and key tiles in turn, and joins the two at the end.
+// places to the same rows and key tiles in turn, and joins the two at the end; with
+// no more than 64 rows these stand in the tile twice, each half of the lanes for
+// one page of a key tile, which halves the softmax's way.
 //
 // Warps 0-3 and 4-7 hold the rows (thread = row = TMEM lane, with registers for
 // its 128 scores); warps 8-11 bring keys, 12-15 values into shared memory as
@@ -108,6 +110,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tiles_kernel(KvAtt a) {
   // turns: no second tile of rows, so that place 0 takes the even key tiles of
   // the one there is and place 1 the odd ones
   const bool turns = tile0 + kTileRows >= n_rows;
+  // split: no more than 64 rows, which stand in the tile twice: lanes 0-63 take the
+  // first page of each key tile, 64-127 the second, half the softmax for each
+  const bool split = tile0 + kTileRows / 2 >= n_rows;
   const int32_t* table = a.c.table + (int64_t)b * a.c.max_pages;
 
   if (tid == 0) {
@@ -123,7 +128,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tiles_kernel(KvAtt a) {
       tc::mbar_init(&v_free[s], 1);
     }
     for (int j = 0; j < 2; ++j) {
-      const int live = n_rows - tile0 - (turns ? 0 : kTileRows * j);  // rows of place j
+      const int rows_of = n_rows - tile0 - (turns ? 0 : kTileRows * j);  // rows of place j
+      const int live = split && rows_of > 32 ? kTileRows : split ? 64 : rows_of;
       tc::mbar_init(&s_ready[j], 1);
       tc::mbar_init(&p_ready[j], max(1, min(4, (live + 31) / 32)));  // warps with rows
       tc::mbar_init(&o_full[j], 1);
@@ -157,7 +163,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tiles_kernel(KvAtt a) {
     // the query rows, f16 (bf16 caches: bf16)
     float scale;
     int hi = 0, lo = 0;
-    const int r = tile0 + (turns ? tid % kTileRows : tid);
+    const int r = tile0 + (split ? tid % (kTileRows / 2) : turns ? tid % kTileRows : tid);
     if (r < n_rows) hi = kv_hi(a, group_of(a, r), rows, keys), lo = kv_lo(a, group_of(a, r), rows, keys);
     {
       // A lane loads parts of four rows, 8 x + its number & 7 of the warp's: 64
@@ -223,8 +229,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tiles_kernel(KvAtt a) {
     const uint32_t s_addr = tc::taddr(tb, lane_base, 128 * j), o_addr = tc::taddr(tb, lane_base, 256 + D * j);
     const bool warp_live = r - lane < n_rows;
     float m = -INFINITY, l = 0.0f;
-    if (warp_live) {
-      int u = 0;  // key tiles of this place so far
+    // this place's key tiles: 32 kChunks keys of each from 32 first on
+    auto soft = [&](auto chunks, int first) {
+      constexpr int kChunks = chunks();
+      int u = 0;  // key tiles so far
       for (int it = turns ? j : 0; it < n_it; it += turns ? 2 : 1, ++u) {
         const int k0 = key0 + it * kTileKeys;
         int v_lo = lo - k0, v_hi = hi - k0;  // the row's keys in this tile
@@ -241,19 +249,20 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tiles_kernel(KvAtt a) {
             }
           }
         }
-        const bool masked = __any_sync(0xffffffffu, v_lo > 0 || v_hi < kTileKeys);
+        v_lo -= 32 * first, v_hi -= 32 * first;
+        const bool masked = __any_sync(0xffffffffu, v_lo > 0 || v_hi < 32 * kChunks);
         if (!__all_sync(0xffffffffu, tc::mbar_wait(&s_ready[j], u & 1))) {
           ok = false;
-          break;
+          return;
         }
         tc::fence_after_sync();
-        uint32_t s[4][32];
+        uint32_t s[kChunks][32];
 #pragma unroll
-        for (int c = 0; c < 4; ++c) tc::tmem_ld32(s_addr + 32 * c, s[c]);
+        for (int c = 0; c < kChunks; ++c) tc::tmem_ld32(s_addr + 32 * (first + c), s[c]);
         tc::tmem_wait_ld();
         if (masked) {
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
+          for (int c = 0; c < kChunks; ++c) {
             const int from = min(max(v_lo - 32 * c, 0), 32), to = min(max(v_hi - 32 * c, 0), 32);
             const uint32_t bits = (uint32_t)((1ull << to) - 1) & (uint32_t)(0xFFFFFFFFull << from);
 #pragma unroll
@@ -261,12 +270,13 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tiles_kernel(KvAtt a) {
               if (!(bits & (1u << x))) s[c][x] = 0xFF800000u;  // -inf
           }
         }
+        constexpr int kRun = 8 * kChunks;  // four maxima at once
         float t4[4];
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
-          t4[c] = __uint_as_float(s[c][0]);
+          t4[c] = __uint_as_float(s[c * kRun / 32][c * kRun % 32]);
 #pragma unroll
-          for (int x = 1; x < 32; ++x) t4[c] = fmaxf(t4[c], __uint_as_float(s[c][x]));
+          for (int x = 1; x < kRun; ++x) t4[c] = fmaxf(t4[c], __uint_as_float(s[(c * kRun + x) / 32][(c * kRun + x) % 32]));
         }
         float top = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3]));
         if (top > -INFINITY) top *= scale;
@@ -292,7 +302,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tiles_kernel(KvAtt a) {
         const uint64_t z2 = pack2(z, z);
         uint64_t sum[2] = {pack2(l, 0.0f), 0ull};
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
+        for (int c = 0; c < kChunks; ++c) {
           uint32_t p[16];
 #pragma unroll
           for (int x = 0; x < 16; ++x) {
@@ -302,7 +312,12 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tiles_kernel(KvAtt a) {
             sum[x & 1] = add2(sum[x & 1], pack2(y0, y1));
             p[x] = kFp4 ? f16x2(y0, y1) : bf16x2(y0, y1);
           }
-          tc::tmem_st16(s_addr + 16 * c, p);
+          tc::tmem_st16(s_addr + 16 * (first + c), p);
+        }
+        if constexpr (kChunks == 2) {  // the other lanes' keys
+          const uint32_t none[16] = {};
+          tc::tmem_st16(s_addr + 16 * (2 - first), none);
+          tc::tmem_st16(s_addr + 16 * (3 - first), none);
         }
         {
           float y0, y1;
@@ -313,104 +328,127 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tiles_kernel(KvAtt a) {
         tc::fence_before_sync();
         warp_arrive(&p_ready[j]);
       }
+    };
+    const int half = (warp >> 1) & 1;
+    if (warp_live) {
+      if (split) soft(Num<2>{}, 2 * half);
+      else soft(Num<4>{}, 0);
     }
     // ---- the rows' outputs: place 0's, place 1's, or (turns) both for one row
     float f[2] = {0.0f, 0.0f};  // factors of the places' outputs
     f[j] = 1.0f;
     if (turns) {
-      half_m[j][tid % kTileRows] = m, half_l[j][tid % kTileRows] = l;
+      const int at = tid % kTileRows;
+      half_m[j][at] = m, half_l[j][at] = l;
       asm volatile("bar.sync 1, 256;" ::: "memory");
-      const float m0 = half_m[0][tid % kTileRows], m1 = half_m[1][tid % kTileRows];
+      const float m0 = half_m[0][at], m1 = half_m[1][at], n0 = half_m[0][at ^ 64], n1 = half_m[1][at ^ 64];
       m = fmaxf(m0, m1);
+      if (split) m = fmaxf(m, fmaxf(n0, n1));
       f[0] = m0 == -INFINITY ? 0.0f : ex2(m0 - m);
       f[1] = m1 == -INFINITY ? 0.0f : ex2(m1 - m);
-      l = f[0] * half_l[0][tid % kTileRows] + f[1] * half_l[1][tid % kTileRows];
+      l = f[0] * half_l[0][at] + f[1] * half_l[1][at];
+      if (split)
+        l += (n0 == -INFINITY ? 0.0f : ex2(n0 - m)) * half_l[0][at ^ 64] + (n1 == -INFINITY ? 0.0f : ex2(n1 - m)) * half_l[1][at ^ 64];
     }
+    bool write = false;  // the products are over and this warp has rows
     if (warp_live && ok) {
       if (n_it > 0) {
         if (!turns) ok = tc::mbar_wait(&o_full[j], 0);
         else ok = tc::mbar_wait(&o_full[0], 0) && (n_it < 2 || tc::mbar_wait(&o_full[1], 0));
       }
       ok = __all_sync(0xffffffffu, ok);
-      if (ok) {
-        tc::fence_after_sync();
-        const bool live = r < n_rows;
-        const int i = row0 + (live ? group_of(a, r) : 0), h = kh * a.group + (live ? r - group_of(a, r) * a.group : 0);
-        const int64_t at = (int64_t)i * a.n_heads + h, pa = (int64_t)part * a.T * a.n_heads + at;
-        const bool whole = n_act <= 1;
-        const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-        const float lse2 = l == 0.0f ? -INFINITY : m + log2f(l);
-        if (live && (!turns || j == 0)) {
-          if (!whole) a.part_l[pa] = lse2;
-          else if (a.lse) a.lse[at] = lse2 * kLn2;
-        }
-        // where this lane's row goes, or 0
-        const uint64_t home = !live ? 0 : whole ? reinterpret_cast<uint64_t>(a.out + (int64_t)i * a.out_stride + h * D)
-                                                : reinterpret_cast<uint64_t>(a.part_o + pa * D);
-        const uint32_t o0 = tc::taddr(tb, lane_base, 256), o1 = tc::taddr(tb, lane_base, 256 + D);
-        // The rows pass through shared memory (the place's queries are done with),
-        // so that neighbouring lanes write neighbouring 16 bytes of a row: its unit x
-        // of 64 bytes stands at x ^ (row / 2 & 3).
-        uint8_t* pad = smem + L::kQ + j * L::kOperand + (warp & 3) * 2048;
-        const float g0 = inv * (turns ? f[0] : 1.0f), g1 = inv * f[1];
-        uint64_t to[4];  // four lanes a row, eight rows at a time
+      write = ok;
+      tc::fence_after_sync();
+    }
+    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+    const float g0 = inv * (turns ? f[0] : 1.0f), g1 = inv * f[1];
+    const uint32_t o0 = tc::taddr(tb, lane_base, 256), o1 = tc::taddr(tb, lane_base, 256 + D);
+    auto take = [&](int c, uint32_t (&o)[32]) {  // this lane's share of 32 channels of the output
+      if (n_it > 0) {
+        tc::tmem_ld32((j == 1 && !turns ? o1 : o0) + 32 * c, o);
+        tc::tmem_wait_ld();
 #pragma unroll
-        for (int x = 0; x < 4; ++x) to[x] = __shfl_sync(0xffffffffu, home, 8 * x + lane / 4);
+        for (int x = 0; x < 32; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * g0);
+      }
+      if (turns && n_it > 1) {
+        uint32_t o2[32];
+        tc::tmem_ld32(o1 + 32 * c, o2);
+        tc::tmem_wait_ld();
 #pragma unroll
-        for (int c = 0; c < D / 32; ++c) {
-          if (turns && c / (D / 64) != j) continue;  // (turns) each place writes one half of the channels
+        for (int x = 0; x < 32; ++x) o[x] = __float_as_uint(fmaf(__uint_as_float(o2[x]), g1, __uint_as_float(o[x])));
+      }
+      if (l == 0.0f) {
+#pragma unroll
+        for (int x = 0; x < 32; ++x) o[x] = 0u;
+      }
+    };
+    // (turns) each place writes one half of the channels; (split) lanes 64-127 hand
+    // theirs over first, in the place of the keys, which are done with
+    float* other = reinterpret_cast<float*>(smem + L::kK) + tid % (kTileRows / 2);
+    if (split) {
+      if (write && half) {
+#pragma unroll 1
+        for (int c = j * (D / 64); c < (j + 1) * (D / 64); ++c) {
           uint32_t o[32];
-          if (n_it > 0) {
-            tc::tmem_ld32((j == 1 && !turns ? o1 : o0) + 32 * c, o);
-            tc::tmem_wait_ld();
+          take(c, o);
 #pragma unroll
-            for (int x = 0; x < 32; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * g0);
-          }
-          if (turns && n_it > 1) {
-            uint32_t o2[32];
-            tc::tmem_ld32(o1 + 32 * c, o2);
-            tc::tmem_wait_ld();
+          for (int x = 0; x < 32; ++x) other[(32 * c + x) * (kTileRows / 2)] = __uint_as_float(o[x]);
+        }
+      }
+      asm volatile("bar.sync 2, 256;" ::: "memory");
+      if (half) write = false;
+    }
+    if (write) {
+      const bool live = r < n_rows;
+      const int i = row0 + (live ? group_of(a, r) : 0), h = kh * a.group + (live ? r - group_of(a, r) * a.group : 0);
+      const int64_t at = (int64_t)i * a.n_heads + h, pa = (int64_t)part * a.T * a.n_heads + at;
+      const bool whole = n_act <= 1;
+      const float lse2 = l == 0.0f ? -INFINITY : m + log2f(l);
+      if (live && (!turns || j == 0)) {
+        if (!whole) a.part_l[pa] = lse2;
+        else if (a.lse) a.lse[at] = lse2 * kLn2;
+      }
+      // where this lane's row goes, or 0
+      const uint64_t home = !live ? 0 : whole ? reinterpret_cast<uint64_t>(a.out + (int64_t)i * a.out_stride + h * D)
+                                              : reinterpret_cast<uint64_t>(a.part_o + pa * D);
+      // The rows pass through shared memory (the place's queries are done with),
+      // so that neighbouring lanes write neighbouring 16 bytes of a row: its unit x
+      // of 64 bytes stands at x ^ (row / 2 & 3).
+      uint8_t* pad = smem + L::kQ + j * L::kOperand + (warp & 3) * 2048;
+      uint64_t to[4];  // four lanes a row, eight rows at a time
 #pragma unroll
-            for (int x = 0; x < 32; ++x) o[x] = __float_as_uint(fmaf(__uint_as_float(o2[x]), g1, __uint_as_float(o[x])));
-          }
-          if (l == 0.0f) {
+      for (int x = 0; x < 4; ++x) to[x] = __shfl_sync(0xffffffffu, home, 8 * x + lane / 4);
+      auto pass = [&](const uint32_t* w, int offset) {  // 64 bytes of each row, to `offset` in it
+        __syncwarp();
 #pragma unroll
-            for (int x = 0; x < 32; ++x) o[x] = 0u;
-          }
-          __syncwarp();
-          if (whole) {  // 64 bytes of a row
+        for (int x = 0; x < 4; ++x)
+          *reinterpret_cast<uint4*>(pad + lane * 64 + ((x ^ ((lane >> 1) & 3)) * 16)) =
+              make_uint4(w[4 * x], w[4 * x + 1], w[4 * x + 2], w[4 * x + 3]);
+        __syncwarp();
 #pragma unroll
-            for (int x = 0; x < 4; ++x) {
-              uint32_t u[4];
+        for (int x = 0; x < 4; ++x) {
+          const int row = 8 * x + lane / 4, unit = lane & 3;
+          const uint4 v = *reinterpret_cast<const uint4*>(pad + row * 64 + ((unit ^ ((row >> 1) & 3)) * 16));
+          if (to[x]) *reinterpret_cast<uint4*>(to[x] + offset + 16 * unit) = v;
+        }
+      };
+#pragma unroll 1
+      for (int c = turns ? j * (D / 64) : 0; c < (turns ? (j + 1) * (D / 64) : D / 32); ++c) {
+        uint32_t o[32];
+        take(c, o);
+        if (split) {
 #pragma unroll
-              for (int y = 0; y < 4; ++y)
-                u[y] = bf16x2(__uint_as_float(o[8 * x + 2 * y]), __uint_as_float(o[8 * x + 2 * y + 1]));
-              *reinterpret_cast<uint4*>(pad + lane * 64 + ((x ^ ((lane >> 1) & 3)) * 16)) = make_uint4(u[0], u[1], u[2], u[3]);
-            }
-            __syncwarp();
+          for (int x = 0; x < 32; ++x)
+            o[x] = __float_as_uint(__uint_as_float(o[x]) + other[(32 * c + x) * (kTileRows / 2)]);
+        }
+        if (whole) {
+          uint32_t u[16];
 #pragma unroll
-            for (int x = 0; x < 4; ++x) {
-              const int row = 8 * x + lane / 4, unit = lane & 3;
-              const uint4 v = *reinterpret_cast<const uint4*>(pad + row * 64 + ((unit ^ ((row >> 1) & 3)) * 16));
-              if (to[x]) *reinterpret_cast<uint4*>(to[x] + 64 * c + 16 * unit) = v;
-            }
-          } else {  // 128 bytes, in halves
-#pragma unroll
-            for (int hf = 0; hf < 2; ++hf) {
-              if (hf) __syncwarp();
-#pragma unroll
-              for (int x = 0; x < 4; ++x)
-                *reinterpret_cast<uint4*>(pad + lane * 64 + ((x ^ ((lane >> 1) & 3)) * 16)) =
-                    make_uint4(o[16 * hf + 4 * x], o[16 * hf + 4 * x + 1], o[16 * hf + 4 * x + 2], o[16 * hf + 4 * x + 3]);
-              __syncwarp();
-#pragma unroll
-              for (int x = 0; x < 4; ++x) {
-                const int row = 8 * x + lane / 4, unit = lane & 3;
-                const uint4 v = *reinterpret_cast<const uint4*>(pad + row * 64 + ((unit ^ ((row >> 1) & 3)) * 16));
-                if (to[x]) *reinterpret_cast<uint4*>(to[x] + 128 * c + 64 * hf + 16 * unit) = v;
-              }
-            }
-          }
+          for (int x = 0; x < 16; ++x) u[x] = bf16x2(__uint_as_float(o[2 * x]), __uint_as_float(o[2 * x + 1]));
+          pass(u, 64 * c);
+        } else {
+          pass(o, 128 * c);
+          pass(o + 16, 128 * c + 64);
         }
       }
     }

@@ -566,23 +566,54 @@ __global__ void __launch_bounds__(256) kv_join_kernel(KvAtt a, int tile_rows) {
   const int n = (p1 - p0 + a.part_pages - 1) / a.part_pages;
   if (n <= 1) return;
   const int64_t at = (int64_t)(row0 + i) * a.n_heads + h, step = (int64_t)a.T * a.n_heads;
+  // The outputs of eight parts are on their way while the maximum is formed, and of
+  // the next eight while these are added.
+  constexpr int kAhead = 8, kLane = D / 32;  // channels of a lane
+  const float* src = a.part_o + at * D + lane * kLane;
+  float x[kAhead][kLane];
+  auto load = [&](int p0) {
+#pragma unroll
+    for (int p = 0; p < kAhead; ++p) {
+      if (p0 + p >= n) break;
+      if constexpr (D == 128) {
+        const float4 v = *reinterpret_cast<const float4*>(src + (p0 + p) * step * D);
+        x[p][0] = v.x, x[p][1] = v.y, x[p][2] = v.z, x[p][3] = v.w;
+      } else {
+        const float2 v = *reinterpret_cast<const float2*>(src + (p0 + p) * step * D);
+        x[p][0] = v.x, x[p][1] = v.y;
+      }
+    }
+  };
+  load(0);
+  float lp[4];  // of parts lane, lane + 32, .. (128 at most)
   float top = -INFINITY;
-  for (int p = lane; p < n; p += 32) top = fmaxf(top, a.part_l[p * step + at]);
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    lp[k] = lane + 32 * k < n ? a.part_l[(lane + 32 * k) * step + at] : -INFINITY;
+    top = fmaxf(top, lp[k]);
+  }
 #pragma unroll
   for (int d = 16; d; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-  float sum = 0.0f, v[D / 32] = {};
-#pragma unroll 4
-  for (int p = 0; p < n; ++p) {
-    const float lp = a.part_l[p * step + at];
-    const float f = lp == -INFINITY ? 0.0f : ex2(lp - top);
-    const float* src = a.part_o + (p * step + at) * D + lane * (D / 32);
-    sum += f;
-    if constexpr (D == 128) {
-      const float4 x = *reinterpret_cast<const float4*>(src);
-      v[0] += f * x.x, v[1] += f * x.y, v[2] += f * x.z, v[3] += f * x.w;
-    } else {
-      const float2 x = *reinterpret_cast<const float2*>(src);
-      v[0] += f * x.x, v[1] += f * x.y;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) lp[k] = lp[k] == -INFINITY ? 0.0f : ex2(lp[k] - top);
+  float sum = 0.0f, v[kLane] = {};
+  for (int p0 = 0; p0 < n; p0 += kAhead) {
+    float y[kAhead][kLane];
+#pragma unroll
+    for (int p = 0; p < kAhead; ++p)
+#pragma unroll
+      for (int c = 0; c < kLane; ++c) y[p][c] = x[p][c];
+    if (p0 + kAhead < n) load(p0 + kAhead);
+#pragma unroll
+    for (int p = 0; p < kAhead; ++p) {
+      const int at_p = p0 + p;
+      const float all = at_p < 32 ? lp[0] : at_p < 64 ? lp[1] : at_p < 96 ? lp[2] : lp[3];
+      const float f = __shfl_sync(0xffffffffu, all, at_p & 31);
+      if (at_p < n) {
+        sum += f;
+#pragma unroll
+        for (int c = 0; c < kLane; ++c) v[c] += f * y[p][c];
+      }
     }
   }
   const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;

@@ -12,13 +12,14 @@
 // computes a few operations on each: bound by HBM for long prompts, by latency
 // for a decode step.  So there are two kernels:
 //  - kv_append_few_kernel: a CTA for 32 or 16 rows of a token (16 a pass), which
-//    reads its rows while it looks up the token's sequence, page and angles;
-//  - kv_append_stream_kernel, from kFewItems pieces on: two CTAs an SM take
-//    pieces of up to 24 KB of a token in turn; one warp looks up 32 pieces at a
-//    time and keeps four pieces on their way by bulk copies, eight warps rotate,
-//    encode and store.  (A CTA for each piece spends its time waiting for the
-//    look-ups: 8 prompts of 37 .. 2021 tokens, 64 + 2 x 8 heads of 128, took
-//    107 us so.)
+//    reads its rows while it looks up the token's sequence, page and angles:
+//    2.3 us for 8 tokens of 64 + 2 x 8 heads of 128 in FP4;
+//  - kv_append_stream_kernel, from kFewItems pieces an SM on: two CTAs an SM
+//    take pieces of up to 24 KB (a token, four small ones or a part of a large
+//    one) in turn; one warp looks up 32 tokens at a time and keeps four pieces on
+//    their way by bulk copies, eight warps rotate, encode and store.  8 prompts
+//    of 37 .. 2021 tokens, 64 + 2 x 8 heads of 128, in FP4 take 66 us, 5.3 TB/s
+//    (107 us with a CTA for each piece, which waits for its look-ups).
 #include <algorithm>
 
 #include "kv.cuh"
@@ -28,7 +29,10 @@ namespace csa2 {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kFewItems = 8;  // pieces an SM from which the stream kernel is the faster
+// Pieces an SM from which the stream kernel is the faster: 600 tokens of 64 + 2 x 8
+// heads of 128 take 8.5 us in the first kernel and 8.9 us in it, 1300 take 16.2
+// and 14.7 us; 1000 of 32 + 2 x 4 heads of 64 take 5.7 and 6.0 us, 2000 9.5 and 8.8.
+constexpr int kFewItems = 8;
 
 struct AppendArgs {
   int B, T, n_q, n_kv, rope_dims, half;
@@ -256,9 +260,11 @@ constexpr int kSlots = 4, kWorkWarps = 8, kStreamThreads = 32 * (kWorkWarps + 1)
 template <int kDim_>
 constexpr int kPieceRows = 24576 / (2 * kDim_);  // at most, of one token
 
-struct StreamPiece {  // what the workers need to know of a piece
-  Place at;
-  int row0, rows;
+constexpr int kSmall = 4;  // small tokens stand this many in a piece
+template <int kTokens>
+struct StreamPiece {   // what the workers need to know of a piece
+  Place at[kTokens];   // n < 0: no token
+  int row0, rows;      // of each token; no rows: the end
 };
 
 // Sequence of token n by bisection over cu (the first that ends behind n), and
@@ -287,65 +293,72 @@ __device__ __forceinline__ bool find_place(const AppendArgs& a, int n, Place& at
 }
 
 template <int kDim_>
-constexpr int slot_bytes() { return kPieceRows<kDim_> * kDim_ * 2 + kDim_ * 4; }  // rows, then the angles
+constexpr int slot_bytes() { return kPieceRows<kDim_> * kDim_ * 2 + kDim_ * 4; }  // each token's rows, then its angles
 
-template <int kDim_, bool kFp4>
+template <int kDim_, bool kFp4, int kTokens>
 __global__ void __launch_bounds__(kStreamThreads, 2) kv_append_stream_kernel(AppendArgs a) {
-  constexpr int kLanes = kDim_ / 8, kRows = 32 * kWorkWarps / kLanes;
+  constexpr int kLanes = kDim_ / 8, kWarpRows = 32 / kLanes;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ __align__(8) uint64_t full[kSlots], empty[kSlots];
-  __shared__ StreamPiece piece[kSlots];
+  __shared__ StreamPiece<kTokens> piece[kSlots];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (tid == 0) {
     for (int s = 0; s < kSlots; ++s) {
-      tc::mbar_init(&full[s], 1);
-      tc::mbar_init(&empty[s], 32 * kWorkWarps);
+      tc::mbar_init(&full[s], kTokens);
+      tc::mbar_init(&empty[s], kWorkWarps);
     }
     tc::fence_mbar_init();
   }
   __syncthreads();
   griddep_wait();  // every input may be the previous kernel's output
   griddep_launch();
-  const int n_rows = a.n_q + 2 * a.n_kv, per = (n_rows + kPieceRows<kDim_> - 1) / kPieceRows<kDim_>;
-  const int most = ((n_rows + per - 1) / per + kRows - 1) / kRows * kRows;  // rows of a piece
-  const int64_t items = (int64_t)a.T * per;
+  // A piece holds kTokens whole tokens, or (per > 1) one of the parts of a token.
+  const int n_rows = a.n_q + 2 * a.n_kv;
+  const int per = kTokens > 1 ? 1 : (n_rows + kPieceRows<kDim_> - 1) / kPieceRows<kDim_>;
+  const int most = ((n_rows + per - 1) / per + 15) / 16 * 16;  // rows of a part
+  const int64_t pieces = per > 1 ? (int64_t)a.T * per : (a.T + kTokens - 1) / kTokens;
+  const int angles = (per > 1 ? most : n_rows) * kDim_ * 2, token_bytes = angles + a.rope_dims * 4;
   bool ok = true;
   if (warp == kWorkWarps) {
     int count = 0;  // pieces sent so far
-    for (int64_t base = blockIdx.x; base < items && ok; base += 32 * (int64_t)gridDim.x) {
-      const int64_t item = base + lane * (int64_t)gridDim.x;
-      Place at{0, -1, 0};
+    const int k = lane % kTokens, groups = 32 / kTokens;
+    for (int64_t base = blockIdx.x; base < pieces && ok; base += groups * (int64_t)gridDim.x) {
+      // each lane looks up one token
+      const int64_t i = base + lane / kTokens * (int64_t)gridDim.x;
+      const int64_t n = per > 1 ? i / per : i * kTokens + k;
+      const int row0 = per > 1 ? (int)(i % per) * most : 0;
+      Place at{-1, -1, 0};
       int64_t pos = 0;
-      // (pieces are whole passes: the last of a token may be empty)
-      const bool there = item < items && (item % per) * most < n_rows && find_place(a, (int)(item / per), at, pos);
-      const int row0 = there ? (int)(item % per) * most : 0;
-      uint32_t todo = __ballot_sync(0xffffffffu, there);
-      while (todo && ok) {
-        const int src = __ffs(todo) - 1;
-        todo &= todo - 1;
+      // (parts are whole passes: a token's last may be empty)
+      const bool there = i < pieces && n < a.T && row0 < n_rows && find_place(a, (int)n, at, pos);
+      const uint32_t found = __ballot_sync(0xffffffffu, there);
+      for (int g = 0; g < groups && ok; ++g) {
+        if (!((found >> (g * kTokens)) & ((2u << (kTokens - 1)) - 1u))) continue;
         const int s = count % kSlots;
         if (count >= kSlots) ok = __all_sync(0xffffffffu, tc::mbar_wait(&empty[s], ((count / kSlots) & 1) ^ 1));
         if (!ok) break;
         ++count;
-        if (lane == src) {
-          const int rows = min(most, n_rows - row0);
-          piece[s] = StreamPiece{at, row0, rows};
-          uint8_t* dst = smem + s * slot_bytes<kDim_>();
-          tc::mbar_arrive_expect_tx(&full[s], rows * kDim_ * 2 + a.rope_dims * 4);
-          // the piece's queries, keys and values: up to three runs
-          const int q1 = min(row0 + rows, a.n_q), k1 = min(row0 + rows, a.n_q + a.n_kv);
-          if (row0 < q1)
-            tc::bulk_g2s(dst, a.q + (int64_t)at.n * a.q_stride + row0 * kDim_, (q1 - row0) * kDim_ * 2, &full[s]);
-          const int k0 = max(row0, a.n_q);
-          if (k0 < k1)
-            tc::bulk_g2s(dst + (k0 - row0) * kDim_ * 2, a.k + (int64_t)at.n * a.k_stride + (k0 - a.n_q) * kDim_,
-                         (k1 - k0) * kDim_ * 2, &full[s]);
-          const int v0 = max(row0, a.n_q + a.n_kv), v1 = row0 + rows;
-          if (v0 < v1)
-            tc::bulk_g2s(dst + (v0 - row0) * kDim_ * 2, a.v + (int64_t)at.n * a.v_stride + (v0 - a.n_q - a.n_kv) * kDim_,
-                         (v1 - v0) * kDim_ * 2, &full[s]);
-          if (a.rope_dims)
-            tc::bulk_g2s(dst + kPieceRows<kDim_> * kDim_ * 2, a.rope + pos * a.rope_dims, a.rope_dims * 4, &full[s]);
+        if (lane / kTokens == g) {
+          const int rows = min(per > 1 ? most : n_rows, n_rows - row0);
+          piece[s].at[k] = at;
+          if (k == 0) piece[s].row0 = row0, piece[s].rows = rows;
+          uint8_t* dst = smem + s * slot_bytes<kDim_>() + k * token_bytes;
+          tc::mbar_arrive_expect_tx(&full[s], there ? rows * kDim_ * 2 + a.rope_dims * 4 : 0);
+          if (there) {
+            // queries, keys and values: up to three runs
+            const int q1 = min(row0 + rows, a.n_q), k1 = min(row0 + rows, a.n_q + a.n_kv);
+            if (row0 < q1) tc::bulk_g2s(dst, a.q + n * a.q_stride + row0 * kDim_, (q1 - row0) * kDim_ * 2, &full[s]);
+            const int k0 = max(row0, a.n_q);
+            if (k0 < k1)
+              tc::bulk_g2s(dst + (k0 - row0) * kDim_ * 2, a.k + n * a.k_stride + (k0 - a.n_q) * kDim_,
+                           (k1 - k0) * kDim_ * 2, &full[s]);
+            const int v0 = max(row0, a.n_q + a.n_kv), v1 = row0 + rows;
+            if (v0 < v1)
+              tc::bulk_g2s(dst + (v0 - row0) * kDim_ * 2, a.v + n * a.v_stride + (v0 - a.n_q - a.n_kv) * kDim_,
+                           (v1 - v0) * kDim_ * 2, &full[s]);
+            if (a.rope_dims)
+              tc::bulk_g2s(dst + angles, a.rope + pos * a.rope_dims, a.rope_dims * 4, &full[s]);
+          }
         }
         __syncwarp();
       }
@@ -353,46 +366,50 @@ __global__ void __launch_bounds__(kStreamThreads, 2) kv_append_stream_kernel(App
     // the end: a piece without rows
     const int s = count % kSlots;
     if (ok && count >= kSlots) ok = __all_sync(0xffffffffu, tc::mbar_wait(&empty[s], ((count / kSlots) & 1) ^ 1));
-    if (lane == 0) {
-      if (ok) {
-        piece[s].rows = 0;
-        tc::mbar_arrive(&full[s]);
-      } else {
-        report(a.status, CSA2_ERR_TIMEOUT);
-      }
+    if (!ok && lane == 0) report(a.status, CSA2_ERR_TIMEOUT);
+    if (ok && lane < kTokens) {
+      if (lane == 0) piece[s].rows = 0;
+      tc::mbar_arrive(&full[s]);
     }
     // nothing may land in shared memory after the CTA has left
-    for (int i = max(0, count - kSlots + 1); i < count; ++i) tc::mbar_wait(&full[i % kSlots], (i / kSlots) & 1);
+    for (int i = max(0, count - kSlots + (ok ? 1 : 0)); i < count; ++i) tc::mbar_wait(&full[i % kSlots], (i / kSlots) & 1);
   } else {
     const int col = tid % kLanes, c0 = 8 * col, pairs = a.rope_dims / 2;
     const bool turned = c0 < a.rope_dims;
     const int mate = (lane + (c0 >= pairs ? -pairs : pairs) / 8) & 31;
+    // each token's share of the warps
+    constexpr int kShare = kWorkWarps / kTokens;
+    const int k = warp / kShare;
     for (int count = 0;; ++count) {
       const int s = count % kSlots;
       if (!__all_sync(0xffffffffu, tc::mbar_wait(&full[s], (count / kSlots) & 1))) {
         if (lane == 0) report(a.status, CSA2_ERR_TIMEOUT);
         break;
       }
-      const StreamPiece p = piece[s];
-      if (p.rows == 0) break;
-      const uint8_t* src = smem + s * slot_bytes<kDim_>();
-      Turn turn = {};
-      if (turned) turn.load(reinterpret_cast<const float4*>(src + kPieceRows<kDim_> * kDim_ * 2), c0, pairs, a.half);
+      const int rows = piece[s].rows, row0 = piece[s].row0;
+      if (rows == 0) break;
+      const Place at = piece[s].at[k];
+      if (at.n >= 0) {
+        const uint8_t* src = smem + s * slot_bytes<kDim_>() + k * token_bytes;
+        Turn turn = {};
+        if (turned) turn.load(reinterpret_cast<const float4*>(src + angles), c0, pairs, a.half);
 #pragma unroll 2
-      for (int r0 = 0; r0 < p.rows; r0 += kRows) {
-        const int r = r0 + tid / kLanes;
-        const bool live = r < p.rows;
-        put_row<kDim_, kFp4>(a, p.at, p.row0 + r, live, col, turn, turned, mate,
-                             live ? *reinterpret_cast<const uint4*>(src + (r * kDim_ + c0) * 2) : make_uint4(0, 0, 0, 0));
+        for (int r0 = warp % kShare * kWarpRows; r0 < rows; r0 += kShare * kWarpRows) {
+          const int r = r0 + lane / kLanes;
+          const bool live = r < rows;
+          put_row<kDim_, kFp4>(a, at, row0 + r, live, col, turn, turned, mate,
+                               live ? *reinterpret_cast<const uint4*>(src + (r * kDim_ + c0) * 2) : make_uint4(0, 0, 0, 0));
+        }
       }
-      tc::mbar_arrive(&empty[s]);
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(&empty[s]);
     }
   }
 }
 
-template <int kDim_, bool kFp4>
+template <int kDim_, bool kFp4, int kTokens>
 cudaError_t stream_of(const AppendArgs& a, int64_t pieces, cudaStream_t stream) {
-  auto kern = kv_append_stream_kernel<kDim_, kFp4>;
+  auto kern = kv_append_stream_kernel<kDim_, kFp4, kTokens>;
   constexpr int kSmem = kSlots * slot_bytes<kDim_>();
   static bool done[64];
   const cudaError_t e = allow_smem(kern, kSmem, done);
@@ -416,12 +433,21 @@ cudaError_t launch_kv_append(const csa2_kv_cfg& cfg, int B, int T, const uint16_
   const int piece_rows = 24576 / (2 * cfg.head_dim);
   const int64_t pieces = (int64_t)T * ((rows + piece_rows - 1) / piece_rows);
   if (pieces >= kFewItems * num_sms()) {
-    if (cfg.head_dim == 128) return fp4 ? stream_of<128, true>(a, pieces, stream) : stream_of<128, false>(a, pieces, stream);
-    return fp4 ? stream_of<64, true>(a, pieces, stream) : stream_of<64, false>(a, pieces, stream);
+    // four small tokens to a piece where they fit: 4096 tokens of 24 + 2 x 8 heads of
+    // 64 take 19 us so and 25 us one by one, 16000 take 42 and 68 us
+    const bool small = kSmall * (rows + 2) <= piece_rows + 2;
+#define CSA2_STREAM(D, F)                                                     \
+  (small ? stream_of<D, F, kSmall>(a, (T + kSmall - 1) / kSmall, stream)      \
+         : stream_of<D, F, 1>(a, pieces, stream))
+    if (cfg.head_dim == 128) return fp4 ? CSA2_STREAM(128, true) : CSA2_STREAM(128, false);
+    return fp4 ? CSA2_STREAM(64, true) : CSA2_STREAM(64, false);
+#undef CSA2_STREAM
   }
   const int per_pass = kThreads / (cfg.head_dim / 8), passes = (rows + per_pass - 1) / per_pass;
-  // one pass a CTA while the passes do not fill the GPU, two beyond
-  const bool few = (int64_t)T * passes <= 4 * num_sms();
+  // one pass a CTA while the passes do not fill the GPU, two beyond: 32 tokens of 128 +
+  // 2 x 16 heads of 128 take 2.6 us by one and 3.0 by two, 300 tokens of 32 + 2 x 4
+  // heads of 64 (600 passes) 3.2 and 2.9
+  const bool few = (int64_t)T * passes <= 3 * num_sms();
   const dim3 grid(T, few ? passes : (passes + 1) / 2), block(kThreads);
 #define CSA2_APPEND(D, F)                                                          \
   (few ? launch_k(kv_append_few_kernel<D, F, 1>, grid, block, 0, stream, 0, a)     \

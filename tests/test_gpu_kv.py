@@ -163,6 +163,39 @@ def test_append_reports_places_out_of_bounds():
             assert bool(cache.k_data[0].any()) == (page is None)
 
 
+@pytest.mark.parametrize("dtype", [FP4, BF16])
+@pytest.mark.parametrize("hq,dim", [(4, 64), (90, 128)])
+def test_append_of_many_tokens_beside_a_bad_place(hq, dim, dtype):
+    # rows ahead of the first sequence and behind the last, and one without a place, beside rows that are written
+    rng = np.random.default_rng(hq)
+    cfg = csa.KVCfg(hq, 1, dim, dtype, rope_dims=dim)
+    lens, first, T = [1, 698, 3, 601], 5, 1320
+    cu = torch.tensor(np.cumsum([first] + lens), dtype=torch.int32, device="cuda")
+    q, k, v = (_dev(_kv.normal(rng, T, h, dim)) for h in (hq, 1, 1))
+    got = []
+    for start in (0, -1):
+        cache, st = csa.KVCache(cfg, 4, 768), _status()
+        out = torch.full_like(q, 7.0)
+        csa.kv_append(cfg, k, v, cu, torch.tensor([3, start, 9, 60], device="cuda"), cache, rope=csa.rope_table(1024, dim),
+                      q=q, q_out=out, status=st)
+        assert int(st.item()) == (17 if start else 0)
+        got.append((cache, out))
+    (good, out), (some, part) = got
+    lo, hi = first + 1, first + 1 + lens[1]
+    assert (part[lo] == 7).all() and torch.equal(part[:lo], out[:lo]) and torch.equal(part[hi:], out[hi:])
+    assert (out[:first] == 7).all() and (out[first + sum(lens):] == 7).all() and not (out[lo] == 7).all()
+    # position -1 is the only one without a place: the rows behind it stand at 0, 1, ..
+    alone, own = csa.KVCache(cfg, 1, 768), q[lo + 1:hi].clone()
+    csa.kv_append(cfg, k[lo + 1:hi], v[lo + 1:hi], _cu([lens[1] - 1]), torch.zeros(1, dtype=torch.int64, device="cuda"), alone,
+                  rope=csa.rope_table(1024, dim), q=own, q_out=own)
+    assert torch.equal(part[lo + 1:hi], own)
+    table = good.block_table.long()
+    for kind in ("k_data", "v_data"):
+        a, b = getattr(good, kind), getattr(some, kind)
+        assert all(torch.equal(a[table[i]], b[table[i]]) for i in (0, 2, 3))
+        assert torch.equal(b[table[1]], getattr(alone, kind)[alone.block_table[0].long()])
+
+
 # -------------------------------------------------------------- attention --
 
 def _attend_case(cfg, nq, kv, cross=False, seed=0, workspace=True, std=1.0, scale=None, pad=0, wide=0, slack=0,

@@ -1,5 +1,5 @@
 // C ABI of the paged key / value operators: argument validation on the host,
-// then the launches of kv_append.cu and kv_attend.cu.
+// then the launches of kv_append.cu and kv_rows.cu.
 #include <cmath>
 #include <cstring>
 

@@ -14,12 +14,12 @@
 //
 // Warps 0-3 and 4-7 hold the rows (thread = row = TMEM lane, with registers for
 // its 128 scores); warps 8-11 bring keys, 12-15 values into shared memory as
-// [channel chunk][128 keys][16 B], which is K-major for the first product and
-// MN-major for the second: FP4 decoded to f16 on the way, one row a thread, from
-// a ring of pages that warps 18 and 19 fill with bulk copies; bf16 pages, stored in
-// that order, by bulk copies (warps 8 and 12).  Warp 16 issues the products (a
-// warp for each place made their batches longer, not the pauses between them
-// shorter).
+// [channel chunk][128 keys][16 B] (copied values: [page][chunk][64 keys][16 B]),
+// which is K-major for the first product and MN-major for the second: FP4 decoded
+// to f16 on the way, one row a thread, from a ring of pages that warps 18 and 19
+// fill with bulk copies; bf16 pages, stored in that order, by bulk copies (warps
+// 8-11 and 12).  Warp 16 issues the products (a warp for each place made their
+// batches longer, not the pauses between them shorter).
 //
 // The output in TMEM is rescaled only when a row's maximum grew by more than
 // 2^8 since its last rescaling (weights up to 2^8 are as exact as those up to
@@ -116,14 +116,13 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tiles_kernel(KvAtt a) {
   const int32_t* table = a.c.table + (int64_t)b * a.c.max_pages;
 
   if (tid == 0) {
-    const uint32_t filling = kFp4 ? 4 : 32;  // warps; or lanes of the one that copies
     for (int s = 0; s < kLongRing; ++s) {
       tc::mbar_init(&raw_full[s], 1);
       tc::mbar_init(&raw_free[s], 4);
     }
     for (int s = 0; s < kStages; ++s) {
-      tc::mbar_init(&k_full[s], filling);
-      tc::mbar_init(&v_full[s], filling);
+      tc::mbar_init(&k_full[s], 4);               // warps
+      tc::mbar_init(&v_full[s], kFp4 ? 4 : 32);   // warps; or lanes of the one that copies
       tc::mbar_init(&k_free[s], 1);
       tc::mbar_init(&v_free[s], 1);
     }
@@ -502,12 +501,14 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tiles_kernel(KvAtt a) {
         tc::fence_async_smem();
         warp_arrive(v ? &v_full[s] : &k_full[s]);
       }
-    } else if (warp == kKeyWarp || warp == kValueWarp) {
+    } else if (warp <= kValueWarp) {
+      // ---- pages as they are: keys by four warps, each a quarter of the chunks (a copy
+      // of 1 KB takes a warp some 90 cycles), values, a page at once, by one
       const bool v = warp == kValueWarp;
-      const uint8_t* src = v ? a.c.v : a.c.k;
       uint64_t* full = v ? v_full : k_full;
       uint64_t* free_ = v ? v_free : k_free;
-      for (int it = 0; it < n_it; ++it) {
+      int it = 0;
+      for (; it < n_it; ++it) {
         const int s = it % kStages;
         uint8_t* dst = smem + (v ? L::kV : L::kK) + s * L::kOperand;
         if (it >= kStages && !__all_sync(0xffffffffu, tc::mbar_wait(&free_[s], ((it / kStages) & 1) ^ 1))) {
@@ -529,15 +530,21 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tiles_kernel(KvAtt a) {
         const int live = keys - key0 - it * kTileKeys;
         const bool tail = v && live < kTileKeys && (live < kPage ? at[0] : at[1]) >= 0;
         uint64_t* bar = tail ? &tail_full : &full[s];
-        if (lane == 0) tc::mbar_arrive_expect_tx(bar, ((at[0] >= 0) + (at[1] >= 0)) * (L::kOperand / 2));
+        if (lane == 0) tc::mbar_arrive_expect_tx(bar, ((at[0] >= 0) + (at[1] >= 0)) * (L::kOperand / (v ? 2 : 8)));
         __syncwarp();
         if (tc::elect_one()) {
 #pragma unroll
           for (int x = 0; x < 2; ++x) {
             if (at[x] < 0) continue;
+            if (v) {
+              tc::bulk_g2s(dst + x * (L::kOperand / 2), a.c.v + at[x], L::kOperand / 2, bar);
+              continue;
+            }
 #pragma unroll
-            for (int c = 0; c < D / 8; ++c)
-              tc::bulk_g2s(dst + c * kChunk + x * (kPage * 16), src + at[x] + c * (kPage * 16), kPage * 16, bar);
+            for (int y = 0; y < D / 32; ++y) {
+              const int c = (warp - kKeyWarp) * (D / 32) + y;
+              tc::bulk_g2s(dst + c * kChunk + x * (kPage * 16), a.c.k + at[x] + c * (kPage * 16), kPage * 16, bar);
+            }
           }
         }
         __syncwarp();
@@ -545,7 +552,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tiles_kernel(KvAtt a) {
           auto clear = [&](int from, int to) {  // values of these keys
             for (int key = from + lane; key < to; key += 32)
 #pragma unroll
-              for (int c = 0; c < D / 8; ++c) *reinterpret_cast<uint4*>(dst + c * kChunk + key * 16) = make_uint4(0, 0, 0, 0);
+              for (int c = 0; c < D / 8; ++c)
+                *reinterpret_cast<uint4*>(dst + key / kPage * (L::kOperand / 2) + (c * kPage + key % kPage) * 16) =
+                    make_uint4(0, 0, 0, 0);
             tc::fence_async_smem();
           };
           if (tail) {  // the last tile
@@ -555,9 +564,11 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tiles_kernel(KvAtt a) {
           }
           if (at[0] < 0) clear(0, kPage);
           if (at[1] < 0 && pb + 2 * it + 1 < pe) clear(kPage, kTileKeys);
+          if (lane != 0 || tail) tc::mbar_arrive(&full[s]);
         }
-        if (lane != 0 || tail) tc::mbar_arrive(&full[s]);
       }
+      // nothing may land in shared memory after the CTA has left
+      for (int i = max(0, it - kStages); !ok && i < it; ++i) tc::mbar_wait(&full[i % kStages], (i / kStages) & 1);
     }
   } else {
     regs_dec<kIssueRegs>();
@@ -566,7 +577,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tiles_kernel(KvAtt a) {
       // ------------------------------------------------------- products --
       constexpr uint32_t kIdS = tc::idesc_f16(128, kTileKeys, !kFp4, !kFp4, false, false);
       constexpr uint32_t kIdO = tc::idesc_f16(128, D, !kFp4, !kFp4, false, true);
-      constexpr uint32_t kHiK = tc::sdesc_hi(128), kHiV = tc::sdesc_hi(kChunk);
+      // values decoded: 128 keys of a chunk together; copied: 64, a page after the other
+      constexpr uint32_t kHiK = tc::sdesc_hi(128), kHiV = tc::sdesc_hi(kFp4 ? kChunk : kChunk / 2);
       constexpr uint32_t kTile16 = L::kOperand / 16;
       static_assert(kStages == 2, "the loops below go over two key tiles");
       // Place and stage are compile-time numbers, the descriptors' low words formed
@@ -596,7 +608,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tiles_kernel(KvAtt a) {
 #pragma unroll
           for (int ks = 1; ks < kTileKeys / 16; ++ks) {
             if (ks >= kPage / 16 && half) break;
-            tc::mma_ts_lo(tb + 256 + D * j(), tb + 128 * j() + 8 * ks, v_lo + s() * kTile16 + ks * (256 / 16), kHiV, kIdO,
+            tc::mma_ts_lo(tb + 256 + D * j(), tb + 128 * j() + 8 * ks, v_lo + s() * kTile16 + ks * (256 / 16) + (kFp4 || ks < kPage / 16 ? 0 : kTile16 / 2 - kPage),
+                          kHiV, kIdO,
                           1u);
           }
           if (done) tc::mma_commit(done);

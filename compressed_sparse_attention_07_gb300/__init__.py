@@ -480,7 +480,8 @@ def kv_append(cfg: KVCfg, k, v, cu, pos0, cache: KVCache, rope=None, q=None, q_o
 
 
 def kv_workspace_bytes(cfg: KVCfg, B: int, T: int, max_q: int, max_kv: int) -> int:
-    """Workspace with which kv_attend and kv_cross_attend divide keys of these sizes as they would best."""
+    """Workspace with which kv_attend and kv_cross_attend divide keys of these sizes, and decode them ahead, as they
+    would best."""
     return int(load().csa2_kv_workspace_bytes(C.byref(cfg), B, T, max_q, max_kv))
 
 

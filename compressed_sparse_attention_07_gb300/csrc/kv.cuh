@@ -101,8 +101,16 @@ struct KvAtt {
   // log2-sum-exp2 to part_l [n_parts][T * n_heads]
   int n_parts, part_pages;
   int cluster;  // the parts of a head join in a cluster instead
+  // row tiles of a sequence and kv head; tiles of the call, in the order of their
+  // CTAs, that are not divided
+  int n_tiles, whole;
   float* part_o;
   float* part_l;
+  // FP4 pages decoded for this call: page p of sequence b and a kv head as f16 in a
+  // BF16 page's order, at block (b * plain_pages + p) * kv_heads + kv head
+  uint8_t* plain_k;  // null: none
+  uint8_t* plain_v;
+  int plain_pages;
   int32_t* status;
 };
 
@@ -155,6 +163,8 @@ cudaError_t launch_kv_append(const csa2_kv_cfg& cfg, int B, int T, const uint16_
 struct KvPlan {
   int n_parts, part_pages;
   bool cluster;  // the parts join in a cluster, without workspace
+  int whole;     // row tiles that are not divided (tile kernel)
+  int64_t ctas;  // of the tile kernel or its joining kernel, whichever has more, or above
 };
 KvPlan kv_plan(const csa2_kv_cfg& cfg, int B, int max_q, int max_kv, bool cross, int most_parts);
 
@@ -172,9 +182,10 @@ cudaError_t allow_smem(K kern, int bytes, bool (&done)[64]) {
 // The plan of the tile kernel, which takes more rows of a kv head than kMostRows;
 // its launch, and the rows of its CTA.
 constexpr int kMostRows = 32;
-void kv_tiles_plan(const csa2_kv_cfg& cfg, int B, int max_q, int64_t max_kv, bool cross, int most_parts, int* n_parts,
-                   int* part_pages);
+KvPlan kv_tiles_plan(const csa2_kv_cfg& cfg, int B, int max_q, int64_t max_kv, bool cross, int most_parts);
 cudaError_t launch_kv_tiles(const csa2_kv_cfg& cfg, int B, const KvAtt& a, cudaStream_t stream);
+// Bytes of the keys decoded for a call, or 0 where they are decoded in passing.
+size_t kv_plain_bytes(const csa2_kv_cfg& cfg, int B, int max_q, int64_t max_kv, bool cross);
 int kv_tiles_rows();
 
 cudaError_t launch_kv_attend(const csa2_kv_cfg& cfg, int B, KvAtt& a, cudaStream_t stream);

@@ -70,12 +70,19 @@ int32_t attend(const csa2_kv_cfg* cfg, bool cross, int32_t B, int32_t T, const u
   a.q = q, a.q_stride = q_stride, a.cu = cu, a.c = view_of(*cache), a.kv_len = kv_len, a.scale = scale;
   a.out = out, a.out_stride = out_stride, a.lse = lse, a.status = status;
   const int64_t rows = (int64_t)T * cfg->n_heads;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  if (const size_t plain = kv_plain_bytes(*cfg, B, a.max_q, max_kv, cross); plain && plain <= workspace_bytes) {
+    a.plain_k = ws, a.plain_v = ws + plain / 2, a.plain_pages = (max_kv + kPage - 1) / kPage;
+    ws += plain, workspace_bytes -= plain;
+  }
   const size_t one = (size_t)rows * (cfg->head_dim + 1) * 4;
   const size_t fit = workspace_bytes / one;
   const KvPlan plan = kv_plan(*cfg, B, a.max_q, max_kv, cross, fit > 1024 ? 1024 : (int)fit);
   a.n_parts = plan.n_parts, a.part_pages = plan.part_pages, a.cluster = plan.cluster ? 1 : 0;
+  a.whole = plan.whole;
+  if (plan.ctas > INT32_MAX) return CSA2_ERR_UNSUPPORTED;
   if (a.n_parts > 1 && !a.cluster) {
-    a.part_o = static_cast<float*>(workspace);
+    a.part_o = reinterpret_cast<float*>(ws);
     a.part_l = a.part_o + a.n_parts * rows * cfg->head_dim;
   }
   return cuda_status(launch_kv_attend(*cfg, B, a, static_cast<cudaStream_t>(stream)));
@@ -116,13 +123,15 @@ int32_t csa2_kv_append(const csa2_kv_cfg* cfg, int32_t B, int32_t T, const uint1
 size_t csa2_kv_workspace_bytes(const csa2_kv_cfg* cfg, int32_t B, int32_t T, int32_t max_q, int32_t max_kv) {
   if (check_cfg(cfg) || B < 0 || T < 0 || max_q < 0 || max_kv < 0 || B == 0 || T == 0 || max_q == 0) return 0;
   if (max_q > T) max_q = T;
-  int n = 1;
+  size_t most = 0;
   for (const bool cross : {false, true}) {
     if (cross && cfg->window) break;
     const KvPlan plan = kv_plan(*cfg, B, max_q, max_kv, cross, 1024);
-    if (!plan.cluster && plan.n_parts > n) n = plan.n_parts;
+    size_t n = kv_plain_bytes(*cfg, B, max_q, max_kv, cross);
+    if (!plan.cluster && plan.n_parts > 1) n += (size_t)plan.n_parts * T * cfg->n_heads * (cfg->head_dim + 1) * 4;
+    if (n > most) most = n;
   }
-  return n > 1 ? (size_t)n * T * cfg->n_heads * (cfg->head_dim + 1) * 4 : 0;
+  return most;
 }
 
 int32_t csa2_kv_attend(const csa2_kv_cfg* cfg, int32_t B, int32_t T, const uint16_t* q, int64_t q_stride,

@@ -548,18 +548,20 @@ __global__ void __launch_bounds__(Rows<D, kFp4, NT, kCluster>::kWarps * 32, Rows
   }
 }
 
-// Joins the parts of each row: out = sum 2^(l_p - l) o_p, one warp a row.
+// Joins the parts of each row of the divided tiles: out = sum 2^(l_p - l) o_p, one
+// warp a row.
 template <int D>
 __global__ void __launch_bounds__(256) kv_join_kernel(KvAtt a, int tile_rows) {
   griddep_wait();
   griddep_launch();
-  const int b = blockIdx.y, lane = threadIdx.x & 31;
+  const int lane = threadIdx.x & 31, per = tile_rows / 8, id = a.whole + blockIdx.x / per;
+  const int kh = id / a.n_tiles % a.kv_heads, b = id / a.n_tiles / a.kv_heads;
+  const int tile0 = (a.n_tiles - 1 - id % a.n_tiles) * tile_rows;
   int row0, rows, keys;
   if (!kv_sequence(a, b, row0, rows, keys)) return;
-  const int64_t r = (int64_t)blockIdx.x * 8 + threadIdx.x / 32;
-  if (r >= (int64_t)rows * a.n_heads) return;
-  const int i = (int)(r / a.n_heads), h = (int)(r % a.n_heads);
-  const int tile0 = (i * a.group + h % a.group) / tile_rows * tile_rows;
+  const int r = tile0 + blockIdx.x % per * 8 + threadIdx.x / 32;
+  if (r >= rows * a.group) return;
+  const int i = group_of(a, r), h = kh * a.group + r - i * a.group;
   const int last = min(tile0 + tile_rows, rows * a.group) - 1;
   int p0, p1;
   kv_pages(a, group_of(a, tile0), group_of(a, last), rows, keys, p0, p1);
@@ -661,11 +663,8 @@ int row_blocks(int64_t n) { return n <= 8 ? 1 : n <= 16 ? 2 : 4; }
 
 KvPlan kv_plan(const csa2_kv_cfg& cfg, int B, int max_q, int max_kv, bool cross, int most_parts) {
   const int group = cfg.n_heads / cfg.kv_heads;
-  KvPlan plan = {1, 1, false};
-  if ((int64_t)max_q * group > kMostRows) {
-    kv_tiles_plan(cfg, B, max_q, max_kv, cross, most_parts, &plan.n_parts, &plan.part_pages);
-    return plan;
-  }
+  if ((int64_t)max_q * group > kMostRows) return kv_tiles_plan(cfg, B, max_q, max_kv, cross, most_parts);
+  KvPlan plan = {1, 1, false, 0, 0};
   const int nt = row_blocks((int64_t)max_q * group);
   const int64_t tiles = ((int64_t)max_q * group + 8 * nt - 1) / (8 * nt);
   int64_t pages = ((int64_t)max_kv + kPage - 1) / kPage;
@@ -708,14 +707,15 @@ cudaError_t launch_kv_attend(const csa2_kv_cfg& cfg, int B, KvAtt& a, cudaStream
   const int nt = row_blocks((int64_t)a.max_q * a.group);
   const bool fp4 = cfg.cache_dtype == CSA2_CACHE_FP4, many = (int64_t)a.max_q * a.group > kMostRows;
   const int tile_rows = many ? kv_tiles_rows() : 8 * nt;
+  a.n_tiles = (int)(((int64_t)a.max_q * a.group + tile_rows - 1) / tile_rows);
   cudaError_t e;
   if (many) e = launch_kv_tiles(cfg, B, a, stream);
   else if (cfg.head_dim == 128) e = fp4 ? launch_rows<128, true>(nt, B, a, stream) : launch_rows<128, false>(nt, B, a, stream);
   else e = fp4 ? launch_rows<64, true>(nt, B, a, stream) : launch_rows<64, false>(nt, B, a, stream);
   if (e != cudaSuccess || a.n_parts <= 1 || a.cluster) return e;
-  const dim3 grid((unsigned)(((int64_t)a.max_q * a.n_heads + 7) / 8), B);
-  return cfg.head_dim == 128 ? launch_k(kv_join_kernel<128>, grid, dim3(256), 0, stream, 0, a, tile_rows)
-                             : launch_k(kv_join_kernel<64>, grid, dim3(256), 0, stream, 0, a, tile_rows);
+  const unsigned grid = ((unsigned)B * a.kv_heads * a.n_tiles - a.whole) * (tile_rows / 8);
+  return cfg.head_dim == 128 ? launch_k(kv_join_kernel<128>, dim3(grid), dim3(256), 0, stream, 0, a, tile_rows)
+                             : launch_k(kv_join_kernel<64>, dim3(grid), dim3(256), 0, stream, 0, a, tile_rows);
 }
 
 }  // namespace csa2

@@ -19,7 +19,8 @@
 // to f16 on the way, one row a thread, from a ring of pages that warps 18 and 19
 // fill with bulk copies; bf16 pages, stored in that order, by bulk copies (warps
 // 8-11 and 12).  Warp 16 issues the products (a warp for each place made their
-// batches longer, not the pauses between them shorter).
+// batches longer, not the pauses between them shorter).  FP4 pages that many
+// rows read are decoded ahead by kv_decode_kernel and then taken as bf16 pages are.
 //
 // The output in TMEM is rescaled only when a row's maximum grew by more than
 // 2^8 since its last rescaling (weights up to 2^8 are as exact as those up to
@@ -59,6 +60,14 @@ struct Tiles {
   }
 };
 
+// Rows that read a key from which FP4 pages are decoded once for the call, into the
+// workspace (up to kMostPlain bytes of it).  Decoding in every CTA takes issue slots
+// from the softmax beside it; ahead, a write and reads from L2.  64 over 8 heads of
+// 128 on 16384 keys, in passing / ahead: 256 tokens (2048 rows) 152 / 157 us, 512
+// 239 / 228, 2048 879 / 797; 2 x 4096 on themselves 547 / 495.
+constexpr int64_t kPlainRows = 4096;
+constexpr size_t kMostPlain = (size_t)2 << 30;
+
 template <int N>
 __device__ __forceinline__ void regs_inc() {
   asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
@@ -77,9 +86,11 @@ struct Num {
 // Chunk-major operand tile: element (row, channel) at ((c / 8) * 128 + row) * 16 + (c % 8) * 2.
 constexpr uint32_t kChunk = 128 * 16;
 
-template <int D, bool kFp4>
+// kPlain: FP4 pages that kv_decode_kernel has decoded.
+template <int D, bool kFp4, bool kPlain>
 __global__ void __launch_bounds__(kThreads, 1) kv_tiles_kernel(KvAtt a) {
   using L = Tiles<D>;
+  constexpr bool kCodes = kFp4 && !kPlain;  // decoded here
   extern __shared__ __align__(1024) uint8_t smem[];
   __shared__ __align__(8) uint64_t k_full[kStages], v_full[kStages], k_free[kStages], v_free[kStages], s_ready[2],
       p_ready[2], o_full[2];
@@ -90,9 +101,13 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tiles_kernel(KvAtt a) {
   __shared__ float half_m[2][kTileRows], half_l[2][kTileRows];
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int n_tiles = gridDim.x / a.n_parts;
-  const int part = blockIdx.x % a.n_parts, kh = blockIdx.y, b = blockIdx.z;
-  const int tile0 = (n_tiles - 1 - (int)(blockIdx.x / a.n_parts)) * kCtaRows;  // the longest first
+  // row tile (the longest first), kv head, sequence and part; with undivided tiles
+  // ahead of the divided ones all in one dimension of the grid
+  int id = blockIdx.x, part = 0, kh = blockIdx.y, b = blockIdx.z;
+  const bool divided = id >= a.whole;
+  if (divided) id -= a.whole, part = id % a.n_parts, id = a.whole + id / a.n_parts;
+  if (a.whole > 0) kh = id / a.n_tiles % a.kv_heads, b = id / a.n_tiles / a.kv_heads, id %= a.n_tiles;
+  const int tile0 = (a.n_tiles - 1 - id) * kCtaRows;
   griddep_wait();
   griddep_launch();
   int row0, rows, keys;
@@ -102,9 +117,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tiles_kernel(KvAtt a) {
   const int last = min(tile0 + kCtaRows, n_rows) - 1;
   int p0, p1;
   kv_pages(a, group_of(a, tile0), group_of(a, last), rows, keys, p0, p1);
-  const int n_act = (p1 - p0 + a.part_pages - 1) / a.part_pages;
+  const int part_pages = divided ? a.part_pages : max(p1 - p0, 1);
+  const int n_act = (p1 - p0 + part_pages - 1) / part_pages;
   if (part > 0 && part >= n_act) return;
-  const int pb = p0 + part * a.part_pages, pe = min(pb + a.part_pages, p1);
+  const int pb = p0 + part * part_pages, pe = min(pb + part_pages, p1);
   const int key0 = pb * kPage;
   const int n_it = (pe - pb + 1) / 2;  // key tiles
   // turns: no second tile of rows, so that place 0 takes the even key tiles of
@@ -122,7 +138,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tiles_kernel(KvAtt a) {
     }
     for (int s = 0; s < kStages; ++s) {
       tc::mbar_init(&k_full[s], 4);               // warps
-      tc::mbar_init(&v_full[s], kFp4 ? 4 : 32);   // warps; or lanes of the one that copies
+      tc::mbar_init(&v_full[s], kCodes ? 4 : 32);  // warps; or lanes of the one that copies
       tc::mbar_init(&k_free[s], 1);
       tc::mbar_init(&v_free[s], 1);
     }
@@ -454,7 +470,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tiles_kernel(KvAtt a) {
   } else if (warp < kProductWarp) {
     regs_dec<kDecodeRegs>();
     const int ring = turns ? kLongRing : kRing;
-    if (kFp4) {
+    if (kCodes) {
       // -------------------------------------------------------- decoding --
       // a row of each tile for each thread: warps 8-11 keys, 12-15 values
       constexpr int W = D / 32;  // 16-byte pieces of a row
@@ -519,6 +535,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tiles_kernel(KvAtt a) {
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
           const int pg = pb + 2 * it + x;
+          if constexpr (kPlain) {
+            at[x] = pg < pe ? (((int64_t)b * a.plain_pages + pg) * a.kv_heads + kh) * kv_block_bytes(D, false) : -1;
+            continue;
+          }
           const int32_t page = pg < pe ? __ldg(table + pg) : -1;
           const bool there = page >= 0 && page < a.c.num_pages;
           if (pg < pe && !there && lane == 0) report(a.status, CSA2_ERR_BAD_PAGE);
@@ -526,9 +546,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tiles_kernel(KvAtt a) {
         }
         // Scores of keys that are not seen are never used, but values are
         // multiplied by weight 0: what lies in slots from kv_len on (anything) and
-        // in the place of a page outside the pool has to be 0.
+        // in the place of a page outside the pool has to be 0 (and is in plain pages).
         const int live = keys - key0 - it * kTileKeys;
-        const bool tail = v && live < kTileKeys && (live < kPage ? at[0] : at[1]) >= 0;
+        const bool tail = !kPlain && v && live < kTileKeys && (live < kPage ? at[0] : at[1]) >= 0;
         uint64_t* bar = tail ? &tail_full : &full[s];
         if (lane == 0) tc::mbar_arrive_expect_tx(bar, ((at[0] >= 0) + (at[1] >= 0)) * (L::kOperand / (v ? 2 : 8)));
         __syncwarp();
@@ -537,13 +557,14 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tiles_kernel(KvAtt a) {
           for (int x = 0; x < 2; ++x) {
             if (at[x] < 0) continue;
             if (v) {
-              tc::bulk_g2s(dst + x * (L::kOperand / 2), a.c.v + at[x], L::kOperand / 2, bar);
+              tc::bulk_g2s(dst + x * (L::kOperand / 2), (kPlain ? a.plain_v : a.c.v) + at[x], L::kOperand / 2, bar);
               continue;
             }
 #pragma unroll
             for (int y = 0; y < D / 32; ++y) {
               const int c = (warp - kKeyWarp) * (D / 32) + y;
-              tc::bulk_g2s(dst + c * kChunk + x * (kPage * 16), a.c.k + at[x] + c * (kPage * 16), kPage * 16, bar);
+              tc::bulk_g2s(dst + c * kChunk + x * (kPage * 16), (kPlain ? a.plain_k : a.c.k) + at[x] + c * (kPage * 16),
+                           kPage * 16, bar);
             }
           }
         }
@@ -562,8 +583,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tiles_kernel(KvAtt a) {
             if (!ok) break;
             clear(live, live < kPage ? kPage : kTileKeys);
           }
-          if (at[0] < 0) clear(0, kPage);
-          if (at[1] < 0 && pb + 2 * it + 1 < pe) clear(kPage, kTileKeys);
+          if (!kPlain && at[0] < 0) clear(0, kPage);
+          if (!kPlain && at[1] < 0 && pb + 2 * it + 1 < pe) clear(kPage, kTileKeys);
           if (lane != 0 || tail) tc::mbar_arrive(&full[s]);
         }
       }
@@ -578,7 +599,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tiles_kernel(KvAtt a) {
       constexpr uint32_t kIdS = tc::idesc_f16(128, kTileKeys, !kFp4, !kFp4, false, false);
       constexpr uint32_t kIdO = tc::idesc_f16(128, D, !kFp4, !kFp4, false, true);
       // values decoded: 128 keys of a chunk together; copied: 64, a page after the other
-      constexpr uint32_t kHiK = tc::sdesc_hi(128), kHiV = tc::sdesc_hi(kFp4 ? kChunk : kChunk / 2);
+      constexpr uint32_t kHiK = tc::sdesc_hi(128), kHiV = tc::sdesc_hi(kCodes ? kChunk : kChunk / 2);
       constexpr uint32_t kTile16 = L::kOperand / 16;
       static_assert(kStages == 2, "the loops below go over two key tiles");
       // Place and stage are compile-time numbers, the descriptors' low words formed
@@ -608,7 +629,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tiles_kernel(KvAtt a) {
 #pragma unroll
           for (int ks = 1; ks < kTileKeys / 16; ++ks) {
             if (ks >= kPage / 16 && half) break;
-            tc::mma_ts_lo(tb + 256 + D * j(), tb + 128 * j() + 8 * ks, v_lo + s() * kTile16 + ks * (256 / 16) + (kFp4 || ks < kPage / 16 ? 0 : kTile16 / 2 - kPage),
+            tc::mma_ts_lo(tb + 256 + D * j(), tb + 128 * j() + 8 * ks, v_lo + s() * kTile16 + ks * (256 / 16) + (kCodes || ks < kPage / 16 ? 0 : kTile16 / 2 - kPage),
                           kHiV, kIdO,
                           1u);
           }
@@ -675,7 +696,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tiles_kernel(KvAtt a) {
         __syncwarp();
         tc::mbar_wait(&drained, 0);
       }
-    } else if (kFp4 && (warp == kFetchWarp || warp == kFetchWarp + 1)) {
+    } else if (kCodes && (warp == kFetchWarp || warp == kFetchWarp + 1)) {
       // ---------------- pages into the ring (K, V, K ..), a warp for each --
       const bool v = warp != kFetchWarp;
       int32_t id[2], next[2] = {-1, -1};
@@ -732,45 +753,113 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tiles_kernel(KvAtt a) {
   if (warp == kProductWarp) tc::tmem_dealloc(tb, 512);
 }
 
-template <int D, bool kFp4>
+// The FP4 pages that a sequence's rows see, as f16 in a BF16 page's order; slots from
+// kv_len on and pages outside the pool are 0.  A CTA for a page and kv head: four (two)
+// threads a key, 32 channels each, read neighbouring 16 bytes and write neighbouring 16
+// bytes of eight (16) keys.
+template <int D>
+__global__ void __launch_bounds__(256) kv_decode_kernel(KvAtt a) {
+  griddep_wait();
+  griddep_launch();
+  const int pg = blockIdx.x, kh = blockIdx.y, b = blockIdx.z;
+  int row0, rows, keys, p0, p1;
+  if (!kv_sequence(a, b, row0, rows, keys) || rows == 0) return;
+  kv_pages(a, 0, rows - 1, rows, keys, p0, p1);
+  if (pg < p0 || pg >= p1) return;
+  const int32_t page = __ldg(a.c.table + (int64_t)b * a.c.max_pages + pg);
+  const bool there = page >= 0 && page < a.c.num_pages;
+  if (!there && threadIdx.x == 0) report(a.status, CSA2_ERR_BAD_PAGE);
+  constexpr int W = D / 32;  // 16-byte pieces of a key
+  const int64_t block = (int64_t)page * a.kv_heads + kh;
+  const int64_t to = (((int64_t)b * a.plain_pages + pg) * a.kv_heads + kh) * kv_block_bytes(D, false);
+#pragma unroll
+  for (int i0 = 0; i0 < 2 * kPage * W; i0 += 256) {
+    const int i = i0 + threadIdx.x, piece = i % W, key = i / W % kPage;
+    const bool v = i >= kPage * W;
+    uint4 w = make_uint4(0, 0, 0, 0);
+    uint32_t sc = 0;
+    if (there && pg * kPage + key < keys) {
+      w = __ldg(reinterpret_cast<const uint4*>((v ? a.c.v : a.c.k) + block * kv_block_bytes(D, true) + key * (D / 2)) + piece);
+      sc = scales2(__ldg(reinterpret_cast<const uint16_t*>((v ? a.c.vs : a.c.ks) + block * kv_scale_bytes(D) + key * (D / 16)) + piece));
+    }
+    uint8_t* dst = (v ? a.plain_v : a.plain_k) + to + (4 * piece * kPage + key) * 16;
+    const uint32_t c[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int y = 0; y < 4; ++y) {
+      uint32_t h[4];
+      codes8(c[y], h);
+      const uint32_t one = __byte_perm(sc, 0, y < 2 ? 0x1010u : 0x3232u);
+      *reinterpret_cast<uint4*>(dst + y * (kPage * 16)) =
+          make_uint4(mul2(h[0], one), mul2(h[1], one), mul2(h[2], one), mul2(h[3], one));
+    }
+  }
+}
+
+template <int D, bool kFp4, bool kPlain>
 cudaError_t launch(int B, const KvAtt& a, cudaStream_t stream) {
-  auto kern = kv_tiles_kernel<D, kFp4>;
+  auto kern = kv_tiles_kernel<D, kFp4, kPlain>;
   static bool done[64];
-  const cudaError_t e = allow_smem(kern, Tiles<D>::kSmem, done);
+  cudaError_t e = allow_smem(kern, Tiles<D>::kSmem, done);
   if (e != cudaSuccess) return e;
-  const int64_t tiles = ((int64_t)a.max_q * a.group + kCtaRows - 1) / kCtaRows;
-  return launch_k(kern, dim3((unsigned)(tiles * a.n_parts), a.kv_heads, B), dim3(kThreads), Tiles<D>::kSmem, stream, 0, a);
+  if constexpr (kPlain) {
+    e = launch_k(kv_decode_kernel<D>, dim3(a.plain_pages, a.kv_heads, B), dim3(256), 0, stream, 0, a);
+    if (e != cudaSuccess) return e;
+  }
+  const dim3 grid = a.whole > 0 ? dim3(a.whole + ((unsigned)a.n_tiles * a.kv_heads * B - a.whole) * a.n_parts)
+                                : dim3((unsigned)a.n_tiles * a.n_parts, a.kv_heads, B);
+  return launch_k(kern, grid, dim3(kThreads), Tiles<D>::kSmem, stream, 0, a);
 }
 
 }  // namespace
 
-void kv_tiles_plan(const csa2_kv_cfg& cfg, int B, int max_q, int64_t max_kv, bool cross, int most_parts, int* n_parts,
-                   int* part_pages) {
+KvPlan kv_tiles_plan(const csa2_kv_cfg& cfg, int B, int max_q, int64_t max_kv, bool cross, int most_parts) {
   const int group = cfg.n_heads / cfg.kv_heads;
-  const int64_t tiles = ((int64_t)max_q * group + kCtaRows - 1) / kCtaRows;
+  const int64_t rows = (int64_t)max_q * group, tiles = (rows + kCtaRows - 1) / kCtaRows;
   int64_t pages = (max_kv + kPage - 1) / kPage;
   if (cfg.window && !cross)
     pages = std::min<int64_t>(pages, ((int64_t)cfg.window + std::min<int64_t>(max_q, kCtaRows / group + 2) + kPage - 2) / kPage + 1);
   const int64_t steps = std::max<int64_t>(1, (pages + 1) / 2), base = B * cfg.kv_heads * tiles, slots = num_sms();
-  // the number of parts whose waves of CTAs end soonest; a CTA's start and end
-  // cost about three key tiles, joining about two
-  int64_t best = 1;
+  // The number of parts whose waves of CTAs end soonest, in key tiles: a CTA's start
+  // and end cost about three, the joining kernel two and its reading two and a half
+  // for each CTA of an SM.  Divided are all row tiles, or those of the last wave, if
+  // it wins 3 %: 2048 tokens on 16384 (64 over 8 heads of 128, FP4; 512 tiles, the
+  // last 56 in five parts) take 733 us so and 797 us whole, three such sequences of
+  // 512 tokens 628 and 665.
+  const double read = 2.5 * std::min<int64_t>(rows, kCtaRows) / kCtaRows / slots;
+  int64_t best = 1, whole = 0;
   double cost = 1e30;
-  for (int64_t s = 1; s <= most_parts && s <= 64; ++s) {
+  for (int64_t s = 1; s <= std::max(most_parts, 1) && s <= 64; ++s) {
     const int64_t n = (steps + s - 1) / s;
     if (s > 1 && n < 2) break;
-    const double c = (double)((base * s + slots - 1) / slots) * (n + 3) + (s > 1 ? 2 : 0);
-    if (c < cost * 0.999) cost = c, best = s;
+    for (const int64_t w : {(int64_t)0, base / slots * slots}) {
+      const int64_t rest = base - w;
+      if (w && (s == 1 || rest == 0)) continue;
+      const double c = (double)(w / slots) * (steps + 3) + (double)((rest * s + slots - 1) / slots) * (n + 3) +
+                       (s > 1 ? 2 + read * rest * s : 0);
+      if (c < cost * 0.999) cost = s == 1 ? 0.97 * c : c, best = s, whole = w;
+    }
   }
-  const int64_t per = (steps + best - 1) / best;
-  *part_pages = (int)(2 * per);
-  *n_parts = (int)((steps + per - 1) / per);
+  const int64_t per = (steps + best - 1) / best, parts = (steps + per - 1) / per;
+  if (parts == 1) whole = 0;
+  const int64_t ctas = whole + (base - whole) * std::max<int64_t>(parts, parts > 1 ? kCtaRows / 8 : 1);
+  return KvPlan{(int)parts, (int)(2 * per), false, (int)std::min<int64_t>(whole, INT32_MAX), ctas};
 }
 
 cudaError_t launch_kv_tiles(const csa2_kv_cfg& cfg, int B, const KvAtt& a, cudaStream_t stream) {
-  const bool fp4 = cfg.cache_dtype == CSA2_CACHE_FP4;
-  if (cfg.head_dim == 128) return fp4 ? launch<128, true>(B, a, stream) : launch<128, false>(B, a, stream);
-  return fp4 ? launch<64, true>(B, a, stream) : launch<64, false>(B, a, stream);
+  const bool fp4 = cfg.cache_dtype == CSA2_CACHE_FP4, plain = a.plain_k != nullptr;
+  if (cfg.head_dim == 128)
+    return !fp4 ? launch<128, false, false>(B, a, stream) : plain ? launch<128, true, true>(B, a, stream)
+                                                                  : launch<128, true, false>(B, a, stream);
+  return !fp4 ? launch<64, false, false>(B, a, stream) : plain ? launch<64, true, true>(B, a, stream)
+                                                               : launch<64, true, false>(B, a, stream);
+}
+
+size_t kv_plain_bytes(const csa2_kv_cfg& cfg, int B, int max_q, int64_t max_kv, bool cross) {
+  if (cfg.cache_dtype != CSA2_CACHE_FP4) return 0;
+  const int64_t seen = cfg.window && !cross ? std::min(max_q, cfg.window) : max_q;
+  if (seen * (cfg.n_heads / cfg.kv_heads) < kPlainRows) return 0;
+  const size_t bytes = (size_t)B * ((max_kv + kPage - 1) / kPage) * cfg.kv_heads * 2 * kv_block_bytes(cfg.head_dim, false);
+  return bytes <= kMostPlain ? bytes : 0;
 }
 
 int kv_tiles_rows() { return kCtaRows; }

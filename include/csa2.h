@@ -436,9 +436,10 @@ CSA2_API int32_t csa2_kv_append(const csa2_kv_cfg* cfg, int32_t B, int32_t T, co
                                 uint16_t* v_out, int32_t* status, void* stream);
 
 /* Workspace bytes with which csa2_kv_attend and csa2_kv_cross_attend divide
- * the keys of these sizes among CTAs as they would best (0 where that needs
- * none); they take any workspace (NULL included) and divide less where it is
- * smaller.  Its contents need not be kept between calls.  Two calls that may
+ * the keys of these sizes among CTAs, and decode FP4 pages that many rows read
+ * once ahead, as they would best (0 where that needs none); they take any
+ * workspace (NULL included) and do less of it where it is smaller: outputs may
+ * then differ by the order of fp32 sums.  Its contents need not be kept between calls.  Two calls that may
  * overlap (other streams, graphs replayed at once) need workspaces of their
  * own. */
 CSA2_API size_t csa2_kv_workspace_bytes(const csa2_kv_cfg* cfg, int32_t B, int32_t T, int32_t max_q, int32_t max_kv);

@@ -288,6 +288,47 @@ def test_long_keys_divided_or_not(dtype, dim, hq, hkv, nq, workspace):
     _attend_case(csa.KVCfg(hq, hkv, dim, dtype), [nq, nq], [6007, 1500], seed=nq, workspace=workspace)
 
 
+@pytest.mark.parametrize("dim,hq,hkv,window", [(128, 64, 2, 0), (64, 32, 1, 0), (128, 64, 1, 60), (128, 64, 1, 70)])
+@pytest.mark.parametrize("cross", [False, True])
+def test_pages_decoded_ahead_or_in_passing(dim, hq, hkv, window, cross):
+    # the products' operands and their order are the same: every bit is
+    rng = np.random.default_rng(dim + window)
+    cfg = csa.KVCfg(hq, hkv, dim, FP4, window=0 if cross else window)
+    nq, kv = [150, 0, 1, 40, 65], [333, 90, 77, 20, 0]
+    B, T, mq, mk = len(nq), sum(nq), 150, 400
+    cache = _cache(cfg, B, mk)
+    _noise(cache)
+    for b, n in enumerate(kv):
+        for kind in "kv":
+            if n:
+                _kv.fill(cache, cfg, b, kind, _kv.normal(rng, n, hkv, dim))
+    cache.block_table[0, 4] = 10 ** 6  # one page is not there
+    q = _dev(_kv.normal(rng, T, hq, dim))
+    cu, lens = _cu(nq), torch.tensor(kv, dtype=torch.int32, device="cuda")
+    call, pages = csa.kv_cross_attend if cross else csa.kv_attend, 2 * B * 7 * hkv * 64 * dim * 2
+    ahead = cross or window != 60  # 60 x 64 rows read a key: fewer than 4096
+    assert csa.kv_workspace_bytes(cfg, B, T, mq, mk) >= (pages if ahead else 0)
+    got = []
+    for n in (0, pages):
+        ws = torch.full((n,), 255, dtype=torch.uint8, device="cuda") if n else None
+        out, lse, st = torch.full_like(q, 7.0), torch.full((T, hq), 7.0, device="cuda"), _status()
+        call(cfg, q, cu, cache, lens, mq, mk, out, lse=lse, workspace=ws, status=st)
+        assert int(st.item()) == 16
+        got.append((out, lse))
+    assert not ahead or bool((ws != 255).any())
+    assert torch.isfinite(got[0][0].float()).all()
+    if ahead:
+        assert torch.equal(got[0][0], got[1][0]) and torch.equal(got[0][1], got[1][1])
+
+
+@pytest.mark.parametrize("dtype", [FP4, BF16])
+def test_last_wave_of_row_tiles_divided(dtype):
+    # 208 and 224 row tiles: the last 56 and 72 with their keys in parts
+    cfg = csa.KVCfg(256, 16, 64, dtype)
+    _attend_case(cfg, [208], [2700], seed=5)
+    _attend_case(cfg, [97, 111], [1500, 2700], seed=6, capture=True)
+
+
 @pytest.mark.parametrize("dtype", [FP4, BF16])
 def test_pages_of_all_last_lengths(dtype):
     # the last page of a tile alone, full, and ending at every kind of place, for one row, few and many

@@ -82,10 +82,25 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
 __host__ __device__ constexpr int kv_block_bytes(int dim, bool fp4) { return fp4 ? kPage * dim / 2 : kPage * dim * 2; }
 __host__ __device__ constexpr int kv_scale_bytes(int dim) { return kPage * dim / 16; }
 
+// n / d for 0 <= n < 2^31 without a division (several hundred cycles at a CTA's
+// start): with s = ceil(log2 d) and m = floor(2^(31 + s) / d) + 1 the error of
+// n m / 2^(31 + s) is below n / 2^(31 + s) < 1 / d.
+struct Divisor {
+  uint32_t mul, shift;
+};
+inline Divisor divisor(int d) {
+  uint32_t s = 0;
+  while ((1ll << s) < d) ++s;
+  return {(uint32_t)((1ull << (31 + s)) / d + 1), 31 + s};
+}
+__device__ __forceinline__ int quotient(int n, const Divisor& d) {
+  return (int)(((uint64_t)(uint32_t)n * d.mul) >> d.shift);
+}
+
 // Arguments of an attention call.
 struct KvAtt {
-  int T, n_heads, kv_heads, group, window, causal, max_q;
-  uint32_t group_mul, group_shift;  // n / group = n * group_mul >> group_shift for 0 <= n < 2^31
+  int B, T, n_heads, kv_heads, group, window, causal, max_q;
+  Divisor by_group, by_heads, by_parts, by_pages;  // group, kv_heads, n_parts, part_pages
   int max_kv;
   const uint16_t* q;
   int64_t q_stride;
@@ -101,9 +116,9 @@ struct KvAtt {
   // log2-sum-exp2 to part_l [n_parts][T * n_heads]
   int n_parts, part_pages;
   int cluster;  // the parts of a head join in a cluster instead
-  // row tiles of a sequence and kv head; tiles of the call, in the order of their
-  // CTAs, that are not divided
-  int n_tiles, whole;
+  // (tile kernel) most row tiles, of all kv heads; how many, in the order of their
+  // CTAs, are not divided
+  int tiles, whole;
   float* part_o;
   float* part_l;
   // FP4 pages decoded for this call: page p of sequence b and a kv head as f16 in a
@@ -114,11 +129,7 @@ struct KvAtt {
   int32_t* status;
 };
 
-// n / group for 0 <= n < 2^31: with s = ceil(log2 group) and m = floor(2^(31 + s) /
-// group) + 1 the error of n m / 2^(31 + s) is below n / 2^(31 + s) < 1 / group.
-__device__ __forceinline__ int group_of(const KvAtt& a, int n) {
-  return (int)(((uint64_t)(uint32_t)n * a.group_mul) >> a.group_shift);
-}
+__device__ __forceinline__ int group_of(const KvAtt& a, int n) { return quotient(n, a.by_group); }
 
 // Rows and keys of sequence b; false (status set) when they are out of bounds.
 __device__ __forceinline__ bool kv_sequence(const KvAtt& a, int b, int& row0, int& rows, int& keys) {
@@ -131,6 +142,62 @@ __device__ __forceinline__ bool kv_sequence(const KvAtt& a, int b, int& row0, in
   rows = hi - lo;
   keys = n;
   return true;
+}
+
+// The id-th row tile of the call: sequences in order, their kv heads, of each the
+// tiles from the last (the longest) on.  Sequences have what tiles their rows fill, so
+// that a batch of one prompt and many single tokens is not a grid of empty CTAs (4096
+// tokens and 63 single ones, 64 over 8 heads of 128: 792 us with the longest's tiles
+// for each, 377 so; four prompts of 700 .. 1500: 132 and 134).  The whole warp; false behind the last tile; sequences out of bounds have none (status set).
+__device__ __forceinline__ bool kv_tile(const KvAtt& a, int tile_rows, int id, int& b, int& kh, int& tile) {
+  const int lane = threadIdx.x & 31, want = quotient(id, a.by_heads);
+  int before = 0;  // tiles of a kv head so far
+  for (int b0 = 0; b0 < a.B; b0 += 128) {  // four sequences a lane
+    int n[4], lo = 0;
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+      const int s = b0 + 4 * lane + x;
+      n[x] = 0;
+      if (s < a.B) {
+        if (x == 0) lo = __ldg(a.cu + s);
+        const int hi = __ldg(a.cu + s + 1), keys = __ldg(a.kv_len + s);
+        if (lo < 0 || hi < lo || hi > a.T || hi - lo > a.max_q || keys < 0 || keys > a.max_kv)
+          report(a.status, CSA2_ERR_BAD_INDEX);
+        else n[x] = ((hi - lo) * a.group + tile_rows - 1) / tile_rows;
+        lo = hi;
+      }
+    }
+    const int own = n[0] + n[1] + n[2] + n[3];
+    int upto = own;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, upto, d);
+      if (lane >= d) upto += v;
+    }
+    upto += before;
+    const uint32_t past = __ballot_sync(0xffffffffu, upto > want);
+    if (past) {
+      int first = upto - own, s = b0 + 4 * lane, count = n[0];
+#pragma unroll
+      for (int x = 1; x < 4; ++x)
+        if (want >= first + count) first += count, count = n[x], ++s;
+      // from the first lane past it; a reduction, so that the compiler knows the
+      // numbers as the warp's, not the lanes'
+      const bool own_it = lane == __ffs(past) - 1;
+      b = __reduce_max_sync(0xffffffffu, own_it ? s : 0), first = __reduce_max_sync(0xffffffffu, own_it ? first : 0);
+      count = __reduce_max_sync(0xffffffffu, own_it ? count : 0);
+      const int at = id - first * a.kv_heads;
+      if ((unsigned)at >= (unsigned)(count * a.kv_heads)) return false;  // rows counted twice (bad cu) past 2^31
+      kh = (int)__fdividef((float)at, (float)count);  // at / count, off by one at most
+      int rest = at - kh * count;
+      if (rest < 0) --kh, rest += count;
+      if (rest >= count) ++kh, rest -= count;
+      tile = count - 1 - rest;
+      return true;
+    }
+    before = __shfl_sync(0xffffffffu, upto, 31);
+  }
+  return false;
 }
 
 // Position up to which (exclusive) row `i` of `rows` sees keys, and from which.
@@ -152,6 +219,11 @@ __device__ __forceinline__ void kv_pages(const KvAtt& a, int i0, int i1, int row
   p1 = hi > lo ? (hi + kPage - 1) / kPage : p0;
 }
 
+// Parts of pages [p0, p1).
+__device__ __forceinline__ int kv_parts(const KvAtt& a, int p0, int p1) {
+  return quotient(p1 - p0 + a.part_pages - 1, a.by_pages);
+}
+
 cudaError_t launch_kv_append(const csa2_kv_cfg& cfg, int B, int T, const uint16_t* q, int64_t q_stride,
                              const uint16_t* k, int64_t k_stride, const uint16_t* v, int64_t v_stride,
                              const int32_t* cu, const int64_t* pos0, const float* rope, int64_t rope_rows,
@@ -163,10 +235,10 @@ cudaError_t launch_kv_append(const csa2_kv_cfg& cfg, int B, int T, const uint16_
 struct KvPlan {
   int n_parts, part_pages;
   bool cluster;  // the parts join in a cluster, without workspace
-  int whole;     // row tiles that are not divided (tile kernel)
-  int64_t ctas;  // of the tile kernel or its joining kernel, whichever has more, or above
+  int64_t tiles, whole;  // (tile kernel) row tiles of all kv heads, those that are not divided
+  int64_t ctas;          // (tile kernel) of it or of the joining kernel, whichever has more
 };
-KvPlan kv_plan(const csa2_kv_cfg& cfg, int B, int max_q, int max_kv, bool cross, int most_parts);
+KvPlan kv_plan(const csa2_kv_cfg& cfg, int B, int T, int max_q, int max_kv, bool cross, int most_parts);
 
 // Let `kern` use `bytes` of dynamic shared memory: set once on each device.
 template <typename K>
@@ -182,10 +254,10 @@ cudaError_t allow_smem(K kern, int bytes, bool (&done)[64]) {
 // The plan of the tile kernel, which takes more rows of a kv head than kMostRows;
 // its launch, and the rows of its CTA.
 constexpr int kMostRows = 32;
-KvPlan kv_tiles_plan(const csa2_kv_cfg& cfg, int B, int max_q, int64_t max_kv, bool cross, int most_parts);
+KvPlan kv_tiles_plan(const csa2_kv_cfg& cfg, int B, int T, int max_q, int64_t max_kv, bool cross, int most_parts);
 cudaError_t launch_kv_tiles(const csa2_kv_cfg& cfg, int B, const KvAtt& a, cudaStream_t stream);
 // Bytes of the keys decoded for a call, or 0 where they are decoded in passing.
-size_t kv_plain_bytes(const csa2_kv_cfg& cfg, int B, int max_q, int64_t max_kv, bool cross);
+size_t kv_plain_bytes(const csa2_kv_cfg& cfg, int B, int T, int max_q, int64_t max_kv, bool cross);
 int kv_tiles_rows();
 
 cudaError_t launch_kv_attend(const csa2_kv_cfg& cfg, int B, KvAtt& a, cudaStream_t stream);

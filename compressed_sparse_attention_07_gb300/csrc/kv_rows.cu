@@ -104,7 +104,7 @@ __global__ void __launch_bounds__(Rows<D, kFp4, NT, kCluster>::kWarps * 32, Rows
   const int last = min(tile0 + kRows, n_rows) - 1;
   int p0, p1;
   kv_pages(a, group_of(a, tile0), group_of(a, last), rows, keys, p0, p1);
-  const int n_act = (p1 - p0 + a.part_pages - 1) / a.part_pages;
+  const int n_act = kv_parts(a, p0, p1);
   if (!kCluster && part > 0 && part >= n_act) return;
   const int pb = min(p0 + part * a.part_pages, p1), pe = min(pb + a.part_pages, p1);
   const int key_end = kv_hi(a, group_of(a, last), rows, keys);  // no row sees keys from here on
@@ -551,12 +551,13 @@ __global__ void __launch_bounds__(Rows<D, kFp4, NT, kCluster>::kWarps * 32, Rows
 // Joins the parts of each row of the divided tiles: out = sum 2^(l_p - l) o_p, one
 // warp a row.
 template <int D>
-__global__ void __launch_bounds__(256) kv_join_kernel(KvAtt a, int tile_rows) {
+__global__ void __launch_bounds__(256) kv_join_kernel(KvAtt a, int tile_rows, int per) {
   griddep_wait();
   griddep_launch();
-  const int lane = threadIdx.x & 31, per = tile_rows / 8, id = a.whole + blockIdx.x / per;
-  const int kh = id / a.n_tiles % a.kv_heads, b = id / a.n_tiles / a.kv_heads;
-  const int tile0 = (a.n_tiles - 1 - id % a.n_tiles) * tile_rows;
+  const int lane = threadIdx.x & 31, id = a.whole + blockIdx.x / per;  // per: CTAs of a tile
+  int b = id / a.kv_heads, kh = id % a.kv_heads, tile = 0;  // kv_rows_kernel has one tile
+  if (tile_rows > kMostRows && !kv_tile(a, tile_rows, id, b, kh, tile)) return;
+  const int tile0 = tile * tile_rows;
   int row0, rows, keys;
   if (!kv_sequence(a, b, row0, rows, keys)) return;
   const int r = tile0 + blockIdx.x % per * 8 + threadIdx.x / 32;
@@ -565,7 +566,7 @@ __global__ void __launch_bounds__(256) kv_join_kernel(KvAtt a, int tile_rows) {
   const int last = min(tile0 + tile_rows, rows * a.group) - 1;
   int p0, p1;
   kv_pages(a, group_of(a, tile0), group_of(a, last), rows, keys, p0, p1);
-  const int n = (p1 - p0 + a.part_pages - 1) / a.part_pages;
+  const int n = kv_parts(a, p0, p1);
   if (n <= 1) return;
   const int64_t at = (int64_t)(row0 + i) * a.n_heads + h, step = (int64_t)a.T * a.n_heads;
   // The outputs of eight parts are on their way while the maximum is formed, and of
@@ -661,10 +662,10 @@ int row_blocks(int64_t n) { return n <= 8 ? 1 : n <= 16 ? 2 : 4; }
 
 }  // namespace
 
-KvPlan kv_plan(const csa2_kv_cfg& cfg, int B, int max_q, int max_kv, bool cross, int most_parts) {
+KvPlan kv_plan(const csa2_kv_cfg& cfg, int B, int T, int max_q, int max_kv, bool cross, int most_parts) {
   const int group = cfg.n_heads / cfg.kv_heads;
-  if ((int64_t)max_q * group > kMostRows) return kv_tiles_plan(cfg, B, max_q, max_kv, cross, most_parts);
-  KvPlan plan = {1, 1, false, 0, 0};
+  if ((int64_t)max_q * group > kMostRows) return kv_tiles_plan(cfg, B, T, max_q, max_kv, cross, most_parts);
+  KvPlan plan = {1, 1, false, 0, 0, 0};
   const int nt = row_blocks((int64_t)max_q * group);
   const int64_t tiles = ((int64_t)max_q * group + 8 * nt - 1) / (8 * nt);
   int64_t pages = ((int64_t)max_kv + kPage - 1) / kPage;
@@ -707,15 +708,15 @@ cudaError_t launch_kv_attend(const csa2_kv_cfg& cfg, int B, KvAtt& a, cudaStream
   const int nt = row_blocks((int64_t)a.max_q * a.group);
   const bool fp4 = cfg.cache_dtype == CSA2_CACHE_FP4, many = (int64_t)a.max_q * a.group > kMostRows;
   const int tile_rows = many ? kv_tiles_rows() : 8 * nt;
-  a.n_tiles = (int)(((int64_t)a.max_q * a.group + tile_rows - 1) / tile_rows);
   cudaError_t e;
   if (many) e = launch_kv_tiles(cfg, B, a, stream);
   else if (cfg.head_dim == 128) e = fp4 ? launch_rows<128, true>(nt, B, a, stream) : launch_rows<128, false>(nt, B, a, stream);
   else e = fp4 ? launch_rows<64, true>(nt, B, a, stream) : launch_rows<64, false>(nt, B, a, stream);
   if (e != cudaSuccess || a.n_parts <= 1 || a.cluster) return e;
-  const unsigned grid = ((unsigned)B * a.kv_heads * a.n_tiles - a.whole) * (tile_rows / 8);
-  return cfg.head_dim == 128 ? launch_k(kv_join_kernel<128>, dim3(grid), dim3(256), 0, stream, 0, a, tile_rows)
-                             : launch_k(kv_join_kernel<64>, dim3(grid), dim3(256), 0, stream, 0, a, tile_rows);
+  const int per = (int)(std::min<int64_t>(tile_rows, (int64_t)a.max_q * a.group) + 7) / 8;
+  const unsigned grid = (many ? a.tiles - a.whole : (unsigned)B * a.kv_heads) * per;
+  return cfg.head_dim == 128 ? launch_k(kv_join_kernel<128>, dim3(grid), dim3(256), 0, stream, 0, a, tile_rows, per)
+                             : launch_k(kv_join_kernel<64>, dim3(grid), dim3(256), 0, stream, 0, a, tile_rows, per);
 }
 
 }  // namespace csa2

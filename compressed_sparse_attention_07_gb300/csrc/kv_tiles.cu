@@ -60,7 +60,7 @@ struct Tiles {
   }
 };
 
-// Rows that read a key from which FP4 pages are decoded once for the call, into the
+// Rows that read a key (of a sequence of mean length) from which FP4 pages are decoded once for the call, into the
 // workspace (up to kMostPlain bytes of it).  Decoding in every CTA takes issue slots
 // from the softmax beside it; ahead, a write and reads from L2.  64 over 8 heads of
 // 128 on 16384 keys, in passing / ahead: 256 tokens (2048 rows) 152 / 157 us, 512
@@ -101,24 +101,24 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tiles_kernel(KvAtt a) {
   __shared__ float half_m[2][kTileRows], half_l[2][kTileRows];
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  // row tile (the longest first), kv head, sequence and part; with undivided tiles
-  // ahead of the divided ones all in one dimension of the grid
-  int id = blockIdx.x, part = 0, kh = blockIdx.y, b = blockIdx.z;
+  int id = blockIdx.x, part = 0, kh, b, tile;
   const bool divided = id >= a.whole;
-  if (divided) id -= a.whole, part = id % a.n_parts, id = a.whole + id / a.n_parts;
-  if (a.whole > 0) kh = id / a.n_tiles % a.kv_heads, b = id / a.n_tiles / a.kv_heads, id %= a.n_tiles;
-  const int tile0 = (a.n_tiles - 1 - id) * kCtaRows;
+  if (divided) {
+    const int x = id - a.whole, q = quotient(x, a.by_parts);
+    part = x - q * a.n_parts, id = a.whole + q;
+  }
   griddep_wait();
   griddep_launch();
+  if (!kv_tile(a, kCtaRows, id, b, kh, tile)) return;
+  const int tile0 = tile * kCtaRows;
   int row0, rows, keys;
   if (!kv_sequence(a, b, row0, rows, keys)) return;
   const int n_rows = rows * a.group;
-  if (tile0 >= n_rows) return;
   const int last = min(tile0 + kCtaRows, n_rows) - 1;
   int p0, p1;
   kv_pages(a, group_of(a, tile0), group_of(a, last), rows, keys, p0, p1);
-  const int part_pages = divided ? a.part_pages : max(p1 - p0, 1);
-  const int n_act = (p1 - p0 + part_pages - 1) / part_pages;
+  const int part_pages = divided ? a.part_pages : p1 - p0;
+  const int n_act = divided ? kv_parts(a, p0, p1) : 1;
   if (part > 0 && part >= n_act) return;
   const int pb = p0 + part * part_pages, pe = min(pb + part_pages, p1);
   const int key0 = pb * kPage;
@@ -805,20 +805,21 @@ cudaError_t launch(int B, const KvAtt& a, cudaStream_t stream) {
     e = launch_k(kv_decode_kernel<D>, dim3(a.plain_pages, a.kv_heads, B), dim3(256), 0, stream, 0, a);
     if (e != cudaSuccess) return e;
   }
-  const dim3 grid = a.whole > 0 ? dim3(a.whole + ((unsigned)a.n_tiles * a.kv_heads * B - a.whole) * a.n_parts)
-                                : dim3((unsigned)a.n_tiles * a.n_parts, a.kv_heads, B);
+  const dim3 grid(a.whole + (unsigned)(a.tiles - a.whole) * a.n_parts);
   return launch_k(kern, grid, dim3(kThreads), Tiles<D>::kSmem, stream, 0, a);
 }
 
 }  // namespace
 
-KvPlan kv_tiles_plan(const csa2_kv_cfg& cfg, int B, int max_q, int64_t max_kv, bool cross, int most_parts) {
+KvPlan kv_tiles_plan(const csa2_kv_cfg& cfg, int B, int T, int max_q, int64_t max_kv, bool cross, int most_parts) {
   const int group = cfg.n_heads / cfg.kv_heads;
-  const int64_t rows = (int64_t)max_q * group, tiles = (rows + kCtaRows - 1) / kCtaRows;
+  const int64_t rows = (int64_t)max_q * group;
+  // at most: each sequence's longest, or what all rows fill and a last one each
+  const int64_t tiles = std::min(B * ((rows + kCtaRows - 1) / kCtaRows), (int64_t)T * group / kCtaRows + B);
   int64_t pages = (max_kv + kPage - 1) / kPage;
   if (cfg.window && !cross)
     pages = std::min<int64_t>(pages, ((int64_t)cfg.window + std::min<int64_t>(max_q, kCtaRows / group + 2) + kPage - 2) / kPage + 1);
-  const int64_t steps = std::max<int64_t>(1, (pages + 1) / 2), base = B * cfg.kv_heads * tiles, slots = num_sms();
+  const int64_t steps = std::max<int64_t>(1, (pages + 1) / 2), base = cfg.kv_heads * tiles, slots = num_sms();
   // The number of parts whose waves of CTAs end soonest, in key tiles: a CTA's start
   // and end cost about three, the joining kernel two and its reading two and a half
   // for each CTA of an SM.  Divided are all row tiles, or those of the last wave, if
@@ -842,7 +843,7 @@ KvPlan kv_tiles_plan(const csa2_kv_cfg& cfg, int B, int max_q, int64_t max_kv, b
   const int64_t per = (steps + best - 1) / best, parts = (steps + per - 1) / per;
   if (parts == 1) whole = 0;
   const int64_t ctas = whole + (base - whole) * std::max<int64_t>(parts, parts > 1 ? kCtaRows / 8 : 1);
-  return KvPlan{(int)parts, (int)(2 * per), false, (int)std::min<int64_t>(whole, INT32_MAX), ctas};
+  return KvPlan{(int)parts, (int)(2 * per), false, base, whole, ctas};
 }
 
 cudaError_t launch_kv_tiles(const csa2_kv_cfg& cfg, int B, const KvAtt& a, cudaStream_t stream) {
@@ -854,9 +855,10 @@ cudaError_t launch_kv_tiles(const csa2_kv_cfg& cfg, int B, const KvAtt& a, cudaS
                                                                : launch<64, true, false>(B, a, stream);
 }
 
-size_t kv_plain_bytes(const csa2_kv_cfg& cfg, int B, int max_q, int64_t max_kv, bool cross) {
+size_t kv_plain_bytes(const csa2_kv_cfg& cfg, int B, int T, int max_q, int64_t max_kv, bool cross) {
   if (cfg.cache_dtype != CSA2_CACHE_FP4) return 0;
-  const int64_t seen = cfg.window && !cross ? std::min(max_q, cfg.window) : max_q;
+  const int mean = std::min(max_q, T / B);  // rows of a sequence
+  const int64_t seen = cfg.window && !cross ? std::min(mean, cfg.window) : mean;
   if (seen * (cfg.n_heads / cfg.kv_heads) < kPlainRows) return 0;
   const size_t bytes = (size_t)B * ((max_kv + kPage - 1) / kPage) * cfg.kv_heads * 2 * kv_block_bytes(cfg.head_dim, false);
   return bytes <= kMostPlain ? bytes : 0;

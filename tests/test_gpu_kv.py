@@ -288,7 +288,7 @@ def test_long_keys_divided_or_not(dtype, dim, hq, hkv, nq, workspace):
     _attend_case(csa.KVCfg(hq, hkv, dim, dtype), [nq, nq], [6007, 1500], seed=nq, workspace=workspace)
 
 
-@pytest.mark.parametrize("dim,hq,hkv,window", [(128, 64, 2, 0), (64, 32, 1, 0), (128, 64, 1, 60), (128, 64, 1, 70)])
+@pytest.mark.parametrize("dim,hq,hkv,window", [(128, 256, 2, 0), (64, 128, 1, 0), (128, 128, 1, 30), (128, 128, 1, 40)])
 @pytest.mark.parametrize("cross", [False, True])
 def test_pages_decoded_ahead_or_in_passing(dim, hq, hkv, window, cross):
     # the products' operands and their order are the same: every bit is
@@ -306,7 +306,7 @@ def test_pages_decoded_ahead_or_in_passing(dim, hq, hkv, window, cross):
     q = _dev(_kv.normal(rng, T, hq, dim))
     cu, lens = _cu(nq), torch.tensor(kv, dtype=torch.int32, device="cuda")
     call, pages = csa.kv_cross_attend if cross else csa.kv_attend, 2 * B * 7 * hkv * 64 * dim * 2
-    ahead = cross or window != 60  # 60 x 64 rows read a key: fewer than 4096
+    ahead = cross or window != 30  # 51 tokens a sequence; 30 x 128 rows that read a key are fewer than 4096
     assert csa.kv_workspace_bytes(cfg, B, T, mq, mk) >= (pages if ahead else 0)
     got = []
     for n in (0, pages):
@@ -319,6 +319,16 @@ def test_pages_decoded_ahead_or_in_passing(dim, hq, hkv, window, cross):
     assert torch.isfinite(got[0][0].float()).all()
     if ahead:
         assert torch.equal(got[0][0], got[1][0]) and torch.equal(got[0][1], got[1][1])
+
+
+@pytest.mark.parametrize("dtype", [FP4, BF16])
+def test_one_prompt_among_many_single_tokens(dtype):
+    # tiles are counted by what the sequences have, over more than one warp's 128 sequences
+    rng = np.random.default_rng(8)
+    nq = [1] * 70 + [90] + [1, 0, 2] * 40 + [200] + [1] * 9
+    kv = [int(n) for n in rng.integers(0, 150, len(nq))]
+    kv[70], kv[191] = 90, 333
+    _attend_case(csa.KVCfg(14, 2, 64, dtype), nq, kv, seed=8, pad=5)
 
 
 @pytest.mark.parametrize("dtype", [FP4, BF16])

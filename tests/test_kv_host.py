@@ -167,3 +167,25 @@ def test_plain_rotation_keeps_lengths_and_both_styles_agree():
     halves = np.concatenate([x[..., 0:96:2], x[..., 1:96:2], x[..., 96:]], -1)
     z = _kv.rotate(halves, t, pos, 96, True)
     assert (z[..., :48] == y[..., 0:96:2].astype(np.float32)).all() and (z[..., 48:96] == y[..., 1:96:2].astype(np.float32)).all()
+
+
+def test_more_row_tiles_than_a_grid_holds_are_refused():
+    c = _cfg(n_heads=1024, kv_heads=1024)
+    many = dict(B=65535, T=2 ** 31 - 1, max_q=10 ** 6, qs=1024 * 128, os=1024 * 128)
+    assert _attend(c, **many) == 2
+    assert _attend(c, cross=True, **many) == 2
+
+
+@pytest.mark.parametrize("dtype,tokens,batch,keys,ahead", [
+    (csa.CACHE_FP4, 512, 1, 16384, True), (csa.CACHE_FP4, 511, 1, 16384, False), (csa.CACHE_BF16, 512, 1, 16384, False),
+    (csa.CACHE_FP4, 512, 1, 16385, True), (csa.CACHE_FP4, 2048, 33, 16384, False)])
+def test_workspace_holds_pages_decoded_ahead(dtype, tokens, batch, keys, ahead):
+    # 64 over 8 heads of 128: 4096 rows read a key from 512 tokens on; 2 GB hold 32 sequences of 16384 keys
+    c = csa.KVCfg(64, 8, 128, dtype)
+    pages = batch * -(-keys // 64) * 8 * 2 * 64 * 128 * 2
+    need = csa.kv_workspace_bytes(c, batch, tokens * batch, tokens, keys)
+    parts = tokens * batch * 64 * 129 * 4  # the rest is whole parts of every row
+    assert (need - (pages if ahead else 0)) % parts == 0 and (not ahead or need >= pages)
+    # the same rows, mostly one sequence's: the mean decides
+    if ahead:
+        assert csa.kv_workspace_bytes(c, 100, tokens + 99, tokens, keys) % ((tokens + 99) * 64 * 129 * 4) == 0

@@ -286,7 +286,8 @@ def swa_encode(x, row0, rows, status=None, stream=None):
 def attend(cfg: Cfg, q, main: PagedCache, n_entries, topk, swa, swa_len, swa_pos0, q_pos, out, lse=None,
            scale=None, status=None, stream=None):
     """a7: q [B][Tq][64][512] bf16, topk [B][Tq][k], swa [B][S][512] bf16 (or [B][S][528] uint8 MXFP8 rows
-    under FMT_SWA_FP8) -> out [B][Tq][64][512] fp32."""
+    under FMT_SWA_FP8) -> out [B][Tq][64][512] fp32.  q, the window rows, swa_len, swa_pos0 and q_pos are read before
+    the wait for the kernel ahead on the stream: enqueue another call between this one and the one that writes them."""
     B, Tq = q.shape[:2]
     S = swa.shape[1] if swa is not None else 0
     d = main.desc()
@@ -454,7 +455,8 @@ def kv_append(cfg: KVCfg, k, v, cu, pos0, cache: KVCache, rope=None, q=None, q_o
               status=None, stream=None):
     """New tokens of a ragged batch into the cache: k, v [T][kv_heads][head_dim] bf16 (row i of sequence b at
     cu[b] + i, position pos0[b] + i), keys and queries q [T][n_heads][head_dim] rotated by `rope` [rows][rope_dims / 2]
-    [2] fp32.  q_out (which may be q) takes the rotated queries, k_out / v_out the values as stored."""
+    [2] fp32.  q_out (which may be q) takes the rotated queries, k_out / v_out the values as stored.  (attend, not
+    kv_attend, reads its queries ahead of time: see there before handing it these outputs.)"""
     _kv_same(cfg, cache)
     dev, h, d = cache.device_index, cfg.kv_heads, cfg.head_dim
     T, B = k.shape[0], cache.batch

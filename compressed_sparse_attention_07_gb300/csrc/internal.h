@@ -16,10 +16,9 @@ namespace csa2 {
 // library waits for its predecessor (griddep_wait) before allocating tensor
 // memory and before any global load whose value a kernel of the library may
 // write -- before the wait a kernel issues L2 prefetch hints and reads only
-// the attention's query and window rows, which only csa2_swa_encode writes,
-// and that kernel lets its successor start only at its completion (a caller
-// that hands on kv_append's or kv_attend's outputs as such keeps the header's
-// rule: another call between the two).
+// the attention's query and window rows, which csa2_swa_encode writes and a
+// caller may have written by csa2_kv_append or the csa2_kv_* attention: the
+// kernels that write these let their successor start only at their completion.
 // cluster_x > 0 adds a cluster shape.
 template <typename... KArgs, typename... Args>
 cudaError_t launch_k(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t stream, int cluster_x,

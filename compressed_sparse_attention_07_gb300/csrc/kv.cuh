@@ -224,6 +224,14 @@ __device__ __forceinline__ int kv_parts(const KvAtt& a, int p0, int p1) {
   return quotient(p1 - p0 + a.part_pages - 1, a.by_pages);
 }
 
+// csa2_attend reads queries and window rows before it waits for the kernel ahead of it,
+// so a kernel that writes a call's outputs lets its successor start only when its CTAs
+// have ended; started early, csa2_attend read what stood there before.  It costs a call
+// the overlap with the next one's start: single-sequence decode 7.33 -> 7.74 us in a graph
+// of such calls, drafts 147 -> 149 us; appends take 2.46 -> 2.36 us.  What is sound is
+// kv_join_kernel's early start, as that kernel writes the outputs and waits before.
+__device__ __forceinline__ bool kv_joined(const KvAtt& a) { return a.n_parts > 1 && !a.cluster; }
+
 cudaError_t launch_kv_append(const csa2_kv_cfg& cfg, int B, int T, const uint16_t* q, int64_t q_stride,
                              const uint16_t* k, int64_t k_stride, const uint16_t* v, int64_t v_stride,
                              const int32_t* cu, const int64_t* pos0, const float* rope, int64_t rope_rows,

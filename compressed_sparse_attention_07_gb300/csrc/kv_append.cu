@@ -205,7 +205,6 @@ __global__ void __launch_bounds__(kThreads) kv_append_few_kernel(AppendArgs a) {
   constexpr int kLanes = kDim_ / 8;              // threads of a row
   constexpr int kRows = kThreads / kLanes;       // rows of a pass
   griddep_wait();  // every input may be the previous kernel's output
-  griddep_launch();
   const int n = blockIdx.x, tid = threadIdx.x;
   const int col = tid % kLanes, c0 = 8 * col;  // this thread's channels in every row
   const int n_rows = a.n_q + 2 * a.n_kv;
@@ -311,7 +310,6 @@ __global__ void __launch_bounds__(kStreamThreads, 2) kv_append_stream_kernel(App
   }
   __syncthreads();
   griddep_wait();  // every input may be the previous kernel's output
-  griddep_launch();
   // A piece holds kTokens whole tokens, or (per > 1) one of the parts of a token.
   const int n_rows = a.n_q + 2 * a.n_kv;
   const int per = kTokens > 1 ? 1 : (n_rows + kPieceRows<kDim_> - 1) / kPieceRows<kDim_>;

@@ -101,7 +101,7 @@ __global__ void __launch_bounds__(Rows<D, kFp4, NT, kCluster>::kWarps * 32, Rows
   if (lane < 2) tc::mbar_init(&bars[warp][lane], 1);
   tc::fence_mbar_init();
   griddep_wait();
-  griddep_launch();
+  if (kv_joined(a)) griddep_launch();
   int row0, rows, keys;
   if (!kv_sequence(a, b, row0, rows, keys)) return;
   const int n_rows = rows * a.group;  // of this kv head
@@ -559,7 +559,6 @@ __global__ void __launch_bounds__(Rows<D, kFp4, NT, kCluster>::kWarps * 32, Rows
 template <int D>
 __global__ void __launch_bounds__(256) kv_join_kernel(KvAtt a, int tile_rows, int per) {
   griddep_wait();
-  griddep_launch();
   const int lane = threadIdx.x & 31, id = a.whole + blockIdx.x / per;  // per: CTAs of a tile
   int b = id / a.kv_heads, kh = id % a.kv_heads, tile = 0;  // kv_rows_kernel has one tile
   if (tile_rows > kMostRows && !kv_tile(a, tile_rows, id, b, kh, tile)) return;

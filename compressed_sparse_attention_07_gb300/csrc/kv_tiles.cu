@@ -115,7 +115,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tiles_kernel(KvAtt a) {
     part = x - q * a.n_parts, id = a.whole + q;
   }
   griddep_wait();
-  griddep_launch();
+  if (kv_joined(a)) griddep_launch();
   if (!kv_tile(a, kCtaRows, id, b, kh, tile)) return;
   const int tile0 = tile * kCtaRows;
   int row0, rows, keys;

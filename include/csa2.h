@@ -241,7 +241,8 @@ CSA2_API int32_t csa2_index_select(const csa2_cfg* cfg, int32_t B, int32_t Tq, c
  * stream; of this library's calls only csa2_swa_encode writes any of them
  * (and csa2_kv_append or the csa2_kv_* attention, where a caller hands on
  * their outputs as such), so enqueue another call (the indexer of a decode
- * step) between the two.
+ * step) between the two.  None of these lets this call start while it still
+ * writes.
  * topk, n_entries and the main cache are read after that kernel has
  * completed. */
 CSA2_API int32_t csa2_attend(const csa2_cfg* cfg, int32_t B, int32_t Tq, const uint16_t* q,

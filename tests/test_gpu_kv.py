@@ -551,3 +551,68 @@ def test_sequences_that_share_pages():
     for b, n in enumerate((130, 64, 1)):
         want = _kv.attend(q[b:b + 1], _kv.fp4_round(x[:n, :8])[0], _kv.fp4_round(x[:n, 8:])[0], 1 / 8, True)
         assert (np.abs(out[b:b + 1].double().cpu().numpy() - want[0]) <= _kv.tolerances(cfg, n, *want)[0]).all()
+
+
+# ------------------------------------------- beside the library's other calls --
+
+def _pages_at_random(cache, seed):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    for t in (cache.k_data, cache.v_data):
+        t.copy_(torch.randint(0, 256, t.shape, generator=g, device="cuda", dtype=torch.uint8))
+    for t in (cache.k_scales, cache.v_scales):
+        t.copy_(torch.randint(32, 64, t.shape, generator=g, device="cuda", dtype=torch.uint8))
+
+
+@pytest.mark.parametrize("how", ["append few", "append many", "rows", "cluster", "parts", "tiles", "tiles divided",
+                                 "decoded ahead"])
+def test_outputs_handed_to_the_sparse_attention(how):
+    """csa2_attend reads its queries before it waits for the kernel ahead of it: handed what one of these calls has just
+    been told to write, it has to see that, not what stood there."""
+    B, hkv, keys = {"append few": (40, 2, 0), "append many": (120, 2, 0), "rows": (20, 32, 300), "cluster": (1, 32, 4000),
+                    "parts": (3, 32, 9000), "tiles": (4, 2, 700), "tiles divided": (2, 2, 5000),
+                    "decoded ahead": (2, 2, 3000)}[how]
+    Tq = {"append few": 10, "append many": 10, "tiles": 64, "decoded ahead": 64}.get(how, 1)
+    cfg = csa.KVCfg(256, hkv, 128, FP4, rope_dims=128)
+    x = torch.empty(B * Tq, 256, 128, dtype=torch.bfloat16, device="cuda")
+    cache = _cache(cfg, B, max(keys, Tq))
+    g = torch.Generator(device="cuda").manual_seed(5)
+    q, k, v = (torch.randn(B * Tq, h, 128, generator=g, device="cuda", dtype=torch.bfloat16) for h in (256, hkv, hkv))
+    cu = _cu([Tq] * B)
+    if keys == 0:
+        pos0, table = torch.zeros(B, dtype=torch.int64, device="cuda"), csa.rope_table(64, 128)
+
+        def call():
+            csa.kv_append(cfg, k, v, cu, pos0, cache, rope=table, q=q, q_out=x)
+    else:
+        _pages_at_random(cache, 6)
+        lens = torch.full((B,), keys, dtype=torch.int32, device="cuda")
+        ws = torch.empty(csa.kv_workspace_bytes(cfg, B, B * Tq, Tq, keys), dtype=torch.uint8, device="cuda")
+
+        def call():
+            csa.kv_attend(cfg, q, cu, cache, lens, Tq, keys, x, workspace=ws)
+
+    sparse = csa.Cfg(ratio=1, topk=512, window=128)
+    main = csa.PagedCache(B, 64, 512, csa.CACHE_FP4)
+    n_ent = torch.zeros(B, dtype=torch.int32, device="cuda")
+    topk = torch.full((B, Tq, 512), -1, dtype=torch.int32, device="cuda")
+    swa = torch.randn(B, 128, 512, generator=g, device="cuda", dtype=torch.bfloat16)
+    swa_len = torch.full((B,), 128, dtype=torch.int32, device="cuda")
+    swa_pos0 = torch.zeros(B, dtype=torch.int64, device="cuda")
+    q_pos = torch.full((B, Tq), 127, dtype=torch.int64, device="cuda")
+    got, want = (torch.empty(B, Tq, 64, 512, device="cuda") for _ in "gw")
+
+    def attend(out):
+        csa.attend(sparse, x.view(B, Tq, 64, 512), main, n_ent, topk, swa, swa_len, swa_pos0, q_pos, out, scale=0.2)
+
+    def handed_on():
+        x.zero_()
+        call()
+        attend(got)
+
+    run = csa.capture(handed_on)  # the launches right behind one another
+    for _ in range(10):
+        run()
+        torch.cuda.synchronize()
+        attend(want)
+        torch.cuda.synchronize()
+        assert x.any() and torch.equal(got, want)

@@ -3,6 +3,8 @@
 // range of keys that a tile of query rows sees.
 #pragma once
 
+#include <atomic>
+
 #include "internal.h"
 
 namespace csa2 {
@@ -248,14 +250,17 @@ struct KvPlan {
 };
 KvPlan kv_plan(const csa2_kv_cfg& cfg, int B, int T, int max_q, int max_kv, bool cross, int most_parts);
 
-// Let `kern` use `bytes` of dynamic shared memory: set once on each device.
+// Let `kern` use `bytes` of dynamic shared memory: set once on each device, as setting it
+// takes the host a microsecond (one token on 4095: 9.4 us a call so, 10.3 set at every
+// call).  Threads may make their first calls at once: `done` is atomic, and setting it
+// twice does no harm.
 template <typename K>
-cudaError_t allow_smem(K kern, int bytes, bool (&done)[64]) {
+cudaError_t allow_smem(K kern, int bytes, std::atomic<bool> (&done)[64]) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess || (dev < 64 && done[dev])) return e;
+  if (e != cudaSuccess || (dev < 64 && done[dev].load(std::memory_order_relaxed))) return e;
   e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-  if (e == cudaSuccess && dev < 64) done[dev] = true;
+  if (e == cudaSuccess && dev < 64) done[dev].store(true, std::memory_order_relaxed);
   return e;
 }
 

@@ -409,7 +409,7 @@ template <int kDim_, bool kFp4, int kTokens>
 cudaError_t stream_of(const AppendArgs& a, int64_t pieces, cudaStream_t stream) {
   auto kern = kv_append_stream_kernel<kDim_, kFp4, kTokens>;
   constexpr int kSmem = kSlots * slot_bytes<kDim_>();
-  static bool done[64];
+  static std::atomic<bool> done[64];
   const cudaError_t e = allow_smem(kern, kSmem, done);
   if (e != cudaSuccess) return e;
   const int64_t ctas = std::min<int64_t>(pieces, 2 * num_sms());

@@ -637,7 +637,7 @@ template <int D, bool kFp4, int NT, bool kCluster>
 cudaError_t launch(int B, const KvAtt& a, cudaStream_t stream) {
   using R = Rows<D, kFp4, NT, kCluster>;
   auto kern = kv_rows_kernel<D, kFp4, NT, kCluster>;
-  static bool done[64];
+  static std::atomic<bool> done[64];
   const cudaError_t e = allow_smem(kern, R::kSmem, done);
   if (e != cudaSuccess) return e;
   const int tiles = (int)(((int64_t)a.max_q * a.group + 8 * NT - 1) / (8 * NT));

@@ -806,7 +806,7 @@ __global__ void __launch_bounds__(256) kv_decode_kernel(KvAtt a) {
 template <int D, bool kFp4, bool kPlain>
 cudaError_t launch(int B, const KvAtt& a, cudaStream_t stream) {
   auto kern = kv_tiles_kernel<D, kFp4, kPlain>;
-  static bool done[64];
+  static std::atomic<bool> done[64];
   cudaError_t e = allow_smem(kern, Tiles<D>::kSmem, done);
   if (e != cudaSuccess) return e;
   if constexpr (kPlain) {

@@ -616,3 +616,51 @@ def test_outputs_handed_to_the_sparse_attention(how):
         attend(want)
         torch.cuda.synchronize()
         assert x.any() and torch.equal(got, want)
+
+
+_THREADS = """
+import threading
+import torch
+import compressed_sparse_attention_07_gb300 as csa
+cfg = csa.KVCfg(64, 8, 128, rope_dims=0)
+jobs = []
+for i in range(8):
+    g = torch.Generator(device="cuda").manual_seed(i)
+    cache = csa.KVCache(cfg, 2, 2048)
+    q, k, v = (torch.randn(3000, h, 128, generator=g, device="cuda", dtype=torch.bfloat16) for h in (64, 8, 8))
+    cu = torch.tensor([0, 1600, 3000], dtype=torch.int32, device="cuda")
+    few = torch.tensor([0, 1, 3], dtype=torch.int32, device="cuda")
+    lens = torch.tensor([1600, 1400], dtype=torch.int32, device="cuda")
+    outs = [torch.zeros_like(q), torch.zeros_like(q[:3])]
+    jobs.append((cache, q, k, v, cu, few, lens, torch.zeros(2, dtype=torch.int64, device="cuda"), outs, torch.cuda.Stream()))
+torch.cuda.synchronize()
+start = threading.Barrier(len(jobs))
+
+def run(job):
+    cache, q, k, v, cu, few, lens, pos0, outs, s = job
+    start.wait()
+    csa.kv_append(cfg, k, v, cu, pos0, cache, stream=s)
+    csa.kv_attend(cfg, q, cu, cache, lens, 1600, 2048, outs[0], stream=s)
+    csa.kv_attend(cfg, q[:3], few, cache, lens, 2, 2048, outs[1], stream=s)
+
+ts = [threading.Thread(target=run, args=(j,)) for j in jobs]
+[t.start() for t in ts]
+[t.join() for t in ts]
+torch.cuda.synchronize()
+for cache, q, k, v, cu, few, lens, pos0, outs, s in jobs:
+    again = [torch.zeros_like(o) for o in outs]
+    csa.kv_attend(cfg, q, cu, cache, lens, 1600, 2048, again[0])
+    csa.kv_attend(cfg, q[:3], few, cache, lens, 2, 2048, again[1])
+    assert outs[0].any() and outs[1].any() and all(torch.equal(a, o) for a, o in zip(again, outs))
+print("same")
+"""
+
+
+def test_first_calls_from_several_threads_at_once():
+    """A process whose first calls of every kernel come from eight threads at the same time."""
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", _THREADS], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "same" in r.stdout, r.stderr[-2000:]

@@ -258,9 +258,9 @@ template <typename K>
 cudaError_t allow_smem(K kern, int bytes, std::atomic<bool> (&done)[64]) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess || (dev < 64 && done[dev].load(std::memory_order_relaxed))) return e;
+  if (e != cudaSuccess || (dev < 64 && done[dev].load(std::memory_order_acquire))) return e;
   e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-  if (e == cudaSuccess && dev < 64) done[dev].store(true, std::memory_order_relaxed);
+  if (e == cudaSuccess && dev < 64) done[dev].store(true, std::memory_order_release);
   return e;
 }
 

@@ -1,5 +1,7 @@
 """Plain restatement of the paged key / value operators for the tests: numpy, attention in fp64, encodings by the
 oracle's codecs, written from include/csa2.h.  Nothing of the library runs here."""
+import math
+
 import numpy as np
 import torch
 
@@ -129,3 +131,48 @@ def tolerances(cfg, keys, out, lse, mag, dot, big):
     tol = 2.0 ** -8 * np.abs(out) + mag * (rel[..., None] if np.ndim(rel) else rel) * (1 + 2.0 ** -7)
     tol = tol + keys * 2.0 ** -25 * 8 * mag.max(initial=0.0) + 1e-30
     return tol, logit + 2.0 ** -21 + (2 * keys + 64) * u32 + 4 * u32 * np.abs(np.where(np.isfinite(lse), lse, 0)) + dot * 8 * u32
+
+
+# ---- sharp checks of long sequences, in torch (on whatever device the rows are)
+
+def attend_sums(q, k, v, scale, causal):
+    """One sequence in fp64: q [n][Hq][D], k, v [m][H][D] -> out, sqrt(sum p^2 v^2), the same with min(p, 2^-25 of the
+    row's largest p) for p [n][Hq][D], and the largest scale sum |q||k| over the seen keys [n][Hq]."""
+    n, hq, D = q.shape
+    m, h = k.shape[:2]
+    out, root, low = (torch.zeros(n, hq, D, dtype=torch.float64, device=q.device) for _ in range(3))
+    dot = torch.zeros(n, hq, dtype=torch.float64, device=q.device)
+    see = torch.ones(n, m, dtype=torch.bool, device=q.device)
+    if causal:
+        see = torch.arange(m, device=q.device) <= (m - n + torch.arange(n, device=q.device))[:, None]
+    for a in range(hq):
+        kk, vv, qq = (x[:, i].double() for x, i in ((k, a * h // hq), (v, a * h // hq), (q, a)))
+        p = torch.softmax((qq @ kk.T * scale).masked_fill(~see, -math.inf), 1)
+        out[:, a], root[:, a] = p @ vv, (p ** 2 @ vv ** 2).sqrt()
+        low[:, a] = (torch.minimum(p, 2.0 ** -25 * p.amax(1, keepdim=True)) ** 2 @ vv ** 2).sqrt()
+        dot[:, a] = (qq.abs() @ kk.abs().T * abs(scale)).masked_fill(~see, 0).amax(1)
+    return out, root, low, dot
+
+
+def far(cfg, keys, got, out, root, low, dot):
+    """How far `got` is from `out` in units of what roundings allow: (the farthest value, the farthest row by the root of
+    its mean square).  Below 1 where a row's channels lie within 2^14 of one another.
+
+    A weight is off by at most w of itself (rounded to f16 or bf16, an exp2, its logit of fp32 sums) or, rounded to f16,
+    by 2^-25 of the row's largest; a value of the output by half a step of bf16, 2^-8 of itself; the fp32 sums by two
+    steps of 2^-24 in each of some keys / 8 additions, of what has been summed so far (4 root and the output at most).
+    Weights are rounded apart from one another, so that their errors, each within w p |v|, go either way: by Hoeffding
+    their sum passes 7 sqrt(sum (w p v)^2) once in 2e10.  Errors of rounding spread evenly over an interval have a root
+    of the mean square of its half / sqrt(3); over a row's 64 or 128 channels the mean is not four times its expectation."""
+    u32 = 2.0 ** -24
+    w = 2.0 ** -22 + 2 * torch.expm1((cfg.head_dim + 10) * u32 * dot)[..., None]
+    if cfg.cache_dtype == csa.CACHE_FP4:
+        off = (w + 2.0 ** -11) * root + low
+    else:
+        off = (w + 2.0 ** -8) * root
+    sums = (keys / 8 + 64) * 2 * u32 * (4 * root + out.abs())
+    err = (got.double() - out).abs()
+    each = err / (2.0 ** -8 * out.abs() + (1 + 2.0 ** -8) * (7 * off + sums) + 1e-30)
+    mean = (off ** 2 + (2.0 ** -8 * out) ** 2).mean(-1) / 3
+    rms = err.square().mean(-1).sqrt() / (2 * mean.sqrt() + sums.square().mean(-1).sqrt() + 1e-30)
+    return each.max().item(), rms.max().item()

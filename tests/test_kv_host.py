@@ -189,3 +189,43 @@ def test_workspace_holds_pages_decoded_ahead(dtype, tokens, batch, keys, ahead):
     # the same rows, mostly one sequence's: the mean decides
     if ahead:
         assert csa.kv_workspace_bytes(c, 100, tokens + 99, tokens, keys) % ((tokens + 99) * 64 * 129 * 4) == 0
+
+
+def _rounded_attention(cfg, q, k, v, scale):
+    """Attention with the roundings that the kernels make and no others: weights to f16 or bf16, the output to bf16."""
+    h, hq = k.shape[1], q.shape[1]
+    out = torch.empty(q.shape, dtype=torch.bfloat16)
+    for a in range(hq):
+        x = q[:, a] @ k[:, a * h // hq].T * scale
+        p = torch.exp(x - x.amax(1, keepdim=True))
+        r = p.to(torch.float16 if cfg.cache_dtype == csa.CACHE_FP4 else torch.bfloat16).double()
+        out[:, a] = (r @ v[:, a * h // hq] / p.sum(1, keepdim=True)).to(torch.bfloat16)
+    return out
+
+
+@pytest.mark.parametrize("dtype", [csa.CACHE_FP4, csa.CACHE_BF16])
+@pytest.mark.parametrize("dim,keys", [(64, 6007), (128, 9000)])
+def test_long_comparison_sees_a_lost_page(dtype, dim, keys):
+    """The comparison for long sequences lets roundings pass, and sees 16 values lost among 6000 and 9000 keys, a page
+    taken from another place and a part of the keys counted twice."""
+    rng = np.random.default_rng(dim)
+    cfg = csa.KVCfg(4, 2, dim, dtype)
+    q = torch.from_numpy(_kv.normal(rng, 3, 4, dim))
+    k, v = (torch.from_numpy(_kv.fp4_round(x)[0] if dtype == csa.CACHE_FP4 else x)
+            for x in (_kv.normal(rng, keys, 2, dim) for _ in "kv"))
+    scale = dim ** -0.5
+    want = _kv.attend_sums(q, k, v, scale, False)
+    plain = _kv.attend(q.numpy(), k.numpy(), v.numpy(), scale, False)[0]
+    assert np.allclose(want[0].numpy(), plain, rtol=1e-9, atol=1e-12)
+    each, rms = _kv.far(cfg, keys, _rounded_attention(cfg, q, k, v, scale), *want)
+    assert each < 1 and rms < 1
+    at = keys // 2 // 64 * 64
+    for lost in (slice(at, at + 64), slice(at, at + 16), slice(keys - 16, keys)):
+        w = v.clone()
+        w[lost] = 0
+        assert _kv.far(cfg, keys, _rounded_attention(cfg, q, k, w, scale), *want)[1] > 1
+    w = v.clone()
+    w[at:at + 64] = v[64:128]
+    assert _kv.far(cfg, keys, _rounded_attention(cfg, q, k, w, scale), *want)[1] > 1
+    twice = _rounded_attention(cfg, q, torch.cat((k, k[:256])), torch.cat((v, v[:256])), scale)
+    assert _kv.far(cfg, keys, twice, *want)[1] > 1

@@ -62,8 +62,9 @@ __device__ __forceinline__ uint32_t e4m3_code(float y) {
   asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(0.0f), "f"(y));
   return r & 0xFFu;
 }
-// Codes of x / s (0 < s; |x| below about 6.4 s, or s the largest scale), ties to
-// the even code, saturating: eight nibbles, channel 0 lowest.  The quotient is
+// Codes of x / s (0 < s), ties to the even code, saturating: eight nibbles, channel
+// 0 lowest.  |x| may pass 6 s, up to 9 s at the smallest scales, whose steps are
+// wide, and without bound at the largest: the conversion saturates.  The quotient is
 // rounded correctly from the reciprocal by one step with the remainder
 // (Markstein), so that a value half way between two codes is seen as such; where
 // the remainder underflows, the code is 0 either way.  The sign of a value that

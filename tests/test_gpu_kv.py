@@ -664,3 +664,51 @@ def test_first_calls_from_several_threads_at_once():
     root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
     r = subprocess.run([sys.executable, "-c", _THREADS], cwd=root, capture_output=True, text=True, timeout=300)
     assert r.returncode == 0 and "same" in r.stdout, r.stderr[-2000:]
+
+
+def _hard_groups(rng, n):
+    """n groups of 16 bf16 values where encoding decides closely: values half way between two codes of every scale and
+    their bf16 neighbours, largest values half way between two scales and theirs, ordinary ones of every size, also far
+    past the largest scale and below the smallest."""
+    def near(x):  # x (exact in bf16) or a neighbour
+        bits = torch.from_numpy(np.asarray(x, np.float32)).to(torch.bfloat16).view(torch.int16)
+        step = torch.from_numpy(rng.integers(-1, 2, bits.shape).astype(np.int16))
+        return torch.where(bits > 0, bits + step, bits).view(torch.bfloat16).double().numpy()
+
+    code = np.arange(127)
+    e, m = code >> 3, code & 7
+    scales = np.where(e == 0, m * 2.0 ** -9, (1 + m / 8) * 2.0 ** (e - 7.0))
+    mids = np.array([0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0])
+    kind = np.arange(n) % 4
+    s = scales[1 + rng.integers(0, 126, n)]
+    x = near(s[:, None] * mids[rng.integers(0, 7, (n, 16))])                     # 0: half way between codes of scale s
+    x[:, 0] = 6 * s
+    up = rng.integers(0, 126, n)                                                 # 1: half way between scales
+    border = near(3 * (scales[up] + scales[up + 1]))
+    some = _kv.bf16(rng.uniform(0, 1, (n, 16)) * border[:, None])
+    some[:, 5] = border
+    x = np.where((kind == 1)[:, None], np.minimum(some, border[:, None]), x)
+    wide = _kv.bf16(np.abs(rng.standard_normal((n, 16))) * 2.0 ** rng.uniform(-18, 18, n)[:, None])
+    x = np.where((kind == 2)[:, None], wide, x)                                  # 2: of every size
+    top = _kv.bf16(rng.uniform(0.01, 3, (n, 16)) * 2.0 ** rng.choice([-126.0, -60, 12, 60, 125], n)[:, None])
+    x = np.where((kind == 3)[:, None], top, x)                                   # 3: far out of the scales' range
+    return x * rng.choice([-1.0, 1.0], x.shape)
+
+
+@pytest.mark.parametrize("tokens", [40, 1300])
+@pytest.mark.parametrize("dim", [64, 128])
+def test_append_encodes_as_the_oracle_at_every_border(tokens, dim):
+    rng = np.random.default_rng(tokens + dim)
+    cfg = csa.KVCfg(8, 8, dim, FP4, rope_dims=0)
+    cache = _cache(cfg, 1, tokens)
+    k, v = (_hard_groups(rng, tokens * 8 * dim // 16).reshape(tokens, 8, dim) for _ in "kv")
+    out, st = torch.empty(2, tokens, 8, dim, dtype=torch.bfloat16, device="cuda"), _status()
+    csa.kv_append(cfg, _dev(k), _dev(v), _cu([tokens]), torch.zeros(1, dtype=torch.int64, device="cuda"), cache,
+                  k_out=out[0], v_out=out[1], status=st)
+    assert int(st.item()) == 0
+    for kind, x, plain in (("k", k, out[0]), ("v", v, out[1])):
+        val, codes, sc = _kv.fp4_round(x)
+        _, gcodes, gsc = _kv.read(cache, cfg, 0, kind, tokens)
+        assert len(np.unique(sc)) == 127  # every scale
+        assert np.array_equal(gsc, sc) and np.array_equal(gcodes, codes)
+        assert np.array_equal(plain.double().cpu().numpy(), val)

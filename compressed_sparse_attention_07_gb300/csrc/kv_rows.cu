@@ -2,7 +2,7 @@
 // decode, drafted blocks): every key and value is read once from HBM for up to
 // 32 rows (query heads of a kv head x new tokens), so the cache's bytes decide.
 //
-// One CTA takes one kv head, up to 8 NT rows and a part of the keys; its warps
+// One CTA takes one kv head, its rows (8 NT at most) and a part of the keys; its warps
 // (four) take tiles of 64 keys (FP4, one page) or 32 (bf16) in turn, each with
 // its own two-stage ring of bulk copies, its own running maximum, sum and
 // output in registers, joined through shared memory at the end.  With several
@@ -97,22 +97,21 @@ __global__ void __launch_bounds__(Rows<D, kFp4, NT, kCluster>::kWarps * 32, Rows
   __shared__ float part_l[kRows];  // (cluster) this CTA's log2-sum-exp2 of each row
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
-  const int part = blockIdx.x, kh = blockIdx.y % a.kv_heads, tile0 = (blockIdx.y / a.kv_heads) * kRows, b = blockIdx.z;
+  const int part = blockIdx.x, kh = blockIdx.y, b = blockIdx.z;
   if (lane < 2) tc::mbar_init(&bars[warp][lane], 1);
   tc::fence_mbar_init();
   griddep_wait();
   if (kv_joined(a)) griddep_launch();
   int row0, rows, keys;
   if (!kv_sequence(a, b, row0, rows, keys)) return;
-  const int n_rows = rows * a.group;  // of this kv head
-  if (tile0 >= n_rows) return;
-  const int last = min(tile0 + kRows, n_rows) - 1;
+  if (rows == 0) return;
+  const int n_rows = rows * a.group;  // of this kv head, kRows at most
   int p0, p1;
-  kv_pages(a, group_of(a, tile0), group_of(a, last), rows, keys, p0, p1);
+  kv_pages(a, 0, rows - 1, rows, keys, p0, p1);
   const int n_act = kv_parts(a, p0, p1);
   if (!kCluster && part > 0 && part >= n_act) return;
   const int pb = min(p0 + part * a.part_pages, p1), pe = min(pb + a.part_pages, p1);
-  const int key_end = kv_hi(a, group_of(a, last), rows, keys);  // no row sees keys from here on
+  const int key_end = kv_hi(a, rows - 1, rows, keys);  // no row sees keys from here on
   const int tb = pb * R::kPerPage, te = min(pe * R::kPerPage, (key_end + R::kTile - 1) / R::kTile);
 
   uint8_t* ring = smem + warp * R::kWarpBytes;
@@ -157,7 +156,7 @@ __global__ void __launch_bounds__(Rows<D, kFp4, NT, kCluster>::kWarps * 32, Rows
   float qs = a.scale * kLog2e;
   uint2* qfrag = reinterpret_cast<uint2*>(smem + kWarps * R::kWarpBytes);  // [KS][NT][32]
   for (int n = warp; n < NT; n += kWarps) {
-    const int r = tile0 + 8 * n + g;
+    const int r = 8 * n + g;
     const bool live = r < n_rows;
     const int i = live ? group_of(a, r) : 0, h = live ? kh * a.group + r - group_of(a, r) * a.group : 0;
     const uint16_t* q = a.q + (int64_t)(row0 + i) * a.q_stride + h * D;
@@ -212,7 +211,7 @@ __global__ void __launch_bounds__(Rows<D, kFp4, NT, kCluster>::kWarps * 32, Rows
   }
   __syncthreads();
   // keys that every row sees: no masks inside
-  const int all_lo = kv_lo(a, group_of(a, last), rows, keys), all_hi = kv_hi(a, group_of(a, tile0), rows, keys);
+  const int all_lo = kv_lo(a, rows - 1, rows, keys), all_hi = kv_hi(a, 0, rows, keys);
 
   float sc[NT][2], m[NT][2], l[NT][2], o[MT][NT][4];
 #pragma unroll
@@ -475,7 +474,7 @@ __global__ void __launch_bounds__(Rows<D, kFp4, NT, kCluster>::kWarps * 32, Rows
   float* joined = reinterpret_cast<float*>(smem + kWarps * R::kWarpBytes + R::kQFrag);  // [kRows][D] (cluster)
   for (int x = tid; x < kRows * (D / 2); x += kWarps * 32) {
     const int r = x / (D / 2), c = 2 * (x % (D / 2));
-    if (tile0 + r >= n_rows) break;
+    if (r >= n_rows) break;
     float top = -INFINITY;
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) top = fmaxf(top, join_m[w][r]);
@@ -494,7 +493,7 @@ __global__ void __launch_bounds__(Rows<D, kFp4, NT, kCluster>::kWarps * 32, Rows
       }
     }
     const float inv = sum > 0.0f ? 1.0f / sum : (sum == 0.0f ? 0.0f : NAN);
-    const int i = row0 + group_of(a, tile0 + r), h = kh * a.group + (tile0 + r - group_of(a, tile0 + r) * a.group);
+    const int i = row0 + group_of(a, r), h = kh * a.group + (r - group_of(a, r) * a.group);
     const int64_t at = (int64_t)i * a.n_heads + h;
     const float lse2 = sum == 0.0f ? -INFINITY : top + log2f(sum);
     if (whole) {
@@ -519,7 +518,7 @@ __global__ void __launch_bounds__(Rows<D, kFp4, NT, kCluster>::kWarps * 32, Rows
       const uint32_t mine_o = tc::smem_u32(joined), mine_l = tc::smem_u32(part_l);
       for (int x = part * (kWarps * 32) + tid; x < kRows * (D / 4); x += gridDim.x * (kWarps * 32)) {
         const int r = x / (D / 4), c = 4 * (x % (D / 4));
-        if (tile0 + r >= n_rows) break;
+        if (r >= n_rows) break;
         float lp[kMostCluster];
         float4 v[kMostCluster];
         float top = -INFINITY;
@@ -542,7 +541,7 @@ __global__ void __launch_bounds__(Rows<D, kFp4, NT, kCluster>::kWarps * 32, Rows
           }
         }
         const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-        const int i = row0 + group_of(a, tile0 + r), h = kh * a.group + (tile0 + r - group_of(a, tile0 + r) * a.group);
+        const int i = row0 + group_of(a, r), h = kh * a.group + (r - group_of(a, r) * a.group);
         *reinterpret_cast<uint2*>(a.out + (int64_t)i * a.out_stride + h * D + c) =
             make_uint2(bf16x2(o0 * inv, o1 * inv), bf16x2(o2 * inv, o3 * inv));
         if (a.lse && c == 0) a.lse[(int64_t)i * a.n_heads + h] = sum == 0.0f ? -INFINITY : (top + log2f(sum)) * kLn2;
@@ -560,7 +559,7 @@ template <int D>
 __global__ void __launch_bounds__(256) kv_join_kernel(KvAtt a, int tile_rows, int per) {
   griddep_wait();
   const int lane = threadIdx.x & 31, id = a.whole + blockIdx.x / per;  // per: CTAs of a tile
-  int b = id / a.kv_heads, kh = id % a.kv_heads, tile = 0;  // kv_rows_kernel has one tile
+  int b = id / a.kv_heads, kh = id % a.kv_heads, tile = 0;  // kv_rows_kernel: one a kv head
   if (tile_rows > kMostRows && !kv_tile(a, tile_rows, id, b, kh, tile)) return;
   const int tile0 = tile * tile_rows;
   int row0, rows, keys;
@@ -640,8 +639,7 @@ cudaError_t launch(int B, const KvAtt& a, cudaStream_t stream) {
   static std::atomic<bool> done[64];
   const cudaError_t e = allow_smem(kern, R::kSmem, done);
   if (e != cudaSuccess) return e;
-  const int tiles = (int)(((int64_t)a.max_q * a.group + 8 * NT - 1) / (8 * NT));
-  return launch_k(kern, dim3(a.n_parts, tiles * a.kv_heads, B), dim3(R::kWarps * 32), R::kSmem, stream,
+  return launch_k(kern, dim3(a.n_parts, a.kv_heads, B), dim3(R::kWarps * 32), R::kSmem, stream,
                   kCluster ? a.n_parts : 0, a);
 }
 
@@ -663,6 +661,8 @@ void shape(int nt, int* ctas, int* warps) {
   *warps = Rows<D, kFp4, 1, true>::kWarps;
 }
 
+// Blocks of eight rows for n rows of a kv head: a CTA takes them all.
+static_assert(kMostRows == 32, "a CTA of four blocks, and kv_join_kernel, take every row of a kv head");
 int row_blocks(int64_t n) { return n <= 8 ? 1 : n <= 16 ? 2 : 4; }
 
 }  // namespace
@@ -672,16 +672,15 @@ KvPlan kv_plan(const csa2_kv_cfg& cfg, int B, int T, int max_q, int max_kv, bool
   if ((int64_t)max_q * group > kMostRows) return kv_tiles_plan(cfg, B, T, max_q, max_kv, cross, most_parts);
   KvPlan plan = {1, 1, false, 0, 0, 0};
   const int nt = row_blocks((int64_t)max_q * group);
-  const int64_t tiles = ((int64_t)max_q * group + 8 * nt - 1) / (8 * nt);
   int64_t pages = ((int64_t)max_kv + kPage - 1) / kPage;
-  if (cfg.window && !cross)  // the rows of a tile see window + their number - 1 keys
-    pages = std::min<int64_t>(pages, ((int64_t)cfg.window + std::min<int64_t>(max_q, 8 * nt) + kPage - 2) / kPage + 1);
+  if (cfg.window && !cross)  // max_q rows see window + max_q - 1 keys
+    pages = std::min<int64_t>(pages, ((int64_t)cfg.window + max_q + kPage - 2) / kPage + 1);
   if (pages < 1) pages = 1;
   const bool fp4 = cfg.cache_dtype == CSA2_CACHE_FP4;
   int per_sm, wide;
   if (cfg.head_dim == 128) fp4 ? shape<128, true>(nt, &per_sm, &wide) : shape<128, false>(nt, &per_sm, &wide);
   else fp4 ? shape<64, true>(nt, &per_sm, &wide) : shape<64, false>(nt, &per_sm, &wide);
-  const int64_t sms = num_sms(), base = (int64_t)B * cfg.kv_heads * tiles;
+  const int64_t sms = num_sms(), base = (int64_t)B * cfg.kv_heads;
   // The number of parts that ends soonest, in units of a page's share of an
   // SM's throughput: an SM's CTAs (n at most, each its pages and about three
   // pages' work besides) share it, but one warp alone needs about ten units for

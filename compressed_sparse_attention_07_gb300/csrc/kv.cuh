@@ -114,9 +114,11 @@ struct KvAtt {
   int64_t out_stride;
   float* lse;
   // division of the keys: parts of `part_pages` pages; with n_parts > 1 the
-  // partial outputs go to part_o [n_parts][T * n_heads][dim] and their
-  // log2-sum-exp2 to part_l [n_parts][T * n_heads]
+  // partial outputs go to part_o [n_parts][part_step][dim] and their log2-sum-exp2 to
+  // part_l [n_parts][part_step] (kv_part_row)
   int n_parts, part_pages;
+  int64_t part_step;  // T * n_heads, or (tile kernel) the divided tiles times part_rows
+  int part_rows;      // most rows of a tile; 0: by row and head
   int cluster;  // the parts of a head join in a cluster instead
   // (tile kernel) most row tiles, of all kv heads; how many, in the order of their
   // CTAs, are not divided
@@ -132,6 +134,12 @@ struct KvAtt {
 };
 
 __device__ __forceinline__ int group_of(const KvAtt& a, int n) { return quotient(n, a.by_group); }
+
+// Where row r of the id-th row tile (its first is tile0; row and head number `at` of the
+// batch) has its partial outputs, in each part.
+__device__ __forceinline__ int64_t kv_part_row(const KvAtt& a, int id, int r, int tile0, int64_t at) {
+  return a.part_rows ? (int64_t)(id - a.whole) * a.part_rows + r - tile0 : at;
+}
 
 // Rows and keys of sequence b; false (status set) when they are out of bounds.
 __device__ __forceinline__ bool kv_sequence(const KvAtt& a, int b, int& row0, int& rows, int& keys) {
@@ -240,15 +248,18 @@ cudaError_t launch_kv_append(const csa2_kv_cfg& cfg, int B, int T, const uint16_
                              const KvView& c, uint16_t* q_out, int64_t q_out_stride, uint16_t* k_out, uint16_t* v_out,
                              int32_t* status, cudaStream_t stream);
 
-// How a call divides the keys, from sizes alone; most_parts: what the workspace
-// holds.
+// How a call divides the keys, from sizes alone, with no more than `room` bytes of
+// partial outputs.
 struct KvPlan {
   int n_parts, part_pages;
   bool cluster;  // the parts join in a cluster, without workspace
   int64_t tiles, whole;  // (tile kernel) row tiles of all kv heads, those that are not divided
   int64_t ctas;          // (tile kernel) of it or of the joining kernel, whichever has more
+  int64_t part_step;     // as in KvAtt
+  int part_rows;
+  size_t bytes;  // of the partial outputs
 };
-KvPlan kv_plan(const csa2_kv_cfg& cfg, int B, int T, int max_q, int max_kv, bool cross, int most_parts);
+KvPlan kv_plan(const csa2_kv_cfg& cfg, int B, int T, int max_q, int max_kv, bool cross, size_t room);
 
 // Let `kern` use `bytes` of dynamic shared memory: set once on each device, as setting it
 // takes the host a microsecond (one token on 4095: 9.4 us a call so, 10.3 set at every
@@ -267,7 +278,7 @@ cudaError_t allow_smem(K kern, int bytes, std::atomic<bool> (&done)[64]) {
 // The plan of the tile kernel, which takes more rows of a kv head than kMostRows;
 // its launch, and the rows of its CTA.
 constexpr int kMostRows = 32;
-KvPlan kv_tiles_plan(const csa2_kv_cfg& cfg, int B, int T, int max_q, int64_t max_kv, bool cross, int most_parts);
+KvPlan kv_tiles_plan(const csa2_kv_cfg& cfg, int B, int T, int max_q, int64_t max_kv, bool cross, size_t room);
 cudaError_t launch_kv_tiles(const csa2_kv_cfg& cfg, int B, const KvAtt& a, cudaStream_t stream);
 // Bytes of the keys decoded for a call, or 0 where they are decoded in passing.
 size_t kv_plain_bytes(const csa2_kv_cfg& cfg, int B, int T, int max_q, int64_t max_kv, bool cross);

@@ -1,5 +1,5 @@
 // C ABI of the paged key / value operators: argument validation on the host,
-// then the launches of kv_append.cu and kv_rows.cu.
+// then the launches of kv_append.cu, kv_rows.cu and kv_tiles.cu.
 #include <cmath>
 #include <cstring>
 
@@ -67,22 +67,21 @@ int32_t attend(const csa2_kv_cfg* cfg, bool cross, int32_t B, int32_t T, const u
   a.causal = cross ? 0 : 1, a.max_q = (int)most, a.max_kv = max_kv;
   a.q = q, a.q_stride = q_stride, a.cu = cu, a.c = view_of(*cache), a.kv_len = kv_len, a.scale = scale;
   a.out = out, a.out_stride = out_stride, a.lse = lse, a.status = status;
-  const int64_t rows = (int64_t)T * cfg->n_heads;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   if (const size_t plain = kv_plain_bytes(*cfg, B, T, a.max_q, max_kv, cross); plain && plain <= workspace_bytes) {
     a.plain_k = ws, a.plain_v = ws + plain / 2, a.plain_pages = (max_kv + kPage - 1) / kPage;
     ws += plain, workspace_bytes -= plain;
   }
-  const size_t one = (size_t)rows * (cfg->head_dim + 1) * 4;
-  const size_t fit = workspace_bytes / one;
-  const KvPlan plan = kv_plan(*cfg, B, T, a.max_q, max_kv, cross, fit > 1024 ? 1024 : (int)fit);
+  KvPlan plan = kv_plan(*cfg, B, T, a.max_q, max_kv, cross, SIZE_MAX);
+  if (plan.bytes > workspace_bytes) plan = kv_plan(*cfg, B, T, a.max_q, max_kv, cross, workspace_bytes);
   if (plan.ctas > INT32_MAX) return CSA2_ERR_UNSUPPORTED;
   a.n_parts = plan.n_parts, a.by_parts = divisor(plan.n_parts), a.cluster = plan.cluster ? 1 : 0;
   a.part_pages = plan.part_pages, a.by_pages = divisor(plan.part_pages);
   a.tiles = (int)plan.tiles, a.whole = (int)plan.whole;
-  if (a.n_parts > 1 && !a.cluster) {
+  if (plan.bytes) {
+    a.part_step = plan.part_step, a.part_rows = plan.part_rows;
     a.part_o = reinterpret_cast<float*>(ws);
-    a.part_l = a.part_o + a.n_parts * rows * cfg->head_dim;
+    a.part_l = a.part_o + a.n_parts * a.part_step * cfg->head_dim;
   }
   return cuda_status(launch_kv_attend(*cfg, B, a, static_cast<cudaStream_t>(stream)));
 }
@@ -125,9 +124,7 @@ size_t csa2_kv_workspace_bytes(const csa2_kv_cfg* cfg, int32_t B, int32_t T, int
   size_t most = 0;
   for (const bool cross : {false, true}) {
     if (cross && cfg->window) break;
-    const KvPlan plan = kv_plan(*cfg, B, T, max_q, max_kv, cross, 1024);
-    size_t n = kv_plain_bytes(*cfg, B, T, max_q, max_kv, cross);
-    if (!plan.cluster && plan.n_parts > 1) n += (size_t)plan.n_parts * T * cfg->n_heads * (cfg->head_dim + 1) * 4;
+    const size_t n = kv_plain_bytes(*cfg, B, T, max_q, max_kv, cross) + kv_plan(*cfg, B, T, max_q, max_kv, cross, SIZE_MAX).bytes;
     if (n > most) most = n;
   }
   return most;

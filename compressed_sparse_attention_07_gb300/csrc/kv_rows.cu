@@ -504,7 +504,7 @@ __global__ void __launch_bounds__(Rows<D, kFp4, NT, kCluster>::kWarps * 32, Rows
       *reinterpret_cast<float2*>(joined + r * D + c) = make_float2(v0 * inv, v1 * inv);
       if (c == 0) part_l[r] = lse2;
     } else {
-      const int64_t pa = (int64_t)part * a.T * a.n_heads + at;
+      const int64_t pa = part * a.part_step + at;
       *reinterpret_cast<float2*>(a.part_o + pa * D + c) = make_float2(v0 * inv, v1 * inv);
       if (c == 0) a.part_l[pa] = lse2;
     }
@@ -572,11 +572,12 @@ __global__ void __launch_bounds__(256) kv_join_kernel(KvAtt a, int tile_rows, in
   kv_pages(a, group_of(a, tile0), group_of(a, last), rows, keys, p0, p1);
   const int n = kv_parts(a, p0, p1);
   if (n <= 1) return;
-  const int64_t at = (int64_t)(row0 + i) * a.n_heads + h, step = (int64_t)a.T * a.n_heads;
+  const int64_t at = (int64_t)(row0 + i) * a.n_heads + h, step = a.part_step;
+  const int64_t from = kv_part_row(a, id, r, tile0, at);
   // The outputs of eight parts are on their way while the maximum is formed, and of
   // the next eight while these are added.
   constexpr int kAhead = 8, kLane = D / 32;  // channels of a lane
-  const float* src = a.part_o + at * D + lane * kLane;
+  const float* src = a.part_o + from * D + lane * kLane;
   float x[kAhead][kLane];
   auto load = [&](int p0) {
 #pragma unroll
@@ -596,7 +597,7 @@ __global__ void __launch_bounds__(256) kv_join_kernel(KvAtt a, int tile_rows, in
   float top = -INFINITY;
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
-    lp[k] = lane + 32 * k < n ? a.part_l[(lane + 32 * k) * step + at] : -INFINITY;
+    lp[k] = lane + 32 * k < n ? a.part_l[(lane + 32 * k) * step + from] : -INFINITY;
     top = fmaxf(top, lp[k]);
   }
 #pragma unroll
@@ -667,10 +668,11 @@ int row_blocks(int64_t n) { return n <= 8 ? 1 : n <= 16 ? 2 : 4; }
 
 }  // namespace
 
-KvPlan kv_plan(const csa2_kv_cfg& cfg, int B, int T, int max_q, int max_kv, bool cross, int most_parts) {
+KvPlan kv_plan(const csa2_kv_cfg& cfg, int B, int T, int max_q, int max_kv, bool cross, size_t room) {
   const int group = cfg.n_heads / cfg.kv_heads;
-  if ((int64_t)max_q * group > kMostRows) return kv_tiles_plan(cfg, B, T, max_q, max_kv, cross, most_parts);
-  KvPlan plan = {1, 1, false, 0, 0, 0};
+  if ((int64_t)max_q * group > kMostRows) return kv_tiles_plan(cfg, B, T, max_q, max_kv, cross, room);
+  KvPlan plan = {1, 1, false, 0, 0, 0, (int64_t)T * cfg.n_heads, 0, 0};
+  const size_t part_bytes = (size_t)plan.part_step * (cfg.head_dim + 1) * 4;
   const int nt = row_blocks((int64_t)max_q * group);
   int64_t pages = ((int64_t)max_kv + kPage - 1) / kPage;
   if (cfg.window && !cross)  // max_q rows see window + max_q - 1 keys
@@ -692,7 +694,7 @@ KvPlan kv_plan(const csa2_kv_cfg& cfg, int B, int T, int max_q, int max_kv, bool
   for (int s = 1; s <= 128; ++s) {
     const int64_t pp = (pages + s - 1) / s, n = (base * s + sms - 1) / sms;
     if (s > 1 && pp < 4) break;
-    if (s <= most_parts || s == 1) {
+    if (s == 1 || s * part_bytes <= room) {
       const double c = std::max((double)n * (pp + 3), (double)((n + per_sm - 1) / per_sm) * ((pp + 3) / 4 * 10 + 8)) +
                        (s > 1 ? 10 : 0);
       if (c < cost * 0.999) cost = c, best = s, plan.cluster = false;
@@ -705,6 +707,7 @@ KvPlan kv_plan(const csa2_kv_cfg& cfg, int B, int T, int max_q, int max_kv, bool
   plan.part_pages = (int)((pages + best - 1) / best);
   plan.n_parts = (int)((pages + plan.part_pages - 1) / plan.part_pages);
   if (plan.n_parts == 1) plan.cluster = false;
+  if (plan.n_parts > 1 && !plan.cluster) plan.bytes = plan.n_parts * part_bytes;
   return plan;
 }
 

@@ -423,7 +423,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tiles_kernel(KvAtt a) {
     if (write) {
       const bool live = r < n_rows;
       const int i = row0 + (live ? group_of(a, r) : 0), h = kh * a.group + (live ? r - group_of(a, r) * a.group : 0);
-      const int64_t at = (int64_t)i * a.n_heads + h, pa = (int64_t)part * a.T * a.n_heads + at;
+      const int64_t at = (int64_t)i * a.n_heads + h, pa = part * a.part_step + kv_part_row(a, id, r, tile0, at);
       const bool whole = n_act <= 1;
       const float lse2 = l == 0.0f ? -INFINITY : m + log2f(l);
       if (live && (!turns || j == 0)) {
@@ -819,7 +819,12 @@ cudaError_t launch(int B, const KvAtt& a, cudaStream_t stream) {
 
 }  // namespace
 
-KvPlan kv_tiles_plan(const csa2_kv_cfg& cfg, int B, int T, int max_q, int64_t max_kv, bool cross, int most_parts) {
+// Partial outputs stand by row and head of the batch up to this many bytes of them, else
+// only the divided tiles' rows, tile by tile, where that is less: 2048 tokens on 16384 (64
+// over 8 heads of 128, 56 of 512 tiles in five parts) take 37 MB instead of 338.
+constexpr size_t kMostByRow = (size_t)64 << 20;
+
+KvPlan kv_tiles_plan(const csa2_kv_cfg& cfg, int B, int T, int max_q, int64_t max_kv, bool cross, size_t room) {
   const int group = cfg.n_heads / cfg.kv_heads;
   const int64_t rows = (int64_t)max_q * group;
   // at most: each sequence's longest, or what all rows fill and a last one each
@@ -835,14 +840,23 @@ KvPlan kv_tiles_plan(const csa2_kv_cfg& cfg, int B, int T, int max_q, int64_t ma
   // last 56 in five parts) take 733 us so and 797 us whole, three such sequences of
   // 512 tokens 628 and 665.
   const double read = 2.5 * std::min<int64_t>(rows, kCtaRows) / kCtaRows / slots;
+  const int64_t tile_rows = std::min<int64_t>(rows, kCtaRows), all = (int64_t)T * cfg.n_heads;
+  const size_t row_bytes = (size_t)(cfg.head_dim + 1) * 4;
+  // rows of a part, with `rest` tiles divided in s; by_tile: tile by tile
+  auto part_step = [&](int64_t s, int64_t rest, bool* by_tile) {
+    *by_tile = rest * tile_rows < all && s * all * row_bytes > std::min(room, kMostByRow);
+    return *by_tile ? rest * tile_rows : all;
+  };
   int64_t best = 1, whole = 0;
+  bool by_tile = false;
   double cost = 1e30;
-  for (int64_t s = 1; s <= std::max(most_parts, 1) && s <= 64; ++s) {
+  for (int64_t s = 1; s <= 64; ++s) {
     const int64_t n = (steps + s - 1) / s;
     if (s > 1 && n < 2) break;
     for (const int64_t w : {(int64_t)0, base / slots * slots}) {
       const int64_t rest = base - w;
       if (w && (s == 1 || rest == 0)) continue;
+      if (s > 1 && s * part_step(s, rest, &by_tile) * row_bytes > room) continue;
       const double c = (double)(w / slots) * (steps + 3) + (double)((rest * s + slots - 1) / slots) * (n + 3) +
                        (s > 1 ? 2 + read * rest * s : 0);
       if (c < cost * 0.999) cost = s == 1 ? 0.97 * c : c, best = s, whole = w;
@@ -851,7 +865,9 @@ KvPlan kv_tiles_plan(const csa2_kv_cfg& cfg, int B, int T, int max_q, int64_t ma
   const int64_t per = (steps + best - 1) / best, parts = (steps + per - 1) / per;
   if (parts == 1) whole = 0;
   const int64_t ctas = whole + (base - whole) * std::max<int64_t>(parts, parts > 1 ? kCtaRows / 8 : 1);
-  return KvPlan{(int)parts, (int)(2 * per), false, base, whole, ctas};
+  const int64_t step = part_step(parts, base - whole, &by_tile);
+  return KvPlan{(int)parts, (int)(2 * per), false, base, whole, ctas, step, by_tile ? (int)tile_rows : 0,
+                parts > 1 ? parts * step * row_bytes : 0};
 }
 
 cudaError_t launch_kv_tiles(const csa2_kv_cfg& cfg, int B, const KvAtt& a, cudaStream_t stream) {

@@ -712,3 +712,38 @@ def test_append_encodes_as_the_oracle_at_every_border(tokens, dim):
         assert len(np.unique(sc)) == 127  # every scale
         assert np.array_equal(gsc, sc) and np.array_equal(gcodes, codes)
         assert np.array_equal(plain.double().cpu().numpy(), val)
+
+
+@pytest.mark.parametrize("dtype", [FP4, BF16])
+def test_workspace_of_the_divided_tiles_alone(dtype):
+    """208 row tiles, of which one wave is not divided: a workspace that holds the partial outputs of the others' rows
+    gives what a larger one does, bit for bit, a smaller one other parts, and nothing is written behind any."""
+    rng = np.random.default_rng(15)
+    cfg, n, keys = csa.KVCfg(256, 16, 64, dtype), 208, 2700
+    cache = _cache(cfg, 1, keys)
+    stored = []
+    for kind in "kv":
+        x = _kv.normal(rng, keys, 16, 64)
+        _kv.fill(cache, cfg, 0, kind, x)
+        stored.append(torch.from_numpy(_kv.fp4_round(x)[0] if dtype == FP4 else x).cuda())
+    q = _dev(_kv.normal(rng, n, 256, 64))
+    want = _kv.attend_sums(q, *stored, 1 / 8, True)
+    lens = torch.tensor([keys], dtype=torch.int32, device="cuda")
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    need, row = csa.kv_workspace_bytes(cfg, 1, n, n, keys), 65 * 4
+    parts, rest = need // (n * 256 * row), n % sms
+    assert parts >= 2 and need == parts * n * 256 * row and 0 < rest < n
+    results = []
+    for size in (need, parts * rest * 256 * row, parts * rest * 256 * row - 256, 2 * 256 * row, 0):
+        ws = torch.full((size + 4096,), 0xFF, dtype=torch.uint8, device="cuda")
+        out, lse, st = torch.empty_like(q), torch.empty(n, 256, device="cuda"), _status()
+        csa.kv_attend(cfg, q, _cu([n]), cache, lens, n, keys, out, lse=lse, workspace=ws[:size] if size else None, status=st)
+        assert int(st.item()) == 0 and (ws[size:] == 0xFF).all()
+        results.append((out, lse))
+    assert torch.equal(results[0][0], results[1][0]) and torch.equal(results[0][1], results[1][1])
+    assert not torch.equal(results[0][1], results[4][1])  # divided or not, the sums go another way
+    for out, lse in results:
+        each, rms = _kv.far(cfg, keys, out, *want)
+        assert each < 1 and rms < 1
+        # two fp32 sums of the same weights
+        assert (lse - results[0][1]).abs().max() <= 2 * (2 * keys + 64) * 2.0 ** -24

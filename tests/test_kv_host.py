@@ -229,3 +229,24 @@ def test_long_comparison_sees_a_lost_page(dtype, dim, keys):
     assert _kv.far(cfg, keys, _rounded_attention(cfg, q, k, w, scale), *want)[1] > 1
     twice = _rounded_attention(cfg, q, torch.cat((k, k[:256])), torch.cat((v, v[:256])), scale)
     assert _kv.far(cfg, keys, twice, *want)[1] > 1
+
+
+@pytest.mark.parametrize("tokens,keys", [(2048, 16384), (2048, 18432), (4000, 131072), (8192, 32768), (1999, 100000)])
+@pytest.mark.parametrize("dtype", [csa.CACHE_FP4, csa.CACHE_BF16])
+def test_workspace_holds_the_divided_tiles_alone(tokens, keys, dtype):
+    # 64 over 8 heads of 128, 256 rows a tile: fewer row tiles than the GPU has SMs are divided, in 64 parts at most;
+    # partial outputs of every row would be 33 KB a token and part
+    c = csa.KVCfg(64, 8, 128, dtype)
+    pages = -(-keys // 64) * 8 * 2 * 64 * 128 * 2 if dtype == csa.CACHE_FP4 else 0
+    need = csa.kv_workspace_bytes(c, 1, tokens, tokens, keys) - (pages if pages <= 2 << 30 else 0)
+    assert 0 <= need <= max(64 << 20, 64 * 160 * 256 * 129 * 4)
+    every = tokens * 64 * 129 * 4
+    assert need <= 64 << 20 or need < every
+
+
+@pytest.mark.parametrize("batch,tokens,max_q,keys", [(1, 2048, 2048, 18432), (3, 900, 700, 5000), (48, 48, 1, 16384),
+                                                     (8, 40, 5, 32768), (2, 300, 290, 9000)])
+def test_workspace_grows_with_no_size_left_out(batch, tokens, max_q, keys):
+    """Multiples of a row's partial outputs, whichever way they stand."""
+    c = csa.KVCfg(64, 8, 128, csa.CACHE_BF16)
+    assert csa.kv_workspace_bytes(c, batch, tokens, max_q, keys) % (129 * 4) == 0

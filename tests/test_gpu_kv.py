@@ -747,3 +747,105 @@ def test_workspace_of_the_divided_tiles_alone(dtype):
         assert each < 1 and rms < 1
         # two fp32 sums of the same weights
         assert (lse - results[0][1]).abs().max() <= 2 * (2 * keys + 64) * 2.0 ** -24
+
+
+# ------------------------------------------------------- the largest of each --
+
+@pytest.mark.parametrize("dtype", [FP4, BF16])
+@pytest.mark.parametrize("dim,hq,hkv", [(64, 1024, 1024), (64, 1024, 1), (128, 1000, 8), (128, 1024, 64)])
+def test_the_most_heads(dtype, dim, hq, hkv):
+    _attend_case(csa.KVCfg(hq, hkv, dim, dtype), [1, 0, 2], [130, 5, 64], seed=hq + hkv)
+    _append_case(dtype, dim, hq, hkv, 64, INTER, [3, 0, 1, 2, 4], [0, 5, 63, 60, 128])
+
+
+@pytest.mark.parametrize("dtype", [FP4, BF16])
+@pytest.mark.parametrize("longest", [1, 40])
+def test_the_most_sequences(dtype, longest):
+    """65535 sequences of 0 to 3 keys with a token each (and one of 40): appended, then attended."""
+    B, dim = 65535, 64
+    cfg = csa.KVCfg(1, 1, dim, dtype, rope_dims=0)
+    g = torch.Generator(device="cuda").manual_seed(longest)
+    cache = csa.KVCache(cfg, B, 64)
+    cache.block_table.copy_(torch.randperm(B, generator=g, device="cuda", dtype=torch.int32)[:, None])
+    n = torch.randint(0, 4, (B,), generator=g, device="cuda", dtype=torch.int32)
+    n[B - 5] = longest if longest > 1 else 1
+    cu = torch.cat((n.new_zeros(1), n.cumsum(0).int()))
+    T = int(cu[-1])
+    k, v, q = (torch.randn(m, 1, dim, generator=g, device="cuda", dtype=torch.bfloat16) for m in (T, T, B - 1 + longest))
+    sk, sv, st = torch.empty_like(k), torch.empty_like(v), _status()
+    csa.kv_append(cfg, k, v, cu, torch.zeros(B, dtype=torch.int64, device="cuda"), cache, k_out=sk, v_out=sv, status=st)
+    rows = torch.ones_like(n)
+    rows[B - 5] = longest
+    cq = torch.cat((n.new_zeros(1), rows.cumsum(0).int()))
+    out, lse = torch.full_like(q, 7.0), torch.full((len(q), 1), 7.0, device="cuda")
+    csa.kv_attend(cfg, q, cq, cache, n, longest, 64, out, lse=lse, status=st)
+    assert int(st.item()) == 0
+    seq = torch.repeat_interleave(torch.arange(B, device="cuda"), rows.long())
+    pos = n[seq] - rows[seq] + (torch.arange(len(q), device="cuda") - cq[seq])
+    at = torch.arange(longest if longest > 3 else 3, device="cuda")
+    see = at <= pos[:, None]
+    idx = (cu[seq][:, None] + at).clamp(max=T - 1).long()
+    x = torch.einsum("td,tjd->tj", q[:, 0].double(), sk[idx, 0].double()) / 8
+    p = torch.softmax(x.masked_fill(~see, -math.inf), 1).nan_to_num(0)
+    want = torch.einsum("tj,tjd->td", p, sv[idx, 0].double())
+    mag = torch.einsum("tj,tjd->td", p, sv[idx, 0].double().abs())
+    empty = ~see.any(1)
+    assert (lse[empty] == -math.inf).all() and (out[empty] == 0).all()
+    # weights within 2^-8 of themselves, the output within 2^-8, logits (below 2^5) within a few steps of 2^-24
+    assert ((out[:, 0].double() - want).abs() <= 2.0 ** -8 * (want.abs() + 1.01 * mag) + 2.0 ** -14 * mag + 1e-30).all()
+    wl = torch.logsumexp(x.masked_fill(~see, -math.inf), 1)
+    assert ((lse[:, 0] - wl)[~empty].abs() <= 2.0 ** -14).all()
+
+
+@pytest.mark.parametrize("dtype", [FP4, BF16])
+@pytest.mark.parametrize("nq", [1, 20])
+def test_rows_further_apart_than_32_bits_and_ahead_of_the_first_sequence(dtype, nq):
+    """Rows of q, k, v, their outputs and out 2^30 + 8 elements apart, and rows ahead of cu[0] that are left alone."""
+    cfg, rng = csa.KVCfg(4, 2, 64, dtype, rope_dims=0), np.random.default_rng(nq)
+    T, step = nq + 3, (1 << 30) + 8 if nq == 1 else (1 << 28) + 8
+    room = [torch.empty((T - 1) * step + 512, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    q, out = (r.as_strided((T, 4, 64), (step, 64, 1)) for r in room)
+    k, v = (room[0].as_strided((T, 2, 64), (step, 64, 1), 256 + 128 * i) for i in (0, 1))
+    hq, hk, hv = (_kv.normal(rng, T, h, 64) for h in (4, 2, 2))
+    for t, x in ((q, hq), (k, hk), (v, hv)):
+        t.copy_(_dev(x))
+    out.fill_(7.0)
+    cache = _cache(cfg, 1, 200)
+    ks, vs = ([_kv.fp4_round(x)[0] if dtype == FP4 else x for x in (_kv.normal(rng, 100, 2, 64), y[2:T - 1])]
+              for y in (hk, hv))
+    for kind, x in (("k", ks), ("v", vs)):
+        _kv.fill(cache, cfg, 0, kind, x[0])
+    cu = torch.tensor([2, T - 1], dtype=torch.int32, device="cuda")
+    st = _status()
+    csa.kv_append(cfg, k, v, cu, torch.tensor([100], device="cuda"), cache, status=st)
+    csa.kv_attend(cfg, q, cu, cache, torch.tensor([100 + nq], dtype=torch.int32, device="cuda"), nq, 200, out, status=st)
+    assert int(st.item()) == 0 and (out[:2] == 7).all() and (out[T - 1:] == 7).all()
+    want = _kv.attend(hq[2:T - 1], np.concatenate(ks), np.concatenate(vs), 1 / 8, True)
+    assert (np.abs(out[2:T - 1].double().cpu().numpy() - want[0]) <= _kv.tolerances(cfg, 100 + nq, *want)[0]).all()
+
+
+@pytest.mark.parametrize("dtype", [FP4, BF16])
+@pytest.mark.parametrize("hq,hkv,nq", [(4, 2, 1), (4, 2, 5), (4, 2, 150), (128, 1, 45)])
+@pytest.mark.parametrize("window", [1, 100, 128])
+def test_pages_behind_the_window_may_be_gone(dtype, hq, hkv, nq, window):
+    """Pages that no row's window reaches are not asked for: their places in the block table may name none."""
+    rng = np.random.default_rng(nq + window)
+    cfg = csa.KVCfg(hq, hkv, 64, dtype, window=window)
+    kv, B = [1000, 64 + nq, 333], 3
+    cache = _cache(cfg, B, 1000)
+    for b, n in enumerate(kv):
+        for kind in "kv":
+            _kv.fill(cache, cfg, b, kind, _kv.normal(rng, n, hkv, 64))
+    q, cu, lens = _dev(_kv.normal(rng, B * nq, hq, 64)), _cu([nq] * B), torch.tensor(kv, dtype=torch.int32, device="cuda")
+    ws = torch.empty(csa.kv_workspace_bytes(cfg, B, B * nq, nq, 1000), dtype=torch.uint8, device="cuda")
+    results = []
+    for gone in (False, True):
+        if gone:
+            for b, n in enumerate(kv):
+                cache.block_table[b, :max(0, n - nq + 1 - window) // 64] = -1
+                cache.block_table[b, -(-n // 64):] = 10 ** 9
+        out, st = torch.empty_like(q), _status()
+        csa.kv_attend(cfg, q, cu, cache, lens, nq, 1000, out, workspace=ws, status=st)
+        assert int(st.item()) == 0
+        results.append(out)
+    assert torch.equal(*results) and torch.isfinite(out.float()).all()

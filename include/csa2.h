@@ -352,11 +352,11 @@ CSA2_API int32_t csa2_layer(const csa2_cfg* cfg, int32_t mode, csa2_group_state*
                    const csa2_layer_io* io, void* stream);
 
 /* ---- layers that keep whole keys and values ----
- * The model's first two layers and its draft layers carry no compressor
- * (compress ratio 0, config list of hn.213312.xyz sec. 1.2), a decoder attends
- * to its encoder's states (CED, sec. 2.2), and the layers of other models that
- * are served beside it are ordinary grouped-query layers: each kv head keeps
- * one key and one value per token.  Three calls serve them over one paged
+ * For the layers of other models that are served beside this one (a draft
+ * model's, an encoder-decoder's): ordinary grouped-query layers, whose kv heads
+ * each keep one key and one value per token.  (This model's own layers do not
+ * use them: those without a compressor attend to a window of 512-channel
+ * latents with key = value, csa2_attend.)  Three calls serve them over one paged
  * cache, in the codec and page size of the latent caches:
  *   csa2_kv_append        rotates new queries and keys, encodes keys and
  *                         values and writes them to their pages;

@@ -426,8 +426,8 @@ CSA2_API size_t csa2_kv_page_bytes(const csa2_kv_cfg* cfg, int32_t which);
  * queries are rounded to bf16 in q_out, which may be q itself.  k_out and
  * v_out [T][kv_heads][head_dim], either or both NULL, receive the values as
  * stored (FP4 values are exact in bf16).  A value that is not finite after the
- * rotation sets CSA2_ERR_RANGE and is stored as the largest of its sign, NaN
- * as 0, so that a cache never holds one.
+ * rotation, or past bf16's largest, sets CSA2_ERR_RANGE and is stored as the
+ * largest of its sign, NaN as 0, so that a cache never holds one.
  * q and q_out may both be NULL (then n_heads is not used); rope is NULL
  * if and only if rope_dims is 0. */
 CSA2_API int32_t csa2_kv_append(const csa2_kv_cfg* cfg, int32_t B, int32_t T, const uint16_t* q, int64_t q_stride,
@@ -440,9 +440,9 @@ CSA2_API int32_t csa2_kv_append(const csa2_kv_cfg* cfg, int32_t B, int32_t T, co
  * the keys of these sizes among CTAs, and decode FP4 pages that many rows read
  * once ahead, as they would best (0 where that needs none); they take any
  * workspace (NULL included) and do less of it where it is smaller: outputs may
- * then differ by the order of fp32 sums.  Its contents need not be kept between calls.  Two calls that may
- * overlap (other streams, graphs replayed at once) need workspaces of their
- * own. */
+ * then differ by the order of fp32 sums.  Its contents need not be kept between
+ * calls.  Two calls that may overlap (other streams, graphs replayed at once)
+ * need workspaces of their own. */
 CSA2_API size_t csa2_kv_workspace_bytes(const csa2_kv_cfg* cfg, int32_t B, int32_t T, int32_t max_q, int32_t max_kv);
 
 /* Attention over the cache: head h reads kv head h / (n_heads / kv_heads),
@@ -457,9 +457,12 @@ CSA2_API size_t csa2_kv_workspace_bytes(const csa2_kv_cfg* cfg, int32_t B, int32
  * grid).  q and out must not overlap.  Queries, logits' factors and weights: over
  * FP4 caches the products multiply f16 (queries relative to a power of two of
  * their row, exact but for channels below 2^-14 of its largest; weights
- * rounded to f16), over bf16 caches bf16; all sums are fp32.  A page whose id is outside the pool counts as not seen.  Cache slots
- * from kv_len on may hold anything.  A query row that is not finite yields NaN
- * or unspecified values in its own outputs alone. */
+ * rounded to f16), over bf16 caches bf16; all sums are fp32.  A page whose id is
+ * outside the pool counts as not seen.  Cache slots from kv_len on may hold
+ * anything, those before it finite values, as csa2_kv_append leaves them: a
+ * value that is not finite may make NaN of rows that do not see it but share
+ * its page.  A query row that is not finite yields NaN or unspecified values in
+ * its own outputs alone. */
 CSA2_API int32_t csa2_kv_attend(const csa2_kv_cfg* cfg, int32_t B, int32_t T, const uint16_t* q, int64_t q_stride,
                                 const int32_t* cu, const csa2_kv_cache* cache, const int32_t* kv_len, int32_t max_q,
                                 int32_t max_kv, float scale, uint16_t* out, int64_t out_stride, float* lse,

@@ -158,7 +158,8 @@ __device__ __forceinline__ bool kv_sequence(const KvAtt& a, int b, int& row0, in
 // tiles from the last (the longest) on.  Sequences have what tiles their rows fill, so
 // that a batch of one prompt and many single tokens is not a grid of empty CTAs (4096
 // tokens and 63 single ones, 64 over 8 heads of 128: 792 us with the longest's tiles
-// for each, 377 so; four prompts of 700 .. 1500: 132 and 134).  The whole warp; false behind the last tile; sequences out of bounds have none (status set).
+// for each, 376 so; four prompts of 700 .. 1500: 132 and 132).  The whole warp; false
+// behind the last tile; sequences out of bounds have none (status set).
 __device__ __forceinline__ bool kv_tile(const KvAtt& a, int tile_rows, int id, int& b, int& kh, int& tile) {
   const int lane = threadIdx.x & 31, want = quotient(id, a.by_heads);
   int before = 0;  // tiles of a kv head so far

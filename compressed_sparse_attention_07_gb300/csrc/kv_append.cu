@@ -29,9 +29,10 @@ namespace csa2 {
 namespace {
 
 constexpr int kThreads = 256;
-// Pieces an SM from which the stream kernel is the faster: 600 tokens of 64 + 2 x 8
-// heads of 128 take 8.5 us in the first kernel and 8.9 us in it, 1300 take 16.2
-// and 14.7 us; 1000 of 32 + 2 x 4 heads of 64 take 5.7 and 6.0 us, 2000 9.5 and 8.8.
+// Pieces an SM from which the stream kernel is the faster: 1000 tokens of 64 + 2 x 8
+// heads of 128 in FP4 take 13.0 us in the first kernel and 13.7 us in it, 1300 take
+// 16.6 and 15.8 us; 1000 of 32 + 2 x 4 heads of 64 in bf16 5.4 and 5.8 us, 2000 9.0
+// and 8.5 (GPU time in graphs of calls on rows of their own, as below).
 constexpr int kFewItems = 8;
 
 struct AppendArgs {
@@ -433,7 +434,7 @@ cudaError_t launch_kv_append(const csa2_kv_cfg& cfg, int B, int T, const uint16_
   const int64_t pieces = (int64_t)T * ((rows + piece_rows - 1) / piece_rows);
   if (pieces >= kFewItems * num_sms()) {
     // four small tokens to a piece where they fit: 4096 tokens of 24 + 2 x 8 heads of
-    // 64 take 19 us so and 25 us one by one, 16000 take 42 and 68 us
+    // 64 in FP4 take 14.0 us so and 19.9 us one by one, 16000 take 37.5 and 65.2 us
     const bool small = kSmall * (rows + 2) <= piece_rows + 2;
 #define CSA2_STREAM(D, F)                                                     \
   (small ? stream_of<D, F, kSmall>(a, (T + kSmall - 1) / kSmall, stream)      \
@@ -444,8 +445,8 @@ cudaError_t launch_kv_append(const csa2_kv_cfg& cfg, int B, int T, const uint16_
   }
   const int per_pass = kThreads / (cfg.head_dim / 8), passes = (rows + per_pass - 1) / per_pass;
   // one pass a CTA while the passes do not fill the GPU, two beyond: 32 tokens of 128 +
-  // 2 x 16 heads of 128 take 2.6 us by one and 3.0 by two, 300 tokens of 32 + 2 x 4
-  // heads of 64 (600 passes) 3.2 and 2.9
+  // 2 x 16 heads of 128 (320 passes) take 2.6 us by one and 3.1 by two, 200 tokens of 64
+  // + 2 x 8 heads of 128 (1000 passes) 5.1 and 4.4
   const bool few = (int64_t)T * passes <= 3 * num_sms();
   const dim3 grid(T, few ? passes : (passes + 1) / 2), block(kThreads);
 #define CSA2_APPEND(D, F)                                                          \

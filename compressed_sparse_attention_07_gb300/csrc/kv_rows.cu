@@ -23,13 +23,14 @@
 // conflicts.  Key nibbles convert in place; value nibbles of two keys are first
 // brought into one byte, which then converts to the pair the second product
 // wants.  E2M1 x E4M3 is exact in f16; a query row is scaled by a power of two
-// to below 1 (its inverse goes into the softmax scale), so bf16 queries of any
-// size are exact too (channels below 2^-14 of the row's largest lose bits).
+// so that its largest channel lies in [1, 2) (below 4 at the end of bf16's range;
+// the inverse goes into the softmax scale), so bf16 queries of any size are exact
+// too (channels below 2^-14 of the row's largest lose bits).
 //
 // Measured: one token of each of 32 sequences of 32767, 64 over 8 heads of 128, FP4:
-// 215 us, 5.6 TB/s (83 % of a copy's rate; 1188 instructions a page and head keep
+// 214 us, 5.7 TB/s (84 % of a copy's rate; 1180 instructions a page and head keep
 // the ALU at 50 %); of 48 sequences of 0 .. 16383, 28 over 4 heads of 64, bf16: 70 us,
-// 5.7 TB/s; of one sequence of 4095: 7.4 us in a graph, launches and look-ups mostly.
+// 5.7 TB/s; of one sequence of 4095: 7.7 us in a graph, launches and look-ups mostly.
 #include <algorithm>
 
 #include "kv.cuh"

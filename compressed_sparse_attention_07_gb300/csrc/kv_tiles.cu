@@ -27,12 +27,13 @@
 // 1), which after the first keys is rare.  Query rows over FP4 caches are
 // scaled by a power of two as in kv_rows.cu.
 //
-// Measured, 64 over 8 heads of 128: 2048 tokens on 16384, FP4 811 us, 1.44 PFLOP/s
-// (tensor pipe 74 % of the busiest SM's cycles); two such in bf16 1.39 ms, 1.67 PFLOP/s.
-// 128 keys of 256 rows are 2048 cycles of products; the rest is the way from one
-// product through the softmax to the other, which the other place's products cover
-// only in part.  Drafts of 5 tokens on 8 x 32763, FP4: 149 us, a key tile of 128 in
-// 2200 cycles of decoding and of the operands' way through shared memory (1600).
+// Measured, 64 over 8 heads of 128 (calls back to back): 2048 tokens on 16384 811 us in
+// FP4, 1.44 PFLOP/s (tensor pipe 74 % of the busiest SM's cycles), 835 us in bf16, two
+// such in bf16 1.64 ms, 1.43 PFLOP/s.  128 keys of 256 rows are 2048 cycles of products;
+// the rest is the way from one product through the softmax to the other, which the other
+// place's products cover only in part.  Drafts of 5 tokens on 8 x 32763, FP4: 150 us, a
+// key tile of 128 in 2200 cycles of decoding and of the operands' way through shared
+// memory (1600).
 #include <algorithm>
 
 #include "kv.cuh"
@@ -70,8 +71,9 @@ struct Tiles {
 // Rows that read a key (of a sequence of mean length) from which FP4 pages are decoded once for the call, into the
 // workspace (up to kMostPlain bytes of it).  Decoding in every CTA takes issue slots
 // from the softmax beside it; ahead, a write and reads from L2.  64 over 8 heads of
-// 128 on 16384 keys, in passing / ahead: 256 tokens (2048 rows) 152 / 157 us, 512
-// 239 / 228, 2048 879 / 797; 2 x 4096 on themselves 547 / 495.
+// 128 on 16384 keys, in passing / ahead: 256 tokens (2048 rows) 138 / 142 us, 512
+// 233 / 225, 2048 (keys not divided) 947 / 872; 2 x 4096 on themselves 527 / 480 (GPU
+// time in graphs of calls, as at the plan below).
 constexpr int64_t kPlainRows = 4096;
 constexpr size_t kMostPlain = (size_t)2 << 30;
 
@@ -836,9 +838,9 @@ KvPlan kv_tiles_plan(const csa2_kv_cfg& cfg, int B, int T, int max_q, int64_t ma
   // The number of parts whose waves of CTAs end soonest, in key tiles: a CTA's start
   // and end cost about three, the joining kernel two and its reading two and a half
   // for each CTA of an SM.  Divided are all row tiles, or those of the last wave, if
-  // it wins 3 %: 2048 tokens on 16384 (64 over 8 heads of 128, FP4; 512 tiles, the
-  // last 56 in five parts) take 733 us so and 797 us whole, three such sequences of
-  // 512 tokens 628 and 665.
+  // it wins 3 %: 2048 tokens on 16384 (64 over 8 heads of 128, FP4 decoded ahead; 512
+  // tiles, the last 56 in five parts) take 806 us so and 872 us whole, three such
+  // sequences of 512 tokens 637 and 665.
   const double read = 2.5 * std::min<int64_t>(rows, kCtaRows) / kCtaRows / slots;
   const int64_t tile_rows = std::min<int64_t>(rows, kCtaRows), all = (int64_t)T * cfg.n_heads;
   const size_t row_bytes = (size_t)(cfg.head_dim + 1) * 4;

@@ -376,10 +376,11 @@ __global__ void __launch_bounds__(kThreads, 1) kv_tiles_kernel(KvAtt a) {
     }
     bool write = false;  // the products are over and this warp has rows
     if (warp_live && ok) {
-      if (n_it > 0) {
-        if (!turns) ok = tc::mbar_wait(&o_full[j], 0);
-        else ok = tc::mbar_wait(&o_full[0], 0) && (n_it < 2 || tc::mbar_wait(&o_full[1], 0));
-      }
+      // The outputs pass through the queries' place: the products have read them, or
+      // (rows that see nothing) every warp has stored its own.
+      if (n_it == 0) ok = tc::mbar_wait(&q_full, 0);
+      else if (!turns) ok = tc::mbar_wait(&o_full[j], 0);
+      else ok = tc::mbar_wait(&o_full[0], 0) && (n_it < 2 || tc::mbar_wait(&o_full[1], 0));
       ok = __all_sync(0xffffffffu, ok);
       write = ok;
       tc::fence_after_sync();

@@ -849,3 +849,31 @@ def test_pages_behind_the_window_may_be_gone(dtype, hq, hkv, nq, window):
         assert int(st.item()) == 0
         results.append(out)
     assert torch.equal(*results) and torch.isfinite(out.float()).all()
+
+
+@pytest.mark.parametrize("dtype", [FP4, BF16])
+@pytest.mark.parametrize("dim,hq,hkv", [(64, 1024, 16), (128, 56, 8), (64, 640, 5)])
+def test_row_tiles_that_see_nothing_at_all(dtype, dim, hq, hkv):
+    """Prompts with fewer keys than rows, and without any: no product runs in the row tiles that see none, and their
+    rows are 0 whatever the queries are."""
+    cfg = csa.KVCfg(hq, hkv, dim, dtype)
+    kv, nq = [20, 0, 3, 0], [100, 90, 47, 100]
+    cache = _cache(cfg, 4, 64, seed=hq)
+    rng = np.random.default_rng(dim)
+    for b, n in enumerate(kv):
+        for kind in "kv":
+            if n:
+                _kv.fill(cache, cfg, b, kind, _kv.normal(rng, n, hkv, dim))
+    g = torch.Generator(device="cuda").manual_seed(7)
+    q = torch.randn(sum(nq), hq, dim, generator=g, device="cuda", dtype=torch.bfloat16)
+    lens = torch.tensor(kv, dtype=torch.int32, device="cuda")
+    at = np.cumsum([0] + nq)
+    for call in (csa.kv_attend, csa.kv_cross_attend):
+        for _ in range(5):
+            out, lse, st = torch.full_like(q, 7.0), torch.full((sum(nq), hq), 7.0, device="cuda"), _status()
+            call(cfg, q, _cu(nq), cache, lens, 100, 20, out, lse=lse, status=st)
+            assert int(st.item()) == 0
+            for b, (n, keys) in enumerate(zip(nq, kv)):
+                none = n if keys == 0 else n - keys if call is csa.kv_attend else 0
+                assert (lse[at[b]:at[b] + none] == -math.inf).all() and (out[at[b]:at[b] + none] == 0).all()
+                assert torch.isfinite(lse[at[b] + none:at[b + 1]]).all() and torch.isfinite(out[at[b]:at[b + 1]].float()).all()

@@ -98,3 +98,23 @@ def test_every_page_answers(dtype, shape, cross, workspace):
         # unrounded), the output's (2^-8), both of the value, and the others' 2^-20 of values up to 6
         far = (out.double() - want.double()).abs() / (2.01 * 2.0 ** -8 * want.double().abs() + 2.0 ** -17)
         assert far.max().item() <= 1, "%.3g" % far.max().item()
+
+
+@pytest.mark.parametrize("dtype", [FP4, BF16])
+@pytest.mark.parametrize("dim,group,nq", [(64, 8, 1), (128, 32, 1), (64, 4, 10), (128, 2, 200)])
+def test_a_million_keys(dtype, dim, group, nq):
+    cfg, keys, cross = csa.KVCfg(group, 1, dim, dtype, rope_dims=0), 1000003, nq > 1
+    cache, (k, v) = _cache(cfg, [keys], dim + nq)
+    g = torch.Generator(device="cuda").manual_seed(nq)
+    q = torch.randn(nq, group, dim, generator=g, device="cuda", dtype=torch.bfloat16)
+    some = min(nq, 8)  # rows that are compared in full, the last ones
+    out = _call(cfg, cache, q, [nq], [keys], cross, True, dim ** -0.5)
+    want = _kv.attend_sums(q[nq - some:], k, v, dim ** -0.5, not cross)
+    each, rms = _kv.far(cfg, keys, out[nq - some:], *want)
+    assert each < 1 and rms < 1, "%.3g and %.3g of what roundings allow" % (each, rms)
+    at = np.random.default_rng(dim).integers(0, keys - nq, nq * group)
+    at[:3] = 0, keys - nq, keys // 2 // 64 * 64
+    at = torch.from_numpy(at.reshape(nq, group)).cuda()
+    picked = _call(cfg, cache, k[at, 0] * 4, [nq], [keys], cross, True, 1.0)
+    value = v[at, 0].double()
+    assert ((picked.double() - value).abs() <= 2.01 * 2.0 ** -8 * value.abs() + 2.0 ** -17).all()

@@ -460,8 +460,8 @@ CSA2_API size_t csa2_kv_workspace_bytes(const csa2_kv_cfg* cfg, int32_t B, int32
  * rounded to f16), over bf16 caches bf16; all sums are fp32.  A page whose id is
  * outside the pool counts as not seen.  Cache slots from kv_len on may hold
  * anything, those before it finite values, as csa2_kv_append leaves them: a
- * value that is not finite may make NaN of rows that do not see it but share
- * its page.  A query row that is not finite yields NaN or unspecified values in
+ * value that is not finite may make NaN of rows of its sequence that do not see
+ * it.  A query row that is not finite yields NaN or unspecified values in
  * its own outputs alone. */
 CSA2_API int32_t csa2_kv_attend(const csa2_kv_cfg* cfg, int32_t B, int32_t T, const uint16_t* q, int64_t q_stride,
                                 const int32_t* cu, const csa2_kv_cache* cache, const int32_t* kv_len, int32_t max_q,

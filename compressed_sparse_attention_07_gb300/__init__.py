@@ -21,6 +21,7 @@ __all__ = [
     "MODE_REINDEX", "MODE_REUSE", "PAGE", "library_path", "capture", "swa_encode", "CACHE_FP4_S32",
     "FMT_IDX_68B", "FMT_SWA_FP8", "FMT_IDX_QFP4", "SWA_FP8_ROW", "KVCfg", "KVCache", "kv_append", "kv_attend",
     "kv_cross_attend", "kv_workspace_bytes", "rope_table", "ROPE_INTERLEAVED", "ROPE_HALF",
+    "kv_append_axes", "kv_reorder", "beam_select", "beam_workspace_bytes", "Fp4Weights", "fp4_linear",
 ]
 
 CACHE_FP4, CACHE_BF16, CACHE_FP4_S32 = 0, 1, 2
@@ -88,6 +89,10 @@ class KVCfg(C.Structure):
         super().__init__(n_heads, kv_heads, head_dim, cache_dtype, window, rope_dims, rope_style, 0)
 
 
+class _Fp4Desc(C.Structure):
+    _fields_ = [("data", C.c_void_p), ("n", C.c_int32), ("k", C.c_int32), ("alpha", C.c_float), ("reserved", C.c_int32)]
+
+
 class _KVCacheDesc(C.Structure):
     _fields_ = [("k_data", C.c_void_p), ("k_scales", C.c_void_p), ("v_data", C.c_void_p), ("v_scales", C.c_void_p),
                 ("block_table", C.c_void_p), ("max_pages", C.c_int32), ("num_pages", C.c_int32)]
@@ -141,6 +146,23 @@ def load():
         L.csa2_kv_append.restype = i32
         L.csa2_kv_append.argtypes = [kvc, i32, i32, vp, i64, vp, i64, vp, i64, vp, vp, vp, i64, kvd, vp, i64, vp, vp,
                                      vp, vp]
+        L.csa2_kv_append_axes.restype = i32
+        L.csa2_kv_append_axes.argtypes = [kvc, i32, i32, vp, i64, vp, i64, vp, i64, vp, vp, vp, i32, C.c_char_p, vp, i64,
+                                          kvd, vp, i64, vp, vp, vp, vp]
+        L.csa2_kv_reorder.restype = i32
+        L.csa2_kv_reorder.argtypes = [kvc, i32, vp, i32, i32, vp, vp, vp, vp]
+        L.csa2_beam_workspace_bytes.restype = sz
+        L.csa2_beam_workspace_bytes.argtypes = [i32, i32, i32, i32]
+        L.csa2_beam_select.restype = i32
+        L.csa2_beam_select.argtypes = [i32, i32, i32, i32, vp, i32, i64, vp, vp, i32, vp, vp, vp, vp, vp, sz, vp, vp]
+        L.csa2_fp4_weight_bytes.restype = sz
+        L.csa2_fp4_weight_bytes.argtypes = [i32, i32]
+        L.csa2_fp4_encode.restype = i32
+        L.csa2_fp4_encode.argtypes = [i32, i32, vp, i64, C.c_float, vp, vp, vp]
+        L.csa2_fp4_pack.restype = i32
+        L.csa2_fp4_pack.argtypes = [i32, i32, vp, vp, vp, vp, vp]
+        L.csa2_fp4_linear.restype = i32
+        L.csa2_fp4_linear.argtypes = [C.POINTER(_Fp4Desc), i32, vp, i64, vp, vp, i32, i64, vp, vp]
         for f in (L.csa2_kv_attend, L.csa2_kv_cross_attend):
             f.restype = i32
             f.argtypes = [kvc, i32, i32, vp, i64, vp, kvd, vp, i32, i32, C.c_float, vp, i64, vp, vp, sz, vp, vp]
@@ -437,9 +459,8 @@ _raw_stream = torch._C._cuda_getCurrentRawStream if hasattr(torch._C, "_cuda_get
     lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
-def _kv_call(fn, cache, stream, *args):
-    """Call fn on `stream`, or on the current stream of the cache's device, with that device current."""
-    index = cache.device_index
+def _on(index, fn, stream, *args):
+    """Call fn on `stream`, or on the current stream of a device, with that device current."""
     if index == torch.cuda.current_device():
         return fn(*args, _raw_stream(index) if stream is None else stream.cuda_stream)
     with torch.cuda.device(index):
@@ -457,6 +478,18 @@ def kv_append(cfg: KVCfg, k, v, cu, pos0, cache: KVCache, rope=None, q=None, q_o
     cu[b] + i, position pos0[b] + i), keys and queries q [T][n_heads][head_dim] rotated by `rope` [rows][rope_dims / 2]
     [2] fp32.  q_out (which may be q) takes the rotated queries, k_out / v_out the values as stored.  (attend, not
     kv_attend, reads its queries ahead of time: see there before handing it these outputs.)"""
+    _kv_append(cfg, k, v, cu, pos0, cache, rope, q, q_out, k_out, v_out, status, stream)
+
+
+def kv_append_axes(cfg: KVCfg, k, v, cu, pos0, cache: KVCache, axes, axis_of, rope, q=None, q_out=None, k_out=None,
+                   v_out=None, status=None, stream=None):
+    """kv_append with rotary positions of several axes (images, video): axes [T][n_axes] int32 holds each row's positions
+    in `rope`, axis_of the axis of each of the rope_dims / 2 pairs (a sequence of small integers, or bytes).  pos0 gives
+    the slots in the cache, as before."""
+    _kv_append(cfg, k, v, cu, pos0, cache, rope, q, q_out, k_out, v_out, status, stream, axes, bytes(axis_of))
+
+
+def _kv_append(cfg, k, v, cu, pos0, cache, rope, q, q_out, k_out, v_out, status, stream, axes=None, axis_of=None):
     _kv_same(cfg, cache)
     dev, h, d = cache.device_index, cfg.kv_heads, cfg.head_dim
     T, B = k.shape[0], cache.batch
@@ -473,9 +506,17 @@ def kv_append(cfg: KVCfg, k, v, cu, pos0, cache: KVCache, rope=None, q=None, q_o
         op, os_ = _kv_rows(q_out, cfg.n_heads, d, "q_out", dev)
         if q.shape[0] != T or q_out.shape[0] != T:
             raise ValueError("q, q_out and k must have the same rows")
-    _check("csa2_kv_append", _kv_call(
-        (_lib or load()).csa2_kv_append, cache, stream, C.byref(cfg), B, T, qp, qs or 0, kp, ks, vp, vs,
-        _kv_ptr(cu, torch.int32, (B + 1,), "cu", dev), _kv_ptr(pos0, torch.int64, (B,), "pos0", dev),
+    lib, name, where = _lib or load(), "csa2_kv_append", ()
+    if axis_of is not None:
+        if len(axis_of) != cfg.rope_dims // 2:
+            raise ValueError("axis_of must name the axis of each of %d pairs" % (cfg.rope_dims // 2))
+        if axes.dim() != 2:
+            raise ValueError("axes must be [T][n_axes]")
+        n = axes.shape[1]
+        name, where = "csa2_kv_append_axes", (_kv_ptr(axes, torch.int32, (T, n), "axes", dev), n, axis_of)
+    _check(name, _on(
+        cache.device_index, getattr(lib, name), stream, C.byref(cfg), B, T, qp, qs or 0, kp, ks, vp, vs,
+        _kv_ptr(cu, torch.int32, (B + 1,), "cu", dev), _kv_ptr(pos0, torch.int64, (B,), "pos0", dev), *where,
         _kv_ptr(rope, torch.float32, (rows, cfg.rope_dims // 2, 2), "rope", dev), rows,
         C.byref(cache._c), op, os_ or 0, _kv_ptr(k_out, torch.bfloat16, (T, h, d), "k_out", dev),
         _kv_ptr(v_out, torch.bfloat16, (T, h, d), "v_out", dev), _kv_ptr(status, torch.int32, (1,), "status", dev)))
@@ -502,9 +543,9 @@ def _kv_attend(name, cfg, q, cu, cache, kv_len, max_q, max_kv, out, lse, scale, 
         wp, wn = workspace.data_ptr(), workspace.numel() * workspace.element_size()
     scale = 1.0 / math.sqrt(d) if scale is None else float(scale)
     lib = _lib or load()
-    _check("csa2_" + name, _kv_call(
-        lib.csa2_kv_attend if name == "kv_attend" else lib.csa2_kv_cross_attend, cache, stream, C.byref(cfg), B, T, qp,
-        qs, _kv_ptr(cu, torch.int32, (B + 1,), "cu", dev), C.byref(cache._c),
+    _check("csa2_" + name, _on(
+        cache.device_index, lib.csa2_kv_attend if name == "kv_attend" else lib.csa2_kv_cross_attend, stream, C.byref(cfg),
+        B, T, qp, qs, _kv_ptr(cu, torch.int32, (B + 1,), "cu", dev), C.byref(cache._c),
         _kv_ptr(kv_len, torch.int32, (B,), "kv_len", dev), int(max_q), int(max_kv), scale, op, os_,
         _kv_ptr(lse, torch.float32, (T, h), "lse", dev), wp if wn else None, wn,
         _kv_ptr(status, torch.int32, (1,), "status", dev)))
@@ -522,6 +563,151 @@ def kv_cross_attend(cfg: KVCfg, q, cu, cache: KVCache, kv_len, max_q: int, max_k
                     workspace=None, status=None, stream=None):
     """kv_attend without a causal mask: every row of sequence b sees all kv_len[b] states of the cache (an encoder's)."""
     _kv_attend("kv_cross_attend", cfg, q, cu, cache, kv_len, max_q, max_kv, out, lse, scale, workspace, status, stream)
+
+
+def kv_reorder(cfg: KVCfg, caches, beams: int, parents, kv_len, status=None, stream=None):
+    """The beams' states in the order of a selection: sequence i of the caches goes on from what sequence parents[i] (of
+    its group of `beams`, or -1: from nothing) had.  `caches`: the layers' caches, over one block table, which is permuted
+    in place; last pages, written in part, are copied where a beam has several children (rules in include/csa2.h)."""
+    first = caches[0]
+    table, n = first.block_table.data_ptr(), first.batch
+    for c in caches:
+        _kv_same(cfg, c)
+        if c.block_table.data_ptr() != table or c.batch != n or c.device_index != first.device_index:
+            raise ValueError("the layers' caches must share one block table")
+    if beams < 1 or n % beams:
+        raise ValueError("the caches must hold whole groups of beams")
+    dev = first.device_index
+    _check("csa2_kv_reorder", _on(
+        dev, (_lib or load()).csa2_kv_reorder, stream, C.byref(cfg), len(caches),
+        (_KVCacheDesc * len(caches))(*[c._c for c in caches]), n // beams, beams,
+        _kv_ptr(parents, torch.int32, (n,), "parents", dev), _kv_ptr(kv_len, torch.int32, (n,), "kv_len", dev),
+        _kv_ptr(status, torch.int32, (1,), "status", dev)))
+
+
+def _plain(t, dtype, shape, name, index):
+    """Address of a contiguous tensor of a given shape on a given CUDA device."""
+    if t is None:
+        return None
+    if t.dtype is dtype and t.shape == shape and t.get_device() == index and t.is_contiguous():
+        return t.data_ptr()
+    if t.dtype != dtype:
+        raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
+    if t.shape != shape:
+        raise ValueError("%s must be %s, got %s" % (name, list(shape), list(t.shape)))
+    if t.get_device() != index:
+        raise ValueError("%s must be on the call's device" % name)
+    raise ValueError("%s must be contiguous" % name)
+
+
+def _rows_of(t, width, name, index):
+    """Address and row distance of [T][width] rows on a given CUDA device; a row is contiguous."""
+    shape, stride = t.shape, t.stride()
+    if len(shape) != 2 or shape[1] != width:
+        raise ValueError("%s must be [T][%d], got %s" % (name, width, list(shape)))
+    if t.get_device() != index or index < 0:
+        raise ValueError("%s must be on the call's device" % name)
+    if stride[1] != 1 and width > 1:
+        raise ValueError("%s: a row must be contiguous" % name)
+    return t.data_ptr(), (stride[0] if shape[0] > 1 else max(width, -(-width // 8) * 8))
+
+
+_FLOATS = {torch.bfloat16: 0, torch.float32: 1}
+
+
+def beam_workspace_bytes(groups: int, beams: int, vocab: int, take: int) -> int:
+    """Workspace of beam_select for these sizes."""
+    return int(load().csa2_beam_workspace_bytes(groups, beams, vocab, take))
+
+
+def beam_select(logits, cum, scores, parents, tokens, workspace, done=None, end_token: int = 0, lse=None, status=None,
+                stream=None):
+    """Best continuations of each group of beams: logits [groups * beams][vocab] (bf16 or fp32; rows may stand apart),
+    cum [groups][beams] fp32 -> the best scores [groups][take] fp32 (cum + log-softmax) in order, their parents (sequence
+    numbers) and tokens [groups][take] int32.  done [groups][beams] uint8: a beam that has ended proposes end_token alone
+    at its score.  lse [groups * beams] fp32 receives the log-sum-exps."""
+    groups, beams = cum.shape
+    take, dev, vocab = scores.shape[1], logits.get_device(), logits.shape[1]
+    if logits.dtype not in _FLOATS:
+        raise TypeError("logits must be bf16 or fp32, got %s" % logits.dtype)
+    n = groups * beams
+    if logits.shape[0] != n:
+        raise ValueError("logits must have %d rows" % n)
+    p, stride = _rows_of(logits, vocab, "logits", dev)
+    if workspace.get_device() != dev or not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous on the call's device")
+    _check("csa2_beam_select", _on(
+        dev, (_lib or load()).csa2_beam_select, stream, groups, beams, vocab, take, p, _FLOATS[logits.dtype], stride,
+        _plain(cum, torch.float32, (groups, beams), "cum", dev), _plain(done, torch.uint8, (groups, beams), "done", dev),
+        int(end_token), _plain(scores, torch.float32, (groups, take), "scores", dev),
+        _plain(parents, torch.int32, (groups, take), "parents", dev),
+        _plain(tokens, torch.int32, (groups, take), "tokens", dev), _plain(lse, torch.float32, (n,), "lse", dev),
+        workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+        _plain(status, torch.int32, (1,), "status", dev)))
+
+
+class Fp4Weights:
+    """Weights [n][k] in the caches' codec (E2M1, one E4M3 scale per 16 channels), laid out for fp4_linear; a weight is
+    alpha * code * scale."""
+
+    def __init__(self, data, n: int, k: int, alpha: float):
+        self.data, self.n, self.k, self.alpha = data, n, k, float(alpha)
+        self.device, self.device_index = data.device, data.get_device()
+        self._c = _Fp4Desc(data.data_ptr(), n, k, self.alpha, 0)
+
+    @staticmethod
+    def _room(n, k, device):
+        size = load().csa2_fp4_weight_bytes(n, k)
+        if size == 0:
+            raise ValueError("unsupported weights [%d][%d]: k must be a multiple of 16" % (n, k))
+        return torch.empty(size, dtype=torch.uint8, device=device)
+
+    @classmethod
+    def pack(cls, codes, scales, alpha: float = 1.0, status=None, stream=None) -> "Fp4Weights":
+        """From codes [n][k / 2] (channel 2i in the low nibble of byte i) and E4M3 scales [n][k / 16], both uint8."""
+        n, k, dev = codes.shape[0], 2 * codes.shape[1], codes.get_device()
+        cp = _plain(codes, torch.uint8, (n, k // 2), "codes", dev)
+        sp = _plain(scales, torch.uint8, (n, k // 16), "scales", dev)
+        data = cls._room(n, k, codes.device)
+        _check("csa2_fp4_pack", _on(dev, load().csa2_fp4_pack, stream, n, k, cp, sp, data.data_ptr(),
+                                    _plain(status, torch.int32, (1,), "status", dev)))
+        return cls(data, n, k, alpha)
+
+    @classmethod
+    def encode(cls, w, gain=None, status=None, stream=None) -> "Fp4Weights":
+        """From bf16 rows w [n][k], encoded times `gain`; alpha becomes 1 / gain.  Without a gain: the power of two that
+        brings the largest weight nearest below the codec's largest value, 448 x 6 (read on the host)."""
+        n, k = w.shape
+        dev = w.get_device()
+        if w.dtype != torch.bfloat16:
+            raise TypeError("w must be torch.bfloat16, got %s" % w.dtype)
+        p, stride = _rows_of(w, k, "w", dev)
+        if gain is None:
+            most = float(w.abs().amax()) if w.numel() else 0.0
+            gain = 2.0 ** math.floor(math.log2(448 * 6 / most)) if 0 < most < math.inf else 1.0
+        data = cls._room(n, k, w.device)
+        _check("csa2_fp4_encode", _on(dev, load().csa2_fp4_encode, stream, n, k, p, stride, float(gain), data.data_ptr(),
+                                      _plain(status, torch.int32, (1,), "status", dev)))
+        return cls(data, n, k, 1.0 / gain)
+
+
+def fp4_linear(x, weights: Fp4Weights, out, bias=None, status=None, stream=None):
+    """out [T][n] (bf16 or fp32) = x [T][k] bf16 times the weights' transpose (+ bias [n] bf16).  Rows of x and out may
+    stand apart."""
+    n, dev = weights.n, weights.device_index
+    if x.dtype is not torch.bfloat16:
+        raise TypeError("x must be torch.bfloat16, got %s" % x.dtype)
+    if out.dtype not in _FLOATS:
+        raise TypeError("out must be bf16 or fp32, got %s" % out.dtype)
+    xp, xs = _rows_of(x, weights.k, "x", dev)
+    op, os_ = _rows_of(out, n, "out", dev)
+    T = x.shape[0]
+    if out.shape[0] != T:
+        raise ValueError("x and out must have the same rows")
+    _check("csa2_fp4_linear", _on(
+        dev, (_lib or load()).csa2_fp4_linear, stream, C.byref(weights._c), T, xp, xs,
+        _plain(bias, torch.bfloat16, (n,), "bias", dev), op, _FLOATS[out.dtype], os_,
+        _plain(status, torch.int32, (1,), "status", dev)))
 
 
 class Captured:

@@ -1,0 +1,87 @@
+// Shared by the projections with 4-bit weights (fp4_pack.cu, fp4_rows.cu,
+// fp4_tiles.cu): how the weights are laid out, and their decoding to bf16.
+//
+// A block is 16 rows x 128 channels in 1152 bytes: 1024 of codes, 128 of scales; the
+// blocks of 16 rows follow one another along k, then the next 16 rows.  A warp reads
+// a block as the left operand of eight 16x8x16 products: lane 4 g + t holds channels
+// 32 t .. 32 t + 31 of rows g (bytes 16 lane ..) and g + 8 (bytes 512 + 16 lane ..), its
+// i-th word the eight channels of 16-byte chunk i ^ t (of the right operand, of which
+// it needs the same channels: so lanes of neighbouring t read and write shared memory
+// in different banks).  Within a word the even channels of the eight stand in the low
+// half, the odd ones in the high half, their codes s e1 e0 m at bits
+//   15 8 7 6 | 12 5 4 3 | 9 2 1 0 | 14 13 11 10
+// of the half, so that one shift and one mask (four more operations for the last)
+// bring two neighbouring channels to s at bit 15 and e1 e0 m at bits 8..6 of the two
+// bf16 of a register.  Read as bf16 that is code x 2^-126 (subnormal where e1 e0 = 0),
+// exactly; times scale x 2^118 it is the weight x 2^-8, exactly, as a code has 2
+// significant bits and a scale 4.  (The conversion to f16, one instruction a pair,
+// needs a third of the instructions, but x would have to become f16 too, which loses
+// bf16's range and costs as much again for few rows: 8 codes 11 + 4 operations in
+// 3.1 cycles a warp and SM, at HBM's rate there are 6.)
+#pragma once
+
+#include "kv.cuh"
+
+namespace csa2 {
+
+constexpr int kBlockRows = 16, kBlockK = 128, kBlockBytes = 1152, kBlockCodes = 1024;
+constexpr float kFp4Unit = 256.0f;  // what the decoded weights are short of
+
+__host__ __device__ __forceinline__ int fp4_row_groups(int n) { return (n + 31) / 32 * 2; }
+__host__ __device__ __forceinline__ int fp4_k_blocks(int k) { return (k + kBlockK - 1) / kBlockK; }
+
+struct Fp4Linear {
+  const uint8_t* w;
+  int n, k, k_blocks, T;
+  const uint16_t* x;
+  int64_t x_stride;
+  const uint16_t* bias;
+  void* out;
+  int64_t out_stride;
+  int f32;      // out's type
+  float alpha;  // times kFp4Unit
+  int32_t* status;
+};
+
+__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+// Byte i of w, an E4M3 scale >= 0, as a pair of bf16 scale x 2^118: its bits are a bf16
+// scale x 2^-120.
+__device__ __forceinline__ uint32_t fp4_scale(uint32_t w, int i) {
+  const uint32_t b = __byte_perm(w, 0, 0x4040 | i | i << 8) * 16u;
+  return mul_bf16x2(mul_bf16x2(b, 0x7F007F00u), 0x77007700u);  // 2^127, 2^111
+}
+// The eight weights of a word, times 2^-8: pair p holds channels 2p and 2p + 1.
+__device__ __forceinline__ void fp4_weights(uint32_t w, uint32_t scale, uint32_t (&r)[4]) {
+  constexpr uint32_t kMask = 0x81C081C0u;
+  r[0] = mul_bf16x2(w & kMask, scale);
+  r[1] = mul_bf16x2((w << 3) & kMask, scale);
+  r[2] = mul_bf16x2((w << 6) & kMask, scale);
+  uint32_t u = ((w << 1) & 0x80008000u) | ((w >> 4) & 0x7FFF7FFFu);
+  u = ((w >> 5) & 0x01000100u) | (u & 0xFEFFFEFFu);
+  r[3] = mul_bf16x2(u & kMask, scale);
+}
+// sum + bias, stored in out's type.
+__device__ __forceinline__ void fp4_store(const Fp4Linear& a, int t, int i, float sum, float bias) {
+  const float y = fmaf(sum, a.alpha, bias);
+  if (a.f32) static_cast<float*>(a.out)[t * a.out_stride + i] = y;
+  else static_cast<__nv_bfloat16*>(a.out)[t * a.out_stride + i] = __float2bfloat16_rn(y);
+}
+__device__ __forceinline__ float fp4_bias(const Fp4Linear& a, int i) {
+  return a.bias ? bf16_bits_to_float(__ldg(a.bias + i)) : 0.0f;
+}
+
+cudaError_t launch_fp4_encode(int n, int k, const uint16_t* w, int64_t stride, float gain, uint8_t* packed,
+                              int32_t* status, cudaStream_t stream);
+cudaError_t launch_fp4_pack(int n, int k, const uint8_t* codes, const uint8_t* scales, uint8_t* packed,
+                            int32_t* status, cudaStream_t stream);
+// Up to kFp4FewRows rows whose x fits shared memory (fp4_rows_ok), and any.
+constexpr int kFp4FewRows = 8;
+bool fp4_rows_ok(const Fp4Linear& a);
+cudaError_t launch_fp4_rows(const Fp4Linear& a, cudaStream_t stream);
+cudaError_t launch_fp4_tiles(const Fp4Linear& a, cudaStream_t stream);
+
+}  // namespace csa2

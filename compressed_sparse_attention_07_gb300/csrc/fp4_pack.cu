@@ -1,0 +1,142 @@
+// Weights laid out for the products (fp4.cuh), from bf16 rows or from codes and
+// scales: a thread for 32 channels of a row.  Runs once, when a program loads its
+// weights: bound by HBM at a few bytes a weight.
+#include "fp4.cuh"
+
+namespace csa2 {
+namespace {
+
+constexpr int kThreads = 256;
+
+// Eight codes, channel 0 lowest -> a word as in fp4.cuh.
+__device__ __forceinline__ uint32_t arrange(uint32_t codes) {
+  uint32_t w = 0;
+#pragma unroll
+  for (int c = 0; c < 8; ++c) {
+    const uint32_t n = (codes >> (4 * c)) & 15u, s = n >> 3, m = n & 7u;
+    const int p = c / 2;
+    const uint32_t h = p == 0   ? s << 15 | m << 6
+                       : p == 1 ? s << 12 | m << 3
+                       : p == 2 ? s << 9 | m
+                                : s << 14 | (m >> 2) << 13 | (m & 3u) << 10;
+    w |= h << (c & 1 ? 16 : 0);
+  }
+  return w;
+}
+
+struct Spot {  // a thread's 32 channels
+  int row, t, k0;
+  int64_t block;
+};
+__device__ __forceinline__ bool spot(int n, int k, Spot& s) {
+  const int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x;
+  const int blocks = fp4_k_blocks(k);
+  s.block = i >> 6;
+  if (s.block >= (int64_t)fp4_row_groups(n) * blocks) return false;
+  const int in = (int)(i & 63);
+  s.t = in & 3;
+  s.row = (int)(s.block / blocks) * kBlockRows + (in >> 2);
+  s.k0 = (int)(s.block % blocks) * kBlockK + 32 * s.t;
+  return true;
+}
+
+// Codes (word j: channels k0 + 8 j ..) and scales (of the first and second 16) of a
+// thread's channels into their block.
+__device__ __forceinline__ void put(uint8_t* packed, const Spot& s, const uint32_t (&codes)[4], const uint32_t (&scale)[2]) {
+  uint8_t* block = packed + s.block * kBlockBytes;
+  const int r = s.row % kBlockRows, lane = (r & 7) * 4 + s.t, half = r >> 3;
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    uint32_t c = codes[0];
+#pragma unroll
+    for (int j = 1; j < 4; ++j)
+      if ((i ^ s.t) == j) c = codes[j];
+    w[i] = arrange(c);
+  }
+  *reinterpret_cast<uint4*>(block + half * 512 + lane * 16) = make_uint4(w[0], w[1], w[2], w[3]);
+  // the scale of words 0 and 1 first
+  const uint32_t first = s.t & 2 ? scale[1] : scale[0], second = s.t & 2 ? scale[0] : scale[1];
+  *reinterpret_cast<uint16_t*>(block + kBlockCodes + lane * 4 + half * 2) = (uint16_t)(first | second << 8);
+}
+
+__global__ void __launch_bounds__(kThreads) fp4_pack_kernel(int n, int k, const uint8_t* codes, const uint8_t* scales,
+                                                            uint8_t* packed, int32_t* status) {
+  griddep_wait();
+  Spot s;
+  if (!spot(n, k, s)) return;
+  uint32_t c[4] = {}, sc[2] = {};
+  if (s.row < n) {
+    const uint8_t* src = codes + (int64_t)s.row * (k / 2) + s.k0 / 2;
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (s.k0 + 8 * j < k) c[j] = __ldg(reinterpret_cast<const uint32_t*>(src) + j);
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+      if (s.k0 + 16 * j < k) {
+        uint32_t b = __ldg(scales + (int64_t)s.row * (k / 16) + s.k0 / 16 + j);
+        if (b & 0x80u) c[2 * j] ^= 0x88888888u, c[2 * j + 1] ^= 0x88888888u;  // the codes take its sign
+        b &= 0x7Fu;
+        if (b == 0x7Fu) {
+          report(status, CSA2_ERR_RANGE);
+          b = 0;
+        }
+        sc[j] = b;
+      }
+  }
+  put(packed, s, c, sc);
+}
+
+__global__ void __launch_bounds__(kThreads) fp4_encode_kernel(int n, int k, const uint16_t* w, int64_t stride, float gain,
+                                                              uint8_t* packed, int32_t* status) {
+  griddep_wait();
+  Spot s;
+  if (!spot(n, k, s)) return;
+  uint32_t c[4] = {}, sc[2] = {};
+  if (s.row < n) {
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      if (s.k0 + 16 * j >= k) break;
+      const uint4* src = reinterpret_cast<const uint4*>(w + (int64_t)s.row * stride + s.k0 + 16 * j);
+      float v[2][8], amax = 0.0f;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const uint4 u = __ldg(src + h);
+        const uint32_t q[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          float x = __fmul_rn(__uint_as_float(i & 1 ? q[i / 2] & 0xFFFF0000u : q[i / 2] << 16), gain);
+          if (!(fabsf(x) <= 3.4028234663852886e38f)) {
+            report(status, CSA2_ERR_RANGE);
+            x = x != x ? 0.0f : copysignf(3.4028234663852886e38f, x);
+          }
+          v[h][i] = x;
+          amax = fmaxf(amax, fabsf(x));
+        }
+      }
+      sc[j] = e4m3_code(__fdiv_rn(amax, 6.0f));
+      if (sc[j]) {
+        const float f = e4m3_to_float(sc[j]);
+        c[2 * j] = e2m1x8(v[0], f), c[2 * j + 1] = e2m1x8(v[1], f);
+      }
+    }
+  }
+  put(packed, s, c, sc);
+}
+
+int64_t grid_of(int n, int k) { return ((int64_t)fp4_row_groups(n) * fp4_k_blocks(k) * 64 + kThreads - 1) / kThreads; }
+
+}  // namespace
+
+cudaError_t launch_fp4_pack(int n, int k, const uint8_t* codes, const uint8_t* scales, uint8_t* packed,
+                            int32_t* status, cudaStream_t stream) {
+  return launch_k(fp4_pack_kernel, dim3((unsigned)grid_of(n, k)), dim3(kThreads), 0, stream, 0, n, k, codes, scales,
+                  packed, status);
+}
+cudaError_t launch_fp4_encode(int n, int k, const uint16_t* w, int64_t stride, float gain, uint8_t* packed,
+                              int32_t* status, cudaStream_t stream) {
+  return launch_k(fp4_encode_kernel, dim3((unsigned)grid_of(n, k)), dim3(kThreads), 0, stream, 0, n, k, w, stride, gain,
+                  packed, status);
+}
+
+}  // namespace csa2

@@ -61,6 +61,38 @@ __device__ __forceinline__ void codes8(uint32_t w, uint32_t (&r)[4]) {
       : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
       : "r"(w));
 }
+// E4M3 code nearest to y >= 0, saturating.
+__device__ __forceinline__ uint32_t e4m3_code(float y) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(0.0f), "f"(y));
+  return r & 0xFFu;
+}
+// Codes of x / s (0 < s), ties to the even code, saturating: eight nibbles, channel
+// 0 lowest.  |x| may pass 6 s, up to 9 s at the smallest scales, whose steps are
+// wide, and without bound at the largest: the conversion saturates.  The quotient is
+// rounded correctly from the reciprocal by one step with the remainder
+// (Markstein), so that a value half way between two codes is seen as such; where
+// the remainder underflows, the code is 0 either way.  The sign of a value that
+// rounds to zero is dropped.
+__device__ __forceinline__ uint32_t e2m1x8(const float (&x)[8], float s) {
+  const float inv = __frcp_rn(s);
+  float y[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float q = __fmul_rn(x[i], inv);
+    y[i] = __fmaf_rn(__fmaf_rn(-q, s, x[i]), inv, q);
+  }
+  uint32_t w;
+  asm("{\n .reg .b8 b0, b1, b2, b3;\n"
+      " cvt.rn.satfinite.e2m1x2.f32 b0, %2, %1;\n cvt.rn.satfinite.e2m1x2.f32 b1, %4, %3;\n"
+      " cvt.rn.satfinite.e2m1x2.f32 b2, %6, %5;\n cvt.rn.satfinite.e2m1x2.f32 b3, %8, %7;\n"
+      " mov.b32 %0, {b0, b1, b2, b3};\n}\n"
+      : "=r"(w)
+      : "f"(y[0]), "f"(y[1]), "f"(y[2]), "f"(y[3]), "f"(y[4]), "f"(y[5]), "f"(y[6]), "f"(y[7]));
+  const uint32_t m = w & 0x77777777u;
+  const uint32_t nz = (m | (m >> 1) | (m >> 2)) & 0x11111111u;
+  return m | (w & (nz << 3));
+}
 // Pairs of fp32 for the packed arithmetic.
 __device__ __forceinline__ uint64_t pack2(float a, float b) {
   uint64_t r;
@@ -243,11 +275,20 @@ __device__ __forceinline__ int kv_parts(const KvAtt& a, int p0, int p1) {
 // kv_join_kernel's early start, as that kernel writes the outputs and waits before.
 __device__ __forceinline__ bool kv_joined(const KvAtt& a) { return a.n_parts > 1 && !a.cluster; }
 
+// Rotary positions of several axes: pos [T][n] (null: the running position), of [pairs].
+struct KvAxes {
+  const int32_t* pos;
+  int n;
+  const uint8_t* of;
+};
 cudaError_t launch_kv_append(const csa2_kv_cfg& cfg, int B, int T, const uint16_t* q, int64_t q_stride,
                              const uint16_t* k, int64_t k_stride, const uint16_t* v, int64_t v_stride,
-                             const int32_t* cu, const int64_t* pos0, const float* rope, int64_t rope_rows,
-                             const KvView& c, uint16_t* q_out, int64_t q_out_stride, uint16_t* k_out, uint16_t* v_out,
-                             int32_t* status, cudaStream_t stream);
+                             const int32_t* cu, const int64_t* pos0, const KvAxes& axes, const float* rope,
+                             int64_t rope_rows, const KvView& c, uint16_t* q_out, int64_t q_out_stride, uint16_t* k_out,
+                             uint16_t* v_out, int32_t* status, cudaStream_t stream);
+// The beams' tables and last pages (kv_reorder.cu).
+cudaError_t launch_kv_reorder(const csa2_kv_cfg& cfg, int layers, const csa2_kv_cache* caches, int groups, int beams,
+                              const int32_t* parents, const int32_t* kv_len, int32_t* status, cudaStream_t stream);
 
 // How a call divides the keys, from sizes alone, with no more than `room` bytes of
 // partial outputs.

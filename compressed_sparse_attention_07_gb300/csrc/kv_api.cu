@@ -1,5 +1,5 @@
 // C ABI of the paged key / value operators: argument validation on the host,
-// then the launches of kv_append.cu, kv_rows.cu and kv_tiles.cu.
+// then the launches of kv_append.cu, kv_rows.cu, kv_tiles.cu and kv_reorder.cu.
 #include <cmath>
 #include <cstring>
 
@@ -86,6 +86,27 @@ int32_t attend(const csa2_kv_cfg* cfg, bool cross, int32_t B, int32_t T, const u
   return cuda_status(launch_kv_attend(*cfg, B, a, static_cast<cudaStream_t>(stream)));
 }
 
+int32_t append(const csa2_kv_cfg* cfg, int32_t B, int32_t T, const uint16_t* q, int64_t q_stride,
+                       const uint16_t* k, int64_t k_stride, const uint16_t* v, int64_t v_stride, const int32_t* cu,
+                       const int64_t* pos0, const KvAxes& axes, const float* rope, int64_t rope_rows, const csa2_kv_cache* cache,
+                       uint16_t* q_out, int64_t q_out_stride, uint16_t* k_out, uint16_t* v_out, int32_t* status,
+                       void* stream) {
+  const int32_t rc = check_cfg(cfg);
+  if (rc) return rc;
+  if (B < 0 || T < 0 || rope_rows < 0) return CSA2_ERR_INVALID_ARG;
+  if (B == 0 || T == 0) return CSA2_OK;
+  const int64_t kw = (int64_t)cfg->kv_heads * cfg->head_dim, qw = (int64_t)cfg->n_heads * cfg->head_dim;
+  if (!rows_ok(k, k_stride, kw) || !rows_ok(v, v_stride, kw) || !cu || !pos0 || !aligned(cu, 4) || !aligned(pos0, 8) ||
+      !aligned(k_out, 16) || !aligned(v_out, 16) || !aligned(status, 4) || !cache_ok(*cfg, cache))
+    return CSA2_ERR_INVALID_ARG;
+  if ((q != nullptr) != (q_out != nullptr)) return CSA2_ERR_INVALID_ARG;
+  if (q && (!rows_ok(q, q_stride, qw) || !rows_ok(q_out, q_out_stride, qw))) return CSA2_ERR_INVALID_ARG;
+  if ((rope != nullptr) != (cfg->rope_dims != 0) || !aligned(rope, 16)) return CSA2_ERR_INVALID_ARG;
+  return cuda_status(launch_kv_append(*cfg, B, T, q, q_stride, k, k_stride, v, v_stride, cu, pos0, axes, rope, rope_rows,
+                                      view_of(*cache), q_out, q_out_stride, k_out, v_out, status,
+                                      static_cast<cudaStream_t>(stream)));
+}
+
 }  // namespace
 
 extern "C" {
@@ -102,20 +123,40 @@ int32_t csa2_kv_append(const csa2_kv_cfg* cfg, int32_t B, int32_t T, const uint1
                        const int64_t* pos0, const float* rope, int64_t rope_rows, const csa2_kv_cache* cache,
                        uint16_t* q_out, int64_t q_out_stride, uint16_t* k_out, uint16_t* v_out, int32_t* status,
                        void* stream) {
+  return append(cfg, B, T, q, q_stride, k, k_stride, v, v_stride, cu, pos0, KvAxes{}, rope, rope_rows, cache, q_out,
+                q_out_stride, k_out, v_out, status, stream);
+}
+
+int32_t csa2_kv_append_axes(const csa2_kv_cfg* cfg, int32_t B, int32_t T, const uint16_t* q, int64_t q_stride,
+                            const uint16_t* k, int64_t k_stride, const uint16_t* v, int64_t v_stride, const int32_t* cu,
+                            const int64_t* pos0, const int32_t* axes, int32_t n_axes, const uint8_t* axis_of,
+                            const float* rope, int64_t rope_rows, const csa2_kv_cache* cache, uint16_t* q_out,
+                            int64_t q_out_stride, uint16_t* k_out, uint16_t* v_out, int32_t* status, void* stream) {
   const int32_t rc = check_cfg(cfg);
   if (rc) return rc;
-  if (B < 0 || T < 0 || rope_rows < 0) return CSA2_ERR_INVALID_ARG;
-  if (B == 0 || T == 0) return CSA2_OK;
-  const int64_t kw = (int64_t)cfg->kv_heads * cfg->head_dim, qw = (int64_t)cfg->n_heads * cfg->head_dim;
-  if (!rows_ok(k, k_stride, kw) || !rows_ok(v, v_stride, kw) || !cu || !pos0 || !aligned(cu, 4) || !aligned(pos0, 8) ||
-      !aligned(k_out, 16) || !aligned(v_out, 16) || !aligned(status, 4) || !cache_ok(*cfg, cache))
+  if (n_axes < 1 || n_axes > 4 || !axis_of || cfg->rope_dims == 0) return CSA2_ERR_INVALID_ARG;
+  for (int i = 0; i < cfg->rope_dims / 2; ++i)
+    if (axis_of[i] >= n_axes) return CSA2_ERR_INVALID_ARG;
+  if (B > 0 && T > 0 && (!axes || !aligned(axes, 4))) return CSA2_ERR_INVALID_ARG;
+  return append(cfg, B, T, q, q_stride, k, k_stride, v, v_stride, cu, pos0, KvAxes{axes, n_axes, axis_of}, rope, rope_rows,
+                cache, q_out, q_out_stride, k_out, v_out, status, stream);
+}
+
+int32_t csa2_kv_reorder(const csa2_kv_cfg* cfg, int32_t layers, const csa2_kv_cache* caches, int32_t groups,
+                        int32_t beams, const int32_t* parents, const int32_t* kv_len, int32_t* status, void* stream) {
+  const int32_t rc = check_cfg(cfg);
+  if (rc) return rc;
+  if (layers < 0 || groups < 0 || beams < 1 || beams > 64) return CSA2_ERR_INVALID_ARG;
+  if (layers > CSA2_MAX_LAYERS || (int64_t)groups * beams > (1 << 24)) return CSA2_ERR_UNSUPPORTED;
+  if (layers == 0 || groups == 0) return CSA2_OK;
+  if (!caches || !parents || !kv_len || !aligned(parents, 4) || !aligned(kv_len, 4) || !aligned(status, 4))
     return CSA2_ERR_INVALID_ARG;
-  if ((q != nullptr) != (q_out != nullptr)) return CSA2_ERR_INVALID_ARG;
-  if (q && (!rows_ok(q, q_stride, qw) || !rows_ok(q_out, q_out_stride, qw))) return CSA2_ERR_INVALID_ARG;
-  if ((rope != nullptr) != (cfg->rope_dims != 0) || !aligned(rope, 16)) return CSA2_ERR_INVALID_ARG;
-  return cuda_status(launch_kv_append(*cfg, B, T, q, q_stride, k, k_stride, v, v_stride, cu, pos0, rope, rope_rows,
-                                      view_of(*cache), q_out, q_out_stride, k_out, v_out, status,
-                                      static_cast<cudaStream_t>(stream)));
+  for (int i = 0; i < layers; ++i)
+    if (!cache_ok(*cfg, caches + i) || caches[i].block_table != caches[0].block_table ||
+        caches[i].max_pages != caches[0].max_pages || caches[i].num_pages != caches[0].num_pages)
+      return CSA2_ERR_INVALID_ARG;
+  return cuda_status(launch_kv_reorder(*cfg, layers, caches, groups, beams, parents, kv_len, status,
+                                       static_cast<cudaStream_t>(stream)));
 }
 
 size_t csa2_kv_workspace_bytes(const csa2_kv_cfg* cfg, int32_t B, int32_t T, int32_t max_q, int32_t max_kv) {

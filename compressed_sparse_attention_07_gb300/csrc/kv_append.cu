@@ -48,7 +48,17 @@ struct AppendArgs {
   int64_t q_out_stride;
   uint16_t *k_out, *v_out;
   int32_t* status;
+  // positions of several axes (kAxes), [T][n_axes], and the axis of each pair, two bits
+  const int32_t* axes;
+  int n_axes;
+  uint32_t axis_of[4];
 };
+
+__device__ __forceinline__ int axis_of(const AppendArgs& a, int pair) {
+  const int w = pair >> 4;
+  const uint32_t bits = w == 0 ? a.axis_of[0] : w == 1 ? a.axis_of[1] : w == 2 ? a.axis_of[2] : a.axis_of[3];
+  return (int)(bits >> (2 * (pair & 15))) & 3;
+}
 
 __device__ __forceinline__ void widen(const uint32_t (&u)[4], float (&x)[8]) {
 #pragma unroll
@@ -57,39 +67,6 @@ __device__ __forceinline__ void widen(const uint32_t (&u)[4], float (&x)[8]) {
     x[2 * i + 1] = __uint_as_float(u[i] & 0xFFFF0000u);
   }
 }
-// E4M3 code nearest to y >= 0, saturating.
-__device__ __forceinline__ uint32_t e4m3_code(float y) {
-  uint16_t r;
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(0.0f), "f"(y));
-  return r & 0xFFu;
-}
-// Codes of x / s (0 < s), ties to the even code, saturating: eight nibbles, channel
-// 0 lowest.  |x| may pass 6 s, up to 9 s at the smallest scales, whose steps are
-// wide, and without bound at the largest: the conversion saturates.  The quotient is
-// rounded correctly from the reciprocal by one step with the remainder
-// (Markstein), so that a value half way between two codes is seen as such; where
-// the remainder underflows, the code is 0 either way.  The sign of a value that
-// rounds to zero is dropped.
-__device__ __forceinline__ uint32_t e2m1x8(const float (&x)[8], float s) {
-  const float inv = __frcp_rn(s);
-  float y[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const float q = __fmul_rn(x[i], inv);
-    y[i] = __fmaf_rn(__fmaf_rn(-q, s, x[i]), inv, q);
-  }
-  uint32_t w;
-  asm("{\n .reg .b8 b0, b1, b2, b3;\n"
-      " cvt.rn.satfinite.e2m1x2.f32 b0, %2, %1;\n cvt.rn.satfinite.e2m1x2.f32 b1, %4, %3;\n"
-      " cvt.rn.satfinite.e2m1x2.f32 b2, %6, %5;\n cvt.rn.satfinite.e2m1x2.f32 b3, %8, %7;\n"
-      " mov.b32 %0, {b0, b1, b2, b3};\n}\n"
-      : "=r"(w)
-      : "f"(y[0]), "f"(y[1]), "f"(y[2]), "f"(y[3]), "f"(y[4]), "f"(y[5]), "f"(y[6]), "f"(y[7]));
-  const uint32_t m = w & 0x77777777u;
-  const uint32_t nz = (m | (m >> 1) | (m >> 2)) & 0x11111111u;
-  return m | (w & (nz << 3));
-}
-
 // What a thread keeps for its eight channels of every row of a token: the
 // cosines, and the sines with the sign they have in that channel.
 struct Turn {
@@ -114,7 +91,38 @@ struct Turn {
       }
     }
   }
+  // row(axis): the row of angles of the token's position on that axis
+  template <typename Row>
+  __device__ __forceinline__ void load_axes(const AppendArgs& a, Row row, int c0, int pairs) {
+    if (a.half) {
+      const bool second = c0 >= pairs;
+      const int p0 = second ? c0 - pairs : c0;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float2 f = row(axis_of(a, p0 + i))[p0 + i];
+        c[i] = f.x, s[i] = second ? f.y : -f.y;
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float2 f = row(axis_of(a, c0 / 2 + i))[c0 / 2 + i];
+        c[2 * i] = c[2 * i + 1] = f.x;
+        s[2 * i] = -f.y, s[2 * i + 1] = f.y;
+      }
+    }
+  }
 };
+
+// A token's positions on the axes; false when one is outside the table.
+__device__ __forceinline__ bool load_axes(const AppendArgs& a, int n, int (&at)[4]) {
+  bool ok = true;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    at[i] = i < a.n_axes ? __ldg(a.axes + (int64_t)n * a.n_axes + i) : 0;
+    ok = ok && at[i] >= 0 && at[i] < a.rope_rows;
+  }
+  return ok;
+}
 
 struct Place {
   int n;         // token
@@ -202,7 +210,7 @@ __device__ __forceinline__ void put_row(const AppendArgs& a, const Place& at, in
   *reinterpret_cast<uint4*>(plain + ((int64_t)at.n * a.n_kv + h) * kDim_ + c0) = stored;
 }
 
-template <int kDim_, bool kFp4, int kPasses>
+template <int kDim_, bool kFp4, int kPasses, bool kAxes>
 __global__ void __launch_bounds__(kThreads) kv_append_few_kernel(AppendArgs a) {
   constexpr int kLanes = kDim_ / 8;              // threads of a row
   constexpr int kRows = kThreads / kLanes;       // rows of a pass
@@ -234,8 +242,9 @@ __global__ void __launch_bounds__(kThreads) kv_append_few_kernel(AppendArgs a) {
   const int lo = __ldg(a.cu + b), hi = __ldg(a.cu + b + 1);
   if (n < lo && b == 0 && lo <= a.T) return;  // ahead of the first
   const int64_t pos = __ldg(a.pos0 + b) + (n - lo);
-  if (lo < 0 || n < lo || n >= hi || hi > a.T || pos < 0 || pos >= (int64_t)a.c.max_pages * kPage ||
-      (a.rope_dims && pos >= a.rope_rows)) {
+  int axes[4];
+  const bool on_table = kAxes ? load_axes(a, n, axes) : !a.rope_dims || pos < a.rope_rows;
+  if (lo < 0 || n < lo || n >= hi || hi > a.T || pos < 0 || pos >= (int64_t)a.c.max_pages * kPage || !on_table) {
     if (tid == 0) report(a.status, CSA2_ERR_BAD_INDEX);
     return;
   }
@@ -247,7 +256,15 @@ __global__ void __launch_bounds__(kThreads) kv_append_few_kernel(AppendArgs a) {
   const int pairs = a.rope_dims / 2;
   const bool turned = c0 < a.rope_dims;
   Turn turn = {};
-  if (turned) turn.load(reinterpret_cast<const float4*>(a.rope + pos * a.rope_dims), c0, pairs, a.half);
+  if constexpr (kAxes) {
+    if (turned)
+      turn.load_axes(a, [&](int axis) {
+        const int at = axis == 0 ? axes[0] : axis == 1 ? axes[1] : axis == 2 ? axes[2] : axes[3];
+        return reinterpret_cast<const float2*>(a.rope + (int64_t)at * a.rope_dims);
+      }, c0, pairs);
+  } else if (turned) {
+    turn.load(reinterpret_cast<const float4*>(a.rope + pos * a.rope_dims), c0, pairs, a.half);
+  }
   const int mate = ((tid & 31) + (c0 >= pairs ? -pairs : pairs) / 8) & 31;
 #pragma unroll
   for (int p = 0; p < kPasses; ++p) {
@@ -270,7 +287,8 @@ struct StreamPiece {   // what the workers need to know of a piece
 
 // Sequence of token n by bisection over cu (the first that ends behind n), and
 // its place; false when it has none.
-__device__ __forceinline__ bool find_place(const AppendArgs& a, int n, Place& at, int64_t& pos) {
+template <bool kAxes>
+__device__ __forceinline__ bool find_place(const AppendArgs& a, int n, Place& at, int64_t& pos, int (&axes)[4]) {
   int lo_b = 0, hi_b = a.B;
   while (lo_b < hi_b) {
     const int mid = (lo_b + hi_b) / 2;
@@ -281,8 +299,8 @@ __device__ __forceinline__ bool find_place(const AppendArgs& a, int n, Place& at
   const int lo = __ldg(a.cu + lo_b), hi = __ldg(a.cu + lo_b + 1);
   if (n < lo && lo_b == 0 && lo <= a.T) return false;  // ahead of the first
   pos = __ldg(a.pos0 + lo_b) + (n - lo);
-  if (lo < 0 || n < lo || n >= hi || hi > a.T || pos < 0 || pos >= (int64_t)a.c.max_pages * kPage ||
-      (a.rope_dims && pos >= a.rope_rows)) {
+  const bool on_table = kAxes ? load_axes(a, n, axes) : !a.rope_dims || pos < a.rope_rows;
+  if (lo < 0 || n < lo || n >= hi || hi > a.T || pos < 0 || pos >= (int64_t)a.c.max_pages * kPage || !on_table) {
     report(a.status, CSA2_ERR_BAD_INDEX);
     return false;
   }
@@ -293,10 +311,11 @@ __device__ __forceinline__ bool find_place(const AppendArgs& a, int n, Place& at
   return true;
 }
 
-template <int kDim_>
-constexpr int slot_bytes() { return kPieceRows<kDim_> * kDim_ * 2 + kDim_ * 4; }  // each token's rows, then its angles
+// Each token's rows, then its angles (of every axis: 4 slots of two CTAs still fit an SM).
+template <int kDim_, bool kAxes>
+constexpr int slot_bytes() { return kPieceRows<kDim_> * kDim_ * 2 + kDim_ * 4 * (kAxes ? 4 : 1); }
 
-template <int kDim_, bool kFp4, int kTokens>
+template <int kDim_, bool kFp4, int kTokens, bool kAxes>
 __global__ void __launch_bounds__(kStreamThreads, 2) kv_append_stream_kernel(AppendArgs a) {
   constexpr int kLanes = kDim_ / 8, kWarpRows = 32 / kLanes;
   extern __shared__ __align__(128) uint8_t smem[];
@@ -317,7 +336,7 @@ __global__ void __launch_bounds__(kStreamThreads, 2) kv_append_stream_kernel(App
   const int per = kTokens > 1 ? 1 : (n_rows + kPieceRows<kDim_> - 1) / kPieceRows<kDim_>;
   const int most = ((n_rows + per - 1) / per + 15) / 16 * 16;  // rows of a part
   const int64_t pieces = per > 1 ? (int64_t)a.T * per : (a.T + kTokens - 1) / kTokens;
-  const int angles = (per > 1 ? most : n_rows) * kDim_ * 2, token_bytes = angles + a.rope_dims * 4;
+  const int angles = (per > 1 ? most : n_rows) * kDim_ * 2, token_bytes = angles + a.rope_dims * 4 * (kAxes ? a.n_axes : 1);
   bool ok = true;
   if (warp == kWorkWarps) {
     int count = 0;  // pieces sent so far
@@ -329,8 +348,9 @@ __global__ void __launch_bounds__(kStreamThreads, 2) kv_append_stream_kernel(App
       const int row0 = per > 1 ? (int)(i % per) * most : 0;
       Place at{-1, -1, 0};
       int64_t pos = 0;
+      int axes[4];
       // (parts are whole passes: a token's last may be empty)
-      const bool there = i < pieces && n < a.T && row0 < n_rows && find_place(a, (int)n, at, pos);
+      const bool there = i < pieces && n < a.T && row0 < n_rows && find_place<kAxes>(a, (int)n, at, pos, axes);
       const uint32_t found = __ballot_sync(0xffffffffu, there);
       for (int g = 0; g < groups && ok; ++g) {
         if (!((found >> (g * kTokens)) & ((2u << (kTokens - 1)) - 1u))) continue;
@@ -342,8 +362,8 @@ __global__ void __launch_bounds__(kStreamThreads, 2) kv_append_stream_kernel(App
           const int rows = min(per > 1 ? most : n_rows, n_rows - row0);
           piece[s].at[k] = at;
           if (k == 0) piece[s].row0 = row0, piece[s].rows = rows;
-          uint8_t* dst = smem + s * slot_bytes<kDim_>() + k * token_bytes;
-          tc::mbar_arrive_expect_tx(&full[s], there ? rows * kDim_ * 2 + a.rope_dims * 4 : 0);
+          uint8_t* dst = smem + s * slot_bytes<kDim_, kAxes>() + k * token_bytes;
+          tc::mbar_arrive_expect_tx(&full[s], there ? rows * kDim_ * 2 + token_bytes - angles : 0);
           if (there) {
             // queries, keys and values: up to three runs
             const int q1 = min(row0 + rows, a.n_q), k1 = min(row0 + rows, a.n_q + a.n_kv);
@@ -356,7 +376,12 @@ __global__ void __launch_bounds__(kStreamThreads, 2) kv_append_stream_kernel(App
             if (v0 < v1)
               tc::bulk_g2s(dst + (v0 - row0) * kDim_ * 2, a.v + n * a.v_stride + (v0 - a.n_q - a.n_kv) * kDim_,
                            (v1 - v0) * kDim_ * 2, &full[s]);
-            if (a.rope_dims)
+            if constexpr (kAxes) {
+              for (int x = 0; x < a.n_axes; ++x)
+                tc::bulk_g2s(dst + angles + x * a.rope_dims * 4,
+                             a.rope + (int64_t)(x == 0 ? axes[0] : x == 1 ? axes[1] : x == 2 ? axes[2] : axes[3]) * a.rope_dims,
+                             a.rope_dims * 4, &full[s]);
+            } else if (a.rope_dims)
               tc::bulk_g2s(dst + angles, a.rope + pos * a.rope_dims, a.rope_dims * 4, &full[s]);
           }
         }
@@ -390,9 +415,16 @@ __global__ void __launch_bounds__(kStreamThreads, 2) kv_append_stream_kernel(App
       if (rows == 0) break;
       const Place at = piece[s].at[k];
       if (at.n >= 0) {
-        const uint8_t* src = smem + s * slot_bytes<kDim_>() + k * token_bytes;
+        const uint8_t* src = smem + s * slot_bytes<kDim_, kAxes>() + k * token_bytes;
         Turn turn = {};
-        if (turned) turn.load(reinterpret_cast<const float4*>(src + angles), c0, pairs, a.half);
+        if constexpr (kAxes) {
+          if (turned)
+            turn.load_axes(a, [&](int axis) {
+              return reinterpret_cast<const float2*>(src + angles + axis * a.rope_dims * 4);
+            }, c0, pairs);
+        } else if (turned) {
+          turn.load(reinterpret_cast<const float4*>(src + angles), c0, pairs, a.half);
+        }
 #pragma unroll 2
         for (int r0 = warp % kShare * kWarpRows; r0 < rows; r0 += kShare * kWarpRows) {
           const int r = r0 + lane / kLanes;
@@ -407,10 +439,10 @@ __global__ void __launch_bounds__(kStreamThreads, 2) kv_append_stream_kernel(App
   }
 }
 
-template <int kDim_, bool kFp4, int kTokens>
+template <int kDim_, bool kFp4, int kTokens, bool kAxes>
 cudaError_t stream_of(const AppendArgs& a, int64_t pieces, cudaStream_t stream) {
-  auto kern = kv_append_stream_kernel<kDim_, kFp4, kTokens>;
-  constexpr int kSmem = kSlots * slot_bytes<kDim_>();
+  auto kern = kv_append_stream_kernel<kDim_, kFp4, kTokens, kAxes>;
+  constexpr int kSmem = kSlots * slot_bytes<kDim_, kAxes>();
   static std::atomic<bool> done[64];
   const cudaError_t e = allow_smem(kern, kSmem, done);
   if (e != cudaSuccess) return e;
@@ -418,27 +450,20 @@ cudaError_t stream_of(const AppendArgs& a, int64_t pieces, cudaStream_t stream) 
   return launch_k(kern, dim3((unsigned)ctas), dim3(kStreamThreads), kSmem, stream, 0, a);
 }
 
-}  // namespace
-
-cudaError_t launch_kv_append(const csa2_kv_cfg& cfg, int B, int T, const uint16_t* q, int64_t q_stride,
-                             const uint16_t* k, int64_t k_stride, const uint16_t* v, int64_t v_stride,
-                             const int32_t* cu, const int64_t* pos0, const float* rope, int64_t rope_rows,
-                             const KvView& c, uint16_t* q_out, int64_t q_out_stride, uint16_t* k_out, uint16_t* v_out,
-                             int32_t* status, cudaStream_t stream) {
-  AppendArgs a{B, T, q ? cfg.n_heads : 0, cfg.kv_heads, cfg.rope_dims, cfg.rope_style == CSA2_ROPE_HALF ? 1 : 0,
-               q, k, v, q_stride, k_stride, v_stride, cu, pos0, rope, rope_rows, c, q_out, q_out_stride, k_out, v_out,
-               status};
-  const int rows = a.n_q + 2 * a.n_kv;
+template <bool kAxes>
+cudaError_t launch_of(const csa2_kv_cfg& cfg, const AppendArgs& a, cudaStream_t stream) {
+  const int rows = a.n_q + 2 * a.n_kv, T = a.T;
   const bool fp4 = cfg.cache_dtype == CSA2_CACHE_FP4;
   const int piece_rows = 24576 / (2 * cfg.head_dim);
   const int64_t pieces = (int64_t)T * ((rows + piece_rows - 1) / piece_rows);
   if (pieces >= kFewItems * num_sms()) {
     // four small tokens to a piece where they fit: 4096 tokens of 24 + 2 x 8 heads of
     // 64 in FP4 take 14.0 us so and 19.9 us one by one, 16000 take 37.5 and 65.2 us
-    const bool small = kSmall * (rows + 2) <= piece_rows + 2;
-#define CSA2_STREAM(D, F)                                                     \
-  (small ? stream_of<D, F, kSmall>(a, (T + kSmall - 1) / kSmall, stream)      \
-         : stream_of<D, F, 1>(a, pieces, stream))
+    // (a slot has room for four rows of angles, each two rows' worth, with kAxes)
+    const bool small = kAxes ? kSmall * (rows + 2 * a.n_axes) <= piece_rows + 8 : kSmall * (rows + 2) <= piece_rows + 2;
+#define CSA2_STREAM(D, F)                                                             \
+  (small ? stream_of<D, F, kSmall, kAxes>(a, (T + kSmall - 1) / kSmall, stream)       \
+         : stream_of<D, F, 1, kAxes>(a, pieces, stream))
     if (cfg.head_dim == 128) return fp4 ? CSA2_STREAM(128, true) : CSA2_STREAM(128, false);
     return fp4 ? CSA2_STREAM(64, true) : CSA2_STREAM(64, false);
 #undef CSA2_STREAM
@@ -449,12 +474,26 @@ cudaError_t launch_kv_append(const csa2_kv_cfg& cfg, int B, int T, const uint16_
   // + 2 x 8 heads of 128 (1000 passes) 5.1 and 4.4
   const bool few = (int64_t)T * passes <= 3 * num_sms();
   const dim3 grid(T, few ? passes : (passes + 1) / 2), block(kThreads);
-#define CSA2_APPEND(D, F)                                                          \
-  (few ? launch_k(kv_append_few_kernel<D, F, 1>, grid, block, 0, stream, 0, a)     \
-       : launch_k(kv_append_few_kernel<D, F, 2>, grid, block, 0, stream, 0, a))
+#define CSA2_APPEND(D, F)                                                                 \
+  (few ? launch_k(kv_append_few_kernel<D, F, 1, kAxes>, grid, block, 0, stream, 0, a)     \
+       : launch_k(kv_append_few_kernel<D, F, 2, kAxes>, grid, block, 0, stream, 0, a))
   if (cfg.head_dim == 128) return fp4 ? CSA2_APPEND(128, true) : CSA2_APPEND(128, false);
   return fp4 ? CSA2_APPEND(64, true) : CSA2_APPEND(64, false);
 #undef CSA2_APPEND
+}
+
+}  // namespace
+
+cudaError_t launch_kv_append(const csa2_kv_cfg& cfg, int B, int T, const uint16_t* q, int64_t q_stride,
+                             const uint16_t* k, int64_t k_stride, const uint16_t* v, int64_t v_stride,
+                             const int32_t* cu, const int64_t* pos0, const KvAxes& axes, const float* rope,
+                             int64_t rope_rows, const KvView& c, uint16_t* q_out, int64_t q_out_stride, uint16_t* k_out,
+                             uint16_t* v_out, int32_t* status, cudaStream_t stream) {
+  AppendArgs a{B, T, q ? cfg.n_heads : 0, cfg.kv_heads, cfg.rope_dims, cfg.rope_style == CSA2_ROPE_HALF ? 1 : 0,
+               q, k, v, q_stride, k_stride, v_stride, cu, pos0, rope, rope_rows, c, q_out, q_out_stride, k_out, v_out,
+               status, axes.pos, axes.n, {}};
+  for (int i = 0; axes.pos && i < cfg.rope_dims / 2; ++i) a.axis_of[i / 16] |= (uint32_t)axes.of[i] << (2 * (i % 16));
+  return axes.pos ? launch_of<true>(cfg, a, stream) : launch_of<false>(cfg, a, stream);
 }
 
 }  // namespace csa2

@@ -436,6 +436,22 @@ CSA2_API int32_t csa2_kv_append(const csa2_kv_cfg* cfg, int32_t B, int32_t T, co
                                 const csa2_kv_cache* cache, uint16_t* q_out, int64_t q_out_stride, uint16_t* k_out,
                                 uint16_t* v_out, int32_t* status, void* stream);
 
+/* csa2_kv_append with rotary positions of several axes (time, height and width
+ * of images and video among text): pair i of a row of sequence b takes its angle
+ * from rope[axes[row][axis_of[i]]][i] instead of rope[p][i].  axes [T][n_axes]
+ * int32 on the device (n_axes 1..4), one row for each row of k; axis_of
+ * [rope_dims / 2] bytes on the HOST, read during the call, each below n_axes; so
+ * runs of pairs for one axis after another and pairs in turn are both served.
+ * The slot in the cache is the running position p = pos0[b] + i as before, and
+ * only the axes' positions index `rope` (one outside [0, rope_rows):
+ * CSA2_ERR_BAD_INDEX, the row is skipped).  rope_dims must not be 0. */
+CSA2_API int32_t csa2_kv_append_axes(const csa2_kv_cfg* cfg, int32_t B, int32_t T, const uint16_t* q, int64_t q_stride,
+                                     const uint16_t* k, int64_t k_stride, const uint16_t* v, int64_t v_stride,
+                                     const int32_t* cu, const int64_t* pos0, const int32_t* axes, int32_t n_axes,
+                                     const uint8_t* axis_of, const float* rope, int64_t rope_rows,
+                                     const csa2_kv_cache* cache, uint16_t* q_out, int64_t q_out_stride, uint16_t* k_out,
+                                     uint16_t* v_out, int32_t* status, void* stream);
+
 /* Workspace bytes with which csa2_kv_attend and csa2_kv_cross_attend divide
  * the keys of these sizes among CTAs, and decode FP4 pages that many rows read
  * once ahead, as they would best (0 where that needs none); they take any
@@ -472,6 +488,112 @@ CSA2_API int32_t csa2_kv_cross_attend(const csa2_kv_cfg* cfg, int32_t B, int32_t
                                       const int32_t* kv_len, int32_t max_q, int32_t max_kv, float scale,
                                       uint16_t* out, int64_t out_stride, float* lse, void* workspace,
                                       size_t workspace_bytes, int32_t* status, void* stream);
+
+/* ---- beams over such caches ----
+ * Beam g * beams + k is sequence g * beams + k of the caches, group g's k-th. */
+
+/* Workspace bytes of csa2_beam_select; 0 for sizes that it refuses. */
+CSA2_API size_t csa2_beam_workspace_bytes(int32_t groups, int32_t beams, int32_t vocab, int32_t take);
+
+/* Best continuations of each group over its beams and the vocabulary.  With
+ * x = logits[g * beams + k] and lse = log sum_v exp x_v (natural), token v of beam
+ * k has the score cum[g][k] + x_v - lse, and the best `take` of a group's scores
+ * are written in order (score descending; of equal scores the lower beam, then the
+ * lower token): scores [groups][take] fp32, parents [groups][take] (the sequence
+ * number g * beams + k) and tokens [groups][take] int32.  Scores are compared in
+ * fp64, lse being summed from fp32 exponentials in fp64, and rounded once.
+ *  - A token of logit -inf (masked) and every token of a beam whose cum is -inf is
+ *    no candidate; where candidates run out, score -inf, parent and token -1.
+ *  - done [groups][beams] bytes or NULL: a beam that is done (not 0) has end_token
+ *    alone as candidate, at score cum; its logits are not read.
+ *  - lse [groups * beams] fp32 or NULL receives each beam's lse (0 where done, -inf
+ *    where every logit is).
+ *  - A logit that is NaN or +inf counts as -inf, a cum that is NaN or +inf too; each
+ *    sets CSA2_ERR_RANGE.
+ * logits: bf16 (logits_dtype CSA2_BF16) or fp32 (CSA2_F32) rows of `vocab` contiguous
+ * values, `stride` elements apart (any distance from vocab on), the first 16-byte
+ * aligned.  beams 1..64, take 1..64, groups * beams < 2^31 / vocab's parts of 16384
+ * (CSA2_ERR_UNSUPPORTED beyond).  Workspace: csa2_beam_workspace_bytes, 256-byte
+ * aligned (smaller: CSA2_ERR_CAPACITY), contents not kept between calls; two calls
+ * that may overlap need one each. */
+CSA2_API int32_t csa2_beam_select(int32_t groups, int32_t beams, int32_t vocab, int32_t take, const void* logits,
+                                  int32_t logits_dtype, int64_t stride, const float* cum, const uint8_t* done,
+                                  int32_t end_token, float* scores, int32_t* parents, int32_t* tokens, float* lse,
+                                  void* workspace, size_t workspace_bytes, int32_t* status, void* stream);
+
+/* The beams' cached states put in the order of a selection: sequence i goes on from
+ * what parents[i] (a sequence of its group, or -1: from nothing) had.  The caches of
+ * `layers` layers (at most CSA2_MAX_LAYERS, all with cfg's shape, one block table and
+ * one page count) are reordered by one call; kv_len [groups * beams] is the same
+ * throughout a group, in which n = kv_len / 64 pages of each sequence are full.
+ *  - Full pages are not copied: block_table[i][0 .. n) becomes a copy of the parent's
+ *    row, so that pages come to be shared by sequences (no append writes to them).
+ *  - The last page, where kv_len % 64 slots are written, must be a sequence's own, and
+ *    stays so: of a parent's children one keeps it (the parent itself if it is its own
+ *    child, else the lowest), and each other child, in order, takes the last page of
+ *    a sequence of the group without children, in order, into which the parent's
+ *    written slots are copied (there are as many of these as of those).
+ *  - block_table[i][n + 1 ..), and [n ..) where kv_len is a multiple of 64, are left
+ *    as they are: pages that a sequence has ahead of its length are its own.
+ * So with tables that start out with pages of their own from the shared prompt's last,
+ * partly written page on (this call with parents 0 makes beams of one prompt), every
+ * append after a reordering writes to pages of its own alone, and no page is needed
+ * that the tables do not hold.  Sequences do not move: kv_len stays as it is.
+ * block_table is written although csa2_kv_cache has it const.
+ * Conditions found on the device: a parent outside its group, lengths that differ in
+ * a group or lie outside the cache (CSA2_ERR_BAD_INDEX, the group is left as it is); a
+ * last page's id outside the pool (CSA2_ERR_BAD_PAGE, not copied).  beams 1..64. */
+#define CSA2_MAX_LAYERS 128
+CSA2_API int32_t csa2_kv_reorder(const csa2_kv_cfg* cfg, int32_t layers, const csa2_kv_cache* caches, int32_t groups,
+                                 int32_t beams, const int32_t* parents, const int32_t* kv_len, int32_t* status,
+                                 void* stream);
+
+/* ---- projections with 4-bit weights ----
+ * What feeds these layers and the sparse path (queries from low-rank ones, indexer
+ * queries, keys and values, logits): y = x W^T with W [n][k] in the caches' codec,
+ * E2M1 codes with one E4M3 scale per 16 of a row, so W[i][j] = alpha * code * scale.
+ * alpha stands for what the scales cannot reach: weights of 0.02 would leave them
+ * few bits, so they are encoded times a gain of, say, 2^14 and alpha undoes it.
+ * Weights are laid out once for the products, in blocks of 16 rows x 128 channels
+ * (rows and channels beyond n and k are zeros): csa2_fp4_encode does it from bf16,
+ * csa2_fp4_pack from codes and scales. */
+enum { CSA2_BF16 = 0, CSA2_F32 = 1 };
+
+typedef struct csa2_fp4_weights {
+  const void* data; /* csa2_fp4_weight_bytes(n, k) bytes, 128-byte aligned */
+  int32_t n, k;     /* rows (outputs); channels, a multiple of 16 */
+  float alpha;      /* finite */
+  int32_t reserved; /* must be 0 */
+} csa2_fp4_weights;
+
+/* Bytes of laid-out weights; 0 unless n >= 1, k >= 16, k % 16 == 0, and both below
+ * 2^24. */
+CSA2_API size_t csa2_fp4_weight_bytes(int32_t n, int32_t k);
+
+/* Weights from bf16 rows w [n][k] (`stride` elements apart, a multiple of 8; 16-byte
+ * aligned) into `packed`: of each w * gain (rounded to fp32), scale = RNE_E4M3(amax / 6),
+ * code = RNE_E2M1(w * gain / scale), ties to even, saturating, a value that rounds to
+ * zero is +0.  A value that is not finite sets CSA2_ERR_RANGE and counts as the
+ * largest of its sign, NaN as 0.  The products' alpha is then 1 / gain. */
+CSA2_API int32_t csa2_fp4_encode(int32_t n, int32_t k, const uint16_t* w, int64_t stride, float gain, void* packed,
+                                 int32_t* status, void* stream);
+
+/* Weights from codes [n][k / 2] (channel 2i in the low nibble of byte i) and E4M3
+ * scales [n][k / 16], both contiguous, the codes 4-byte aligned, into `packed`.  A scale's sign counts; the NaN pattern (0x7F, 0xFF) sets
+ * CSA2_ERR_RANGE and counts as 0. */
+CSA2_API int32_t csa2_fp4_pack(int32_t n, int32_t k, const uint8_t* codes, const uint8_t* scales, void* packed,
+                               int32_t* status, void* stream);
+
+/* out[t][i] = alpha * sum_j x[t][j] code[i][j] scale[i][j / 16] (+ bias[i]): products of
+ * bf16 x and the exact weights, which bf16 holds, summed in fp32, rounded once.
+ * x [T][k] bf16, rows `x_stride` elements apart (a multiple of 8), 16-byte aligned; bias
+ * [n] bf16 or NULL; out [T][n] bf16 (out_dtype CSA2_BF16) or fp32 (CSA2_F32), rows
+ * `out_stride` elements apart (any distance from n on).  out must not overlap x or
+ * the weights.  An x that is not finite has effect on its own row's outputs alone.
+ * Rows' sums do not depend on what other rows hold, but their order may depend on T. */
+CSA2_API int32_t csa2_fp4_linear(const csa2_fp4_weights* w, int32_t T, const uint16_t* x, int64_t x_stride,
+                                 const uint16_t* bias, void* out, int32_t out_dtype, int64_t out_stride,
+                                 int32_t* status, void* stream);
 
 #ifdef __cplusplus
 }

@@ -49,19 +49,7 @@ int32_t csa2_fp4_linear(const csa2_fp4_weights* w, int32_t T, const uint16_t* x,
   Fp4Linear a{static_cast<const uint8_t*>(w->data), w->n, w->k, fp4_k_blocks(w->k), T, x, x_stride, bias, out, out_stride,
               out_dtype == CSA2_F32 ? 1 : 0, w->alpha * kFp4Unit, status};
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (fp4_rows_ok(a)) return cuda_status(launch_fp4_rows(a, s));
-  // as many rows at a time as fit
-  a.T = kFp4FewRows;
-  while (a.T > 1 && !fp4_rows_ok(a)) --a.T;
-  if (!fp4_rows_ok(a)) return CSA2_ERR_UNSUPPORTED;
-  for (int t = 0; t < T; t += a.T) {
-    Fp4Linear b = a;
-    b.T = T - t < a.T ? T - t : a.T;
-    b.x = x + t * x_stride;
-    b.out = static_cast<uint8_t*>(out) + t * out_stride * (a.f32 ? 4 : 2);
-    if (const cudaError_t e = launch_fp4_rows(b, s)) return cuda_status(e);
-  }
-  return CSA2_OK;
+  return cuda_status(fp4_rows_ok(a) ? launch_fp4_rows(a, s) : launch_fp4_tiles(a, s));
 }
 
 }  // extern "C"

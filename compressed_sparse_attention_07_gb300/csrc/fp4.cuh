@@ -2,12 +2,15 @@
 // fp4_tiles.cu): how the weights are laid out, and their decoding to bf16.
 //
 // A block is 16 rows x 128 channels in 1152 bytes: 1024 of codes, 128 of scales; the
-// blocks of 16 rows follow one another along k, then the next 16 rows.  A warp reads
-// a block as the left operand of eight 16x8x16 products: lane 4 g + t holds channels
-// 32 t .. 32 t + 31 of rows g (bytes 16 lane ..) and g + 8 (bytes 512 + 16 lane ..), its
-// i-th word the eight channels of 16-byte chunk i ^ t (of the right operand, of which
-// it needs the same channels: so lanes of neighbouring t read and write shared memory
-// in different banks).  Within a word the even channels of the eight stand in the low
+// eight blocks of 128 rows and 128 channels follow one another, these along k, then the
+// next 128 rows.  In a block the codes are in units of 16 bytes, 32 channels of a row:
+// those of row r and channels 32 t .. at fp4_unit(r, t).  A warp reads them conflict-free
+// both as the left operand of eight 16x8x16 products (lane 4 g + t: unit t of rows g and
+// g + 8) and a row a lane.  The i-th word of unit t has the eight channels of 16-byte
+// chunk i ^ t of the unit's 32 in bf16, so that lanes of neighbouring t read different
+// banks of rows of x too.  The two scales of a row's unit stand at fp4_unit_scales(r, t),
+// that of words 0 and 1 first.
+// Within a word the even channels of the eight stand in the low
 // half, the odd ones in the high half, their codes s e1 e0 m at bits
 //   15 8 7 6 | 12 5 4 3 | 9 2 1 0 | 14 13 11 10
 // of the half, so that one shift and one mask (four more operations for the last)
@@ -27,7 +30,13 @@ namespace csa2 {
 constexpr int kBlockRows = 16, kBlockK = 128, kBlockBytes = 1152, kBlockCodes = 1024;
 constexpr float kFp4Unit = 256.0f;  // what the decoded weights are short of
 
-__host__ __device__ __forceinline__ int fp4_row_groups(int n) { return (n + 31) / 32 * 2; }
+constexpr int kTileRows = 128, kTileBlocks = kTileRows / kBlockRows, kTileBytes = kTileBlocks * kBlockBytes;
+
+__host__ __device__ constexpr int fp4_unit(int r, int t) { return t * 256 + (r >> 3) * 128 + ((r & 7) ^ (2 * t)) * 16; }
+__host__ __device__ constexpr int fp4_unit_scales(int r, int t) {
+  return kBlockCodes + ((r & 7) * 4 + t) * 4 + (r >> 3) * 2;
+}
+__host__ __device__ __forceinline__ int fp4_row_tiles(int n) { return (n + kTileRows - 1) / kTileRows; }
 __host__ __device__ __forceinline__ int fp4_k_blocks(int k) { return (k + kBlockK - 1) / kBlockK; }
 
 struct Fp4Linear {

@@ -17,7 +17,7 @@ bool sizes_ok(int32_t n, int32_t k) { return n >= 1 && k >= 16 && k % 16 == 0 &&
 extern "C" {
 
 size_t csa2_fp4_weight_bytes(int32_t n, int32_t k) {
-  return sizes_ok(n, k) ? (size_t)fp4_row_groups(n) * fp4_k_blocks(k) * kBlockBytes : 0;
+  return sizes_ok(n, k) ? (size_t)fp4_row_tiles(n) * fp4_k_blocks(k) * kTileBytes : 0;
 }
 
 int32_t csa2_fp4_encode(int32_t n, int32_t k, const uint16_t* w, int64_t stride, float gain, void* packed,

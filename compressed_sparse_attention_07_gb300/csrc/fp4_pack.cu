@@ -32,11 +32,12 @@ __device__ __forceinline__ bool spot(int n, int k, Spot& s) {
   const int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x;
   const int blocks = fp4_k_blocks(k);
   s.block = i >> 6;
-  if (s.block >= (int64_t)fp4_row_groups(n) * blocks) return false;
+  const int64_t tile = s.block / kTileBlocks;  // of 128 rows x 128 channels
+  if (tile >= (int64_t)fp4_row_tiles(n) * blocks) return false;
   const int in = (int)(i & 63);
   s.t = in & 3;
-  s.row = (int)(s.block / blocks) * kBlockRows + (in >> 2);
-  s.k0 = (int)(s.block % blocks) * kBlockK + 32 * s.t;
+  s.row = (int)(tile / blocks) * kTileRows + (int)(s.block % kTileBlocks) * kBlockRows + (in >> 2);
+  s.k0 = (int)(tile % blocks) * kBlockK + 32 * s.t;
   return true;
 }
 
@@ -44,7 +45,7 @@ __device__ __forceinline__ bool spot(int n, int k, Spot& s) {
 // thread's channels into their block.
 __device__ __forceinline__ void put(uint8_t* packed, const Spot& s, const uint32_t (&codes)[4], const uint32_t (&scale)[2]) {
   uint8_t* block = packed + s.block * kBlockBytes;
-  const int r = s.row % kBlockRows, lane = (r & 7) * 4 + s.t, half = r >> 3;
+  const int r = s.row % kBlockRows;
   uint32_t w[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -54,10 +55,10 @@ __device__ __forceinline__ void put(uint8_t* packed, const Spot& s, const uint32
       if ((i ^ s.t) == j) c = codes[j];
     w[i] = arrange(c);
   }
-  *reinterpret_cast<uint4*>(block + half * 512 + lane * 16) = make_uint4(w[0], w[1], w[2], w[3]);
+  *reinterpret_cast<uint4*>(block + fp4_unit(r, s.t)) = make_uint4(w[0], w[1], w[2], w[3]);
   // the scale of words 0 and 1 first
   const uint32_t first = s.t & 2 ? scale[1] : scale[0], second = s.t & 2 ? scale[0] : scale[1];
-  *reinterpret_cast<uint16_t*>(block + kBlockCodes + lane * 4 + half * 2) = (uint16_t)(first | second << 8);
+  *reinterpret_cast<uint16_t*>(block + fp4_unit_scales(r, s.t)) = (uint16_t)(first | second << 8);
 }
 
 __global__ void __launch_bounds__(kThreads) fp4_pack_kernel(int n, int k, const uint8_t* codes, const uint8_t* scales,
@@ -124,7 +125,7 @@ __global__ void __launch_bounds__(kThreads) fp4_encode_kernel(int n, int k, cons
   put(packed, s, c, sc);
 }
 
-int64_t grid_of(int n, int k) { return ((int64_t)fp4_row_groups(n) * fp4_k_blocks(k) * 64 + kThreads - 1) / kThreads; }
+int64_t grid_of(int n, int k) { return (int64_t)fp4_row_tiles(n) * fp4_k_blocks(k) * kTileBlocks * 64 / kThreads; }
 
 }  // namespace
 

@@ -74,20 +74,27 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_rows_kernel(const Fp4Linear a
   const int tile0 = (int)((int64_t)blockIdx.x * tiles / gridDim.x);
   const int units = ((int)((int64_t)(blockIdx.x + 1) * tiles / gridDim.x) - tile0) * a.k_blocks;
   const int u0 = (int)((int64_t)warp * units / kWarps), u1 = (int)((int64_t)(warp + 1) * units / kWarps);
-  auto source = [&](int u, int i) {  // block of the i-th 16 rows of unit u
-    const int tile = tile0 + u / a.k_blocks, kb = u % a.k_blocks;
-    return a.w + (((int64_t)tile * kGroups + i) * a.k_blocks + kb) * kBlockBytes;
-  };
-  auto fetch = [&](int u) {
-    const int s = (u - u0) % slots;
-    tc::mbar_arrive_expect_tx(&full[warp][s], kGroups * kBlockBytes);
-#pragma unroll
-    for (int i = 0; i < kGroups; ++i)
-      tc::bulk_g2s(ring + (s * kGroups + i) * kBlockBytes, source(u, i), kBlockBytes, &full[warp][s]);
+  // the next unit to fetch: its blocks, its place in k and in the ring (no division in
+  // the loop: with u / k_blocks and u % slots in it a unit of 32 rows took 512
+  // instructions, and takes 340)
+  const int kb0 = units ? u0 % a.k_blocks : 0, first = units ? u0 / a.k_blocks : 0;
+  constexpr int kParts = kTileBlocks / kGroups;  // tiles of this kernel in 128 rows
+  const int64_t far = (int64_t)(a.k_blocks - 1) * kTileBytes;
+  int src_tile = tile0 + first, src_kb = kb0, src_slot = 0;
+  const uint8_t* src = a.w + ((int64_t)(src_tile / kParts) * a.k_blocks + kb0) * kTileBytes +
+                       src_tile % kParts * (kGroups * kBlockBytes);
+  auto fetch = [&]() {
+    tc::mbar_arrive_expect_tx(&full[warp][src_slot], kGroups * kBlockBytes);
+    tc::bulk_g2s(ring + src_slot * (kGroups * kBlockBytes), src, kGroups * kBlockBytes, &full[warp][src_slot]);
+    src += kTileBytes;
+    if (++src_kb == a.k_blocks) {  // the next tile's first block: beside this one's, or at the next 128 rows
+      src_kb = 0, ++src_tile;
+      src += kGroups * kBlockBytes - (src_tile % kParts ? far + kTileBytes : kTileBytes);
+    }
+    if (++src_slot == slots) src_slot = 0;
   };
   if (lane == 0) {
-    for (int u = u0; u < min(u1, u0 + slots); ++u)
-      for (int i = 0; i < kGroups; ++i) tc::bulk_prefetch_l2(source(u, i), kBlockBytes);
+    if (u0 < u1) tc::bulk_prefetch_l2(src, kGroups * kBlockBytes);
     for (int s = 0; s < slots; ++s) tc::mbar_init(&full[warp][s], 1);
     tc::fence_mbar_init();
     piece_tile[2 * warp] = piece_tile[2 * warp + 1] = -1;
@@ -95,7 +102,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_rows_kernel(const Fp4Linear a
   __syncwarp();
   griddep_wait();  // every input may be the previous kernel's output
   if (lane == 0)
-    for (int u = u0; u < min(u1, u0 + slots); ++u) fetch(u);
+    for (int u = u0; u < min(u1, u0 + slots); ++u) fetch();
   {  // x, zeros from channel k on
     const int chunks = a.k_blocks * 16;
     for (int r = 0; r < a.T; ++r)
@@ -109,28 +116,28 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_rows_kernel(const Fp4Linear a
   const uint8_t* xr = xs + min(g, a.T - 1) * pitch + t * 64;  // (columns from T on are dropped)
 
   float acc[kGroups][4] = {};
-  int kb = units ? u0 % a.k_blocks : 0, tile = units ? u0 / a.k_blocks : 0, piece = 0;
+  int kb = kb0, tile = first, piece = 0, s = 0;
+  uint32_t phase = 0;
   bool whole = kb == 0, ok = true;
-  int sent = u0;  // one past the last unit whose copy has landed
   for (int u = u0; u < u1; ++u) {
-    const int s = (u - u0) % slots;
-    ok = __all_sync(0xffffffffu, tc::mbar_wait(&full[warp][s], ((u - u0) / slots) & 1));
-    if (!ok) break;
-    sent = u + 1;
+    tc::mbar_wait_or(&full[warp][s], phase, ok);  // (sums of what stands there, and a status, where it gives up)
+    __syncwarp();
     uint4 lo[kGroups], hi[kGroups];
     uint32_t sc[kGroups];
 #pragma unroll
     for (int i = 0; i < kGroups; ++i) {
       const uint8_t* b = ring + (s * kGroups + i) * kBlockBytes;
-      lo[i] = *reinterpret_cast<const uint4*>(b + 16 * lane);
-      hi[i] = *reinterpret_cast<const uint4*>(b + 512 + 16 * lane);
+      lo[i] = *reinterpret_cast<const uint4*>(b + fp4_unit(g, t));
+      hi[i] = *reinterpret_cast<const uint4*>(b + fp4_unit(g + 8, t));
       sc[i] = *reinterpret_cast<const uint32_t*>(b + kBlockCodes + 4 * lane);
     }
     __syncwarp();
-    if (lane == 0 && u + slots < u1) fetch(u + slots);
+    if (lane == 0 && u + slots < u1) fetch();
+    if (++s == slots) s = 0, phase ^= 1;
+    const uint8_t* xk = xr + kb * 256;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const uint4 x = *reinterpret_cast<const uint4*>(xr + kb * 256 + (j ^ t) * 16);
+      const uint4 x = *reinterpret_cast<const uint4*>(xk + (j ^ t) * 16);
 #pragma unroll
       for (int i = 0; i < kGroups; ++i) {
         const uint32_t wl = j == 0 ? lo[i].x : j == 1 ? lo[i].y : j == 2 ? lo[i].z : lo[i].w;
@@ -159,9 +166,9 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_rows_kernel(const Fp4Linear a
     }
   }
   if (!ok) {
-    if (lane == 0) report(a.status, CSA2_ERR_TIMEOUT);
+    report(a.status, CSA2_ERR_TIMEOUT);
     // nothing may land in shared memory after the CTA has left
-    for (int u = sent; u < min(u1, sent + slots); ++u) tc::mbar_wait(&full[warp][(u - u0) % slots], ((u - u0) / slots) & 1);
+    for (int u = max(u0, u1 - slots); u < u1; ++u) tc::mbar_wait(&full[warp][(u - u0) % slots], ((u - u0) / slots) & 1);
   }
   __syncthreads();
   // a shared tile's pieces stand in the order of its channels, two places a warp: the

@@ -2,17 +2,17 @@
 // 128 rows of W x 16 .. 256 rows of x.
 //
 // D[128][rows of x] = W x^T accumulates in tensor memory over steps of 128 channels.  A
-// step's packed weights (9 KB) come by bulk copies, its rows of x by tensor copies (two
-// boxes of 64 channels, 128-byte swizzle; rows and channels outside are zeros);
-// sixteen warps decode the weights, 32 of a row a lane, into the left operand's tile
-// in shared memory, whose 8-row columns of 16 bytes stand 2080 bytes apart so that
-// lanes of one phase write different banks; one warp issues the eight products of
-// 128 x rows x 16.  Few rows are bound by the weights' bytes and their decoding, many
-// by the products (256 rows: 512 cycles a step, of which decoding takes 320 issue slots
-// of each scheduler).  A CTA takes tile after tile, with two accumulators, so that the
-// sums of one are stored while the next is formed.  Where the tiles fill less than
-// half the SMs, a cluster divides k, and its CTAs join their sums through distributed
-// shared memory in rank order.
+// step's packed weights (9 KB) come by one bulk copy, its rows of x by two tensor copies
+// (64 channels each, 128-byte swizzle; rows and channels outside are zeros); four
+// sets of four warps, a step each, decode the weights, a row a lane, into tensor memory,
+// from where the products take their left operand; one warp issues the eight products of
+// 128 x rows x 16.  Few rows are bound by the weights' bytes and their decoding, many by
+// the products (256 rows: 1024 cycles a step) and shared memory beside them: x goes in and
+// is read once a step, 1024 cycles at 128 bytes a cycle; with the left operand in shared
+// memory too they were 1570, and took 1690.  A CTA takes tile after tile, up to 128 rows
+// of x with two accumulators, so that the sums of one are stored while the next is
+// formed.  Where the tiles fill less than half the SMs, a cluster divides k, and its
+// CTAs join their sums through distributed shared memory in rank order.
 #include <cuda.h>
 
 #include <algorithm>
@@ -23,21 +23,37 @@
 namespace csa2 {
 namespace {
 
-constexpr int kDecoders = 16, kWarps = 8 + kDecoders, kThreads = 32 * kWarps;
-constexpr int kRows = 128;                      // of W a tile
-constexpr int kStepBytes = 8 * kBlockBytes;     // packed
-constexpr int kChunk = kRows * 16 + 32;         // 16 bytes of every row
-constexpr int kABytes = 16 * kChunk;
+constexpr int kSets = 4, kDecoders = 4 * kSets, kWarps = 8 + kDecoders, kThreads = 32 * kWarps;
 constexpr int kSmemMost = 227 * 1024 - 1024;
 
-// Places of the rings for kTok rows of x.
+// Places of the rings for kTok rows of x: kS steps of decoded weights in tensor memory,
+// 64 columns each beside kD accumulators; kX places of kBoxes boxes of x; kP packed steps.
+// Four decoding warps, a set, have every kSets-th step, so a set does not see every phase
+// of every place, and must not take the phase before the last (of the same parity) for
+// the last.  Packed steps may land out of order: with kP a multiple of kSets a set sees
+// every phase of its own places.  Decoded steps become free in order: a set that passed
+// step n - kSets knows step n - kSets - kS to be free, hence step n - 2 kS if kS >= kSets.
 template <int kTok>
 struct Rings {
-  static constexpr int kXBytes = kTok * 2 * kBlockK;
-  static constexpr int kX = kTok == 256 ? 2 : kTok == 128 ? 3 : 4;
-  static constexpr int kA = kTok == 256 ? 2 : 3;
-  static constexpr int kP = kTok >= 128 ? 3 : kTok == 64 ? 6 : 9;
-  static constexpr int kSmem = 1024 + kX * kXBytes + kA * kABytes + kP * kStepBytes;
+  static constexpr int kD = kTok == 256 ? 1 : 2, kS = kTok >= 128 ? 4 : 6;
+  static constexpr int kBoxes = kTok == 256 ? 1 : 2, kX = kTok == 256 ? 5 : kTok == 128 ? 4 : 6;
+  static constexpr int kBoxBytes = kTok * 128, kXBytes = kBoxes * kBoxBytes;
+  static constexpr int kP = kTok == 256 ? 4 : kTok == 128 ? 8 : kTok == 64 ? 12 : kTok == 32 ? 16 : 20;
+  static constexpr int kSmem = 1024 + kX * kXBytes + kP * kTileBytes;
+  static constexpr int kA = kD * kTok;  // first column of the decoded weights
+  static constexpr int kCols = 512;
+  static_assert(kP % kSets == 0 && kS >= kSets && kA + 64 * kS <= kCols && kSmem <= kSmemMost &&
+                    kX * kXBytes >= kTok * kTileRows * 4, "");
+};
+
+// A place of a ring and the parity of its next phase.
+template <int kSlots>
+struct Place {
+  int s = 0;
+  uint32_t phase = 0;
+  __device__ __forceinline__ void next() {
+    if (++s == kSlots) s = 0, phase ^= 1;
+  }
 };
 
 struct TileArgs {
@@ -53,21 +69,44 @@ __device__ __forceinline__ void tensor_g2s(uint32_t dst, const CUtensorMap* map,
       : "memory");
 }
 
+__device__ __forceinline__ void put(float* o, float y) { *o = y; }
+__device__ __forceinline__ void put(__nv_bfloat16* o, float y) { *o = __float2bfloat16_rn(y); }
+// A lane's sums of `most` rows of x, one of each row of out.
+template <typename T, int kCols>
+__device__ __forceinline__ void store_columns(T* o, const uint32_t (&v)[kCols], int most, const Fp4Linear& l, float bias) {
+  if (most == kCols) {
+#pragma unroll
+    for (int j = 0; j < kCols; ++j, o += l.out_stride) put(o, fmaf(__uint_as_float(v[j]), l.alpha, bias));
+  } else {
+#pragma unroll
+    for (int j = 0; j < kCols; ++j, o += l.out_stride)
+      if (j < most) put(o, fmaf(__uint_as_float(v[j]), l.alpha, bias));
+  }
+}
+
+template <int kI>
+struct Number {
+  __device__ constexpr int operator()() const { return kI; }
+};
+
+// A value that is the same in all lanes, in a register that is known to be.
+__device__ __forceinline__ uint32_t uniform(uint32_t v) { return __reduce_max_sync(0xffffffffu, v); }
+
 template <int kTok>
 __global__ void __launch_bounds__(kThreads, 1) fp4_tiles_kernel(const __grid_constant__ CUtensorMap map, const TileArgs a) {
   using R = Rings<kTok>;
   extern __shared__ uint8_t raw[];
   uint8_t* smem = raw + ((1024 - (tc::smem_u32(raw) & 1023)) & 1023);
-  uint8_t *xs = smem, *as = xs + R::kX * R::kXBytes, *ps = as + R::kA * kABytes;
-  __shared__ __align__(8) uint64_t full_p[R::kP], empty_p[R::kP], full_x[R::kX], empty_x[R::kX], full_a[R::kA],
-      empty_a[R::kA], full_d[2], empty_d[2], drained;
+  uint8_t *xs = smem, *ps = xs + R::kX * R::kXBytes;
+  __shared__ __align__(8) uint64_t full_p[R::kP], empty_p[R::kP], full_x[R::kX], empty_x[R::kX], full_a[R::kS],
+      empty_a[R::kS], full_d[R::kD], empty_d[R::kD], drained;
   __shared__ uint32_t tmem;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (tid == 0) {
-    for (int i = 0; i < R::kP; ++i) tc::mbar_init(&full_p[i], 1), tc::mbar_init(&empty_p[i], kDecoders);
+    for (int i = 0; i < R::kP; ++i) tc::mbar_init(&full_p[i], 1), tc::mbar_init(&empty_p[i], 4);
     for (int i = 0; i < R::kX; ++i) tc::mbar_init(&full_x[i], 1), tc::mbar_init(&empty_x[i], 1);
-    for (int i = 0; i < R::kA; ++i) tc::mbar_init(&full_a[i], kDecoders), tc::mbar_init(&empty_a[i], 1);
-    for (int i = 0; i < 2; ++i) tc::mbar_init(&full_d[i], 1), tc::mbar_init(&empty_d[i], 4);
+    for (int i = 0; i < R::kS; ++i) tc::mbar_init(&full_a[i], 4), tc::mbar_init(&empty_a[i], 1);
+    for (int i = 0; i < R::kD; ++i) tc::mbar_init(&full_d[i], 1), tc::mbar_init(&empty_d[i], 4);
     tc::mbar_init(&drained, 1);
     tc::fence_mbar_init();
   }
@@ -75,164 +114,187 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_tiles_kernel(const __grid_con
   const int rank = a.split > 1 ? (int)tc::cluster_rank() : 0;
   const int first = blockIdx.x / a.split, stride = gridDim.x / a.split;
   const int s0 = (int)((int64_t)rank * a.l.k_blocks / a.split), s1 = (int)((int64_t)(rank + 1) * a.l.k_blocks / a.split);
-  const int groups = (a.l.n + kBlockRows - 1) / kBlockRows;  // of 16 rows
-  auto weights = [&](int tile, int step, int g) {
-    return a.l.w + (((int64_t)(tile % a.row_tiles) * 8 + g) * a.l.k_blocks + step) * kBlockBytes;
-  };
-  if (warp == 0 && lane < 8 && first < a.tiles && first % a.row_tiles * 8 + lane < groups)
-    for (int i = s0; i < min(s1, s0 + R::kP); ++i) tc::bulk_prefetch_l2(weights(first, i, lane), kBlockBytes);
+  auto weights = [&](int tile) { return a.l.w + (int64_t)(tile % a.row_tiles) * a.l.k_blocks * kTileBytes; };
+  // blocks of 16 rows that a tile has (what it decodes beyond them is not stored)
+  auto blocks = [&](int tile) { return min(kTileBlocks, (a.l.n + kBlockRows - 1) / kBlockRows - tile % a.row_tiles * kTileBlocks); };
+  if (tid == 0 && first < a.tiles)
+    tc::bulk_prefetch_l2(weights(first) + (int64_t)s0 * kTileBytes, min(R::kP, s1 - s0) * kTileBytes);
   griddep_wait();  // every input may be the previous kernel's output
   if (warp == 3) {
-    tc::tmem_alloc(&tmem, 2 * kTok);
+    tc::tmem_alloc(&tmem, R::kCols);
     tc::tmem_relinquish();
   }
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
+  // Every wait gives up after a second; its thread then goes on with what is there (all
+  // addresses stay inside the rings), but starts no copy, and reports.
   bool ok = true;
 
   if (warp == 0) {  // packed weights
     int n = 0;
+    Place<R::kP> at;
     for (int tile = first; tile < a.tiles && ok; tile += stride) {
-      const int there = min(8, groups - tile % a.row_tiles * 8);
-      for (int step = s0; step < s1 && ok; ++step, ++n) {
-        const int s = n % R::kP;
-        if (n >= R::kP) ok = __all_sync(0xffffffffu, tc::mbar_wait(&empty_p[s], ((n / R::kP) & 1) ^ 1));
-        if (!ok) break;
-        if (lane == 0) tc::mbar_arrive_expect_tx(&full_p[s], there * kBlockBytes);
-        __syncwarp();
-        if (lane < there) tc::bulk_g2s(ps + s * kStepBytes + lane * kBlockBytes, weights(tile, step, lane), kBlockBytes, &full_p[s]);
+      const uint8_t* src = weights(tile) + (int64_t)s0 * kTileBytes;
+      const int bytes = blocks(tile) * kBlockBytes;
+      for (int step = s0; step < s1; ++step, ++n, at.next(), src += kTileBytes) {
+        if (n >= R::kP) tc::mbar_wait_or(&empty_p[at.s], at.phase ^ 1, ok);
+        if (!__all_sync(0xffffffffu, ok)) break;
+        if (tc::elect_one()) {
+          tc::mbar_arrive_expect_tx(&full_p[at.s], bytes);
+          tc::bulk_g2s(ps + at.s * kTileBytes, src, bytes, &full_p[at.s]);
+        }
       }
     }
     // nothing may land in shared memory after the CTA has left
-    for (int i = max(0, n - R::kP); i < n; ++i) tc::mbar_wait(&full_p[i % R::kP], (i / R::kP) & 1);
+    for (int i = max(0, n - R::kP); i < n && tc::mbar_wait(&full_p[i % R::kP], (i / R::kP) & 1); ++i) {}
   } else if (warp == 1) {  // rows of x
     int n = 0;
+    Place<R::kX> at;
     for (int tile = first; tile < a.tiles && ok; tile += stride) {
       const int row = tile / a.row_tiles * kTok;
-      for (int step = s0; step < s1 && ok; ++step, ++n) {
-        const int s = n % R::kX;
-        if (n >= R::kX) ok = __all_sync(0xffffffffu, tc::mbar_wait(&empty_x[s], ((n / R::kX) & 1) ^ 1));
-        if (!ok) break;
-        if (lane == 0) {
-          tc::mbar_arrive_expect_tx(&full_x[s], R::kXBytes);
-          const uint32_t dst = tc::smem_u32(xs + s * R::kXBytes);
-          tensor_g2s(dst, &map, step * kBlockK, row, &full_x[s]);
-          tensor_g2s(dst + R::kXBytes / 2, &map, step * kBlockK + 64, row, &full_x[s]);
+      for (int box = 2 * s0; box < 2 * s1; box += R::kBoxes, ++n, at.next()) {
+        if (n >= R::kX) tc::mbar_wait_or(&empty_x[at.s], at.phase ^ 1, ok);
+        if (!__all_sync(0xffffffffu, ok)) break;
+        if (tc::elect_one()) {
+          tc::mbar_arrive_expect_tx(&full_x[at.s], R::kXBytes);
+#pragma unroll
+          for (int i = 0; i < R::kBoxes; ++i)
+            tensor_g2s(tc::smem_u32(xs + at.s * R::kXBytes + i * R::kBoxBytes), &map, (box + i) * 64, row, &full_x[at.s]);
         }
-        __syncwarp();
       }
     }
-    for (int i = max(0, n - R::kX); i < n; ++i) tc::mbar_wait(&full_x[i % R::kX], (i / R::kX) & 1);
+    for (int i = max(0, n - R::kX); i < n && tc::mbar_wait(&full_x[i % R::kX], (i / R::kX) & 1); ++i) {}
   } else if (warp == 2) {  // products
-    constexpr uint32_t kIdesc = tc::idesc_f16(kRows, kTok, true, true, false, false);
-    constexpr uint32_t kAHi = tc::sdesc_hi(128), kBHi = tc::sdesc_hi(1024) | 2u << 29;  // B: 128-byte swizzle
-    int n = 0, it = 0;
-    for (int tile = first; tile < a.tiles && ok; tile += stride, ++it) {
-      const int d = it & 1;
-      if (it >= 2) ok = __all_sync(0xffffffffu, tc::mbar_wait(&empty_d[d], ((it / 2) & 1) ^ 1));
-      for (int step = s0; step < s1 && ok; ++step, ++n) {
-        const int sa = n % R::kA, sx = n % R::kX;
-        ok = __all_sync(0xffffffffu, tc::mbar_wait(&full_x[sx], (n / R::kX) & 1));
-        ok = ok && __all_sync(0xffffffffu, tc::mbar_wait(&full_a[sa], (n / R::kA) & 1));
-        if (!ok) break;
-        tc::fence_after_sync();
-        const uint32_t a_lo = tc::sdesc_lo(tc::smem_u32(as + sa * kABytes), kChunk);
-        const uint32_t b_lo = tc::sdesc_lo(tc::smem_u32(xs + sx * R::kXBytes), 16);
-        if (tc::elect_one()) {
+    constexpr uint32_t kIdesc = tc::idesc_f16(kTileRows, kTok, true, true, false, false);
+    constexpr uint32_t kHi = tc::sdesc_hi(1024) | 2u << 29;  // 128-byte swizzle
+    const uint32_t x_lo = tc::sdesc_lo(tc::smem_u32(xs), 16);
+    Place<R::kX> px;
+    Place<R::kS> pa;
+    Place<R::kD> pd;
+    int it = 0;
+    for (int tile = first; tile < a.tiles; tile += stride, ++it, pd.next()) {
+      if (it >= R::kD) tc::mbar_wait_or(&empty_d[pd.s], pd.phase ^ 1, ok);
+      for (int step = s0; step < s1; ++step, pa.next()) {
+        tc::mbar_wait_or(&full_a[pa.s], pa.phase, ok);
+        // (issued from registers that are known to be uniform: tc.cuh)
+        const uint32_t d = uniform(tmem + pd.s * kTok), w = uniform(tmem + R::kA + 64 * pa.s);
 #pragma unroll
-          for (int k = 0; k < 8; ++k)
-            tc::mma_ss_lo(tmem + d * kTok, a_lo + k * (2 * kChunk / 16),
-                          b_lo + (k / 4) * (R::kXBytes / 2 / 16) + (k % 4) * 2, kAHi, kBHi, kIdesc, step > s0 || k > 0);
-          tc::mma_commit(&empty_x[sx]);
-          tc::mma_commit(&empty_a[sa]);
-          if (step + 1 == s1) tc::mma_commit(&full_d[d]);
+        for (int half = 0; half < 2 / R::kBoxes; ++half, px.next()) {
+          tc::mbar_wait_or(&full_x[px.s], px.phase, ok);
+          const uint32_t x = uniform(x_lo + px.s * (R::kXBytes / 16));
+          tc::fence_after_sync();
+          if (tc::elect_one()) {
+#pragma unroll
+            for (int k = 0; k < 4 * R::kBoxes; ++k)
+              tc::mma_ts_lo(d, w + 8 * (4 * half + k), x + (k / 4) * (R::kBoxBytes / 16) + (k % 4) * 2, kHi, kIdesc,
+                            half > 0 || k > 0 || step > s0);
+            tc::mma_commit(&empty_x[px.s]);
+            if (half + 1 == 2 / R::kBoxes) tc::mma_commit(&empty_a[pa.s]);
+            if (half + 1 == 2 / R::kBoxes && step + 1 == s1) tc::mma_commit(&full_d[pd.s]);
+          }
+          __syncwarp();
         }
-        __syncwarp();
       }
     }
     if (tc::elect_one()) tc::mma_commit(&drained);
     __syncwarp();
     tc::mbar_wait(&drained, 0);
   } else if (warp >= 8) {  // decoding
-    const int d = warp - 8, group = d >> 1, half = d & 1, g = lane >> 2, t = lane & 3;
-    int n = 0;
-    for (int tile = first; tile < a.tiles && ok; tile += stride)
-      for (int step = s0; step < s1 && ok; ++step, ++n) {
-        const int sp = n % R::kP, sa = n % R::kA;
-        ok = __all_sync(0xffffffffu, tc::mbar_wait(&full_p[sp], (n / R::kP) & 1));
-        if (!ok) break;
-        const uint8_t* b = ps + sp * kStepBytes + group * kBlockBytes;
-        const uint4 w = *reinterpret_cast<const uint4*>(b + half * 512 + lane * 16);
-        const uint32_t sc = *reinterpret_cast<const uint32_t*>(b + kBlockCodes + lane * 4) >> (16 * half);
-        __syncwarp();
-        if (lane == 0) tc::mbar_arrive(&empty_p[sp]);
-        if (n >= R::kA) ok = __all_sync(0xffffffffu, tc::mbar_wait(&empty_a[sa], ((n / R::kA) & 1) ^ 1));
-        if (!ok) break;
-        uint8_t* dst = as + sa * kABytes + d * 128 + g * 16;
-        const uint32_t s[2] = {fp4_scale(sc, 0), fp4_scale(sc, 1)};
-        const uint32_t words[4] = {w.x, w.y, w.z, w.w};
+    const int set = (warp - 8) >> 2, q = warp & 3, r = lane & 15;  // rows 32 q .. of every kSets-th step
+    const uint8_t* const src = ps + (2 * q + (lane >> 4)) * kBlockBytes;
+    const uint32_t dst0 = tc::taddr(tmem, 32 * q, R::kA);
+    const int steps = s1 - s0;
+    const int mine = first < a.tiles ? ((a.tiles - 1 - first) / stride + 1) * steps : 0;  // of all tiles
+    int p = set % R::kP, s = set % R::kS;
+    uint32_t p_phase = 0, s_phase = set / R::kS & 1;
+    for (int n = set; n < mine; n += kSets) {
+      tc::mbar_wait_or(&full_p[p], p_phase, ok);
+      __syncwarp();
+      const uint8_t* b = src + p * kTileBytes;
+      uint4 u[4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          uint32_t r[4];
-          fp4_weights(words[j], s[j / 2], r);
-          *reinterpret_cast<uint4*>(dst + (4 * t + (j ^ t)) * kChunk) = make_uint4(r[0], r[1], r[2], r[3]);
+      for (int t = 0; t < 4; ++t) u[t] = *reinterpret_cast<const uint4*>(b + fp4_unit(r, t));
+      const uint4 sc = *reinterpret_cast<const uint4*>(b + kBlockCodes + (r & 7) * 16);
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(&empty_p[p]);
+      const uint32_t scales[4] = {sc.x, sc.y, sc.z, sc.w};
+      const uint32_t dst = dst0 + 64 * s;
+      auto decode = [&](auto t, uint32_t (&c)[16]) {
+        const uint32_t words[4] = {u[t()].x, u[t()].y, u[t()].z, u[t()].w};
+        const uint32_t two = scales[t()] >> (r & 8 ? 16 : 0);
+        const uint32_t f[2] = {fp4_scale(two, 0), fp4_scale(two, 1)};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          uint32_t v[4];
+          fp4_weights(words[i], f[i / 2], v);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) c[(i ^ t()) * 4 + j] = v[j];
         }
-        tc::fence_async_smem();
-        __syncwarp();
-        if (lane == 0) tc::mbar_arrive(&full_a[sa]);
-      }
+      };
+      // two units ahead of the wait, so that a place is not held while they are decoded
+      uint32_t c0[16], c1[16];
+      decode(Number<0>(), c0);
+      decode(Number<1>(), c1);
+      if (n >= R::kS) tc::mbar_wait_or(&empty_a[s], s_phase ^ 1, ok);
+      __syncwarp();
+      tc::fence_after_sync();
+      tc::tmem_st16(dst, c0);
+      tc::tmem_st16(dst + 16, c1);
+      decode(Number<2>(), c0);
+      tc::tmem_st16(dst + 32, c0);
+      decode(Number<3>(), c1);
+      tc::tmem_st16(dst + 48, c1);
+      tc::tmem_wait_st();
+      tc::fence_before_sync();
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(&full_a[s]);
+      if ((p += kSets) >= R::kP) p -= R::kP, p_phase ^= 1;
+      if ((s += kSets) >= R::kS) s -= R::kS, s_phase ^= 1;
+    }
   } else if (warp >= 4) {  // sums out: a lane has a row of W
     const int lane0 = 32 * (warp & 3);
     constexpr int kCols = kTok < 32 ? kTok : 32;
-    int it = 0;
-    for (int tile = first; tile < a.tiles && ok; tile += stride, ++it) {
-      const int d = it & 1, i = tile % a.row_tiles * kRows + lane0 + lane, t0 = tile / a.row_tiles * kTok;
+    Place<R::kD> at;
+    for (int tile = first; tile < a.tiles; tile += stride, at.next()) {
+      const int i = tile % a.row_tiles * kTileRows + lane0 + lane, t0 = tile / a.row_tiles * kTok;
       const bool there = i < a.l.n;
-      const float bias = there && rank == 0 ? fp4_bias(a.l, i) : 0.0f;
-      ok = __all_sync(0xffffffffu, tc::mbar_wait(&full_d[d], (it / 2) & 1));
-      if (!ok) break;
+      const float bias = there ? fp4_bias(a.l, i) : 0.0f;
+      tc::mbar_wait_or(&full_d[at.s], at.phase, ok);
+      __syncwarp();
       tc::fence_after_sync();
 #pragma unroll 1
       for (int c = 0; c < kTok; c += kCols) {
         uint32_t v[kCols];
-        if constexpr (kCols == 32) tc::tmem_ld32(tc::taddr(tmem, lane0, d * kTok + c), v);
-        else tc::tmem_ld16(tc::taddr(tmem, lane0, d * kTok + c), v);
+        if constexpr (kCols == 32) tc::tmem_ld32(tc::taddr(tmem, lane0, at.s * kTok + c), v);
+        else tc::tmem_ld16(tc::taddr(tmem, lane0, at.s * kTok + c), v);
         tc::tmem_wait_ld();
-        if (a.split > 1) {  // [row of x][row of W], in the rings, which nothing fills any more
+        if (a.split > 1) {  // [row of x][row of W], in x's ring, which nothing fills any more
 #pragma unroll
-          for (int j = 0; j < kCols; ++j) reinterpret_cast<uint32_t*>(xs)[(c + j) * kRows + lane0 + lane] = v[j];
+          for (int j = 0; j < kCols; ++j) reinterpret_cast<uint32_t*>(xs)[(c + j) * kTileRows + lane0 + lane] = v[j];
         } else if (there) {
-          const int most = a.l.T - t0 - c;
-          if (a.l.f32) {
-            float* o = static_cast<float*>(a.l.out) + (int64_t)(t0 + c) * a.l.out_stride + i;
-#pragma unroll
-            for (int j = 0; j < kCols; ++j)
-              if (j < most) o[j * a.l.out_stride] = fmaf(__uint_as_float(v[j]), a.l.alpha, bias);
-          } else {
-            __nv_bfloat16* o = static_cast<__nv_bfloat16*>(a.l.out) + (int64_t)(t0 + c) * a.l.out_stride + i;
-#pragma unroll
-            for (int j = 0; j < kCols; ++j)
-              if (j < most) o[j * a.l.out_stride] = __float2bfloat16_rn(fmaf(__uint_as_float(v[j]), a.l.alpha, bias));
-          }
+          const int most = min(kCols, a.l.T - t0 - c);
+          const int64_t at0 = (int64_t)(t0 + c) * a.l.out_stride + i;
+          if (a.l.f32) store_columns(static_cast<float*>(a.l.out) + at0, v, most, a.l, bias);
+          else store_columns(static_cast<__nv_bfloat16*>(a.l.out) + at0, v, most, a.l, bias);
         }
       }
       tc::fence_before_sync();
       __syncwarp();
-      if (lane == 0) tc::mbar_arrive(&empty_d[d]);
+      if (lane == 0) tc::mbar_arrive(&empty_d[at.s]);
     }
   }
-  if (!ok && lane == 0) report(a.l.status, CSA2_ERR_TIMEOUT);
+  if (!ok) report(a.l.status, CSA2_ERR_TIMEOUT);
   __syncwarp();
   __syncthreads();
-  if (warp == 3) tc::tmem_dealloc(tmem, 2 * kTok);
+  if (warp == 3) tc::tmem_dealloc(tmem, R::kCols);
   if (a.split > 1) {
     tc::cluster_sync();
     // this CTA's share of the tile's rows of x
-    const int t0 = first / a.row_tiles * kTok, i = first % a.row_tiles * kRows + tid % kRows;
+    const int t0 = first / a.row_tiles * kTok, i = first % a.row_tiles * kTileRows + tid % kTileRows;
     const uint32_t mine = tc::smem_u32(xs);
-    for (int t = rank + a.split * (tid / kRows); t < kTok && t0 + t < a.l.T; t += a.split * (kThreads / kRows)) {
-      const uint32_t at = mine + (t * kRows + tid % kRows) * 4;
+    for (int t = rank + a.split * (tid / kTileRows); t < kTok && t0 + t < a.l.T; t += a.split * (kThreads / kTileRows)) {
+      const uint32_t at = mine + (t * kTileRows + tid % kTileRows) * 4;
       float sum = 0.0f;
       for (int r = 0; r < a.split; ++r) sum += tc::ld_dsmem(tc::map_rank(at, r));
       if (i < a.l.n) fp4_store(a.l, t0 + t, i, sum, fp4_bias(a.l, i));
@@ -261,7 +323,6 @@ Encode encoder() {
 template <int kTok>
 cudaError_t launch_of(const Fp4Linear& l, cudaStream_t stream) {
   using R = Rings<kTok>;
-  static_assert(R::kSmem <= kSmemMost && R::kX * R::kXBytes + R::kA * kABytes >= kTok * kRows * 4, "");
   auto kern = fp4_tiles_kernel<kTok>;
   static std::atomic<bool> done[64];
   const cudaError_t e = allow_smem(kern, R::kSmem, done);
@@ -275,7 +336,7 @@ cudaError_t launch_of(const Fp4Linear& l, cudaStream_t stream) {
              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
     return cudaErrorInvalidValue;
-  TileArgs a{l, (l.n + kRows - 1) / kRows, 0, 1};
+  TileArgs a{l, fp4_row_tiles(l.n), 0, 1};
   const int64_t tiles = (int64_t)a.row_tiles * ((l.T + kTok - 1) / kTok);
   if (tiles > INT32_MAX / 8) return cudaErrorInvalidValue;
   a.tiles = (int)tiles;

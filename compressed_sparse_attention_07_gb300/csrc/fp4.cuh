@@ -10,17 +10,17 @@
 // chunk i ^ t of the unit's 32 in bf16, so that lanes of neighbouring t read different
 // banks of rows of x too.  The two scales of a row's unit stand at fp4_unit_scales(r, t),
 // that of words 0 and 1 first.
-// Within a word the even channels of the eight stand in the low
-// half, the odd ones in the high half, their codes s e1 e0 m at bits
-//   15 8 7 6 | 12 5 4 3 | 9 2 1 0 | 14 13 11 10
-// of the half, so that one shift and one mask (four more operations for the last)
-// bring two neighbouring channels to s at bit 15 and e1 e0 m at bits 8..6 of the two
-// bf16 of a register.  Read as bf16 that is code x 2^-126 (subnormal where e1 e0 = 0),
-// exactly; times scale x 2^118 it is the weight x 2^-8, exactly, as a code has 2
-// significant bits and a scale 4.  (The conversion to f16, one instruction a pair,
-// needs a third of the instructions, but x would have to become f16 too, which loses
-// bf16's range and costs as much again for few rows: 8 codes 11 + 4 operations in
-// 3.1 cycles a warp and SM, at HBM's rate there are 6.)
+// Nibble p of a word is the code of the chunk's channel 2 p, nibble 4 + p of channel
+// 2 p + 1, so that a mask and two shifts bring two neighbouring channels to the halves of a
+// register (fp4_bf16), and its bytes hold channels (0, 2), (4, 6), (1, 3), (5, 7) for the
+// conversion of pairs to f16 (fp4_f16).
+//
+// To bf16, for x as it comes: a code's sign at bit 15 and the rest at bits 8..6 of a bf16
+// is code x 2^-126 (subnormal where the exponent is 0), exactly; times scale x 2^118 it is
+// the weight x 2^-8, exactly, as a code has 2 significant bits and a scale 4.  Eight
+// codes take 15 + 4 instructions and 4.4 cycles of a warp and SM.  To f16, which the
+// kernel for few rows brings x to: 4 + 4 instructions, 1.4 cycles; at HBM's rate there are
+// 6, of which the products of 8 rows of x take 2.
 #pragma once
 
 #include "kv.cuh"
@@ -28,7 +28,7 @@
 namespace csa2 {
 
 constexpr int kBlockRows = 16, kBlockK = 128, kBlockBytes = 1152, kBlockCodes = 1024;
-constexpr float kFp4Unit = 256.0f;  // what the decoded weights are short of
+constexpr float kFp4Unit = 256.0f;  // what fp4_bf16's weights are short of
 
 constexpr int kTileRows = 128, kTileBlocks = kTileRows / kBlockRows, kTileBytes = kTileBlocks * kBlockBytes;
 
@@ -48,7 +48,7 @@ struct Fp4Linear {
   void* out;
   int64_t out_stride;
   int f32;      // out's type
-  float alpha;  // times kFp4Unit
+  float alpha;
   int32_t* status;
 };
 
@@ -64,18 +64,22 @@ __device__ __forceinline__ uint32_t fp4_scale(uint32_t w, int i) {
   return mul_bf16x2(mul_bf16x2(b, 0x7F007F00u), 0x77007700u);  // 2^127, 2^111
 }
 // The eight weights of a word, times 2^-8: pair p holds channels 2p and 2p + 1.
-__device__ __forceinline__ void fp4_weights(uint32_t w, uint32_t scale, uint32_t (&r)[4]) {
-  constexpr uint32_t kMask = 0x81C081C0u;
-  r[0] = mul_bf16x2(w & kMask, scale);
-  r[1] = mul_bf16x2((w << 3) & kMask, scale);
-  r[2] = mul_bf16x2((w << 6) & kMask, scale);
-  uint32_t u = ((w << 1) & 0x80008000u) | ((w >> 4) & 0x7FFF7FFFu);
-  u = ((w >> 5) & 0x01000100u) | (u & 0xFEFFFEFFu);
-  r[3] = mul_bf16x2(u & kMask, scale);
+__device__ __forceinline__ void fp4_bf16(uint32_t w, uint32_t scale, uint32_t (&r)[4]) {
+  constexpr uint32_t kRest = 0x01C001C0u, kSign = 0x80008000u;
+  r[0] = mul_bf16x2(((w << 6) & kRest) | ((w << 12) & kSign), scale);
+  r[1] = mul_bf16x2(((w << 2) & kRest) | ((w << 8) & kSign), scale);
+  r[2] = mul_bf16x2(((w >> 2) & kRest) | ((w << 4) & kSign), scale);
+  r[3] = mul_bf16x2(((w >> 6) & kRest) | (w & kSign), scale);
 }
-// sum + bias, stored in out's type.
-__device__ __forceinline__ void fp4_store(const Fp4Linear& a, int t, int i, float sum, float bias) {
-  const float y = fmaf(sum, a.alpha, bias);
+// The eight weights of a word in f16, channels (0, 2), (4, 6), (1, 3), (5, 7); scale a pair.
+__device__ __forceinline__ void fp4_f16(uint32_t w, uint32_t scale, uint32_t (&r)[4]) {
+  codes8(w, r);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) r[i] = mul2(r[i], scale);
+}
+// sum x alpha + bias, stored in out's type.
+__device__ __forceinline__ void fp4_store(const Fp4Linear& a, int t, int i, float sum, float alpha, float bias) {
+  const float y = fmaf(sum, alpha, bias);
   if (a.f32) static_cast<float*>(a.out)[t * a.out_stride + i] = y;
   else static_cast<__nv_bfloat16*>(a.out)[t * a.out_stride + i] = __float2bfloat16_rn(y);
 }
@@ -88,7 +92,7 @@ cudaError_t launch_fp4_encode(int n, int k, const uint16_t* w, int64_t stride, f
 cudaError_t launch_fp4_pack(int n, int k, const uint8_t* codes, const uint8_t* scales, uint8_t* packed,
                             int32_t* status, cudaStream_t stream);
 // Up to kFp4FewRows rows whose x fits shared memory (fp4_rows_ok), and any.
-constexpr int kFp4FewRows = 8;
+constexpr int kFp4FewRows = 16;
 bool fp4_rows_ok(const Fp4Linear& a);
 cudaError_t launch_fp4_rows(const Fp4Linear& a, cudaStream_t stream);
 cudaError_t launch_fp4_tiles(const Fp4Linear& a, cudaStream_t stream);

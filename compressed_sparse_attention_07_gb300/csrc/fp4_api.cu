@@ -47,7 +47,7 @@ int32_t csa2_fp4_linear(const csa2_fp4_weights* w, int32_t T, const uint16_t* x,
       !aligned(out, out_dtype == CSA2_F32 ? 4 : 2) || out_stride < w->n || !aligned(status, 4))
     return CSA2_ERR_INVALID_ARG;
   Fp4Linear a{static_cast<const uint8_t*>(w->data), w->n, w->k, fp4_k_blocks(w->k), T, x, x_stride, bias, out, out_stride,
-              out_dtype == CSA2_F32 ? 1 : 0, w->alpha * kFp4Unit, status};
+              out_dtype == CSA2_F32 ? 1 : 0, w->alpha, status};
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   return cuda_status(fp4_rows_ok(a) ? launch_fp4_rows(a, s) : launch_fp4_tiles(a, s));
 }

@@ -12,15 +12,7 @@ constexpr int kThreads = 256;
 __device__ __forceinline__ uint32_t arrange(uint32_t codes) {
   uint32_t w = 0;
 #pragma unroll
-  for (int c = 0; c < 8; ++c) {
-    const uint32_t n = (codes >> (4 * c)) & 15u, s = n >> 3, m = n & 7u;
-    const int p = c / 2;
-    const uint32_t h = p == 0   ? s << 15 | m << 6
-                       : p == 1 ? s << 12 | m << 3
-                       : p == 2 ? s << 9 | m
-                                : s << 14 | (m >> 2) << 13 | (m & 3u) << 10;
-    w |= h << (c & 1 ? 16 : 0);
-  }
+  for (int c = 0; c < 8; ++c) w |= ((codes >> (4 * c)) & 15u) << (4 * (c / 2) + 16 * (c & 1));
   return w;
 }
 

@@ -2,16 +2,19 @@
 //
 // y = x W^T reads every weight once, 9/16 of a byte each, for 2 operations a row of x:
 // bound by the weights' bytes.  The products run transposed, D[16 rows of W][8 rows of
-// x], so that up to 8 rows of x fill a 16x8x16 instruction; the weights are decoded in
-// registers, as the left operand, with about 18 instructions for 8 of a lane.  tcgen05
-// has nothing to add here: its 128 rows of W would want the decoded weights in shared
-// memory, for 8 columns.
+// x], so that few rows of x fill a 16x8x16 instruction; the weights are decoded to f16 in
+// registers, as the left operand.  (To bf16, which x would not have to be brought
+// from, decoding bound the kernel: 8 rows of 4096 -> 128001 took 65 us.)  tcgen05
+// has nothing to add here: its 128 rows of W would want the decoded weights in tensor
+// memory, for 8 or 16 columns.
 // A CTA, one an SM, takes an equal run of tiles (16 or 32 rows of W over all of k), and
 // its 16 warps take equal runs of the tiles' blocks laid end to end, whatever tile
 // they are of: a warp streams its blocks through a ring of bulk copies of its own and
 // stores the sums of whole tiles itself; pieces of tiles that several warps share
 // are joined in their order through shared memory, so sums do not depend on timing.
-// x stands in shared memory for the whole call.
+// x stands in shared memory for the whole call, as f16 relative to a power of two of its
+// row that brings the row's largest to [2^14, 2^15): exact down to 2^-29 of the largest,
+// and off by 2^-40 of it at most below.
 #include <algorithm>
 
 #include "fp4.cuh"
@@ -21,7 +24,7 @@ namespace csa2 {
 namespace {
 
 constexpr int kWarps = 16, kThreads = 32 * kWarps, kMostSlots = 8;
-constexpr int kSmemMost = 227 * 1024 - 2048;  // beside the barriers
+constexpr int kSmemMost = 227 * 1024 - 3072;  // beside the barriers
 // x rows stand an odd multiple of 64 bytes apart (two rows' chunks in different banks).
 __host__ __device__ __forceinline__ int x_pitch(int k_blocks) { return k_blocks * 256 + 64; }
 
@@ -29,10 +32,10 @@ struct Shape {
   int slots;  // of a warp's ring
   int smem;
 };
-// (16 lg) rows a tile; slots 0: does not fit
-Shape shape_of(const Fp4Linear& a, int lg) {
-  const int64_t fixed = (int64_t)a.T * x_pitch(a.k_blocks) + 2 * kWarps * lg * 512;
-  const int64_t ring = (int64_t)kWarps * lg * kBlockBytes;
+// groups x 16 rows of W a tile; slots 0: does not fit
+Shape shape_of(const Fp4Linear& a, int groups) {
+  const int64_t fixed = (int64_t)a.T * x_pitch(a.k_blocks) + (int64_t)kWarps * groups * 512 * ((a.T + 7) / 8);
+  const int64_t ring = (int64_t)kWarps * groups * kBlockBytes;
   const int64_t n = std::min<int64_t>(kMostSlots, (kSmemMost - fixed) / ring);
   if (fixed > kSmemMost || n < 2) return {0, 0};
   return {(int)n, (int)(fixed + n * ring)};
@@ -40,85 +43,138 @@ Shape shape_of(const Fp4Linear& a, int lg) {
 
 __device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
   asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// A lane's sums of 16 rows of W: rows g and g + 8, rows 2 t and 2 t + 1 of x.
-__device__ __forceinline__ void store_group(const Fp4Linear& a, int row0, int lane, float4 d) {
-  const int g = lane >> 2, t = 2 * (lane & 3);
+// A lane's sums of 16 rows of W: rows g and g + 8, rows t and t + 1 of x; what of them is there.
+__device__ __forceinline__ void store_group(const Fp4Linear& a, int row0, int t, const float* unscale, float4 d) {
   if (t >= a.T) return;
   const float v[4] = {d.x, d.y, d.z, d.w};
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
-    const int i = row0 + g + 8 * h;
+    const int i = row0 + 8 * h;
     if (i >= a.n) return;
     const float b = fp4_bias(a, i);
-    fp4_store(a, t, i, v[2 * h], b);
-    if (t + 1 < a.T) fp4_store(a, t + 1, i, v[2 * h + 1], b);
+    fp4_store(a, t, i, v[2 * h] * unscale[t], a.alpha, b);
+    if (t + 1 < a.T) fp4_store(a, t + 1, i, v[2 * h + 1] * unscale[t + 1], a.alpha, b);
   }
 }
 
-template <int kGroups>
+// x from bf16 to f16, in place, in the order of channels that fp4_f16 has, all threads.
+__device__ __forceinline__ void convert_x(const Fp4Linear& a, uint8_t* xs, int pitch, uint32_t* most, float* unscale) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, chunks = a.k / 8;
+  // a power of two of warps for each row
+  int share = 1;
+  while (2 * share * a.T <= kWarps) share *= 2;
+  for (int r = warp / share; r < a.T; r += kWarps / share) {
+    uint32_t m = 0;  // largest finite magnitude, as bf16 bits
+    for (int c = warp % share * 32 + lane; c < chunks; c += share * 32) {
+      const uint4 v = *reinterpret_cast<const uint4*>(xs + r * pitch + c * 16);
+      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t lo = w[i] & 0x7FFFu, hi = w[i] >> 16 & 0x7FFFu;
+        m = max(m, max(lo < 0x7F80u ? lo : 0u, hi < 0x7F80u ? hi : 0u));
+      }
+    }
+    m = __reduce_max_sync(0xffffffffu, m);
+    if (lane == 0) atomicMax(&most[r], m);
+  }
+  __syncthreads();
+  for (int r = warp / share; r < a.T; r += kWarps / share) {
+    // 2^e brings the largest, of exponent field f, to [2^14, 2^15)
+    const int f = (int)(most[r] >> 7);
+    const int e = most[r] ? min(14 + 127 - f, 126) : 0;
+    const float scale = __int_as_float((e + 127) << 23);
+    if (warp % share == 0 && lane == 0) unscale[r] = __int_as_float((127 - e) << 23);
+    for (int c = warp % share * 32 + lane; c < chunks; c += share * 32) {
+      uint4* p = reinterpret_cast<uint4*>(xs + r * pitch + c * 16);
+      const uint4 v = *p;
+      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+      float lo[4], hi[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        lo[i] = __uint_as_float(w[i] << 16) * scale;
+        hi[i] = __uint_as_float(w[i] & 0xFFFF0000u) * scale;
+      }
+      *p = make_uint4(f16x2(lo[0], lo[1]), f16x2(lo[2], lo[3]), f16x2(hi[0], hi[1]), f16x2(hi[2], hi[3]));
+    }
+  }
+  __syncthreads();
+}
+
+// kGroups x 16 rows of W a tile, up to kNt x 8 rows of x.
+template <int kGroups, int kNt>
 __global__ void __launch_bounds__(kThreads, 1) fp4_rows_kernel(const Fp4Linear a, int tiles, int slots) {
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ __align__(8) uint64_t full[kWarps][kMostSlots];
+  __shared__ __align__(8) uint64_t full_x;
   __shared__ int piece_tile[2 * kWarps];
+  __shared__ uint32_t most[kFp4FewRows];
+  __shared__ float unscale[kFp4FewRows];
+  constexpr int kUnit = kGroups * kBlockBytes, kPiece = kGroups * kNt * 32;  // bytes; float4
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
   const int pitch = x_pitch(a.k_blocks);
-  uint8_t* ring = smem + warp * slots * (kGroups * kBlockBytes);
-  float4* pieces = reinterpret_cast<float4*>(smem + kWarps * slots * (kGroups * kBlockBytes));
-  uint8_t* xs = reinterpret_cast<uint8_t*>(pieces + 2 * kWarps * kGroups * 32);
+  uint8_t* ring = smem + warp * slots * kUnit;
+  float4* firsts = reinterpret_cast<float4*>(smem + kWarps * slots * kUnit);  // a warp's first piece
+  uint8_t* xs = reinterpret_cast<uint8_t*>(firsts + kWarps * kPiece);
 
   const int tile0 = (int)((int64_t)blockIdx.x * tiles / gridDim.x);
   const int units = ((int)((int64_t)(blockIdx.x + 1) * tiles / gridDim.x) - tile0) * a.k_blocks;
   const int u0 = (int)((int64_t)warp * units / kWarps), u1 = (int)((int64_t)(warp + 1) * units / kWarps);
   // the next unit to fetch: its blocks, its place in k and in the ring (no division in
-  // the loop: with u / k_blocks and u % slots in it a unit of 32 rows took 512
-  // instructions, and takes 340)
-  const int kb0 = units ? u0 % a.k_blocks : 0, first = units ? u0 / a.k_blocks : 0;
+  // the loop: with u / k_blocks and u % slots in it a unit took 170 instructions more)
+  const int kb0 = u0 % a.k_blocks, first = u0 / a.k_blocks;
   constexpr int kParts = kTileBlocks / kGroups;  // tiles of this kernel in 128 rows
-  const int64_t far = (int64_t)(a.k_blocks - 1) * kTileBytes;
   int src_tile = tile0 + first, src_kb = kb0, src_slot = 0;
-  const uint8_t* src = a.w + ((int64_t)(src_tile / kParts) * a.k_blocks + kb0) * kTileBytes +
-                       src_tile % kParts * (kGroups * kBlockBytes);
+  const uint8_t* src = a.w + ((int64_t)(src_tile / kParts) * a.k_blocks + kb0) * kTileBytes + src_tile % kParts * kUnit;
   auto fetch = [&]() {
-    tc::mbar_arrive_expect_tx(&full[warp][src_slot], kGroups * kBlockBytes);
-    tc::bulk_g2s(ring + src_slot * (kGroups * kBlockBytes), src, kGroups * kBlockBytes, &full[warp][src_slot]);
+    tc::mbar_arrive_expect_tx(&full[warp][src_slot], kUnit);
+    tc::bulk_g2s(ring + src_slot * kUnit, src, kUnit, &full[warp][src_slot]);
     src += kTileBytes;
     if (++src_kb == a.k_blocks) {  // the next tile's first block: beside this one's, or at the next 128 rows
       src_kb = 0, ++src_tile;
-      src += kGroups * kBlockBytes - (src_tile % kParts ? far + kTileBytes : kTileBytes);
+      src += kUnit - (src_tile % kParts ? (int64_t)a.k_blocks * kTileBytes : kTileBytes);
     }
     if (++src_slot == slots) src_slot = 0;
   };
   if (lane == 0) {
-    if (u0 < u1) tc::bulk_prefetch_l2(src, kGroups * kBlockBytes);
+    if (u0 < u1) tc::bulk_prefetch_l2(src, kUnit);
     for (int s = 0; s < slots; ++s) tc::mbar_init(&full[warp][s], 1);
+    if (warp == 1) tc::mbar_init(&full_x, 1);
     tc::fence_mbar_init();
     piece_tile[2 * warp] = piece_tile[2 * warp + 1] = -1;
+    most[warp] = 0;
   }
   __syncwarp();
   griddep_wait();  // every input may be the previous kernel's output
-  if (lane == 0)
+  if (lane == 0) {
+    if (warp == 1) {
+      tc::mbar_arrive_expect_tx(&full_x, a.T * a.k * 2);
+      for (int r = 0; r < a.T; ++r) tc::bulk_g2s(xs + r * pitch, a.x + r * a.x_stride, a.k * 2, &full_x);
+    }
     for (int u = u0; u < min(u1, u0 + slots); ++u) fetch();
-  {  // x, zeros from channel k on
-    const int chunks = a.k_blocks * 16;
-    for (int r = 0; r < a.T; ++r)
-      for (int c = tid; c < chunks; c += kThreads) {
-        uint4 v = make_uint4(0, 0, 0, 0);
-        if (8 * c < a.k) v = __ldg(reinterpret_cast<const uint4*>(a.x + r * a.x_stride) + c);
-        *reinterpret_cast<uint4*>(xs + r * pitch + c * 16) = v;
-      }
   }
+  // zeros from channel k on
+  const int pad = a.k_blocks * 16 - a.k / 8;  // 16-byte chunks
+  for (int i = tid; i < a.T * pad; i += kThreads)
+    *reinterpret_cast<uint4*>(xs + i / pad * pitch + a.k * 2 + i % pad * 16) = make_uint4(0, 0, 0, 0);
   __syncthreads();
-  const uint8_t* xr = xs + min(g, a.T - 1) * pitch + t * 64;  // (columns from T on are dropped)
+  bool ok = true;
+  tc::mbar_wait_or(&full_x, 0, ok);
+  __syncwarp();
+  convert_x(a, xs, pitch, most, unscale);
+  // this lane's rows of x (columns from T on are dropped), its chunk of word 0
+  const uint8_t* xr[kNt];
+#pragma unroll
+  for (int m = 0; m < kNt; ++m) xr[m] = xs + min(8 * m + g, a.T - 1) * pitch + t * 64;
 
-  float acc[kGroups][4] = {};
-  int kb = kb0, tile = first, piece = 0, s = 0;
+  float acc[kGroups][kNt][4] = {};
+  int kb = kb0, tile = first, s = 0;
   uint32_t phase = 0;
-  bool whole = kb == 0, ok = true;
+  bool whole = kb == 0;
   for (int u = u0; u < u1; ++u) {
     tc::mbar_wait_or(&full[warp][s], phase, ok);  // (sums of what stands there, and a status, where it gives up)
     __syncwarp();
@@ -126,7 +182,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_rows_kernel(const Fp4Linear a
     uint32_t sc[kGroups];
 #pragma unroll
     for (int i = 0; i < kGroups; ++i) {
-      const uint8_t* b = ring + (s * kGroups + i) * kBlockBytes;
+      const uint8_t* b = ring + s * kUnit + i * kBlockBytes;
       lo[i] = *reinterpret_cast<const uint4*>(b + fp4_unit(g, t));
       hi[i] = *reinterpret_cast<const uint4*>(b + fp4_unit(g + 8, t));
       sc[i] = *reinterpret_cast<const uint32_t*>(b + kBlockCodes + 4 * lane);
@@ -134,33 +190,47 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_rows_kernel(const Fp4Linear a
     __syncwarp();
     if (lane == 0 && u + slots < u1) fetch();
     if (++s == slots) s = 0, phase ^= 1;
-    const uint8_t* xk = xr + kb * 256;
+    uint32_t f[kGroups][4];  // scales of words 0, 1 and 2, 3 of row g, of row g + 8
+#pragma unroll
+    for (int i = 0; i < kGroups; ++i) {
+      const uint32_t p = scales2(sc[i] & 0xFFFFu), q = scales2(sc[i] >> 16);
+      f[i][0] = __byte_perm(p, 0, 0x1010), f[i][1] = __byte_perm(p, 0, 0x3232);
+      f[i][2] = __byte_perm(q, 0, 0x1010), f[i][3] = __byte_perm(q, 0, 0x3232);
+    }
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const uint4 x = *reinterpret_cast<const uint4*>(xk + (j ^ t) * 16);
+      uint4 x[kNt];
+#pragma unroll
+      for (int m = 0; m < kNt; ++m) x[m] = *reinterpret_cast<const uint4*>(xr[m] + kb * 256 + (j ^ t) * 16);
 #pragma unroll
       for (int i = 0; i < kGroups; ++i) {
         const uint32_t wl = j == 0 ? lo[i].x : j == 1 ? lo[i].y : j == 2 ? lo[i].z : lo[i].w;
         const uint32_t wh = j == 0 ? hi[i].x : j == 1 ? hi[i].y : j == 2 ? hi[i].z : hi[i].w;
         uint32_t l[4], h[4];
-        fp4_weights(wl, fp4_scale(sc[i], j / 2), l);
-        fp4_weights(wh, fp4_scale(sc[i], 2 + j / 2), h);
-        mma(acc[i], l[0], h[0], l[1], h[1], x.x, x.y);
-        mma(acc[i], l[2], h[2], l[3], h[3], x.z, x.w);
+        fp4_f16(wl, f[i][j / 2], l);
+        fp4_f16(wh, f[i][2 + j / 2], h);
+#pragma unroll
+        for (int m = 0; m < kNt; ++m) {
+          mma(acc[i][m], l[0], h[0], l[1], h[1], x[m].x, x[m].y);
+          mma(acc[i][m], l[2], h[2], l[3], h[3], x[m].z, x[m].w);
+        }
       }
     }
     if (++kb == a.k_blocks || u + 1 == u1) {  // the end of the tile, or of the warp's part of it
+      const bool all = whole && kb == a.k_blocks, end = u + 1 == u1;
+      // the warp's last piece goes to its ring, which is empty by then
+      float4* piece = end ? reinterpret_cast<float4*>(ring) : firsts + warp * kPiece;
 #pragma unroll
-      for (int i = 0; i < kGroups; ++i) {
-        const float4 d = make_float4(acc[i][0], acc[i][1], acc[i][2], acc[i][3]);
-        if (whole && kb == a.k_blocks) store_group(a, ((tile0 + tile) * kGroups + i) * kBlockRows, lane, d);
-        else pieces[((2 * warp + piece) * kGroups + i) * 32 + lane] = d;
-        acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.0f;
-      }
-      if (!(whole && kb == a.k_blocks)) {
-        if (lane == 0) piece_tile[2 * warp + piece] = tile;
-        ++piece;
-      }
+      for (int i = 0; i < kGroups; ++i)
+#pragma unroll
+        for (int m = 0; m < kNt; ++m) {
+          float(&d)[4] = acc[i][m];
+          const float4 v = make_float4(d[0], d[1], d[2], d[3]);
+          if (all) store_group(a, ((tile0 + tile) * kGroups + i) * kBlockRows + g, 8 * m + 2 * t, unscale, v);
+          else piece[(i * kNt + m) * 32 + lane] = v;
+          d[0] = d[1] = d[2] = d[3] = 0.0f;
+        }
+      if (!all && lane == 0) piece_tile[2 * warp + (end ? 1 : 0)] = tile;
       if (kb == a.k_blocks) kb = 0, ++tile;
       whole = true;
     }
@@ -169,32 +239,40 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_rows_kernel(const Fp4Linear a
     report(a.status, CSA2_ERR_TIMEOUT);
     // nothing may land in shared memory after the CTA has left
     for (int u = max(u0, u1 - slots); u < u1; ++u) tc::mbar_wait(&full[warp][(u - u0) % slots], ((u - u0) / slots) & 1);
+    tc::mbar_wait(&full_x, 0);
   }
   __syncthreads();
-  // a shared tile's pieces stand in the order of its channels, two places a warp: the
-  // warp with the first of them joins them
-  for (int p = warp; p < 2 * kWarps; p += kWarps) {
-    const int at = piece_tile[p];
-    if (at < 0) continue;
-    bool first = true;
-    for (int q = 0; q < p; ++q) first = first && piece_tile[q] != at;
-    if (!first) continue;
+  // a shared tile's pieces stand in the order of its channels, two places a warp, a place
+  // a lane here: the warp with the first of them joins them
+  const int of_lane = piece_tile[lane];
 #pragma unroll
-    for (int i = 0; i < kGroups; ++i) {
-      float4 d = pieces[(p * kGroups + i) * 32 + lane];
-      for (int q = p + 1; q < 2 * kWarps; ++q) {
-        if (piece_tile[q] != at) continue;
-        const float4 e = pieces[(q * kGroups + i) * 32 + lane];
-        d.x += e.x, d.y += e.y, d.z += e.z, d.w += e.w;
+  for (int p = 0; p < 2; ++p) {
+    const int at = piece_tile[2 * warp + p];
+    uint32_t same = __ballot_sync(0xffffffffu, of_lane == at);
+    if (at < 0 || __ffs(same) - 1 != 2 * warp + p) continue;
+    float4 sum[kGroups * kNt];
+#pragma unroll
+    for (int i = 0; i < kGroups * kNt; ++i) sum[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    for (; same; same &= same - 1) {
+      const int q = __ffs(same) - 1;
+      const float4* piece = q & 1 ? reinterpret_cast<const float4*>(smem + (q >> 1) * slots * kUnit) : firsts + (q >> 1) * kPiece;
+#pragma unroll
+      for (int i = 0; i < kGroups * kNt; ++i) {
+        const float4 e = piece[i * 32 + lane];
+        sum[i].x += e.x, sum[i].y += e.y, sum[i].z += e.z, sum[i].w += e.w;
       }
-      store_group(a, ((tile0 + at) * kGroups + i) * kBlockRows, lane, d);
     }
+#pragma unroll
+    for (int i = 0; i < kGroups; ++i)
+#pragma unroll
+      for (int m = 0; m < kNt; ++m)
+        store_group(a, ((tile0 + at) * kGroups + i) * kBlockRows + g, 8 * m + 2 * t, unscale, sum[i * kNt + m]);
   }
 }
 
-template <int kGroups>
+template <int kGroups, int kNt>
 cudaError_t launch_of(const Fp4Linear& a, const Shape& s, cudaStream_t stream) {
-  auto kern = fp4_rows_kernel<kGroups>;
+  auto kern = fp4_rows_kernel<kGroups, kNt>;
   static std::atomic<bool> done[64];
   const cudaError_t e = allow_smem(kern, kSmemMost, done);
   if (e != cudaSuccess) return e;
@@ -210,8 +288,9 @@ cudaError_t launch_fp4_rows(const Fp4Linear& a, cudaStream_t stream) {
   // 32 rows a tile, which halve x's way through shared memory, where the SMs have
   // several each and the rings stay deep
   const Shape two = shape_of(a, 2);
-  if (a.n >= 32 * 8 * num_sms() && two.slots >= 3) return launch_of<2>(a, two, stream);
-  return launch_of<1>(a, shape_of(a, 1), stream);
+  const bool wide = a.n >= 32 * 8 * num_sms() && two.slots >= 3;
+  if (a.T <= 8) return wide ? launch_of<2, 1>(a, two, stream) : launch_of<1, 1>(a, shape_of(a, 1), stream);
+  return wide ? launch_of<2, 2>(a, two, stream) : launch_of<1, 2>(a, shape_of(a, 1), stream);
 }
 
 }  // namespace csa2

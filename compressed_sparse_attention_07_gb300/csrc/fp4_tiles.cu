@@ -227,7 +227,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_tiles_kernel(const __grid_con
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           uint32_t v[4];
-          fp4_weights(words[i], f[i / 2], v);
+          fp4_bf16(words[i], f[i / 2], v);
 #pragma unroll
           for (int j = 0; j < 4; ++j) c[(i ^ t()) * 4 + j] = v[j];
         }
@@ -297,7 +297,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_tiles_kernel(const __grid_con
       const uint32_t at = mine + (t * kTileRows + tid % kTileRows) * 4;
       float sum = 0.0f;
       for (int r = 0; r < a.split; ++r) sum += tc::ld_dsmem(tc::map_rank(at, r));
-      if (i < a.l.n) fp4_store(a.l, t0 + t, i, sum, fp4_bias(a.l, i));
+      if (i < a.l.n) fp4_store(a.l, t0 + t, i, sum, a.l.alpha, fp4_bias(a.l, i));
     }
     tc::cluster_sync();
   }
@@ -337,6 +337,7 @@ cudaError_t launch_of(const Fp4Linear& l, cudaStream_t stream) {
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
     return cudaErrorInvalidValue;
   TileArgs a{l, fp4_row_tiles(l.n), 0, 1};
+  a.l.alpha *= kFp4Unit;
   const int64_t tiles = (int64_t)a.row_tiles * ((l.T + kTok - 1) / kTok);
   if (tiles > INT32_MAX / 8) return cudaErrorInvalidValue;
   a.tiles = (int)tiles;

@@ -4,11 +4,15 @@
 // are among the best `take` logits of each beam; their scores need the beam's log-sum-
 // exp, a shift.  So one pass over the logits, which bounds the call (HBM for a serving
 // batch, latency for one user's beams):
-//  - beam_part_kernel: a CTA holds a part of up to 16384 logits of a row in registers and
-//    forms the part's maximum m, the sum of exp(x - m) (32 in fp32, these in fp64), and its best `take` logits in
-//    order: the `take`-th largest of 64 groups' maxima is a lower bound of the take-th
-//    largest logit, the few logits that reach it go to a list, and the list is ranked by
-//    counting.  Where ties make the list too long, the best are found one by one.
+//  - beam_part_kernel: a warp streams a part of a row through registers, 2048 bf16 or 1024
+//    fp32 logits (a window) at a time, so nothing waits on another warp (with 16384
+//    logits a CTA and five barriers, 512 beams of 128001 took 84 us).  It keeps the
+//    largest so far, the sum of exp(x - it), and a list of the logits that may be among the
+//    best: of the lanes' maxima so far the `take`-th largest, to 16 bits, is a lower
+//    bound of the take-th largest logit; the few 16-byte vectors of the window whose
+//    maximum reaches it are read again, and the logits that do are listed.  In the end
+//    those that reach the last bound are ranked by counting.  Where ties make the list
+//    too long, the best are found one by one.
 //  - beam_join_kernel: a CTA a group adds the parts' sums in fp64, forms the candidates'
 //    scores in fp64 and ranks them in the same way, by (score, beam, token).
 #include <algorithm>
@@ -18,16 +22,19 @@
 namespace csa2 {
 namespace {
 
-constexpr int kThreads = 512, kWarps = kThreads / 32, kList = 1024;
-constexpr int kPart = 16384, kPer = kPart / kThreads;  // logits of a CTA, of a thread
-constexpr int kMost = 64;                               // take, beams
+constexpr int kMost = 64;  // take, beams
+// part: warps of a CTA, 16-byte vectors of a lane in a window, windows of a warp, list of a warp
+constexpr int kPartWarps = 4, kN = 8, kMostWindows = 8, kPartList = 512;
+// join
+constexpr int kThreads = 512, kWarps = kThreads / 32, kList = 2048;
 
 struct PartSum {
   double sum;  // of exp(x - most)
   float most, pad;
 };
 struct BeamArgs {
-  int groups, beams, vocab, take, parts;
+  int groups, beams, vocab, take, parts, part;  // part: logits of one
+  Divisor by_parts;
   const void* logits;
   int64_t stride;
   const float* cum;
@@ -49,6 +56,7 @@ __device__ __forceinline__ uint32_t key_of(float x) {
 }
 __device__ __forceinline__ float of_key(uint32_t k) { return __uint_as_float(k & 0x80000000u ? k & 0x7FFFFFFFu : ~k); }
 constexpr uint32_t kNone = 0x007FFFFFu;  // of -inf
+constexpr uint32_t kDone = 0xFFFFFFFFu;  // of no number: what a beam that is done proposes
 
 __device__ __forceinline__ float clean(float x, bool& bad) {
   if (!(x < INFINITY)) {
@@ -57,134 +65,259 @@ __device__ __forceinline__ float clean(float x, bool& bad) {
   }
   return x;
 }
+// The larger, NaN if one is.
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ uint32_t max_nan2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ float low(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float high(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
+
+// A lane's logits of a window as they come, vectors of 16 bytes, 32 apart.
+template <bool kBf16>
+struct Held {
+  static constexpr int kVec = kBf16 ? 8 : 4;
+  uint4 v[kN];
+  static __device__ __forceinline__ float get(const uint4& u, int i) {
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+    if constexpr (kBf16) return i & 1 ? high(w[i / 2]) : low(w[i / 2]);
+    else return __uint_as_float(w[i]);
+  }
+  // what is no number, or +inf, as -inf
+  static __device__ __forceinline__ uint32_t clean_word(uint32_t w) {
+    if constexpr (kBf16) {
+      if (!(low(w) < INFINITY)) w = (w & 0xFFFF0000u) | 0xFF80u;
+      if (!(high(w) < INFINITY)) w = (w & 0xFFFFu) | 0xFF800000u;
+      return w;
+    } else {
+      return __uint_as_float(w) < INFINITY ? w : 0xFF800000u;
+    }
+  }
+  static __device__ __forceinline__ void clean_vector(uint4& u) {
+    u = make_uint4(clean_word(u.x), clean_word(u.y), clean_word(u.z), clean_word(u.w));
+  }
+  // the largest of vector j, NaN if one is
+  __device__ __forceinline__ float most(int j) const {
+    const uint4 u = v[j];
+    if constexpr (kBf16) {
+      const uint32_t m = max_nan2(max_nan2(u.x, u.y), max_nan2(u.z, u.w));
+      return max_nan(low(m), high(m));
+    } else {
+      return max_nan(max_nan(get(u, 0), get(u, 1)), max_nan(get(u, 2), get(u, 3)));
+    }
+  }
+};
 
 template <bool kBf16>
-__global__ void __launch_bounds__(kThreads) beam_part_kernel(const BeamArgs a) {
-  __shared__ double sums[kWarps];
-  __shared__ float most;
-  __shared__ uint32_t best[64];
-  __shared__ uint32_t bound, count;
-  __shared__ uint2 list[kList];
-  griddep_wait();  // every input may be the previous kernel's output
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int part = blockIdx.x;
-  const int64_t row = blockIdx.y + (int64_t)blockIdx.z * 65535;
-  if (row >= (int64_t)a.groups * a.beams) return;
-  const int64_t at = row * a.parts + part;
-  if (a.done && a.done[row]) return;
-  const int v0 = part * kPart, n = min(kPart, a.vocab - v0);
-  // element j of a thread: v0 + (j / 8) * 8 * kThreads + 8 * tid + j % 8
-  float x[kPer];
-  bool bad = false;
+__global__ void __launch_bounds__(32 * kPartWarps, 7) beam_part_kernel(const BeamArgs a) {
+  using H = Held<kBf16>;
+  constexpr int kVec = H::kVec;
+  constexpr uint32_t kAll = 0xffffffffu;
+  __shared__ uint2 lists[kPartWarps][kPartList];
+  __shared__ int counts[kPartWarps];
+  griddep_wait();    // every input may be the previous kernel's output
+  griddep_launch();  // (the join waits for this kernel, and alone writes a call's outputs)
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int at = blockIdx.x * kPartWarps + warp, row = quotient(at, a.by_parts);
+  if (row >= a.groups * a.beams) return;  // (whole warps)
+  if (a.done && a.done[row]) {            // one candidate, at cum: of lse 0 and a key of its own
+    const bool has = at == row * a.parts;
+    for (int r = lane; r < a.take; r += 32)
+      a.part_best[(int64_t)at * a.take + r] = make_uint2(has && r == 0 ? kDone : kNone, (uint32_t)a.end_token);
+    if (lane == 0) a.part_sum[at] = has ? PartSum{1.0, 0.0f, 0.0f} : PartSum{0.0, -INFINITY, 0.0f};
+    return;
+  }
+  // Values [v0, v1) of the row: whole 16 bytes of memory from v0 + head on, and what is
+  // before and behind them (rows of an odd size begin anywhere), a value a lane.
+  const int v0 = (at - row * a.parts) * a.part, v1 = min(v0 + a.part, a.vocab), n = max(0, v1 - v0);
+  const int64_t e0 = row * a.stride + v0;
+  const int head = min(n, (int)(-e0 & (kVec - 1))), vectors = (n - head) / kVec, tail = n - head - vectors * kVec;
+  const uint8_t* first = static_cast<const uint8_t*>(a.logits) + e0 * (kBf16 ? 2 : 4);
+  const uint4* window = reinterpret_cast<const uint4*>(first + head * (kBf16 ? 2 : 4)) + lane;
+  const uint32_t none = kBf16 ? 0xFF80FF80u : 0xFF800000u;
+  H x;
+  auto load = [&](int from) {
 #pragma unroll
-  for (int j = 0; j < kPer; ++j) {
-    const int i = (j / 8) * (8 * kThreads) + 8 * tid + (j & 7);
-    x[j] = -INFINITY;
-    if (i < n) {
-      const int64_t e = row * a.stride + v0 + i;
-      x[j] = clean(kBf16 ? bf16_bits_to_float(__ldg(static_cast<const uint16_t*>(a.logits) + e))
-                         : __ldg(static_cast<const float*>(a.logits) + e), bad);
+    for (int j = 0; j < kN; ++j) {
+      x.v[j] = make_uint4(none, none, none, none);
+      if (from + 32 * j + lane < vectors) x.v[j] = __ldg(window + from + 32 * j);
     }
+  };
+  load(0);
+  const int odd = lane < head ? lane : lane - head < tail ? n - tail + lane - head : -1;  // its place in the part
+  float alone = -INFINITY;
+  bool bad = false;
+  if (odd >= 0)
+    alone = clean(kBf16 ? bf16_bits_to_float(__ldg(reinterpret_cast<const uint16_t*>(first) + odd))
+                        : __ldg(reinterpret_cast<const float*>(first) + odd), bad);
+  uint2* list = lists[warp];
+  if (lane == 0) counts[warp] = 0;
+  __syncwarp();
+  auto take_in = [&](float value, int place) {
+    const int c = atomicAdd(&counts[warp], 1);
+    if (c < kPartList) list[c] = make_uint2(key_of(value), v0 + place);
+  };
+
+  float run0 = alone, run1 = -INFINITY;  // the lane's largest so far, of each half of its vectors
+  float top = -INFINITY;                 // the warp's
+  double sum = 0.0;                      // of exp(x - top), the lane's
+  uint32_t bound = kNone + 1;            // of keys
+  for (int from = 0; from == 0 || from < vectors; from += 32 * kN) {
+    float vm[kN], m0 = -INFINITY, m1 = -INFINITY;
+#pragma unroll
+    for (int j = 0; j < kN; ++j) {
+      vm[j] = x.most(j);
+      float& m = j < kN / 2 ? m0 : m1;
+      m = max_nan(m, vm[j]);
+    }
+    const bool odd_ones = !__all_sync(kAll, max_nan(m0, m1) < INFINITY);  // NaN or +inf
+    if (odd_ones) {
+      bad = bad || !(max_nan(m0, m1) < INFINITY);
+      m0 = m1 = -INFINITY;
+#pragma unroll
+      for (int j = 0; j < kN; ++j) {
+        H::clean_vector(x.v[j]);
+        vm[j] = x.most(j);
+        float& m = j < kN / 2 ? m0 : m1;
+        m = fmaxf(m, vm[j]);
+      }
+    }
+    run0 = fmaxf(run0, m0), run1 = fmaxf(run1, m1);
+    const uint32_t k0 = key_of(a.take > 16 ? run0 : fmaxf(run0, run1)), k1 = key_of(run1);
+    const float most = of_key(__reduce_max_sync(kAll, max(k0, k1)));
+    uint32_t hits = 0;
+    if (most > -INFINITY) {
+      if (most > top) {
+        if (top > -INFINITY) sum *= (double)ex2((top - most) * kLog2e);
+        top = most;
+      }
+      // the largest multiple of 2^16 that `take` of the maxima reach: of 32 up to 16 (of
+      // which 22 logits are expected to reach it), else of 64
+      uint32_t b = 0;
+      if (a.take <= 16) {
+#pragma unroll
+        for (int i = 31; i >= 16; --i)
+          if (__popc(__ballot_sync(kAll, k0 >= (b | 1u << i))) >= a.take) b |= 1u << i;
+      } else {
+#pragma unroll
+        for (int i = 31; i >= 16; --i)
+          if (__popc(__ballot_sync(kAll, k0 >= (b | 1u << i))) + __popc(__ballot_sync(kAll, k1 >= (b | 1u << i))) >= a.take)
+            b |= 1u << i;
+      }
+      bound = max(bound, b);
+      const float least = of_key(bound);
+#pragma unroll
+      for (int j = 0; j < kN; ++j) hits |= (vm[j] >= least ? 1u : 0u) << j;
+      if (from == 0 && alone >= least) take_in(alone, odd);
+      // the sum, two at a time, in fp32 for a window
+      uint64_t sum2 = pack2(from == 0 ? ex2((alone - top) * kLog2e) : 0.0f, 0.0f);
+      const uint64_t minus = pack2(-top, -top), scale = pack2(kLog2e, kLog2e);
+#pragma unroll
+      for (int j = 0; j < kN; ++j)
+#pragma unroll
+        for (int i = 0; i < kVec; i += 2) {
+          float p, q;
+          unpack2(fma2(add2(pack2(H::get(x.v[j], i), H::get(x.v[j], i + 1)), minus), scale, 0), p, q);
+          sum2 = add2(sum2, pack2(ex2(p), ex2(q)));
+        }
+      float p, q;
+      unpack2(sum2, p, q);
+      sum += (double)(p + q);
+    }
+    // the next window's loads, before what this one has to list
+    load(from + 32 * kN);
+    while (hits) {
+      const int j = __ffs(hits) - 1;
+      hits &= hits - 1;
+      uint4 u = __ldg(window + from + 32 * j);
+      if (odd_ones) H::clean_vector(u);
+      uint32_t which = 0;
+      const float least = of_key(bound);
+#pragma unroll
+      for (int i = 0; i < kVec; ++i) which |= (H::get(u, i) >= least ? 1u : 0u) << i;
+      while (which) {
+        const int i = __ffs(which) - 1;
+        which &= which - 1;
+        uint32_t w = i / (kVec / 4) == 0 ? u.x : i / (kVec / 4) == 1 ? u.y : i / (kVec / 4) == 2 ? u.z : u.w;
+        if (kBf16) w = i & 1 ? w & 0xFFFF0000u : w << 16;
+        take_in(__uint_as_float(w), head + (from + 32 * j + lane) * kVec + i);
+      }
+    }
+    __syncwarp();
   }
   if (bad) report(a.status, CSA2_ERR_RANGE);
-  float m = -INFINITY;
 #pragma unroll
-  for (int j = 0; j < kPer; ++j) m = fmaxf(m, x[j]);
-  // maxima of 64 groups of 8 threads
-  uint32_t mine = key_of(m);
-  uint32_t group = mine;
-#pragma unroll
-  for (int d = 1; d < 8; d <<= 1) group = max(group, __shfl_xor_sync(0xffffffffu, group, d));
-  if ((tid & 7) == 0) best[tid >> 3] = group;
-  if (tid == 0) count = 0;
-  __syncthreads();
-  if (tid < 64) {
-    const uint32_t k = best[tid];
-    int rank = 0;
-    for (int j = 0; j < 64; ++j) rank += best[j] > k || (best[j] == k && j < tid);
-    if (rank == a.take - 1) bound = max(k, kNone + 1);
-    if (rank == 0) most = of_key(k);
-  }
-  __syncthreads();
-  const uint32_t least = bound;
-  const float top = most;
-  // the sum, and what reaches the bound
-  float sum = 0.0f;
-  constexpr float kHi = 1.44269502f, kLo = 1.92596299e-8f;  // log2 e
-  if (top > -INFINITY) {
-#pragma unroll
-    for (int j = 0; j < kPer; ++j) {
-      const float d = x[j] - top;
-      sum += ex2(fmaf(d, kHi, d * kLo));
+  for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(kAll, sum, d);
+  if (lane == 0) a.part_sum[at] = PartSum{sum, top, 0.0f};
+  uint2* out = a.part_best + (int64_t)at * a.take;
+  int c = counts[warp];
+  __syncwarp();
+  if (c <= kPartList) {
+    // those that reach the last bound
+    int kept = 0;
+    for (int p0 = 0; p0 < c; p0 += 32) {
+      const uint2 e = p0 + lane < c ? list[p0 + lane] : make_uint2(0, 0);
+      const uint32_t stay = __ballot_sync(kAll, e.x >= bound);
+      if (e.x >= bound) list[kept + __popc(stay & ((1u << lane) - 1))] = e;
+      kept += __popc(stay);
+      __syncwarp();
     }
-  }
-#pragma unroll
-  for (int j = 0; j < kPer; ++j) {
-    const uint32_t k = key_of(x[j]);
-    if (k >= least) {
-      const uint32_t p = atomicAdd(&count, 1u);
-      if (p < kList) list[p] = make_uint2(k, v0 + (j / 8) * (8 * kThreads) + 8 * tid + (j & 7));
-    }
-  }
-  double wide = sum;
-#pragma unroll
-  for (int d = 16; d > 0; d >>= 1) wide += __shfl_xor_sync(0xffffffffu, wide, d);
-  if (lane == 0) sums[warp] = wide;
-  __syncthreads();
-  if (tid == 0) {
-    double s = 0.0;
-    for (int w = 0; w < kWarps; ++w) s += sums[w];
-    a.part_sum[at] = PartSum{s, top, 0.0f};
-  }
-  uint2* out = a.part_best + at * a.take;
-  const int c = (int)count;
-  if (c <= kList) {
-    for (int p = tid; p < c; p += kThreads) {
+    c = kept;
+    for (int p = lane; p < c; p += 32) {
       const uint2 e = list[p];
       int rank = 0;
+#pragma unroll 4
       for (int q = 0; q < c; ++q) {
         const uint2 f = list[q];
         rank += f.x > e.x || (f.x == e.x && f.y < e.y);
       }
       if (rank < a.take) out[rank] = e;
     }
-    for (int p = c + tid; p < a.take; p += kThreads) out[p] = make_uint2(kNone, 0);
-  } else {
-    // one by one: the best behind the last, (key, place) as one number
-    __shared__ unsigned long long next[kWarps];
-    unsigned long long last = ~0ull;
-    for (int r = 0; r < a.take; ++r) {
-      unsigned long long b = 0;
+    for (int p = c + lane; p < a.take; p += 32) out[p] = make_uint2(kNone, 0);
+    return;
+  }
+  // one by one: the best behind the last, (key, place) as one number
+  unsigned long long last = ~0ull;
+  for (int r = 0; r < a.take; ++r) {
+    unsigned long long b = 0;
+    auto look = [&](float value, int place) {
+      const unsigned long long e = (unsigned long long)key_of(value) << 32 | (0xffffffffu - (uint32_t)(v0 + place));
+      if (e < last && e > b) b = e;
+    };
+    if (odd >= 0) look(alone, odd);
+#pragma unroll 1
+    for (int j = lane; j < vectors; j += 32) {
+      uint4 u = __ldg(window - lane + j);
+      H::clean_vector(u);
 #pragma unroll
-      for (int j = 0; j < kPer; ++j) {
-        const uint32_t i = v0 + (j / 8) * (8 * kThreads) + 8 * tid + (j & 7);
-        const unsigned long long e = (unsigned long long)key_of(x[j]) << 32 | (0xffffffffu - i);
-        if (e < last && e > b) b = e;
-      }
-#pragma unroll
-      for (int d = 16; d > 0; d >>= 1) {
-        const unsigned long long o = __shfl_xor_sync(0xffffffffu, b, d);
-        b = o > b ? o : b;
-      }
-      __syncthreads();
-      if (lane == 0) next[warp] = b;
-      __syncthreads();
-      for (int w = 0; w < kWarps; ++w) b = next[w] > b ? next[w] : b;
-      last = b;
-      if (tid == 0) out[r] = make_uint2((uint32_t)(b >> 32), 0xffffffffu - (uint32_t)b);
+      for (int i = 0; i < kVec; ++i) look(H::get(u, i), head + j * kVec + i);
     }
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) {
+      const unsigned long long o = __shfl_xor_sync(kAll, b, d);
+      b = o > b ? o : b;
+    }
+    last = b;
+    if (lane == 0) out[r] = make_uint2((uint32_t)(b >> 32), 0xffffffffu - (uint32_t)b);
   }
 }
 
-// fp64 -> unsigned in the same order.
+// fp64 -> unsigned in the same order (no -0 comes here).
 __device__ __forceinline__ uint64_t key_of(double x) {
-  const uint64_t u = (uint64_t)__double_as_longlong(x + 0.0);
+  const uint64_t u = (uint64_t)__double_as_longlong(x);
   return u >> 63 ? ~u : u | 1ull << 63;
 }
 constexpr uint64_t kNone64 = 0x000FFFFFFFFFFFFFull;  // of -inf
 
 __global__ void __launch_bounds__(kThreads) beam_join_kernel(const BeamArgs a) {
-  __shared__ double shift[kMost];  // cum - lse
+  __shared__ double shift[kMost];  // first the sums, then cum - lse
+  __shared__ float most[kMost];
   __shared__ uint64_t best[64];
   __shared__ uint64_t bound;
   __shared__ uint32_t count;
@@ -194,68 +327,83 @@ __global__ void __launch_bounds__(kThreads) beam_join_kernel(const BeamArgs a) {
   griddep_wait();
   const int g = blockIdx.x, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int64_t row0 = (int64_t)g * a.beams;
-  for (int k = warp; k < a.beams; k += kWarps) {
-    const int64_t row = row0 + k;
-    const bool over = a.done && a.done[row];
-    double lse = 0.0;
-    if (!over) {
-      float m = -INFINITY;
-      for (int p = lane; p < a.parts; p += 32) m = fmaxf(m, a.part_sum[row * a.parts + p].most);
-      m = of_key(__reduce_max_sync(0xffffffffu, key_of(m)));
-      double s = 0.0;
-      for (int p = lane; p < a.parts; p += 32) {
-        const PartSum e = a.part_sum[row * a.parts + p];
-        if (e.most > -INFINITY) s += e.sum * exp((double)e.most - (double)m);
+  // A list is what a part has, in order; list c is beam c / parts's.  Of the lists'
+  // beginnings, 64 candidates at least where there are as many, the `take`-th largest of 64
+  // groups' maxima is a bound, and few candidates reach it.
+  const int lists = a.beams * a.parts, depth = min(a.take, (63 + lists) / lists), samples = lists * depth;
+  const uint2* mine = a.part_best + row0 * a.parts * a.take;
+  auto score_of = [&](uint2 e, int beam) {
+    return e.x <= kNone ? -(double)INFINITY : e.x == kDone ? shift[beam] : (double)of_key(e.x) + shift[beam];
+  };
+  auto beam_of = [&](int list) { return quotient(list, a.by_parts); };
+  // (asked for ahead of the beams' sums; neighbouring samples in different groups)
+  const int sample0 = (tid & 7) * 64 + (tid >> 3);
+  uint2 raw0 = make_uint2(0, 0);
+  if (sample0 < samples) raw0 = mine[(sample0 % lists) * a.take + sample0 / lists];
+  float cum = tid < a.beams ? a.cum[row0 + tid] : 0.0f;
+  {  // the beams' sums: eight threads a beam (fp64 is slow here: 16 cycles a warp's instruction)
+    const int k = tid >> 3;
+    float m = -INFINITY;
+    double s = 0.0;
+    if (k < a.beams)
+      for (int p = tid & 7; p < a.parts; p += 8) {
+        const PartSum e = a.part_sum[(row0 + k) * a.parts + p];
+        if (e.most > m) s *= (double)ex2((m - e.most) * kLog2e), m = e.most;
+        if (e.most > -INFINITY) s += e.sum * (double)ex2((e.most - m) * kLog2e);
       }
+    float all = m;
 #pragma unroll
-      for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
-      lse = m > -INFINITY ? (double)m + log(s) : -INFINITY;
+    for (int d = 1; d < 8; d <<= 1) all = fmaxf(all, __shfl_xor_sync(0xffffffffu, all, d));
+    if (__any_sync(0xffffffffu, k < a.beams)) {
+      if (all > -INFINITY) s *= (double)ex2((m - all) * kLog2e);
+#pragma unroll
+      for (int d = 1; d < 8; d <<= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
     }
-    if (lane == 0) {
-      bool bad = false;
-      const float c = clean(a.cum[row], bad);
-      if (bad) report(a.status, CSA2_ERR_RANGE);
-      shift[k] = lse > -INFINITY ? (double)c - lse : -INFINITY;
-      if (a.lse) a.lse[row] = (float)lse;
-    }
+    if ((tid & 7) == 0) shift[k] = s, most[k] = all;
   }
   if (tid == 0) count = 0;
   __syncthreads();
-  // candidate c: beam c / per, then part, then rank in it; a done beam has its first alone
-  const int per = a.parts * a.take, total = a.beams * per;
-  auto score_of = [&](int c, int& beam, int& token) {
-    beam = c / per;
-    const int64_t row = row0 + beam;
-    if (a.done && a.done[row]) {
-      token = a.end_token;
-      return c % per == 0 ? shift[beam] : -(double)INFINITY;
-    }
-    const uint2 e = a.part_best[row * per + c % per];
-    token = (int)e.y;
-    return e.x > kNone ? (double)of_key(e.x) + shift[beam] : -(double)INFINITY;
-  };
-  uint64_t top = kNone64;
-  for (int c = tid; c < total; c += kThreads) {
-    int b, t;
-    top = max(top, key_of(score_of(c, b, t)));
+  if (tid < a.beams) {
+    bool bad = false;
+    cum = clean(cum, bad);
+    if (bad) report(a.status, CSA2_ERR_RANGE);
+    const double lse = most[tid] > -INFINITY ? (double)most[tid] + log(shift[tid]) : -(double)INFINITY;
+    shift[tid] = lse > -INFINITY ? (double)cum - lse + 0.0 : -(double)INFINITY;
+    if (a.lse) a.lse[row0 + tid] = (float)lse;
   }
+  __syncthreads();
+  uint64_t top = sample0 < samples ? key_of(score_of(raw0, beam_of(sample0 % lists))) : kNone64;
+  for (int i = sample0 + kThreads; i < samples; i += kThreads)
+    top = max(top, key_of(score_of(mine[(i % lists) * a.take + i / lists], beam_of(i % lists))));
 #pragma unroll
   for (int d = 1; d < 8; d <<= 1) top = max(top, (uint64_t)__shfl_xor_sync(0xffffffffu, (unsigned long long)top, d));
   if ((tid & 7) == 0) best[tid >> 3] = top;
   __syncthreads();
-  if (tid < 64) {
-    const uint64_t k = best[tid];
+  {  // eight threads rank a maximum
+    const int i = tid >> 3, j0 = (tid & 7) * 8;
     int rank = 0;
-    for (int j = 0; j < 64; ++j) rank += best[j] > k || (best[j] == k && j < tid);
-    if (rank == a.take - 1) bound = max(k, kNone64 + 1);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) rank += best[j0 + j] > top || (best[j0 + j] == top && j0 + j < i);
+#pragma unroll
+    for (int d = 1; d < 8; d <<= 1) rank += __shfl_xor_sync(0xffffffffu, rank, d);
+    if ((tid & 7) == 0 && rank == a.take - 1) bound = max(top, kNone64 + 1);
   }
   __syncthreads();
-  for (int c = tid; c < total; c += kThreads) {
-    int b, t;
-    const uint64_t k = key_of(score_of(c, b, t));
-    if (k >= bound) {
-      const uint32_t p = atomicAdd(&count, 1u);
-      if (p < kList) lkey[p] = k, lplace[p] = make_uint2(b, t);
+  const uint64_t least = bound;
+  for (int c = tid; c < lists; c += kThreads) {
+    const int b = beam_of(c);
+    bool more = true;
+    for (int r0 = 0; r0 < a.take && more; r0 += 4) {
+      uint2 e[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) e[i] = r0 + i < a.take ? mine[c * a.take + r0 + i] : make_uint2(0, 0);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint64_t k = key_of(score_of(e[i], b));
+        if (!(more = more && k >= least)) continue;
+        const uint32_t p = atomicAdd(&count, 1u);
+        if (p < kList) lkey[p] = k, lplace[p] = make_uint2(b, e[i].y);
+      }
     }
   }
   __syncthreads();
@@ -287,9 +435,10 @@ __global__ void __launch_bounds__(kThreads) beam_join_kernel(const BeamArgs a) {
   unsigned long long last_k = ~0ull, last_p = 0;
   for (int r = 0; r < a.take; ++r) {
     unsigned long long bk = kNone64, bp = ~0ull;  // place: the smaller first
-    for (int c = tid; c < total; c += kThreads) {
-      int b, t;
-      const unsigned long long k = key_of(score_of(c, b, t)), p = (unsigned long long)b << 32 | (uint32_t)t;
+    for (int c = tid; c < lists * a.take; c += kThreads) {
+      const uint2 e = mine[c];
+      const int b = beam_of(c / a.take);
+      const unsigned long long k = key_of(score_of(e, b)), p = (unsigned long long)b << 32 | e.y;
       const bool behind = k < last_k || (k == last_k && p > last_p);
       if (behind && (k > bk || (k == bk && p < bp))) bk = k, bp = p;
     }
@@ -310,17 +459,26 @@ __global__ void __launch_bounds__(kThreads) beam_join_kernel(const BeamArgs a) {
   }
 }
 
-int parts_of(int vocab) { return (int)(((int64_t)vocab + kPart - 1) / kPart); }
+// Parts of a row, all of like size: as few as make 4096 warps, of 1 to kMostWindows windows.
+struct Parts {
+  int n, size;
+};
+Parts parts_of(int64_t rows, int vocab, bool bf16) {
+  const int vec = bf16 ? 8 : 4, window = kN * 32 * vec, windows = (vocab - 1) / window + 1;
+  const int each = (int)std::max<int64_t>(1, std::min<int64_t>(kMostWindows, rows * windows / 4096));
+  const int n = (windows + each - 1) / each;
+  return {n, ((vocab - 1) / n / vec + 1) * vec};
+}
+int most_parts(int64_t rows, int vocab) { return std::max(parts_of(rows, vocab, true).n, parts_of(rows, vocab, false).n); }
 bool sizes_ok(int32_t groups, int32_t beams, int32_t vocab, int32_t take) {
   return groups >= 0 && beams >= 1 && vocab >= 1 && take >= 1;
 }
 bool sizes_fit(int32_t groups, int32_t beams, int32_t vocab, int32_t take) {
-  return beams <= kMost && take <= kMost && (int64_t)groups * beams * parts_of(vocab) <= INT32_MAX &&
-         (int64_t)parts_of(vocab) * beams * take <= INT32_MAX / 2;
+  if (beams > kMost || take > kMost || (int64_t)groups * beams > INT32_MAX) return false;
+  const int64_t parts = most_parts((int64_t)groups * beams, vocab);
+  return groups * beams * parts <= INT32_MAX - kPartWarps && parts * beams * take <= INT32_MAX / 2;
 }
-size_t sums_bytes(int64_t groups, int beams, int vocab) {
-  return (size_t)((groups * beams * parts_of(vocab) * sizeof(PartSum) + 255) / 256 * 256);
-}
+size_t sums_bytes(int64_t rows, int64_t parts) { return (size_t)((rows * parts * sizeof(PartSum) + 255) / 256 * 256); }
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
 }  // namespace
@@ -332,7 +490,8 @@ extern "C" {
 
 size_t csa2_beam_workspace_bytes(int32_t groups, int32_t beams, int32_t vocab, int32_t take) {
   if (!sizes_ok(groups, beams, vocab, take) || !sizes_fit(groups, beams, vocab, take)) return 0;
-  return sums_bytes(groups, beams, vocab) + (size_t)groups * beams * parts_of(vocab) * take * sizeof(uint2);
+  const int64_t rows = (int64_t)groups * beams, parts = most_parts(rows, vocab);
+  return sums_bytes(rows, parts) + (size_t)(rows * parts * take) * sizeof(uint2);
 }
 
 int32_t csa2_beam_select(int32_t groups, int32_t beams, int32_t vocab, int32_t take, const void* logits,
@@ -348,14 +507,16 @@ int32_t csa2_beam_select(int32_t groups, int32_t beams, int32_t vocab, int32_t t
       (done && (end_token < 0 || end_token >= vocab)) || !aligned(workspace, 256))
     return CSA2_ERR_INVALID_ARG;
   if (!workspace || workspace_bytes < csa2_beam_workspace_bytes(groups, beams, vocab, take)) return CSA2_ERR_CAPACITY;
-  BeamArgs a{groups, beams, vocab, take, parts_of(vocab), logits, stride, cum, done, end_token, scores, parents, tokens, lse,
-             static_cast<PartSum*>(workspace),
-             reinterpret_cast<uint2*>(static_cast<uint8_t*>(workspace) + sums_bytes(groups, beams, vocab)), status};
   const int64_t rows = (int64_t)groups * beams;
-  const dim3 grid(a.parts, (unsigned)std::min<int64_t>(rows, 65535), (unsigned)((rows + 65534) / 65535));
+  const bool bf16 = logits_dtype == CSA2_BF16;
+  const Parts parts = parts_of(rows, vocab, bf16);
+  BeamArgs a{groups, beams, vocab, take, parts.n, parts.size, divisor(parts.n), logits, stride, cum, done, end_token, scores,
+             parents, tokens, lse, static_cast<PartSum*>(workspace),
+             reinterpret_cast<uint2*>(static_cast<uint8_t*>(workspace) + sums_bytes(rows, parts.n)), status};
+  const dim3 grid((unsigned)((rows * parts.n + kPartWarps - 1) / kPartWarps)), block(32 * kPartWarps);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  cudaError_t e = logits_dtype == CSA2_BF16 ? launch_k(beam_part_kernel<true>, grid, dim3(kThreads), 0, s, 0, a)
-                                            : launch_k(beam_part_kernel<false>, grid, dim3(kThreads), 0, s, 0, a);
+  cudaError_t e = bf16 ? launch_k(beam_part_kernel<true>, grid, block, 0, s, 0, a)
+                       : launch_k(beam_part_kernel<false>, grid, block, 0, s, 0, a);
   if (e == cudaSuccess) e = launch_k(beam_join_kernel, dim3(groups), dim3(kThreads), 0, s, 0, a);
   return e == cudaSuccess ? CSA2_OK : CSA2_ERR_CUDA;
 }

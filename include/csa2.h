@@ -512,8 +512,9 @@ CSA2_API size_t csa2_beam_workspace_bytes(int32_t groups, int32_t beams, int32_t
  *    sets CSA2_ERR_RANGE.
  * logits: bf16 (logits_dtype CSA2_BF16) or fp32 (CSA2_F32) rows of `vocab` contiguous
  * values, `stride` elements apart (any distance from vocab on), the first 16-byte
- * aligned.  beams 1..64, take 1..64, groups * beams < 2^31 / vocab's parts of 16384
- * (CSA2_ERR_UNSUPPORTED beyond).  Workspace: csa2_beam_workspace_bytes, 256-byte
+ * aligned.  beams 1..64, take 1..64 (CSA2_ERR_UNSUPPORTED beyond, or where a group or
+ * the call has more than 2^30 partial results, one for every 500 logits and place in
+ * `take`).  Workspace: csa2_beam_workspace_bytes, 256-byte
  * aligned (smaller: CSA2_ERR_CAPACITY), contents not kept between calls; two calls
  * that may overlap need one each. */
 CSA2_API int32_t csa2_beam_select(int32_t groups, int32_t beams, int32_t vocab, int32_t take, const void* logits,

@@ -316,8 +316,9 @@ __device__ __forceinline__ uint64_t key_of(double x) {
 constexpr uint64_t kNone64 = 0x000FFFFFFFFFFFFFull;  // of -inf
 
 __global__ void __launch_bounds__(kThreads) beam_join_kernel(const BeamArgs a) {
-  __shared__ double shift[kMost];  // first the sums, then cum - lse
+  __shared__ double sums[kMost], logs[kMost];  // of exp(x - most), their logarithms
   __shared__ float most[kMost];
+  __shared__ double cums[kMost];
   __shared__ uint64_t best[64];
   __shared__ uint64_t bound;
   __shared__ uint32_t count;
@@ -333,7 +334,10 @@ __global__ void __launch_bounds__(kThreads) beam_join_kernel(const BeamArgs a) {
   const int lists = a.beams * a.parts, depth = min(a.take, (63 + lists) / lists), samples = lists * depth;
   const uint2* mine = a.part_best + row0 * a.parts * a.take;
   auto score_of = [&](uint2 e, int beam) {
-    return e.x <= kNone ? -(double)INFINITY : e.x == kDone ? shift[beam] : (double)of_key(e.x) + shift[beam];
+    // relative to the beam's largest (beside logits near fp32's lowest the rest would be
+    // lost), what fp64 adds exactly first
+    const double x = e.x == kDone ? 0.0 : (double)of_key(e.x) - (double)most[beam];
+    return e.x <= kNone ? -(double)INFINITY : x + cums[beam] - logs[beam];
   };
   auto beam_of = [&](int list) { return quotient(list, a.by_parts); };
   // (asked for ahead of the beams' sums; neighbouring samples in different groups)
@@ -359,17 +363,24 @@ __global__ void __launch_bounds__(kThreads) beam_join_kernel(const BeamArgs a) {
 #pragma unroll
       for (int d = 1; d < 8; d <<= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
     }
-    if ((tid & 7) == 0) shift[k] = s, most[k] = all;
+    if ((tid & 7) == 0) sums[k] = s, most[k] = all;
   }
   if (tid == 0) count = 0;
   __syncthreads();
   if (tid < a.beams) {
+    // Beams whose logits are the same have the same sum.  What they have may differ in its
+    // last bits where their rows begin differently far from 16 bytes; so a beam that is
+    // like a lower one, by its largest logit and its sum to 2^-20, takes that one's.
     bool bad = false;
     cum = clean(cum, bad);
     if (bad) report(a.status, CSA2_ERR_RANGE);
-    const double lse = most[tid] > -INFINITY ? (double)most[tid] + log(shift[tid]) : -(double)INFINITY;
-    shift[tid] = lse > -INFINITY ? (double)cum - lse + 0.0 : -(double)INFINITY;
-    if (a.lse) a.lse[row0 + tid] = (float)lse;
+    double s = sums[tid];
+    for (int b = tid - 1; b >= 0; --b)
+      if (most[b] == most[tid] && fabs(sums[b] - sums[tid]) <= 0x1p-20 * sums[tid]) s = sums[b];
+    const bool some = most[tid] > -INFINITY;
+    logs[tid] = some ? log(s) : 0.0;
+    cums[tid] = some ? (double)cum + 0.0 : -(double)INFINITY;
+    if (a.lse) a.lse[row0 + tid] = some ? (float)((double)most[tid] + logs[tid]) : -INFINITY;
   }
   __syncthreads();
   uint64_t top = sample0 < samples ? key_of(score_of(raw0, beam_of(sample0 % lists))) : kNone64;

@@ -50,15 +50,17 @@ __device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uin
 
 // A lane's sums of 16 rows of W: rows g and g + 8, rows t and t + 1 of x; what of them is there.
 __device__ __forceinline__ void store_group(const Fp4Linear& a, int row0, int t, const float* unscale, float4 d) {
-  if (t >= a.T) return;
   const float v[4] = {d.x, d.y, d.z, d.w};
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const int i = row0 + 8 * h;
-    if (i >= a.n) return;
-    const float b = fp4_bias(a, i);
-    fp4_store(a, t, i, v[2 * h] * unscale[t], a.alpha, b);
-    if (t + 1 < a.T) fp4_store(a, t + 1, i, v[2 * h + 1] * unscale[t + 1], a.alpha, b);
+  for (int c = 0; c < 2; ++c) {
+    if (t + c >= a.T) return;
+    // the smaller factor first: what fp32 holds in the end is not lost on the way
+    const float u = unscale[t + c], first = u > 1.0f ? a.alpha : u, second = u > 1.0f ? u : a.alpha;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int i = row0 + 8 * h;
+      if (i < a.n) fp4_store(a, t + c, i, v[2 * h + c] * first, second, fp4_bias(a, i));
+    }
   }
 }
 

@@ -501,7 +501,8 @@ CSA2_API size_t csa2_beam_workspace_bytes(int32_t groups, int32_t beams, int32_t
  * are written in order (score descending; of equal scores the lower beam, then the
  * lower token): scores [groups][take] fp32, parents [groups][take] (the sequence
  * number g * beams + k) and tokens [groups][take] int32.  Scores are compared in
- * fp64, lse being summed from fp32 exponentials in fp64, and rounded once.
+ * fp64, lse being summed from fp32 exponentials in fp64, and rounded once; beams whose
+ * logits are the same have the same lse.
  *  - A token of logit -inf (masked) and every token of a beam whose cum is -inf is
  *    no candidate; where candidates run out, score -inf, parent and token -1.
  *  - done [groups][beams] bytes or NULL: a beam that is done (not 0) has end_token
@@ -590,7 +591,8 @@ CSA2_API int32_t csa2_fp4_pack(int32_t n, int32_t k, const uint8_t* codes, const
  * x [T][k] bf16, rows `x_stride` elements apart (a multiple of 8), 16-byte aligned; bias
  * [n] bf16 or NULL; out [T][n] bf16 (out_dtype CSA2_BF16) or fp32 (CSA2_F32), rows
  * `out_stride` elements apart (any distance from n on).  out must not overlap x or
- * the weights.  An x that is not finite has effect on its own row's outputs alone.
+ * the weights.  An x that is not finite has effect on its own row's outputs alone; a row
+ * whose products' magnitudes (before alpha) sum up past fp32's largest may yield such.
  * Rows' sums do not depend on what other rows hold, but their order may depend on T. */
 CSA2_API int32_t csa2_fp4_linear(const csa2_fp4_weights* w, int32_t T, const uint16_t* x, int64_t x_stride,
                                  const uint16_t* bias, void* out, int32_t out_dtype, int64_t out_stride,

@@ -308,6 +308,22 @@ __global__ void __launch_bounds__(32 * kPartWarps, 7) beam_part_kernel(const Bea
   }
 }
 
+// Natural logarithm of s >= 1/2, off by 2^-29 at most, nearly all of it in fp32 (the library's in
+// fp64 took 3000 cycles): s = 2^e m, m in [2/3, 4/3); log m = 2 (z + z^3 / 3 + z^5 / 5 ..) with
+// z = (m - 1) / (m + 1), |z| <= 1/5, as a sum of two fp32, and what s has beyond fp32.
+__device__ __forceinline__ double log_of(double s) {
+  const float h = (float)s;
+  const float rest = (float)(s - (double)h) / h;
+  const int bits = __float_as_int(h), e = (bits - 0x3F2AAAABu) >> 23;
+  const float m = __int_as_float(bits - (e << 23));
+  const float f = m - 1.0f, g = m + 1.0f, gl = m - (g - 1.0f);  // g + gl = m + 1
+  const float z = f / g;
+  const float zl = (fmaf(-z, g, f) - z * gl) / g;
+  const float w = z * z;
+  const float tail = z * w * fmaf(w, fmaf(w, fmaf(w, fmaf(w, fmaf(w, 1.0f / 13, 1.0f / 11), 1.0f / 9), 1.0f / 7), 1.0f / 5), 1.0f / 3);
+  return fma((double)e, 0.693147180559945309, (double)(2.0f * z)) + (double)(2.0f * (zl + tail) + rest);
+}
+
 // fp64 -> unsigned in the same order (no -0 comes here).
 __device__ __forceinline__ uint64_t key_of(double x) {
   const uint64_t u = (uint64_t)__double_as_longlong(x);
@@ -319,19 +335,20 @@ __global__ void __launch_bounds__(kThreads) beam_join_kernel(const BeamArgs a) {
   __shared__ double sums[kMost], logs[kMost];  // of exp(x - most), their logarithms
   __shared__ float most[kMost];
   __shared__ double cums[kMost];
-  __shared__ uint64_t best[64];
-  __shared__ uint64_t bound;
-  __shared__ uint32_t count;
+  __shared__ float cums32[kMost], logs32[kMost];
+  __shared__ uint32_t best[64];
+  __shared__ uint32_t bound, far, count;
   __shared__ uint64_t lkey[kList];
-  __shared__ uint2 lplace[kList];  // beam, token
+  __shared__ uint64_t lplace[kList];  // beam, token
   __shared__ unsigned long long wkey[kWarps], wplace[kWarps];
   griddep_wait();
   const int g = blockIdx.x, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int64_t row0 = (int64_t)g * a.beams;
   // A list is what a part has, in order; list c is beam c / parts's.  Of the lists'
   // beginnings, 64 candidates at least where there are as many, the `take`-th largest of 64
-  // groups' maxima is a bound, and few candidates reach it.
-  const int lists = a.beams * a.parts, depth = min(a.take, (63 + lists) / lists), samples = lists * depth;
+  // groups' maxima is a bound, and few candidates reach it: found in fp32, up to what that
+  // may be off by, as an fp64 instruction of a warp takes an SM 16 cycles here.
+  const int lists = a.beams * a.parts, depth = min(a.take, max(1, max((63 + lists) / lists, kThreads / lists))), samples = lists * depth;
   const uint2* mine = a.part_best + row0 * a.parts * a.take;
   auto score_of = [&](uint2 e, int beam) {
     // relative to the beam's largest (beside logits near fp32's lowest the rest would be
@@ -339,13 +356,16 @@ __global__ void __launch_bounds__(kThreads) beam_join_kernel(const BeamArgs a) {
     const double x = e.x == kDone ? 0.0 : (double)of_key(e.x) - (double)most[beam];
     return e.x <= kNone ? -(double)INFINITY : x + cums[beam] - logs[beam];
   };
+  auto near_of = [&](uint2 e, int beam) {
+    return e.x <= kNone ? -INFINITY : (e.x == kDone ? 0.0f : of_key(e.x) - most[beam]) + cums32[beam] - logs32[beam];
+  };
   auto beam_of = [&](int list) { return quotient(list, a.by_parts); };
   // (asked for ahead of the beams' sums; neighbouring samples in different groups)
   const int sample0 = (tid & 7) * 64 + (tid >> 3);
   uint2 raw0 = make_uint2(0, 0);
   if (sample0 < samples) raw0 = mine[(sample0 % lists) * a.take + sample0 / lists];
   float cum = tid < a.beams ? a.cum[row0 + tid] : 0.0f;
-  {  // the beams' sums: eight threads a beam (fp64 is slow here: 16 cycles a warp's instruction)
+  {  // the beams' sums: eight threads a beam
     const int k = tid >> 3;
     float m = -INFINITY;
     double s = 0.0;
@@ -365,7 +385,7 @@ __global__ void __launch_bounds__(kThreads) beam_join_kernel(const BeamArgs a) {
     }
     if ((tid & 7) == 0) sums[k] = s, most[k] = all;
   }
-  if (tid == 0) count = 0;
+  if (tid == 0) count = 0, far = 0;
   __syncthreads();
   if (tid < a.beams) {
     // Beams whose logits are the same have the same sum.  What they have may differ in its
@@ -378,16 +398,18 @@ __global__ void __launch_bounds__(kThreads) beam_join_kernel(const BeamArgs a) {
     for (int b = tid - 1; b >= 0; --b)
       if (most[b] == most[tid] && fabs(sums[b] - sums[tid]) <= 0x1p-20 * sums[tid]) s = sums[b];
     const bool some = most[tid] > -INFINITY;
-    logs[tid] = some ? log(s) : 0.0;
+    logs[tid] = some ? log_of(s) : 0.0;
     cums[tid] = some ? (double)cum + 0.0 : -(double)INFINITY;
+    cums32[tid] = some ? cum : -INFINITY, logs32[tid] = (float)logs[tid];
+    if (some && cum > -INFINITY) atomicMax(&far, __float_as_uint(fabsf(cum) + logs32[tid] + 1.0f));  // (sums are 1 at least)
     if (a.lse) a.lse[row0 + tid] = some ? (float)((double)most[tid] + logs[tid]) : -INFINITY;
   }
   __syncthreads();
-  uint64_t top = sample0 < samples ? key_of(score_of(raw0, beam_of(sample0 % lists))) : kNone64;
+  uint32_t top = sample0 < samples ? key_of(near_of(raw0, beam_of(sample0 % lists))) : kNone;
   for (int i = sample0 + kThreads; i < samples; i += kThreads)
-    top = max(top, key_of(score_of(mine[(i % lists) * a.take + i / lists], beam_of(i % lists))));
+    top = max(top, key_of(near_of(mine[(i % lists) * a.take + i / lists], beam_of(i % lists))));
 #pragma unroll
-  for (int d = 1; d < 8; d <<= 1) top = max(top, (uint64_t)__shfl_xor_sync(0xffffffffu, (unsigned long long)top, d));
+  for (int d = 1; d < 8; d <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, d));
   if ((tid & 7) == 0) best[tid >> 3] = top;
   __syncthreads();
   {  // eight threads rank a maximum
@@ -397,24 +419,25 @@ __global__ void __launch_bounds__(kThreads) beam_join_kernel(const BeamArgs a) {
     for (int j = 0; j < 8; ++j) rank += best[j0 + j] > top || (best[j0 + j] == top && j0 + j < i);
 #pragma unroll
     for (int d = 1; d < 8; d <<= 1) rank += __shfl_xor_sync(0xffffffffu, rank, d);
-    if ((tid & 7) == 0 && rank == a.take - 1) bound = max(top, kNone64 + 1);
+    if ((tid & 7) == 0 && rank == a.take - 1) bound = top;
   }
   __syncthreads();
-  const uint64_t least = bound;
-  for (int c = tid; c < lists; c += kThreads) {
-    const int b = beam_of(c);
-    bool more = true;
-    for (int r0 = 0; r0 < a.take && more; r0 += 4) {
-      uint2 e[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) e[i] = r0 + i < a.take ? mine[c * a.take + r0 + i] : make_uint2(0, 0);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const uint64_t k = key_of(score_of(e[i], b));
-        if (!(more = more && k >= least)) continue;
+  // Three roundings, and those of cum's and the logarithm's: of terms that are no larger than
+  // the score, cum and the logarithm together, each 2^-24 of it; twice, for the bound's and
+  // a candidate's.
+  const float reach = of_key(bound);
+  const float least = bound <= kNone ? -INFINITY : reach - 0x1p-20f * (fabsf(reach) + __uint_as_float(far));
+  for (int i = sample0; i < samples; i += kThreads) {
+    const int c = i % lists, b = beam_of(c);
+    uint2 e = i == sample0 ? raw0 : mine[c * a.take + i / lists];
+    // the last sample of a list goes on with the rest of it
+    for (int r = i / lists; e.x > kNone && near_of(e, b) >= least; e = mine[c * a.take + r]) {
+      const uint64_t k = key_of(score_of(e, b));
+      if (k > kNone64) {
         const uint32_t p = atomicAdd(&count, 1u);
-        if (p < kList) lkey[p] = k, lplace[p] = make_uint2(b, e[i].y);
+        if (p < kList) lkey[p] = k, lplace[p] = (uint64_t)b << 32 | e.y;
       }
+      if (++r < depth || r == a.take) break;
     }
   }
   __syncthreads();
@@ -430,14 +453,11 @@ __global__ void __launch_bounds__(kThreads) beam_join_kernel(const BeamArgs a) {
   const int n = (int)count;
   if (n <= kList) {
     for (int p = tid; p < n; p += kThreads) {
-      const uint64_t k = lkey[p];
-      const uint2 e = lplace[p];
+      const uint64_t k = lkey[p], e = lplace[p];
       int rank = 0;
-      for (int q = 0; q < n; ++q) {
-        const uint2 f = lplace[q];
-        rank += lkey[q] > k || (lkey[q] == k && (f.x < e.x || (f.x == e.x && f.y < e.y)));
-      }
-      if (rank < a.take) put(rank, k, e.x, e.y);
+#pragma unroll 8
+      for (int q = 0; q < n; ++q) rank += lkey[q] > k || (lkey[q] == k && lplace[q] < e);
+      if (rank < a.take) put(rank, k, (uint32_t)(e >> 32), (uint32_t)e);
     }
     for (int r = n + tid; r < a.take; r += kThreads) none(r);
     return;

@@ -7,8 +7,7 @@
 // copies the written slots of E last pages a group, in every layer, which is bound by
 // HBM (2 x the slots' bytes) or, for a few beams, by the latency of parents -> page ids ->
 // slots; kv_table_kernel then permutes the table's columns in place, which the first
-// still reads.  Each warp works out its group's permutation by itself, by ballots: a few
-// dozen instructions, against a barrier and a pass through memory.
+// still reads.  A warp of each CTA works its group's permutation out by ballots.
 #include <algorithm>
 
 #include "kv.cuh"
@@ -23,8 +22,10 @@ struct Layer {
 };
 template <int kLayers>
 struct ReorderArgs {
-  int beams, max_pages, num_pages;
-  int runs, run_step, slot_bytes, sruns, srun_step, sslot_bytes;  // data, scales of a page
+  int beams, layers, max_pages, num_pages;
+  // a page's data in units of 16 bytes, its scales in units of 4; slots 0 .. 63 fill each run
+  // of so many of them (a kv head's codes or scales, a 16-byte chunk of its bf16 channels)
+  int units, run, sunits, srun;
   int32_t* table;
   const int32_t* parents;
   const int32_t* kv_len;
@@ -92,44 +93,68 @@ __device__ __forceinline__ bool plan_of(int g, int beams, int max_pages, const i
   return true;
 }
 
-// Runs of `bytes` bytes, `step` apart, of one page into another, by the warps of the CTA.
-template <typename V>
-__device__ __forceinline__ void copy_runs(uint8_t* dst, const uint8_t* src, int runs, int step, int bytes) {
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, n = bytes / (int)sizeof(V);
-  for (int r = warp; r < runs; r += kThreads / 32) {
-    const V* s = reinterpret_cast<const V*>(src + (int64_t)r * step);
-    V* d = reinterpret_cast<V*>(dst + (int64_t)r * step);
-#pragma unroll 4
-    for (int i = lane; i < n; i += 32) d[i] = s[i];
+// The first n of every `run` units (a power of two up to kThreads) of a page of `units`, all
+// threads, kDeep units of each on their way.
+template <typename V, int kDeep>
+__device__ __forceinline__ void copy_page(uint8_t* to, const uint8_t* from, int units, int run, int n) {
+  if ((int)(threadIdx.x & (run - 1)) >= n) return;
+  const V* src = reinterpret_cast<const V*>(from) + threadIdx.x;
+  V* dst = reinterpret_cast<V*>(to) + threadIdx.x;
+  for (int u = threadIdx.x; u < units; u += kDeep * kThreads, src += kDeep * kThreads, dst += kDeep * kThreads) {
+    V v[kDeep];
+#pragma unroll
+    for (int i = 0; i < kDeep; ++i)
+      if (u + i * kThreads < units) v[i] = src[i * kThreads];
+#pragma unroll
+    for (int i = 0; i < kDeep; ++i)
+      if (u + i * kThreads < units) dst[i * kThreads] = v[i];
   }
 }
 
-// One beam's last page in one layer: keys (blockIdx.z even) or values.
+// Some of a group's copies: job e's last page, its keys (even x) or values in layer x / 2,
+// is number e + jobs x.
 template <int kLayers>
-__global__ void __launch_bounds__(kThreads) kv_tails_kernel(const __grid_constant__ ReorderArgs<kLayers> a) {
-  griddep_wait();  // every input may be the previous kernel's output
-  const int g = blockIdx.x / a.beams, i = blockIdx.x % a.beams;
-  Plan p;
-  if (!plan_of(g, a.beams, a.max_pages, a.parents, a.kv_len, a.status, p) || p.rest == 0) return;
-  const int h = i >> 5, from = i & 31;
-  const bool extra = __shfl_sync(0xffffffffu, h ? p.extra[1] : p.extra[0], from);
-  const int parent = __shfl_sync(0xffffffffu, h ? p.parent[1] : p.parent[0], from);
-  const int tail = __shfl_sync(0xffffffffu, h ? p.tail[1] : p.tail[0], from);
-  if (!extra || parent < 0) return;
-  const int64_t row = (int64_t)g * a.beams;
-  const int src = a.table[(row + parent) * a.max_pages + p.n], dst = a.table[(row + tail) * a.max_pages + p.n];
-  if (src < 0 || src >= a.num_pages || dst < 0 || dst >= a.num_pages) {
-    if (threadIdx.x == 0) report(a.status, CSA2_ERR_BAD_PAGE);
-    return;
+__global__ void __launch_bounds__(kThreads, 3) kv_tails_kernel(const __grid_constant__ ReorderArgs<kLayers> a) {
+  __shared__ int from[kMaxBeams], to[kMaxBeams], jobs, slots;
+  griddep_wait();    // every input may be the previous kernel's output
+  griddep_launch();  // (kv_table_kernel waits for this one, and lets its own successor start at its end)
+  const int g = blockIdx.x, lane = threadIdx.x & 31;
+  if (threadIdx.x < 32) {
+    Plan p;
+    int n = 0;
+    if (plan_of(g, a.beams, a.max_pages, a.parents, a.kv_len, a.status, p) && p.rest) {
+      const int32_t* column = a.table + (int64_t)g * a.beams * a.max_pages + p.n;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        bool job = p.extra[h] && p.parent[h] >= 0;
+        int src = 0, dst = 0;
+        if (job) {
+          src = column[(int64_t)p.parent[h] * a.max_pages], dst = column[(int64_t)p.tail[h] * a.max_pages];
+          if (src < 0 || src >= a.num_pages || dst < 0 || dst >= a.num_pages) {
+            report(a.status, CSA2_ERR_BAD_PAGE);
+            job = false;
+          }
+        }
+        const uint32_t who = __ballot_sync(0xffffffffu, job);
+        const int at = n + __popc(who & ((1u << lane) - 1));
+        if (job) from[at] = src, to[at] = dst;
+        n += __popc(who);
+      }
+    }
+    if (lane == 0) jobs = n, slots = n ? p.rest : 0;
   }
-  const Layer& l = a.layer[blockIdx.y];
-  uint8_t* data = blockIdx.z ? l.v : l.k;
-  const int64_t page = (int64_t)a.runs * a.run_step;
-  copy_runs<uint4>(data + dst * page, data + src * page, a.runs, a.run_step, p.rest * a.slot_bytes);
-  if (a.sruns) {
-    uint8_t* scales = blockIdx.z ? l.vs : l.ks;
-    const int64_t spage = (int64_t)a.sruns * a.srun_step;
-    copy_runs<uint32_t>(scales + dst * spage, scales + src * spage, a.sruns, a.srun_step, p.rest * a.sslot_bytes);
+  __syncthreads();
+  const int n = jobs, rest = slots;
+  const int64_t page = (int64_t)a.units * 16, spage = (int64_t)a.sunits * 4;
+  for (int i = blockIdx.y; i < n * 2 * a.layers; i += gridDim.y) {
+    const int x = i / n, src = from[i - x * n], dst = to[i - x * n];
+    const Layer& l = a.layer[x / 2];
+    uint8_t* data = x & 1 ? l.v : l.k;
+    copy_page<uint4, 8>(data + dst * page, data + src * page, a.units, a.run, rest * a.run / kPage);
+    if (a.sunits) {
+      uint8_t* scales = x & 1 ? l.vs : l.ks;
+      copy_page<uint32_t, 4>(scales + dst * spage, scales + src * spage, a.sunits, a.srun, rest * a.srun / kPage);
+    }
   }
 }
 
@@ -168,15 +193,18 @@ cudaError_t tails_of(const csa2_kv_cfg& cfg, int layers, const csa2_kv_cache* ca
   const bool fp4 = cfg.cache_dtype == CSA2_CACHE_FP4;
   const int d = cfg.head_dim;
   ReorderArgs<kLayers> a = {};
-  a.beams = beams, a.max_pages = caches[0].max_pages, a.num_pages = caches[0].num_pages;
-  a.runs = fp4 ? cfg.kv_heads : cfg.kv_heads * (d / 8);
-  a.run_step = fp4 ? kv_block_bytes(d, true) : kPage * 16, a.slot_bytes = fp4 ? d / 2 : 16;
-  if (fp4) a.sruns = cfg.kv_heads, a.srun_step = kv_scale_bytes(d), a.sslot_bytes = d / 16;
+  a.beams = beams, a.layers = layers, a.max_pages = caches[0].max_pages, a.num_pages = caches[0].num_pages;
+  a.units = cfg.kv_heads * kv_block_bytes(d, fp4) / 16, a.run = fp4 ? kv_block_bytes(d, true) / 16 : kPage;
+  if (fp4) a.sunits = cfg.kv_heads * kv_scale_bytes(d) / 4, a.srun = kv_scale_bytes(d) / 4;
   a.table = const_cast<int32_t*>(caches[0].block_table), a.parents = parents, a.kv_len = kv_len, a.status = status;
   for (int i = 0; i < layers; ++i)
     a.layer[i] = Layer{static_cast<uint8_t*>(caches[i].k_data), static_cast<uint8_t*>(caches[i].k_scales),
                        static_cast<uint8_t*>(caches[i].v_data), static_cast<uint8_t*>(caches[i].v_scales)};
-  return launch_k(kv_tails_kernel<kLayers>, dim3(groups * beams, layers, 2), dim3(kThreads), 0, stream, 0, a);
+  // twelve CTAs an SM in all: with three, groups of 63 slots to copy end late beside groups of
+  // few (16 groups of 8 beams in 16 layers of 4 heads of 128 in bf16: 26.0 us; so 24.5)
+  const int64_t across = std::max<int64_t>(1, 12 * (int64_t)num_sms() / groups);
+  return launch_k(kv_tails_kernel<kLayers>, dim3(groups, (unsigned)std::min<int64_t>(2 * layers * beams, across)), dim3(kThreads),
+                  0, stream, 0, a);
 }
 
 }  // namespace

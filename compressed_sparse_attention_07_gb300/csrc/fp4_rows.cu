@@ -64,44 +64,71 @@ __device__ __forceinline__ void store_group(const Fp4Linear& a, int row0, int t,
   }
 }
 
-// x from bf16 to f16, in place, in the order of channels that fp4_f16 has, all threads.
-__device__ __forceinline__ void convert_x(const Fp4Linear& a, uint8_t* xs, int pitch, uint32_t* most, float* unscale) {
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, chunks = a.k / 8;
-  // a power of two of warps for each row
-  int share = 1;
-  while (2 * share * a.T <= kWarps) share *= 2;
-  for (int r = warp / share; r < a.T; r += kWarps / share) {
-    uint32_t m = 0;  // largest finite magnitude, as bf16 bits
-    for (int c = warp % share * 32 + lane; c < chunks; c += share * 32) {
-      const uint4 v = *reinterpret_cast<const uint4*>(xs + r * pitch + c * 16);
-      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+// x into shared memory as f16 in the order of channels that fp4_f16 has, zeros from channel k
+// on, all threads: a power of two of warps for each row, whose largest it takes first.
+// `then` is called once the first loads are on their way (behind the rings' copies they took
+// up to 3000 cycles more).
+template <typename Then>
+__device__ __forceinline__ void stage_x(const Fp4Linear& a, uint8_t* xs, int pitch, uint32_t* most, float* unscale, Then then) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, chunks = a.k / 8, all = a.k_blocks * 16;
+  const int share = a.T <= 1 ? 16 : a.T <= 2 ? 8 : a.T <= 4 ? 4 : a.T <= 8 ? 2 : 1;
+  const int r = warp / share, first = (warp & (share - 1)) * 32 + lane, step = share * 32;
+  uint8_t* row = xs + r * pitch;
+  const uint4* src = reinterpret_cast<const uint4*>(a.x + r * a.x_stride);
+  uint4 v[8];
+  auto load = [&](int c0) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const uint32_t lo = w[i] & 0x7FFFu, hi = w[i] >> 16 & 0x7FFFu;
-        m = max(m, max(lo < 0x7F80u ? lo : 0u, hi < 0x7F80u ? hi : 0u));
+    for (int i = 0; i < 8; ++i)
+      v[i] = r < a.T && c0 + i * step < chunks ? __ldg(src + c0 + i * step) : make_uint4(0, 0, 0, 0);
+  };
+  load(first);
+  __syncthreads();
+  then();
+  if (r < a.T) {
+    uint32_t m = 0;  // largest magnitudes, as bf16 bits, two at a time
+    for (int c0 = first; c0 < all; c0 += 8 * step) {
+      if (c0 != first) load(c0);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) m = __vmaxu2(m, w[j] & 0x7FFF7FFFu);
+        if (c0 + i * step < all) *reinterpret_cast<uint4*>(row + (c0 + i * step) * 16) = v[i];
+      }
+    }
+    m = max(m & 0xFFFFu, m >> 16);
+    if (__any_sync(0xffffffffu, m >= 0x7F80u)) {  // the largest finite one
+      m = 0;
+      for (int c = first; c < chunks; c += step) {
+        const uint4 v = *reinterpret_cast<const uint4*>(row + c * 16);
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+        for (int j = 0; j < 8; ++j) {
+          const uint32_t h = (w[j / 2] >> (j & 1 ? 16 : 0)) & 0x7FFFu;
+          if (h < 0x7F80u) m = max(m, h);
+        }
       }
     }
     m = __reduce_max_sync(0xffffffffu, m);
     if (lane == 0) atomicMax(&most[r], m);
   }
   __syncthreads();
-  for (int r = warp / share; r < a.T; r += kWarps / share) {
+  if (r < a.T) {
     // 2^e brings the largest, of exponent field f, to [2^14, 2^15)
-    const int f = (int)(most[r] >> 7);
-    const int e = most[r] ? min(14 + 127 - f, 126) : 0;
+    const uint32_t m = most[r];
+    const int e = m ? min(14 + 127 - (int)(m >> 7), 126) : 0;
+    if (first == 0) unscale[r] = __int_as_float((127 - e) << 23);
     const float scale = __int_as_float((e + 127) << 23);
-    if (warp % share == 0 && lane == 0) unscale[r] = __int_as_float((127 - e) << 23);
-    for (int c = warp % share * 32 + lane; c < chunks; c += share * 32) {
-      uint4* p = reinterpret_cast<uint4*>(xs + r * pitch + c * 16);
+    const uint64_t both = pack2(scale, scale);
+#pragma unroll 2
+    for (int c = first; c < all; c += step) {
+      uint4* p = reinterpret_cast<uint4*>(row + c * 16);
       const uint4 v = *p;
       const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-      float lo[4], hi[4];
+      float x[8];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        lo[i] = __uint_as_float(w[i] << 16) * scale;
-        hi[i] = __uint_as_float(w[i] & 0xFFFF0000u) * scale;
-      }
-      *p = make_uint4(f16x2(lo[0], lo[1]), f16x2(lo[2], lo[3]), f16x2(hi[0], hi[1]), f16x2(hi[2], hi[3]));
+      for (int i = 0; i < 4; ++i)
+        unpack2(fma2(pack2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u)), both, 0), x[2 * i], x[2 * i + 1]);
+      *p = make_uint4(f16x2(x[0], x[2]), f16x2(x[4], x[6]), f16x2(x[1], x[3]), f16x2(x[5], x[7]));
     }
   }
   __syncthreads();
@@ -112,7 +139,6 @@ template <int kGroups, int kNt>
 __global__ void __launch_bounds__(kThreads, 1) fp4_rows_kernel(const Fp4Linear a, int tiles, int slots) {
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ __align__(8) uint64_t full[kWarps][kMostSlots];
-  __shared__ __align__(8) uint64_t full_x;
   __shared__ int piece_tile[2 * kWarps];
   __shared__ uint32_t most[kFp4FewRows];
   __shared__ float unscale[kFp4FewRows];
@@ -123,15 +149,28 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_rows_kernel(const Fp4Linear a
   float4* firsts = reinterpret_cast<float4*>(smem + kWarps * slots * kUnit);  // a warp's first piece
   uint8_t* xs = reinterpret_cast<uint8_t*>(firsts + kWarps * kPiece);
 
-  const int tile0 = (int)((int64_t)blockIdx.x * tiles / gridDim.x);
-  const int units = ((int)((int64_t)(blockIdx.x + 1) * tiles / gridDim.x) - tile0) * a.k_blocks;
-  const int u0 = (int)((int64_t)warp * units / kWarps), u1 = (int)((int64_t)(warp + 1) * units / kWarps);
+  const uint32_t tile0 = blockIdx.x * tiles / gridDim.x, tile1 = (blockIdx.x + 1) * tiles / gridDim.x;  // (2^20 x SMs)
+  const uint32_t units = (tile1 - tile0) * a.k_blocks;
+  const int u0 = (int)((uint64_t)warp * units / kWarps), u1 = (int)((uint64_t)(warp + 1) * units / kWarps);
+  constexpr int kParts = kTileBlocks / kGroups;  // tiles of this kernel in 128 rows
+  auto source = [&](uint32_t tile, uint32_t kb) {
+    return a.w + ((int64_t)(tile / kParts) * a.k_blocks + kb) * kTileBytes + tile % kParts * kUnit;
+  };
+  const int first = u0 / a.k_blocks, kb0 = u0 - first * a.k_blocks;
+  if (lane < slots) tc::mbar_init(&full[warp][lane], 1);
+  tc::fence_mbar_init();
+  if (lane < 2) piece_tile[2 * warp + lane] = -1;
+  if (lane == 0) {
+    if (u0 < u1) tc::bulk_prefetch_l2(source(tile0 + first, kb0), kUnit);
+    most[warp] = 0;
+  }
+  __syncwarp();
+  griddep_wait();  // every input may be the previous kernel's output
   // the next unit to fetch: its blocks, its place in k and in the ring (no division in
   // the loop: with u / k_blocks and u % slots in it a unit took 170 instructions more)
-  const int kb0 = u0 % a.k_blocks, first = u0 / a.k_blocks;
-  constexpr int kParts = kTileBlocks / kGroups;  // tiles of this kernel in 128 rows
-  int src_tile = tile0 + first, src_kb = kb0, src_slot = 0;
-  const uint8_t* src = a.w + ((int64_t)(src_tile / kParts) * a.k_blocks + kb0) * kTileBytes + src_tile % kParts * kUnit;
+  uint32_t src_tile = tile0 + (u0 + slots) / a.k_blocks;
+  int src_kb = (u0 + slots) % a.k_blocks, src_slot = 0;
+  const uint8_t* src = source(src_tile, src_kb);
   auto fetch = [&]() {
     tc::mbar_arrive_expect_tx(&full[warp][src_slot], kUnit);
     tc::bulk_g2s(ring + src_slot * kUnit, src, kUnit, &full[warp][src_slot]);
@@ -142,32 +181,14 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_rows_kernel(const Fp4Linear a
     }
     if (++src_slot == slots) src_slot = 0;
   };
-  if (lane == 0) {
-    if (u0 < u1) tc::bulk_prefetch_l2(src, kUnit);
-    for (int s = 0; s < slots; ++s) tc::mbar_init(&full[warp][s], 1);
-    if (warp == 1) tc::mbar_init(&full_x, 1);
-    tc::fence_mbar_init();
-    piece_tile[2 * warp] = piece_tile[2 * warp + 1] = -1;
-    most[warp] = 0;
-  }
-  __syncwarp();
-  griddep_wait();  // every input may be the previous kernel's output
-  if (lane == 0) {
-    if (warp == 1) {
-      tc::mbar_arrive_expect_tx(&full_x, a.T * a.k * 2);
-      for (int r = 0; r < a.T; ++r) tc::bulk_g2s(xs + r * pitch, a.x + r * a.x_stride, a.k * 2, &full_x);
+  stage_x(a, xs, pitch, most, unscale, [&]() {
+    if (u0 + lane < u1 && lane < slots) {
+      const int u = u0 + lane, tile = u / a.k_blocks;
+      tc::mbar_arrive_expect_tx(&full[warp][lane], kUnit);
+      tc::bulk_g2s(ring + lane * kUnit, source(tile0 + tile, u - tile * a.k_blocks), kUnit, &full[warp][lane]);
     }
-    for (int u = u0; u < min(u1, u0 + slots); ++u) fetch();
-  }
-  // zeros from channel k on
-  const int pad = a.k_blocks * 16 - a.k / 8;  // 16-byte chunks
-  for (int i = tid; i < a.T * pad; i += kThreads)
-    *reinterpret_cast<uint4*>(xs + i / pad * pitch + a.k * 2 + i % pad * 16) = make_uint4(0, 0, 0, 0);
-  __syncthreads();
+  });
   bool ok = true;
-  tc::mbar_wait_or(&full_x, 0, ok);
-  __syncwarp();
-  convert_x(a, xs, pitch, most, unscale);
   // this lane's rows of x (columns from T on are dropped), its chunk of word 0
   const uint8_t* xr[kNt];
 #pragma unroll
@@ -241,7 +262,6 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_rows_kernel(const Fp4Linear a
     report(a.status, CSA2_ERR_TIMEOUT);
     // nothing may land in shared memory after the CTA has left
     for (int u = max(u0, u1 - slots); u < u1; ++u) tc::mbar_wait(&full[warp][(u - u0) % slots], ((u - u0) / slots) & 1);
-    tc::mbar_wait(&full_x, 0);
   }
   __syncthreads();
   // a shared tile's pieces stand in the order of its channels, two places a warp, a place
@@ -287,10 +307,12 @@ cudaError_t launch_of(const Fp4Linear& a, const Shape& s, cudaStream_t stream) {
 bool fp4_rows_ok(const Fp4Linear& a) { return a.T <= kFp4FewRows && shape_of(a, 1).slots != 0; }
 
 cudaError_t launch_fp4_rows(const Fp4Linear& a, cudaStream_t stream) {
-  // 32 rows a tile, which halve x's way through shared memory, where the SMs have
-  // several each and the rings stay deep
+  // 32 rows a tile, which halve x's way through shared memory and what a unit costs beside
+  // its products, where the rings stay deep and the SM with the most tiles has less of
+  // them: a unit of 32 rows takes 1.5 times one of 16
   const Shape two = shape_of(a, 2);
-  const bool wide = a.n >= 32 * 8 * num_sms() && two.slots >= 3;
+  const int sms = num_sms(), tiles1 = (a.n + 15) / 16, tiles2 = (a.n + 31) / 32;
+  const bool wide = two.slots >= 3 && 3 * ((tiles2 + sms - 1) / sms) <= 2 * ((tiles1 + sms - 1) / sms);
   if (a.T <= 8) return wide ? launch_of<2, 1>(a, two, stream) : launch_of<1, 1>(a, shape_of(a, 1), stream);
   return wide ? launch_of<2, 2>(a, two, stream) : launch_of<1, 2>(a, shape_of(a, 1), stream);
 }

@@ -68,17 +68,17 @@ __device__ __forceinline__ void store_group(const Fp4Linear& a, int row0, int t,
 // on, all threads: a power of two of warps for each row, whose largest it takes first.
 // `then` is called once the first loads are on their way (behind the rings' copies they took
 // up to 3000 cycles more).
-template <typename Then>
+template <int kBatch, typename Then>
 __device__ __forceinline__ void stage_x(const Fp4Linear& a, uint8_t* xs, int pitch, uint32_t* most, float* unscale, Then then) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, chunks = a.k / 8, all = a.k_blocks * 16;
   const int share = a.T <= 1 ? 16 : a.T <= 2 ? 8 : a.T <= 4 ? 4 : a.T <= 8 ? 2 : 1;
   const int r = warp / share, first = (warp & (share - 1)) * 32 + lane, step = share * 32;
   uint8_t* row = xs + r * pitch;
   const uint4* src = reinterpret_cast<const uint4*>(a.x + r * a.x_stride);
-  uint4 v[8];
+  uint4 v[kBatch];
   auto load = [&](int c0) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
+    for (int i = 0; i < kBatch; ++i)
       v[i] = r < a.T && c0 + i * step < chunks ? __ldg(src + c0 + i * step) : make_uint4(0, 0, 0, 0);
   };
   load(first);
@@ -86,10 +86,10 @@ __device__ __forceinline__ void stage_x(const Fp4Linear& a, uint8_t* xs, int pit
   then();
   if (r < a.T) {
     uint32_t m = 0;  // largest magnitudes, as bf16 bits, two at a time
-    for (int c0 = first; c0 < all; c0 += 8 * step) {
+    for (int c0 = first; c0 < all; c0 += kBatch * step) {
       if (c0 != first) load(c0);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
+      for (int i = 0; i < kBatch; ++i) {
         const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
 #pragma unroll
         for (int j = 0; j < 4; ++j) m = __vmaxu2(m, w[j] & 0x7FFF7FFFu);
@@ -181,7 +181,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_rows_kernel(const Fp4Linear a
     }
     if (++src_slot == slots) src_slot = 0;
   };
-  stage_x(a, xs, pitch, most, unscale, [&]() {
+  stage_x<8 * kNt>(a, xs, pitch, most, unscale, [&]() {
     if (u0 + lane < u1 && lane < slots) {
       const int u = u0 + lane, tile = u / a.k_blocks;
       tc::mbar_arrive_expect_tx(&full[warp][lane], kUnit);

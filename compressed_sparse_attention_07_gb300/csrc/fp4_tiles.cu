@@ -4,7 +4,7 @@
 // D[128][rows of x] = W x^T accumulates in tensor memory over steps of 128 channels.  A
 // step's packed weights (9 KB) come by one bulk copy, its rows of x by two tensor copies
 // (64 channels each, 128-byte swizzle; rows and channels outside are zeros); four
-// sets of four warps, a step each, decode the weights, a row a lane, into tensor memory,
+// or six sets of four warps, a step each, decode the weights, a row a lane, into tensor memory,
 // from where the products take their left operand; one warp issues the eight products of
 // 128 x rows x 16.  Few rows are bound by the weights' bytes and their decoding, many by
 // the products (256 rows: 1024 cycles a step) and shared memory beside them: x goes in and
@@ -23,22 +23,23 @@
 namespace csa2 {
 namespace {
 
-constexpr int kSets = 4, kDecoders = 4 * kSets, kWarps = 8 + kDecoders, kThreads = 32 * kWarps;
 constexpr int kSmemMost = 227 * 1024 - 1024;
 
 // Places of the rings for kTok rows of x: kS steps of decoded weights in tensor memory,
 // 64 columns each beside kD accumulators; kX places of kBoxes boxes of x; kP packed steps.
-// Four decoding warps, a set, have every kSets-th step, so a set does not see every phase
+// Four decoding warps, a set, have every kSets-th step (six sets where registers and columns
+// allow: 40 rows of 4096 -> 10240 take 19.5 us with four), so a set does not see every phase
 // of every place, and must not take the phase before the last (of the same parity) for
 // the last.  Packed steps may land out of order: with kP a multiple of kSets a set sees
 // every phase of its own places.  Decoded steps become free in order: a set that passed
 // step n - kSets knows step n - kSets - kS to be free, hence step n - 2 kS if kS >= kSets.
 template <int kTok>
 struct Rings {
+  static constexpr int kSets = kTok >= 128 ? 4 : 6, kThreads = 32 * (8 + 4 * kSets);
   static constexpr int kD = kTok == 256 ? 1 : 2, kS = kTok >= 128 ? 4 : 6;
   static constexpr int kBoxes = kTok == 256 ? 1 : 2, kX = kTok == 256 ? 5 : kTok == 128 ? 4 : 6;
   static constexpr int kBoxBytes = kTok * 128, kXBytes = kBoxes * kBoxBytes;
-  static constexpr int kP = kTok == 256 ? 4 : kTok == 128 ? 8 : kTok == 64 ? 12 : kTok == 32 ? 16 : 20;
+  static constexpr int kP = kTok == 256 ? 4 : kTok == 128 ? 8 : kTok == 64 ? 12 : 18;
   static constexpr int kSmem = 1024 + kX * kXBytes + kP * kTileBytes;
   static constexpr int kA = kD * kTok;  // first column of the decoded weights
   static constexpr int kCols = 512;
@@ -93,7 +94,7 @@ struct Number {
 __device__ __forceinline__ uint32_t uniform(uint32_t v) { return __reduce_max_sync(0xffffffffu, v); }
 
 template <int kTok>
-__global__ void __launch_bounds__(kThreads, 1) fp4_tiles_kernel(const __grid_constant__ CUtensorMap map, const TileArgs a) {
+__global__ void __launch_bounds__(Rings<kTok>::kThreads, 1) fp4_tiles_kernel(const __grid_constant__ CUtensorMap map, const TileArgs a) {
   using R = Rings<kTok>;
   extern __shared__ uint8_t raw[];
   uint8_t* smem = raw + ((1024 - (tc::smem_u32(raw) & 1023)) & 1023);
@@ -132,74 +133,71 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_tiles_kernel(const __grid_con
   bool ok = true;
 
   if (warp == 0) {  // packed weights
-    int n = 0;
-    Place<R::kP> at;
-    for (int tile = first; tile < a.tiles && ok; tile += stride) {
-      const uint8_t* src = weights(tile) + (int64_t)s0 * kTileBytes;
-      const int bytes = blocks(tile) * kBlockBytes;
-      for (int step = s0; step < s1; ++step, ++n, at.next(), src += kTileBytes) {
-        if (n >= R::kP) tc::mbar_wait_or(&empty_p[at.s], at.phase ^ 1, ok);
-        if (!__all_sync(0xffffffffu, ok)) break;
-        if (tc::elect_one()) {
+    if (tc::elect_one()) {
+      int n = 0;
+      Place<R::kP> at;
+      for (int tile = first; tile < a.tiles && ok; tile += stride) {
+        const uint8_t* src = weights(tile) + (int64_t)s0 * kTileBytes;
+        const int bytes = blocks(tile) * kBlockBytes;
+        for (int step = s0; step < s1; ++step, ++n, at.next(), src += kTileBytes) {
+          if (n >= R::kP) tc::mbar_wait_or(&empty_p[at.s], at.phase ^ 1, ok);
+          if (!ok) break;
           tc::mbar_arrive_expect_tx(&full_p[at.s], bytes);
           tc::bulk_g2s(ps + at.s * kTileBytes, src, bytes, &full_p[at.s]);
         }
       }
+      // nothing may land in shared memory after the CTA has left
+      for (int i = max(0, n - R::kP); i < n && tc::mbar_wait(&full_p[i % R::kP], (i / R::kP) & 1); ++i) {}
     }
-    // nothing may land in shared memory after the CTA has left
-    for (int i = max(0, n - R::kP); i < n && tc::mbar_wait(&full_p[i % R::kP], (i / R::kP) & 1); ++i) {}
   } else if (warp == 1) {  // rows of x
-    int n = 0;
-    Place<R::kX> at;
-    for (int tile = first; tile < a.tiles && ok; tile += stride) {
-      const int row = tile / a.row_tiles * kTok;
-      for (int box = 2 * s0; box < 2 * s1; box += R::kBoxes, ++n, at.next()) {
-        if (n >= R::kX) tc::mbar_wait_or(&empty_x[at.s], at.phase ^ 1, ok);
-        if (!__all_sync(0xffffffffu, ok)) break;
-        if (tc::elect_one()) {
+    if (tc::elect_one()) {
+      int n = 0;
+      Place<R::kX> at;
+      for (int tile = first; tile < a.tiles && ok; tile += stride) {
+        const int row = tile / a.row_tiles * kTok;
+        for (int box = 2 * s0; box < 2 * s1; box += R::kBoxes, ++n, at.next()) {
+          if (n >= R::kX) tc::mbar_wait_or(&empty_x[at.s], at.phase ^ 1, ok);
+          if (!ok) break;
           tc::mbar_arrive_expect_tx(&full_x[at.s], R::kXBytes);
 #pragma unroll
           for (int i = 0; i < R::kBoxes; ++i)
             tensor_g2s(tc::smem_u32(xs + at.s * R::kXBytes + i * R::kBoxBytes), &map, (box + i) * 64, row, &full_x[at.s]);
         }
       }
+      for (int i = max(0, n - R::kX); i < n && tc::mbar_wait(&full_x[i % R::kX], (i / R::kX) & 1); ++i) {}
     }
-    for (int i = max(0, n - R::kX); i < n && tc::mbar_wait(&full_x[i % R::kX], (i / R::kX) & 1); ++i) {}
   } else if (warp == 2) {  // products
     constexpr uint32_t kIdesc = tc::idesc_f16(kTileRows, kTok, true, true, false, false);
     constexpr uint32_t kHi = tc::sdesc_hi(1024) | 2u << 29;  // 128-byte swizzle
-    const uint32_t x_lo = tc::sdesc_lo(tc::smem_u32(xs), 16);
-    Place<R::kX> px;
-    Place<R::kS> pa;
-    Place<R::kD> pd;
-    int it = 0;
-    for (int tile = first; tile < a.tiles; tile += stride, ++it, pd.next()) {
-      if (it >= R::kD) tc::mbar_wait_or(&empty_d[pd.s], pd.phase ^ 1, ok);
-      for (int step = s0; step < s1; ++step, pa.next()) {
-        tc::mbar_wait_or(&full_a[pa.s], pa.phase, ok);
-        // (issued from registers that are known to be uniform: tc.cuh)
-        const uint32_t d = uniform(tmem + pd.s * kTok), w = uniform(tmem + R::kA + 64 * pa.s);
+    const uint32_t tb = uniform(tmem), x_lo = uniform(tc::sdesc_lo(tc::smem_u32(xs), 16));
+    if (tc::elect_one()) {  // one thread for all of it: with a vote and an election a step took 900 cycles
+      Place<R::kX> px;
+      Place<R::kS> pa;
+      Place<R::kD> pd;
+      int it = 0;
+      for (int tile = first; tile < a.tiles; tile += stride, ++it, pd.next()) {
+        if (it >= R::kD) tc::mbar_wait_or(&empty_d[pd.s], pd.phase ^ 1, ok);
+        for (int step = s0; step < s1; ++step, pa.next()) {
+          tc::mbar_wait_or(&full_a[pa.s], pa.phase, ok);
+          const uint32_t d = tb + pd.s * kTok, w = tb + R::kA + 64 * pa.s;
 #pragma unroll
-        for (int half = 0; half < 2 / R::kBoxes; ++half, px.next()) {
-          tc::mbar_wait_or(&full_x[px.s], px.phase, ok);
-          const uint32_t x = uniform(x_lo + px.s * (R::kXBytes / 16));
-          tc::fence_after_sync();
-          if (tc::elect_one()) {
+          for (int half = 0; half < 2 / R::kBoxes; ++half, px.next()) {
+            tc::mbar_wait_or(&full_x[px.s], px.phase, ok);
+            const uint32_t x = x_lo + px.s * (R::kXBytes / 16);
+            tc::fence_after_sync();
 #pragma unroll
             for (int k = 0; k < 4 * R::kBoxes; ++k)
               tc::mma_ts_lo(d, w + 8 * (4 * half + k), x + (k / 4) * (R::kBoxBytes / 16) + (k % 4) * 2, kHi, kIdesc,
                             half > 0 || k > 0 || step > s0);
             tc::mma_commit(&empty_x[px.s]);
-            if (half + 1 == 2 / R::kBoxes) tc::mma_commit(&empty_a[pa.s]);
-            if (half + 1 == 2 / R::kBoxes && step + 1 == s1) tc::mma_commit(&full_d[pd.s]);
           }
-          __syncwarp();
+          tc::mma_commit(&empty_a[pa.s]);
         }
+        tc::mma_commit(&full_d[pd.s]);
       }
+      tc::mma_commit(&drained);
+      tc::mbar_wait(&drained, 0);
     }
-    if (tc::elect_one()) tc::mma_commit(&drained);
-    __syncwarp();
-    tc::mbar_wait(&drained, 0);
   } else if (warp >= 8) {  // decoding
     const int set = (warp - 8) >> 2, q = warp & 3, r = lane & 15;  // rows 32 q .. of every kSets-th step
     const uint8_t* const src = ps + (2 * q + (lane >> 4)) * kBlockBytes;
@@ -208,7 +206,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_tiles_kernel(const __grid_con
     const int mine = first < a.tiles ? ((a.tiles - 1 - first) / stride + 1) * steps : 0;  // of all tiles
     int p = set % R::kP, s = set % R::kS;
     uint32_t p_phase = 0, s_phase = set / R::kS & 1;
-    for (int n = set; n < mine; n += kSets) {
+    for (int n = set; n < mine; n += R::kSets) {
       tc::mbar_wait_or(&full_p[p], p_phase, ok);
       __syncwarp();
       const uint8_t* b = src + p * kTileBytes;
@@ -232,14 +230,15 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_tiles_kernel(const __grid_con
           for (int j = 0; j < 4; ++j) c[(i ^ t()) * 4 + j] = v[j];
         }
       };
-      // two units ahead of the wait, so that a place is not held while they are decoded
+      // a unit or two ahead of the wait, so that a place is not held while they are decoded
       uint32_t c0[16], c1[16];
       decode(Number<0>(), c0);
-      decode(Number<1>(), c1);
+      if constexpr (R::kSets == 4) decode(Number<1>(), c1);
       if (n >= R::kS) tc::mbar_wait_or(&empty_a[s], s_phase ^ 1, ok);
       __syncwarp();
       tc::fence_after_sync();
       tc::tmem_st16(dst, c0);
+      if constexpr (R::kSets != 4) decode(Number<1>(), c1);
       tc::tmem_st16(dst + 16, c1);
       decode(Number<2>(), c0);
       tc::tmem_st16(dst + 32, c0);
@@ -249,8 +248,8 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_tiles_kernel(const __grid_con
       tc::fence_before_sync();
       __syncwarp();
       if (lane == 0) tc::mbar_arrive(&full_a[s]);
-      if ((p += kSets) >= R::kP) p -= R::kP, p_phase ^= 1;
-      if ((s += kSets) >= R::kS) s -= R::kS, s_phase ^= 1;
+      if ((p += R::kSets) >= R::kP) p -= R::kP, p_phase ^= 1;
+      if ((s += R::kSets) >= R::kS) s -= R::kS, s_phase ^= 1;
     }
   } else if (warp >= 4) {  // sums out: a lane has a row of W
     const int lane0 = 32 * (warp & 3);
@@ -293,7 +292,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_tiles_kernel(const __grid_con
     // this CTA's share of the tile's rows of x
     const int t0 = first / a.row_tiles * kTok, i = first % a.row_tiles * kTileRows + tid % kTileRows;
     const uint32_t mine = tc::smem_u32(xs);
-    for (int t = rank + a.split * (tid / kTileRows); t < kTok && t0 + t < a.l.T; t += a.split * (kThreads / kTileRows)) {
+    for (int t = rank + a.split * (tid / kTileRows); t < kTok && t0 + t < a.l.T; t += a.split * (R::kThreads / kTileRows)) {
       const uint32_t at = mine + (t * kTileRows + tid % kTileRows) * 4;
       float sum = 0.0f;
       for (int r = 0; r < a.split; ++r) sum += tc::ld_dsmem(tc::map_rank(at, r));
@@ -344,7 +343,7 @@ cudaError_t launch_of(const Fp4Linear& l, cudaStream_t stream) {
   const int sms = num_sms();
   if (2 * tiles <= sms) a.split = (int)std::max<int64_t>(1, std::min<int64_t>({8, sms / tiles, l.k_blocks}));
   const int ctas = a.split > 1 ? a.tiles * a.split : std::min(a.tiles, sms);
-  return launch_k(kern, dim3(ctas), dim3(kThreads), R::kSmem, stream, a.split > 1 ? a.split : 0, map, a);
+  return launch_k(kern, dim3(ctas), dim3(R::kThreads), R::kSmem, stream, a.split > 1 ? a.split : 0, map, a);
 }
 
 }  // namespace

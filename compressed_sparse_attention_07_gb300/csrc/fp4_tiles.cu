@@ -132,72 +132,79 @@ __global__ void __launch_bounds__(Rings<kTok>::kThreads, 1) fp4_tiles_kernel(con
   // addresses stay inside the rings), but starts no copy, and reports.
   bool ok = true;
 
+  // (Warps that issue copies or products stay together, and one lane issues: where an elected
+  // thread ran the whole loop, calls of several tiles a CTA ended in illegal accesses.)
   if (warp == 0) {  // packed weights
-    if (tc::elect_one()) {
-      int n = 0;
-      Place<R::kP> at;
-      for (int tile = first; tile < a.tiles && ok; tile += stride) {
-        const uint8_t* src = weights(tile) + (int64_t)s0 * kTileBytes;
-        const int bytes = blocks(tile) * kBlockBytes;
-        for (int step = s0; step < s1; ++step, ++n, at.next(), src += kTileBytes) {
-          if (n >= R::kP) tc::mbar_wait_or(&empty_p[at.s], at.phase ^ 1, ok);
-          if (!ok) break;
+    int n = 0;
+    Place<R::kP> at;
+    for (int tile = first; tile < a.tiles && ok; tile += stride) {
+      const uint8_t* src = weights(tile) + (int64_t)s0 * kTileBytes;
+      const int bytes = blocks(tile) * kBlockBytes;
+      for (int step = s0; step < s1; ++step, ++n, at.next(), src += kTileBytes) {
+        if (n >= R::kP) tc::mbar_wait_or(&empty_p[at.s], at.phase ^ 1, ok);
+        if (!__all_sync(0xffffffffu, ok)) break;
+        if (tc::elect_one()) {
           tc::mbar_arrive_expect_tx(&full_p[at.s], bytes);
           tc::bulk_g2s(ps + at.s * kTileBytes, src, bytes, &full_p[at.s]);
         }
+        __syncwarp();
       }
-      // nothing may land in shared memory after the CTA has left
-      for (int i = max(0, n - R::kP); i < n && tc::mbar_wait(&full_p[i % R::kP], (i / R::kP) & 1); ++i) {}
     }
+    // nothing may land in shared memory after the CTA has left
+    for (int i = max(0, n - R::kP); i < n && tc::mbar_wait(&full_p[i % R::kP], (i / R::kP) & 1); ++i) {}
   } else if (warp == 1) {  // rows of x
-    if (tc::elect_one()) {
-      int n = 0;
-      Place<R::kX> at;
-      for (int tile = first; tile < a.tiles && ok; tile += stride) {
-        const int row = tile / a.row_tiles * kTok;
-        for (int box = 2 * s0; box < 2 * s1; box += R::kBoxes, ++n, at.next()) {
-          if (n >= R::kX) tc::mbar_wait_or(&empty_x[at.s], at.phase ^ 1, ok);
-          if (!ok) break;
+    int n = 0;
+    Place<R::kX> at;
+    for (int tile = first; tile < a.tiles && ok; tile += stride) {
+      const int row = tile / a.row_tiles * kTok;
+      for (int box = 2 * s0; box < 2 * s1; box += R::kBoxes, ++n, at.next()) {
+        if (n >= R::kX) tc::mbar_wait_or(&empty_x[at.s], at.phase ^ 1, ok);
+        if (!__all_sync(0xffffffffu, ok)) break;
+        if (tc::elect_one()) {
           tc::mbar_arrive_expect_tx(&full_x[at.s], R::kXBytes);
 #pragma unroll
           for (int i = 0; i < R::kBoxes; ++i)
             tensor_g2s(tc::smem_u32(xs + at.s * R::kXBytes + i * R::kBoxBytes), &map, (box + i) * 64, row, &full_x[at.s]);
         }
+        __syncwarp();
       }
-      for (int i = max(0, n - R::kX); i < n && tc::mbar_wait(&full_x[i % R::kX], (i / R::kX) & 1); ++i) {}
     }
+    for (int i = max(0, n - R::kX); i < n && tc::mbar_wait(&full_x[i % R::kX], (i / R::kX) & 1); ++i) {}
   } else if (warp == 2) {  // products
     constexpr uint32_t kIdesc = tc::idesc_f16(kTileRows, kTok, true, true, false, false);
     constexpr uint32_t kHi = tc::sdesc_hi(1024) | 2u << 29;  // 128-byte swizzle
     const uint32_t tb = uniform(tmem), x_lo = uniform(tc::sdesc_lo(tc::smem_u32(xs), 16));
-    if (tc::elect_one()) {  // one thread for all of it: with a vote and an election a step took 900 cycles
-      Place<R::kX> px;
-      Place<R::kS> pa;
-      Place<R::kD> pd;
-      int it = 0;
-      for (int tile = first; tile < a.tiles; tile += stride, ++it, pd.next()) {
-        if (it >= R::kD) tc::mbar_wait_or(&empty_d[pd.s], pd.phase ^ 1, ok);
-        for (int step = s0; step < s1; ++step, pa.next()) {
-          tc::mbar_wait_or(&full_a[pa.s], pa.phase, ok);
-          const uint32_t d = tb + pd.s * kTok, w = tb + R::kA + 64 * pa.s;
+    Place<R::kS> pa;
+    Place<R::kX> px;
+    Place<R::kD> pd;
+    int it = 0;
+    for (int tile = first; tile < a.tiles; tile += stride, ++it, pd.next()) {
+      if (it >= R::kD) tc::mbar_wait_or(&empty_d[pd.s], pd.phase ^ 1, ok);
+      for (int step = s0; step < s1; ++step, pa.next()) {
+        tc::mbar_wait_or(&full_a[pa.s], pa.phase, ok);
 #pragma unroll
-          for (int half = 0; half < 2 / R::kBoxes; ++half, px.next()) {
-            tc::mbar_wait_or(&full_x[px.s], px.phase, ok);
-            const uint32_t x = x_lo + px.s * (R::kXBytes / 16);
-            tc::fence_after_sync();
+        for (int half = 0; half < 2 / R::kBoxes; ++half, px.next()) {
+          tc::mbar_wait_or(&full_x[px.s], px.phase, ok);
+          __syncwarp();
+          tc::fence_after_sync();
+          if (tc::elect_one()) {
 #pragma unroll
             for (int k = 0; k < 4 * R::kBoxes; ++k)
-              tc::mma_ts_lo(d, w + 8 * (4 * half + k), x + (k / 4) * (R::kBoxBytes / 16) + (k % 4) * 2, kHi, kIdesc,
+              tc::mma_ts_lo(tb + pd.s * kTok, tb + R::kA + 64 * pa.s + 8 * (4 * half + k),
+                            x_lo + px.s * (R::kXBytes / 16) + (k / 4) * (R::kBoxBytes / 16) + (k % 4) * 2, kHi, kIdesc,
                             half > 0 || k > 0 || step > s0);
             tc::mma_commit(&empty_x[px.s]);
+            if (half + 1 == 2 / R::kBoxes) tc::mma_commit(&empty_a[pa.s]);
           }
-          tc::mma_commit(&empty_a[pa.s]);
+          __syncwarp();
         }
-        tc::mma_commit(&full_d[pd.s]);
       }
-      tc::mma_commit(&drained);
-      tc::mbar_wait(&drained, 0);
+      if (tc::elect_one()) tc::mma_commit(&full_d[pd.s]);
+      __syncwarp();
     }
+    if (tc::elect_one()) tc::mma_commit(&drained);
+    __syncwarp();
+    tc::mbar_wait(&drained, 0);
   } else if (warp >= 8) {  // decoding
     const int set = (warp - 8) >> 2, q = warp & 3, r = lane & 15;  // rows 32 q .. of every kSets-th step
     const uint8_t* const src = ps + (2 * q + (lane >> 4)) * kBlockBytes;
@@ -265,6 +272,7 @@ __global__ void __launch_bounds__(Rings<kTok>::kThreads, 1) fp4_tiles_kernel(con
 #pragma unroll 1
       for (int c = 0; c < kTok; c += kCols) {
         uint32_t v[kCols];
+        __syncwarp();
         if constexpr (kCols == 32) tc::tmem_ld32(tc::taddr(tmem, lane0, at.s * kTok + c), v);
         else tc::tmem_ld16(tc::taddr(tmem, lane0, at.s * kTok + c), v);
         tc::tmem_wait_ld();
@@ -278,6 +286,7 @@ __global__ void __launch_bounds__(Rings<kTok>::kThreads, 1) fp4_tiles_kernel(con
           else store_columns(static_cast<__nv_bfloat16*>(a.l.out) + at0, v, most, a.l, bias);
         }
       }
+      __syncwarp();
       tc::fence_before_sync();
       __syncwarp();
       if (lane == 0) tc::mbar_arrive(&empty_d[at.s]);

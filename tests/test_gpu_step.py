@@ -39,7 +39,10 @@ LINEAR = [(1, 128, 16), (1, 16, 1), (2, 48, 17), (3, 1280, 130), (5, 4096, 200),
           (12, 128, 2450), (16, 4096, 33), (16, 16, 257), (17, 128, 128), (17, 16, 1), (31, 400, 300), (32, 4096, 17),
           (33, 1040, 640), (64, 128, 129), (65, 272, 500), (100, 4096, 128), (128, 144, 1100), (129, 64, 96), (200, 1296, 257),
           (256, 128, 128), (257, 144, 130), (300, 2064, 700), (513, 32, 20000), (1, 70000, 20), (8, 9000 // 16 * 16, 40),
-          (16, 20000, 36), (20, 33008, 130)]
+          (16, 20000, 36), (20, 33008, 130),
+          # several tiles a CTA, for each number of rows that a tile takes
+          (11, 70000, 300), (20, 128, 41000), (24, 400, 39001), (50, 272, 58000), (64, 528, 40000), (100, 144, 45000),
+          (128, 656, 39000), (150, 272, 40001), (1500, 400, 4000)]
 
 
 @pytest.mark.parametrize("f32", [False, True])

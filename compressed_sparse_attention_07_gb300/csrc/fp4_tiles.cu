@@ -38,12 +38,14 @@ struct Rings {
   static constexpr int kSets = kTok >= 128 ? 4 : 6, kThreads = 32 * (8 + 4 * kSets);
   static constexpr int kD = kTok == 256 ? 1 : 2, kS = kTok >= 128 ? 4 : 6;
   static constexpr int kBoxes = kTok == 256 ? 1 : 2, kX = kTok == 256 ? 5 : kTok == 128 ? 4 : 6;
+  // a step's decoded weights and rows of x come and go by the same barriers: full_a, empty_a
+  static constexpr bool kJoint = kTok < 256;
   static constexpr int kBoxBytes = kTok * 128, kXBytes = kBoxes * kBoxBytes;
   static constexpr int kP = kTok == 256 ? 4 : kTok == 128 ? 8 : kTok == 64 ? 12 : 18;
   static constexpr int kSmem = 1024 + kX * kXBytes + kP * kTileBytes;
   static constexpr int kA = kD * kTok;  // first column of the decoded weights
   static constexpr int kCols = 512;
-  static_assert(kP % kSets == 0 && kS >= kSets && kA + 64 * kS <= kCols && kSmem <= kSmemMost &&
+  static_assert((!kJoint || kX == kS) && kP % kSets == 0 && kS >= kSets && kA + 64 * kS <= kCols && kSmem <= kSmemMost &&
                     kX * kXBytes >= kTok * kTileRows * 4, "");
 };
 
@@ -106,7 +108,7 @@ __global__ void __launch_bounds__(Rings<kTok>::kThreads, 1) fp4_tiles_kernel(con
   if (tid == 0) {
     for (int i = 0; i < R::kP; ++i) tc::mbar_init(&full_p[i], 1), tc::mbar_init(&empty_p[i], 4);
     for (int i = 0; i < R::kX; ++i) tc::mbar_init(&full_x[i], 1), tc::mbar_init(&empty_x[i], 1);
-    for (int i = 0; i < R::kS; ++i) tc::mbar_init(&full_a[i], 4), tc::mbar_init(&empty_a[i], 1);
+    for (int i = 0; i < R::kS; ++i) tc::mbar_init(&full_a[i], R::kJoint ? 5 : 4), tc::mbar_init(&empty_a[i], 1);
     for (int i = 0; i < R::kD; ++i) tc::mbar_init(&full_d[i], 1), tc::mbar_init(&empty_d[i], 4);
     tc::mbar_init(&drained, 1);
     tc::fence_mbar_init();
@@ -155,21 +157,22 @@ __global__ void __launch_bounds__(Rings<kTok>::kThreads, 1) fp4_tiles_kernel(con
   } else if (warp == 1) {  // rows of x
     int n = 0;
     Place<R::kX> at;
+    uint64_t *const full = R::kJoint ? full_a : full_x, *const empty = R::kJoint ? empty_a : empty_x;
     for (int tile = first; tile < a.tiles && ok; tile += stride) {
       const int row = tile / a.row_tiles * kTok;
       for (int box = 2 * s0; box < 2 * s1; box += R::kBoxes, ++n, at.next()) {
-        if (n >= R::kX) tc::mbar_wait_or(&empty_x[at.s], at.phase ^ 1, ok);
+        if (n >= R::kX) tc::mbar_wait_or(&empty[at.s], at.phase ^ 1, ok);
         if (!__all_sync(0xffffffffu, ok)) break;
         if (tc::elect_one()) {
-          tc::mbar_arrive_expect_tx(&full_x[at.s], R::kXBytes);
+          tc::mbar_arrive_expect_tx(&full[at.s], R::kXBytes);
 #pragma unroll
           for (int i = 0; i < R::kBoxes; ++i)
-            tensor_g2s(tc::smem_u32(xs + at.s * R::kXBytes + i * R::kBoxBytes), &map, (box + i) * 64, row, &full_x[at.s]);
+            tensor_g2s(tc::smem_u32(xs + at.s * R::kXBytes + i * R::kBoxBytes), &map, (box + i) * 64, row, &full[at.s]);
         }
         __syncwarp();
       }
     }
-    for (int i = max(0, n - R::kX); i < n && tc::mbar_wait(&full_x[i % R::kX], (i / R::kX) & 1); ++i) {}
+    for (int i = max(0, n - R::kX); i < n && tc::mbar_wait(&full[i % R::kX], (i / R::kX) & 1); ++i) {}
   } else if (warp == 2) {  // products
     constexpr uint32_t kIdesc = tc::idesc_f16(kTileRows, kTok, true, true, false, false);
     constexpr uint32_t kHi = tc::sdesc_hi(1024) | 2u << 29;  // 128-byte swizzle
@@ -184,7 +187,7 @@ __global__ void __launch_bounds__(Rings<kTok>::kThreads, 1) fp4_tiles_kernel(con
         tc::mbar_wait_or(&full_a[pa.s], pa.phase, ok);
 #pragma unroll
         for (int half = 0; half < 2 / R::kBoxes; ++half, px.next()) {
-          tc::mbar_wait_or(&full_x[px.s], px.phase, ok);
+          if (!R::kJoint) tc::mbar_wait_or(&full_x[px.s], px.phase, ok);
           __syncwarp();
           tc::fence_after_sync();
           if (tc::elect_one()) {
@@ -193,7 +196,7 @@ __global__ void __launch_bounds__(Rings<kTok>::kThreads, 1) fp4_tiles_kernel(con
               tc::mma_ts_lo(tb + pd.s * kTok, tb + R::kA + 64 * pa.s + 8 * (4 * half + k),
                             x_lo + px.s * (R::kXBytes / 16) + (k / 4) * (R::kBoxBytes / 16) + (k % 4) * 2, kHi, kIdesc,
                             half > 0 || k > 0 || step > s0);
-            tc::mma_commit(&empty_x[px.s]);
+            if (!R::kJoint) tc::mma_commit(&empty_x[px.s]);
             if (half + 1 == 2 / R::kBoxes) tc::mma_commit(&empty_a[pa.s]);
           }
           __syncwarp();

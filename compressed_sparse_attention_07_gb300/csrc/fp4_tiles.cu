@@ -183,23 +183,55 @@ __global__ void __launch_bounds__(Rings<kTok>::kThreads, 1) fp4_tiles_kernel(con
     int it = 0;
     for (int tile = first; tile < a.tiles; tile += stride, ++it, pd.next()) {
       if (it >= R::kD) tc::mbar_wait_or(&empty_d[pd.s], pd.phase ^ 1, ok);
-      for (int step = s0; step < s1; ++step, pa.next()) {
-        tc::mbar_wait_or(&full_a[pa.s], pa.phase, ok);
-#pragma unroll
-        for (int half = 0; half < 2 / R::kBoxes; ++half, px.next()) {
-          if (!R::kJoint) tc::mbar_wait_or(&full_x[px.s], px.phase, ok);
+      if constexpr (R::kJoint) {
+        // two steps at a time where there are two
+        for (int step = s0; step < s1; step += 2) {
+          const bool two = step + 1 < s1;
+          const int s = pa.s;
+          tc::mbar_wait_or(&full_a[s], pa.phase, ok);
+          pa.next();
+          const int s2 = pa.s;
+          if (two) {
+            tc::mbar_wait_or(&full_a[s2], pa.phase, ok);
+            pa.next();
+          }
           __syncwarp();
           tc::fence_after_sync();
           if (tc::elect_one()) {
 #pragma unroll
-            for (int k = 0; k < 4 * R::kBoxes; ++k)
-              tc::mma_ts_lo(tb + pd.s * kTok, tb + R::kA + 64 * pa.s + 8 * (4 * half + k),
-                            x_lo + px.s * (R::kXBytes / 16) + (k / 4) * (R::kBoxBytes / 16) + (k % 4) * 2, kHi, kIdesc,
-                            half > 0 || k > 0 || step > s0);
-            if (!R::kJoint) tc::mma_commit(&empty_x[px.s]);
-            if (half + 1 == 2 / R::kBoxes) tc::mma_commit(&empty_a[pa.s]);
+            for (int k = 0; k < 8; ++k)
+              tc::mma_ts_lo(tb + pd.s * kTok, tb + R::kA + 64 * s + 8 * k,
+                            x_lo + s * (R::kXBytes / 16) + (k / 4) * (R::kBoxBytes / 16) + (k % 4) * 2, kHi, kIdesc,
+                            k > 0 || step > s0);
+            tc::mma_commit(&empty_a[s]);
+            if (two) {
+#pragma unroll
+              for (int k = 0; k < 8; ++k)
+                tc::mma_ts_lo(tb + pd.s * kTok, tb + R::kA + 64 * s2 + 8 * k,
+                              x_lo + s2 * (R::kXBytes / 16) + (k / 4) * (R::kBoxBytes / 16) + (k % 4) * 2, kHi, kIdesc, 1);
+              tc::mma_commit(&empty_a[s2]);
+            }
           }
           __syncwarp();
+        }
+      } else {
+        for (int step = s0; step < s1; ++step, pa.next()) {
+          tc::mbar_wait_or(&full_a[pa.s], pa.phase, ok);
+#pragma unroll
+          for (int half = 0; half < 2; ++half, px.next()) {
+            tc::mbar_wait_or(&full_x[px.s], px.phase, ok);
+            __syncwarp();
+            tc::fence_after_sync();
+            if (tc::elect_one()) {
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                tc::mma_ts_lo(tb + pd.s * kTok, tb + R::kA + 64 * pa.s + 8 * (4 * half + k),
+                              x_lo + px.s * (R::kXBytes / 16) + k * 2, kHi, kIdesc, half > 0 || k > 0 || step > s0);
+              tc::mma_commit(&empty_x[px.s]);
+              if (half == 1) tc::mma_commit(&empty_a[pa.s]);
+            }
+            __syncwarp();
+          }
         }
       }
       if (tc::elect_one()) tc::mma_commit(&full_d[pd.s]);

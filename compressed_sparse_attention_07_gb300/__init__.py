@@ -411,6 +411,7 @@ class KVCache:
         self.batch, self.max_pages, self.num_pages = block_table.shape[0], block_table.shape[1], n
         self.capacity = self.max_pages * PAGE
         self.layout = (h, d, cfg.cache_dtype)
+        self.place = (block_table.data_ptr(), self.batch, self.max_pages, self.device_index)
         self._c = _KVCacheDesc(k_data.data_ptr(), k_scales.data_ptr() if fp4 else None, v_data.data_ptr(),
                                v_scales.data_ptr() if fp4 else None, block_table.data_ptr(), self.max_pages, n)
 
@@ -570,10 +571,11 @@ def kv_reorder(cfg: KVCfg, caches, beams: int, parents, kv_len, status=None, str
     its group of `beams`, or -1: from nothing) had.  `caches`: the layers' caches, over one block table, which is permuted
     in place; last pages, written in part, are copied where a beam has several children (rules in include/csa2.h)."""
     first = caches[0]
-    table, n = first.block_table.data_ptr(), first.batch
+    layout, place, n = (cfg.kv_heads, cfg.head_dim, cfg.cache_dtype), first.place, first.batch
     for c in caches:
-        _kv_same(cfg, c)
-        if c.block_table.data_ptr() != table or c.batch != n or c.device_index != first.device_index:
+        if c.layout != layout:
+            raise ValueError("the cache was made for another configuration")
+        if c.place != place:
             raise ValueError("the layers' caches must share one block table")
     if beams < 1 or n % beams:
         raise ValueError("the caches must hold whole groups of beams")
@@ -609,7 +611,7 @@ def _rows_of(t, width, name, index):
         raise ValueError("%s must be on the call's device" % name)
     if stride[1] != 1 and width > 1:
         raise ValueError("%s: a row must be contiguous" % name)
-    return t.data_ptr(), (stride[0] if shape[0] > 1 else max(width, -(-width // 8) * 8))
+    return t.data_ptr(), (stride[0] if shape[0] > 1 else -(-width // 8) * 8)
 
 
 _FLOATS = {torch.bfloat16: 0, torch.float32: 1}
@@ -654,6 +656,7 @@ class Fp4Weights:
         self.data, self.n, self.k, self.alpha = data, n, k, float(alpha)
         self.device, self.device_index = data.device, data.get_device()
         self._c = _Fp4Desc(data.data_ptr(), n, k, self.alpha, 0)
+        self._ref = C.byref(self._c)
 
     @staticmethod
     def _room(n, k, device):
@@ -705,7 +708,7 @@ def fp4_linear(x, weights: Fp4Weights, out, bias=None, status=None, stream=None)
     if out.shape[0] != T:
         raise ValueError("x and out must have the same rows")
     _check("csa2_fp4_linear", _on(
-        dev, (_lib or load()).csa2_fp4_linear, stream, C.byref(weights._c), T, xp, xs,
+        dev, (_lib or load()).csa2_fp4_linear, stream, weights._ref, T, xp, xs,
         _plain(bias, torch.bfloat16, (n,), "bias", dev), op, _FLOATS[out.dtype], os_,
         _plain(status, torch.int32, (1,), "status", dev)))
 

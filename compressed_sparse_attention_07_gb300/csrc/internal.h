@@ -17,8 +17,9 @@ namespace csa2 {
 // memory and before any global load whose value a kernel of the library may
 // write -- before the wait a kernel issues L2 prefetch hints and reads only
 // the attention's query and window rows, which csa2_swa_encode writes and a
-// caller may have written by csa2_kv_append or the csa2_kv_* attention: the
-// kernels that write these let their successor start only at their completion.
+// caller may have written by csa2_kv_append, the csa2_kv_* attention or
+// csa2_fp4_linear: the kernels that write these let their successor start only at
+// their completion.
 // cluster_x > 0 adds a cluster shape.
 template <typename... KArgs, typename... Args>
 cudaError_t launch_k(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t stream, int cluster_x,

@@ -483,6 +483,56 @@ def test_reorder_reports_what_is_wrong():
 
 # ----------------------------------------------- a run of them, as in use --
 
+@pytest.mark.parametrize("batch", [3, 24])
+def test_projections_feed_the_sparse_path(batch):
+    """The model's own decode step with its queries projected just ahead: low-rank ones to the indexer's and to the
+    attention's, which the calls read as soon as they may.  Compared with the same calls on queries that lie there."""
+    rng = np.random.default_rng(batch)
+    cfg = csa.Cfg(ratio=2, topk=64, window=32)
+    ctx, lora = 600, 1280
+    main = csa.PagedCache(batch, ctx // 2, 512, FP4)
+    idx = csa.PagedCache(batch, ctx // 2, 128, FP4)
+    x = _dev(_kv.normal(rng, batch, ctx, 512))
+    n_ent = torch.zeros(batch, dtype=torch.int32, device="cuda")
+    merge = _dev(np.full((2, 512), 0.7), torch.float32)
+    csa.compress(cfg, x, torch.zeros(batch, dtype=torch.int64, device="cuda"), merge, _dev(_kv.normal(rng, 512, 128, std=0.04)),
+                 main, idx, n_ent)
+    wq = csa.Fp4Weights.encode(_dev(_kv.normal(rng, 64 * 512, lora, std=0.02)))
+    wi = csa.Fp4Weights.encode(_dev(_kv.normal(rng, 32 * 128, lora, std=0.02)))
+    swa = _dev(_kv.normal(rng, batch, 32, 512))
+    swa_len = torch.full((batch,), 32, dtype=torch.int32, device="cuda")
+    pos = torch.full((batch, 1), ctx - 1, dtype=torch.int64, device="cuda")
+    swa_pos0 = torch.full((batch,), ctx - 32, dtype=torch.int64, device="cuda")
+    ws = torch.empty(csa.index_workspace_bytes(cfg, batch, 1, ctx // 2), dtype=torch.uint8, device="cuda")
+
+    def step(low, q, q_idx, topk, out, project):
+        if project:
+            csa.fp4_linear(low, wq, q.view(batch, -1))
+            csa.fp4_linear(low, wi, q_idx.view(batch, -1))
+        csa.index_topk(cfg, q_idx, pos, idx, n_ent, ctx // 2, topk, ws)
+        csa.attend(cfg, q, main, n_ent, topk, swa, swa_len, swa_pos0, pos, out)
+
+    def room():
+        return (torch.zeros(batch, 1, 64, 512, dtype=torch.bfloat16, device="cuda"),
+                torch.zeros(batch, 1, 32, 128, dtype=torch.bfloat16, device="cuda"),
+                torch.zeros(batch, 1, 64, dtype=torch.int32, device="cuda"), torch.zeros(batch, 1, 64, 512, device="cuda"))
+
+    a, b = room(), room()
+    low = _dev(_kv.normal(rng, batch, lora))
+    graph = csa.capture(lambda: step(low, *a, True))
+    for _ in range(4):
+        low.copy_(_dev(_kv.normal(rng, batch, lora)))
+        graph()
+        torch.cuda.synchronize()
+        b[0].copy_(a[0]), b[1].copy_(a[1])
+        torch.cuda.synchronize()
+        step(low, *b, False)
+        torch.cuda.synchronize()
+        assert torch.isfinite(a[3]).all() and (a[3] != 0).any()
+        assert torch.equal(a[2], b[2]) and torch.equal(a[3], b[3])
+
+
+
 @pytest.mark.parametrize("dtype", [FP4, BF16])
 def test_a_captioner_writes_with_beams(dtype):
     """Prompts with image tokens, then steps of: projection -> append -> attention -> logits -> beams -> reorder, over

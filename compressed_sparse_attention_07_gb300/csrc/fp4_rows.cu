@@ -24,7 +24,7 @@ namespace csa2 {
 namespace {
 
 constexpr int kWarps = 16, kThreads = 32 * kWarps, kMostSlots = 8;
-constexpr int kSmemMost = 227 * 1024 - 3072;  // beside the barriers
+constexpr int kSmemMost = 224 * 1024;  // beside the barriers
 // x rows stand an odd multiple of 64 bytes apart (two rows' chunks in different banks).
 __host__ __device__ __forceinline__ int x_pitch(int k_blocks) { return k_blocks * 256 + 64; }
 
@@ -220,6 +220,11 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_rows_kernel(const Fp4Linear a
       f[i][0] = __byte_perm(p, 0, 0x1010), f[i][1] = __byte_perm(p, 0, 0x3232);
       f[i][2] = __byte_perm(q, 0, 0x1010), f[i][3] = __byte_perm(q, 0, 0x3232);
     }
+    // A unit's products are summed by themselves first, then added to the tile's sums: the tensor
+    // core's own additions cut off, and over a long run that adds up.  16 rows of 4096 -> 32768
+    // in fp32, error relative to the outputs' norm: 9.0e-8 so, 6.1e-7 with one running sum.  It
+    // costs 16 rows over 128001 words 71.7 -> 75.1 us, 8 rows 50.5 -> 50.8 us.
+    float part[kGroups][kNt][4] = {};
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       uint4 x[kNt];
@@ -234,11 +239,17 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_rows_kernel(const Fp4Linear a
         fp4_f16(wh, f[i][2 + j / 2], h);
 #pragma unroll
         for (int m = 0; m < kNt; ++m) {
-          mma(acc[i][m], l[0], h[0], l[1], h[1], x[m].x, x[m].y);
-          mma(acc[i][m], l[2], h[2], l[3], h[3], x[m].z, x[m].w);
+          mma(part[i][m], l[0], h[0], l[1], h[1], x[m].x, x[m].y);
+          mma(part[i][m], l[2], h[2], l[3], h[3], x[m].z, x[m].w);
         }
       }
     }
+#pragma unroll
+    for (int i = 0; i < kGroups; ++i)
+#pragma unroll
+      for (int m = 0; m < kNt; ++m)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) acc[i][m][c] += part[i][m][c];
     if (++kb == a.k_blocks || u + 1 == u1) {  // the end of the tile, or of the warp's part of it
       const bool all = whole && kb == a.k_blocks, end = u + 1 == u1;
       // the warp's last piece goes to its ring, which is empty by then

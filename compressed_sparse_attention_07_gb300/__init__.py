@@ -570,6 +570,8 @@ def kv_reorder(cfg: KVCfg, caches, beams: int, parents, kv_len, status=None, str
     """The beams' states in the order of a selection: sequence i of the caches goes on from what sequence parents[i] (of
     its group of `beams`, or -1: from nothing) had.  `caches`: the layers' caches, over one block table, which is permuted
     in place; last pages, written in part, are copied where a beam has several children (rules in include/csa2.h)."""
+    if not caches:
+        raise ValueError("at least one layer's cache is needed")
     first = caches[0]
     layout, place, n = (cfg.kv_heads, cfg.head_dim, cfg.cache_dtype), first.place, first.batch
     for c in caches:
@@ -626,7 +628,7 @@ def beam_select(logits, cum, scores, parents, tokens, workspace, done=None, end_
                 stream=None):
     """Best continuations of each group of beams: logits [groups * beams][vocab] (bf16 or fp32; rows may stand apart),
     cum [groups][beams] fp32 -> the best scores [groups][take] fp32 (cum + log-softmax) in order, their parents (sequence
-    numbers) and tokens [groups][take] int32.  done [groups][beams] uint8: a beam that has ended proposes end_token alone
+    numbers) and tokens [groups][take] int32.  scores may be cum where take == beams.  done [groups][beams] uint8: a beam that has ended proposes end_token alone
     at its score.  lse [groups * beams] fp32 receives the log-sum-exps."""
     groups, beams = cum.shape
     take, dev, vocab = scores.shape[1], logits.get_device(), logits.shape[1]
@@ -687,7 +689,9 @@ class Fp4Weights:
         p, stride = _rows_of(w, k, "w", dev)
         if gain is None:
             most = float(w.abs().amax()) if w.numel() else 0.0
-            gain = 2.0 ** math.floor(math.log2(448 * 6 / most)) if 0 < most < math.inf else 1.0
+            gain = 2.0 ** min(126, math.floor(math.log2(448 * 6 / most))) if 0 < most < math.inf else 1.0
+        if not 2.0 ** -126 <= abs(gain) <= 2.0 ** 126:
+            raise ValueError("gain must be one that fp32 has with its reciprocal, got %r" % gain)
         data = cls._room(n, k, w.device)
         _check("csa2_fp4_encode", _on(dev, load().csa2_fp4_encode, stream, n, k, p, stride, float(gain), data.data_ptr(),
                                       _plain(status, torch.int32, (1,), "status", dev)))

@@ -505,7 +505,8 @@ bool sizes_ok(int32_t groups, int32_t beams, int32_t vocab, int32_t take) {
   return groups >= 0 && beams >= 1 && vocab >= 1 && take >= 1;
 }
 bool sizes_fit(int32_t groups, int32_t beams, int32_t vocab, int32_t take) {
-  if (beams > kMost || take > kMost || (int64_t)groups * beams > INT32_MAX) return false;
+  // (a part's end is its beginning and its size, in 32 bits)
+  if (beams > kMost || take > kMost || vocab > (1 << 30) || (int64_t)groups * beams > INT32_MAX) return false;
   const int64_t parts = most_parts((int64_t)groups * beams, vocab);
   return groups * beams * parts <= INT32_MAX - kPartWarps && parts * beams * take <= INT32_MAX / 2;
 }

@@ -43,6 +43,7 @@ int32_t csa2_fp4_linear(const csa2_fp4_weights* w, int32_t T, const uint16_t* x,
       T < 0 || (out_dtype != CSA2_BF16 && out_dtype != CSA2_F32))
     return CSA2_ERR_INVALID_ARG;
   if (T == 0) return CSA2_OK;
+  if (T > (1 << 30)) return CSA2_ERR_UNSUPPORTED;  // (rows rounded up to a tile, in 32 bits)
   if (!x || !out || !aligned(x, 16) || x_stride < w->k || x_stride % 8 || !aligned(bias, 2) ||
       !aligned(out, out_dtype == CSA2_F32 ? 4 : 2) || out_stride < w->n || !aligned(status, 4))
     return CSA2_ERR_INVALID_ARG;

@@ -513,9 +513,9 @@ CSA2_API size_t csa2_beam_workspace_bytes(int32_t groups, int32_t beams, int32_t
  *    sets CSA2_ERR_RANGE.
  * logits: bf16 (logits_dtype CSA2_BF16) or fp32 (CSA2_F32) rows of `vocab` contiguous
  * values, `stride` elements apart (any distance from vocab on), the first 16-byte
- * aligned.  beams 1..64, take 1..64 (CSA2_ERR_UNSUPPORTED beyond, or where a group or
- * the call has more than 2^30 partial results, one for every 500 logits and place in
- * `take`).  Workspace: csa2_beam_workspace_bytes, 256-byte
+ * aligned.  beams 1..64, take 1..64, vocab to 2^30 (CSA2_ERR_UNSUPPORTED beyond, or where a
+ * group or the call has more than 2^30 partial results, one for every 500 logits and place in
+ * `take`).  scores may be cum where take == beams.  Workspace: csa2_beam_workspace_bytes, 256-byte
  * aligned (smaller: CSA2_ERR_CAPACITY), contents not kept between calls; two calls
  * that may overlap need one each. */
 CSA2_API int32_t csa2_beam_select(int32_t groups, int32_t beams, int32_t vocab, int32_t take, const void* logits,
@@ -590,7 +590,8 @@ CSA2_API int32_t csa2_fp4_pack(int32_t n, int32_t k, const uint8_t* codes, const
  * bf16 x and the exact weights, which bf16 holds, summed in fp32, rounded once.
  * x [T][k] bf16, rows `x_stride` elements apart (a multiple of 8), 16-byte aligned; bias
  * [n] bf16 or NULL; out [T][n] bf16 (out_dtype CSA2_BF16) or fp32 (CSA2_F32), rows
- * `out_stride` elements apart (any distance from n on).  out must not overlap x or
+ * `out_stride` elements apart (any distance from n on).  T is 2^30 at most
+ * (CSA2_ERR_UNSUPPORTED).  out must not overlap x or
  * the weights.  An x that is not finite has effect on its own row's outputs alone; a row
  * whose products' magnitudes (before alpha) sum up past fp32's largest may yield such.
  * Rows' sums do not depend on what other rows hold, but their order may depend on T. */

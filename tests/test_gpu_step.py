@@ -122,6 +122,17 @@ def test_weights_encoded_as_the_oracle():
     assert 448 * 3 < most <= 448 * 6 and np.log2(a.alpha) % 1 == 0
 
 
+def test_weights_near_nothing_are_encoded():
+    """The largest below 2^-115: no gain that fp32 has would bring it to the codec's largest."""
+    w = torch.full((16, 16), 2.0 ** -130, dtype=torch.bfloat16, device="cuda")
+    got = csa.Fp4Weights.encode(w)
+    assert got.alpha == 2.0 ** -126
+    # 2^-130 x 2^126 = 1/16: scale e4m3(1/96) = 5/512 (steps of 2^-9 there), 6.4 of it: code 6
+    out = torch.empty(1, 16, device="cuda")
+    csa.fp4_linear(torch.full((1, 16), 2.0 ** 100, dtype=torch.bfloat16, device="cuda"), got, out)
+    assert torch.equal(out, torch.full_like(out, 16 * 6 * 5 / 512 * 2.0 ** -26))
+
+
 def test_packing_reports_scales_that_are_no_number():
     codes, scales = np.full((2, 32), 0x22, np.uint8), np.full((2, 4), 0x38, np.uint8)
     scales[1, 2], scales[0, 3] = 0x7F, 0xFF
@@ -356,6 +367,18 @@ def test_beams_that_cannot_go_on(vocab, dtype):
     x[4:7] = torch.nan_to_num(x[4:7], 0, 0, -1)
     cum[0, 2], cum[0, 3] = float("nan"), inf
     _check_beams(x, cum, 8, code=19)
+
+
+@pytest.mark.parametrize("groups,beams,vocab", [(1, 1, 17), (5, 4, 32000), (70, 8, 999), (2, 64, 3001)])
+def test_scores_written_over_the_sums_they_come_from(groups, beams, vocab):
+    rng = np.random.default_rng(vocab)
+    x = _dev(rng.standard_normal((groups * beams, vocab)) * 3)
+    cum = _dev(rng.standard_normal((groups, beams)), torch.float32)
+    want = _select(x, cum, beams)
+    parents, tokens = (torch.empty(groups, beams, dtype=torch.int32, device="cuda") for _ in range(2))
+    ws = torch.empty(csa.beam_workspace_bytes(groups, beams, vocab, beams), dtype=torch.uint8, device="cuda")
+    csa.beam_select(x, cum, cum, parents, tokens, ws)
+    assert torch.equal(cum, want[0]) and torch.equal(parents, want[1]) and torch.equal(tokens, want[2])
 
 
 def test_beams_beyond_32_bits_of_logits():

@@ -226,3 +226,23 @@ def test_plain_selection_by_hand():
     assert np.allclose(lse, 0) and p.tolist() == [[0, 1, 0, 0]] and t.tolist() == [[0, 1, 1, 2]]
     s, p, t, lse, _ = _step.beam_select(logits, np.array([[0.0, -0.1]]), 3, np.array([[0, 1]]), end=2)
     assert p.tolist() == [[1, 0, 0]] and t.tolist() == [[2, 0, 1]] and lse[1] == 0 and s[0, 0] == -0.1
+
+
+def test_sizes_that_32_bits_of_places_do_not_hold_are_refused():
+    assert csa.beam_workspace_bytes(1, 1, 1 << 30, 1) > 0
+    for vocab in ((1 << 30) + 1, (1 << 31) - 1):
+        assert csa.beam_workspace_bytes(1, 1, vocab, 1) == 0
+        assert _beam(groups=1, beams=1, vocab=vocab, take=1, stride=vocab) == 2
+    for T in ((1 << 30) + 1, (1 << 31) - 1):
+        assert _linear(dict(n=1, k=16), T=T) == 2
+
+
+@pytest.mark.parametrize("gain", [0.0, float("inf"), float("nan"), 1e39, 1e-39])
+def test_gains_without_a_reciprocal_refused(gain):
+    with pytest.raises(ValueError):
+        csa.Fp4Weights.encode(torch.ones(1, 16, dtype=torch.bfloat16), gain)
+
+
+def test_no_layers_to_reorder_refused():
+    with pytest.raises(ValueError):
+        csa.kv_reorder(csa.KVCfg(4, 2, 64, csa.CACHE_FP4, 0, 0, csa.ROPE_HALF), [], 1, None, None)

@@ -490,27 +490,45 @@ __global__ void __launch_bounds__(kThreads) beam_join_kernel(const BeamArgs a) {
   }
 }
 
-// Parts of a row, all of like size: as few as make 4096 warps, of 1 to kMostWindows windows.
+// Parts of a row, all of like size, of 1 to kMostWindows windows: those of least time, of
+// which a window takes a warp 5 parts alone and 9 more with the SM full (28 warps; 1.25 and
+// 2.25 us), and its start a window.  512 rows of 128001 in bf16 take 37.1 us in 8 parts,
+// one wave of 27 warps an SM, and 43.6 in 9, which begin a second one.  (152 SMs by number, and
+// no more partial results than most_results has, as that has to hold for every call that
+// is no larger in any size.)
 struct Parts {
   int n, size;
 };
+int windows_of(int vocab, bool bf16) { return (vocab - 1) / (kN * 32 * (bf16 ? 8 : 4)) + 1; }
+int64_t most_results(int64_t rows, int vocab) {
+  const int64_t windows = windows_of(vocab, false);
+  return std::max(rows * ((windows + kMostWindows - 1) / kMostWindows), std::min<int64_t>(rows * windows, 8192));
+}
 Parts parts_of(int64_t rows, int vocab, bool bf16) {
-  const int vec = bf16 ? 8 : 4, window = kN * 32 * vec, windows = (vocab - 1) / window + 1;
-  const int each = (int)std::max<int64_t>(1, std::min<int64_t>(kMostWindows, rows * windows / 4096));
-  const int n = (windows + each - 1) / each;
+  constexpr int64_t kWave = 152 * 28;
+  const int vec = bf16 ? 8 : 4, windows = windows_of(vocab, bf16);
+  const int64_t most = most_results(rows, vocab);
+  int n = 0;
+  double least = INFINITY;
+  for (int each = 1; each <= kMostWindows; ++each) {
+    const int64_t parts = (windows + each - 1) / each, warps = rows * parts;
+    if (warps > most) continue;
+    const double time = (each + 1) * (5.0 * (double)((warps + kWave - 1) / kWave) + 9.0 * (double)warps / (double)kWave);
+    if (time < least) least = time, n = (int)parts;
+  }
   return {n, ((vocab - 1) / n / vec + 1) * vec};
 }
-int most_parts(int64_t rows, int vocab) { return std::max(parts_of(rows, vocab, true).n, parts_of(rows, vocab, false).n); }
 bool sizes_ok(int32_t groups, int32_t beams, int32_t vocab, int32_t take) {
   return groups >= 0 && beams >= 1 && vocab >= 1 && take >= 1;
 }
 bool sizes_fit(int32_t groups, int32_t beams, int32_t vocab, int32_t take) {
   // (a part's end is its beginning and its size, in 32 bits)
   if (beams > kMost || take > kMost || vocab > (1 << 30) || (int64_t)groups * beams > INT32_MAX) return false;
-  const int64_t parts = most_parts((int64_t)groups * beams, vocab);
-  return groups * beams * parts <= INT32_MAX - kPartWarps && parts * beams * take <= INT32_MAX / 2;
+  // (a group's lists, times take, are numbered in 32 bits too)
+  return most_results((int64_t)groups * beams, vocab) <= INT32_MAX - kPartWarps &&
+         most_results(beams, vocab) * take <= INT32_MAX / 2;
 }
-size_t sums_bytes(int64_t rows, int64_t parts) { return (size_t)((rows * parts * sizeof(PartSum) + 255) / 256 * 256); }
+size_t sums_bytes(int64_t results) { return (size_t)((results * sizeof(PartSum) + 255) / 256 * 256); }
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
 }  // namespace
@@ -522,8 +540,8 @@ extern "C" {
 
 size_t csa2_beam_workspace_bytes(int32_t groups, int32_t beams, int32_t vocab, int32_t take) {
   if (!sizes_ok(groups, beams, vocab, take) || !sizes_fit(groups, beams, vocab, take)) return 0;
-  const int64_t rows = (int64_t)groups * beams, parts = most_parts(rows, vocab);
-  return sums_bytes(rows, parts) + (size_t)(rows * parts * take) * sizeof(uint2);
+  const int64_t results = most_results((int64_t)groups * beams, vocab);
+  return sums_bytes(results) + (size_t)(results * take) * sizeof(uint2);
 }
 
 int32_t csa2_beam_select(int32_t groups, int32_t beams, int32_t vocab, int32_t take, const void* logits,
@@ -544,7 +562,7 @@ int32_t csa2_beam_select(int32_t groups, int32_t beams, int32_t vocab, int32_t t
   const Parts parts = parts_of(rows, vocab, bf16);
   BeamArgs a{groups, beams, vocab, take, parts.n, parts.size, divisor(parts.n), logits, stride, cum, done, end_token, scores,
              parents, tokens, lse, static_cast<PartSum*>(workspace),
-             reinterpret_cast<uint2*>(static_cast<uint8_t*>(workspace) + sums_bytes(rows, parts.n)), status};
+             reinterpret_cast<uint2*>(static_cast<uint8_t*>(workspace) + sums_bytes(rows * parts.n)), status};
   const dim3 grid((unsigned)((rows * parts.n + kPartWarps - 1) / kPartWarps)), block(32 * kPartWarps);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   cudaError_t e = bf16 ? launch_k(beam_part_kernel<true>, grid, block, 0, s, 0, a)

@@ -492,7 +492,8 @@ CSA2_API int32_t csa2_kv_cross_attend(const csa2_kv_cfg* cfg, int32_t B, int32_t
 /* ---- beams over such caches ----
  * Beam g * beams + k is sequence g * beams + k of the caches, group g's k-th. */
 
-/* Workspace bytes of csa2_beam_select; 0 for sizes that it refuses. */
+/* Workspace bytes of csa2_beam_select, enough for every call that is no larger in any
+ * of these sizes; 0 for sizes that it refuses. */
 CSA2_API size_t csa2_beam_workspace_bytes(int32_t groups, int32_t beams, int32_t vocab, int32_t take);
 
 /* Best continuations of each group over its beams and the vocabulary.  With
@@ -594,7 +595,10 @@ CSA2_API int32_t csa2_fp4_pack(int32_t n, int32_t k, const uint8_t* codes, const
  * (CSA2_ERR_UNSUPPORTED).  out must not overlap x or
  * the weights.  An x that is not finite has effect on its own row's outputs alone; a row
  * whose products' magnitudes (before alpha) sum up past fp32's largest may yield such.
- * Rows' sums do not depend on what other rows hold, but their order may depend on T. */
+ * Rows' sums do not depend on what other rows hold, but their order may depend on T.
+ * Of more than 16 rows, or rows that do not fit shared memory (16 of more than 5376
+ * channels), sums run through the tensor core's accumulator, which cuts off: fp32 outputs
+ * are then off by 1e-6 of their norm at 4096 channels, 6e-6 at 16384. */
 CSA2_API int32_t csa2_fp4_linear(const csa2_fp4_weights* w, int32_t T, const uint16_t* x, int64_t x_stride,
                                  const uint16_t* bias, void* out, int32_t out_dtype, int64_t out_stride,
                                  int32_t* status, void* stream);

@@ -246,3 +246,11 @@ def test_gains_without_a_reciprocal_refused(gain):
 def test_no_layers_to_reorder_refused():
     with pytest.raises(ValueError):
         csa.kv_reorder(csa.KVCfg(4, 2, 64, csa.CACHE_FP4, 0, 0, csa.ROPE_HALF), [], 1, None, None)
+
+
+def test_a_workspace_serves_smaller_calls():
+    f, rng = csa.beam_workspace_bytes, np.random.default_rng(3)
+    for _ in range(3000):
+        a = [int(2 ** (rng.random() * m)) for m in (8, 6, 18, 6)]
+        b = [int(rng.integers(1, v + 1)) if rng.random() < 0.7 else v for v in a]
+        assert 0 < f(*b) <= f(*a), (b, a)

@@ -11,9 +11,12 @@
 // is read once a step, 1024 cycles at 128 bytes a cycle; with the left operand in shared
 // memory too they were 1570, and took 1690.  A CTA takes tile after tile, up to 128 rows
 // of x with two accumulators, so that the sums of one are stored while the next is
-// formed.  The accumulator's additions cut off: fp32 outputs are 1.0e-6 of their norm off at
-// 4096 channels, 6.2e-6 at 16384.  Where the tiles fill less than half the SMs, a cluster divides k, and its
-// CTAs join their sums through distributed shared memory in rank order.
+// formed.  Each tile of the last wave is divided among a cluster, along k, where that ends sooner
+// (512 rows of 4096 -> 10240, 160 tiles: 46.6 -> 35.3 us, 40 rows of 4096 -> 20480 26.7 -> 20.2);
+// its CTAs join their sums through distributed shared memory in rank order.
+// The accumulator's additions cut off: fp32 outputs are 1.0e-6 of their norm off at 4096
+// channels, 6.2e-6 at 16384.
+// 64 rows over 128001 words take 79 us, 40 rows of 4096 -> 10240 14.9, 4096 rows 215.
 #include <cuda.h>
 
 #include <algorithm>
@@ -29,8 +32,7 @@ constexpr int kSmemMost = 227 * 1024 - 1024;
 // Places of the rings for kTok rows of x: kS steps of decoded weights in tensor memory,
 // 64 columns each beside kD accumulators; kX places of kBoxes boxes of x; kP packed steps.
 // Four decoding warps, a set, have every kSets-th step (six sets where registers and columns
-// allow), so a set does not see every phase
-// of every place, and must not take the phase before the last (of the same parity) for
+// allow), so a set does not see every phase of every place, and must not take the phase before the last (of the same parity) for
 // the last.  Packed steps may land out of order: with kP a multiple of kSets a set sees
 // every phase of its own places.  Decoded steps become free in order: a set that passed
 // step n - kSets knows step n - kSets - kS to be free, hence step n - 2 kS if kS >= kSets.
@@ -60,11 +62,19 @@ struct Place {
   }
 };
 
+// A CTA's work: `whole` tiles to itself, every gridDim.x-th; then, in a cluster, its share of the
+// steps of one tile that the cluster's CTAs divide, if there is one for it.
 struct TileArgs {
   Fp4Linear l;
   int row_tiles, tiles;  // of W, in all
-  int split;             // CTAs of a cluster that divide k
+  int size;              // CTAs of a cluster
+  int whole;
+  Divisor by_rows, by_size;  // row_tiles, size
 };
+struct Run {
+  int tile, s0, s1;  // steps [s0, s1)
+};
+constexpr int kMostCluster = 8;
 
 __device__ __forceinline__ void tensor_g2s(uint32_t dst, const CUtensorMap* map, int x, int y, uint64_t* bar) {
   asm volatile(
@@ -93,7 +103,9 @@ struct Number {
   __device__ constexpr int operator()() const { return kI; }
 };
 
-// A value that is the same in all lanes, in a register that is known to be.
+// A value that is the same in all lanes, in a register that is known to be.  What a run's loops
+// of copies and products start from goes through it: found a lane in its own register, 64 rows
+// over 128001 words took 82.0 us instead of 79.0, 300 rows of 8192 -> 8192 46.4 instead of 44.2.
 __device__ __forceinline__ uint32_t uniform(uint32_t v) { return __reduce_max_sync(0xffffffffu, v); }
 
 template <int kTok>
@@ -114,15 +126,24 @@ __global__ void __launch_bounds__(Rings<kTok>::kThreads, 1) fp4_tiles_kernel(con
     tc::mbar_init(&drained, 1);
     tc::fence_mbar_init();
   }
-  // a CTA's tiles: first, first + stride ..; its steps of each: [s0, s1)
-  const int rank = a.split > 1 ? (int)tc::cluster_rank() : 0;
-  const int first = blockIdx.x / a.split, stride = gridDim.x / a.split;
-  const int s0 = (int)((int64_t)rank * a.l.k_blocks / a.split), s1 = (int)((int64_t)(rank + 1) * a.l.k_blocks / a.split);
-  auto weights = [&](int tile) { return a.l.w + (int64_t)(tile % a.row_tiles) * a.l.k_blocks * kTileBytes; };
+  const int k_blocks = a.l.k_blocks, rank = a.size > 1 ? (int)tc::cluster_rank() : 0;
+  const int wholes = a.whole + (a.size == 1 && (int)blockIdx.x < a.tiles - a.whole * (int)gridDim.x ? 1 : 0);
+  const int divided = a.whole * (int)gridDim.x + quotient(blockIdx.x, a.by_size);  // the cluster's tile
+  const bool shares = a.size > 1 && divided < a.tiles;
+  const int p0 = shares ? quotient(rank * k_blocks, a.by_size) : 0, p1 = shares ? quotient((rank + 1) * k_blocks, a.by_size) : 0;
+  const int runs = wholes + (shares ? 1 : 0);
+  auto run_of = [&](int i) {
+    return i < wholes ? Run{(int)(blockIdx.x + i * gridDim.x), 0, k_blocks} : Run{divided, p0, p1};
+  };
+  auto x_tile = [&](int tile) { return quotient(tile, a.by_rows); };
+  auto w_tile = [&](int tile) { return tile - quotient(tile, a.by_rows) * a.row_tiles; };
+  auto weights = [&](int tile) { return a.l.w + (int64_t)w_tile(tile) * k_blocks * kTileBytes; };
   // blocks of 16 rows that a tile has (what it decodes beyond them is not stored)
-  auto blocks = [&](int tile) { return min(kTileBlocks, (a.l.n + kBlockRows - 1) / kBlockRows - tile % a.row_tiles * kTileBlocks); };
-  if (tid == 0 && first < a.tiles)
-    tc::bulk_prefetch_l2(weights(first) + (int64_t)s0 * kTileBytes, min(R::kP, s1 - s0) * kTileBytes);
+  auto blocks = [&](int tile) { return min(kTileBlocks, (a.l.n + kBlockRows - 1) / kBlockRows - w_tile(tile) * kTileBlocks); };
+  if (tid == 0) {
+    const Run r = run_of(0);
+    tc::bulk_prefetch_l2(weights(r.tile) + (int64_t)r.s0 * kTileBytes, min(R::kP, r.s1 - r.s0) * kTileBytes);
+  }
   griddep_wait();  // every input may be the previous kernel's output
   if (warp == 3) {
     tc::tmem_alloc(&tmem, R::kCols);
@@ -140,10 +161,12 @@ __global__ void __launch_bounds__(Rings<kTok>::kThreads, 1) fp4_tiles_kernel(con
   if (warp == 0) {  // packed weights
     int n = 0;
     Place<R::kP> at;
-    for (int tile = first; tile < a.tiles && ok; tile += stride) {
-      const uint8_t* src = weights(tile) + (int64_t)s0 * kTileBytes;
-      const int bytes = blocks(tile) * kBlockBytes;
-      for (int step = s0; step < s1; ++step, ++n, at.next(), src += kTileBytes) {
+    for (int i = 0; i < runs && ok; ++i) {
+      const Run r = run_of(i);
+      const uint64_t first = reinterpret_cast<uint64_t>(weights(r.tile) + (int64_t)r.s0 * kTileBytes);
+      const uint8_t* src = reinterpret_cast<const uint8_t*>((uint64_t)uniform((uint32_t)(first >> 32)) << 32 | uniform((uint32_t)first));
+      const int bytes = (int)uniform(blocks(r.tile) * kBlockBytes), steps = (int)uniform(r.s1 - r.s0);
+      for (int step = 0; step < steps; ++step, ++n, at.next(), src += kTileBytes) {
         if (n >= R::kP) tc::mbar_wait_or(&empty_p[at.s], at.phase ^ 1, ok);
         if (!__all_sync(0xffffffffu, ok)) break;
         if (tc::elect_one()) {
@@ -159,9 +182,10 @@ __global__ void __launch_bounds__(Rings<kTok>::kThreads, 1) fp4_tiles_kernel(con
     int n = 0;
     Place<R::kX> at;
     uint64_t *const full = R::kJoint ? full_a : full_x, *const empty = R::kJoint ? empty_a : empty_x;
-    for (int tile = first; tile < a.tiles && ok; tile += stride) {
-      const int row = tile / a.row_tiles * kTok;
-      for (int box = 2 * s0; box < 2 * s1; box += R::kBoxes, ++n, at.next()) {
+    for (int i = 0; i < runs && ok; ++i) {
+      const Run r = run_of(i);
+      const int row = (int)uniform(x_tile(r.tile) * kTok), end = (int)uniform(2 * r.s1);
+      for (int box = (int)uniform(2 * r.s0); box < end; box += R::kBoxes, ++n, at.next()) {
         if (n >= R::kX) tc::mbar_wait_or(&empty[at.s], at.phase ^ 1, ok);
         if (!__all_sync(0xffffffffu, ok)) break;
         if (tc::elect_one()) {
@@ -181,13 +205,14 @@ __global__ void __launch_bounds__(Rings<kTok>::kThreads, 1) fp4_tiles_kernel(con
     Place<R::kS> pa;
     Place<R::kX> px;
     Place<R::kD> pd;
-    int it = 0;
-    for (int tile = first; tile < a.tiles; tile += stride, ++it, pd.next()) {
-      if (it >= R::kD) tc::mbar_wait_or(&empty_d[pd.s], pd.phase ^ 1, ok);
+    for (int i = 0; i < runs; ++i, pd.next()) {
+      const Run run = run_of(i);
+      const int steps = (int)uniform(run.s1 - run.s0);
+      if (i >= R::kD) tc::mbar_wait_or(&empty_d[pd.s], pd.phase ^ 1, ok);
       if constexpr (R::kJoint) {
         // two steps at a time where there are two
-        for (int step = s0; step < s1; step += 2) {
-          const bool two = step + 1 < s1;
+        for (int step = 0; step < steps; step += 2) {
+          const bool two = step + 1 < steps;
           const int s = pa.s;
           tc::mbar_wait_or(&full_a[s], pa.phase, ok);
           pa.next();
@@ -203,7 +228,7 @@ __global__ void __launch_bounds__(Rings<kTok>::kThreads, 1) fp4_tiles_kernel(con
             for (int k = 0; k < 8; ++k)
               tc::mma_ts_lo(tb + pd.s * kTok, tb + R::kA + 64 * s + 8 * k,
                             x_lo + s * (R::kXBytes / 16) + (k / 4) * (R::kBoxBytes / 16) + (k % 4) * 2, kHi, kIdesc,
-                            k > 0 || step > s0);
+                            k > 0 || step > 0);
             tc::mma_commit(&empty_a[s]);
             if (two) {
 #pragma unroll
@@ -216,7 +241,7 @@ __global__ void __launch_bounds__(Rings<kTok>::kThreads, 1) fp4_tiles_kernel(con
           __syncwarp();
         }
       } else {
-        for (int step = s0; step < s1; ++step, pa.next()) {
+        for (int step = 0; step < steps; ++step, pa.next()) {
           tc::mbar_wait_or(&full_a[pa.s], pa.phase, ok);
 #pragma unroll
           for (int half = 0; half < 2; ++half, px.next()) {
@@ -227,7 +252,7 @@ __global__ void __launch_bounds__(Rings<kTok>::kThreads, 1) fp4_tiles_kernel(con
 #pragma unroll
               for (int k = 0; k < 4; ++k)
                 tc::mma_ts_lo(tb + pd.s * kTok, tb + R::kA + 64 * pa.s + 8 * (4 * half + k),
-                              x_lo + px.s * (R::kXBytes / 16) + k * 2, kHi, kIdesc, half > 0 || k > 0 || step > s0);
+                              x_lo + px.s * (R::kXBytes / 16) + k * 2, kHi, kIdesc, half > 0 || k > 0 || step > 0);
               tc::mma_commit(&empty_x[px.s]);
               if (half == 1) tc::mma_commit(&empty_a[pa.s]);
             }
@@ -245,8 +270,7 @@ __global__ void __launch_bounds__(Rings<kTok>::kThreads, 1) fp4_tiles_kernel(con
     const int set = (warp - 8) >> 2, q = warp & 3, r = lane & 15;  // rows 32 q .. of every kSets-th step
     const uint8_t* const src = ps + (2 * q + (lane >> 4)) * kBlockBytes;
     const uint32_t dst0 = tc::taddr(tmem, 32 * q, R::kA);
-    const int steps = s1 - s0;
-    const int mine = first < a.tiles ? ((a.tiles - 1 - first) / stride + 1) * steps : 0;  // of all tiles
+    const int mine = wholes * k_blocks + p1 - p0;  // steps of all runs
     int p = set % R::kP, s = set % R::kS;
     uint32_t p_phase = 0, s_phase = set / R::kS & 1;
     for (int n = set; n < mine; n += R::kSets) {
@@ -298,11 +322,14 @@ __global__ void __launch_bounds__(Rings<kTok>::kThreads, 1) fp4_tiles_kernel(con
     const int lane0 = 32 * (warp & 3);
     constexpr int kCols = kTok < 32 ? kTok : 32;
     Place<R::kD> at;
-    for (int tile = first; tile < a.tiles; tile += stride, at.next()) {
-      const int i = tile % a.row_tiles * kTileRows + lane0 + lane, t0 = tile / a.row_tiles * kTok;
+    for (int n = 0; n < runs; ++n, at.next()) {
+      const int tile = run_of(n).tile;
+      const int i = w_tile(tile) * kTileRows + lane0 + lane, t0 = x_tile(tile) * kTok;
       const bool there = i < a.l.n;
       const float bias = there ? fp4_bias(a.l, i) : 0.0f;
       tc::mbar_wait_or(&full_d[at.s], at.phase, ok);
+      // (the last run: nothing fills x's ring or reads it any more)
+      uint32_t* const piece = n < wholes ? nullptr : reinterpret_cast<uint32_t*>(xs);
       __syncwarp();
       tc::fence_after_sync();
 #pragma unroll 1
@@ -312,9 +339,9 @@ __global__ void __launch_bounds__(Rings<kTok>::kThreads, 1) fp4_tiles_kernel(con
         if constexpr (kCols == 32) tc::tmem_ld32(tc::taddr(tmem, lane0, at.s * kTok + c), v);
         else tc::tmem_ld16(tc::taddr(tmem, lane0, at.s * kTok + c), v);
         tc::tmem_wait_ld();
-        if (a.split > 1) {  // [row of x][row of W], in x's ring, which nothing fills any more
+        if (piece) {  // [row of x][row of W]
 #pragma unroll
-          for (int j = 0; j < kCols; ++j) reinterpret_cast<uint32_t*>(xs)[(c + j) * kTileRows + lane0 + lane] = v[j];
+          for (int j = 0; j < kCols; ++j) piece[(c + j) * kTileRows + lane0 + lane] = v[j];
         } else if (there) {
           const int most = min(kCols, a.l.T - t0 - c);
           const int64_t at0 = (int64_t)(t0 + c) * a.l.out_stride + i;
@@ -332,16 +359,22 @@ __global__ void __launch_bounds__(Rings<kTok>::kThreads, 1) fp4_tiles_kernel(con
   __syncwarp();
   __syncthreads();
   if (warp == 3) tc::tmem_dealloc(tmem, R::kCols);
-  if (a.split > 1) {
+  if (a.size > 1) {
     tc::cluster_sync();
-    // this CTA's share of the tile's rows of x
-    const int t0 = first / a.row_tiles * kTok, i = first % a.row_tiles * kTileRows + tid % kTileRows;
+    // this CTA's share of the divided tile's rows of x
+    const int t0 = x_tile(divided) * kTok, i = w_tile(divided) * kTileRows + tid % kTileRows;
     const uint32_t mine = tc::smem_u32(xs);
-    for (int t = rank + a.split * (tid / kTileRows); t < kTok && t0 + t < a.l.T; t += a.split * (R::kThreads / kTileRows)) {
-      const uint32_t at = mine + (t * kTileRows + tid % kTileRows) * 4;
-      float sum = 0.0f;
-      for (int r = 0; r < a.split; ++r) sum += tc::ld_dsmem(tc::map_rank(at, r));
-      if (i < a.l.n) fp4_store(a.l, t0 + t, i, sum, a.l.alpha, fp4_bias(a.l, i));
+    if (shares && i < a.l.n) {
+      const float bias = fp4_bias(a.l, i);
+      for (int t = rank + a.size * (tid / kTileRows); t < kTok && t0 + t < a.l.T; t += a.size * (R::kThreads / kTileRows)) {
+        const uint32_t at = mine + (t * kTileRows + tid % kTileRows) * 4;
+        float v[kMostCluster], sum = 0.0f;
+#pragma unroll
+        for (int r = 0; r < kMostCluster; ++r) v[r] = r < a.size ? tc::ld_dsmem(tc::map_rank(at, r)) : 0.0f;
+#pragma unroll
+        for (int r = 0; r < kMostCluster; ++r) sum += v[r];
+        fp4_store(a.l, t0 + t, i, sum, a.l.alpha, bias);
+      }
     }
     tc::cluster_sync();
   }
@@ -364,6 +397,30 @@ Encode encoder() {
   return f;
 }
 
+// Clusters of c CTAs that the device runs at once.
+template <int kTok>
+int clusters_of(int c) {
+  using R = Rings<kTok>;
+  static std::atomic<int> known[64][kMostCluster + 1];  // and 1
+  int device = 0;
+  if (cudaGetDevice(&device) != cudaSuccess || device < 0 || device >= 64) return 0;
+  int n = known[device][c].load(std::memory_order_relaxed);
+  if (n) return n - 1;
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr = {};
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = c, attr.val.clusterDim.y = 1, attr.val.clusterDim.z = 1;
+  cfg.gridDim = dim3(c), cfg.blockDim = dim3(R::kThreads), cfg.dynamicSmemBytes = R::kSmem;
+  cfg.attrs = &attr, cfg.numAttrs = 1;
+  if (cudaOccupancyMaxActiveClusters(&n, fp4_tiles_kernel<kTok>, &cfg) != cudaSuccess) {
+    (void)cudaGetLastError();
+    n = 0;
+  }
+  n = std::min(n, num_sms() / c);
+  known[device][c].store(n + 1, std::memory_order_relaxed);
+  return n;
+}
+
 template <int kTok>
 cudaError_t launch_of(const Fp4Linear& l, cudaStream_t stream) {
   using R = Rings<kTok>;
@@ -380,15 +437,26 @@ cudaError_t launch_of(const Fp4Linear& l, cudaStream_t stream) {
              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
     return cudaErrorInvalidValue;
-  TileArgs a{l, fp4_row_tiles(l.n), 0, 1};
+  TileArgs a{l, fp4_row_tiles(l.n), 0, 1, 0, {}, {}};
   a.l.alpha *= kFp4Unit;
   const int64_t tiles = (int64_t)a.row_tiles * ((l.T + kTok - 1) / kTok);
   if (tiles > INT32_MAX / 8) return cudaErrorInvalidValue;
   a.tiles = (int)tiles;
+  // Whole tiles as long as every CTA has one; a cluster divides each tile of the last wave where that
+  // ends sooner by a tenth, in steps, of which the join of so many sums takes about kJoin.
+  constexpr int kJoin = kTok / 8 < 12 ? kTok / 8 : 12;
   const int sms = num_sms();
-  if (2 * tiles <= sms) a.split = (int)std::max<int64_t>(1, std::min<int64_t>({8, sms / tiles, l.k_blocks}));
-  const int ctas = a.split > 1 ? a.tiles * a.split : std::min(a.tiles, sms);
-  return launch_k(kern, dim3(ctas), dim3(R::kThreads), R::kSmem, stream, a.split > 1 ? a.split : 0, map, a);
+  int ctas = std::min(a.tiles, sms);
+  int64_t least = (int64_t)((a.tiles + sms - 1) / sms) * l.k_blocks * 10 / 11;
+  for (int c = 2; c <= std::min(kMostCluster, l.k_blocks); ++c) {
+    const int n = clusters_of<kTok>(c), whole = n ? a.tiles / (n * c) : 0, rest = n ? a.tiles % (n * c) : 0;
+    const int64_t steps = (int64_t)whole * l.k_blocks + (l.k_blocks + c - 1) / c + kJoin;
+    if (rest == 0 || rest > n || steps > least) continue;
+    least = steps, a.size = c, a.whole = whole, ctas = (whole ? n : rest) * c;
+  }
+  if (a.size == 1) a.whole = a.tiles / ctas;
+  a.by_rows = divisor(a.row_tiles), a.by_size = divisor(a.size);
+  return launch_k(kern, dim3(ctas), dim3(R::kThreads), R::kSmem, stream, a.size > 1 ? a.size : 0, map, a);
 }
 
 }  // namespace

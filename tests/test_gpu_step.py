@@ -68,6 +68,13 @@ def test_linear(T, k, n, f32):
     assert (room[T:] == 7).all() and (room[:, n:] == 7).all()
 
 
+@pytest.mark.parametrize("f32", [False, True])
+@pytest.mark.parametrize("T,k,n", [(20, 784, 20470), (50, 1552, 20480), (100, 2320, 20400), (1270, 2320, 4000)])
+def test_linear_where_some_tiles_are_left_for_a_last_wave(T, k, n, f32):
+    """160 tiles: each CTA has one, and clusters divide what is left."""
+    test_linear(T, k, n, f32)
+
+
 @pytest.mark.parametrize("T,k,n", [(1, 4096, 300), (8, 1280, 4096), (8, 4096, 39000), (11, 2048, 700), (16, 4096, 39000),
                                    (24, 1280, 3000), (40, 4096, 2560), (100, 4096, 640), (256, 1280, 1024), (700, 512, 2000)])
 def test_linear_of_whole_numbers_is_exact(T, k, n):

@@ -13,8 +13,8 @@
 //    maximum reaches it are read again, and the logits that do are listed.  In the end
 //    those that reach the last bound are ranked by counting.  Where ties make the list
 //    too long, the best are found one by one.
-//  - beam_join_kernel: a CTA a group adds the parts' sums in fp64, forms the candidates'
-//    scores in fp64 and ranks them in the same way, by (score, beam, token).
+//  - beam_join_kernel: a CTA a group adds the parts' sums as sums of two fp32, forms the
+//    candidates' scores in fp64 and ranks them in the same way, by (score, beam, token).
 #include <algorithm>
 
 #include "kv.cuh"
@@ -23,13 +23,14 @@ namespace csa2 {
 namespace {
 
 constexpr int kMost = 64;  // take, beams
-// part: warps of a CTA, 16-byte vectors of a lane in a window, windows of a warp, list of a warp
-constexpr int kPartWarps = 4, kN = 8, kMostWindows = 8, kPartList = 512;
+// part: warps of a CTA, 16-byte vectors of a lane in a window, list of a warp, windows of a warp
+constexpr int kPartWarps = 4, kN = 8, kPartList = 512;
+__host__ __device__ constexpr int most_windows(int take) { return take > 32 ? 4 : 8; }  // (what they list fits kPartList)
 // join
 constexpr int kThreads = 512, kWarps = kThreads / 32, kList = 2048;
 
 struct PartSum {
-  double sum;  // of exp(x - most)
+  float sum, low;  // of exp(x - most), as the sum of two fp32
   float most, pad;
 };
 struct BeamArgs {
@@ -114,15 +115,15 @@ struct Held {
   }
 };
 
-template <bool kBf16>
-__global__ void __launch_bounds__(32 * kPartWarps, 7) beam_part_kernel(const BeamArgs a) {
+// kMany: more than 32 to take.
+template <bool kBf16, bool kMany>
+__global__ void __launch_bounds__(32 * kPartWarps, kMany ? 6 : 7) beam_part_kernel(const BeamArgs a) {
   using H = Held<kBf16>;
   constexpr int kVec = H::kVec;
   constexpr uint32_t kAll = 0xffffffffu;
   __shared__ uint2 lists[kPartWarps][kPartList];
   __shared__ int counts[kPartWarps];
   griddep_wait();    // every input may be the previous kernel's output
-  griddep_launch();  // (the join waits for this kernel, and alone writes a call's outputs)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int at = blockIdx.x * kPartWarps + warp, row = quotient(at, a.by_parts);
   if (row >= a.groups * a.beams) return;  // (whole warps)
@@ -130,7 +131,7 @@ __global__ void __launch_bounds__(32 * kPartWarps, 7) beam_part_kernel(const Bea
     const bool has = at == row * a.parts;
     for (int r = lane; r < a.take; r += 32)
       a.part_best[(int64_t)at * a.take + r] = make_uint2(has && r == 0 ? kDone : kNone, (uint32_t)a.end_token);
-    if (lane == 0) a.part_sum[at] = has ? PartSum{1.0, 0.0f, 0.0f} : PartSum{0.0, -INFINITY, 0.0f};
+    if (lane == 0) a.part_sum[at] = has ? PartSum{1.0f, 0.0f, 0.0f, 0.0f} : PartSum{0.0f, 0.0f, -INFINITY, 0.0f};
     return;
   }
   // Values [v0, v1) of the row: whole 16 bytes of memory from v0 + head on, and what is
@@ -210,6 +211,21 @@ __global__ void __launch_bounds__(32 * kPartWarps, 7) beam_part_kernel(const Bea
           if (__popc(__ballot_sync(kAll, k0 >= (b | 1u << i))) + __popc(__ballot_sync(kAll, k1 >= (b | 1u << i))) >= a.take)
             b |= 1u << i;
       }
+      if constexpr (kMany) {
+        // the last of 64 maxima is a weak bound (of 2048 logits 250 reach it, at times more than
+        // the list holds, and one such warp took 500 us): of 128, the window's alone, 87
+        uint32_t k[kN / 2], w = 0;
+#pragma unroll
+        for (int j = 0; j < kN / 2; ++j) k[j] = key_of(fmaxf(vm[2 * j], vm[2 * j + 1]));
+#pragma unroll 1
+        for (int i = 31; i >= 16; --i) {
+          int reach = 0;
+#pragma unroll
+          for (int j = 0; j < kN / 2; ++j) reach += __popc(__ballot_sync(kAll, k[j] >= (w | 1u << i)));
+          if (reach >= a.take) w |= 1u << i;
+        }
+        b = max(b, w);
+      }
       bound = max(bound, b);
       const float least = of_key(bound);
 #pragma unroll
@@ -251,10 +267,13 @@ __global__ void __launch_bounds__(32 * kPartWarps, 7) beam_part_kernel(const Bea
     }
     __syncwarp();
   }
+  // (the join waits for this kernel, and alone writes a call's outputs; let in at the beginning, its
+  // CTAs gather on the SMs that have room first)
+  griddep_launch();
   if (bad) report(a.status, CSA2_ERR_RANGE);
 #pragma unroll
   for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(kAll, sum, d);
-  if (lane == 0) a.part_sum[at] = PartSum{sum, top, 0.0f};
+  if (lane == 0) a.part_sum[at] = PartSum{(float)sum, (float)(sum - (double)(float)sum), top, 0.0f};
   uint2* out = a.part_best + (int64_t)at * a.take;
   int c = counts[warp];
   __syncwarp();
@@ -308,12 +327,27 @@ __global__ void __launch_bounds__(32 * kPartWarps, 7) beam_part_kernel(const Bea
   }
 }
 
-// Natural logarithm of s >= 1/2, off by 2^-29 at most, nearly all of it in fp32 (the library's in
-// fp64 took 3000 cycles): s = 2^e m, m in [2/3, 4/3); log m = 2 (z + z^3 / 3 + z^5 / 5 ..) with
-// z = (m - 1) / (m + 1), |z| <= 1/5, as a sum of two fp32, and what s has beyond fp32.
-__device__ __forceinline__ double log_of(double s) {
-  const float h = (float)s;
-  const float rest = (float)(s - (double)h) / h;
+// s + low times f, and the sum of two, as sums of two fp32 (Dekker, Knuth).  An addition in fp64
+// takes longer here than these six.
+__device__ __forceinline__ void scale2(float& s, float& low, float f) {
+  const float p = __fmul_rn(s, f);
+  low = fmaf(low, f, fmaf(s, f, -p)), s = p;
+}
+__device__ __forceinline__ void sum2(float& s, float& low, float t, float t_low) {
+  const float r = __fadd_rn(s, t), u = __fsub_rn(r, s);
+  const float e = __fadd_rn(__fsub_rn(s, __fsub_rn(r, u)), __fsub_rn(t, u)) + (low + t_low);
+  s = __fadd_rn(r, e), low = __fsub_rn(e, __fsub_rn(s, r));
+}
+
+// Natural logarithm of h + l >= 1/2 as e log 2 + z + rest, off by 2^-29 at most (the
+// library's in fp64 took 3000 cycles): h = 2^e m, m in [2/3, 4/3); log m = 2 (z + z^3 / 3 +
+// z^5 / 5 ..) with z = (m - 1) / (m + 1), |z| <= 1/5, as a sum of two fp32, and what there is
+// beside h.
+struct Log {
+  float e, z, rest;
+  __device__ __forceinline__ double exact() const { return fma((double)e, 0.693147180559945309, (double)z) + (double)rest; }
+};
+__device__ __forceinline__ Log log_of(float h, float l) {
   const int bits = __float_as_int(h), e = (bits - 0x3F2AAAABu) >> 23;
   const float m = __int_as_float(bits - (e << 23));
   const float f = m - 1.0f, g = m + 1.0f, gl = m - (g - 1.0f);  // g + gl = m + 1
@@ -321,7 +355,7 @@ __device__ __forceinline__ double log_of(double s) {
   const float zl = (fmaf(-z, g, f) - z * gl) / g;
   const float w = z * z;
   const float tail = z * w * fmaf(w, fmaf(w, fmaf(w, fmaf(w, fmaf(w, 1.0f / 13, 1.0f / 11), 1.0f / 9), 1.0f / 7), 1.0f / 5), 1.0f / 3);
-  return fma((double)e, 0.693147180559945309, (double)(2.0f * z)) + (double)(2.0f * (zl + tail) + rest);
+  return Log{(float)e, 2.0f * z, 2.0f * (zl + tail) + l / h};
 }
 
 // fp64 -> unsigned in the same order (no -0 comes here).
@@ -332,10 +366,9 @@ __device__ __forceinline__ uint64_t key_of(double x) {
 constexpr uint64_t kNone64 = 0x000FFFFFFFFFFFFFull;  // of -inf
 
 __global__ void __launch_bounds__(kThreads) beam_join_kernel(const BeamArgs a) {
-  __shared__ double sums[kMost], logs[kMost];  // of exp(x - most), their logarithms
-  __shared__ float most[kMost];
-  __shared__ double cums[kMost];
-  __shared__ float cums32[kMost], logs32[kMost];
+  __shared__ float sums[kMost], lows[kMost];  // of exp(x - most)
+  __shared__ Log logs[kMost];
+  __shared__ float most[kMost], cums[kMost], logs32[kMost];
   __shared__ uint32_t best[64];
   __shared__ uint32_t bound, far, count;
   __shared__ uint64_t lkey[kList];
@@ -354,10 +387,10 @@ __global__ void __launch_bounds__(kThreads) beam_join_kernel(const BeamArgs a) {
     // relative to the beam's largest (beside logits near fp32's lowest the rest would be
     // lost), what fp64 adds exactly first
     const double x = e.x == kDone ? 0.0 : (double)of_key(e.x) - (double)most[beam];
-    return e.x <= kNone ? -(double)INFINITY : x + cums[beam] - logs[beam];
+    return e.x <= kNone ? -(double)INFINITY : x + (double)cums[beam] - logs[beam].exact();
   };
   auto near_of = [&](uint2 e, int beam) {
-    return e.x <= kNone ? -INFINITY : (e.x == kDone ? 0.0f : of_key(e.x) - most[beam]) + cums32[beam] - logs32[beam];
+    return e.x <= kNone ? -INFINITY : (e.x == kDone ? 0.0f : of_key(e.x) - most[beam]) + cums[beam] - logs32[beam];
   };
   auto beam_of = [&](int list) { return quotient(list, a.by_parts); };
   // (asked for ahead of the beams' sums; neighbouring samples in different groups)
@@ -367,23 +400,27 @@ __global__ void __launch_bounds__(kThreads) beam_join_kernel(const BeamArgs a) {
   float cum = tid < a.beams ? a.cum[row0 + tid] : 0.0f;
   {  // the beams' sums: eight threads a beam
     const int k = tid >> 3;
-    float m = -INFINITY;
-    double s = 0.0;
+    float m = -INFINITY, s = 0.0f, low = 0.0f;
     if (k < a.beams)
       for (int p = tid & 7; p < a.parts; p += 8) {
         const PartSum e = a.part_sum[(row0 + k) * a.parts + p];
-        if (e.most > m) s *= (double)ex2((m - e.most) * kLog2e), m = e.most;
-        if (e.most > -INFINITY) s += e.sum * (double)ex2((e.most - m) * kLog2e);
+        if (e.most > m) scale2(s, low, ex2((m - e.most) * kLog2e)), m = e.most;
+        if (e.most > -INFINITY) {
+          float t = e.sum, t_low = e.low;
+          scale2(t, t_low, ex2((e.most - m) * kLog2e));
+          sum2(s, low, t, t_low);
+        }
       }
     float all = m;
 #pragma unroll
     for (int d = 1; d < 8; d <<= 1) all = fmaxf(all, __shfl_xor_sync(0xffffffffu, all, d));
-    if (__any_sync(0xffffffffu, k < a.beams)) {
-      if (all > -INFINITY) s *= (double)ex2((m - all) * kLog2e);
+    if (all > -INFINITY) scale2(s, low, ex2((m - all) * kLog2e));
 #pragma unroll
-      for (int d = 1; d < 8; d <<= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
+    for (int d = 1; d < 8; d <<= 1) {
+      const float t = __shfl_xor_sync(0xffffffffu, s, d), t_low = __shfl_xor_sync(0xffffffffu, low, d);
+      sum2(s, low, t, t_low);
     }
-    if ((tid & 7) == 0) sums[k] = s, most[k] = all;
+    if ((tid & 7) == 0) sums[k] = s, lows[k] = low, most[k] = all;
   }
   if (tid == 0) count = 0, far = 0;
   __syncthreads();
@@ -394,37 +431,46 @@ __global__ void __launch_bounds__(kThreads) beam_join_kernel(const BeamArgs a) {
     bool bad = false;
     cum = clean(cum, bad);
     if (bad) report(a.status, CSA2_ERR_RANGE);
-    double s = sums[tid];
+    float s = sums[tid], low = lows[tid];
     for (int b = tid - 1; b >= 0; --b)
-      if (most[b] == most[tid] && fabs(sums[b] - sums[tid]) <= 0x1p-20 * sums[tid]) s = sums[b];
+      if (most[b] == most[tid] && fabsf((sums[b] - sums[tid]) + (lows[b] - lows[tid])) <= 0x1p-20f * sums[tid])
+        s = sums[b], low = lows[b];
     const bool some = most[tid] > -INFINITY;
-    logs[tid] = some ? log_of(s) : 0.0;
-    cums[tid] = some ? (double)cum + 0.0 : -(double)INFINITY;
-    cums32[tid] = some ? cum : -INFINITY, logs32[tid] = (float)logs[tid];
-    if (some && cum > -INFINITY) atomicMax(&far, __float_as_uint(fabsf(cum) + logs32[tid] + 1.0f));  // (sums are 1 at least)
-    if (a.lse) a.lse[row0 + tid] = some ? (float)((double)most[tid] + logs[tid]) : -INFINITY;
+    const Log l = some ? log_of(s, low) : Log{0.0f, 0.0f, 0.0f};
+    const float near = fmaf(l.e, 0.693147181f, l.z) + l.rest;
+    logs[tid] = l, logs32[tid] = near;
+    cums[tid] = some ? cum + 0.0f : -INFINITY;
+    if (some && cum > -INFINITY) atomicMax(&far, __float_as_uint(fabsf(cum) + near + 1.0f));  // (sums are 1 at least)
   }
   __syncthreads();
   uint32_t top = sample0 < samples ? key_of(near_of(raw0, beam_of(sample0 % lists))) : kNone;
   for (int i = sample0 + kThreads; i < samples; i += kThreads)
     top = max(top, key_of(near_of(mine[(i % lists) * a.take + i / lists], beam_of(i % lists))));
+  if (a.take <= 16) {
 #pragma unroll
-  for (int d = 1; d < 8; d <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, d));
-  if ((tid & 7) == 0) best[tid >> 3] = top;
-  __syncthreads();
-  {  // eight threads rank a maximum
-    const int i = tid >> 3, j0 = (tid & 7) * 8;
-    int rank = 0;
+    for (int d = 1; d < 8; d <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, d));
+    if ((tid & 7) == 0) best[tid >> 3] = top;
+    __syncthreads();
+    {  // eight threads rank a maximum
+      const int i = tid >> 3, j0 = (tid & 7) * 8;
+      int rank = 0;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) rank += best[j0 + j] > top || (best[j0 + j] == top && j0 + j < i);
+      for (int j = 0; j < 8; ++j) rank += best[j0 + j] > top || (best[j0 + j] == top && j0 + j < i);
 #pragma unroll
-    for (int d = 1; d < 8; d <<= 1) rank += __shfl_xor_sync(0xffffffffu, rank, d);
-    if ((tid & 7) == 0 && rank == a.take - 1) bound = top;
+      for (int d = 1; d < 8; d <<= 1) rank += __shfl_xor_sync(0xffffffffu, rank, d);
+      if ((tid & 7) == 0 && rank == a.take - 1) bound = top;
+    }
+    __syncthreads();
+  } else {
+    // (of 64 maxima the last few are weak bounds: of all threads', to 20 bits)
+    uint32_t b = 0;
+    for (int i = 31; i >= 12; --i)
+      if (__syncthreads_count(top >= (b | 1u << i)) >= a.take) b |= 1u << i;
+    if (tid == 0) bound = b;
+    __syncthreads();
   }
-  __syncthreads();
-  // Three roundings, and those of cum's and the logarithm's: of terms that are no larger than
-  // the score, cum and the logarithm together, each 2^-24 of it; twice, for the bound's and
-  // a candidate's.
+  // Three roundings, and the logarithm's three: of terms that are no larger than the score, cum
+  // and the logarithm together, each 2^-24 of it; twice, for the bound's and a candidate's.
   const float reach = of_key(bound);
   const float least = bound <= kNone ? -INFINITY : reach - 0x1p-20f * (fabsf(reach) + __uint_as_float(far));
   for (int i = sample0; i < samples; i += kThreads) {
@@ -451,13 +497,21 @@ __global__ void __launch_bounds__(kThreads) beam_join_kernel(const BeamArgs a) {
     a.scores[o] = -INFINITY, a.parents[o] = -1, a.tokens[o] = -1;
   };
   const int n = (int)count;
+  // (by the last warps, which have less to do in what follows)
+  if (a.lse && tid >= kThreads - kMost && tid - (kThreads - kMost) < a.beams) {
+    const int k = tid - (kThreads - kMost);
+    a.lse[row0 + k] = most[k] > -INFINITY ? (float)((double)most[k] + logs[k].exact()) : -INFINITY;
+  }
   if (n <= kList) {
-    for (int p = tid; p < n; p += kThreads) {
-      const uint64_t k = lkey[p], e = lplace[p];
+    for (int p0 = 0; p0 < n; p0 += kThreads / 8) {  // eight threads rank a candidate
+      const int p = p0 + (tid >> 3);
+      const uint64_t k = lkey[min(p, n - 1)], e = lplace[min(p, n - 1)];
       int rank = 0;
-#pragma unroll 8
-      for (int q = 0; q < n; ++q) rank += lkey[q] > k || (lkey[q] == k && lplace[q] < e);
-      if (rank < a.take) put(rank, k, (uint32_t)(e >> 32), (uint32_t)e);
+#pragma unroll 4
+      for (int q = tid & 7; q < n; q += 8) rank += (int)(lkey[q] > k) | ((int)(lkey[q] == k) & (int)(lplace[q] < e));
+#pragma unroll
+      for (int d = 1; d < 8; d <<= 1) rank += __shfl_xor_sync(0xffffffffu, rank, d);
+      if ((tid & 7) == 0 && p < n && rank < a.take) put(rank, k, (uint32_t)(e >> 32), (uint32_t)e);
     }
     for (int r = n + tid; r < a.take; r += kThreads) none(r);
     return;
@@ -490,7 +544,7 @@ __global__ void __launch_bounds__(kThreads) beam_join_kernel(const BeamArgs a) {
   }
 }
 
-// Parts of a row, all of like size, of 1 to kMostWindows windows: those of least time, of
+// Parts of a row, all of like size, of 1 to most_windows() windows: those of least time, of
 // which a window takes a warp 5 parts alone and 9 more with the SM full (28 warps; 1.25 and
 // 2.25 us), and its start a window.  512 rows of 128001 in bf16 take 37.1 us in 8 parts,
 // one wave of 27 warps an SM, and 43.6 in 9, which begin a second one.  (152 SMs by number, and
@@ -500,17 +554,18 @@ struct Parts {
   int n, size;
 };
 int windows_of(int vocab, bool bf16) { return (vocab - 1) / (kN * 32 * (bf16 ? 8 : 4)) + 1; }
-int64_t most_results(int64_t rows, int vocab) {
+int64_t most_results(int64_t rows, int vocab, int take) {
   const int64_t windows = windows_of(vocab, false);
-  return std::max(rows * ((windows + kMostWindows - 1) / kMostWindows), std::min<int64_t>(rows * windows, 8192));
+  const int each = most_windows(take);
+  return std::max(rows * ((windows + each - 1) / each), std::min<int64_t>(rows * windows, 8192));
 }
-Parts parts_of(int64_t rows, int vocab, bool bf16) {
+Parts parts_of(int64_t rows, int vocab, int take, bool bf16) {
   constexpr int64_t kWave = 152 * 28;
   const int vec = bf16 ? 8 : 4, windows = windows_of(vocab, bf16);
-  const int64_t most = most_results(rows, vocab);
+  const int64_t most = most_results(rows, vocab, take);
   int n = 0;
   double least = INFINITY;
-  for (int each = 1; each <= kMostWindows; ++each) {
+  for (int each = 1; each <= most_windows(take); ++each) {
     const int64_t parts = (windows + each - 1) / each, warps = rows * parts;
     if (warps > most) continue;
     const double time = (each + 1) * (5.0 * (double)((warps + kWave - 1) / kWave) + 9.0 * (double)warps / (double)kWave);
@@ -525,8 +580,8 @@ bool sizes_fit(int32_t groups, int32_t beams, int32_t vocab, int32_t take) {
   // (a part's end is its beginning and its size, in 32 bits)
   if (beams > kMost || take > kMost || vocab > (1 << 30) || (int64_t)groups * beams > INT32_MAX) return false;
   // (a group's lists, times take, are numbered in 32 bits too)
-  return most_results((int64_t)groups * beams, vocab) <= INT32_MAX - kPartWarps &&
-         most_results(beams, vocab) * take <= INT32_MAX / 2;
+  return most_results((int64_t)groups * beams, vocab, take) <= INT32_MAX - kPartWarps &&
+         most_results(beams, vocab, take) * take <= INT32_MAX / 2;
 }
 size_t sums_bytes(int64_t results) { return (size_t)((results * sizeof(PartSum) + 255) / 256 * 256); }
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
@@ -540,7 +595,7 @@ extern "C" {
 
 size_t csa2_beam_workspace_bytes(int32_t groups, int32_t beams, int32_t vocab, int32_t take) {
   if (!sizes_ok(groups, beams, vocab, take) || !sizes_fit(groups, beams, vocab, take)) return 0;
-  const int64_t results = most_results((int64_t)groups * beams, vocab);
+  const int64_t results = most_results((int64_t)groups * beams, vocab, take);
   return sums_bytes(results) + (size_t)(results * take) * sizeof(uint2);
 }
 
@@ -559,14 +614,16 @@ int32_t csa2_beam_select(int32_t groups, int32_t beams, int32_t vocab, int32_t t
   if (!workspace || workspace_bytes < csa2_beam_workspace_bytes(groups, beams, vocab, take)) return CSA2_ERR_CAPACITY;
   const int64_t rows = (int64_t)groups * beams;
   const bool bf16 = logits_dtype == CSA2_BF16;
-  const Parts parts = parts_of(rows, vocab, bf16);
+  const Parts parts = parts_of(rows, vocab, take, bf16);
   BeamArgs a{groups, beams, vocab, take, parts.n, parts.size, divisor(parts.n), logits, stride, cum, done, end_token, scores,
              parents, tokens, lse, static_cast<PartSum*>(workspace),
              reinterpret_cast<uint2*>(static_cast<uint8_t*>(workspace) + sums_bytes(rows * parts.n)), status};
   const dim3 grid((unsigned)((rows * parts.n + kPartWarps - 1) / kPartWarps)), block(32 * kPartWarps);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  cudaError_t e = bf16 ? launch_k(beam_part_kernel<true>, grid, block, 0, s, 0, a)
-                       : launch_k(beam_part_kernel<false>, grid, block, 0, s, 0, a);
+  cudaError_t e = take > 32 ? (bf16 ? launch_k(beam_part_kernel<true, true>, grid, block, 0, s, 0, a)
+                                    : launch_k(beam_part_kernel<false, true>, grid, block, 0, s, 0, a))
+                            : (bf16 ? launch_k(beam_part_kernel<true, false>, grid, block, 0, s, 0, a)
+                                    : launch_k(beam_part_kernel<false, false>, grid, block, 0, s, 0, a));
   if (e == cudaSuccess) e = launch_k(beam_join_kernel, dim3(groups), dim3(kThreads), 0, s, 0, a);
   return e == cudaSuccess ? CSA2_OK : CSA2_ERR_CUDA;
 }

@@ -431,7 +431,7 @@ cudaError_t launch_of(const Fp4Linear& l, cudaStream_t stream) {
   const Encode encode = encoder();
   if (!encode) return cudaErrorNotSupported;
   CUtensorMap map;
-  const cuuint64_t dims[2] = {(cuuint64_t)l.k, (cuuint64_t)l.T}, strides[1] = {(cuuint64_t)l.x_stride * 2};
+  const cuuint64_t dims[2] = {(cuuint64_t)l.k, (cuuint64_t)l.T}, strides[1] = {(cuuint64_t)(l.T > 1 ? l.x_stride : l.k) * 2};
   const cuuint32_t box[2] = {64, kTok}, unit[2] = {1, 1};
   if (encode(&map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<uint16_t*>(l.x), dims, strides, box, unit,
              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,

@@ -1,5 +1,9 @@
 """The operators of a generation step on the GPU against their plain restatement in 64 bits: projections with 4-bit
 weights, appends with positions of several axes, beam selection, reordering of cached beams, and a run of all of them."""
+import os
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 import torch
@@ -66,6 +70,18 @@ def test_linear(T, k, n, f32):
         tol = tol * (1 + 2.0 ** -8) + 2.0 ** -8 * np.abs(y)
     assert (np.abs(got - y) <= tol).all(), float((np.abs(got - y) / tol).max())
     assert (room[T:] == 7).all() and (room[:, n:] == 7).all()
+
+
+@pytest.mark.parametrize("k", [400, 100000])
+def test_a_single_row_has_no_stride(k):
+    rng = np.random.default_rng(k)
+    w, plain = _packed(rng, 40, k)
+    x = _dev(_kv.normal(rng, 1, k))
+    out = [torch.empty(1, 40, device="cuda") for _ in range(2)]
+    csa.fp4_linear(x, w, out[0])
+    assert csa.load().csa2_fp4_linear(w._ref, 1, x.data_ptr(), 1 << 60, None, out[1].data_ptr(), 1, 1 << 60, None,
+                                      torch.cuda.current_stream().cuda_stream) == 0
+    assert torch.equal(out[0], out[1])
 
 
 @pytest.mark.parametrize("f32", [False, True])
@@ -400,6 +416,44 @@ def test_beams_beyond_32_bits_of_logits():
     z = [np.logaddexp(others, a) for a in (9.0, 8.0, -4.0)]
     assert parents.tolist() == [[rows - 1, 3, 0]] and tokens.tolist() == [[vocab - 7, 59_000_001, 0]]
     assert np.allclose(scores.cpu().numpy(), [[9 - z[0], 8 - z[1], -4 - z[2]]], rtol=0, atol=1e-5)
+
+
+FIRST = """
+import sys, torch
+import compressed_sparse_attention_07_gb300 as csa
+rows = int(sys.argv[1])
+torch.manual_seed(rows)
+w = csa.Fp4Weights.encode(torch.randn(20480, 1280, device="cuda").bfloat16())
+x = torch.randn(rows, 1280, device="cuda").bfloat16()
+out, again = (torch.full((rows, 20480), 5.0, device="cuda") for _ in range(2))
+cum = torch.zeros(rows // 4, 4, device="cuda")
+s, p, t = (torch.zeros(rows // 4, 40, dtype=d, device="cuda") for d in (torch.float32, torch.int32, torch.int32))
+ws = torch.empty(csa.beam_workspace_bytes(rows // 4, 4, 20480, 40), dtype=torch.uint8, device="cuda")
+
+def step():
+    csa.fp4_linear(x, w, out)
+    csa.beam_select(out, cum, s, p, t, ws)
+
+g = torch.cuda.CUDAGraph()
+torch.cuda.synchronize()
+with torch.cuda.graph(g):
+    step()
+g.replay()
+csa.fp4_linear(x, w, again)
+torch.cuda.synchronize()
+assert torch.equal(out, again)
+best, at = again.view(rows // 4, -1).double().sub(torch.logsumexp(again.double(), 1).view(rows // 4, 4, 1).expand(-1, -1, 20480).reshape(rows // 4, -1)).topk(40)
+# half a step of a score below 128 (2^-18) and the exponentials' 2^-20
+assert best.min() > -128 and (s.double() - best).abs().max() < 2.0 ** -18 + 2.0 ** -20
+print("fine")
+"""
+
+
+@pytest.mark.parametrize("rows", [8, 20, 64, 516])
+def test_the_first_calls_of_a_process_inside_a_capture(rows):
+    run = subprocess.run([sys.executable, "-c", FIRST, str(rows)], capture_output=True, text=True, timeout=300,
+                         cwd=os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
+    assert run.returncode == 0 and run.stdout.strip() == "fine", run.stderr[-2000:]
 
 
 def test_beams_in_graphs_on_two_streams():

@@ -418,6 +418,21 @@ def test_beams_beyond_32_bits_of_logits():
     assert np.allclose(scores.cpu().numpy(), [[9 - z[0], 8 - z[1], -4 - z[2]]], rtol=0, atol=1e-5)
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("vocab,take", [(30, 64), (5000, 17), (9000, 33), (40001, 64)])
+def test_beams_with_fewer_candidates_than_are_taken(vocab, take, dtype):
+    rng = np.random.default_rng(vocab)
+    x = torch.full((6, vocab), -float("inf"), dtype=dtype, device="cuda")
+    x[0, vocab // 2], x[1, 0], x[4, vocab - 1] = 1.0, -2.0, torch.finfo(dtype).min
+    x[5, :9] = _dev(rng.standard_normal(9), dtype)
+    cum = _dev(rng.standard_normal((2, 3)), torch.float32)
+    _check_beams(x, cum, take)
+    _check_beams(x, cum, take, _dev(np.array([[0, 1, 0], [1, 1, 0]]), torch.uint8), 3)
+    # a row whose logits are all alike beside them
+    x[2] = 0.5
+    _check_beams(x, cum, take)
+
+
 FIRST = """
 import sys, torch
 import compressed_sparse_attention_07_gb300 as csa

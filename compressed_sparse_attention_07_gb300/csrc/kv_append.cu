@@ -20,6 +20,8 @@
 //    their way by bulk copies, eight warps rotate, encode and store.  8 prompts
 //    of 37 .. 2021 tokens, 64 + 2 x 8 heads of 128, in FP4 take 66 us, 5.3 TB/s
 //    (107 us with a CTA for each piece, which waits for its look-ups).
+// With positions of three axes the same calls take 3.8 us (all of an append's GPU time in a
+// graph) and 67 us.
 #include <algorithm>
 
 #include "kv.cuh"

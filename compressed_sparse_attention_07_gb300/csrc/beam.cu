@@ -48,6 +48,7 @@ struct BeamArgs {
   PartSum* part_sum;  // [rows][parts]
   uint2* part_best;   // [rows][parts][take] logit bits, token
   int32_t* status;
+  int bf16, uneven;  // (of logits) uneven: a group's rows may begin differently far from 16 bytes
 };
 
 // fp32 -> unsigned in the same order; -inf -> 0x007FFFFF.
@@ -59,12 +60,10 @@ __device__ __forceinline__ float of_key(uint32_t k) { return __uint_as_float(k &
 constexpr uint32_t kNone = 0x007FFFFFu;  // of -inf
 constexpr uint32_t kDone = 0xFFFFFFFFu;  // of no number: what a beam that is done proposes
 
+__device__ __forceinline__ float counts_as(float x) { return x < INFINITY ? x : -INFINITY; }
 __device__ __forceinline__ float clean(float x, bool& bad) {
-  if (!(x < INFINITY)) {
-    bad = true;
-    return -INFINITY;
-  }
-  return x;
+  bad = bad || !(x < INFINITY);
+  return counts_as(x);
 }
 // The larger, NaN if one is.
 __device__ __forceinline__ float max_nan(float a, float b) {
@@ -365,10 +364,106 @@ __device__ __forceinline__ uint64_t key_of(double x) {
 }
 constexpr uint64_t kNone64 = 0x000FFFFFFFFFFFFFull;  // of -inf
 
+struct Likes {
+  uint32_t marks[kMost];
+  int of[kMost];  // whose sum a beam has: its own number, -1 without candidates
+  uint32_t set[2][2], differ[2][2];
+};
+// Of the beams in `set` those whose logits are beam b's; all threads.
+template <bool kBf16>
+__device__ __forceinline__ uint64_t same_rows(const BeamArgs& a, int64_t row0, int b, uint64_t set, Likes& likes) {
+  constexpr int kEach = 16;
+  const uint8_t* first = static_cast<const uint8_t*>(a.logits);
+  auto load = [&](int beam, int v0, float (&x)[kEach]) {
+    const uint8_t* row = first + (row0 + beam) * a.stride * (kBf16 ? 2 : 4);
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+      const int v = min(v0 + i * kThreads + (int)threadIdx.x, a.vocab - 1);
+      x[i] = kBf16 ? bf16_bits_to_float(__ldg(reinterpret_cast<const uint16_t*>(row) + v)) : __ldg(reinterpret_cast<const float*>(row) + v);
+    }
+  };
+  for (int v0 = 0, c = 0; v0 < a.vocab; v0 += kEach * kThreads, c ^= 1) {
+    float x[kEach], y[kEach];
+    uint64_t differ = 0;
+    load(b, v0, x);
+    for (uint64_t m = set; m; m &= m - 1) {
+      const int k = __ffsll((long long)m) - 1;
+      bool no = false;
+      load(k, v0, y);
+#pragma unroll
+      for (int i = 0; i < kEach; ++i) no |= counts_as(x[i]) != counts_as(y[i]);
+      if (no) differ |= 1ull << k;
+    }
+    if (differ) atomicOr(&likes.differ[c][0], (uint32_t)differ), atomicOr(&likes.differ[c][1], (uint32_t)(differ >> 32));
+    __syncthreads();
+    set &= ~((uint64_t)likes.differ[c][1] << 32 | likes.differ[c][0]);
+    if (!set) break;
+  }
+  return set;
+}
+// Beams whose logits are the same are given the same sum, so that their scores are ties.  Rows that
+// begin equally far from 16 bytes are summed alike to the last bit; this is for those that do not
+// (a.uneven), whose sums differ by 2^-16 at most: twice 33 additions of a window in fp32 (2^-19), and
+// exponents off by 2^-23 of themselves, of which those up to log 2^30 count (2^-18.6), in the terms and
+// where a larger logit rescales them.  Sums that near with the same largest logit are common (one likely
+// word: 1 and a little), so the rows themselves are compared, after a mark of each part's best (key,
+// token), which rarely agrees where rows differ.  All threads; `live`: beam tid has candidates.
+// Where all rows are the same, 64 x 8 of 128001 in bf16 take 156 us in place of 40.5, 16 x 5 of 51865 in
+// fp32 37 in place of 13.0; where sums are near and rows differ 43.0 and 14.9.
+__device__ __forceinline__ void share_sums(const BeamArgs& a, int64_t row0, bool live, float* sums, float* lows, const float* most,
+                                           Likes& likes) {
+  const int tid = threadIdx.x;
+  auto near = [&](int b, int k) {
+    return likes.of[b] == b && most[b] == most[k] && fabsf((sums[b] - sums[k]) + (lows[b] - lows[k])) <= 0x1p-15f * sums[k];
+  };
+  if (tid < kMost) likes.of[tid] = live ? tid : -1;
+  __syncthreads();
+  bool some = false;
+  if (live)
+    for (int b = 0; b < tid; ++b) some |= near(b, tid);
+  if (!__syncthreads_or(some)) return;
+  {  // eight threads a beam
+    const int k = tid >> 3;
+    uint32_t mark = 0;
+    if (k < a.beams)
+      for (int p = tid & 7; p < a.parts; p += 8) {
+        const uint2 e = a.part_best[((row0 + k) * a.parts + p) * a.take];
+        mark += (e.x ^ __funnelshift_l(e.y, e.y, 13)) * (0x9E3779B1u * (2 * p + 1));
+      }
+#pragma unroll
+    for (int d = 1; d < 8; d <<= 1) mark += __shfl_xor_sync(0xffffffffu, mark, d);
+    if ((tid & 7) == 0) likes.marks[k] = mark;
+  }
+  __syncthreads();
+  auto next = [&](int b) {  // the first from b on that may be beam tid's like
+    while (b < tid && !(near(b, tid) && likes.marks[b] == likes.marks[tid])) ++b;
+    return b < tid ? b : -1;
+  };
+  int like = live ? next(0) : -1;
+  for (int b = 0; b < a.beams - 1; ++b) {
+    if (tid < 64) {
+      const uint32_t m = __ballot_sync(0xffffffffu, like == b);
+      if ((tid & 31) == 0) likes.set[b & 1][tid >> 5] = m;
+    } else if (tid < 68) {
+      likes.differ[tid >> 1 & 1][tid & 1] = 0;
+    }
+    __syncthreads();
+    uint64_t set = (uint64_t)likes.set[b & 1][1] << 32 | likes.set[b & 1][0];
+    if (!set) continue;
+    set = a.bf16 ? same_rows<true>(a, row0, b, set, likes) : same_rows<false>(a, row0, b, set, likes);
+    const bool same = like == b && (set >> tid & 1);
+    if (same) sums[tid] = sums[b], lows[tid] = lows[b], likes.of[tid] = b;
+    __syncthreads();
+    if (like == b) like = same ? -1 : next(b + 1);
+  }
+  __syncthreads();
+}
+
 __global__ void __launch_bounds__(kThreads) beam_join_kernel(const BeamArgs a) {
   __shared__ float sums[kMost], lows[kMost];  // of exp(x - most)
   __shared__ Log logs[kMost];
   __shared__ float most[kMost], cums[kMost], logs32[kMost];
+  __shared__ Likes likes;
   __shared__ uint32_t best[64];
   __shared__ uint32_t bound, far, count;
   __shared__ uint64_t lkey[kList];
@@ -398,6 +493,7 @@ __global__ void __launch_bounds__(kThreads) beam_join_kernel(const BeamArgs a) {
   uint2 raw0 = make_uint2(0, 0);
   if (sample0 < samples) raw0 = mine[(sample0 % lists) * a.take + sample0 / lists];
   float cum = tid < a.beams ? a.cum[row0 + tid] : 0.0f;
+  const bool ended = tid < a.beams && a.done && a.done[row0 + tid];
   {  // the beams' sums: eight threads a beam
     const int k = tid >> 3;
     float m = -INFINITY, s = 0.0f, low = 0.0f;
@@ -424,17 +520,12 @@ __global__ void __launch_bounds__(kThreads) beam_join_kernel(const BeamArgs a) {
   }
   if (tid == 0) count = 0, far = 0;
   __syncthreads();
+  bool bad = false;
+  cum = clean(cum, bad);
+  if (bad) report(a.status, CSA2_ERR_RANGE);
+  if (a.uneven) share_sums(a, row0, tid < a.beams && !ended && cum > -INFINITY && most[tid] > -INFINITY, sums, lows, most, likes);
   if (tid < a.beams) {
-    // Beams whose logits are the same have the same sum.  What they have may differ in its
-    // last bits where their rows begin differently far from 16 bytes; so a beam that is
-    // like a lower one, by its largest logit and its sum to 2^-20, takes that one's.
-    bool bad = false;
-    cum = clean(cum, bad);
-    if (bad) report(a.status, CSA2_ERR_RANGE);
-    float s = sums[tid], low = lows[tid];
-    for (int b = tid - 1; b >= 0; --b)
-      if (most[b] == most[tid] && fabsf((sums[b] - sums[tid]) + (lows[b] - lows[tid])) <= 0x1p-20f * sums[tid])
-        s = sums[b], low = lows[b];
+    const float s = sums[tid], low = lows[tid];
     const bool some = most[tid] > -INFINITY;
     const Log l = some ? log_of(s, low) : Log{0.0f, 0.0f, 0.0f};
     const float near = fmaf(l.e, 0.693147181f, l.z) + l.rest;
@@ -617,7 +708,8 @@ int32_t csa2_beam_select(int32_t groups, int32_t beams, int32_t vocab, int32_t t
   const Parts parts = parts_of(rows, vocab, take, bf16);
   BeamArgs a{groups, beams, vocab, take, parts.n, parts.size, divisor(parts.n), logits, stride, cum, done, end_token, scores,
              parents, tokens, lse, static_cast<PartSum*>(workspace),
-             reinterpret_cast<uint2*>(static_cast<uint8_t*>(workspace) + sums_bytes(rows * parts.n)), status};
+             reinterpret_cast<uint2*>(static_cast<uint8_t*>(workspace) + sums_bytes(rows * parts.n)), status, bf16,
+             beams > 1 && stride % (bf16 ? 8 : 4) != 0};
   const dim3 grid((unsigned)((rows * parts.n + kPartWarps - 1) / kPartWarps)), block(32 * kPartWarps);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   cudaError_t e = take > 32 ? (bf16 ? launch_k(beam_part_kernel<true, true>, grid, block, 0, s, 0, a)

@@ -502,8 +502,9 @@ CSA2_API size_t csa2_beam_workspace_bytes(int32_t groups, int32_t beams, int32_t
  * are written in order (score descending; of equal scores the lower beam, then the
  * lower token): scores [groups][take] fp32, parents [groups][take] (the sequence
  * number g * beams + k) and tokens [groups][take] int32.  Scores are compared in
- * fp64, lse being summed from fp32 exponentials in fp64, and rounded once; beams whose
- * logits are the same have the same lse.
+ * fp64, lse being summed from fp32 exponentials in fp64, and rounded once; beams of a
+ * group whose logits are the same have the same lse where their cum is not -inf, so that
+ * their scores are ties.
  *  - A token of logit -inf (masked) and every token of a beam whose cum is -inf is
  *    no candidate; where candidates run out, score -inf, parent and token -1.
  *  - done [groups][beams] bytes or NULL: a beam that is done (not 0) has end_token

@@ -733,3 +733,53 @@ def test_a_captioner_writes_with_beams(dtype):
                     out, lse, *rest = _kv.attend(q[j:j + 1].double().cpu().numpy(), *stored[l][j], dim ** -0.5, True)
                     tol, _ = _kv.tolerances(cfg, n, out, lse, *rest)
                     assert (np.abs(o[j:j + 1].double().cpu().numpy() - out) <= tol).all()
+
+
+def _peaked_bound(x):
+    """Of rows whose largest stands alone, a bound on |log-sum-exp - largest - exact| in fp32: what is beside the largest is
+    off by 2^-22 and by its distance times 2^-22 (arguments of exponentials), and 2^-24 by rounding."""
+    x = np.asarray(x, np.float64)
+    d = np.where(np.isfinite(x), x, -1e4) - x.max(1, keepdims=True)
+    e = np.exp(d) * (d < 0)
+    return (e * (2.0 ** -22 + 2.0 ** -22 * np.abs(d))).sum(1) + 2.0 ** -24 * np.log1p(e.sum(1))
+
+
+@pytest.mark.parametrize("stride", [2, 3, 4, 5, 8])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_beams_with_the_same_largest_logit_keep_their_own_sums(dtype, stride):
+    """Two words, the second far below: the sums are 1 and a little, and the beam with less beside it comes first.  A beam
+    that is done beside them (its sum counts as 1 of a largest of 0) lends its sum to none."""
+    wide = torch.zeros(6, stride, dtype=dtype, device="cuda")
+    wide[:, 1] = torch.tensor([-14, -16.1, -15, -16.1, -14, -30], dtype=dtype)
+    x = wide[:, :2]
+    xs = x.double().cpu().numpy()
+    for cum in (torch.zeros(1, 6, device="cuda"), torch.zeros(3, 2, device="cuda")):
+        for done in (None, torch.zeros_like(cum, dtype=torch.uint8)):
+            if done is not None:
+                done.view(-1)[4] = 1
+            scores, parents, tokens, lse = _select(x, cum, 4, done, 1)
+            s, p, t, want, _ = _step.beam_select(xs, cum.double().cpu().numpy(), 4, None if done is None else done.cpu().numpy(), 1)
+            assert np.array_equal(parents.cpu().numpy(), p) and np.array_equal(tokens.cpu().numpy(), t)
+            off = _peaked_bound(xs)
+            assert (np.abs(lse.double().cpu().numpy() - want) <= off).all()
+            there = p >= 0
+            got = scores.double().cpu().numpy()
+            assert (np.abs(got[there] - s[there]) <= off[p[there]] + 2.0 ** -24 * np.abs(s[there])).all()
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("beams,vocab,pad", [(2, 9, 0), (5, 51865, 0), (8, 128001, 0), (64, 1003, 0), (16, 4099, 2), (8, 70000, 1)])
+def test_beams_of_the_same_logits_have_the_same_sums(beams, vocab, pad, dtype):
+    """Wherever their rows begin: ties go to the lower beam.  A row that differs in one
+    word is not the same."""
+    rng = np.random.default_rng(beams + vocab)
+    wide = torch.full((2 * beams, vocab + pad), float("nan"), dtype=dtype, device="cuda")
+    x = wide[:, :vocab]
+    x[:] = _dev(rng.standard_normal(vocab) * 3, dtype)
+    x[:, vocab // 2] = -0.0
+    x[1::2, vocab // 2] = 0.0
+    x[beams + 1, vocab // 4] = 5.5  # (in the second group; of 128001 words a change of 2e-5, and an error of 2^-18 at most)
+    cum = torch.full((2, beams), -3.5, device="cuda")
+    _check_beams(x, cum, min(64, 2 * beams))
+    lse = _select(x, cum, 4)[3].view(2, beams)
+    assert (lse[0] == lse[0, 0]).all() and (lse[1, [i for i in range(beams) if i != 1]] == lse[1, 0]).all()

@@ -230,20 +230,40 @@ __global__ void __launch_bounds__(32 * kPartWarps, kMany ? 6 : 7) beam_part_kern
 #pragma unroll
       for (int j = 0; j < kN; ++j) hits |= (vm[j] >= least ? 1u : 0u) << j;
       if (from == 0 && alone >= least) take_in(alone, odd);
-      // the sum, two at a time, in fp32 for a window
-      uint64_t sum2 = pack2(from == 0 ? ex2((alone - top) * kLog2e) : 0.0f, 0.0f);
-      const uint64_t minus = pack2(-top, -top), scale = pack2(kLog2e, kLog2e);
+      const float odd_one = from == 0 ? ex2((alone - top) * kLog2e) : 0.0f;
+      // The largest, 1 here, is counted apart where it stands alone: added in fp32 to what is beside it,
+      // it would leave that to 2^-24, and of two beams with one likely word the better is the one
+      // with less beside it.  Where another lane has a logit within 3 of it (nearly always of usual
+      // rows) what is beside it is 0.05 at least.  64 x 8 beams of 128001 take 40.1 us so, 39.6 without
+      // (within 2: 40.7).
+      if (__popc(__ballot_sync(kAll, fmaxf(run0, run1) >= top - 3.0f)) == 1) {
+        float ones = odd_one == 1.0f ? 1.0f : 0.0f, beside = odd_one == 1.0f ? 0.0f : odd_one;
 #pragma unroll
-      for (int j = 0; j < kN; ++j)
+        for (int j = 0; j < kN; ++j)
 #pragma unroll
-        for (int i = 0; i < kVec; i += 2) {
-          float p, q;
-          unpack2(fma2(add2(pack2(H::get(x.v[j], i), H::get(x.v[j], i + 1)), minus), scale, 0), p, q);
-          sum2 = add2(sum2, pack2(ex2(p), ex2(q)));
-        }
-      float p, q;
-      unpack2(sum2, p, q);
-      sum += (double)(p + q);
+          for (int i = 0; i < kVec; ++i) {
+            const float d = H::get(x.v[j], i) - top, e = ex2(d * kLog2e);
+            if (d == 0.0f) ones += 1.0f;
+            else beside += e;
+          }
+        sum += (double)ones;
+        sum += (double)beside;
+      } else {
+        // two at a time, in fp32 for a window
+        uint64_t both = pack2(odd_one, 0.0f);
+        const uint64_t minus = pack2(-top, -top), scale = pack2(kLog2e, kLog2e);
+#pragma unroll
+        for (int j = 0; j < kN; ++j)
+#pragma unroll
+          for (int i = 0; i < kVec; i += 2) {
+            float p, q;
+            unpack2(fma2(add2(pack2(H::get(x.v[j], i), H::get(x.v[j], i + 1)), minus), scale, 0), p, q);
+            both = add2(both, pack2(ex2(p), ex2(q)));
+          }
+        float p, q;
+        unpack2(both, p, q);
+        sum += (double)(p + q);
+      }
     }
     // the next window's loads, before what this one has to list
     load(from + 32 * kN);

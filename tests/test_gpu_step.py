@@ -737,11 +737,12 @@ def test_a_captioner_writes_with_beams(dtype):
 
 def _peaked_bound(x):
     """Of rows whose largest stands alone, a bound on |log-sum-exp - largest - exact| in fp32: what is beside the largest is
-    off by 2^-22 and by its distance times 2^-22 (arguments of exponentials), and 2^-24 by rounding."""
+    off by 2^-22 and by its distance times 2^-22 (arguments of exponentials), and 2^-24 by rounding; the 64-bit sum of 1 and
+    what is beside it is itself rounded at 2^-53, and so is its logarithm."""
     x = np.asarray(x, np.float64)
     d = np.where(np.isfinite(x), x, -1e4) - x.max(1, keepdims=True)
     e = np.exp(d) * (d < 0)
-    return (e * (2.0 ** -22 + 2.0 ** -22 * np.abs(d))).sum(1) + 2.0 ** -24 * np.log1p(e.sum(1))
+    return (e * (2.0 ** -22 + 2.0 ** -22 * np.abs(d))).sum(1) + 2.0 ** -24 * np.log1p(e.sum(1)) + 2.0 ** -52
 
 
 @pytest.mark.parametrize("stride", [2, 3, 4, 5, 8])
@@ -783,3 +784,26 @@ def test_beams_of_the_same_logits_have_the_same_sums(beams, vocab, pad, dtype):
     _check_beams(x, cum, min(64, 2 * beams))
     lse = _select(x, cum, 4)[3].view(2, beams)
     assert (lse[0] == lse[0, 0]).all() and (lse[1, [i for i in range(beams) if i != 1]] == lse[1, 0]).all()
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("vocab,beams,likely", [(32000, 16, 28), (32001, 16, 28), (8, 4, 17), (2048, 8, 21), (128001, 8, 30), (5003, 64, 24)])
+def test_beams_of_one_likely_word_each(vocab, beams, likely, dtype):
+    """The same likely word everywhere: what is beside it, 1e-7 of it or so, decides between the beams, and is their score."""
+    rng = np.random.default_rng(vocab + beams)
+    x = _dev(rng.standard_normal((3 * beams, vocab)) * 2, dtype)
+    x[:, vocab // 3] = likely
+    x[beams:2 * beams, 1] = likely - 12  # beside another word in its vector's or another's
+    x[2 * beams:, vocab - 1] = likely - 9
+    cum = torch.zeros(3, beams, device="cuda")
+    take = max(1, beams // 2)
+    got = [t.double().cpu().numpy() for t in _select(x, cum, take)]
+    xs = x.double().cpu().numpy()
+    s, p, t, lse, _ = _step.beam_select(xs, cum.double().cpu().numpy(), take + 1)
+    off = _peaked_bound(xs)
+    gap = 2 * off.reshape(3, beams).max(1, keepdims=True)
+    sure = (s[:, :-1] - s[:, 1:] > gap) & (np.concatenate([np.full((3, 1), np.inf), s[:, :-2] - s[:, 1:-1]], 1) > gap)
+    assert sure[0].mean() > 0.9 and sure.mean() > 0.5
+    assert np.array_equal(got[1][sure], p[:, :-1][sure]) and np.array_equal(got[2], t[:, :-1])
+    assert (np.abs(got[0] - s[:, :-1])[sure] <= (off[p[:, :-1]] + 2.0 ** -24 * np.abs(s[:, :-1]))[sure]).all()
+    assert (np.abs(got[3] - lse) <= off + 2.0 ** -24 * np.abs(lse)).all()

@@ -168,7 +168,8 @@ __global__ void __launch_bounds__(Rings<kTok>::kThreads, 1) fp4_tiles_kernel(con
       const int bytes = (int)uniform(blocks(r.tile) * kBlockBytes), steps = (int)uniform(r.s1 - r.s0);
       for (int step = 0; step < steps; ++step, ++n, at.next(), src += kTileBytes) {
         if (n >= R::kP) tc::mbar_wait_or(&empty_p[at.s], at.phase ^ 1, ok);
-        if (!__all_sync(0xffffffffu, ok)) break;
+        ok = __all_sync(0xffffffffu, ok);  // all lanes leave, or none
+        if (!ok) break;
         if (tc::elect_one()) {
           tc::mbar_arrive_expect_tx(&full_p[at.s], bytes);
           tc::bulk_g2s(ps + at.s * kTileBytes, src, bytes, &full_p[at.s]);
@@ -187,7 +188,8 @@ __global__ void __launch_bounds__(Rings<kTok>::kThreads, 1) fp4_tiles_kernel(con
       const int row = (int)uniform(x_tile(r.tile) * kTok), end = (int)uniform(2 * r.s1);
       for (int box = (int)uniform(2 * r.s0); box < end; box += R::kBoxes, ++n, at.next()) {
         if (n >= R::kX) tc::mbar_wait_or(&empty[at.s], at.phase ^ 1, ok);
-        if (!__all_sync(0xffffffffu, ok)) break;
+        ok = __all_sync(0xffffffffu, ok);  // all lanes leave, or none
+        if (!ok) break;
         if (tc::elect_one()) {
           tc::mbar_arrive_expect_tx(&full[at.s], R::kXBytes);
 #pragma unroll
@@ -376,6 +378,7 @@ __global__ void __launch_bounds__(Rings<kTok>::kThreads, 1) fp4_tiles_kernel(con
         fp4_store(a.l, t0 + t, i, sum, a.l.alpha, bias);
       }
     }
+    __syncwarp();
     tc::cluster_sync();
   }
 }

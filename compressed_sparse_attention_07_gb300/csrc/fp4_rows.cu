@@ -199,9 +199,10 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_rows_kernel(const Fp4Linear a
   float acc[kGroups][kNt][4] = {};
   int kb = kb0, tile = first, s = 0;
   uint32_t phase = 0;
+  int sent = min(u1, u0 + slots);  // (lane 0) where the units end whose copies have begun
   bool whole = kb == 0;
   for (int u = u0; u < u1; ++u) {
-    tc::mbar_wait_or(&full[warp][s], phase, ok);  // (sums of what stands there, and a status, where it gives up)
+    tc::mbar_wait_or(&full[warp][s], phase, ok);  // (sums of what stands there, and a status, where it gives up; no more copies)
     __syncwarp();
     uint4 lo[kGroups], hi[kGroups];
     uint32_t sc[kGroups];
@@ -213,7 +214,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_rows_kernel(const Fp4Linear a
       sc[i] = *reinterpret_cast<const uint32_t*>(b + kBlockCodes + 4 * lane);
     }
     __syncwarp();
-    if (lane == 0 && u + slots < u1) fetch();
+    if (lane == 0 && ok && u + slots < u1) fetch(), ++sent;
     if (++s == slots) s = 0, phase ^= 1;
     uint32_t f[kGroups][4];  // scales of words 0, 1 and 2, 3 of row g, of row g + 8
 #pragma unroll
@@ -274,7 +275,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_rows_kernel(const Fp4Linear a
   if (!ok) {
     report(a.status, CSA2_ERR_TIMEOUT);
     // nothing may land in shared memory after the CTA has left
-    for (int u = max(u0, u1 - slots); u < u1; ++u) tc::mbar_wait(&full[warp][(u - u0) % slots], ((u - u0) / slots) & 1);
+    for (int u = max(u0, sent - slots); lane == 0 && u < sent; ++u) tc::mbar_wait(&full[warp][(u - u0) % slots], ((u - u0) / slots) & 1);
   }
   __syncthreads();
   // a shared tile's pieces stand in the order of its channels, two places a warp, a place

@@ -69,3 +69,44 @@ def test_lanes_of_a_copying_warp_leave_together(warp):
 def test_a_vote_that_is_not_taken_back_parts_the_lanes():
     assert not _run(2, 2, [0] * 5 + [None] * 27, False)
     assert _run(2, 2, [None] * 32, False)
+
+
+ROWS = os.path.join(os.path.dirname(SOURCE), "fp4_rows.cu")
+
+
+def _ring(units, slots, lost, guarded):
+    """A warp of the few-row kernel: units through a ring of bulk copies, of which those in `lost` never land; lane 0's
+    waits run out on them.  None, or what went wrong."""
+    arrived, landed, ok = [0] * slots, [0] * slots, True  # phases begun and over, of each place
+
+    def fetch(u):
+        s = u % slots
+        if arrived[s] > landed[s]:
+            return False  # an arrival too many, and two copies to one place
+        arrived[s] += 1
+        if u not in lost:
+            landed[s] += 1
+        return True
+
+    for u in range(min(units, slots)):
+        fetch(u)
+    for u in range(units):
+        if ok and landed[u % slots] <= u // slots:
+            ok = False  # the wait ran out; no more waits
+        if u + slots < units and (ok or not guarded) and not fetch(u + slots):
+            return "a copy to a place whose copy is on its way"
+    return None
+
+
+def test_no_copy_starts_after_a_wait_that_ran_out():
+    text = open(ROWS).read()
+    loop = text[text.index("for (int u = u0; u < u1; ++u) {"):]
+    guarded = re.search(r"if \(lane == 0 && ok && u \+ slots < u1\)[^;]*fetch\(\)", loop) is not None
+    rnd = random.Random(1)
+    for _ in range(500):
+        units, slots = rnd.randint(1, 40), rnd.randint(2, 8)
+        assert _ring(units, slots, {rnd.randrange(units)} if rnd.random() < 0.8 else set(), guarded) is None
+
+
+def test_copies_after_a_wait_that_ran_out_are_found_wrong():
+    assert _ring(9, 3, {2}, False) and _ring(9, 3, set(), False) is None

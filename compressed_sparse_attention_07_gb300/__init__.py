@@ -652,7 +652,8 @@ def beam_select(logits, cum, scores, parents, tokens, workspace, done=None, end_
 
 class Fp4Weights:
     """Weights [n][k] in the caches' codec (E2M1, one E4M3 scale per 16 channels), laid out for fp4_linear; a weight is
-    alpha * code * scale."""
+    alpha * code * scale.  pack and encode take the memory for them on the stream that they are given, or the current one:
+    it is that stream's, as any tensor made there."""
 
     def __init__(self, data, n: int, k: int, alpha: float):
         self.data, self.n, self.k, self.alpha = data, n, k, float(alpha)
@@ -673,9 +674,10 @@ class Fp4Weights:
         n, k, dev = codes.shape[0], 2 * codes.shape[1], codes.get_device()
         cp = _plain(codes, torch.uint8, (n, k // 2), "codes", dev)
         sp = _plain(scales, torch.uint8, (n, k // 16), "scales", dev)
-        data = cls._room(n, k, codes.device)
-        _check("csa2_fp4_pack", _on(dev, load().csa2_fp4_pack, stream, n, k, cp, sp, data.data_ptr(),
-                                    _plain(status, torch.int32, (1,), "status", dev)))
+        st = _plain(status, torch.int32, (1,), "status", dev)
+        with torch.cuda.stream(stream):  # the memory's stream too, which knows what else uses it
+            data = cls._room(n, k, codes.device)
+            _check("csa2_fp4_pack", _on(dev, load().csa2_fp4_pack, stream, n, k, cp, sp, data.data_ptr(), st))
         return cls(data, n, k, alpha)
 
     @classmethod
@@ -687,14 +689,16 @@ class Fp4Weights:
         if w.dtype != torch.bfloat16:
             raise TypeError("w must be torch.bfloat16, got %s" % w.dtype)
         p, stride = _rows_of(w, k, "w", dev)
-        if gain is None:
-            most = float(w.abs().amax()) if w.numel() else 0.0
-            gain = 2.0 ** min(126, math.floor(math.log2(448 * 6 / most))) if 0 < most < math.inf else 1.0
-        if not 2.0 ** -126 <= abs(gain) <= 2.0 ** 126:
-            raise ValueError("gain must be one that fp32 has with its reciprocal, got %r" % gain)
-        data = cls._room(n, k, w.device)
-        _check("csa2_fp4_encode", _on(dev, load().csa2_fp4_encode, stream, n, k, p, stride, float(gain), data.data_ptr(),
-                                      _plain(status, torch.int32, (1,), "status", dev)))
+        st = _plain(status, torch.int32, (1,), "status", dev)
+        with torch.cuda.stream(stream):
+            if gain is None:
+                most = float(w.abs().amax()) if w.numel() else 0.0
+                gain = 2.0 ** min(126, math.floor(math.log2(448 * 6 / most))) if 0 < most < math.inf else 1.0
+            if not 2.0 ** -126 <= abs(gain) <= 2.0 ** 126:
+                raise ValueError("gain must be one that fp32 has with its reciprocal, got %r" % gain)
+            data = cls._room(n, k, w.device)
+            _check("csa2_fp4_encode", _on(dev, load().csa2_fp4_encode, stream, n, k, p, stride, float(gain),
+                                          data.data_ptr(), st))
         return cls(data, n, k, 1.0 / gain)
 
 

@@ -807,3 +807,31 @@ def test_beams_of_one_likely_word_each(vocab, beams, likely, dtype):
     assert np.array_equal(got[1][sure], p[:, :-1][sure]) and np.array_equal(got[2], t[:, :-1])
     assert (np.abs(got[0] - s[:, :-1])[sure] <= (off[p[:, :-1]] + 2.0 ** -24 * np.abs(s[:, :-1]))[sure]).all()
     assert (np.abs(got[3] - lse) <= off + 2.0 ** -24 * np.abs(lse)).all()
+
+
+def test_weights_laid_out_on_another_stream():
+    """What the current stream still does with memory that was freed does not reach the weights, and the largest weight is
+    read after what the given stream has yet to write."""
+    rng = np.random.default_rng(3)
+    n, k = 512, 1024
+    codes, scales = _dev(rng.integers(0, 256, (n, k // 2)), torch.uint8), _dev(rng.integers(0x20, 0x50, (n, k // 16)), torch.uint8)
+    w = _dev(_kv.normal(rng, n, k, std=0.02))
+    want, same = csa.Fp4Weights.pack(codes, scales), csa.Fp4Weights.encode(w)
+    late = torch.full_like(w, 100.0)
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    for wanted, make in ((want, lambda: csa.Fp4Weights.pack(codes, scales, stream=s)),
+                         (same, lambda: csa.Fp4Weights.encode(w, 1 / same.alpha, stream=s))):
+        freed = torch.empty_like(want.data)
+        torch.cuda._sleep(20_000_000)
+        freed.fill_(255)
+        del freed
+        got = make()
+        torch.cuda.synchronize()
+        assert torch.equal(got.data, wanted.data)
+    with torch.cuda.stream(s):
+        torch.cuda._sleep(20_000_000)
+        late.copy_(w)
+    got = csa.Fp4Weights.encode(late, stream=s)
+    torch.cuda.synchronize()
+    assert got.alpha == same.alpha and torch.equal(got.data, same.data)

@@ -254,3 +254,52 @@ def test_a_workspace_serves_smaller_calls():
         a = [int(2 ** (rng.random() * m)) for m in (8, 6, 18, 6)]
         b = [int(rng.integers(1, v + 1)) if rng.random() < 0.7 else v for v in a]
         assert 0 < f(*b) <= f(*a), (b, a)
+
+
+@pytest.mark.parametrize("given", [True, False])
+@pytest.mark.parametrize("how", ["pack", "encode"])
+def test_weights_are_laid_out_on_the_callers_stream(how, given, monkeypatch):
+    """Memory, the largest weight and the kernel all on one stream: the given one, or the current."""
+    import contextlib
+
+    class Stream:
+        cuda_stream = 7
+
+    current, seen, mine = ["current"], [], Stream()
+    want = mine if given else "current"
+
+    @contextlib.contextmanager
+    def on(stream):
+        current.append(current[-1] if stream is None else stream)
+        yield
+        current.pop()
+
+    class Lib:
+        csa2_fp4_weight_bytes = csa.load().csa2_fp4_weight_bytes
+        csa2_fp4_pack = csa2_fp4_encode = None
+
+    def note(name, fn):
+        def run(*args, **kw):
+            seen.append((name, current[-1]))
+            return fn(*args, **kw)
+        return run
+
+    def call(index, fn, stream, *args):
+        seen.append(("kernel", current[-1] if stream is None else stream))
+        return 0
+
+    monkeypatch.setattr(csa, "load", lambda: Lib)
+    monkeypatch.setattr(csa, "_on", call)
+    monkeypatch.setattr(csa, "_plain", lambda t, *rest: None if t is None else t.data_ptr())
+    monkeypatch.setattr(csa, "_rows_of", lambda t, width, name, index: (t.data_ptr(), t.stride(0)))
+    monkeypatch.setattr(torch.cuda, "stream", on)
+    monkeypatch.setattr(torch, "empty", note("memory", torch.empty))
+    monkeypatch.setattr(torch.Tensor, "amax", note("largest", torch.Tensor.amax))
+    s = mine if given else None
+    if how == "pack":
+        csa.Fp4Weights.pack(torch.zeros(16, 8, dtype=torch.uint8), torch.zeros(16, 1, dtype=torch.uint8), stream=s)
+    else:
+        csa.Fp4Weights.encode(torch.ones(16, 16, dtype=torch.bfloat16), stream=s)
+    names = {name for name, _ in seen}
+    assert names == ({"memory", "kernel"} if how == "pack" else {"memory", "kernel", "largest"})
+    assert all(where is want for _, where in seen), seen

@@ -672,6 +672,8 @@ class Fp4Weights:
     def pack(cls, codes, scales, alpha: float = 1.0, status=None, stream=None) -> "Fp4Weights":
         """From codes [n][k / 2] (channel 2i in the low nibble of byte i) and E4M3 scales [n][k / 16], both uint8."""
         n, k, dev = codes.shape[0], 2 * codes.shape[1], codes.get_device()
+        if not codes.is_cuda:
+            raise ValueError("codes must be a CUDA tensor")
         cp = _plain(codes, torch.uint8, (n, k // 2), "codes", dev)
         sp = _plain(scales, torch.uint8, (n, k // 16), "scales", dev)
         st = _plain(status, torch.int32, (1,), "status", dev)

@@ -295,6 +295,7 @@ def test_weights_are_laid_out_on_the_callers_stream(how, given, monkeypatch):
     monkeypatch.setattr(torch.cuda, "stream", on)
     monkeypatch.setattr(torch, "empty", note("memory", torch.empty))
     monkeypatch.setattr(torch.Tensor, "amax", note("largest", torch.Tensor.amax))
+    monkeypatch.setattr(torch.Tensor, "is_cuda", True)
     s = mine if given else None
     if how == "pack":
         csa.Fp4Weights.pack(torch.zeros(16, 8, dtype=torch.uint8), torch.zeros(16, 1, dtype=torch.uint8), stream=s)
@@ -303,3 +304,8 @@ def test_weights_are_laid_out_on_the_callers_stream(how, given, monkeypatch):
     names = {name for name, _ in seen}
     assert names == ({"memory", "kernel"} if how == "pack" else {"memory", "kernel", "largest"})
     assert all(where is want for _, where in seen), seen
+
+
+def test_packing_refuses_host_tensors():
+    with pytest.raises(ValueError, match="CUDA"):
+        csa.Fp4Weights.pack(torch.zeros(16, 8, dtype=torch.uint8), torch.zeros(16, 1, dtype=torch.uint8))

@@ -656,17 +656,25 @@ class Fp4Weights:
     it is that stream's, as any tensor made there."""
 
     def __init__(self, data, n: int, k: int, alpha: float):
+        if data.dtype != torch.uint8:
+            raise TypeError("data must be torch.uint8, got %s" % data.dtype)
+        if not data.is_contiguous() or data.numel() < self._size(n, k):
+            raise ValueError("data must be contiguous and hold weights [%d][%d]" % (n, k))
         self.data, self.n, self.k, self.alpha = data, n, k, float(alpha)
         self.device, self.device_index = data.device, data.get_device()
         self._c = _Fp4Desc(data.data_ptr(), n, k, self.alpha, 0)
         self._ref = C.byref(self._c)
 
     @staticmethod
-    def _room(n, k, device):
+    def _size(n, k):
         size = load().csa2_fp4_weight_bytes(n, k)
         if size == 0:
             raise ValueError("unsupported weights [%d][%d]: k must be a multiple of 16" % (n, k))
-        return torch.empty(size, dtype=torch.uint8, device=device)
+        return size
+
+    @classmethod
+    def _room(cls, n, k, device):
+        return torch.empty(cls._size(n, k), dtype=torch.uint8, device=device)
 
     @classmethod
     def pack(cls, codes, scales, alpha: float = 1.0, status=None, stream=None) -> "Fp4Weights":

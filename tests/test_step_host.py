@@ -309,3 +309,12 @@ def test_weights_are_laid_out_on_the_callers_stream(how, given, monkeypatch):
 def test_packing_refuses_host_tensors():
     with pytest.raises(ValueError, match="CUDA"):
         csa.Fp4Weights.pack(torch.zeros(16, 8, dtype=torch.uint8), torch.zeros(16, 1, dtype=torch.uint8))
+
+
+@pytest.mark.parametrize("data,error", [(torch.zeros(9215, dtype=torch.uint8), ValueError), (torch.zeros(9216), TypeError),
+                                        (torch.zeros(2, 9216, dtype=torch.uint8).t(), ValueError)])
+def test_weights_over_memory_that_does_not_hold_them_refused(data, error):
+    with pytest.raises(error):
+        csa.Fp4Weights(data, 16, 64, 1.0)
+    with pytest.raises(ValueError):
+        csa.Fp4Weights(torch.zeros(9216, dtype=torch.uint8), 16, 72, 1.0)

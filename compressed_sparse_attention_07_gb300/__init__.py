@@ -487,7 +487,8 @@ def kv_append_axes(cfg: KVCfg, k, v, cu, pos0, cache: KVCache, axes, axis_of, ro
     """kv_append with rotary positions of several axes (images, video): axes [T][n_axes] int32 holds each row's positions
     in `rope`, axis_of the axis of each of the rope_dims / 2 pairs (a sequence of small integers, or bytes).  pos0 gives
     the slots in the cache, as before."""
-    _kv_append(cfg, k, v, cu, pos0, cache, rope, q, q_out, k_out, v_out, status, stream, axes, bytes(axis_of))
+    _kv_append(cfg, k, v, cu, pos0, cache, rope, q, q_out, k_out, v_out, status, stream, axes,
+               axis_of if isinstance(axis_of, bytes) else bytes(list(axis_of)))
 
 
 def _kv_append(cfg, k, v, cu, pos0, cache, rope, q, q_out, k_out, v_out, status, stream, axes=None, axis_of=None):

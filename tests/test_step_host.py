@@ -318,3 +318,18 @@ def test_weights_over_memory_that_does_not_hold_them_refused(data, error):
         csa.Fp4Weights(data, 16, 64, 1.0)
     with pytest.raises(ValueError):
         csa.Fp4Weights(torch.zeros(9216, dtype=torch.uint8), 16, 72, 1.0)
+
+
+@pytest.mark.parametrize("of", [[0, 1, 2], (0, 1, 2), b"\0\1\2", bytearray(b"\0\1\2"), np.array([0, 1, 2]),
+                                np.array([0, 1, 2], np.int32), np.array([0, 1, 2], np.uint8), torch.tensor([0, 1, 2])])
+def test_axes_of_pairs_may_be_any_sequence(of, monkeypatch):
+    got = []
+    monkeypatch.setattr(csa, "_kv_append", lambda *args: got.append(args[-1]))
+    csa.kv_append_axes(None, None, None, None, None, None, None, of, None)
+    assert got == [b"\0\1\2"]
+
+
+@pytest.mark.parametrize("of", [3, [0, 256], [0, -1], [0.5]])
+def test_axes_of_pairs_that_are_no_small_integers_refused(of):
+    with pytest.raises((TypeError, ValueError)):
+        csa.kv_append_axes(None, None, None, None, None, None, None, of, None)

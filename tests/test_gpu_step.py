@@ -835,3 +835,18 @@ def test_weights_laid_out_on_another_stream():
     got = csa.Fp4Weights.encode(late, stream=s)
     torch.cuda.synchronize()
     assert got.alpha == same.alpha and torch.equal(got.data, same.data)
+
+
+@pytest.mark.parametrize("f32", [False, True])
+@pytest.mark.parametrize("T,k,n", [(1, 64, 40), (16, 64, 40), (20, 64, 40), (40, 2048, 700), (70, 64, 300), (300, 64, 300)])
+@pytest.mark.parametrize("alpha", [2.0 ** 127, -1.5 * 2.0 ** 121, 2.0 ** -126])
+def test_any_factor_that_fp32_has(alpha, T, k, n, f32):
+    rng = np.random.default_rng(T + n)
+    w, plain = _packed(rng, n, k, alpha, 0x38, 0x39)
+    size = 2.0 ** -60 if abs(alpha) > 1 else 2.0 ** 60
+    x = rng.integers(-3, 4, (T, k)) * size
+    x[-1] = 0.0
+    out = torch.empty(T, n, dtype=torch.float32 if f32 else torch.bfloat16, device="cuda")
+    csa.fp4_linear(_dev(x), w, out)
+    want = torch.from_numpy(x @ plain.T * alpha)  # (whole multiples, which fp32 holds)
+    assert torch.equal(out.cpu().double(), want.to(out.dtype).double())

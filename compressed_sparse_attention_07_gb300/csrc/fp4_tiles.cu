@@ -14,8 +14,8 @@
 // formed.  Each tile of the last wave is divided among a cluster, along k, where that ends sooner
 // (512 rows of 4096 -> 10240, 160 tiles: 46.6 -> 35.3 us, 40 rows of 4096 -> 20480 26.7 -> 20.2);
 // its CTAs join their sums through distributed shared memory in rank order.
-// The accumulator's additions cut off: fp32 outputs are 1.0e-6 of their norm off at 4096
-// channels, 6.2e-6 at 16384.
+// The accumulator's additions cut off, so for fp32 outputs an accumulator takes 1024 channels and
+// the storing warps add such sums in fp32 (kApart; launch_fp4_tiles has the figures).
 // 64 rows over 128001 words take 79 us, 40 rows of 4096 -> 10240 14.9, 4096 rows 215.
 #include <cuda.h>
 
@@ -37,18 +37,27 @@ constexpr int kSmemMost = 227 * 1024 - 1024;
 // the last.  Packed steps may land out of order: with kP a multiple of kSets a set sees
 // every phase of its own places.  Decoded steps become free in order: a set that passed
 // step n - kSets knows step n - kSets - kS to be free, hence step n - 2 kS if kS >= kSets.
-template <int kTok>
+// kApart: an accumulator takes kSpan steps, which the storing warps add to sums of their own.  Those stand in
+// registers, kTok of a thread, so that what the CTA starts with is dealt out anew (kSplit); 64 rows leave out
+// a set of decoding warps for it (over 128001 words, in sums of 2048 channels, six sets of 56 registers take
+// 83.8 us, five of 64 82.4).
+template <int kTok, bool kApart>
 struct Rings {
-  static constexpr int kSets = kTok >= 128 ? 4 : 6, kThreads = 32 * (8 + 4 * kSets);
-  static constexpr int kD = kTok == 256 ? 1 : 2, kS = kTok >= 128 ? 4 : 6;
-  static constexpr int kBoxes = kTok == 256 ? 1 : 2, kX = kTok == 256 ? 5 : kTok == 128 ? 4 : 6;
+  static constexpr int kSpan = kApart ? 8 : 1 << 30;
+  static constexpr int kSets = kTok >= 128 ? 4 : kApart && kTok == 64 ? 5 : 6, kThreads = 32 * (8 + 4 * kSets);
+  static constexpr int kD = kTok == 256 ? 1 : 2, kS = kSets;
+  static constexpr int kBoxes = kTok == 256 ? 1 : 2, kX = kTok == 256 ? 5 : kSets;
   // a step's decoded weights and rows of x come and go by the same barriers: full_a, empty_a
   static constexpr bool kJoint = kTok < 256;
   static constexpr int kBoxBytes = kTok * 128, kXBytes = kBoxes * kBoxBytes;
-  static constexpr int kP = kTok == 256 ? 4 : kTok == 128 ? 8 : kTok == 64 ? 12 : 18;
+  static constexpr int kP = kTok == 256 ? 4 : kTok == 128 ? 8 : kTok == 64 ? 2 * kSets : 18;
   static constexpr int kSmem = 1024 + kX * kXBytes + kP * kTileBytes;
   static constexpr int kA = kD * kTok;  // first column of the decoded weights
   static constexpr int kCols = 512;
+  static constexpr bool kSplit = kApart && kTok >= 32;
+  static constexpr int kLaunchRegs = 65536 / kThreads / 8 * 8, kIssueRegs = 40, kDecodeRegs = 64;
+  static constexpr int kSumRegs = (2 + kSets) * kLaunchRegs - kIssueRegs - kSets * kDecodeRegs;
+  static_assert((kSpan & (kSpan - 1)) == 0 && (!kSplit || (kSumRegs % 8 == 0 && kSumRegs <= 256 && kSumRegs > kTok)), "");
   static_assert((!kJoint || kX == kS) && kP % kSets == 0 && kS >= kSets && kA + 64 * kS <= kCols && kSmem <= kSmemMost &&
                     kX * kXBytes >= kTok * kTileRows * 4, "");
 };
@@ -102,6 +111,15 @@ __device__ __forceinline__ void store_columns(T* o, const uint32_t (&v)[kCols], 
   }
 }
 
+template <int N>
+__device__ __forceinline__ void regs_inc() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void regs_dec() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
 template <int kI>
 struct Number {
   __device__ constexpr int operator()() const { return kI; }
@@ -112,9 +130,9 @@ struct Number {
 // over 128001 words took 82.0 us instead of 79.0, 300 rows of 8192 -> 8192 46.4 instead of 44.2.
 __device__ __forceinline__ uint32_t uniform(uint32_t v) { return __reduce_max_sync(0xffffffffu, v); }
 
-template <int kTok>
-__global__ void __launch_bounds__(Rings<kTok>::kThreads, 1) fp4_tiles_kernel(const __grid_constant__ CUtensorMap map, const TileArgs a) {
-  using R = Rings<kTok>;
+template <int kTok, bool kApart>
+__global__ void __launch_bounds__(Rings<kTok, kApart>::kThreads, 1) fp4_tiles_kernel(const __grid_constant__ CUtensorMap map, const TileArgs a) {
+  using R = Rings<kTok, kApart>;
   extern __shared__ uint8_t raw[];
   uint8_t* smem = raw + ((1024 - (tc::smem_u32(raw) & 1023)) & 1023);
   uint8_t *xs = smem, *ps = xs + R::kX * R::kXBytes;
@@ -162,7 +180,7 @@ __global__ void __launch_bounds__(Rings<kTok>::kThreads, 1) fp4_tiles_kernel(con
 
   // (Warps that issue copies or products stay together, and one lane issues: where an elected
   // thread ran the whole loop, calls of several tiles a CTA ended in illegal accesses.)
-  if (warp == 0) {  // packed weights
+  auto copy_weights = [&]() {
     int n = 0;
     Place<R::kP> at;
     for (int i = 0; i < runs && ok; ++i) {
@@ -172,18 +190,19 @@ __global__ void __launch_bounds__(Rings<kTok>::kThreads, 1) fp4_tiles_kernel(con
       const int bytes = (int)uniform(blocks(r.tile) * kBlockBytes), steps = (int)uniform(r.s1 - r.s0);
       for (int step = 0; step < steps; ++step, ++n, at.next(), src += kTileBytes) {
         if (n >= R::kP) tc::mbar_wait_or(&empty_p[at.s], at.phase ^ 1, ok);
-        ok = __all_sync(0xffffffffu, ok);  // all lanes leave, or none
-        if (!ok) break;
+        if (!__all_sync(0xffffffffu, ok)) break;
         if (tc::elect_one()) {
           tc::mbar_arrive_expect_tx(&full_p[at.s], bytes);
           tc::bulk_g2s(ps + at.s * kTileBytes, src, bytes, &full_p[at.s]);
         }
         __syncwarp();
       }
+      ok = __all_sync(0xffffffffu, ok);  // (a wait may run out for some lanes alone; voted on in each step, 64 rows 2 % slower)
     }
     // nothing may land in shared memory after the CTA has left
     for (int i = max(0, n - R::kP); i < n && tc::mbar_wait(&full_p[i % R::kP], (i / R::kP) & 1); ++i) {}
-  } else if (warp == 1) {  // rows of x
+  };
+  auto copy_rows = [&]() {
     int n = 0;
     Place<R::kX> at;
     uint64_t *const full = R::kJoint ? full_a : full_x, *const empty = R::kJoint ? empty_a : empty_x;
@@ -192,8 +211,7 @@ __global__ void __launch_bounds__(Rings<kTok>::kThreads, 1) fp4_tiles_kernel(con
       const int row = (int)uniform(x_tile(r.tile) * kTok), end = (int)uniform(2 * r.s1);
       for (int box = (int)uniform(2 * r.s0); box < end; box += R::kBoxes, ++n, at.next()) {
         if (n >= R::kX) tc::mbar_wait_or(&empty[at.s], at.phase ^ 1, ok);
-        ok = __all_sync(0xffffffffu, ok);  // all lanes leave, or none
-        if (!ok) break;
+        if (!__all_sync(0xffffffffu, ok)) break;
         if (tc::elect_one()) {
           tc::mbar_arrive_expect_tx(&full[at.s], R::kXBytes);
 #pragma unroll
@@ -202,23 +220,32 @@ __global__ void __launch_bounds__(Rings<kTok>::kThreads, 1) fp4_tiles_kernel(con
         }
         __syncwarp();
       }
+      ok = __all_sync(0xffffffffu, ok);  // (a wait may run out for some lanes alone; voted on in each step, 64 rows 2 % slower)
     }
     for (int i = max(0, n - R::kX); i < n && tc::mbar_wait(&full[i % R::kX], (i / R::kX) & 1); ++i) {}
-  } else if (warp == 2) {  // products
+  };
+  auto products = [&]() {
     constexpr uint32_t kIdesc = tc::idesc_f16(kTileRows, kTok, true, true, false, false);
     constexpr uint32_t kHi = tc::sdesc_hi(1024) | 2u << 29;  // 128-byte swizzle
     const uint32_t tb = uniform(tmem), x_lo = uniform(tc::sdesc_lo(tc::smem_u32(xs), 16));
     Place<R::kS> pa;
     Place<R::kX> px;
     Place<R::kD> pd;
-    for (int i = 0; i < runs; ++i, pd.next()) {
+    int sums = 0;  // begun so far
+    for (int i = 0; i < runs; ++i, ++sums, pd.next()) {
       const Run run = run_of(i);
       const int steps = (int)uniform(run.s1 - run.s0);
-      if (i >= R::kD) tc::mbar_wait_or(&empty_d[pd.s], pd.phase ^ 1, ok);
+      if ((kApart ? sums : i) >= R::kD) tc::mbar_wait_or(&empty_d[pd.s], pd.phase ^ 1, ok);
       if constexpr (R::kJoint) {
         // two steps at a time where there are two
         for (int step = 0; step < steps; step += 2) {
-          const bool two = step + 1 < steps;
+          const bool two = step + 1 < steps, fresh = kApart ? (step & (R::kSpan - 1)) == 0 : step == 0;
+          if (kApart && fresh && step > 0) {  // the next accumulator
+            if (tc::elect_one()) tc::mma_commit(&full_d[pd.s]);
+            __syncwarp();
+            pd.next();
+            if (++sums >= R::kD) tc::mbar_wait_or(&empty_d[pd.s], pd.phase ^ 1, ok);
+          }
           const int s = pa.s;
           tc::mbar_wait_or(&full_a[s], pa.phase, ok);
           pa.next();
@@ -234,7 +261,7 @@ __global__ void __launch_bounds__(Rings<kTok>::kThreads, 1) fp4_tiles_kernel(con
             for (int k = 0; k < 8; ++k)
               tc::mma_ts_lo(tb + pd.s * kTok, tb + R::kA + 64 * s + 8 * k,
                             x_lo + s * (R::kXBytes / 16) + (k / 4) * (R::kBoxBytes / 16) + (k % 4) * 2, kHi, kIdesc,
-                            k > 0 || step > 0);
+                            k > 0 || !fresh);
             tc::mma_commit(&empty_a[s]);
             if (two) {
 #pragma unroll
@@ -272,7 +299,8 @@ __global__ void __launch_bounds__(Rings<kTok>::kThreads, 1) fp4_tiles_kernel(con
     if (tc::elect_one()) tc::mma_commit(&drained);
     __syncwarp();
     tc::mbar_wait(&drained, 0);
-  } else if (warp >= 8) {  // decoding
+  };
+  auto decode_steps = [&]() {
     const int set = (warp - 8) >> 2, q = warp & 3, r = lane & 15;  // rows 32 q .. of every kSets-th step
     const uint8_t* const src = ps + (2 * q + (lane >> 4)) * kBlockBytes;
     const uint32_t dst0 = tc::taddr(tmem, 32 * q, R::kA);
@@ -324,46 +352,110 @@ __global__ void __launch_bounds__(Rings<kTok>::kThreads, 1) fp4_tiles_kernel(con
       if ((p += R::kSets) >= R::kP) p -= R::kP, p_phase ^= 1;
       if ((s += R::kSets) >= R::kS) s -= R::kS, s_phase ^= 1;
     }
-  } else if (warp >= 4) {  // sums out: a lane has a row of W
+  };
+  auto store_sums = [&]() {  // a lane has a row of W
     const int lane0 = 32 * (warp & 3);
-    constexpr int kCols = kTok < 32 ? kTok : 32;
+    constexpr int kCols = kApart ? (kTok < 32 || kTok == 128 ? 16 : 32) : kTok < 32 ? kTok : 32;
     Place<R::kD> at;
-    for (int n = 0; n < runs; ++n, at.next()) {
+    for (int n = 0; n < runs; ++n) {
       const int tile = run_of(n).tile;
       const int i = w_tile(tile) * kTileRows + lane0 + lane, t0 = x_tile(tile) * kTok;
       const bool there = i < a.l.n;
       const float bias = there ? fp4_bias(a.l, i) : 0.0f;
-      tc::mbar_wait_or(&full_d[at.s], at.phase, ok);
-      // (the last run: nothing fills x's ring or reads it any more)
-      uint32_t* const piece = n < wholes ? nullptr : reinterpret_cast<uint32_t*>(xs);
-      __syncwarp();
-      tc::fence_after_sync();
-#pragma unroll 1
-      for (int c = 0; c < kTok; c += kCols) {
-        uint32_t v[kCols];
+      if constexpr (kApart) {
+        // (the last run: nothing fills x's ring or reads it any more)
+        uint32_t* const piece = n < wholes ? nullptr : reinterpret_cast<uint32_t*>(xs);
+        float sum[kTok / kCols][kCols] = {};
+        const Run run = run_of(n);
+        for (int left = run.s1 - run.s0; left > 0; left -= R::kSpan, at.next()) {
+          tc::mbar_wait_or(&full_d[at.s], at.phase, ok);
+          __syncwarp();
+          tc::fence_after_sync();
+#pragma unroll
+          for (int c = 0; c < kTok / kCols; ++c) {
+            uint32_t v[kCols];
+            if constexpr (kCols == 32) tc::tmem_ld32(tc::taddr(tmem, lane0, at.s * kTok + c * kCols), v);
+            else tc::tmem_ld_n<kCols>(tc::taddr(tmem, lane0, at.s * kTok + c * kCols), v);
+            tc::tmem_wait_ld();
+#pragma unroll
+            for (int j = 0; j < kCols; ++j) sum[c][j] += __uint_as_float(v[j]);
+          }
+          tc::fence_before_sync();
+          __syncwarp();
+          if (lane == 0) tc::mbar_arrive(&empty_d[at.s]);
+        }
+#pragma unroll
+        for (int c = 0; c < kTok; c += kCols) {
+          uint32_t v[kCols];
+#pragma unroll
+          for (int j = 0; j < kCols; ++j) v[j] = __float_as_uint(sum[c / kCols][j]);
+          if (a.unit != 1.0f) {
+#pragma unroll
+            for (int j = 0; j < kCols; ++j) v[j] = __float_as_uint(__uint_as_float(v[j]) * a.unit);
+          }
+          if (piece) {  // [row of x][row of W]
+#pragma unroll
+            for (int j = 0; j < kCols; ++j) piece[(c + j) * kTileRows + lane0 + lane] = v[j];
+          } else if (there) {
+            const int most = min(kCols, a.l.T - t0 - c);
+            const int64_t at0 = (int64_t)(t0 + c) * a.l.out_stride + i;
+            if (a.l.f32) store_columns(static_cast<float*>(a.l.out) + at0, v, most, a.l, bias);
+            else store_columns(static_cast<__nv_bfloat16*>(a.l.out) + at0, v, most, a.l, bias);
+          }
+        }
+      } else {
+        tc::mbar_wait_or(&full_d[at.s], at.phase, ok);
+        // (the last run: nothing fills x's ring or reads it any more)
+        uint32_t* const piece = n < wholes ? nullptr : reinterpret_cast<uint32_t*>(xs);
         __syncwarp();
-        if constexpr (kCols == 32) tc::tmem_ld32(tc::taddr(tmem, lane0, at.s * kTok + c), v);
-        else tc::tmem_ld16(tc::taddr(tmem, lane0, at.s * kTok + c), v);
-        tc::tmem_wait_ld();
-        if (a.unit != 1.0f) {
+        tc::fence_after_sync();
+#pragma unroll 1
+        for (int c = 0; c < kTok; c += kCols) {
+          uint32_t v[kCols];
+          __syncwarp();
+          if constexpr (kCols == 32) tc::tmem_ld32(tc::taddr(tmem, lane0, at.s * kTok + c), v);
+          else tc::tmem_ld16(tc::taddr(tmem, lane0, at.s * kTok + c), v);
+          tc::tmem_wait_ld();
+          if (piece) {  // [row of x][row of W]
 #pragma unroll
-          for (int j = 0; j < kCols; ++j) v[j] = __float_as_uint(__uint_as_float(v[j]) * a.unit);
+            for (int j = 0; j < kCols; ++j) piece[(c + j) * kTileRows + lane0 + lane] = v[j];
+          } else if (there) {
+            const int most = min(kCols, a.l.T - t0 - c);
+            const int64_t at0 = (int64_t)(t0 + c) * a.l.out_stride + i;
+            if (a.l.f32) store_columns(static_cast<float*>(a.l.out) + at0, v, most, a.l, bias);
+            else store_columns(static_cast<__nv_bfloat16*>(a.l.out) + at0, v, most, a.l, bias);
+          }
         }
-        if (piece) {  // [row of x][row of W]
-#pragma unroll
-          for (int j = 0; j < kCols; ++j) piece[(c + j) * kTileRows + lane0 + lane] = v[j];
-        } else if (there) {
-          const int most = min(kCols, a.l.T - t0 - c);
-          const int64_t at0 = (int64_t)(t0 + c) * a.l.out_stride + i;
-          if (a.l.f32) store_columns(static_cast<float*>(a.l.out) + at0, v, most, a.l, bias);
-          else store_columns(static_cast<__nv_bfloat16*>(a.l.out) + at0, v, most, a.l, bias);
-        }
+        __syncwarp();
+        tc::fence_before_sync();
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(&empty_d[at.s]);
+        at.next();
       }
-      __syncwarp();
-      tc::fence_before_sync();
-      __syncwarp();
-      if (lane == 0) tc::mbar_arrive(&empty_d[at.s]);
     }
+  };
+  // (kSplit: the issuing warps under one condition, as what they run is then fitted to their registers.
+  // The order counts: 1024 rows of 4096 -> 10240 take 59.1 us with the issuing warps first, 58.1 so,
+  // and where sums are held 128 rows 18.8 with them first, 19.8 with the others)
+  if constexpr (R::kSplit) {
+    if (warp < 4) {
+      regs_dec<R::kIssueRegs>();
+      if (warp == 0) copy_weights();
+      else if (warp == 1) copy_rows();
+      else if (warp == 2) products();
+    } else if (warp < 8) {
+      regs_inc<R::kSumRegs>();
+      store_sums();
+    } else {
+      if constexpr (R::kDecodeRegs < R::kLaunchRegs) regs_dec<R::kDecodeRegs>();
+      decode_steps();
+    }
+  } else {
+    if (warp >= 8) decode_steps();
+    else if (warp >= 4) store_sums();
+    else if (warp == 0) copy_weights();
+    else if (warp == 1) copy_rows();
+    else if (warp == 2) products();
   }
   if (!ok) report(a.l.status, CSA2_ERR_TIMEOUT);
   __syncwarp();
@@ -409,9 +501,9 @@ Encode encoder() {
 }
 
 // Clusters of c CTAs that the device runs at once.
-template <int kTok>
+template <int kTok, bool kApart>
 int clusters_of(int c) {
-  using R = Rings<kTok>;
+  using R = Rings<kTok, kApart>;
   static std::atomic<int> known[64][kMostCluster + 1];  // and 1
   int device = 0;
   if (cudaGetDevice(&device) != cudaSuccess || device < 0 || device >= 64) return 0;
@@ -423,7 +515,7 @@ int clusters_of(int c) {
   attr.val.clusterDim.x = c, attr.val.clusterDim.y = 1, attr.val.clusterDim.z = 1;
   cfg.gridDim = dim3(c), cfg.blockDim = dim3(R::kThreads), cfg.dynamicSmemBytes = R::kSmem;
   cfg.attrs = &attr, cfg.numAttrs = 1;
-  if (cudaOccupancyMaxActiveClusters(&n, fp4_tiles_kernel<kTok>, &cfg) != cudaSuccess) {
+  if (cudaOccupancyMaxActiveClusters(&n, fp4_tiles_kernel<kTok, kApart>, &cfg) != cudaSuccess) {
     (void)cudaGetLastError();
     n = 0;
   }
@@ -432,13 +524,23 @@ int clusters_of(int c) {
   return n;
 }
 
-template <int kTok>
+template <int kTok, bool kApart>
 cudaError_t launch_of(const Fp4Linear& l, cudaStream_t stream) {
-  using R = Rings<kTok>;
-  auto kern = fp4_tiles_kernel<kTok>;
+  using R = Rings<kTok, kApart>;
+  auto kern = fp4_tiles_kernel<kTok, kApart>;
   static std::atomic<bool> done[64];
   const cudaError_t e = allow_smem(kern, R::kSmem, done);
   if (e != cudaSuccess) return e;
+  if constexpr (R::kSplit) {  // (shares beyond what the CTA starts with would be waited for without end)
+    static std::atomic<int> regs{0};
+    if (!regs.load(std::memory_order_relaxed)) {
+      cudaFuncAttributes at;
+      const cudaError_t e = cudaFuncGetAttributes(&at, kern);
+      if (e != cudaSuccess) return e;
+      regs.store(at.numRegs, std::memory_order_relaxed);
+    }
+    if ((regs.load(std::memory_order_relaxed) + 7) / 8 * 8 < R::kLaunchRegs) return cudaErrorInvalidConfiguration;
+  }
   const Encode encode = encoder();
   if (!encode) return cudaErrorNotSupported;
   CUtensorMap map;
@@ -461,7 +563,7 @@ cudaError_t launch_of(const Fp4Linear& l, cudaStream_t stream) {
   int ctas = std::min(a.tiles, sms);
   int64_t least = (int64_t)((a.tiles + sms - 1) / sms) * l.k_blocks * 10 / 11;
   for (int c = 2; c <= std::min(kMostCluster, l.k_blocks); ++c) {
-    const int n = clusters_of<kTok>(c), whole = n ? a.tiles / (n * c) : 0, rest = n ? a.tiles % (n * c) : 0;
+    const int n = clusters_of<kTok, kApart>(c), whole = n ? a.tiles / (n * c) : 0, rest = n ? a.tiles % (n * c) : 0;
     const int64_t steps = (int64_t)whole * l.k_blocks + (l.k_blocks + c - 1) / c + kJoin;
     if (rest == 0 || rest > n || steps > least) continue;
     least = steps, a.size = c, a.whole = whole, ctas = (whole ? n : rest) * c;
@@ -474,11 +576,24 @@ cudaError_t launch_of(const Fp4Linear& l, cudaStream_t stream) {
 }  // namespace
 
 cudaError_t launch_fp4_tiles(const Fp4Linear& l, cudaStream_t stream) {
-  if (l.T <= 16) return launch_of<16>(l, stream);
-  if (l.T <= 32) return launch_of<32>(l, stream);
-  if (l.T <= 64) return launch_of<64>(l, stream);
-  if (l.T <= 128) return launch_of<128>(l, stream);
-  return launch_of<256>(l, stream);
+  // The accumulator's additions cut off: what it sums over 1024 channels is 1.9e-7 of its norm off for
+  // normal weights (a plain product in fp32: 2e-7) and 4.2e-7 for codes drawn evenly, over 4096 9.6e-7 and
+  // 2.0e-6, over 16384 6.2e-6.  fp32 outputs are therefore summed 1024 channels at a time (17 rows of 4096 ->
+  // 10240 13.7 -> 14.4 us, 40 14.4 -> 15.2, 64 over 128001 words 78.2 -> 82.8, 128 rows 17.3 -> 18.8); beyond 128
+  // rows, where that takes the narrower tile, from 4096 channels on (1024 rows 58.5 us, 73 so; 256 rows of
+  // 16384 -> 4096 28.7 -> 35.0).  bf16 outputs, rounded by 2^-9 and more, from 32768 on.
+  const int most = !l.f32 ? 256 : l.T > 128 ? 32 : 8;
+  if (l.k_blocks > most || !std::isfinite(l.alpha * kFp4Unit)) {
+    if (l.T <= 16) return launch_of<16, true>(l, stream);
+    if (l.T <= 32) return launch_of<32, true>(l, stream);
+    if (l.T <= 64) return launch_of<64, true>(l, stream);
+    return launch_of<128, true>(l, stream);
+  }
+  if (l.T <= 16) return launch_of<16, false>(l, stream);
+  if (l.T <= 32) return launch_of<32, false>(l, stream);
+  if (l.T <= 64) return launch_of<64, false>(l, stream);
+  if (l.T <= 128) return launch_of<128, false>(l, stream);
+  return launch_of<256, false>(l, stream);
 }
 
 }  // namespace csa2

@@ -850,3 +850,39 @@ def test_any_factor_that_fp32_has(alpha, T, k, n, f32):
     csa.fp4_linear(_dev(x), w, out)
     want = torch.from_numpy(x @ plain.T * alpha)  # (whole multiples, which fp32 holds)
     assert torch.equal(out.cpu().double(), want.to(out.dtype).double())
+
+
+def _cut_off(adds, joins):
+    """Of what additions to an accumulator that cuts off below 24 bits, and then of such sums in fp32, make of a sum of
+    random terms, relative to it.  The j-th of `adds` finds (j / adds)^(1/2) of the sum and loses, towards zero, half a
+    step of 2^-23 of that times 0.72 (the mean of 1 / m for a mantissa m in [1, 2) is log 2 = 0.69, weighted as 1 / m by
+    Benford 0.72): all of them 2 / 3 adds 2^-24 0.72.  Joins round either way, by 2^-24 / 3^(1/2) of the sum so far."""
+    return adds * 2 / 3 * 2.0 ** -24 * 0.72 + (joins / 6) ** 0.5 * 2.0 ** -24 + 2.0 ** -24
+
+
+@pytest.mark.parametrize("T,k,n,adds", [(1, 4096, 700, 8), (16, 4096, 700, 8), (17, 4096, 700, 64), (40, 4096, 40000, 64),
+                                        (64, 1280, 700, 64), (128, 4096, 700, 64), (16, 16384, 300, 64),
+                                        (60, 16384, 300, 64), (300, 16384, 300, 64), (300, 1024, 700, 64),
+                                        (300, 4096, 300, 256), (20, 70000, 40, 64), (130, 70000, 40, 64)])
+def test_fp32_outputs_are_sums_of_short_sums(T, k, n, adds):
+    """An accumulator takes 128 channels of few rows, 1024 of more, 4096 of more than 128: that many 16s."""
+    rng = np.random.default_rng(T + k)
+    w, plain = _packed(rng, n, k, 1.0 / np.sqrt(k))
+    x = _dev(_kv.normal(rng, T, k))
+    out = torch.empty(T, n, device="cuda")
+    csa.fp4_linear(x, w, out)
+    y = x.double() @ torch.from_numpy(plain).cuda().T * float(np.float32(1.0 / np.sqrt(k)))
+    assert float((out.double() - y).norm() / y.norm()) <= _cut_off(adds, k / (16 * adds))
+
+
+def test_bf16_outputs_of_very_long_rows():
+    rng = np.random.default_rng(1)
+    k = 1 << 18
+    w, plain = _packed(rng, 36, k, 1.0 / np.sqrt(k))
+    for T in (20, 200):
+        x = _dev(_kv.normal(rng, T, k))
+        out = torch.empty(T, 36, dtype=torch.bfloat16, device="cuda")
+        csa.fp4_linear(x, w, out)
+        y = x.double() @ torch.from_numpy(plain).cuda().T * float(np.float32(1.0 / np.sqrt(k)))
+        # half a step of bf16, and five times what sums of 1024 channels lose
+        assert ((out.double() - y).abs() <= 2.0 ** -8 * y.abs() + 5 * _cut_off(64, k / 1024) * y.norm() / y.numel() ** 0.5).all()

@@ -358,7 +358,7 @@ __device__ __forceinline__ void sum2(float& s, float& low, float t, float t_low)
   s = __fadd_rn(r, e), low = __fsub_rn(e, __fsub_rn(s, r));
 }
 
-// Natural logarithm of h + l >= 1/2 as e log 2 + z + rest, off by 2^-29 at most (the
+// Natural logarithm of h + l >= 1/2 as e log 2 + z + rest, off by 2^-28 at most (the
 // library's in fp64 took 3000 cycles): h = 2^e m, m in [2/3, 4/3); log m = 2 (z + z^3 / 3 +
 // z^5 / 5 ..) with z = (m - 1) / (m + 1), |z| <= 1/5, as a sum of two fp32, and what there is
 // beside h.
@@ -367,7 +367,7 @@ struct Log {
   __device__ __forceinline__ double exact() const { return fma((double)e, 0.693147180559945309, (double)z) + (double)rest; }
 };
 __device__ __forceinline__ Log log_of(float h, float l) {
-  const int bits = __float_as_int(h), e = (bits - 0x3F2AAAABu) >> 23;
+  const int bits = __float_as_int(h), e = (bits - 0x3F2AAAAB) >> 23;
   const float m = __int_as_float(bits - (e << 23));
   const float f = m - 1.0f, g = m + 1.0f, gl = m - (g - 1.0f);  // g + gl = m + 1
   const float z = f / g;

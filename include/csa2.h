@@ -501,10 +501,13 @@ CSA2_API size_t csa2_beam_workspace_bytes(int32_t groups, int32_t beams, int32_t
  * k has the score cum[g][k] + x_v - lse, and the best `take` of a group's scores
  * are written in order (score descending; of equal scores the lower beam, then the
  * lower token): scores [groups][take] fp32, parents [groups][take] (the sequence
- * number g * beams + k) and tokens [groups][take] int32.  Scores are compared in
- * fp64, lse being summed from fp32 exponentials in fp64, and rounded once; beams of a
- * group whose logits are the same have the same lse where their cum is not -inf, so that
- * their scores are ties.
+ * number g * beams + k) and tokens [groups][take] int32.  Scores are compared in fp64 and
+ * rounded once.  lse is the largest logit plus the logarithm of a sum of fp32 exponentials,
+ * in fp32 for up to 66 at a time and with twice its bits beyond.  That logarithm is off by 2^-17
+ * at most (2^-20 for usual logits), and by 2^-17 of itself where one logit alone is within
+ * 3 of the largest; tokens of different beams whose scores are nearer may come in either order.
+ * Beams of a group whose logits are the same have the same lse where their cum is not -inf,
+ * so that their scores are ties.
  *  - A token of logit -inf (masked) and every token of a beam whose cum is -inf is
  *    no candidate; where candidates run out, score -inf, parent and token -1.
  *  - done [groups][beams] bytes or NULL: a beam that is done (not 0) has end_token

@@ -600,8 +600,10 @@ CSA2_API int32_t csa2_fp4_pack(int32_t n, int32_t k, const uint8_t* codes, const
  * the weights.  An x that is not finite has effect on its own row's outputs alone; a row
  * whose products' magnitudes (before alpha) sum up past fp32's largest may yield such.
  * Rows' sums do not depend on what other rows hold, but their order may depend on T.
+ * Of up to 16 rows that fit shared memory (16 of no more than 5376 channels), an x below 2^-31 of its
+ * row's largest magnitude is rounded, by 2^-39 of that at most; otherwise x is taken as it is.
  * The tensor core's accumulator cuts off what it adds, so that no more than 1024 channels are summed in
- * one before fp32 takes over (128 where up to 16 rows fit shared memory, 16 of no more than 5376 channels): fp32
+ * one before fp32 takes over (128 of such few rows): fp32
  * outputs are off by about 2e-7 of their norm for normal x and weights (1e-7).  4096 channels are, for fp32 outputs
  * of more than 128 rows (1e-6), and 32768 for bf16 outputs. */
 CSA2_API int32_t csa2_fp4_linear(const csa2_fp4_weights* w, int32_t T, const uint16_t* x, int64_t x_stride,

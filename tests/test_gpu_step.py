@@ -886,3 +886,25 @@ def test_bf16_outputs_of_very_long_rows():
         y = x.double() @ torch.from_numpy(plain).cuda().T * float(np.float32(1.0 / np.sqrt(k)))
         # half a step of bf16, and five times what sums of 1024 channels lose
         assert ((out.double() - y).abs() <= 2.0 ** -8 * y.abs() + 5 * _cut_off(64, k / 1024) * y.norm() / y.numel() ** 0.5).all()
+
+
+@pytest.mark.parametrize("T", [1, 8, 16, 17, 200])
+@pytest.mark.parametrize("below", [24, 31, 34, 39, 41, 60])
+def test_channels_far_below_their_rows_largest(T, below):
+    """The largest meets a weight of 0, and the outputs come from channels 2^-below of it: exact down to 2^-31, else off by
+    2^-39 of the largest each (what f16 keeps beside it); more than 16 rows are exact."""
+    rng = np.random.default_rng(below)
+    n, k = 48, 256
+    codes = rng.integers(0, 256, (n, k // 2), dtype=np.uint8)
+    codes[:, 0] &= 0xF0
+    w = csa.Fp4Weights.pack(_dev(codes, torch.uint8), torch.full((n, k // 16), 0x38, dtype=torch.uint8, device="cuda"))
+    plain = _step.weights(codes, np.full((n, k // 16), 0x38, np.uint8))
+    x = rng.integers(64, 128, (T, k)) / 64.0 * np.where(rng.random((T, k)) < 0.5, -1, 1) * 2.0 ** -below
+    x[:, 0] = 1.75
+    out = torch.empty(T, n, device="cuda")
+    csa.fp4_linear(_dev(x), w, out)
+    got, want = out.double().cpu().numpy(), x @ plain.T  # (whole multiples of 2^-7 below, less than 2^17 of them: fp32 holds every sum)
+    if T > 16 or below <= 31:
+        assert np.array_equal(got, want)
+    else:
+        assert (np.abs(got - want) <= 2.0 ** -39 * 1.75 * np.abs(plain).sum(1)).all()

@@ -48,7 +48,7 @@ struct BeamArgs {
   PartSum* part_sum;  // [rows][parts]
   uint2* part_best;   // [rows][parts][take] logit bits, token
   int32_t* status;
-  int bf16, uneven;  // (of logits) uneven: a group's rows may begin differently far from 16 bytes
+  int bf16;
 };
 
 // fp32 -> unsigned in the same order; -inf -> 0x007FFFFF.
@@ -234,7 +234,7 @@ __global__ void __launch_bounds__(32 * kPartWarps, kMany ? 6 : 7) beam_part_kern
       // The largest, 1 here, is counted apart where it stands alone: added in fp32 to what is beside it,
       // it would leave that to 2^-24, and of two beams with one likely word the better is the one
       // with less beside it.  Where another lane has a logit within 3 of it (nearly always of usual
-      // rows) what is beside it is 0.05 at least.  64 x 8 beams of 128001 take 40.1 us so, 39.6 without
+      // rows) what is beside it is 0.05 at least.  64 x 8 beams of 128001 take 39.9 us so, 39.3 without
       // (within 2: 40.7).
       if (__popc(__ballot_sync(kAll, fmaxf(run0, run1) >= top - 3.0f)) == 1) {
         float ones = odd_one == 1.0f ? 1.0f : 0.0f, beside = odd_one == 1.0f ? 0.0f : odd_one;
@@ -423,25 +423,33 @@ __device__ __forceinline__ uint64_t same_rows(const BeamArgs& a, int64_t row0, i
 }
 // Beams whose logits are the same are given the same sum, so that their scores are ties.  Rows that
 // begin equally far from 16 bytes are summed alike to the last bit; this is for those that do not
-// (a.uneven), whose sums differ by 2^-16 at most: twice 33 additions of a window in fp32 (2^-19), and
+// (kUneven), whose sums differ by 2^-16 at most: twice 33 additions of a window in fp32 (2^-19), and
 // exponents off by 2^-23 of themselves, of which those up to log 2^30 count (2^-18.6), in the terms and
 // where a larger logit rescales them.  Sums that near with the same largest logit are common (one likely
 // word: 1 and a little), so the rows themselves are compared, after a mark of each part's best (key,
 // token), which rarely agrees where rows differ.  All threads; `live`: beam tid has candidates.
-// Where all rows are the same, 64 x 8 of 128001 in bf16 take 156 us in place of 40.5, 16 x 5 of 51865 in
-// fp32 37 in place of 13.0; where sums are near and rows differ 43.0 and 14.9.
-__device__ __forceinline__ void share_sums(const BeamArgs& a, int64_t row0, bool live, float* sums, float* lows, const float* most,
+// Where all rows are the same, 64 x 8 of 128001 in bf16 take 175 us in place of 40.8, 16 x 5 of 51865 in
+// fp32 39 in place of 12.6; where sums are near and rows differ 45.4 and 15.6.
+__device__ __forceinline__ bool near_sums(int b, int k, const float* sums, const float* lows, const float* most) {
+  return most[b] == most[k] && fabsf((sums[b] - sums[k]) + (lows[b] - lows[k])) <= 0x1p-15f * sums[k];
+}
+// Whether beam tid's sum is near a lower one's; the first kMost threads.
+__device__ __forceinline__ bool may_share(bool live, const float* sums, const float* lows, const float* most) {
+  const int tid = threadIdx.x, lane = tid & 31;
+  uint32_t same = __match_any_sync(0xffffffffu, __float_as_uint(live ? most[tid] + 0.0f : INFINITY)) & ((1u << lane) - 1);
+  bool some = false;
+  if (live) {
+    for (; same; same &= same - 1) some |= near_sums(tid - lane + __ffs(same) - 1, tid, sums, lows, most);
+    for (int b = 0; b < tid - lane; ++b) some |= near_sums(b, tid, sums, lows, most);
+  }
+  return some;
+}
+// (Not inlined, so that what is common stays small: 16 x 5 of 51865 12.9 -> 12.7 us.)
+__device__ __noinline__ void share_sums(const BeamArgs& a, int64_t row0, bool live, float* sums, float* lows, const float* most,
                                            Likes& likes) {
   const int tid = threadIdx.x;
-  auto near = [&](int b, int k) {
-    return likes.of[b] == b && most[b] == most[k] && fabsf((sums[b] - sums[k]) + (lows[b] - lows[k])) <= 0x1p-15f * sums[k];
-  };
+  auto near = [&](int b, int k) { return likes.of[b] == b && near_sums(b, k, sums, lows, most); };
   if (tid < kMost) likes.of[tid] = live ? tid : -1;
-  __syncthreads();
-  bool some = false;
-  if (live)
-    for (int b = 0; b < tid; ++b) some |= near(b, tid);
-  if (!__syncthreads_or(some)) return;
   {  // eight threads a beam
     const int k = tid >> 3;
     uint32_t mark = 0;
@@ -479,11 +487,12 @@ __device__ __forceinline__ void share_sums(const BeamArgs& a, int64_t row0, bool
   __syncthreads();
 }
 
-__global__ void __launch_bounds__(kThreads) beam_join_kernel(const BeamArgs a) {
+// kUneven: a group's rows may begin differently far from 16 bytes.
+template <bool kUneven>
+__global__ void __launch_bounds__(kThreads, 2) beam_join_kernel(const BeamArgs a) {
   __shared__ float sums[kMost], lows[kMost];  // of exp(x - most)
   __shared__ Log logs[kMost];
   __shared__ float most[kMost], cums[kMost], logs32[kMost];
-  __shared__ Likes likes;
   __shared__ uint32_t best[64];
   __shared__ uint32_t bound, far, count;
   __shared__ uint64_t lkey[kList];
@@ -513,7 +522,7 @@ __global__ void __launch_bounds__(kThreads) beam_join_kernel(const BeamArgs a) {
   uint2 raw0 = make_uint2(0, 0);
   if (sample0 < samples) raw0 = mine[(sample0 % lists) * a.take + sample0 / lists];
   float cum = tid < a.beams ? a.cum[row0 + tid] : 0.0f;
-  const bool ended = tid < a.beams && a.done && a.done[row0 + tid];
+  const bool ended = kUneven && tid < a.beams && a.done && a.done[row0 + tid];
   {  // the beams' sums: eight threads a beam
     const int k = tid >> 3;
     float m = -INFINITY, s = 0.0f, low = 0.0f;
@@ -543,17 +552,26 @@ __global__ void __launch_bounds__(kThreads) beam_join_kernel(const BeamArgs a) {
   bool bad = false;
   cum = clean(cum, bad);
   if (bad) report(a.status, CSA2_ERR_RANGE);
-  if (a.uneven) share_sums(a, row0, tid < a.beams && !ended && cum > -INFINITY && most[tid] > -INFINITY, sums, lows, most, likes);
-  if (tid < a.beams) {
-    const float s = sums[tid], low = lows[tid];
+  auto take_log = [&]() {
     const bool some = most[tid] > -INFINITY;
-    const Log l = some ? log_of(s, low) : Log{0.0f, 0.0f, 0.0f};
+    const Log l = some ? log_of(sums[tid], lows[tid]) : Log{0.0f, 0.0f, 0.0f};
     const float near = fmaf(l.e, 0.693147181f, l.z) + l.rest;
     logs[tid] = l, logs32[tid] = near;
     cums[tid] = some ? cum + 0.0f : -INFINITY;
     if (some && cum > -INFINITY) atomicMax(&far, __float_as_uint(fabsf(cum) + near + 1.0f));  // (sums are 1 at least)
+  };
+  if (tid < a.beams) take_log();
+  if constexpr (kUneven) {
+    __shared__ Likes likes;
+    const bool live = tid < a.beams && !ended && cum > -INFINITY && most[tid] > -INFINITY;
+    if (__syncthreads_or(tid < kMost && may_share(live, sums, lows, most))) {
+      share_sums(a, row0, live, sums, lows, most, likes);
+      if (tid < a.beams) take_log();
+      __syncthreads();
+    }
+  } else {
+    __syncthreads();
   }
-  __syncthreads();
   uint32_t top = sample0 < samples ? key_of(near_of(raw0, beam_of(sample0 % lists))) : kNone;
   for (int i = sample0 + kThreads; i < samples; i += kThreads)
     top = max(top, key_of(near_of(mine[(i % lists) * a.take + i / lists], beam_of(i % lists))));
@@ -728,15 +746,15 @@ int32_t csa2_beam_select(int32_t groups, int32_t beams, int32_t vocab, int32_t t
   const Parts parts = parts_of(rows, vocab, take, bf16);
   BeamArgs a{groups, beams, vocab, take, parts.n, parts.size, divisor(parts.n), logits, stride, cum, done, end_token, scores,
              parents, tokens, lse, static_cast<PartSum*>(workspace),
-             reinterpret_cast<uint2*>(static_cast<uint8_t*>(workspace) + sums_bytes(rows * parts.n)), status, bf16,
-             beams > 1 && stride % (bf16 ? 8 : 4) != 0};
+             reinterpret_cast<uint2*>(static_cast<uint8_t*>(workspace) + sums_bytes(rows * parts.n)), status, bf16};
   const dim3 grid((unsigned)((rows * parts.n + kPartWarps - 1) / kPartWarps)), block(32 * kPartWarps);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   cudaError_t e = take > 32 ? (bf16 ? launch_k(beam_part_kernel<true, true>, grid, block, 0, s, 0, a)
                                     : launch_k(beam_part_kernel<false, true>, grid, block, 0, s, 0, a))
                             : (bf16 ? launch_k(beam_part_kernel<true, false>, grid, block, 0, s, 0, a)
                                     : launch_k(beam_part_kernel<false, false>, grid, block, 0, s, 0, a));
-  if (e == cudaSuccess) e = launch_k(beam_join_kernel, dim3(groups), dim3(kThreads), 0, s, 0, a);
+  const bool uneven = beams > 1 && stride % (bf16 ? 8 : 4) != 0;
+  if (e == cudaSuccess) e = launch_k(uneven ? beam_join_kernel<true> : beam_join_kernel<false>, dim3(groups), dim3(kThreads), 0, s, 0, a);
   return e == cudaSuccess ? CSA2_OK : CSA2_ERR_CUDA;
 }
 

@@ -15,8 +15,8 @@
 // x stands in shared memory for the whole call, as f16 relative to a power of two of its
 // row that brings the row's largest to [2^14, 2^15): exact down to 2^-31 of the largest,
 // and off by 2^-39 of it at most below.
-// 8 rows over 128001 words of 4096 channels take 50.9 us, 87 % of measured bandwidth; 16
-// rows 75 us, bound by issue; 1 row of 1280 -> 4096 4.4 us.
+// In graphs 8 rows over 128001 words of 4096 channels take 50.9 us, 87 % of measured bandwidth; 16
+// rows 74 us, bound by issue; 1 row of 1280 -> 4096 4.5 us.
 #include <algorithm>
 
 #include "fp4.cuh"

@@ -908,3 +908,16 @@ def test_channels_far_below_their_rows_largest(T, below):
         assert np.array_equal(got, want)
     else:
         assert (np.abs(got - want) <= 2.0 ** -39 * 1.75 * np.abs(plain).sum(1)).all()
+
+
+@pytest.mark.parametrize("stride", [4000, 4001])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_what_fp64_does_not_hold_beside_one_decides_nothing(dtype, stride):
+    """One word with all the probability that fp64 tells from 1, what is beside it anywhere in the row: ties, of which the
+    lower beam comes first."""
+    wide = torch.full((6, stride), -1000.0, dtype=dtype, device="cuda")
+    for i, (word, gap) in enumerate([(3, 44), (2000, 60), (3999, 50), (17, 48), (1234, 80), (3000, 41)]):
+        wide[i, word] = 20.0
+        wide[i, (word + 1777 * (i + 1)) % 4000] = 20.0 - gap
+    _check_beams(wide[:, :4000], torch.zeros(1, 6, device="cuda"), 6)
+    _check_beams(wide[:, :4000], torch.zeros(2, 3, device="cuda"), 3)

@@ -553,9 +553,9 @@ __global__ void __launch_bounds__(kThreads, 2) beam_join_kernel(const BeamArgs a
   cum = clean(cum, bad);
   if (bad) report(a.status, CSA2_ERR_RANGE);
   auto take_log = [&]() {
-    // (as fp64 holds the sum: what is beside 1 and below 2^-53 of it makes no difference)
+    // (as fp64 holds the sum: up to 2^-53 of it, what is beside 1 makes no difference)
     const bool some = most[tid] > -INFINITY;
-    const float low = (float)((double)sums[tid] + (double)lows[tid] - (double)sums[tid]);
+    const float low = fabsf(lows[tid]) <= 0x1p-53f * sums[tid] ? 0.0f : lows[tid];
     const Log l = some ? log_of(sums[tid], low) : Log{0.0f, 0.0f, 0.0f};
     const float near = fmaf(l.e, 0.693147181f, l.z) + l.rest;
     logs[tid] = l, logs32[tid] = near;
